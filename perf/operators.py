@@ -178,7 +178,7 @@ def _plain_recurrence(s):
     out = {"out": h.to(s["x"].dtype), "final": final}
     if not case["train"]:
         return out
-    b = s["dout"].float()
+    b = s["dout"].to(torch.float32, copy=True)  # the state's own tensor stays as it is
     if s["dfinal"] is not None:
         b[last] += s["dfinal"][held]
     nxt = torch.cat([decay[1:], decay[:1]])
