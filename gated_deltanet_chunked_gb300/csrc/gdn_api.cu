@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "gdn_common.cuh"
+#include "gdn_linrec.cuh"
 #include "tma_host.cuh"
 
 namespace gdn {
@@ -103,7 +104,7 @@ using namespace gdn;
 
 extern "C" {
 
-int gdn_version(void) { return 102; }
+int gdn_version(void) { return 103; }
 
 const char *gdn_status_string(int status) {
     switch (status) {
@@ -335,6 +336,200 @@ int gdn_gating(const gdn_problem *p, const float *a, const float *b, const float
             return GDN_EINVAL;
     }
     return cuda_status(launch_gating(a, b, A_log, dt_bias, g, beta, n, p->hv, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace gdn {
+namespace {
+
+// Descriptor checks of the gated linear recurrence's forward and backward pass.
+int check_linrec(const gdn_problem *p, bool packed) {
+    if (!p || p->hv <= 0 || p->dv <= 0 || p->num_seqs < 1 || p->total_tokens < 0) return GDN_EINVAL;
+    if (p->io_dtype != GDN_DT_F32 && p->io_dtype != GDN_DT_BF16) return GDN_EINVAL;
+    if (p->dv != kHeadDim || (p->flags & ~uint32_t(GDN_FLAG_GATE_CHANNEL))) return GDN_EUNSUPPORTED;
+    if (!packed) {
+        if (p->batch < 1 || p->seqlen < 0 || p->num_seqs != p->batch) return GDN_EINVAL;
+        if (int64_t(p->batch) * p->seqlen != p->total_tokens) return GDN_EINVAL;
+    }
+    // token indices a few tiles past the end stay in int; heads and sequences are grid axes
+    if (p->total_tokens > INT32_MAX - 65536 || p->hv > 65535 || p->num_seqs > 65535) return GDN_EINVAL;
+    return GDN_OK;
+}
+
+// g and dg: per channel like x, or f32 per head
+bool gate_ok(const gdn_problem *p, const void *g) {
+    return g && (p->flags & GDN_FLAG_GATE_CHANNEL ? aligned16(g) : aligned4(g));
+}
+
+RecArgs linrec_args(const gdn_problem *p, const void *x, const void *g, const float *s0, const int32_t *cu) {
+    RecArgs a{};
+    a.x = x; a.g = g; a.s0 = s0; a.cu = cu;
+    a.total_tokens = p->total_tokens; a.num_seqs = p->num_seqs; a.hv = p->hv;
+    a.dense_seqlen = cu ? 0 : p->seqlen;
+    return a;
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" {
+
+size_t gdn_linear_recurrence_states_size(const gdn_problem *p) {
+    if (check_linrec(p, /*packed=*/true) != GDN_OK) return 0;  // the size does not depend on the layout
+    return (size_t(p->total_tokens) + kRecTile - 1) / kRecTile * size_t(p->hv) * kHeadDim * sizeof(float);
+}
+
+int gdn_linear_recurrence(const gdn_problem *p, const void *x, const void *g, const float *initial_state,
+                          const int32_t *cu_seqlens, void *out, float *final_state, float *states, void *stream) {
+    int st = check_linrec(p, cu_seqlens != nullptr);
+    if (st) return st;
+    if (p->total_tokens > 0 && (!x || !out || x == out || !aligned16(x) || !aligned16(out) || !gate_ok(p, g)))
+        return GDN_EINVAL;
+    if (!aligned16(initial_state) || !aligned4(cu_seqlens) || !aligned16(final_state) || !aligned16(states))
+        return GDN_EINVAL;
+    if (final_state && final_state == initial_state) return GDN_EINVAL;
+    RecArgs a = linrec_args(p, x, g, initial_state, cu_seqlens);
+    a.out = out; a.final_state = final_state; a.states = states;
+    if (!(a.status = status_ptr())) return GDN_ECUDA;
+    return cuda_status(launch_linrec(a, p->io_dtype, p->flags & GDN_FLAG_GATE_CHANNEL,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_linear_recurrence_bwd(const gdn_problem *p, const void *dout, const void *x, const void *g,
+                              const float *states, const float *initial_state, const float *dfinal_state,
+                              const int32_t *cu_seqlens, void *dx, void *dg, float *dinitial_state, void *stream) {
+    int st = check_linrec(p, cu_seqlens != nullptr);
+    if (st) return st;
+    if (p->total_tokens > 0) {
+        if (!dout || !x || !states || !dx || !gate_ok(p, g) || !gate_ok(p, dg)) return GDN_EINVAL;
+        if (!aligned16(dout) || !aligned16(x) || !aligned16(states) || !aligned16(dx)) return GDN_EINVAL;
+        for (const void *in : {dout, x, g})
+            if (dx == in || dg == in) return GDN_EINVAL;
+        if (dx == dg) return GDN_EINVAL;
+    }
+    if (!aligned16(initial_state) || !aligned16(dfinal_state) || !aligned4(cu_seqlens) || !aligned16(dinitial_state))
+        return GDN_EINVAL;
+    if (dinitial_state && (dinitial_state == initial_state || dinitial_state == dfinal_state)) return GDN_EINVAL;
+    RecArgs a = linrec_args(p, x, g, initial_state, cu_seqlens);
+    a.dout = dout; a.dfinal = dfinal_state; a.dx = dx; a.dg = dg; a.dinitial = dinitial_state;
+    a.states = const_cast<float *>(states);  // read only
+    if (!(a.status = status_ptr())) return GDN_ECUDA;
+    return cuda_status(launch_linrec_bwd(a, p->io_dtype, p->flags & GDN_FLAG_GATE_CHANNEL,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_linear_recurrence_step(const gdn_problem *p, const void *x, const void *g, float *state,
+                               const int32_t *state_indices, void *out, void *stream) {
+    if (!p || p->hv <= 0 || p->dv <= 0 || p->num_seqs < 0 || p->total_tokens != p->num_seqs) return GDN_EINVAL;
+    if (p->io_dtype != GDN_DT_F32 && p->io_dtype != GDN_DT_BF16) return GDN_EINVAL;
+    if (p->dv != kHeadDim || (p->flags & ~uint32_t(GDN_FLAG_GATE_CHANNEL))) return GDN_EUNSUPPORTED;
+    if (p->num_state_slots < 0 || (!state_indices && p->num_state_slots < p->num_seqs)) return GDN_EINVAL;
+    if (int64_t(p->num_seqs) * p->hv > INT32_MAX - 65536) return GDN_EINVAL;
+    if (p->num_seqs > 0) {
+        if (!x || !state || !out || !gate_ok(p, g)) return GDN_EINVAL;
+        if (!aligned16(x) || !aligned16(state) || !aligned16(out) || !aligned4(state_indices)) return GDN_EINVAL;
+        if (out == g || out == state) return GDN_EINVAL;
+    }
+    int *status = status_ptr();
+    if (!status) return GDN_ECUDA;
+    return cuda_status(launch_linrec_step(x, g, state, state_indices, out, p->num_seqs, p->hv, p->num_state_slots,
+                                          p->io_dtype, p->flags & GDN_FLAG_GATE_CHANNEL, status,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace gdn {
+namespace {
+
+int check_layernorm(const gdn_problem *p) {
+    if (!p || p->dv <= 0 || p->total_tokens < 0) return GDN_EINVAL;
+    if (p->io_dtype != GDN_DT_F32 && p->io_dtype != GDN_DT_BF16) return GDN_EINVAL;
+    return p->dv > kLayerNormMaxWidth ? GDN_EUNSUPPORTED : GDN_OK;
+}
+
+bool workspace_ok(const void *ws, size_t have, size_t need) {
+    return ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) && have >= need;
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" {
+
+int gdn_layernorm(const gdn_problem *p, const void *x, const float *weight, const float *bias, float eps, void *y,
+                  float *mean, float *rstd, void *stream) {
+    const int st = check_layernorm(p);
+    if (st) return st;
+    if (!(eps >= 0.f) || !aligned16(weight) || !aligned16(bias)) return GDN_EINVAL;
+    if (p->total_tokens > 0) {
+        if (!x || !y || !aligned16(x) || !aligned16(y) || !aligned4(mean) || !aligned4(rstd)) return GDN_EINVAL;
+    }
+    return cuda_status(launch_layernorm(x, weight, bias, eps, y, mean, rstd, p->total_tokens, p->dv, p->io_dtype,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_layernorm_bwd_workspace_size(const gdn_problem *p) {
+    return check_layernorm(p) == GDN_OK ? layernorm_bwd_workspace(p->total_tokens, p->dv) : 0;
+}
+
+int gdn_layernorm_bwd(const gdn_problem *p, const void *dy, const void *x, const float *mean, const float *rstd,
+                      const float *weight, void *dx, float *dweight, float *dbias, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    const int st = check_layernorm(p);
+    if (st) return st;
+    if (!aligned16(weight) || !aligned16(dweight) || !aligned16(dbias)) return GDN_EINVAL;
+    if (p->total_tokens > 0) {
+        if (!dy || !x || !mean || !rstd || !dx) return GDN_EINVAL;
+        if (!aligned16(dy) || !aligned16(x) || !aligned16(dx) || !aligned4(mean) || !aligned4(rstd))
+            return GDN_EINVAL;
+        if ((dweight || dbias) && !workspace_ok(workspace, workspace_bytes, gdn_layernorm_bwd_workspace_size(p)))
+            return GDN_EINVAL;
+    }
+    return cuda_status(launch_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace,
+                                            p->total_tokens, p->dv, p->io_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace gdn {
+namespace {
+
+int check_gate_norm(const gdn_problem *p) {
+    if (!p || p->hv <= 0 || p->total_tokens < 0) return GDN_EINVAL;
+    if (p->io_dtype != GDN_DT_F32 && p->io_dtype != GDN_DT_BF16) return GDN_EINVAL;
+    if (p->dv != kHeadDim) return p->dv > 0 ? GDN_EUNSUPPORTED : GDN_EINVAL;
+    return GDN_OK;
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" {
+
+size_t gdn_gated_rmsnorm_bwd_workspace_size(const gdn_problem *p) {
+    if (check_gate_norm(p) != GDN_OK) return 0;
+    return gated_rmsnorm_bwd_workspace((long long)p->total_tokens * p->hv, p->io_dtype);
+}
+
+int gdn_gated_rmsnorm_bwd(const gdn_problem *p, const void *dy, const void *o, const void *z, const float *weight,
+                          float eps, void *d_o, void *d_z, float *d_weight, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+    const int st = check_gate_norm(p);
+    if (st) return st;
+    if (!(eps >= 0.f) || !aligned16(d_weight)) return GDN_EINVAL;
+    const long long rows = (long long)p->total_tokens * p->hv;
+    if (rows > 0) {
+        if (!dy || !o || !z || !weight || !d_o || !d_z || d_o == d_z) return GDN_EINVAL;
+        if (!aligned16(dy) || !aligned16(o) || !aligned16(z) || !aligned16(weight) || !aligned16(d_o) ||
+            !aligned16(d_z))
+            return GDN_EINVAL;
+        if (d_weight && !workspace_ok(workspace, workspace_bytes, gdn_gated_rmsnorm_bwd_workspace_size(p)))
+            return GDN_EINVAL;
+    }
+    return cuda_status(launch_gated_rmsnorm_bwd(dy, o, z, weight, eps, d_o, d_z, d_weight, workspace, rows,
+                                                p->io_dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int gdn_read_device_status(void *stream, int clear) {

@@ -1,0 +1,136 @@
+// Output gate, backward pass (gdn_gated_rmsnorm_bwd).
+//
+// Per (token, head) row of 128 channels, with r = 1 / sqrt(mean o^2 + eps),
+// n = o r, s = sigmoid(z) and u = dy w z s:
+//   d_o = r (u - n mean(u n)),  d_z = dy n w (s + z s (1 - s)),
+//   d_weight = sum over rows of dy n z s.
+//
+// HBM-bound: three rows in, two out. A thread owns eight (bf16: 16 lanes a
+// row) or four (f32: 32 lanes a row) channels, so that every access is 16
+// bytes; its sum over rows stays in registers and each CTA writes one partial
+// row, added by a second launch in a fixed order.
+#include "gdn_vec.cuh"
+
+namespace gdn {
+namespace {
+
+using vec::Pack;
+
+constexpr int kBThreads = 256;
+constexpr int kMaxCtas = 1216;  // 8 CTAs on each of 152 SMs
+
+struct GateBwdArgs {
+    const void *dy, *o, *z;
+    const float *weight;
+    float eps;
+    void *d_o, *d_z;
+    float *part;  // [gridDim.x, 128] or null
+    long long rows;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kBThreads) k_gated_rmsnorm_bwd(const GateBwdArgs a) {
+    constexpr int VE = 16 / int(sizeof(T)), G = kHeadDim / VE, kGroups = kBThreads / G;
+    const int tid = threadIdx.x % G, group = threadIdx.x / G;
+    const T *dy = static_cast<const T *>(a.dy) + tid * VE, *o = static_cast<const T *>(a.o) + tid * VE,
+            *z = static_cast<const T *>(a.z) + tid * VE;
+    T *d_o = static_cast<T *>(a.d_o) + tid * VE, *d_z = static_cast<T *>(a.d_z) + tid * VE;
+    float w[VE], dw[VE];
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+        w[j] = a.weight[tid * VE + j];
+        dw[j] = 0.f;
+    }
+    const long long step = (long long)gridDim.x * kGroups;
+    long long row = (long long)blockIdx.x * kGroups + group;
+    const long long first = row - (threadIdx.x & 31) / G;  // the warp's rows advance together
+    Pack<T, VE> po, pz, py;
+    po.zero();
+    pz.zero();
+    py.zero();
+    auto fetch = [&](long long r) {
+        po.load(o + r * kHeadDim);
+        pz.load(z + r * kHeadDim);
+        py.load(dy + r * kHeadDim);
+    };
+    if (row < a.rows) fetch(row);
+    for (long long base = first; base < a.rows; base += step, row += step) {
+        float n[VE], zz[VE], g[VE], ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            n[j] = po.f(j);
+            zz[j] = pz.f(j);
+            g[j] = py.f(j);
+            ss = fmaf(n[j], n[j], ss);
+        }
+        if (row + step < a.rows) fetch(row + step);
+        const bool live = row < a.rows;
+        const float r = 1.f / sqrtf(fmaf(vec::group_sum<G>(ss), 1.f / kHeadDim, a.eps));
+        float u[VE], un = 0.f;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            const float sig = 1.f / (1.f + expf(-zz[j]));
+            const float silu = __fmul_rn(zz[j], sig);
+            n[j] = __fmul_rn(n[j], r);
+            const float gn = __fmul_rn(g[j], n[j]);
+            if (live) dw[j] = fmaf(gn, silu, dw[j]);
+            u[j] = __fmul_rn(__fmul_rn(g[j], w[j]), silu);
+            un = fmaf(u[j], n[j], un);
+            zz[j] = __fmul_rn(gn, w[j]) * fmaf(silu, 1.f - sig, sig);
+        }
+        un = vec::group_sum<G>(un) * (1.f / kHeadDim);
+        if (live) {
+            Pack<T, VE> q, t;
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+                q.set(j, r * fmaf(-n[j], un, u[j]));
+                t.set(j, zz[j]);
+            }
+            q.store(d_o + row * kHeadDim);
+            t.store(d_z + row * kHeadDim);
+        }
+    }
+    if (!a.part) return;
+    __shared__ float sums[kGroups][kHeadDim];
+#pragma unroll
+    for (int j = 0; j < VE; ++j) sums[group][tid * VE + j] = dw[j];
+    __syncthreads();
+    if (threadIdx.x < kHeadDim) {
+        float t = 0.f;
+        for (int k = 0; k < kGroups; ++k) t += sums[k][threadIdx.x];
+        a.part[blockIdx.x * kHeadDim + threadIdx.x] = t;
+    }
+}
+
+// CTAs of a launch (a bound that does not depend on the device)
+int ctas_of(long long rows, int io_dtype) {
+    const int groups = kBThreads / (io_dtype == GDN_DT_BF16 ? 16 : 32);
+    const long long c = (rows + groups - 1) / groups;
+    return int(c < kMaxCtas ? c : kMaxCtas);
+}
+
+}  // namespace
+
+size_t gated_rmsnorm_bwd_workspace(long long rows, int io_dtype) {
+    return size_t(ctas_of(rows, io_dtype)) * kHeadDim * sizeof(float);  // a multiple of 256
+}
+
+cudaError_t launch_gated_rmsnorm_bwd(const void *dy, const void *o, const void *z, const float *weight, float eps,
+                                     void *d_o, void *d_z, float *d_weight, void *workspace, long long rows,
+                                     int io_dtype, cudaStream_t s) {
+    const int ctas = ctas_of(rows, io_dtype);
+    float *part = d_weight ? static_cast<float *>(workspace) : nullptr;
+    if (rows > 0) {
+        const GateBwdArgs a{dy, o, z, weight, eps, d_o, d_z, part, rows};
+        LaunchScope scope(GDN_K_GATED_RMSNORM_BWD, s);
+        if (io_dtype == GDN_DT_BF16)
+            k_gated_rmsnorm_bwd<__nv_bfloat16><<<unsigned(ctas), kBThreads, 0, s>>>(a);
+        else
+            k_gated_rmsnorm_bwd<float><<<unsigned(ctas), kBThreads, 0, s>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return launch_row_sums(part, nullptr, ctas, kHeadDim, d_weight, nullptr, s);
+}
+
+}  // namespace gdn

@@ -7,11 +7,14 @@ no fallback: if libgdn.so cannot be built or loaded, ``load()`` raises.
 The entry points keep the C names:
   gdn_chunk_fwd, gdn_chunk_fwd_workspace_size, gdn_recurrent_step,
   gdn_recurrent_step_gated, gdn_gated_rmsnorm, gdn_causal_conv1d_silu,
-  gdn_causal_conv1d_silu_step, gdn_gating,
+  gdn_causal_conv1d_silu_step, gdn_gating, gdn_linear_recurrence,
+  gdn_linear_recurrence_bwd, gdn_linear_recurrence_step, gdn_layernorm,
+  gdn_layernorm_bwd, gdn_gated_rmsnorm_bwd,
   gdn_read_device_status, gdn_get_device_status, gdn_status_string, gdn_version.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import threading
 from typing import Optional
@@ -23,14 +26,16 @@ from . import build as _build
 GDN_OK, GDN_EINVAL, GDN_EUNSUPPORTED, GDN_ECUDA, GDN_ETIMEOUT, GDN_EDEVICE_INPUT, GDN_ETOOBIG = range(7)
 GDN_NOALLOC_SCRATCH_BYTES = 32 << 20
 GDN_DT_F32, GDN_DT_BF16 = 0, 1
-GDN_FLAG_BETA_BF16, GDN_FLAG_STATE_BF16 = 1 << 1, 1 << 2
+GDN_FLAG_BETA_BF16, GDN_FLAG_STATE_BF16, GDN_FLAG_GATE_CHANNEL = 1 << 1, 1 << 2, 1 << 3
 
 SYMBOLS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "gdn_recurrent_step", "gdn_read_device_status",
            "gdn_status_string", "gdn_version", "gdn_profile_enable", "gdn_profile_collect", "gdn_kernel_name",
            "gdn_chunk_fwd_noalloc", "gdn_recurrent_step_gated", "gdn_gated_rmsnorm", "gdn_causal_conv1d_silu",
            "gdn_gating", "gdn_causal_conv1d_silu_step", "gdn_chunk_fwd_gated", "gdn_get_device_status",
-           "gdn_set_wait_limit_ns")
-GDN_K_COUNT = 11
+           "gdn_set_wait_limit_ns", "gdn_linear_recurrence", "gdn_linear_recurrence_states_size",
+           "gdn_linear_recurrence_bwd", "gdn_linear_recurrence_step", "gdn_layernorm", "gdn_layernorm_bwd",
+           "gdn_layernorm_bwd_workspace_size", "gdn_gated_rmsnorm_bwd", "gdn_gated_rmsnorm_bwd_workspace_size")
+GDN_K_COUNT = 18
 
 
 class GdnProblem(ctypes.Structure):
@@ -97,6 +102,22 @@ def load(path: Optional[str] = None):
             lib.gdn_chunk_fwd_noalloc.argtypes = [P, _vp, _vp, _vp, _fp, _fp, ctypes.c_float, _fp, _ip, _vp, _fp,
                                                   _vp]
             lib.gdn_chunk_fwd_noalloc.restype = ctypes.c_int
+            cf, sz = ctypes.c_float, ctypes.c_size_t
+            for name, res, args in (
+                    ("gdn_linear_recurrence", ctypes.c_int, [P, _vp, _vp, _fp, _ip, _vp, _fp, _fp, _vp]),
+                    ("gdn_linear_recurrence_states_size", sz, [P]),
+                    ("gdn_linear_recurrence_bwd", ctypes.c_int,
+                     [P, _vp, _vp, _vp, _fp, _fp, _fp, _ip, _vp, _vp, _fp, _vp]),
+                    ("gdn_linear_recurrence_step", ctypes.c_int, [P, _vp, _vp, _fp, _ip, _vp, _vp]),
+                    ("gdn_layernorm", ctypes.c_int, [P, _vp, _fp, _fp, cf, _vp, _fp, _fp, _vp]),
+                    ("gdn_layernorm_bwd", ctypes.c_int,
+                     [P, _vp, _vp, _fp, _fp, _fp, _vp, _fp, _fp, _vp, sz, _vp]),
+                    ("gdn_layernorm_bwd_workspace_size", sz, [P]),
+                    ("gdn_gated_rmsnorm_bwd", ctypes.c_int,
+                     [P, _vp, _vp, _vp, _fp, cf, _vp, _vp, _fp, _vp, sz, _vp]),
+                    ("gdn_gated_rmsnorm_bwd_workspace_size", sz, [P])):
+                fn = getattr(lib, name)
+                fn.restype, fn.argtypes = res, args
             lib.gdn_kernel_name.argtypes = [ctypes.c_int]
             lib.gdn_kernel_name.restype = ctypes.c_char_p
             _lib = lib
@@ -142,6 +163,24 @@ def _stream(stream, device=None) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+@contextlib.contextmanager
+def _launching(stream, dev):
+    """Makes ``dev`` and, if given, ``stream`` current and yields the stream's
+    handle: what the call allocates then belongs to the stream it runs on, so
+    that PyTorch's allocator hands none of it to other work too early."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield _stream(None, dev)
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = _stream(stream).value or 0
+            stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, expected {dev} (the device of the first input)")
+        with torch.cuda.stream(stream):
+            yield _stream(stream)
 
 
 def _on_device(dev: torch.device, **tensors):
@@ -467,6 +506,240 @@ def gdn_gating(a, b, A_log, dt_bias, g=None, beta=None, stream=None):
     if st != GDN_OK:
         raise GdnError(st, "gdn_gating")
     return g, beta
+
+
+def _linrec_checks(x, g, initial_state, cu_seqlens, states=None, **like_x):
+    """Checks shared by the recurrence's forward and backward wrappers;
+    returns (problem, device). ``like_x``: tensors of x's shape and type."""
+    packed = cu_seqlens is not None
+    if x.dim() != (3 if packed else 4):
+        raise ValueError("x must be [T, Hv, 128] with cu_seqlens, else [B, T, Hv, 128]")
+    if packed and cu_seqlens.dim() != 1:
+        raise ValueError("cu_seqlens must be a 1-D int32 tensor [N + 1]")
+    lead, hv, dv = x.shape[:-2], x.shape[-2], x.shape[-1]
+    num_seqs = cu_seqlens.numel() - 1 if packed else x.shape[0]
+    total = x.shape[0] if packed else x.shape[0] * x.shape[1]
+    channel = g.dim() == x.dim()
+    _shape("g", g, *(x.shape if channel else (*lead, hv)))
+    _want(x.dtype if channel else torch.float32, g=g)
+    _want(x.dtype, **like_x)
+    _want(torch.float32, initial_state=initial_state, states=states)
+    _want(torch.int32, cu_seqlens=cu_seqlens)
+    for name, t in like_x.items():
+        _shape(name, t, *x.shape)
+    _shape("initial_state", initial_state, num_seqs, hv, dv)
+    _shape("states", states, (total + 63) // 64, hv, dv)
+    _on_device(x.device, g=g, initial_state=initial_state, cu_seqlens=cu_seqlens, states=states, **like_x)
+    prob = GdnProblem(1 if packed else x.shape[0], 0 if packed else x.shape[1], num_seqs, total, hv, hv, dv, dv,
+                      _io_dtype(x), GDN_FLAG_GATE_CHANNEL if channel else 0, 0)
+    return prob, x.device
+
+
+def gdn_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, out=None, final_state=None,
+                          output_final_state=True, save_states=False, states=None, stream=None):
+    """s_t = exp(g_t) s_{t-1} + x_t per channel, out = s: x [T, Hv, 128] packed
+    by ``cu_seqlens`` (int32 [N + 1]) or [B, T, Hv, 128]; the log-decays g <= 0
+    per head ([T, Hv] f32, as gdn_gating gives them) or per channel (x's shape
+    and type). ``initial_state`` and the returned final state are
+    [N, Hv, 128] f32.
+
+    Returns (out, final_state), and with ``save_states`` (or ``states`` given)
+    also the states that gdn_linear_recurrence_bwd starts from,
+    [ceil(T / 64), Hv, 128] f32 over all T rows."""
+    prob, dev = _linrec_checks(x, g, initial_state, cu_seqlens, states, out=out)
+    _want(torch.float32, final_state=final_state)
+    _shape("final_state", final_state, prob.num_seqs, prob.hv, prob.dv)
+    _on_device(dev, final_state=final_state)
+    with _launching(stream, dev) as handle:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if final_state is None and output_final_state:
+            final_state = torch.empty((prob.num_seqs, prob.hv, prob.dv), dtype=torch.float32, device=dev)
+        if states is None and save_states:
+            states = torch.empty(((prob.total_tokens + 63) // 64, prob.hv, prob.dv), dtype=torch.float32, device=dev)
+        st = load().gdn_linear_recurrence(ctypes.byref(prob), _ptr(x), _ptr(g), _ptr(initial_state),
+                                          _ptr(cu_seqlens), _ptr(out), _ptr(final_state), _ptr(states),
+                                          handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_linear_recurrence")
+    return (out, final_state) if states is None else (out, final_state, states)
+
+
+def gdn_linear_recurrence_bwd(dout, x, g, states, initial_state=None, cu_seqlens=None, dfinal_state=None, dx=None,
+                              dg=None, dinitial_state=None, stream=None):
+    """Backward pass of gdn_linear_recurrence from the gradients of out and of
+    the final state (None: zeros), with ``states`` of the forward pass.
+    Returns (dx, dg, dinitial_state); dinitial_state is None unless an
+    ``initial_state`` or a dinitial_state to write is given."""
+    if states is None:
+        raise ValueError("the backward pass needs the forward pass's states (save_states=True)")
+    prob, dev = _linrec_checks(x, g, initial_state, cu_seqlens, states, dout=dout, dx=dx)
+    state_shape = (prob.num_seqs, prob.hv, prob.dv)
+    _want(g.dtype, dg=dg)
+    _want(torch.float32, dfinal_state=dfinal_state, dinitial_state=dinitial_state)
+    _shape("dg", dg, *g.shape)
+    _shape("dfinal_state", dfinal_state, *state_shape)
+    _shape("dinitial_state", dinitial_state, *state_shape)
+    _on_device(dev, dg=dg, dfinal_state=dfinal_state, dinitial_state=dinitial_state)
+    with _launching(stream, dev) as handle:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
+        dg = torch.empty(g.shape, dtype=g.dtype, device=dev) if dg is None else dg
+        if dinitial_state is None and initial_state is not None:
+            dinitial_state = torch.empty(state_shape, dtype=torch.float32, device=dev)
+        st = load().gdn_linear_recurrence_bwd(ctypes.byref(prob), _ptr(dout), _ptr(x), _ptr(g), _ptr(states),
+                                              _ptr(initial_state), _ptr(dfinal_state), _ptr(cu_seqlens), _ptr(dx),
+                                              _ptr(dg), _ptr(dinitial_state), handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_linear_recurrence_bwd")
+    return dx, dg, dinitial_state
+
+
+def gdn_linear_recurrence_step(x, g, state, state_indices=None, out=None, stream=None):
+    """One decode token per sequence: x [N, Hv, 128]; ``state``
+    [slots, Hv, 128] f32 is updated in place at ``state_indices`` (int32 [N];
+    None: slot n; negative: skipped, its out rows are not written)."""
+    if x.dim() != 3 or state.dim() != 3:
+        raise ValueError("x must be [N, Hv, 128] and state [slots, Hv, 128]")
+    N, hv, dv = x.shape
+    channel = g.dim() == 3
+    _shape("g", g, *(x.shape if channel else (N, hv)))
+    _want(x.dtype if channel else torch.float32, g=g)
+    _want(x.dtype, out=out)
+    _want(torch.float32, state=state)
+    _want(torch.int32, state_indices=state_indices)
+    _shape("out", out, *x.shape)
+    _shape("state", state, state.shape[0], hv, dv)
+    _shape("state_indices", state_indices, N)
+    dev = x.device
+    _on_device(dev, g=g, state=state, state_indices=state_indices, out=out)
+    prob = GdnProblem(N, 1, N, N, hv, hv, dv, dv, _io_dtype(x), GDN_FLAG_GATE_CHANNEL if channel else 0,
+                      state.shape[0])
+    with _launching(stream, dev) as handle:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        st = load().gdn_linear_recurrence_step(ctypes.byref(prob), _ptr(x), _ptr(g), _ptr(state),
+                                               _ptr(state_indices), _ptr(out), handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_linear_recurrence_step")
+    return out
+
+
+def _rows_problem(x) -> GdnProblem:
+    """Descriptor of a row-wise norm over the last dimension of x."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("the last dimension must not be empty")
+    rows = x.numel() // x.shape[-1]
+    if rows >= 1 << 31:
+        raise ValueError("too many rows")
+    return GdnProblem(1, 0, 1, rows, 1, 1, x.shape[-1], x.shape[-1], _io_dtype(x), 0, 0)
+
+
+def gdn_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, save_stats=False, mean=None, rstd=None,
+                  stream=None):
+    """y = (x - mean) / sqrt(var + eps) * weight + bias over the last dimension
+    of x (1 to 16384 wide); weight and bias [D] f32 or None. ``out`` may be x.
+    Returns y, and with ``save_stats`` (y, mean, rstd), the last two f32 of
+    x's leading shape, for gdn_layernorm_bwd."""
+    prob = _rows_problem(x)
+    dev, lead = x.device, x.shape[:-1]
+    _want(x.dtype, out=out)
+    _want(torch.float32, weight=weight, bias=bias, mean=mean, rstd=rstd)
+    _shape("weight", weight, x.shape[-1])
+    _shape("bias", bias, x.shape[-1])
+    _shape("out", out, *x.shape)
+    _shape("mean", mean, *lead)
+    _shape("rstd", rstd, *lead)
+    _on_device(dev, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
+    with _launching(stream, dev) as handle:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        if save_stats:
+            mean = torch.empty(lead, dtype=torch.float32, device=dev) if mean is None else mean
+            rstd = torch.empty(lead, dtype=torch.float32, device=dev) if rstd is None else rstd
+        st = load().gdn_layernorm(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), ctypes.c_float(eps),
+                                  _ptr(out), _ptr(mean), _ptr(rstd), handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_layernorm")
+    return (out, mean, rstd) if save_stats else out
+
+
+def _workspace(workspace, need, dev):
+    """The caller's uint8 workspace, or one of ``need`` bytes."""
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a uint8 tensor")
+    return workspace
+
+
+def gdn_layernorm_bwd(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, need_dweight=True,
+                      need_dbias=True, workspace=None, stream=None):
+    """Backward pass of gdn_layernorm with the forward pass's mean and rstd.
+    Returns (dx, dweight, dbias), the last two [D] f32 sums over all rows (None
+    where not needed). ``dx`` may be dy or x. ``workspace`` (uint8, of
+    gdn_layernorm_bwd_workspace_size bytes) is allocated when not supplied."""
+    prob = _rows_problem(x)
+    dev, lead, D = x.device, x.shape[:-1], x.shape[-1]
+    _want(x.dtype, dy=dy, dx=dx)
+    _want(torch.float32, mean=mean, rstd=rstd, weight=weight, dweight=dweight, dbias=dbias)
+    _shape("dy", dy, *x.shape)
+    _shape("dx", dx, *x.shape)
+    _shape("mean", mean, *lead)
+    _shape("rstd", rstd, *lead)
+    for name, t in (("weight", weight), ("dweight", dweight), ("dbias", dbias)):
+        _shape(name, t, D)
+    _on_device(dev, dy=dy, mean=mean, rstd=rstd, weight=weight, dx=dx, dweight=dweight, dbias=dbias,
+               workspace=workspace)
+    with _launching(stream, dev) as handle:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
+        if dweight is None and need_dweight:
+            dweight = torch.empty(D, dtype=torch.float32, device=dev)
+        if dbias is None and need_dbias:
+            dbias = torch.empty(D, dtype=torch.float32, device=dev)
+        if dweight is not None or dbias is not None or workspace is not None:
+            workspace = _workspace(workspace, int(load().gdn_layernorm_bwd_workspace_size(ctypes.byref(prob))), dev)
+        st = load().gdn_layernorm_bwd(ctypes.byref(prob), _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
+                                      _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+                                      ctypes.c_size_t(0 if workspace is None else workspace.numel()),
+                                      handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_layernorm_bwd")
+    return dx, dweight, dbias
+
+
+def gdn_gated_rmsnorm_bwd(dy, o, z, weight, eps, do=None, dz=None, dweight=None, need_dweight=True, workspace=None,
+                          stream=None):
+    """Backward pass of gdn_gated_rmsnorm: dy, o, z [T, Hv, 128], weight [128]
+    f32. Returns (do, dz, dweight); dweight [128] f32 sums over all (token,
+    head) rows (None where not needed). do and dz may be any of dy, o and z.
+    ``workspace`` (uint8, of gdn_gated_rmsnorm_bwd_workspace_size bytes) is
+    allocated when not supplied."""
+    if o.dim() != 3:
+        raise ValueError("o must be [T, Hv, 128]")
+    T, hv, dv = o.shape
+    dev = o.device
+    _want(o.dtype, dy=dy, z=z, do=do, dz=dz)
+    _want(torch.float32, weight=weight, dweight=dweight)
+    for name, t in (("dy", dy), ("z", z), ("do", do), ("dz", dz)):
+        _shape(name, t, *o.shape)
+    _shape("weight", weight, dv)
+    _shape("dweight", dweight, dv)
+    _on_device(dev, dy=dy, z=z, weight=weight, do=do, dz=dz, dweight=dweight, workspace=workspace)
+    prob = GdnProblem(1, 0, 1, T, 1, hv, dv, dv, _io_dtype(o), 0, 0)
+    with _launching(stream, dev) as handle:
+        do = torch.empty_like(o) if do is None else do
+        dz = torch.empty_like(o) if dz is None else dz
+        if dweight is None and need_dweight:
+            dweight = torch.empty(dv, dtype=torch.float32, device=dev)
+        if dweight is not None or workspace is not None:
+            workspace = _workspace(workspace, int(load().gdn_gated_rmsnorm_bwd_workspace_size(ctypes.byref(prob))),
+                                   dev)
+        st = load().gdn_gated_rmsnorm_bwd(ctypes.byref(prob), _ptr(dy), _ptr(o), _ptr(z), _ptr(weight),
+                                          ctypes.c_float(eps), _ptr(do), _ptr(dz), _ptr(dweight), _ptr(workspace),
+                                          ctypes.c_size_t(0 if workspace is None else workspace.numel()),
+                                          handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_gated_rmsnorm_bwd")
+    return do, dz, dweight
 
 
 def gdn_read_device_status(stream=None, clear: bool = True) -> int:

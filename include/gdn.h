@@ -79,6 +79,11 @@ typedef enum gdn_dtype {
 #define GDN_FLAG_STATE_BF16 (1u << 2) /* the state array holds bf16: loaded to f32, the updated state
                                           rounded to bf16 when written back */
 
+/* gdn_problem.flags of the gated linear recurrence (gdn_linear_recurrence and
+ * its backward pass and decode step; no other entry point takes it). */
+#define GDN_FLAG_GATE_CHANNEL (1u << 3) /* a gate for every channel, [rows, hv, 128] in the io dtype;
+                                           without it one per head, [rows, hv] f32 */
+
 /* Problem descriptor.
  *  Dense prefill  : batch = B, seqlen = T, num_seqs = B, total_tokens = B*T,
  *                   cu_seqlens = NULL (sequence b = rows [b*T, (b+1)*T)).
@@ -307,6 +312,124 @@ int gdn_causal_conv1d_silu_step(const gdn_problem *p, const void *x, const float
 int gdn_gating(const gdn_problem *p, const float *a, const float *b, const float *A_log, const float *dt_bias,
                float *g, float *beta, void *stream);
 
+/* ---- training and long sequences: recurrence, norm, output gate ---- */
+
+/* Gated linear recurrence, a mixer whose state is one value per channel: for
+ * every sequence, in token order, and every head h and channel j,
+ *   s[t,h,j] = exp(g[t,h,j]) * s[t-1,h,j] + x[t,h,j],   out[t,h,j] = s[t,h,j],
+ * s before the first token being the sequence's initial state. The sequence
+ * layout, dense or packed, is gdn_chunk_fwd's. Only batch, seqlen, num_seqs,
+ * total_tokens, hv, dv (128), io_dtype and flags of `p` are used.
+ *   x, out        [total_tokens, hv, 128] io dtype, 16-byte aligned; out may
+ *                 not be x
+ *   g             log-decays, g <= 0 (-inf forgets the state): [total_tokens,
+ *                 hv] f32, 4-byte aligned, one per head (gdn_gating's g), or
+ *                 with GDN_FLAG_GATE_CHANNEL [total_tokens, hv, 128] io dtype,
+ *                 16-byte aligned. A gate above 0 is not refused, but partial
+ *                 products of the decays may then overflow where the
+ *                 recurrence itself does not.
+ *   initial_state [num_seqs, hv, 128] f32, 16-byte aligned, or NULL for zeros
+ *   cu_seqlens    int32 [num_seqs + 1] packed offsets, 4-byte aligned, or
+ *                 NULL (dense). Checked on the device: offsets that do not
+ *                 start at 0, rise and end at total_tokens are recorded as
+ *                 GDN_EDEVICE_INPUT and nothing is written.
+ *   final_state   [num_seqs, hv, 128] f32, 16-byte aligned, or NULL; a
+ *                 sequence without tokens gets its initial state (or zeros)
+ *   states        NULL, or f32 storage of gdn_linear_recurrence_states_size(p)
+ *                 bytes, 16-byte aligned, that the backward pass reads: s
+ *                 before every 64th row of the packed token axis (what it
+ *                 holds for a row that starts a sequence is unspecified)
+ * The state and all sums are f32; out is rounded once. */
+int gdn_linear_recurrence(const gdn_problem *p, const void *x, const void *g, const float *initial_state,
+                          const int32_t *cu_seqlens, void *out, float *final_state, float *states, void *stream);
+
+/* Bytes of gdn_linear_recurrence's `states` for problem `p` (0 if `p` is
+ * invalid): ceil(total_tokens / 64) * hv * 128 floats. */
+size_t gdn_linear_recurrence_states_size(const gdn_problem *p);
+
+/* Backward pass of gdn_linear_recurrence. With e the gradient that reaches a
+ * token from the tokens after it (dfinal_state at a sequence's last token):
+ *   ds[t] = dout[t] + e,  dx[t] = ds[t],
+ *   dg[t] = exp(g[t]) * s[t-1] * ds[t]  (with gates per head summed over the
+ *           head's channels),  e = exp(g[t]) * ds[t] for token t - 1,
+ * and dinitial_state is the e that leaves the first token.
+ *   dout, x, dx    [total_tokens, hv, 128] io dtype, 16-byte aligned
+ *   g, dg          as gdn_linear_recurrence's g
+ *   states         what gdn_linear_recurrence wrote for the same inputs
+ *   initial_state  what the forward pass was given (or NULL)
+ *   dfinal_state   [num_seqs, hv, 128] f32, 16-byte aligned, or NULL for zeros
+ *   dinitial_state [num_seqs, hv, 128] f32, 16-byte aligned, or NULL; a
+ *                  sequence without tokens gets its dfinal_state (or zeros)
+ * The state is recomputed in f32 from `states` and x, not taken from the
+ * rounded out. No output may be an input. */
+int gdn_linear_recurrence_bwd(const gdn_problem *p, const void *dout, const void *x, const void *g,
+                              const float *states, const float *initial_state, const float *dfinal_state,
+                              const int32_t *cu_seqlens, void *dx, void *dg, float *dinitial_state, void *stream);
+
+/* Decode step of the gated linear recurrence, one token per sequence: for
+ * n < num_seqs with slot i = state_indices[n] (n when NULL),
+ *   state[i,h,j] = exp(g[n,h,j]) * state[i,h,j] + x[n,h,j], out[n] = state[i].
+ *   x, out [num_seqs, hv, 128] io dtype; g as gdn_linear_recurrence's
+ *   state  [num_state_slots, hv, 128] f32, 16-byte aligned, in place
+ *   state_indices int32 [num_seqs], 4-byte aligned, or NULL. A negative index
+ *   skips the sequence (its out rows stay as they were); one >=
+ *   num_state_slots is skipped and recorded as GDN_EDEVICE_INPUT. Two
+ *   sequences must not name the same slot.
+ * out may be x. */
+int gdn_linear_recurrence_step(const gdn_problem *p, const void *x, const void *g, float *state,
+                               const int32_t *state_indices, void *out, void *stream);
+
+/* Layer norm over the last dimension: for every row r of x,
+ *   y[r,j] = (x[r,j] - mean_r) * rstd_r * weight[j] + bias[j],
+ *   rstd_r = 1 / sqrt(mean_j (x[r,j] - mean_r)^2 + eps).
+ * Only total_tokens (rows), dv (the row's width, 1 .. 16384, else
+ * GDN_EUNSUPPORTED) and io_dtype of `p` are used.
+ *   x, y         [total_tokens, dv] io dtype, 16-byte aligned; y may be x
+ *   weight, bias [dv] f32, 16-byte aligned, or NULL (1 and 0)
+ *   mean, rstd   [total_tokens] f32, 4-byte aligned, or NULL to skip: kept
+ *                for the backward pass
+ * The statistics are f32: the mean first, then the squares about it. */
+int gdn_layernorm(const gdn_problem *p, const void *x, const float *weight, const float *bias, float eps, void *y,
+                  float *mean, float *rstd, void *stream);
+
+/* Backward pass of gdn_layernorm, xhat = (x - mean) rstd, u = dy * weight:
+ *   dx = rstd * (u - mean_j u - xhat * mean_j (u * xhat)),
+ *   dweight[j] = sum_r dy[r,j] xhat[r,j],  dbias[j] = sum_r dy[r,j].
+ *   dy, x, dx      [total_tokens, dv] io dtype, 16-byte aligned; dx may be dy
+ *                  or x
+ *   mean, rstd     [total_tokens] f32 from the forward pass, 4-byte aligned
+ *   weight         as in the forward pass (NULL: 1)
+ *   dweight, dbias [dv] f32, 16-byte aligned, or NULL to skip; written (not
+ *                  added to), with no rows zeros
+ *   workspace      gdn_layernorm_bwd_workspace_size(p) bytes, 256-byte
+ *                  aligned; may be NULL when dweight and dbias are. Calls that
+ *                  share it must be ordered on one stream.
+ * The sums over rows are taken in a fixed order: the same call gives the same
+ * bits. */
+int gdn_layernorm_bwd(const gdn_problem *p, const void *dy, const void *x, const float *mean, const float *rstd,
+                      const float *weight, void *dx, float *dweight, float *dbias, void *workspace,
+                      size_t workspace_bytes, void *stream);
+size_t gdn_layernorm_bwd_workspace_size(const gdn_problem *p);
+
+/* Backward pass of gdn_gated_rmsnorm, per (token, head) row with r =
+ * 1 / sqrt(mean_j o_j^2 + eps), n = o r, u = dy * weight * silu(z):
+ *   d_o = r * (u - n * mean_j (u * n)),
+ *   d_z = dy * n * weight * silu'(z),  silu'(z) = s + z s (1 - s), s = 1 / (1 + exp(-z)),
+ *   d_weight[j] = sum over rows of dy * n * silu(z).
+ *   dy, o, z, d_o, d_z [total_tokens, hv, 128] io dtype, 16-byte aligned; an
+ *                output may be any of the inputs (not the other output)
+ *   weight       [128] f32, eps: as in the forward pass
+ *   d_weight     [128] f32, 16-byte aligned, or NULL to skip; written (not
+ *                added to), with no rows zeros
+ *   workspace    gdn_gated_rmsnorm_bwd_workspace_size(p) bytes, 256-byte
+ *                aligned; may be NULL when d_weight is. Calls that share it
+ *                must be ordered on one stream.
+ * The sum over rows is taken in a fixed order. */
+int gdn_gated_rmsnorm_bwd(const gdn_problem *p, const void *dy, const void *o, const void *z, const float *weight,
+                          float eps, void *d_o, void *d_z, float *d_weight, void *workspace, size_t workspace_bytes,
+                          void *stream);
+size_t gdn_gated_rmsnorm_bwd_workspace_size(const gdn_problem *p);
+
 /* Synchronises `stream`, returns the device status word (GDN_OK or the first
  * device-side error recorded since the last clear) and clears it when
  * `clear` is non-zero. Returns GDN_ECUDA if the CUDA calls themselves fail. */
@@ -340,7 +463,14 @@ typedef enum gdn_kernel {
     GDN_K_CONV1D_SILU = 8,        /* short causal convolution + SiLU with conv state, split into q, k, v */
     GDN_K_GATING = 9,             /* g and beta from the gate projections, every token */
     GDN_K_CONV1D_STEP = 10,       /* short convolution, one token per sequence (decode) */
-    GDN_K_COUNT = 11
+    GDN_K_LINREC = 11,            /* gated linear recurrence, forward */
+    GDN_K_LINREC_BWD = 12,        /* gated linear recurrence, backward */
+    GDN_K_LINREC_STEP = 13,       /* gated linear recurrence, decode step */
+    GDN_K_LAYERNORM = 14,         /* layer norm */
+    GDN_K_LAYERNORM_BWD = 15,     /* layer norm, backward: dx and partial sums over rows */
+    GDN_K_GATED_RMSNORM_BWD = 16, /* output gate, backward: d_o, d_z and partial sums over rows */
+    GDN_K_ROW_SUMS = 17,          /* partial sums over rows -> weight and bias gradients */
+    GDN_K_COUNT = 18
 } gdn_kernel;
 
 /* Turns per-kernel CUDA-event timing on (non-zero) or off for every later
