@@ -352,8 +352,8 @@ int check_linrec(const gdn_problem *p, bool packed) {
         if (p->batch < 1 || p->seqlen < 0 || p->num_seqs != p->batch) return GDN_EINVAL;
         if (int64_t(p->batch) * p->seqlen != p->total_tokens) return GDN_EINVAL;
     }
-    // token indices a few tiles past the end stay in int; heads and sequences are grid axes
-    if (p->total_tokens > INT32_MAX - 65536 || p->hv > 65535 || p->num_seqs > 65535) return GDN_EINVAL;
+    // token indices a few tiles past the end stay in int, and so does the number of CTAs
+    if (p->total_tokens > INT32_MAX - 65536 || p->hv > (1 << 24) || p->num_seqs == INT32_MAX) return GDN_EINVAL;
     return GDN_OK;
 }
 
@@ -367,6 +367,7 @@ RecArgs linrec_args(const gdn_problem *p, const void *x, const void *g, const fl
     a.x = x; a.g = g; a.s0 = s0; a.cu = cu;
     a.total_tokens = p->total_tokens; a.num_seqs = p->num_seqs; a.hv = p->hv;
     a.dense_seqlen = cu ? 0 : p->seqlen;
+    a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     return a;
 }
 

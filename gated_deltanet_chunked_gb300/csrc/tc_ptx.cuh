@@ -200,6 +200,35 @@ __device__ __forceinline__ void st_release_gpu(int *p, int v) {
 }
 
 // ---------------------------------------------------------------------------
+// thread-block clusters: rank, distributed shared memory, cluster barrier
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_ctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// address, in the cluster's shared window, of this CTA's shared variable `p` in CTA `rank`
+__device__ __forceinline__ uint32_t cluster_map(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ void cluster_st(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Barrier over every thread of the cluster; shared-memory writes before it,
+// remote ones too, are visible after it. The hardware counts threads that
+// have exited as arrived, and no code path skips one, so it always ends.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();  // .aligned: the warp's lanes together
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // tcgen05: tensor memory
 // ---------------------------------------------------------------------------
 // Allocates `ncols` TMEM columns (power of two, >= 32); one full warp calls
