@@ -378,7 +378,7 @@ extern "C" {
 
 size_t gdn_linear_recurrence_states_size(const gdn_problem *p) {
     if (check_linrec(p, /*packed=*/true) != GDN_OK) return 0;  // the size does not depend on the layout
-    return (size_t(p->total_tokens) + kRecTile - 1) / kRecTile * size_t(p->hv) * kHeadDim * sizeof(float);
+    return (size_t(p->total_tokens) + kStateRows - 1) / kStateRows * size_t(p->hv) * kHeadDim * sizeof(float);
 }
 
 int gdn_linear_recurrence(const gdn_problem *p, const void *x, const void *g, const float *initial_state,

@@ -9,19 +9,22 @@
 // reads x, g and dout and writes dx and dg, each once. What has to be won is
 // parallelism along the time axis. A row's map s -> a s + x composes: a
 // segment of rows is s -> A s + B with A the product of its decays. A cluster
-// of CTAs takes one head and walks the packed token axis in rounds; in a round
-// each CTA takes the next tile of kRecTile rows, each of its warps a segment
-// of kSeg rows, each lane four channels:
+// of CTAs takes half of a head's channels and walks the packed token axis in
+// rounds; in a round each CTA takes the next tile of 128 rows, each of its
+// warps a segment of kSeg rows, each lane two channels:
 //  1. every warp composes its segment's rows (tile in shared memory by TMA,
 //     kept in registers from here on);
-//  2. the CTA composes its segments and writes the result into every CTA of
-//     the cluster (distributed shared memory);
-//  3. one cluster barrier; then every CTA knows the state at its tile's first
-//     row and, all in the same order, the state that the next round starts from;
+//  2. the CTA composes its segments and stores the result into every CTA of
+//     the cluster (distributed shared memory, asynchronous stores that count
+//     on the receiver's mbarrier);
+//  3. when all have arrived, every CTA knows the state at its tile's first row
+//     and, all in the same order, the state that the next round starts from;
 //  4. every warp walks its segment again from its state and writes its rows.
-// So a round costs one barrier instead of a chain of flags through global
-// memory, needs no workspace, and adds in a fixed order: the same call gives
-// the same bits. While a round runs, the next tiles are on their way.
+// So a round costs one exchange inside the cluster instead of a chain of
+// flags through global memory, needs no workspace, and adds in a fixed order:
+// the same call gives the same bits. While a round runs, the next tiles are on
+// their way. (A cluster barrier in the place of the counted stores has to be a
+// release, and then waits for the rows written in the round before.)
 //
 // Sequences are boundaries on the one axis. A segment that holds a sequence's
 // first row (for the backward pass: last row) does not depend on what comes
@@ -30,9 +33,12 @@
 //
 // The backward pass walks the rounds from the last to the first with e in the
 // place of s. It needs s_{t-1} too: the forward pass left the state before
-// every tile in `states` (1/64 of x's rows), from which each CTA recomputes
-// its tile's states by the same steps 1, 2 and 4 without any exchange.
+// every tile in `states`, from which each CTA recomputes its tile's states by
+// the same steps without any exchange. With gates per head dg is a sum over
+// the head, so there a CTA takes all 128 channels of tiles of 64 rows.
 // s and e are f32 throughout; only out, dx and dg are rounded.
+#include <type_traits>
+
 #include "gdn_linrec.cuh"
 #include "gdn_vec.cuh"
 #include "tc_ptx.cuh"
@@ -43,23 +49,56 @@ namespace {
 
 using vec::Pack;
 
-constexpr int kSeg = 8;                     // rows of a warp in a round
-constexpr int kRecWarps = kRecTile / kSeg;  // 8
+constexpr int kRecWarps = 8;
 constexpr int kRecThreads = 32 * kRecWarps;
+constexpr int kSeg = 16;  // rows of a warp in a round
+constexpr int kHalf = kSeg / 2;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxCtas = 2 * 152;  // two on each SM
 constexpr float kReset = -1.f;  // in the place of a product of decays (never negative)
 
-static_assert(kRecThreads == 2 * kHeadDim, "two threads a channel between the barriers");
+// A CTA's tile: 64 channels x 8 segments of rows, or (WIDE) 128 x 4. A warp
+// has 64 channels, two a lane, of one segment.
+template <bool WIDE>
+struct Tile {
+    static constexpr int kCh = WIDE ? 128 : 64;
+    static constexpr int kSegs = WIDE ? 4 : 8;
+    static constexpr int kRows = kSegs * kSeg;
+    static constexpr int kParts = kHeadDim / kCh;  // clusters of a head
+    static constexpr int kQ = kRecThreads / kCh;   // threads of a channel in the exchange
+    static constexpr int kPitch = kCh + 4;         // of segment rows: the exchange's reads hit every bank once
+    static constexpr int kCtaPitch = kCh + 2;      // of CTA rows (pairs of f32), likewise
+    static_assert(kRows % kStateRows == 0, "");
+
+    static __device__ __forceinline__ int seg() { return (threadIdx.x >> 5) % kSegs; }
+    // the lane's first channel in the tile
+    static __device__ __forceinline__ int channel() { return (threadIdx.x >> 5) / kSegs * 64 + (threadIdx.x & 31) * 2; }
+};
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// exp of two log-decays on the base-2 unit: with y = g log2 e rounded and r
+// what the rounding left, exp g = 2^y (1 + r ln 2), so that the only errors
+// are the unit's (2 steps) and one rounding. Below -200 (and at -inf, where r
+// would be NaN) the result is the same zero.
+__device__ __forceinline__ float2 decay2(float2 g) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g.x) : "f"(-200.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g.y) : "f"(-200.f));
+    const float2 l = make_float2(1.4426950408889634f, 1.4426950408889634f);
+    const float2 y = mul2(g, l);
+    const float2 r = mul2(fma2(g, l, make_float2(-y.x, -y.y)), make_float2(0.6931471805599453f, 0.6931471805599453f));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
+    return fma2(e, r, e);
+}
 
 // (a, b) followed by (a2, b2)
 __device__ __forceinline__ void compose(float &a, float &b, float a2, float b2) {
-    if (a2 < 0.f) {
-        a = kReset;
-        b = b2;
-    } else {
-        b = fmaf(a2, b, b2);
-        a = a < 0.f ? kReset : a * a2;
-    }
+    const float nb = fmaf(a2, b, b2), na = a * a2;
+    b = a2 < 0.f ? b2 : nb;
+    a = a < 0.f || a2 < 0.f ? kReset : na;
 }
 
 __device__ __forceinline__ float apply(float a, float b, float s) { return a < 0.f ? b : fmaf(a, s, b); }
@@ -68,16 +107,15 @@ __device__ __forceinline__ float apply(float a, float b, float s) { return a < 0
 struct Bounds {
     const int32_t *cu;
     int n, seqlen, total;
-    int next;  // packed: first offset not below the last segment asked for (monotone use)
 
     __device__ __forceinline__ int start(int i) const { return cu ? cu[i] : i * seqlen; }
 
     // bit i (0 .. kSeg): a sequence ends before, or starts at, row t0 + i.
-    // Called by whole warps; packed: the offsets are searched 32 at a time on
-    // from the last call's place (forward: t0 rises from call to call;
-    // backward: t0 falls).
+    // Called by whole warps. Packed: the offsets are searched 32 at a time
+    // from `next` on, where the last call left it (FORWARD: t0 rises from call
+    // to call and next starts at 0; else t0 falls and next starts at n + 1).
     template <bool FORWARD>
-    __device__ __forceinline__ uint32_t mask(int t0) {
+    __device__ __forceinline__ uint32_t mask(int t0, int &next) const {
         uint32_t m = 0;
         if (!cu) {
             for (int b = (t0 + seqlen - 1) / seqlen * seqlen; b <= t0 + kSeg && b <= total; b += seqlen)
@@ -85,21 +123,16 @@ struct Bounds {
             return m;
         }
         const int lane = threadIdx.x & 31;
-        if (FORWARD) {
-            for (;;) {
-                const int v = next + lane <= n ? cu[next + lane] : INT_MAX;
-                const uint32_t below = __ballot_sync(0xffffffffu, v < t0);
-                next += __popc(below);
-                if (below != 0xffffffffu) break;
+        uint32_t moved;
+        do {  // next becomes the first offset that is not below t0
+            if (FORWARD) {
+                moved = __ballot_sync(0xffffffffu, next + lane <= n && cu[next + lane] < t0);
+                next += __popc(moved);
+            } else {
+                moved = __ballot_sync(0xffffffffu, next - 1 - lane >= 0 && cu[next - 1 - lane] >= t0);
+                next -= __popc(moved);
             }
-        } else {
-            for (;;) {  // next: an offset index from which on all are >= t0 of the last call
-                const int v = next - 1 - lane >= 0 ? cu[next - 1 - lane] : INT_MIN;
-                const uint32_t above = __ballot_sync(0xffffffffu, v >= t0);
-                next -= __popc(above);
-                if (above != 0xffffffffu) break;
-            }
-        }
+        } while (moved == 0xffffffffu);
         for (int k = next;; k += 32) {
             const int v = k + lane <= n ? cu[k + lane] : INT_MAX;
             const bool in = v <= t0 + kSeg;
@@ -108,7 +141,7 @@ struct Bounds {
         }
     }
 
-    // the sequence that starts at row t (some sequence with rows does)
+    // the sequence that starts at row t (one with rows does)
     __device__ __forceinline__ int starting(int t) const {
         if (!cu) return t / seqlen;
         int lo = 0, hi = n - 1;  // the last i with cu[i] <= t
@@ -133,6 +166,22 @@ struct Bounds {
     }
 };
 
+// A lane's channels of per-sequence states [num_seqs, hv, 128], read or
+// written at a boundary. Out of line: boundaries are rare, and the walks hold
+// one such place for every row.
+template <bool ENDING>
+__device__ __noinline__ float2 boundary_load(const float *from, Bounds bd, int t, int hv, int hc) {
+    if (!from) return make_float2(0.f, 0.f);
+    return *reinterpret_cast<const float2 *>(from + (long long)(ENDING ? bd.ending(t) : bd.starting(t)) * hv * kHeadDim +
+                                             hc);
+}
+template <bool ENDING>
+__device__ __noinline__ void boundary_store(float *to, Bounds bd, int t, int hv, int hc, float2 v) {
+    *reinterpret_cast<float2 *>(to + (long long)(ENDING ? bd.ending(t) : bd.starting(t)) * hv * kHeadDim + hc) = v;
+}
+
+__device__ __forceinline__ float2 &pair(float *p) { return *reinterpret_cast<float2 *>(p); }
+
 // Offsets start at 0, do not fall and end at the last row; the same answer in
 // every CTA. A bad one is recorded.
 __device__ __forceinline__ bool offsets_ok(const RecArgs &a) {
@@ -145,114 +194,161 @@ __device__ __forceinline__ bool offsets_ok(const RecArgs &a) {
     return false;
 }
 
-// Sequences without rows: `to` gets `from` (null: zeros). One cluster per head.
-__device__ __forceinline__ void copy_empty(const RecArgs &a, const Bounds &bd, const float *from, float *to, int h,
+// Sequences without rows: `to` gets `from` (null: zeros).
+template <bool WIDE>
+__device__ __forceinline__ void copy_empty(const RecArgs &a, const Bounds &bd, const float *from, float *to, int hc,
                                            int rank, int ctas) {
     if (!to) return;
-    const int c = (threadIdx.x & 31) * 4;
-    for (int i = rank * kRecWarps + (threadIdx.x >> 5); i < a.num_seqs; i += ctas * kRecWarps) {
+    using S = Tile<WIDE>;
+    for (int i = rank * S::kSegs + S::seg(); i < a.num_seqs; i += ctas * S::kSegs) {
         if (bd.start(i) != bd.start(i + 1)) continue;
-        const long long o = ((long long)i * a.hv + h) * kHeadDim + c;
-        *reinterpret_cast<float4 *>(to + o) =
-            from ? *reinterpret_cast<const float4 *>(from + o) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const long long o = (long long)i * a.hv * kHeadDim + hc;
+        *reinterpret_cast<float2 *>(to + o) =
+            from ? *reinterpret_cast<const float2 *>(from + o) : make_float2(0.f, 0.f);
     }
 }
 
-__device__ __forceinline__ void load4(float (&v)[4], const float *p) {
-    const float4 t = *reinterpret_cast<const float4 *>(p);
-    v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-}
-__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-
-// Shared memory between the barriers of a round.
+// Shared memory of a round's exchange.
+template <bool WIDE>
 struct Exchange {
-    float seg_a[kRecWarps][kHeadDim], seg_b[kRecWarps][kHeadDim];  // segments; seg_b then the state at each
-    float cta[2][kMaxCluster][2][kHeadDim];  // by round parity: every CTA's composed segments (a, b)
+    using S = Tile<WIDE>;
+    float seg_a[S::kSegs][S::kPitch], seg_b[S::kSegs][S::kPitch];  // segments; seg_b then the state at each
+    float2 cta[2][kMaxCluster][S::kCtaPitch];  // by round parity: every CTA's composed segments (a, b)
+    uint64_t bar[2];
 };
 
-// Steps 2 and 3 for two threads a channel: composes this CTA's segments, hands
-// them to the cluster and, with everyone's, moves `carry` (the value before
-// the round) on to the next round's. seg_b becomes the value that each
-// segment starts from; returns the one that the CTA's first segment starts
-// from. REVERSE: segments and CTAs from the last to the first.
-template <bool REVERSE>
-__device__ __forceinline__ float exchange(Exchange &ex, float &carry, int parity, int rank, int ctas) {
-    using namespace tc;
-    const int c = threadIdx.x % kHeadDim, half = threadIdx.x / kHeadDim;
-    {
-        const int w0 = REVERSE ? kRecWarps - 1 : 0;
-        float a = ex.seg_a[w0][c], b = ex.seg_b[w0][c];
+// Inclusive scan over the Q lanes of a channel (lane order = walking order).
+template <int Q>
+__device__ __forceinline__ void scan_lanes(float &a, float &b, int q) {
 #pragma unroll
-        for (int i = 1; i < kRecWarps; ++i) {
-            const int w = REVERSE ? kRecWarps - 1 - i : i;
-            compose(a, b, ex.seg_a[w][c], ex.seg_b[w][c]);
-        }
-        float *slot = &ex.cta[parity][rank][half][c];
-        const float v = half ? b : a;
-        if (ctas == 1) {
-            *slot = v;
-        } else {
-            for (int r = 0; r < ctas; ++r) cluster_st(cluster_map(slot, r), v);
-        }
+    for (int m = 1; m < Q; m *= 2) {
+        float pa = __shfl_up_sync(0xffffffffu, a, m, Q), pb = __shfl_up_sync(0xffffffffu, b, m, Q);
+        compose(pa, pb, a, b);
+        if (q >= m) a = pa, b = pb;
     }
-    if (ctas == 1) __syncthreads();
-    else cluster_sync();
-    float in = carry, s = carry;
-    for (int i = 0; i < ctas; ++i) {
-        const int r = REVERSE ? ctas - 1 - i : i;
-        if (r == rank) in = s;
-        s = apply(ex.cta[parity][r][0][c], ex.cta[parity][r][1][c], s);
-    }
-    carry = s;
-    if (half == 0) {
-        s = in;
-#pragma unroll
-        for (int i = 0; i < kRecWarps; ++i) {
-            const int w = REVERSE ? kRecWarps - 1 - i : i;
-            const float b = ex.seg_b[w][c];
-            ex.seg_b[w][c] = s;
-            s = apply(ex.seg_a[w][c], b, s);
-        }
-    }
-    return in;
 }
 
-// Bytes of one stage: the tiles of x (and dout) and, with gates per channel, of g.
-template <typename T, bool CHANNEL, bool BACKWARD>
-constexpr uint32_t stage_bytes() {
-    return uint32_t(kRecTile * kHeadDim * sizeof(T)) * (1 + CHANNEL + BACKWARD);
+// A channel's segments, kQ lanes with kSegs / kQ segments each.
+template <bool WIDE, bool REVERSE>
+struct Segments {
+    using S = Tile<WIDE>;
+    static constexpr int kEach = S::kSegs / S::kQ;
+    float a[kEach], b[kEach];  // this lane's segments
+    float ia, ib;              // everything up to and with them
+
+    static __device__ __forceinline__ int seg(int q, int k) {
+        const int i = q * kEach + k;
+        return REVERSE ? S::kSegs - 1 - i : i;
+    }
+    __device__ __forceinline__ void load(const float (*sa)[S::kPitch], const float (*sb)[S::kPitch], int ch, int q) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) a[k] = sa[seg(q, k)][ch], b[k] = sb[seg(q, k)][ch];
+        ia = a[0], ib = b[0];
+#pragma unroll
+        for (int k = 1; k < kEach; ++k) compose(ia, ib, a[k], b[k]);
+        scan_lanes<S::kQ>(ia, ib, q);
+    }
+    // writes the value that each segment starts from, `in` at the first, and
+    // calls at(segment, value) for each
+    template <typename F>
+    __device__ __forceinline__ void finish(float (*sb)[S::kPitch], int ch, int q, float in, F at) {
+        const float pa = __shfl_up_sync(0xffffffffu, ia, 1, S::kQ), pb = __shfl_up_sync(0xffffffffu, ib, 1, S::kQ);
+        float s = q ? apply(pa, pb, in) : in;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            sb[seg(q, k)][ch] = s;
+            at(seg(q, k), s);
+            s = apply(a[k], b[k], s);
+        }
+    }
+};
+
+// Steps 2 and 3, all threads, after the segments are in shared memory: moves
+// `carry` (the value before the round) on to the next round's; seg_b becomes
+// the value that each segment starts from, which at(segment, value) gets too.
+// REVERSE: segments and CTAs from the last to the first. ok turns false when a
+// wait runs out (later ones are skipped).
+template <bool WIDE, bool REVERSE, typename F>
+__device__ __forceinline__ void exchange(Exchange<WIDE> &ex, float &carry, int round, int rank, int ctas, bool &ok,
+                                         unsigned long long limit, F at) {
+    using namespace tc;
+    using S = Tile<WIDE>;
+    constexpr int Q = S::kQ, kRanks = kMaxCluster / Q;
+    const int ch = threadIdx.x / Q, q = threadIdx.x % Q, p = round & 1;
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&ex.bar[p], uint32_t(ctas) * S::kCh * 8);
+    Segments<WIDE, REVERSE> sg;
+    sg.load(ex.seg_a, ex.seg_b, ch, q);
+    {
+        const float ta = __shfl_sync(0xffffffffu, sg.ia, Q - 1, Q), tb = __shfl_sync(0xffffffffu, sg.ib, Q - 1, Q);
+#pragma unroll
+        for (int k = 0; k < kRanks; ++k) {
+            const int r = k * Q + q;
+            if (r < ctas)
+                cluster_st_async(cluster_map(&ex.cta[p][rank][ch], r), ta, tb, cluster_map(&ex.bar[p], r));
+        }
+    }
+    if (ok && !mbar_wait_cluster(&ex.bar[p], uint32_t(round >> 1) & 1, limit)) ok = false;
+    // ranks in walking order, kRanks a lane
+    const int mine = REVERSE ? ctas - 1 - rank : rank;
+    float2 v[kRanks];
+#pragma unroll
+    for (int k = 0; k < kRanks; ++k) {
+        const int i = q * kRanks + k;
+        v[k] = i < ctas ? ex.cta[p][REVERSE ? ctas - 1 - i : i][ch] : make_float2(1.f, 0.f);
+    }
+    float a = v[0].x, b = v[0].y;
+#pragma unroll
+    for (int k = 1; k < kRanks; ++k) compose(a, b, v[k].x, v[k].y);
+    scan_lanes<Q>(a, b, q);
+    const float pa = __shfl_up_sync(0xffffffffu, a, 1, Q), pb = __shfl_up_sync(0xffffffffu, b, 1, Q);
+    float s = q ? apply(pa, pb, carry) : carry, in = s;
+#pragma unroll
+    for (int k = 0; k < kRanks; ++k) {
+        if (q * kRanks + k == mine) in = s;
+        s = apply(v[k].x, v[k].y, s);
+    }
+    carry = __shfl_sync(0xffffffffu, s, Q - 1, Q);
+    in = __shfl_sync(0xffffffffu, in, mine / kRanks, Q);
+    sg.finish(ex.seg_b, ch, q, in, at);
 }
-template <bool BACKWARD>
-constexpr int stages() { return BACKWARD ? 1 : 2; }
 
 // Tile loads through a ring of stages: one thread issues, everyone waits.
 template <typename T, bool CHANNEL, bool BACKWARD>
 struct Ring {
-    static constexpr int kStages = stages<BACKWARD>();
-    static constexpr uint32_t kTile = kRecTile * kHeadDim * sizeof(T);
+    using S = Tile<BACKWARD && !CHANNEL>;
+    static constexpr int kTile = S::kRows * S::kCh;                                 // elements of one tensor's tile
+    static constexpr uint32_t kTiles = kTile * sizeof(T) * (1 + CHANNEL + BACKWARD);  // x, g per channel, dout
+    static constexpr uint32_t kState = BACKWARD ? S::kCh * 4 : 0;                     // the state before the tile
+    static constexpr uint32_t kBytes = kTiles + kState;
+    // two CTAs of an SM have two stages each where they fit
+    static constexpr int kStages = kTiles <= 32768 ? 2 : 1;
+    static constexpr size_t kSmem = size_t(kStages) * kBytes + 128;
     uint8_t *base;
     uint64_t *full;
-    bool dead;  // a wait ran out: later ones are skipped
 
-    __device__ __forceinline__ const T *x(int i) const {
-        return reinterpret_cast<const T *>(base + (i % kStages) * stage_bytes<T, CHANNEL, BACKWARD>());
+    __device__ __forceinline__ const T *x(int i) const { return reinterpret_cast<const T *>(base + (i % kStages) * kBytes); }
+    __device__ __forceinline__ const T *g(int i) const { return x(i) + kTile; }
+    __device__ __forceinline__ const T *dout(int i) const { return x(i) + (1 + CHANNEL) * kTile; }
+
+    __device__ __forceinline__ const float *state(int i) const {
+        return reinterpret_cast<const float *>(base + (i % kStages) * kBytes + kTiles);
     }
-    __device__ __forceinline__ const T *g(int i) const { return x(i) + kRecTile * kHeadDim; }
-    __device__ __forceinline__ const T *dout(int i) const { return x(i) + (1 + CHANNEL) * kRecTile * kHeadDim; }
 
-    // by one thread: tile i of this CTA's walk, rows from t0 of head h
+    // by one thread: tile i of this CTA's walk, rows from t0, channels from c0 of head h
     __device__ __forceinline__ void load(int i, const CUtensorMap *mx, const CUtensorMap *mg, const CUtensorMap *md,
-                                         int h, int t0) {
+                                         const RecArgs &a, int c0, int h, int t0) {
         uint64_t *bar = &full[i % kStages];
-        tc::mbar_arrive_expect_tx(bar, stage_bytes<T, CHANNEL, BACKWARD>());
-        tc::tma_load_3d(const_cast<T *>(x(i)), mx, 0, h, t0, bar);
-        if (CHANNEL) tc::tma_load_3d(const_cast<T *>(g(i)), mg, 0, h, t0, bar);
-        if (BACKWARD) tc::tma_load_3d(const_cast<T *>(dout(i)), md, 0, h, t0, bar);
+        const bool state = BACKWARD && t0 < a.total_tokens;
+        tc::mbar_arrive_expect_tx(bar, state ? kBytes : kTiles);
+        if (state)
+            tc::bulk_load(base + (i % kStages) * kBytes + kTiles,
+                          a.states + ((long long)(t0 / kStateRows) * a.hv + h) * kHeadDim + c0, kState, bar);
+        tc::tma_load_3d(const_cast<T *>(x(i)), mx, c0, h, t0, bar);
+        if (CHANNEL) tc::tma_load_3d(const_cast<T *>(g(i)), mg, c0, h, t0, bar);
+        if (BACKWARD) tc::tma_load_3d(const_cast<T *>(dout(i)), md, c0, h, t0, bar);
     }
-    __device__ __forceinline__ void wait(int i, unsigned long long limit) {
-        if (!dead && !tc::mbar_wait(&full[i % kStages], uint32_t((i / kStages) & 1), limit)) dead = true;
+    __device__ __forceinline__ void wait(int i, bool &ok, unsigned long long limit) {
+        if (ok && !tc::mbar_wait(&full[i % kStages], uint32_t((i / kStages) & 1), limit)) ok = false;
     }
 };
 
@@ -264,280 +360,322 @@ __device__ __forceinline__ float head_gate(const RecArgs &a, int t0, int h) {
                                                      : 0.f;
 }
 
-// Decays of a segment's rows, from the tile of gates per channel or from head_gate's value.
+// Decays of a segment's rows for the lane's two channels, and what the walks
+// do with them: packed operations on pairs of their own, scalar ones on the
+// head's one value.
 template <typename T, bool CHANNEL>
-__device__ __forceinline__ void decays(float (&a)[kSeg][4], const T *g_tile, float g_head) {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const float v = CHANNEL ? 0.f : expf(g_head);
+struct Decays;
+template <typename T>
+struct Decays<T, true> {
+    using Product = float2;
+    float2 d[kSeg];
+    __device__ __forceinline__ Decays(const T *g_tile, float) {
 #pragma unroll
-    for (int i = 0; i < kSeg; ++i) {
-        if (CHANNEL) {
-            Pack<T, 4> p;
-            p.load(g_tile + (w * kSeg + i) * kHeadDim + lane * 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[i][j] = expf(p.f(j));
-        } else {
-            a[i][0] = a[i][1] = a[i][2] = a[i][3] = __shfl_sync(0xffffffffu, v, i);
+        for (int i = 0; i < kSeg; ++i) {
+            Pack<T, 2> p;
+            p.load(g_tile + i * Tile<false>::kCh);
+            d[i] = decay2(make_float2(p.f(0), p.f(1)));
         }
+    }
+    __device__ __forceinline__ float2 fma(int i, float2 s, float2 x) const { return fma2(d[i], s, x); }
+    __device__ __forceinline__ float2 mul(int i, float2 s) const { return mul2(d[i], s); }
+    __device__ __forceinline__ float2 product() const {
+        float2 p = d[0];
+#pragma unroll
+        for (int i = 1; i < kSeg; ++i) p = mul2(p, d[i]);
+        return p;
+    }
+};
+template <typename T>
+struct Decays<T, false> {
+    float d[kSeg];
+    __device__ __forceinline__ Decays(const T *, float g_head) {
+        const float t = decay2(make_float2(g_head, g_head)).x;
+#pragma unroll
+        for (int i = 0; i < kSeg; ++i) d[i] = __shfl_sync(0xffffffffu, t, i);
+    }
+    __device__ __forceinline__ float2 fma(int i, float2 s, float2 x) const {
+        return make_float2(fmaf(d[i], s.x, x.x), fmaf(d[i], s.y, x.y));
+    }
+    __device__ __forceinline__ float2 mul(int i, float2 s) const {
+        return make_float2(__fmul_rn(d[i], s.x), __fmul_rn(d[i], s.y));
+    }
+    __device__ __forceinline__ float2 product() const {
+        float p = d[0];
+#pragma unroll
+        for (int i = 1; i < kSeg; ++i) p = __fmul_rn(p, d[i]);
+        return make_float2(p, p);
+    }
+};
+
+// A walk over a segment, one body(row, checked) a row: most segments hold no
+// boundary and no row past the end, and run without the checks for them.
+template <int FROM, int TO, typename F>
+__device__ __forceinline__ void walk(bool plain, F body) {
+    constexpr int kStep = FROM <= TO ? 1 : -1, kCount = (FROM <= TO ? TO - FROM : FROM - TO) + 1;
+    if (plain) {
+#pragma unroll
+        for (int n = 0; n < kCount; ++n) body(FROM + kStep * n, std::false_type{});
+    } else {
+#pragma unroll
+        for (int n = 0; n < kCount; ++n) body(FROM + kStep * n, std::true_type{});
     }
 }
 
+__device__ __forceinline__ float2 f2(const Pack<float, 2> &p) { return make_float2(p.e[0], p.e[1]); }
+__device__ __forceinline__ float2 f2(const Pack<__nv_bfloat16, 2> &p) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&p.r));
+}
+template <typename T>
+__device__ __forceinline__ void store2(T *to, float2 v);
+template <>
+__device__ __forceinline__ void store2<float>(float *to, float2 v) { *reinterpret_cast<float2 *>(to) = v; }
+template <>
+__device__ __forceinline__ void store2<__nv_bfloat16>(__nv_bfloat16 *to, float2 v) {
+    *reinterpret_cast<__nv_bfloat162 *>(to) = __floats2bfloat162_rn(v.x, v.y);
+}
+
 template <typename T, bool CHANNEL>
-__global__ void __launch_bounds__(kRecThreads)
+__global__ void __launch_bounds__(kRecThreads, 2)
 k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg, int ctas) {
     using namespace tc;
+    using R = Ring<T, CHANNEL, false>;
+    using S = typename R::S;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Exchange ex;
-    __shared__ uint64_t full[stages<false>()];
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane * 4;
-    const int rank = ctas == 1 ? 0 : int(cluster_ctarank()), h = int(blockIdx.x) / ctas;
-    if (!offsets_ok(a)) return;  // the same in every CTA
-    Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens, 0};
-    copy_empty(a, bd, a.s0, a.final_state, h, rank, ctas);
-    const int tiles = (a.total_tokens + kRecTile - 1) / kRecTile;
+    __shared__ Exchange<false> ex;
+    __shared__ uint64_t full[R::kStages];
+    const int w = S::seg(), c = S::channel();
+    const int rank = int(cluster_ctarank()), unit = int(blockIdx.x) / ctas;
+    const int h = unit / S::kParts, c0 = unit % S::kParts * S::kCh;
+    const int hc = h * kHeadDim + c0 + c;  // this lane's first channel in a row [hv, 128]
+    if (!offsets_ok(a)) return;            // the same in every CTA
+    const Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens};
+    copy_empty<false>(a, bd, a.s0, a.final_state, hc, rank, ctas);
+    const int tiles = (a.total_tokens + S::kRows - 1) / S::kRows;
     const int rounds = (tiles + ctas - 1) / ctas;
     if (!rounds) return;
-    Ring<T, CHANNEL, false> ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)),
-                                 full, false};
+    R ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)), full};
     if (threadIdx.x == 0) {
-        for (int i = 0; i < ring.kStages; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < R::kStages; ++i) mbar_init(&full[i], 1);
+        mbar_init(&ex.bar[0], 1);
+        mbar_init(&ex.bar[1], 1);
         fence_mbar_init();
-        for (int i = 0; i < ring.kStages && i < rounds; ++i)
-            ring.load(i, &mx, &mg, nullptr, h, (i * ctas + rank) * kRecTile);
+        for (int i = 0; i < R::kStages && i < rounds; ++i)
+            ring.load(i, &mx, &mg, nullptr, a, c0, h, (i * ctas + rank) * S::kRows);
     }
-    __syncthreads();
-    if (ctas > 1) cluster_sync();  // every CTA of the cluster runs before its shared memory is written
-    float carry = 0.f;  // of channel threadIdx.x % 128, before the round
-    float gate = CHANNEL ? 0.f : head_gate(a, rank * kRecTile + w * kSeg, h);
+    cluster_sync();  // every CTA's barriers are ready
+    float carry = 0.f;  // of this thread's channel in the exchange, before the round
+    float gate = CHANNEL ? 0.f : head_gate(a, rank * S::kRows + w * kSeg, h);
+    bool ok = true;
+    int next = 0;
+    const long long pitch = (long long)a.hv * kHeadDim;
     for (int round = 0; round < rounds; ++round) {
-        const int tile = round * ctas + rank, t0 = tile * kRecTile + w * kSeg;
-        const uint32_t starts = t0 < a.total_tokens ? bd.mask<true>(t0) : 0u;  // bit kSeg: before the next segment
-        ring.wait(round, a.wait_ns);
-        float d[kSeg][4];
-        Pack<T, 4> x[kSeg];
-        decays<T, CHANNEL>(d, ring.g(round), gate);
-        if (!CHANNEL) gate = head_gate(a, t0 + ctas * kRecTile, h);
-        const T *xt = ring.x(round) + w * kSeg * kHeadDim + c;
-        float A[4] = {1.f, 1.f, 1.f, 1.f}, B[4] = {0.f, 0.f, 0.f, 0.f};
-        bool reset = false;
+        const int t0 = (round * ctas + rank) * S::kRows, tw = t0 + w * kSeg;  // the tile's and the warp's first row
+        const int rows = min(kSeg, a.total_tokens - tw);                     // may be negative
+        uint32_t starts = 0;  // bit kSeg: before the next segment
+        if (rows > 0) starts = bd.mask<true>(tw, next);
+        ring.wait(round, ok, a.wait_ns);
+        Pack<T, 2> x[kSeg];
+        const int o = w * kSeg * S::kCh + c;
 #pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
-            x[i].load(xt + i * kHeadDim);
-            if ((starts >> i & 1) && t0 + i < a.total_tokens) {
-                reset = true;
-                if (a.s0)
-                    load4(B, a.s0 + ((long long)bd.starting(t0 + i) * a.hv + h) * kHeadDim + c);
-                else
-                    B[0] = B[1] = B[2] = B[3] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                B[j] = fmaf(d[i][j], B[j], x[i].f(j));
-                A[j] *= d[i][j];
-            }
+        for (int i = 0; i < kSeg; ++i) x[i].load(ring.x(round) + o + i * S::kCh);
+        const Decays<T, CHANNEL> d(ring.g(round) + o, gate);
+        if (!CHANNEL) gate = head_gate(a, tw + ctas * S::kRows, h);
+        const bool plain = starts == 0 && rows == kSeg;
+        {
+            float2 A = d.product(), B = make_float2(0.f, 0.f);
+            walk<0, kSeg - 1>(plain, [&](int i, auto checked) {
+                if (checked && (starts >> i & 1) && i < rows) B = boundary_load<false>(a.s0, bd, tw + i, a.hv, hc);
+                B = d.fma(i, B, f2(x[i]));
+            });
+            if (starts & ((1u << max(rows, 0)) - 1)) A = make_float2(kReset, kReset);
+            pair(&ex.seg_a[w][c]) = A;
+            pair(&ex.seg_b[w][c]) = B;
         }
-        if (reset) A[0] = A[1] = A[2] = A[3] = kReset;
-        store4(&ex.seg_a[w][c], A);
-        store4(&ex.seg_b[w][c], B);
         __syncthreads();
         // the tile is in registers: its stage takes a later one
-        if (threadIdx.x == 0 && round + ring.kStages < rounds)
-            ring.load(round + ring.kStages, &mx, &mg, nullptr, h, (tile + ring.kStages * ctas) * kRecTile);
-        const float in = exchange<false>(ex, carry, round & 1, rank, ctas);
-        if (a.states && tile < tiles && threadIdx.x < kHeadDim)
-            a.states[((long long)tile * a.hv + h) * kHeadDim + threadIdx.x] = in;
+        if (threadIdx.x == 0 && round + R::kStages < rounds)
+            ring.load(round + R::kStages, &mx, &mg, nullptr, a, c0, h, t0 + R::kStages * ctas * S::kRows);
+        __syncwarp();
+        exchange<false, false>(ex, carry, round, rank, ctas, ok, a.wait_ns, [&](int seg, float s) {
+            const int t = t0 + seg * kSeg;
+            if (a.states && t % kStateRows == 0 && t < a.total_tokens)
+                a.states[(long long)(t / kStateRows) * pitch + h * kHeadDim + c0 + threadIdx.x / S::kQ] = s;
+        });
         __syncthreads();
-        float s[4];
-        load4(s, &ex.seg_b[w][c]);
-        T *out = static_cast<T *>(a.out) + ((long long)t0 * a.hv + h) * kHeadDim + c;
-#pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
-            if (t0 + i >= a.total_tokens) break;
-            if (starts >> i & 1) {
-                if (a.s0)
-                    load4(s, a.s0 + ((long long)bd.starting(t0 + i) * a.hv + h) * kHeadDim + c);
-                else
-                    s[0] = s[1] = s[2] = s[3] = 0.f;
+        float2 s = pair(&ex.seg_b[w][c]);
+        T *out = static_cast<T *>(a.out) + tw * pitch + hc;
+        walk<0, kSeg - 1>(plain, [&](int i, auto checked) {
+            if (checked) {
+                if (i >= rows) return;
+                if (starts >> i & 1) s = boundary_load<false>(a.s0, bd, tw + i, a.hv, hc);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[j] = fmaf(d[i][j], s[j], x[i].f(j));
-                x[i].set(j, s[j]);
-            }
-            x[i].store(out + (long long)i * a.hv * kHeadDim);
-            if (a.final_state && (starts >> (i + 1) & 1))
-                store4(a.final_state + ((long long)bd.ending(t0 + i) * a.hv + h) * kHeadDim + c, s);
-        }
+            s = d.fma(i, s, f2(x[i]));
+            store2(out, s);
+            out += pitch;
+            if (checked && a.final_state && (starts >> (i + 1) & 1))
+                boundary_store<true>(a.final_state, bd, tw + i, a.hv, hc, s);
+        });
     }
-    if (ring.dead && lane == 0) record_status(a.status, GDN_ETIMEOUT);
+    if (!ok && (threadIdx.x & 31) == 0) record_status(a.status, GDN_ETIMEOUT);
+    cluster_sync_relaxed();  // no CTA leaves while others may still store to it
 }
 
 template <typename T, bool CHANNEL>
-__global__ void __launch_bounds__(kRecThreads)
+__global__ void __launch_bounds__(kRecThreads, sizeof(T) == 2 ? 2 : 1)
 k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
              const __grid_constant__ CUtensorMap md, int ctas) {
     using namespace tc;
+    using R = Ring<T, CHANNEL, true>;
+    using S = typename R::S;
+    constexpr bool WIDE = !CHANNEL;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Exchange ex;
-    __shared__ float fwd_a[kRecWarps][kHeadDim], fwd_b[kRecWarps][kHeadDim];
-    __shared__ uint64_t full[stages<true>()];
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane * 4;
-    const int rank = ctas == 1 ? 0 : int(cluster_ctarank()), h = int(blockIdx.x) / ctas;
+    __shared__ Exchange<WIDE> ex;
+    __shared__ float fwd_a[S::kSegs][S::kPitch], fwd_b[S::kSegs][S::kPitch];
+    __shared__ float head_sums[CHANNEL ? 1 : 2][2][CHANNEL ? 1 : S::kRows];  // by round parity, half of the head, row
+    __shared__ uint64_t full[R::kStages];
+    const int w = S::seg(), c = S::channel(), lane = threadIdx.x & 31;
+    const int rank = int(cluster_ctarank()), unit = int(blockIdx.x) / ctas;
+    const int h = unit / S::kParts, c0 = unit % S::kParts * S::kCh;
+    const int hc = h * kHeadDim + c0 + c;
     if (!offsets_ok(a)) return;
-    Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens, a.num_seqs + 1};
-    copy_empty(a, bd, a.dfinal, a.dinitial, h, rank, ctas);
-    const int tiles = (a.total_tokens + kRecTile - 1) / kRecTile;
+    const Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens};
+    copy_empty<WIDE>(a, bd, a.dfinal, a.dinitial, hc, rank, ctas);
+    const int tiles = (a.total_tokens + S::kRows - 1) / S::kRows;
     const int rounds = (tiles + ctas - 1) / ctas;
     if (!rounds) return;
-    Ring<T, CHANNEL, true> ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)),
-                                full, false};
+    R ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)), full};
     if (threadIdx.x == 0) {
-        for (int i = 0; i < ring.kStages; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < R::kStages; ++i) mbar_init(&full[i], 1);
+        mbar_init(&ex.bar[0], 1);
+        mbar_init(&ex.bar[1], 1);
         fence_mbar_init();
-        for (int i = 0; i < ring.kStages && i < rounds; ++i)
-            ring.load(i, &mx, &mg, &md, h, ((rounds - 1 - i) * ctas + rank) * kRecTile);
+        for (int i = 0; i < R::kStages && i < rounds; ++i)
+            ring.load(i, &mx, &mg, &md, a, c0, h, ((rounds - 1 - i) * ctas + rank) * S::kRows);
     }
-    __syncthreads();
-    if (ctas > 1) cluster_sync();
+    cluster_sync();
     float carry = 0.f;
-    float gate = CHANNEL ? 0.f : head_gate(a, ((rounds - 1) * ctas + rank) * kRecTile + w * kSeg, h);
+    float gate = CHANNEL ? 0.f : head_gate(a, ((rounds - 1) * ctas + rank) * S::kRows + w * kSeg, h);
+    bool ok = true;
+    int next = a.num_seqs + 1;
+    const long long pitch = (long long)a.hv * kHeadDim;
+    // dg per head of the tile at row t: the sums of the head's two halves
+    auto write_head_sums = [&](int parity, int t) {
+        const int r = threadIdx.x;
+        if (r < S::kRows && t + r < a.total_tokens)
+            static_cast<float *>(a.dg)[(long long)(t + r) * a.hv + h] = head_sums[parity][0][r] + head_sums[parity][1][r];
+    };
     for (int round = 0; round < rounds; ++round) {
-        const int tile = (rounds - 1 - round) * ctas + rank, t0 = tile * kRecTile + w * kSeg;
-        const uint32_t bounds = t0 < a.total_tokens ? bd.mask<false>(t0) : 0u;
-        // the state before the tile, of this thread's channel (unused where the tile starts a sequence)
-        float state = 0.f;
-        if (threadIdx.x >= kHeadDim && tile < tiles)
-            state = a.states[((long long)tile * a.hv + h) * kHeadDim + threadIdx.x - kHeadDim];
-        ring.wait(round, a.wait_ns);
-        float d[kSeg][4];
-        Pack<T, 4> x[kSeg], dy[kSeg];
-        decays<T, CHANNEL>(d, ring.g(round), gate);
-        if (!CHANNEL && round + 1 < rounds) gate = head_gate(a, t0 - ctas * kRecTile, h);
-        const T *xt = ring.x(round) + w * kSeg * kHeadDim + c, *yt = ring.dout(round) + w * kSeg * kHeadDim + c;
-        // the rows' maps: forward for s, in reverse for e
-        {
-            float A[4] = {1.f, 1.f, 1.f, 1.f}, B[4] = {0.f, 0.f, 0.f, 0.f};
-            bool reset = false;
-#pragma unroll
-            for (int i = 0; i < kSeg; ++i) {
-                x[i].load(xt + i * kHeadDim);
-                dy[i].load(yt + i * kHeadDim);
-                if ((bounds >> i & 1) && t0 + i < a.total_tokens) {
-                    reset = true;
-                    if (a.s0)
-                        load4(B, a.s0 + ((long long)bd.starting(t0 + i) * a.hv + h) * kHeadDim + c);
-                    else
-                        B[0] = B[1] = B[2] = B[3] = 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    B[j] = fmaf(d[i][j], B[j], x[i].f(j));
-                    A[j] *= d[i][j];
-                }
-            }
-            float R[4] = {A[0], A[1], A[2], A[3]};
-            if (reset) A[0] = A[1] = A[2] = A[3] = kReset;
-            store4(&fwd_a[w][c], A);
-            store4(&fwd_b[w][c], B);
-            float E[4] = {0.f, 0.f, 0.f, 0.f};
-            reset = false;
-#pragma unroll
-            for (int i = kSeg - 1; i >= 0; --i) {
-                if (bounds >> (i + 1) & 1) {
-                    reset = true;
-                    if (a.dfinal && t0 + i < a.total_tokens)
-                        load4(E, a.dfinal + ((long long)bd.ending(t0 + i) * a.hv + h) * kHeadDim + c);
-                    else
-                        E[0] = E[1] = E[2] = E[3] = 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) E[j] = d[i][j] * (dy[i].f(j) + E[j]);
-            }
-            if (reset) R[0] = R[1] = R[2] = R[3] = kReset;
-            store4(&ex.seg_a[w][c], R);
-            store4(&ex.seg_b[w][c], E);
-        }
-        __syncthreads();
-        if (threadIdx.x == 0 && round + ring.kStages < rounds)
-            ring.load(round + ring.kStages, &mx, &mg, &md, h, (tile - ring.kStages * ctas) * kRecTile);
-        exchange<true>(ex, carry, round & 1, rank, ctas);
-        if (threadIdx.x >= kHeadDim) {  // the other half of the threads: the state at every segment
-            const int ch = threadIdx.x - kHeadDim;
-#pragma unroll
-            for (int i = 0; i < kRecWarps; ++i) {
-                const float b = fwd_b[i][ch];
-                fwd_b[i][ch] = state;
-                state = apply(fwd_a[i][ch], b, state);
-            }
-        }
-        __syncthreads();
-        float before[kSeg][4], s[4];
-        load4(s, &fwd_b[w][c]);
+        const int t0 = ((rounds - 1 - round) * ctas + rank) * S::kRows, tw = t0 + w * kSeg;
+        const int rows = min(kSeg, a.total_tokens - tw);
+        uint32_t bounds = 0;
+        if (rows > 0) bounds = bd.mask<false>(tw, next);
+        // the segment's rows that start (s is reset) and end (e is reset) a sequence
+        const uint32_t starts = bounds & ((1u << max(rows, 0)) - 1), ends = bounds >> 1;
+        const bool plain = bounds == 0 && rows == kSeg;
+        ring.wait(round, ok, a.wait_ns);
+        const float state = ring.state(round)[threadIdx.x / S::kQ];  // unused where the tile starts a sequence
+        Pack<T, 2> x[kSeg], dy[kSeg];
+        const int o = w * kSeg * S::kCh + c;
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
-            if ((bounds >> i & 1) && t0 + i < a.total_tokens) {
-                if (a.s0)
-                    load4(s, a.s0 + ((long long)bd.starting(t0 + i) * a.hv + h) * kHeadDim + c);
-                else
-                    s[0] = s[1] = s[2] = s[3] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                before[i][j] = s[j];
-                s[j] = fmaf(d[i][j], s[j], x[i].f(j));
-            }
+            x[i].load(ring.x(round) + o + i * S::kCh);
+            dy[i].load(ring.dout(round) + o + i * S::kCh);
         }
-        float e[4], sums[kSeg];
-        load4(e, &ex.seg_b[w][c]);
-        const long long row0 = ((long long)t0 * a.hv + h) * kHeadDim + c;
-#pragma unroll
-        for (int i = kSeg - 1; i >= 0; --i) {
-            const bool live = t0 + i < a.total_tokens;
-            if (bounds >> (i + 1) & 1) {
-                if (a.dfinal && live)
-                    load4(e, a.dfinal + ((long long)bd.ending(t0 + i) * a.hv + h) * kHeadDim + c);
-                else
-                    e[0] = e[1] = e[2] = e[3] = 0.f;
-            }
-            sums[i] = 0.f;
-            Pack<T, 4> q;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float ds = dy[i].f(j) + e[j];
-                dy[i].set(j, ds);
-                e[j] = d[i][j] * ds;
-                const float dg = e[j] * before[i][j];
-                if (CHANNEL) q.set(j, dg);
-                else sums[i] += dg;
-            }
-            if (live) {
-                const long long row = row0 + (long long)i * a.hv * kHeadDim;
-                dy[i].store(static_cast<T *>(a.dx) + row);
-                if (CHANNEL) q.store(static_cast<T *>(a.dg) + row);
-                if (a.dinitial && (bounds >> i & 1))
-                    store4(a.dinitial + ((long long)bd.starting(t0 + i) * a.hv + h) * kHeadDim + c, e);
-            }
+        const Decays<T, CHANNEL> d(ring.g(round) + o, gate);
+        if (!CHANNEL && round + 1 < rounds) gate = head_gate(a, tw - ctas * S::kRows, h);
+        // the rows' maps: forward for s, in reverse for e
+        {
+            const float2 A = d.product();
+            float2 B = make_float2(0.f, 0.f), E = make_float2(0.f, 0.f);
+            walk<0, kSeg - 1>(plain, [&](int i, auto checked) {
+                if (checked && (starts >> i & 1)) B = boundary_load<false>(a.s0, bd, tw + i, a.hv, hc);
+                B = d.fma(i, B, f2(x[i]));
+            });
+            walk<kSeg - 1, 0>(plain, [&](int i, auto checked) {
+                if (checked && (ends >> i & 1)) E = boundary_load<true>(a.dfinal, bd, tw + i, a.hv, hc);
+                E = d.mul(i, __fadd2_rn(f2(dy[i]), E));
+            });
+            const float2 reset = make_float2(kReset, kReset);
+            pair(&fwd_a[w][c]) = starts ? reset : A;
+            pair(&fwd_b[w][c]) = B;
+            pair(&ex.seg_a[w][c]) = ends ? reset : A;
+            pair(&ex.seg_b[w][c]) = E;
         }
-        if (!CHANNEL) {
-            // eight rows' sums over the head's channels: lanes halve the rows they add, lane 4 r ends with row r
-#pragma unroll
-            for (int m = 16, k = kSeg / 2; k; m >>= 1, k >>= 1) {
-                const bool up = lane & m;
-#pragma unroll
-                for (int i = 0; i < k; ++i) {
-                    const float send = up ? sums[i] : sums[i + k], keep = up ? sums[i + k] : sums[i];
-                    sums[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+        __syncthreads();
+        if (threadIdx.x == 0 && round + R::kStages < rounds)
+            ring.load(round + R::kStages, &mx, &mg, &md, a, c0, h, t0 - R::kStages * ctas * S::kRows);
+        __syncwarp();
+        if (!CHANNEL && round) write_head_sums((round - 1) & 1, t0 + ctas * S::kRows);
+        exchange<WIDE, true>(ex, carry, round, rank, ctas, ok, a.wait_ns, [](int, float) {});
+        {
+            const int ch = threadIdx.x / S::kQ, q = threadIdx.x % S::kQ;
+            Segments<WIDE, false> sg;
+            sg.load(fwd_a, fwd_b, ch, q);
+            sg.finish(fwd_b, ch, q, state, [](int, float) {});
+        }
+        __syncthreads();
+        // The segment's states are kept for half of its rows at a time, the
+        // last half first: half the registers for one more walk over the
+        // first half.
+        float2 e = pair(&ex.seg_b[w][c]);
+        const float2 s0 = pair(&fwd_b[w][c]);
+        T *dx = static_cast<T *>(a.dx) + (tw + kSeg - 1) * pitch + hc;
+        T *dgc = static_cast<T *>(a.dg) + (tw + kSeg - 1) * pitch + hc;  // per channel
+        auto half_walk = [&](auto half_) {
+            constexpr int half = decltype(half_)::value;
+            float2 s = s0, before[kHalf];
+            walk<0, (half + 1) * kHalf - 1>(plain, [&](int i, auto checked) {
+                if (checked && (starts >> i & 1)) s = boundary_load<false>(a.s0, bd, tw + i, a.hv, hc);
+                if (i >= half * kHalf) before[i % kHalf] = s;
+                s = d.fma(i, s, f2(x[i]));
+            });
+            float sums[kHalf];
+            walk<half * kHalf + kHalf - 1, half * kHalf>(plain, [&](int i, auto checked) {
+                if (checked && (ends >> i & 1)) e = boundary_load<true>(a.dfinal, bd, tw + i, a.hv, hc);
+                const float2 ds = __fadd2_rn(f2(dy[i]), e);
+                e = d.mul(i, ds);
+                const float2 dg = mul2(e, before[i % kHalf]);
+                if (!CHANNEL) sums[i % kHalf] = dg.x + dg.y;
+                if (!checked || i < rows) {
+                    store2(dx, ds);
+                    if (CHANNEL) store2(dgc, dg);
+                    if (checked && a.dinitial && (starts >> i & 1))
+                        boundary_store<false>(a.dinitial, bd, tw + i, a.hv, hc, e);
                 }
+                dx -= pitch;
+                dgc -= pitch;
+            });
+            if (!CHANNEL) {
+                // eight rows' sums over the warp's channels: lanes halve the
+                // rows they add, lane 4 r ends with row r
+#pragma unroll
+                for (int m = 16, k = kHalf / 2; k; m >>= 1, k >>= 1) {
+                    const bool up = lane & m;
+#pragma unroll
+                    for (int i = 0; i < k; ++i) {
+                        const float send = up ? sums[i] : sums[i + k], keep = up ? sums[i + k] : sums[i];
+                        sums[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                    }
+                }
+                sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 2);
+                sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 1);
+                // written out after the next round's first barrier
+                if ((lane & 3) == 0) head_sums[round & 1][c / 64][w * kSeg + half * kHalf + (lane >> 2)] = sums[0];
             }
-            sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 2);
-            sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 1);
-            const int r = lane >> 2;
-            if ((lane & 3) == 0 && t0 + r < a.total_tokens)
-                static_cast<float *>(a.dg)[(long long)(t0 + r) * a.hv + h] = sums[0];
-        }
+        };
+        half_walk(std::integral_constant<int, 1>{});
+        half_walk(std::integral_constant<int, 0>{});
     }
-    if (ring.dead && lane == 0) record_status(a.status, GDN_ETIMEOUT);
+    if (!CHANNEL) {
+        __syncthreads();
+        write_head_sums((rounds - 1) & 1, rank * S::kRows);
+    }
+    if (!ok && lane == 0) record_status(a.status, GDN_ETIMEOUT);
+    cluster_sync_relaxed();
 }
+
+static_assert(kHalf == 8, "the sums over a head's channels take eight rows at a time");
 
 // Decode step: a warp takes one (sequence, head) row, four channels a lane.
 // HBM-bound (state read and written, x and out); every access of a warp is
@@ -579,22 +717,25 @@ k_linrec_step(const void *x_, const void *g_, float *state, const int32_t *idx, 
     px.store(static_cast<T *>(out_) + i);
 }
 
-// CTAs of a cluster: as many as there are tiles, at most the portable eight
-int cluster_of(int total) {
-    const int tiles = (total + kRecTile - 1) / kRecTile;
-    int c = 1;
-    while (c < kMaxCluster && c < tiles) c *= 2;
-    return c;
+// CTAs of a cluster: the more, the more of the time axis is in work, but not
+// more than there are tiles, than the portable eight, or than lets all
+// clusters run at once (two CTAs an SM): a second wave of clusters would start
+// on the whole axis when the first is done.
+int cluster_of(int total, int rows, int units) {
+    const int tiles = (total + rows - 1) / rows;
+    int c = kMaxCtas / units;
+    c = c < tiles ? c : tiles;
+    return c < 1 ? 1 : c < kMaxCluster ? c : kMaxCluster;
 }
 
-// launches `fn` with one cluster of `ctas` CTAs a head
+// launches `fn` with `units` clusters of `ctas` CTAs
 template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*fn)(P...), int hv, int ctas, size_t smem, cudaStream_t s, const A &...args) {
+cudaError_t launch_clusters(void (*fn)(P...), int units, int ctas, size_t smem, cudaStream_t s, const A &...args) {
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(hv) * unsigned(ctas));
+    cfg.gridDim = dim3(unsigned(units) * unsigned(ctas));
     cfg.blockDim = dim3(kRecThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -607,36 +748,38 @@ cudaError_t launch_clusters(void (*fn)(P...), int hv, int ctas, size_t smem, cud
     return cudaLaunchKernelEx(&cfg, fn, P(args)...);
 }
 
+// the tensor map of a [total_tokens, hv, 128] tensor's tiles
+template <typename S, typename T>
+bool tile_map(CUtensorMap *map, const void *base, const RecArgs &a) {
+    return make_tmap_head_rows(map, base, sizeof(T) == 4, a.hv, a.total_tokens, S::kCh, S::kRows);
+}
+
 template <typename T, bool CHANNEL>
 cudaError_t forward(const RecArgs &a, cudaStream_t s) {
+    using R = Ring<T, CHANNEL, false>;
+    using S = typename R::S;
     CUtensorMap mx = {}, mg = {};
     if (a.total_tokens > 0) {
-        const bool f32 = sizeof(T) == 4;
-        if (!make_tmap_head_rows(&mx, a.x, f32, a.hv, a.total_tokens, kRecTile)) return cudaErrorInvalidValue;
-        if (CHANNEL && !make_tmap_head_rows(&mg, a.g, f32, a.hv, a.total_tokens, kRecTile))
-            return cudaErrorInvalidValue;
+        if (!tile_map<S, T>(&mx, a.x, a)) return cudaErrorInvalidValue;
+        if (CHANNEL && !tile_map<S, T>(&mg, a.g, a)) return cudaErrorInvalidValue;
     }
-    const size_t smem = stages<false>() * size_t(stage_bytes<T, CHANNEL, false>()) + 128;
-    const int ctas = cluster_of(a.total_tokens);
+    const int units = a.hv * S::kParts, ctas = cluster_of(a.total_tokens, S::kRows, units);
     LaunchScope scope(GDN_K_LINREC, s);
-    return launch_clusters(k_linrec<T, CHANNEL>, a.hv, ctas, smem, s, a, mx, mg, ctas);
+    return launch_clusters(k_linrec<T, CHANNEL>, units, ctas, R::kSmem, s, a, mx, mg, ctas);
 }
 
 template <typename T, bool CHANNEL>
 cudaError_t backward(const RecArgs &a, cudaStream_t s) {
+    using R = Ring<T, CHANNEL, true>;
+    using S = typename R::S;
     CUtensorMap mx = {}, mg = {}, md = {};
     if (a.total_tokens > 0) {
-        const bool f32 = sizeof(T) == 4;
-        if (!make_tmap_head_rows(&mx, a.x, f32, a.hv, a.total_tokens, kRecTile) ||
-            !make_tmap_head_rows(&md, a.dout, f32, a.hv, a.total_tokens, kRecTile))
-            return cudaErrorInvalidValue;
-        if (CHANNEL && !make_tmap_head_rows(&mg, a.g, f32, a.hv, a.total_tokens, kRecTile))
-            return cudaErrorInvalidValue;
+        if (!tile_map<S, T>(&mx, a.x, a) || !tile_map<S, T>(&md, a.dout, a)) return cudaErrorInvalidValue;
+        if (CHANNEL && !tile_map<S, T>(&mg, a.g, a)) return cudaErrorInvalidValue;
     }
-    const size_t smem = stages<true>() * size_t(stage_bytes<T, CHANNEL, true>()) + 128;
-    const int ctas = cluster_of(a.total_tokens);
+    const int units = a.hv * S::kParts, ctas = cluster_of(a.total_tokens, S::kRows, units);
     LaunchScope scope(GDN_K_LINREC_BWD, s);
-    return launch_clusters(k_linrec_bwd<T, CHANNEL>, a.hv, ctas, smem, s, a, mx, mg, md, ctas);
+    return launch_clusters(k_linrec_bwd<T, CHANNEL>, units, ctas, R::kSmem, s, a, mx, mg, md, ctas);
 }
 
 }  // namespace

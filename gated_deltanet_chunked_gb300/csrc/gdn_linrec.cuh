@@ -5,7 +5,7 @@
 
 namespace gdn {
 
-constexpr int kRecTile = 64;  // rows between the states that the backward pass starts from
+constexpr int kStateRows = 64;  // rows between the states that the backward pass starts from
 
 struct RecArgs {
     const void *x, *g, *dout;
@@ -13,7 +13,7 @@ struct RecArgs {
     const int32_t *cu;         // [num_seqs + 1] or null: sequences of dense_seqlen rows
     void *out, *dx, *dg;
     float *final_state, *dinitial;
-    float *states;  // [ceil(total_tokens / kRecTile), hv, 128]; written forward (or null), read backward
+    float *states;  // [ceil(total_tokens / kStateRows), hv, 128]; written forward (or null), read backward
     int total_tokens, num_seqs, dense_seqlen, hv;
     int *status;
     unsigned long long wait_ns;  // limit of a wait for a copy

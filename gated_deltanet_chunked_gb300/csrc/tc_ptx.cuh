@@ -215,17 +215,47 @@ __device__ __forceinline__ uint32_t cluster_map(const void *p, uint32_t rank) {
     return a;
 }
 
-__device__ __forceinline__ void cluster_st(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Two f32 to `addr` in another CTA's shared memory (8-byte aligned), counted
+// as 8 bytes on the barrier at `bar` in the same CTA: a store that needs no
+// fence of its own and no cluster barrier.
+__device__ __forceinline__ void cluster_st_async(uint32_t addr, float a, float b, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+                 "f"(a), "f"(b), "r"(bar)
+                 : "memory");
 }
 
-// Barrier over every thread of the cluster; shared-memory writes before it,
-// remote ones too, are visible after it. The hardware counts threads that
-// have exited as arrived, and no code path skips one, so it always ends.
+// Bounded wait for a phase that stores of the cluster's other CTAs complete.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t limit_ns = 2000000000ull) {
+    auto done = [&] {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+    if (done()) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!done())
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    return true;
+}
+
+// Barrier over every thread of the cluster. Relaxed: orders no memory (a
+// release would wait for this thread's stores to global memory). No code
+// path skips one, so it always ends.
 __device__ __forceinline__ void cluster_sync() {
     __syncwarp();  // .aligned: the warp's lanes together
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------

@@ -70,15 +70,16 @@ inline bool make_tmap_bf16_3d(CUtensorMap *map, const void *base, uint64_t d0, u
 }
 
 // 3-D tensor [d2][d1][128] of bf16 or f32 with d1 x 128 elements a slab,
-// copied as unswizzled boxes of rows [128] of one d1 index and b2 slabs;
+// copied as unswizzled boxes of b0 elements of one d1 index of b2 slabs;
 // out-of-range slabs read as zero.
-inline bool make_tmap_head_rows(CUtensorMap *map, const void *base, bool f32, uint64_t d1, uint64_t d2, uint32_t b2) {
+inline bool make_tmap_head_rows(CUtensorMap *map, const void *base, bool f32, uint64_t d1, uint64_t d2, uint32_t b0,
+                                uint32_t b2) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t es = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {128, d1, d2};
     const cuuint64_t strides[2] = {128 * es, d1 * 128 * es};
-    const cuuint32_t box[3] = {128, 1, b2};
+    const cuuint32_t box[3] = {b0, 1, b2};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
