@@ -352,8 +352,8 @@ int check_linrec(const gdn_problem *p, bool packed) {
         if (p->batch < 1 || p->seqlen < 0 || p->num_seqs != p->batch) return GDN_EINVAL;
         if (int64_t(p->batch) * p->seqlen != p->total_tokens) return GDN_EINVAL;
     }
-    // token indices a few tiles past the end stay in int, and so does the number of CTAs
-    if (p->total_tokens > INT32_MAX - 65536 || p->hv > (1 << 24) || p->num_seqs == INT32_MAX) return GDN_EINVAL;
+    // token indices a few tiles past the end, a row's bytes and the number of CTAs stay in 32 bits
+    if (p->total_tokens > INT32_MAX - 65536 || p->hv > (1 << 20) || p->num_seqs == INT32_MAX) return GDN_EINVAL;
     return GDN_OK;
 }
 

@@ -65,9 +65,6 @@ struct Tile {
     static constexpr int kSegs = WIDE ? 4 : 8;
     static constexpr int kRows = kSegs * kSeg;
     static constexpr int kParts = kHeadDim / kCh;  // clusters of a head
-    static constexpr int kQ = kRecThreads / kCh;   // threads of a channel in the exchange
-    static constexpr int kPitch = kCh + 4;         // of segment rows: the exchange's reads hit every bank once
-    static constexpr int kCtaPitch = kCh + 2;      // of CTA rows (pairs of f32), likewise
     static_assert(kRows % kStateRows == 0, "");
 
     static __device__ __forceinline__ int seg() { return (threadIdx.x >> 5) % kSegs; }
@@ -110,19 +107,27 @@ struct Bounds {
 
     __device__ __forceinline__ int start(int i) const { return cu ? cu[i] : i * seqlen; }
 
-    // bit i (0 .. kSeg): a sequence ends before, or starts at, row t0 + i.
-    // Called by whole warps. Packed: the offsets are searched 32 at a time
-    // from `next` on, where the last call left it (FORWARD: t0 rises from call
-    // to call and next starts at 0; else t0 falls and next starts at n + 1).
-    template <bool FORWARD>
-    __device__ __forceinline__ uint32_t mask(int t0, int &next) const {
-        uint32_t m = 0;
+    // Boundaries of a tile of SEGS segments from row t0, by one warp: bit i
+    // (0 .. kSeg) of m[k] says that a sequence ends before, or starts at, row
+    // t0 + k kSeg + i. Packed: the offsets are searched 32 at a time from
+    // `next` on, where the last call left it (FORWARD: t0 rises from call to
+    // call and next starts at 0; else t0 falls and next starts at n + 1).
+    template <bool FORWARD, int SEGS>
+    __device__ __forceinline__ void masks(int t0, int &next, uint32_t *m) const {
+        const int lane = threadIdx.x & 31, end = min(t0 + SEGS * kSeg, total);
+        if (lane < SEGS) m[lane] = 0;
+        __syncwarp();
+        auto mark = [&](int r) {  // row r of the tile
+            if (r < SEGS * kSeg) atomicOr(&m[r / kSeg], 1u << (r % kSeg));
+            if (r && r % kSeg == 0) atomicOr(&m[r / kSeg - 1], 1u << kSeg);
+        };
+        if (t0 >= total) return;
         if (!cu) {
-            for (int b = (t0 + seqlen - 1) / seqlen * seqlen; b <= t0 + kSeg && b <= total; b += seqlen)
-                m |= 1u << (b - t0);
-            return m;
+            for (long long b = (long long)(t0 + seqlen - 1) / seqlen * seqlen + (long long)lane * seqlen; b <= end;
+                 b += 32ll * seqlen)
+                mark(int(b) - t0);
+            return;
         }
-        const int lane = threadIdx.x & 31;
         uint32_t moved;
         do {  // next becomes the first offset that is not below t0
             if (FORWARD) {
@@ -133,11 +138,11 @@ struct Bounds {
                 next -= __popc(moved);
             }
         } while (moved == 0xffffffffu);
-        for (int k = next;; k += 32) {
-            const int v = k + lane <= n ? cu[k + lane] : INT_MAX;
-            const bool in = v <= t0 + kSeg;
-            m |= __reduce_or_sync(0xffffffffu, in ? 1u << (v - t0) : 0u);
-            if (__ballot_sync(0xffffffffu, in) != 0xffffffffu) return m;
+        bool in = true;
+        for (int k = next + lane; __ballot_sync(0xffffffffu, in) == 0xffffffffu; k += 32) {
+            const int v = k <= n ? cu[k] : INT_MAX;
+            in = v <= end;
+            if (in) mark(v - t0);
         }
     }
 
@@ -212,104 +217,76 @@ __device__ __forceinline__ void copy_empty(const RecArgs &a, const Bounds &bd, c
 template <bool WIDE>
 struct Exchange {
     using S = Tile<WIDE>;
-    float seg_a[S::kSegs][S::kPitch], seg_b[S::kSegs][S::kPitch];  // segments; seg_b then the state at each
-    float2 cta[2][kMaxCluster][S::kCtaPitch];  // by round parity: every CTA's composed segments (a, b)
+    float seg_a[S::kSegs][S::kCh], seg_b[S::kSegs][S::kCh];  // segments; seg_b then the state at each
+    float2 cta[2][kMaxCluster][S::kCh];  // by round parity: every CTA's composed segments (a, b)
     uint64_t bar[2];
+    uint32_t masks[2][S::kSegs];  // boundaries, by round parity
+    float decays[2][S::kRows];    // of gates per head, by round parity
 };
 
-// Inclusive scan over the Q lanes of a channel (lane order = walking order).
-template <int Q>
-__device__ __forceinline__ void scan_lanes(float &a, float &b, int q) {
-#pragma unroll
-    for (int m = 1; m < Q; m *= 2) {
-        float pa = __shfl_up_sync(0xffffffffu, a, m, Q), pb = __shfl_up_sync(0xffffffffu, b, m, Q);
-        compose(pa, pb, a, b);
-        if (q >= m) a = pa, b = pb;
-    }
-}
-
-// A channel's segments, kQ lanes with kSegs / kQ segments each.
+// A channel's segments of a tile in walking order.
 template <bool WIDE, bool REVERSE>
 struct Segments {
     using S = Tile<WIDE>;
-    static constexpr int kEach = S::kSegs / S::kQ;
-    float a[kEach], b[kEach];  // this lane's segments
-    float ia, ib;              // everything up to and with them
+    float a[S::kSegs], b[S::kSegs];
 
-    static __device__ __forceinline__ int seg(int q, int k) {
-        const int i = q * kEach + k;
-        return REVERSE ? S::kSegs - 1 - i : i;
-    }
-    __device__ __forceinline__ void load(const float (*sa)[S::kPitch], const float (*sb)[S::kPitch], int ch, int q) {
+    static __device__ __forceinline__ int seg(int i) { return REVERSE ? S::kSegs - 1 - i : i; }
+    __device__ __forceinline__ Segments(const float (*sa)[S::kCh], const float (*sb)[S::kCh], int ch) {
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) a[k] = sa[seg(q, k)][ch], b[k] = sb[seg(q, k)][ch];
-        ia = a[0], ib = b[0];
-#pragma unroll
-        for (int k = 1; k < kEach; ++k) compose(ia, ib, a[k], b[k]);
-        scan_lanes<S::kQ>(ia, ib, q);
+        for (int i = 0; i < S::kSegs; ++i) a[i] = sa[seg(i)][ch], b[i] = sb[seg(i)][ch];
     }
-    // writes the value that each segment starts from, `in` at the first, and
+    __device__ __forceinline__ float2 composed() const {
+        float ca = a[0], cb = b[0];
+#pragma unroll
+        for (int i = 1; i < S::kSegs; ++i) compose(ca, cb, a[i], b[i]);
+        return make_float2(ca, cb);
+    }
+    // writes the value that each segment starts from, `s` at the first, and
     // calls at(segment, value) for each
     template <typename F>
-    __device__ __forceinline__ void finish(float (*sb)[S::kPitch], int ch, int q, float in, F at) {
-        const float pa = __shfl_up_sync(0xffffffffu, ia, 1, S::kQ), pb = __shfl_up_sync(0xffffffffu, ib, 1, S::kQ);
-        float s = q ? apply(pa, pb, in) : in;
+    __device__ __forceinline__ void finish(float (*sb)[S::kCh], int ch, float s, F at) {
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            sb[seg(q, k)][ch] = s;
-            at(seg(q, k), s);
-            s = apply(a[k], b[k], s);
+        for (int i = 0; i < S::kSegs; ++i) {
+            sb[seg(i)][ch] = s;
+            at(seg(i), s);
+            s = apply(a[i], b[i], s);
         }
     }
 };
 
-// Steps 2 and 3, all threads, after the segments are in shared memory: moves
-// `carry` (the value before the round) on to the next round's; seg_b becomes
-// the value that each segment starts from, which at(segment, value) gets too.
-// REVERSE: segments and CTAs from the last to the first. ok turns false when a
-// wait runs out (later ones are skipped).
+// Steps 2 and 3, the first kCh threads, one a channel, after the segments are
+// in shared memory: moves `carry` (the value before the round) on to the next
+// round's; seg_b becomes the value that each segment starts from, which
+// at(segment, value) gets too. REVERSE: segments and CTAs from the last to the
+// first. ok turns false when a wait runs out (later ones are skipped). One
+// thread a channel is the fewest instructions; the other warps have the
+// forward states of the backward pass, the next tiles' boundaries and gates
+// to see to meanwhile.
 template <bool WIDE, bool REVERSE, typename F>
 __device__ __forceinline__ void exchange(Exchange<WIDE> &ex, float &carry, int round, int rank, int ctas, bool &ok,
                                          unsigned long long limit, F at) {
     using namespace tc;
     using S = Tile<WIDE>;
-    constexpr int Q = S::kQ, kRanks = kMaxCluster / Q;
-    const int ch = threadIdx.x / Q, q = threadIdx.x % Q, p = round & 1;
+    const int ch = threadIdx.x, p = round & 1;
     if (threadIdx.x == 0) mbar_arrive_expect_tx(&ex.bar[p], uint32_t(ctas) * S::kCh * 8);
-    Segments<WIDE, REVERSE> sg;
-    sg.load(ex.seg_a, ex.seg_b, ch, q);
-    {
-        const float ta = __shfl_sync(0xffffffffu, sg.ia, Q - 1, Q), tb = __shfl_sync(0xffffffffu, sg.ib, Q - 1, Q);
+    Segments<WIDE, REVERSE> sg(ex.seg_a, ex.seg_b, ch);
+    const float2 mine = sg.composed();
 #pragma unroll
-        for (int k = 0; k < kRanks; ++k) {
-            const int r = k * Q + q;
-            if (r < ctas)
-                cluster_st_async(cluster_map(&ex.cta[p][rank][ch], r), ta, tb, cluster_map(&ex.bar[p], r));
+    for (int r = 0; r < kMaxCluster; ++r)
+        if (r < ctas) cluster_st_async(cluster_map(&ex.cta[p][rank][ch], r), mine.x, mine.y, cluster_map(&ex.bar[p], r));
+    if (ok && !mbar_wait_cluster(&ex.bar[p], uint32_t(round >> 1) & 1, limit)) ok = false;
+    float s = carry, in = carry;
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i) {
+        if (i < ctas) {
+            const int r = REVERSE ? ctas - 1 - i : i;
+            const float2 v = ex.cta[p][r][ch];
+            if (r == rank) in = s;
+            s = apply(v.x, v.y, s);
         }
     }
-    if (ok && !mbar_wait_cluster(&ex.bar[p], uint32_t(round >> 1) & 1, limit)) ok = false;
-    // ranks in walking order, kRanks a lane
-    const int mine = REVERSE ? ctas - 1 - rank : rank;
-    float2 v[kRanks];
-#pragma unroll
-    for (int k = 0; k < kRanks; ++k) {
-        const int i = q * kRanks + k;
-        v[k] = i < ctas ? ex.cta[p][REVERSE ? ctas - 1 - i : i][ch] : make_float2(1.f, 0.f);
-    }
-    float a = v[0].x, b = v[0].y;
-#pragma unroll
-    for (int k = 1; k < kRanks; ++k) compose(a, b, v[k].x, v[k].y);
-    scan_lanes<Q>(a, b, q);
-    const float pa = __shfl_up_sync(0xffffffffu, a, 1, Q), pb = __shfl_up_sync(0xffffffffu, b, 1, Q);
-    float s = q ? apply(pa, pb, carry) : carry, in = s;
-#pragma unroll
-    for (int k = 0; k < kRanks; ++k) {
-        if (q * kRanks + k == mine) in = s;
-        s = apply(v[k].x, v[k].y, s);
-    }
-    carry = __shfl_sync(0xffffffffu, s, Q - 1, Q);
-    in = __shfl_sync(0xffffffffu, in, mine / kRanks, Q);
-    sg.finish(ex.seg_b, ch, q, in, at);
+    carry = s;
+    sg.finish(ex.seg_b, ch, in, at);
 }
 
 // Tile loads through a ring of stages: one thread issues, everyone waits.
@@ -352,13 +329,28 @@ struct Ring {
     }
 };
 
-// Gate per head of row t0 + lane (lanes 0 .. kSeg - 1; 0, which passes the
-// state on, past the end). Loaded a round ahead of its use.
-__device__ __forceinline__ float head_gate(const RecArgs &a, int t0, int h) {
-    const int lane = threadIdx.x & 31;
-    return lane < kSeg && t0 + lane < a.total_tokens ? static_cast<const float *>(a.g)[(long long)(t0 + lane) * a.hv + h]
-                                                     : 0.f;
-}
+// Gates per head of a tile's rows, by one warp a round ahead: load() issues the
+// reads for a tile, store() turns what the last load() brought into decays
+// (rows past the end pass the state on).
+template <int ROWS>
+struct HeadGates {
+    float g[ROWS / 32];
+    __device__ __forceinline__ void load(const RecArgs &a, int t0, int h) {
+#pragma unroll
+        for (int k = 0; k < ROWS / 32; ++k) {
+            const int t = t0 + k * 32 + int(threadIdx.x & 31);
+            g[k] = t >= 0 && t < a.total_tokens ? static_cast<const float *>(a.g)[(long long)t * a.hv + h] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void store(float *to) const {
+#pragma unroll
+        for (int k = 0; k < ROWS / 32; k += 2) {
+            const float2 d = decay2(make_float2(g[k], g[k + 1]));
+            to[k * 32 + int(threadIdx.x & 31)] = d.x;
+            to[(k + 1) * 32 + int(threadIdx.x & 31)] = d.y;
+        }
+    }
+};
 
 // Decays of a segment's rows for the lane's two channels, and what the walks
 // do with them: packed operations on pairs of their own, scalar ones on the
@@ -369,7 +361,7 @@ template <typename T>
 struct Decays<T, true> {
     using Product = float2;
     float2 d[kSeg];
-    __device__ __forceinline__ Decays(const T *g_tile, float) {
+    __device__ __forceinline__ Decays(const T *g_tile, const float *) {
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
             Pack<T, 2> p;
@@ -389,10 +381,12 @@ struct Decays<T, true> {
 template <typename T>
 struct Decays<T, false> {
     float d[kSeg];
-    __device__ __forceinline__ Decays(const T *, float g_head) {
-        const float t = decay2(make_float2(g_head, g_head)).x;
+    __device__ __forceinline__ Decays(const T *, const float *decays) {
 #pragma unroll
-        for (int i = 0; i < kSeg; ++i) d[i] = __shfl_sync(0xffffffffu, t, i);
+        for (int i = 0; i < kSeg; i += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(decays + i);
+            d[i] = v.x, d[i + 1] = v.y, d[i + 2] = v.z, d[i + 3] = v.w;
+        }
     }
     __device__ __forceinline__ float2 fma(int i, float2 s, float2 x) const {
         return make_float2(fmaf(d[i], s.x, x.x), fmaf(d[i], s.y, x.y));
@@ -426,6 +420,12 @@ __device__ __forceinline__ float2 f2(const Pack<float, 2> &p) { return make_floa
 __device__ __forceinline__ float2 f2(const Pack<__nv_bfloat16, 2> &p) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&p.r));
 }
+// row i from `base`: rows are `pitch` bytes apart
+template <typename T>
+__device__ __forceinline__ T *row_at(T *base, unsigned pitch, int i) {
+    return reinterpret_cast<T *>(reinterpret_cast<char *>(base) + (unsigned long long)pitch * unsigned(i));
+}
+
 template <typename T>
 __device__ __forceinline__ void store2(T *to, float2 v);
 template <>
@@ -445,6 +445,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     __shared__ Exchange<false> ex;
     __shared__ uint64_t full[R::kStages];
     const int w = S::seg(), c = S::channel();
+    const bool last_warp = threadIdx.x >= kRecThreads - 32, feeder = threadIdx.x == kRecThreads - 1;
     const int rank = int(cluster_ctarank()), unit = int(blockIdx.x) / ctas;
     const int h = unit / S::kParts, c0 = unit % S::kParts * S::kCh;
     const int hc = h * kHeadDim + c0 + c;  // this lane's first channel in a row [hv, 128]
@@ -455,7 +456,10 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     const int rounds = (tiles + ctas - 1) / ctas;
     if (!rounds) return;
     R ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)), full};
-    if (threadIdx.x == 0) {
+    bool ok = true;
+    int next = 0;
+    HeadGates<S::kRows> gates;
+    if (feeder) {
         for (int i = 0; i < R::kStages; ++i) mbar_init(&full[i], 1);
         mbar_init(&ex.bar[0], 1);
         mbar_init(&ex.bar[1], 1);
@@ -463,24 +467,30 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
         for (int i = 0; i < R::kStages && i < rounds; ++i)
             ring.load(i, &mx, &mg, nullptr, a, c0, h, (i * ctas + rank) * S::kRows);
     }
+    if (last_warp) {
+        __syncwarp();
+        bd.masks<true, S::kSegs>(rank * S::kRows, next, ex.masks[0]);
+        if (!CHANNEL) {
+            gates.load(a, rank * S::kRows, h);
+            gates.store(ex.decays[0]);
+            gates.load(a, (ctas + rank) * S::kRows, h);
+        }
+    }
+    __syncthreads();
     cluster_sync();  // every CTA's barriers are ready
     float carry = 0.f;  // of this thread's channel in the exchange, before the round
-    float gate = CHANNEL ? 0.f : head_gate(a, rank * S::kRows + w * kSeg, h);
-    bool ok = true;
-    int next = 0;
-    const long long pitch = (long long)a.hv * kHeadDim;
+    const int width = a.hv * kHeadDim;  // of a row
+    const unsigned pitch = unsigned(width) * sizeof(T);
     for (int round = 0; round < rounds; ++round) {
         const int t0 = (round * ctas + rank) * S::kRows, tw = t0 + w * kSeg;  // the tile's and the warp's first row
         const int rows = min(kSeg, a.total_tokens - tw);                     // may be negative
-        uint32_t starts = 0;  // bit kSeg: before the next segment
-        if (rows > 0) starts = bd.mask<true>(tw, next);
+        const uint32_t starts = ex.masks[round & 1][w];  // bit kSeg: before the next segment
         ring.wait(round, ok, a.wait_ns);
         Pack<T, 2> x[kSeg];
         const int o = w * kSeg * S::kCh + c;
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) x[i].load(ring.x(round) + o + i * S::kCh);
-        const Decays<T, CHANNEL> d(ring.g(round) + o, gate);
-        if (!CHANNEL) gate = head_gate(a, tw + ctas * S::kRows, h);
+        const Decays<T, CHANNEL> d(ring.g(round) + o, ex.decays[round & 1] + w * kSeg);
         const bool plain = starts == 0 && rows == kSeg;
         {
             float2 A = d.product(), B = make_float2(0.f, 0.f);
@@ -493,26 +503,33 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
             pair(&ex.seg_b[w][c]) = B;
         }
         __syncthreads();
-        // the tile is in registers: its stage takes a later one
-        if (threadIdx.x == 0 && round + R::kStages < rounds)
-            ring.load(round + R::kStages, &mx, &mg, nullptr, a, c0, h, t0 + R::kStages * ctas * S::kRows);
-        __syncwarp();
-        exchange<false, false>(ex, carry, round, rank, ctas, ok, a.wait_ns, [&](int seg, float s) {
-            const int t = t0 + seg * kSeg;
-            if (a.states && t % kStateRows == 0 && t < a.total_tokens)
-                a.states[(long long)(t / kStateRows) * pitch + h * kHeadDim + c0 + threadIdx.x / S::kQ] = s;
-        });
+        if (threadIdx.x < S::kCh)
+            exchange<false, false>(ex, carry, round, rank, ctas, ok, a.wait_ns, [&](int seg, float s) {
+                const int t = t0 + seg * kSeg;
+                if (seg % (kStateRows / kSeg) == 0 && a.states && t < a.total_tokens)
+                    a.states[(long long)(t / kStateRows) * width + h * kHeadDim + c0 + threadIdx.x] = s;
+            });
+        if (last_warp && round + 1 < rounds) {
+            // the tile is in registers: its stage takes a later one
+            if (feeder && round + R::kStages < rounds)
+                ring.load(round + R::kStages, &mx, &mg, nullptr, a, c0, h, t0 + R::kStages * ctas * S::kRows);
+            __syncwarp();
+            bd.masks<true, S::kSegs>(t0 + ctas * S::kRows, next, ex.masks[(round + 1) & 1]);
+            if (!CHANNEL) {
+                gates.store(ex.decays[(round + 1) & 1]);
+                gates.load(a, t0 + 2 * ctas * S::kRows, h);
+            }
+        }
         __syncthreads();
         float2 s = pair(&ex.seg_b[w][c]);
-        T *out = static_cast<T *>(a.out) + tw * pitch + hc;
+        T *out = static_cast<T *>(a.out) + (long long)tw * width + hc;
         walk<0, kSeg - 1>(plain, [&](int i, auto checked) {
             if (checked) {
                 if (i >= rows) return;
                 if (starts >> i & 1) s = boundary_load<false>(a.s0, bd, tw + i, a.hv, hc);
             }
             s = d.fma(i, s, f2(x[i]));
-            store2(out, s);
-            out += pitch;
+            store2(row_at(out, pitch, i), s);
             if (checked && a.final_state && (starts >> (i + 1) & 1))
                 boundary_store<true>(a.final_state, bd, tw + i, a.hv, hc, s);
         });
@@ -531,10 +548,11 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     constexpr bool WIDE = !CHANNEL;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Exchange<WIDE> ex;
-    __shared__ float fwd_a[S::kSegs][S::kPitch], fwd_b[S::kSegs][S::kPitch];
+    __shared__ float fwd_a[S::kSegs][S::kCh], fwd_b[S::kSegs][S::kCh];
     __shared__ float head_sums[CHANNEL ? 1 : 2][2][CHANNEL ? 1 : S::kRows];  // by round parity, half of the head, row
     __shared__ uint64_t full[R::kStages];
     const int w = S::seg(), c = S::channel(), lane = threadIdx.x & 31;
+    const bool last_warp = threadIdx.x >= kRecThreads - 32, feeder = threadIdx.x == kRecThreads - 1;
     const int rank = int(cluster_ctarank()), unit = int(blockIdx.x) / ctas;
     const int h = unit / S::kParts, c0 = unit % S::kParts * S::kCh;
     const int hc = h * kHeadDim + c0 + c;
@@ -545,20 +563,32 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     const int rounds = (tiles + ctas - 1) / ctas;
     if (!rounds) return;
     R ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)), full};
-    if (threadIdx.x == 0) {
+    bool ok = true;
+    int next = a.num_seqs + 1;
+    HeadGates<S::kRows> gates;
+    const int t_first = ((rounds - 1) * ctas + rank) * S::kRows, t_step = ctas * S::kRows;
+    if (feeder) {
         for (int i = 0; i < R::kStages; ++i) mbar_init(&full[i], 1);
         mbar_init(&ex.bar[0], 1);
         mbar_init(&ex.bar[1], 1);
         fence_mbar_init();
         for (int i = 0; i < R::kStages && i < rounds; ++i)
-            ring.load(i, &mx, &mg, &md, a, c0, h, ((rounds - 1 - i) * ctas + rank) * S::kRows);
+            ring.load(i, &mx, &mg, &md, a, c0, h, t_first - i * t_step);
     }
+    if (last_warp) {
+        __syncwarp();
+        bd.masks<false, S::kSegs>(t_first, next, ex.masks[0]);
+        if (!CHANNEL) {
+            gates.load(a, t_first, h);
+            gates.store(ex.decays[0]);
+            gates.load(a, t_first - t_step, h);
+        }
+    }
+    __syncthreads();
     cluster_sync();
     float carry = 0.f;
-    float gate = CHANNEL ? 0.f : head_gate(a, ((rounds - 1) * ctas + rank) * S::kRows + w * kSeg, h);
-    bool ok = true;
-    int next = a.num_seqs + 1;
-    const long long pitch = (long long)a.hv * kHeadDim;
+    const int width = a.hv * kHeadDim;  // of a row
+    const unsigned pitch = unsigned(width) * sizeof(T);
     // dg per head of the tile at row t: the sums of the head's two halves
     auto write_head_sums = [&](int parity, int t) {
         const int r = threadIdx.x;
@@ -566,15 +596,14 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
             static_cast<float *>(a.dg)[(long long)(t + r) * a.hv + h] = head_sums[parity][0][r] + head_sums[parity][1][r];
     };
     for (int round = 0; round < rounds; ++round) {
-        const int t0 = ((rounds - 1 - round) * ctas + rank) * S::kRows, tw = t0 + w * kSeg;
+        const int t0 = t_first - round * t_step, tw = t0 + w * kSeg;
         const int rows = min(kSeg, a.total_tokens - tw);
-        uint32_t bounds = 0;
-        if (rows > 0) bounds = bd.mask<false>(tw, next);
+        const uint32_t bounds = ex.masks[round & 1][w];
         // the segment's rows that start (s is reset) and end (e is reset) a sequence
         const uint32_t starts = bounds & ((1u << max(rows, 0)) - 1), ends = bounds >> 1;
         const bool plain = bounds == 0 && rows == kSeg;
         ring.wait(round, ok, a.wait_ns);
-        const float state = ring.state(round)[threadIdx.x / S::kQ];  // unused where the tile starts a sequence
+        const float state = ring.state(round)[threadIdx.x % S::kCh];  // unused where the tile starts a sequence
         Pack<T, 2> x[kSeg], dy[kSeg];
         const int o = w * kSeg * S::kCh + c;
 #pragma unroll
@@ -582,8 +611,7 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
             x[i].load(ring.x(round) + o + i * S::kCh);
             dy[i].load(ring.dout(round) + o + i * S::kCh);
         }
-        const Decays<T, CHANNEL> d(ring.g(round) + o, gate);
-        if (!CHANNEL && round + 1 < rounds) gate = head_gate(a, tw - ctas * S::kRows, h);
+        const Decays<T, CHANNEL> d(ring.g(round) + o, ex.decays[round & 1] + w * kSeg);
         // the rows' maps: forward for s, in reverse for e
         {
             const float2 A = d.product();
@@ -603,16 +631,24 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
             pair(&ex.seg_b[w][c]) = E;
         }
         __syncthreads();
-        if (threadIdx.x == 0 && round + R::kStages < rounds)
-            ring.load(round + R::kStages, &mx, &mg, &md, a, c0, h, t0 - R::kStages * ctas * S::kRows);
+        if (feeder && round + R::kStages < rounds)
+            ring.load(round + R::kStages, &mx, &mg, &md, a, c0, h, t0 - R::kStages * t_step);
+        if (!CHANNEL && round) write_head_sums((round - 1) & 1, t0 + t_step);
         __syncwarp();
-        if (!CHANNEL && round) write_head_sums((round - 1) & 1, t0 + ctas * S::kRows);
-        exchange<WIDE, true>(ex, carry, round, rank, ctas, ok, a.wait_ns, [](int, float) {});
-        {
-            const int ch = threadIdx.x / S::kQ, q = threadIdx.x % S::kQ;
-            Segments<WIDE, false> sg;
-            sg.load(fwd_a, fwd_b, ch, q);
-            sg.finish(fwd_b, ch, q, state, [](int, float) {});
+        if (threadIdx.x < S::kCh) {
+            exchange<WIDE, true>(ex, carry, round, rank, ctas, ok, a.wait_ns, [](int, float) {});
+        } else if (threadIdx.x < 2 * S::kCh) {
+            const int ch = threadIdx.x - S::kCh;
+            Segments<WIDE, false> sg(fwd_a, fwd_b, ch);
+            sg.finish(fwd_b, ch, state, [](int, float) {});
+        }
+        if (last_warp && round + 1 < rounds) {
+            __syncwarp();
+            bd.masks<false, S::kSegs>(t0 - t_step, next, ex.masks[(round + 1) & 1]);
+            if (!CHANNEL) {
+                gates.store(ex.decays[(round + 1) & 1]);
+                gates.load(a, t0 - 2 * t_step, h);
+            }
         }
         __syncthreads();
         // The segment's states are kept for half of its rows at a time, the
@@ -620,8 +656,8 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         // first half.
         float2 e = pair(&ex.seg_b[w][c]);
         const float2 s0 = pair(&fwd_b[w][c]);
-        T *dx = static_cast<T *>(a.dx) + (tw + kSeg - 1) * pitch + hc;
-        T *dgc = static_cast<T *>(a.dg) + (tw + kSeg - 1) * pitch + hc;  // per channel
+        T *dx = static_cast<T *>(a.dx) + (long long)tw * width + hc;
+        T *dgc = static_cast<T *>(a.dg) + (long long)tw * width + hc;  // per channel
         auto half_walk = [&](auto half_) {
             constexpr int half = decltype(half_)::value;
             float2 s = s0, before[kHalf];
@@ -638,13 +674,11 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
                 const float2 dg = mul2(e, before[i % kHalf]);
                 if (!CHANNEL) sums[i % kHalf] = dg.x + dg.y;
                 if (!checked || i < rows) {
-                    store2(dx, ds);
-                    if (CHANNEL) store2(dgc, dg);
+                    store2(row_at(dx, pitch, i), ds);
+                    if (CHANNEL) store2(row_at(dgc, pitch, i), dg);
                     if (checked && a.dinitial && (starts >> i & 1))
                         boundary_store<false>(a.dinitial, bd, tw + i, a.hv, hc, e);
                 }
-                dx -= pitch;
-                dgc -= pitch;
             });
             if (!CHANNEL) {
                 // eight rows' sums over the warp's channels: lanes halve the
