@@ -37,6 +37,7 @@
 // the same steps without any exchange. With gates per head dg is a sum over
 // the head, so there a CTA takes all 128 channels of tiles of 64 rows.
 // s and e are f32 throughout; only out, dx and dg are rounded.
+#include <atomic>
 #include <type_traits>
 
 #include "gdn_linrec.cuh"
@@ -53,8 +54,7 @@ constexpr int kRecWarps = 8;
 constexpr int kRecThreads = 32 * kRecWarps;
 constexpr int kSeg = 16;  // rows of a warp in a round
 constexpr int kHalf = kSeg / 2;
-constexpr int kMaxCluster = 8;
-constexpr int kMaxCtas = 2 * 152;  // two on each SM
+constexpr int kMaxCluster = 16;  // above the portable eight
 constexpr float kReset = -1.f;  // in the place of a product of decays (never negative)
 
 // A CTA's tile: 64 channels x 8 segments of rows, or (WIDE) 128 x 4. A warp
@@ -271,19 +271,17 @@ __device__ __forceinline__ void exchange(Exchange<WIDE> &ex, float &carry, int r
     if (threadIdx.x == 0) mbar_arrive_expect_tx(&ex.bar[p], uint32_t(ctas) * S::kCh * 8);
     Segments<WIDE, REVERSE> sg(ex.seg_a, ex.seg_b, ch);
     const float2 mine = sg.composed();
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-        if (r < ctas) cluster_st_async(cluster_map(&ex.cta[p][rank][ch], r), mine.x, mine.y, cluster_map(&ex.bar[p], r));
+#pragma unroll 4
+    for (int r = 0; r < ctas; ++r)
+        cluster_st_async(cluster_map(&ex.cta[p][rank][ch], r), mine.x, mine.y, cluster_map(&ex.bar[p], r));
     if (ok && !mbar_wait_cluster(&ex.bar[p], uint32_t(round >> 1) & 1, limit)) ok = false;
     float s = carry, in = carry;
-#pragma unroll
-    for (int i = 0; i < kMaxCluster; ++i) {
-        if (i < ctas) {
-            const int r = REVERSE ? ctas - 1 - i : i;
-            const float2 v = ex.cta[p][r][ch];
-            if (r == rank) in = s;
-            s = apply(v.x, v.y, s);
-        }
+#pragma unroll 4
+    for (int i = 0; i < ctas; ++i) {
+        const int r = REVERSE ? ctas - 1 - i : i;
+        const float2 v = ex.cta[p][r][ch];
+        if (r == rank) in = s;
+        s = apply(v.x, v.y, s);
     }
     carry = s;
     sg.finish(ex.seg_b, ch, in, at);
@@ -297,8 +295,9 @@ struct Ring {
     static constexpr uint32_t kTiles = kTile * sizeof(T) * (1 + CHANNEL + BACKWARD);  // x, g per channel, dout
     static constexpr uint32_t kState = BACKWARD ? S::kCh * 4 : 0;                     // the state before the tile
     static constexpr uint32_t kBytes = kTiles + kState;
-    // two CTAs of an SM have two stages each where they fit
-    static constexpr int kStages = kTiles <= 32768 ? 2 : 1;
+    // CTAs of an SM that registers allow, and stages that shared memory then allows
+    static constexpr int kCtasPerSm = BACKWARD && sizeof(T) == 4 ? 1 : 2;
+    static constexpr int kStages = kTiles <= 16384 ? 3 : kTiles <= 32768 ? 2 : 1;
     static constexpr size_t kSmem = size_t(kStages) * kBytes + 128;
     uint8_t *base;
     uint64_t *full;
@@ -436,7 +435,7 @@ __device__ __forceinline__ void store2<__nv_bfloat16>(__nv_bfloat16 *to, float2 
 }
 
 template <typename T, bool CHANNEL>
-__global__ void __launch_bounds__(kRecThreads, 2)
+__global__ void __launch_bounds__(kRecThreads, Ring<T, CHANNEL, false>::kCtasPerSm)
 k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg, int ctas) {
     using namespace tc;
     using R = Ring<T, CHANNEL, false>;
@@ -449,16 +448,9 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     const int rank = int(cluster_ctarank()), unit = int(blockIdx.x) / ctas;
     const int h = unit / S::kParts, c0 = unit % S::kParts * S::kCh;
     const int hc = h * kHeadDim + c0 + c;  // this lane's first channel in a row [hv, 128]
-    if (!offsets_ok(a)) return;            // the same in every CTA
-    const Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens};
-    copy_empty<false>(a, bd, a.s0, a.final_state, hc, rank, ctas);
     const int tiles = (a.total_tokens + S::kRows - 1) / S::kRows;
     const int rounds = (tiles + ctas - 1) / ctas;
-    if (!rounds) return;
     R ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)), full};
-    bool ok = true;
-    int next = 0;
-    HeadGates<S::kRows> gates;
     if (feeder) {
         for (int i = 0; i < R::kStages; ++i) mbar_init(&full[i], 1);
         mbar_init(&ex.bar[0], 1);
@@ -467,8 +459,18 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
         for (int i = 0; i < R::kStages && i < rounds; ++i)
             ring.load(i, &mx, &mg, nullptr, a, c0, h, (i * ctas + rank) * S::kRows);
     }
+    __syncthreads();
+    cluster_arrive();  // this CTA's barriers are ready
+    bool ok = true;
+    if (!offsets_ok(a)) {  // the same in every CTA: nothing is written
+        for (int i = 0; i < R::kStages && i < rounds; ++i) ring.wait(i, ok, a.wait_ns);
+        cluster_wait();
+        return;
+    }
+    const Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens};
+    int next = 0;
+    HeadGates<S::kRows> gates;
     if (last_warp) {
-        __syncwarp();
         bd.masks<true, S::kSegs>(rank * S::kRows, next, ex.masks[0]);
         if (!CHANNEL) {
             gates.load(a, rank * S::kRows, h);
@@ -476,8 +478,8 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
             gates.load(a, (ctas + rank) * S::kRows, h);
         }
     }
+    copy_empty<false>(a, bd, a.s0, a.final_state, hc, rank, ctas);
     __syncthreads();
-    cluster_sync();  // every CTA's barriers are ready
     float carry = 0.f;  // of this thread's channel in the exchange, before the round
     const int width = a.hv * kHeadDim;  // of a row
     const unsigned pitch = unsigned(width) * sizeof(T);
@@ -503,6 +505,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
             pair(&ex.seg_b[w][c]) = B;
         }
         __syncthreads();
+        if (round == 0) cluster_wait();  // every CTA's barriers are ready
         if (threadIdx.x < S::kCh)
             exchange<false, false>(ex, carry, round, rank, ctas, ok, a.wait_ns, [&](int seg, float s) {
                 const int t = t0 + seg * kSeg;
@@ -535,11 +538,13 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
         });
     }
     if (!ok && (threadIdx.x & 31) == 0) record_status(a.status, GDN_ETIMEOUT);
-    cluster_sync_relaxed();  // no CTA leaves while others may still store to it
+    if (!rounds) cluster_wait();
+    cluster_arrive_relaxed();  // no CTA leaves while others may still store to it
+    cluster_wait();
 }
 
 template <typename T, bool CHANNEL>
-__global__ void __launch_bounds__(kRecThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kRecThreads, Ring<T, CHANNEL, true>::kCtasPerSm)
 k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
              const __grid_constant__ CUtensorMap md, int ctas) {
     using namespace tc;
@@ -556,17 +561,10 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     const int rank = int(cluster_ctarank()), unit = int(blockIdx.x) / ctas;
     const int h = unit / S::kParts, c0 = unit % S::kParts * S::kCh;
     const int hc = h * kHeadDim + c0 + c;
-    if (!offsets_ok(a)) return;
-    const Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens};
-    copy_empty<WIDE>(a, bd, a.dfinal, a.dinitial, hc, rank, ctas);
     const int tiles = (a.total_tokens + S::kRows - 1) / S::kRows;
     const int rounds = (tiles + ctas - 1) / ctas;
-    if (!rounds) return;
-    R ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)), full};
-    bool ok = true;
-    int next = a.num_seqs + 1;
-    HeadGates<S::kRows> gates;
     const int t_first = ((rounds - 1) * ctas + rank) * S::kRows, t_step = ctas * S::kRows;
+    R ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)), full};
     if (feeder) {
         for (int i = 0; i < R::kStages; ++i) mbar_init(&full[i], 1);
         mbar_init(&ex.bar[0], 1);
@@ -575,8 +573,18 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         for (int i = 0; i < R::kStages && i < rounds; ++i)
             ring.load(i, &mx, &mg, &md, a, c0, h, t_first - i * t_step);
     }
+    __syncthreads();
+    cluster_arrive();
+    bool ok = true;
+    if (!offsets_ok(a)) {
+        for (int i = 0; i < R::kStages && i < rounds; ++i) ring.wait(i, ok, a.wait_ns);
+        cluster_wait();
+        return;
+    }
+    const Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens};
+    int next = a.num_seqs + 1;
+    HeadGates<S::kRows> gates;
     if (last_warp) {
-        __syncwarp();
         bd.masks<false, S::kSegs>(t_first, next, ex.masks[0]);
         if (!CHANNEL) {
             gates.load(a, t_first, h);
@@ -584,8 +592,8 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
             gates.load(a, t_first - t_step, h);
         }
     }
+    copy_empty<WIDE>(a, bd, a.dfinal, a.dinitial, hc, rank, ctas);
     __syncthreads();
-    cluster_sync();
     float carry = 0.f;
     const int width = a.hv * kHeadDim;  // of a row
     const unsigned pitch = unsigned(width) * sizeof(T);
@@ -634,6 +642,7 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         if (feeder && round + R::kStages < rounds)
             ring.load(round + R::kStages, &mx, &mg, &md, a, c0, h, t0 - R::kStages * t_step);
         if (!CHANNEL && round) write_head_sums((round - 1) & 1, t0 + t_step);
+        if (round == 0) cluster_wait();
         __syncwarp();
         if (threadIdx.x < S::kCh) {
             exchange<WIDE, true>(ex, carry, round, rank, ctas, ok, a.wait_ns, [](int, float) {});
@@ -701,12 +710,14 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         half_walk(std::integral_constant<int, 1>{});
         half_walk(std::integral_constant<int, 0>{});
     }
-    if (!CHANNEL) {
+    if (!CHANNEL && rounds) {
         __syncthreads();
         write_head_sums((rounds - 1) & 1, rank * S::kRows);
     }
     if (!ok && lane == 0) record_status(a.status, GDN_ETIMEOUT);
-    cluster_sync_relaxed();
+    if (!rounds) cluster_wait();
+    cluster_arrive_relaxed();
+    cluster_wait();
 }
 
 static_assert(kHalf == 8, "the sums over a head's channels take eight rows at a time");
@@ -751,35 +762,65 @@ k_linrec_step(const void *x_, const void *g_, float *state, const int32_t *idx, 
     px.store(static_cast<T *>(out_) + i);
 }
 
-// CTAs of a cluster: the more, the more of the time axis is in work, but not
-// more than there are tiles, than the portable eight, or than lets all
-// clusters run at once (two CTAs an SM): a second wave of clusters would start
-// on the whole axis when the first is done.
-int cluster_of(int total, int rows, int units) {
-    const int tiles = (total + rows - 1) / rows;
-    int c = kMaxCtas / units;
-    c = c < tiles ? c : tiles;
-    return c < 1 ? 1 : c < kMaxCluster ? c : kMaxCluster;
-}
-
-// launches `fn` with `units` clusters of `ctas` CTAs
-template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*fn)(P...), int units, int ctas, size_t smem, cudaStream_t s, const A &...args) {
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(units) * unsigned(ctas));
+void launch_shape(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &at, int grid, int ctas, size_t smem) {
+    cfg.gridDim = dim3(unsigned(grid));
     cfg.blockDim = dim3(kRecThreads);
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at = {};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = unsigned(ctas);
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, P(args)...);
+}
+
+// Clusters of `ctas` CTAs of kernel `fn` that the current device runs at once.
+// Asked once for each size (it takes the driver some microseconds).
+template <typename R, typename F>
+cudaError_t active_clusters(F *fn, int ctas, int &clusters) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][kMaxCluster + 1];  // 0: not asked yet; one array a kernel
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kDevices && (clusters = known[dev][ctas].load(std::memory_order_relaxed)) > 0) {
+        clusters -= 1;
+        return cudaSuccess;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at = {};
+    launch_shape(cfg, at, ctas, ctas, R::kSmem);
+    e = cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg);
+    if (e != cudaSuccess) return e;
+    if (dev < kDevices) known[dev][ctas].store(clusters + 1, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+// Launches `units` clusters of kernel `fn`, each over the whole token axis.
+// The more CTAs a cluster has, the more of the axis is in work: as many as
+// there are tiles, as kMaxCluster, and as lets all clusters run at once (a
+// second wave would start on the whole axis when the first is done: at
+// T = 65536 with 64 units, 286 us with clusters of 4 against 317 with 8).
+template <typename R, typename... P, typename... A>
+cudaError_t launch_clusters(void (*fn)(P...), const RecArgs &a, cudaStream_t s, const A &...maps) {
+    using S = typename R::S;
+    const void *f = reinterpret_cast<const void *>(fn);
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(R::kSmem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    const int units = a.hv * S::kParts, tiles = (a.total_tokens + S::kRows - 1) / S::kRows;
+    int ctas = tiles < kMaxCluster ? tiles : kMaxCluster;
+    for (; ctas > 1; --ctas) {
+        int clusters = 0;
+        e = active_clusters<R>(fn, ctas, clusters);
+        if (e != cudaSuccess) return e;
+        if (clusters >= units) break;
+    }
+    if (ctas < 1) ctas = 1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at = {};
+    launch_shape(cfg, at, units * ctas, ctas, R::kSmem);
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, fn, a, maps..., ctas);
 }
 
 // the tensor map of a [total_tokens, hv, 128] tensor's tiles
@@ -797,9 +838,8 @@ cudaError_t forward(const RecArgs &a, cudaStream_t s) {
         if (!tile_map<S, T>(&mx, a.x, a)) return cudaErrorInvalidValue;
         if (CHANNEL && !tile_map<S, T>(&mg, a.g, a)) return cudaErrorInvalidValue;
     }
-    const int units = a.hv * S::kParts, ctas = cluster_of(a.total_tokens, S::kRows, units);
     LaunchScope scope(GDN_K_LINREC, s);
-    return launch_clusters(k_linrec<T, CHANNEL>, units, ctas, R::kSmem, s, a, mx, mg, ctas);
+    return launch_clusters<R>(k_linrec<T, CHANNEL>, a, s, mx, mg);
 }
 
 template <typename T, bool CHANNEL>
@@ -811,9 +851,8 @@ cudaError_t backward(const RecArgs &a, cudaStream_t s) {
         if (!tile_map<S, T>(&mx, a.x, a) || !tile_map<S, T>(&md, a.dout, a)) return cudaErrorInvalidValue;
         if (CHANNEL && !tile_map<S, T>(&mg, a.g, a)) return cudaErrorInvalidValue;
     }
-    const int units = a.hv * S::kParts, ctas = cluster_of(a.total_tokens, S::kRows, units);
     LaunchScope scope(GDN_K_LINREC_BWD, s);
-    return launch_clusters(k_linrec_bwd<T, CHANNEL>, units, ctas, R::kSmem, s, a, mx, mg, md, ctas);
+    return launch_clusters<R>(k_linrec_bwd<T, CHANNEL>, a, s, mx, mg, md);
 }
 
 }  // namespace

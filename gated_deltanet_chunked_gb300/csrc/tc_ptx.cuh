@@ -244,18 +244,20 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     return true;
 }
 
-// Barrier over every thread of the cluster. Relaxed: orders no memory (a
-// release would wait for this thread's stores to global memory). No code
-// path skips one, so it always ends.
-__device__ __forceinline__ void cluster_sync() {
+// Barrier over every thread of the cluster: each arrives, then waits. The
+// release waits for this thread's stores to global memory; relaxed orders no
+// memory. No code path skips one, so it always ends.
+__device__ __forceinline__ void cluster_arrive() {
     __syncwarp();  // .aligned: the warp's lanes together
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_sync_relaxed() {
+__device__ __forceinline__ void cluster_arrive_relaxed() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
