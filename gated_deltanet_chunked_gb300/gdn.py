@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import threading
 from typing import Optional
 
@@ -59,6 +60,8 @@ _vp, _fp, _ip = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p
 def load(path: Optional[str] = None):
     """Build (if stale) and load libgdn.so; raises if either step fails."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             lib = ctypes.CDLL(path or _build.build())
@@ -167,12 +170,14 @@ def _stream(stream, device=None) -> ctypes.c_void_p:
 
 @contextlib.contextmanager
 def _launching(stream, dev):
-    """Makes ``dev`` and, if given, ``stream`` current and yields the stream's
-    handle: what the call allocates then belongs to the stream it runs on, so
-    that PyTorch's allocator hands none of it to other work too early."""
+    """Makes ``dev`` and, if given, ``stream`` current: what a call allocates
+    then belongs to the stream it runs on, so that PyTorch's allocator hands
+    none of it to other work too early."""
+    if dev.type != "cuda":
+        raise ValueError(f"libgdn wants CUDA tensors, got a tensor on {dev}")
     with torch.cuda.device(dev):
         if stream is None:
-            yield _stream(None, dev)
+            yield
             return
         if not isinstance(stream, torch.cuda.Stream):
             handle = _stream(stream).value or 0
@@ -180,7 +185,7 @@ def _launching(stream, dev):
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, expected {dev} (the device of the first input)")
         with torch.cuda.stream(stream):
-            yield _stream(stream)
+            yield
 
 
 def _on_device(dev: torch.device, **tensors):
@@ -508,31 +513,60 @@ def gdn_gating(a, b, A_log, dt_bias, g=None, beta=None, stream=None):
     return g, beta
 
 
-def _linrec_checks(x, g, initial_state, cu_seqlens, states=None, **like_x):
-    """Checks shared by the recurrence's forward and backward wrappers;
-    returns (problem, device). ``like_x``: tensors of x's shape and type."""
+def _arg(name, t, dtype, shape, dev):
+    """Address of tensor ``t`` (None: None) after the checks of its type,
+    shape, device and layout: ValueError before any call."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev} (the device of the first input)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=1024)
+def _descriptor(*fields):
+    """A problem descriptor and the reference that calls take (never written to)."""
+    prob = GdnProblem(*fields)
+    return prob, ctypes.byref(prob)
+
+
+def _elsewhere(dev, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or (dev.type == "cuda" and dev.index != torch.cuda.current_device())
+
+
+def _current(dev) -> int:
+    """Handle of the current stream of ``dev``, the current device."""
+    if dev.type != "cuda":
+        raise ValueError(f"libgdn wants CUDA tensors, got a tensor on {dev}")
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _linrec_layout(x, g, cu_seqlens):
+    """(descriptor's reference, state shape, states shape, gate's type and
+    shape) of the recurrence on x [T, Hv, 128] or [B, T, Hv, 128]."""
     packed = cu_seqlens is not None
     if x.dim() != (3 if packed else 4):
         raise ValueError("x must be [T, Hv, 128] with cu_seqlens, else [B, T, Hv, 128]")
     if packed and cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens must be a 1-D int32 tensor [N + 1]")
-    lead, hv, dv = x.shape[:-2], x.shape[-2], x.shape[-1]
-    num_seqs = cu_seqlens.numel() - 1 if packed else x.shape[0]
-    total = x.shape[0] if packed else x.shape[0] * x.shape[1]
+    if packed:
+        total, hv, dv = x.shape
+        batch, seqlen, num_seqs = 1, 0, cu_seqlens.shape[0] - 1
+    else:
+        batch, seqlen, hv, dv = x.shape
+        total, num_seqs = batch * seqlen, batch
     channel = g.dim() == x.dim()
-    _shape("g", g, *(x.shape if channel else (*lead, hv)))
-    _want(x.dtype if channel else torch.float32, g=g)
-    _want(x.dtype, **like_x)
-    _want(torch.float32, initial_state=initial_state, states=states)
-    _want(torch.int32, cu_seqlens=cu_seqlens)
-    for name, t in like_x.items():
-        _shape(name, t, *x.shape)
-    _shape("initial_state", initial_state, num_seqs, hv, dv)
-    _shape("states", states, (total + 63) // 64, hv, dv)
-    _on_device(x.device, g=g, initial_state=initial_state, cu_seqlens=cu_seqlens, states=states, **like_x)
-    prob = GdnProblem(1 if packed else x.shape[0], 0 if packed else x.shape[1], num_seqs, total, hv, hv, dv, dv,
-                      _io_dtype(x), GDN_FLAG_GATE_CHANNEL if channel else 0, 0)
-    return prob, x.device
+    _, ref = _descriptor(batch, seqlen, num_seqs, total, hv, hv, dv, dv, _io_dtype(x),
+                         GDN_FLAG_GATE_CHANNEL if channel else 0, 0)
+    gate = (x.dtype, x.shape) if channel else (torch.float32, x.shape[:-1])
+    return ref, (num_seqs, hv, dv), ((total + 63) // 64, hv, dv), gate
 
 
 def gdn_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, out=None, final_state=None,
@@ -546,20 +580,31 @@ def gdn_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, out=None, f
     Returns (out, final_state), and with ``save_states`` (or ``states`` given)
     also the states that gdn_linear_recurrence_bwd starts from,
     [ceil(T / 64), Hv, 128] f32 over all T rows."""
-    prob, dev = _linrec_checks(x, g, initial_state, cu_seqlens, states, out=out)
-    _want(torch.float32, final_state=final_state)
-    _shape("final_state", final_state, prob.num_seqs, prob.hv, prob.dv)
-    _on_device(dev, final_state=final_state)
-    with _launching(stream, dev) as handle:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        if final_state is None and output_final_state:
-            final_state = torch.empty((prob.num_seqs, prob.hv, prob.dv), dtype=torch.float32, device=dev)
-        if states is None and save_states:
-            states = torch.empty(((prob.total_tokens + 63) // 64, prob.hv, prob.dv), dtype=torch.float32, device=dev)
-        st = load().gdn_linear_recurrence(ctypes.byref(prob), _ptr(x), _ptr(g), _ptr(initial_state),
-                                          _ptr(cu_seqlens), _ptr(out), _ptr(final_state), _ptr(states),
-                                          handle)
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_linear_recurrence(x, g, initial_state, cu_seqlens, out, final_state, output_final_state,
+                                         save_states, states)
+    ref, state_shape, states_shape, gate = _linrec_layout(x, g, cu_seqlens)
+    f32 = torch.float32
+    px = _arg("x", x, x.dtype, x.shape, dev)
+    pg = _arg("g", g, *gate, dev)
+    ps0 = _arg("initial_state", initial_state, f32, state_shape, dev)
+    pcu = _arg("cu_seqlens", cu_seqlens, torch.int32, (state_shape[0] + 1,), dev)
+    po = _arg("out", out, x.dtype, x.shape, dev)
+    pf = _arg("final_state", final_state, f32, state_shape, dev)
+    pst = _arg("states", states, f32, states_shape, dev)
+    handle = _current(dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        po = out.data_ptr()
+    if final_state is None and output_final_state:
+        final_state = torch.empty(state_shape, dtype=f32, device=dev)
+        pf = final_state.data_ptr()
+    if states is None and save_states:
+        states = torch.empty(states_shape, dtype=f32, device=dev)
+        pst = states.data_ptr()
+    st = load().gdn_linear_recurrence(ref, px, pg, ps0, pcu, po, pf, pst, handle)
     if st != GDN_OK:
         raise GdnError(st, "gdn_linear_recurrence")
     return (out, final_state) if states is None else (out, final_state, states)
@@ -571,24 +616,36 @@ def gdn_linear_recurrence_bwd(dout, x, g, states, initial_state=None, cu_seqlens
     the final state (None: zeros), with ``states`` of the forward pass.
     Returns (dx, dg, dinitial_state); dinitial_state is None unless an
     ``initial_state`` or a dinitial_state to write is given."""
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_linear_recurrence_bwd(dout, x, g, states, initial_state, cu_seqlens, dfinal_state, dx, dg,
+                                             dinitial_state)
     if states is None:
         raise ValueError("the backward pass needs the forward pass's states (save_states=True)")
-    prob, dev = _linrec_checks(x, g, initial_state, cu_seqlens, states, dout=dout, dx=dx)
-    state_shape = (prob.num_seqs, prob.hv, prob.dv)
-    _want(g.dtype, dg=dg)
-    _want(torch.float32, dfinal_state=dfinal_state, dinitial_state=dinitial_state)
-    _shape("dg", dg, *g.shape)
-    _shape("dfinal_state", dfinal_state, *state_shape)
-    _shape("dinitial_state", dinitial_state, *state_shape)
-    _on_device(dev, dg=dg, dfinal_state=dfinal_state, dinitial_state=dinitial_state)
-    with _launching(stream, dev) as handle:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
-        dg = torch.empty(g.shape, dtype=g.dtype, device=dev) if dg is None else dg
-        if dinitial_state is None and initial_state is not None:
-            dinitial_state = torch.empty(state_shape, dtype=torch.float32, device=dev)
-        st = load().gdn_linear_recurrence_bwd(ctypes.byref(prob), _ptr(dout), _ptr(x), _ptr(g), _ptr(states),
-                                              _ptr(initial_state), _ptr(dfinal_state), _ptr(cu_seqlens), _ptr(dx),
-                                              _ptr(dg), _ptr(dinitial_state), handle)
+    ref, state_shape, states_shape, gate = _linrec_layout(x, g, cu_seqlens)
+    f32 = torch.float32
+    px = _arg("x", x, x.dtype, x.shape, dev)
+    pdo = _arg("dout", dout, x.dtype, x.shape, dev)
+    pg = _arg("g", g, *gate, dev)
+    pst = _arg("states", states, f32, states_shape, dev)
+    ps0 = _arg("initial_state", initial_state, f32, state_shape, dev)
+    pcu = _arg("cu_seqlens", cu_seqlens, torch.int32, (state_shape[0] + 1,), dev)
+    pdf = _arg("dfinal_state", dfinal_state, f32, state_shape, dev)
+    pdx = _arg("dx", dx, x.dtype, x.shape, dev)
+    pdg = _arg("dg", dg, *gate, dev)
+    pd0 = _arg("dinitial_state", dinitial_state, f32, state_shape, dev)
+    handle = _current(dev)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        pdx = dx.data_ptr()
+    if dg is None:
+        dg = torch.empty(g.shape, dtype=g.dtype, device=dev)
+        pdg = dg.data_ptr()
+    if dinitial_state is None and initial_state is not None:
+        dinitial_state = torch.empty(state_shape, dtype=f32, device=dev)
+        pd0 = dinitial_state.data_ptr()
+    st = load().gdn_linear_recurrence_bwd(ref, pdo, px, pg, pst, ps0, pdf, pcu, pdx, pdg, pd0, handle)
     if st != GDN_OK:
         raise GdnError(st, "gdn_linear_recurrence_bwd")
     return dx, dg, dinitial_state
@@ -598,40 +655,40 @@ def gdn_linear_recurrence_step(x, g, state, state_indices=None, out=None, stream
     """One decode token per sequence: x [N, Hv, 128]; ``state``
     [slots, Hv, 128] f32 is updated in place at ``state_indices`` (int32 [N];
     None: slot n; negative: skipped, its out rows are not written)."""
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_linear_recurrence_step(x, g, state, state_indices, out)
     if x.dim() != 3 or state.dim() != 3:
         raise ValueError("x must be [N, Hv, 128] and state [slots, Hv, 128]")
     N, hv, dv = x.shape
+    slots = state.shape[0]
     channel = g.dim() == 3
-    _shape("g", g, *(x.shape if channel else (N, hv)))
-    _want(x.dtype if channel else torch.float32, g=g)
-    _want(x.dtype, out=out)
-    _want(torch.float32, state=state)
-    _want(torch.int32, state_indices=state_indices)
-    _shape("out", out, *x.shape)
-    _shape("state", state, state.shape[0], hv, dv)
-    _shape("state_indices", state_indices, N)
-    dev = x.device
-    _on_device(dev, g=g, state=state, state_indices=state_indices, out=out)
-    prob = GdnProblem(N, 1, N, N, hv, hv, dv, dv, _io_dtype(x), GDN_FLAG_GATE_CHANNEL if channel else 0,
-                      state.shape[0])
-    with _launching(stream, dev) as handle:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        st = load().gdn_linear_recurrence_step(ctypes.byref(prob), _ptr(x), _ptr(g), _ptr(state),
-                                               _ptr(state_indices), _ptr(out), handle)
+    px = _arg("x", x, x.dtype, x.shape, dev)
+    pg = _arg("g", g, x.dtype if channel else torch.float32, x.shape if channel else (N, hv), dev)
+    ps = _arg("state", state, torch.float32, (slots, hv, dv), dev)
+    pi = _arg("state_indices", state_indices, torch.int32, (N,), dev)
+    po = _arg("out", out, x.dtype, x.shape, dev)
+    _, ref = _descriptor(N, 1, N, N, hv, hv, dv, dv, _io_dtype(x), GDN_FLAG_GATE_CHANNEL if channel else 0, slots)
+    handle = _current(dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        po = out.data_ptr()
+    st = load().gdn_linear_recurrence_step(ref, px, pg, ps, pi, po, handle)
     if st != GDN_OK:
         raise GdnError(st, "gdn_linear_recurrence_step")
     return out
 
 
-def _rows_problem(x) -> GdnProblem:
-    """Descriptor of a row-wise norm over the last dimension of x."""
+def _rows_descriptor(x):
+    """(descriptor's reference, leading shape, width) of a row-wise norm over the last dimension of x."""
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("the last dimension must not be empty")
-    rows = x.numel() // x.shape[-1]
+    width = x.shape[-1]
+    rows = x.numel() // width
     if rows >= 1 << 31:
         raise ValueError("too many rows")
-    return GdnProblem(1, 0, 1, rows, 1, 1, x.shape[-1], x.shape[-1], _io_dtype(x), 0, 0)
+    return _descriptor(1, 0, 1, rows, 1, 1, width, width, _io_dtype(x), 0, 0)[1], x.shape[:-1], width
 
 
 def gdn_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, save_stats=False, mean=None, rstd=None,
@@ -640,35 +697,44 @@ def gdn_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, save_stats=Fals
     of x (1 to 16384 wide); weight and bias [D] f32 or None. ``out`` may be x.
     Returns y, and with ``save_stats`` (y, mean, rstd), the last two f32 of
     x's leading shape, for gdn_layernorm_bwd."""
-    prob = _rows_problem(x)
-    dev, lead = x.device, x.shape[:-1]
-    _want(x.dtype, out=out)
-    _want(torch.float32, weight=weight, bias=bias, mean=mean, rstd=rstd)
-    _shape("weight", weight, x.shape[-1])
-    _shape("bias", bias, x.shape[-1])
-    _shape("out", out, *x.shape)
-    _shape("mean", mean, *lead)
-    _shape("rstd", rstd, *lead)
-    _on_device(dev, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
-    with _launching(stream, dev) as handle:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-        if save_stats:
-            mean = torch.empty(lead, dtype=torch.float32, device=dev) if mean is None else mean
-            rstd = torch.empty(lead, dtype=torch.float32, device=dev) if rstd is None else rstd
-        st = load().gdn_layernorm(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), ctypes.c_float(eps),
-                                  _ptr(out), _ptr(mean), _ptr(rstd), handle)
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_layernorm(x, weight, bias, eps, out, save_stats, mean, rstd)
+    ref, lead, width = _rows_descriptor(x)
+    f32 = torch.float32
+    px = _arg("x", x, x.dtype, x.shape, dev)
+    pw = _arg("weight", weight, f32, (width,), dev)
+    pb = _arg("bias", bias, f32, (width,), dev)
+    po = _arg("out", out, x.dtype, x.shape, dev)
+    pm = _arg("mean", mean, f32, lead, dev)
+    pr = _arg("rstd", rstd, f32, lead, dev)
+    handle = _current(dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        po = out.data_ptr()
+    if save_stats:
+        if mean is None:
+            mean = torch.empty(lead, dtype=f32, device=dev)
+            pm = mean.data_ptr()
+        if rstd is None:
+            rstd = torch.empty(lead, dtype=f32, device=dev)
+            pr = rstd.data_ptr()
+    st = load().gdn_layernorm(ref, px, pw, pb, eps, po, pm, pr, handle)
     if st != GDN_OK:
         raise GdnError(st, "gdn_layernorm")
     return (out, mean, rstd) if save_stats else out
 
 
 def _workspace(workspace, need, dev):
-    """The caller's uint8 workspace, or one of ``need`` bytes."""
+    """(address, bytes, tensor) of the caller's uint8 workspace, or of one of
+    ``need`` bytes."""
     if workspace is None:
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        return workspace.data_ptr(), max(need, 256), workspace
     if workspace.dtype != torch.uint8:
         raise ValueError("workspace must be a uint8 tensor")
-    return workspace
+    return _arg("workspace", workspace, torch.uint8, workspace.shape, dev), workspace.numel(), workspace
 
 
 def gdn_layernorm_bwd(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, need_dweight=True,
@@ -677,30 +743,35 @@ def gdn_layernorm_bwd(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbi
     Returns (dx, dweight, dbias), the last two [D] f32 sums over all rows (None
     where not needed). ``dx`` may be dy or x. ``workspace`` (uint8, of
     gdn_layernorm_bwd_workspace_size bytes) is allocated when not supplied."""
-    prob = _rows_problem(x)
-    dev, lead, D = x.device, x.shape[:-1], x.shape[-1]
-    _want(x.dtype, dy=dy, dx=dx)
-    _want(torch.float32, mean=mean, rstd=rstd, weight=weight, dweight=dweight, dbias=dbias)
-    _shape("dy", dy, *x.shape)
-    _shape("dx", dx, *x.shape)
-    _shape("mean", mean, *lead)
-    _shape("rstd", rstd, *lead)
-    for name, t in (("weight", weight), ("dweight", dweight), ("dbias", dbias)):
-        _shape(name, t, D)
-    _on_device(dev, dy=dy, mean=mean, rstd=rstd, weight=weight, dx=dx, dweight=dweight, dbias=dbias,
-               workspace=workspace)
-    with _launching(stream, dev) as handle:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
-        if dweight is None and need_dweight:
-            dweight = torch.empty(D, dtype=torch.float32, device=dev)
-        if dbias is None and need_dbias:
-            dbias = torch.empty(D, dtype=torch.float32, device=dev)
-        if dweight is not None or dbias is not None or workspace is not None:
-            workspace = _workspace(workspace, int(load().gdn_layernorm_bwd_workspace_size(ctypes.byref(prob))), dev)
-        st = load().gdn_layernorm_bwd(ctypes.byref(prob), _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
-                                      _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
-                                      ctypes.c_size_t(0 if workspace is None else workspace.numel()),
-                                      handle)
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, need_dweight, need_dbias,
+                                     workspace)
+    ref, lead, width = _rows_descriptor(x)
+    f32 = torch.float32
+    px = _arg("x", x, x.dtype, x.shape, dev)
+    pdy = _arg("dy", dy, x.dtype, x.shape, dev)
+    pm = _arg("mean", mean, f32, lead, dev)
+    pr = _arg("rstd", rstd, f32, lead, dev)
+    pw = _arg("weight", weight, f32, (width,), dev)
+    pdx = _arg("dx", dx, x.dtype, x.shape, dev)
+    pdw = _arg("dweight", dweight, f32, (width,), dev)
+    pdb = _arg("dbias", dbias, f32, (width,), dev)
+    handle = _current(dev)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        pdx = dx.data_ptr()
+    if dweight is None and need_dweight:
+        dweight = torch.empty(width, dtype=f32, device=dev)
+        pdw = dweight.data_ptr()
+    if dbias is None and need_dbias:
+        dbias = torch.empty(width, dtype=f32, device=dev)
+        pdb = dbias.data_ptr()
+    lib, pws, nbytes = load(), None, 0
+    if pdw or pdb or workspace is not None:
+        pws, nbytes, workspace = _workspace(workspace, lib.gdn_layernorm_bwd_workspace_size(ref), dev)
+    st = lib.gdn_layernorm_bwd(ref, pdy, px, pm, pr, pw, pdx, pdw, pdb, pws, nbytes, handle)
     if st != GDN_OK:
         raise GdnError(st, "gdn_layernorm_bwd")
     return dx, dweight, dbias
@@ -713,30 +784,36 @@ def gdn_gated_rmsnorm_bwd(dy, o, z, weight, eps, do=None, dz=None, dweight=None,
     head) rows (None where not needed). do and dz may be any of dy, o and z.
     ``workspace`` (uint8, of gdn_gated_rmsnorm_bwd_workspace_size bytes) is
     allocated when not supplied."""
+    dev = o.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_gated_rmsnorm_bwd(dy, o, z, weight, eps, do, dz, dweight, need_dweight, workspace)
     if o.dim() != 3:
         raise ValueError("o must be [T, Hv, 128]")
-    T, hv, dv = o.shape
-    dev = o.device
-    _want(o.dtype, dy=dy, z=z, do=do, dz=dz)
-    _want(torch.float32, weight=weight, dweight=dweight)
-    for name, t in (("dy", dy), ("z", z), ("do", do), ("dz", dz)):
-        _shape(name, t, *o.shape)
-    _shape("weight", weight, dv)
-    _shape("dweight", dweight, dv)
-    _on_device(dev, dy=dy, z=z, weight=weight, do=do, dz=dz, dweight=dweight, workspace=workspace)
-    prob = GdnProblem(1, 0, 1, T, 1, hv, dv, dv, _io_dtype(o), 0, 0)
-    with _launching(stream, dev) as handle:
-        do = torch.empty_like(o) if do is None else do
-        dz = torch.empty_like(o) if dz is None else dz
-        if dweight is None and need_dweight:
-            dweight = torch.empty(dv, dtype=torch.float32, device=dev)
-        if dweight is not None or workspace is not None:
-            workspace = _workspace(workspace, int(load().gdn_gated_rmsnorm_bwd_workspace_size(ctypes.byref(prob))),
-                                   dev)
-        st = load().gdn_gated_rmsnorm_bwd(ctypes.byref(prob), _ptr(dy), _ptr(o), _ptr(z), _ptr(weight),
-                                          ctypes.c_float(eps), _ptr(do), _ptr(dz), _ptr(dweight), _ptr(workspace),
-                                          ctypes.c_size_t(0 if workspace is None else workspace.numel()),
-                                          handle)
+    T, hv, dv = shape = o.shape
+    f32, io = torch.float32, o.dtype
+    po = _arg("o", o, io, shape, dev)
+    pdy = _arg("dy", dy, io, shape, dev)
+    pz = _arg("z", z, io, shape, dev)
+    pw = _arg("weight", weight, f32, (dv,), dev)
+    pdo = _arg("do", do, io, shape, dev)
+    pdz = _arg("dz", dz, io, shape, dev)
+    pdw = _arg("dweight", dweight, f32, (dv,), dev)
+    _, ref = _descriptor(1, 0, 1, T, 1, hv, dv, dv, _io_dtype(o), 0, 0)
+    handle = _current(dev)
+    if do is None:
+        do = torch.empty(shape, dtype=io, device=dev)
+        pdo = do.data_ptr()
+    if dz is None:
+        dz = torch.empty(shape, dtype=io, device=dev)
+        pdz = dz.data_ptr()
+    if dweight is None and need_dweight:
+        dweight = torch.empty(dv, dtype=f32, device=dev)
+        pdw = dweight.data_ptr()
+    lib, pws, nbytes = load(), None, 0
+    if pdw or workspace is not None:
+        pws, nbytes, workspace = _workspace(workspace, lib.gdn_gated_rmsnorm_bwd_workspace_size(ref), dev)
+    st = lib.gdn_gated_rmsnorm_bwd(ref, pdy, po, pz, pw, eps, pdo, pdz, pdw, pws, nbytes, handle)
     if st != GDN_OK:
         raise GdnError(st, "gdn_gated_rmsnorm_bwd")
     return do, dz, dweight
