@@ -472,7 +472,7 @@ int gdn_layernorm(const gdn_problem *p, const void *x, const float *weight, cons
 }
 
 size_t gdn_layernorm_bwd_workspace_size(const gdn_problem *p) {
-    return check_layernorm(p) == GDN_OK ? layernorm_bwd_workspace(p->total_tokens, p->dv) : 0;
+    return check_layernorm(p) == GDN_OK ? layernorm_bwd_workspace(p->total_tokens, p->dv, p->io_dtype) : 0;
 }
 
 int gdn_layernorm_bwd(const gdn_problem *p, const void *dy, const void *x, const float *mean, const float *rstd,

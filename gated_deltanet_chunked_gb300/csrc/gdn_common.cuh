@@ -106,7 +106,7 @@ cudaError_t launch_gated_rmsnorm(const void *o, const void *z, const float *weig
 cudaError_t launch_layernorm(const void *x, const float *weight, const float *bias, float eps, void *y, float *mean,
                              float *rstd, int rows, int width, int io_dtype, cudaStream_t s);
 constexpr int kLayerNormMaxWidth = 16384;  // widest row the layer norm's kernels hold in registers
-size_t layernorm_bwd_workspace(int rows, int width);
+size_t layernorm_bwd_workspace(int rows, int width, int io_dtype);
 cudaError_t launch_layernorm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
                                  const float *weight, void *dx, float *dweight, float *dbias, void *workspace,
                                  int rows, int width, int io_dtype, cudaStream_t s);

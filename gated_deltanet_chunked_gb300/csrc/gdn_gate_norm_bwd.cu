@@ -17,7 +17,7 @@ namespace {
 using vec::Pack;
 
 constexpr int kBThreads = 256;
-constexpr int kMaxCtas = 1216;  // 8 CTAs on each of 152 SMs
+constexpr int kMaxCtas = 456;  // three CTAs on each of 152 SMs: what registers allow
 
 struct GateBwdArgs {
     const void *dy, *o, *z;
@@ -29,7 +29,7 @@ struct GateBwdArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kBThreads) k_gated_rmsnorm_bwd(const GateBwdArgs a) {
+__global__ void __launch_bounds__(kBThreads, 3) k_gated_rmsnorm_bwd(const GateBwdArgs a) {
     constexpr int VE = 16 / int(sizeof(T)), G = kHeadDim / VE, kGroups = kBThreads / G;
     const int tid = threadIdx.x % G, group = threadIdx.x / G;
     const T *dy = static_cast<const T *>(a.dy) + tid * VE, *o = static_cast<const T *>(a.o) + tid * VE,

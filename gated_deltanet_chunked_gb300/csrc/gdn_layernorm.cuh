@@ -1,65 +1,145 @@
 // How the layer norm's kernels divide a row of `width` elements.
 //
-// A row is held in registers, so that it is read once: EPT = VE * NV elements
-// a thread, VE of them consecutive (one load). VE is the widest load that
-// every row's start is aligned to: 16 bytes where the width allows, else one
-// element (an odd width leaves every other row unaligned). G lanes of a warp
-// share a row where it is short, so that no lane is without elements; longer
-// rows take a whole CTA (G = 0).
+// A row is held in registers, so that it is read once; every load is 16 bytes,
+// VE elements, NV of them a thread. Rows whose width is no multiple of VE do
+// not start on 16 bytes: such a row's vectors begin up to VE - 1 elements
+// before it, at the last aligned address, and its first and last vector go
+// element by element. A CTA's rows are a multiple of eight apart, so all rows
+// of a thread have the same misalignment and it owns the same columns of all.
+// G lanes of a warp share a row where it is short, so that no lane is without
+// elements; longer rows take a whole CTA (G = 0).
 #pragma once
+
+#include <atomic>
 
 #include "gdn_vec.cuh"
 
 namespace gdn {
 namespace ln {
 
-constexpr int kEpt = 16;          // elements per thread at most
-constexpr int kWarpWidth = 512;   // widest row of one warp: 32 x kEpt
-constexpr int kRowThreads = 256;  // threads of a CTA whose warps take rows of their own
+constexpr int kSms = 152;
+constexpr int kRowThreads = 256;  // threads of a CTA whose warps take rows of their own, and wanted of others
 
 struct Shape {
-    int ve, nv, g;     // elements per load, loads per thread, lanes per row (0: the CTA)
+    bool aligned;      // every row starts on 16 bytes
+    int nv, g;         // loads per thread, lanes per row (0: the CTA)
     int threads;       // of a CTA
     int rows_per_cta;  // rows in work at a time
 };
 
 template <typename T>
 inline Shape shape_of(int width) {
-    constexpr int kVec = 16 / int(sizeof(T));
+    constexpr int VE = 16 / int(sizeof(T)), kMost = 16 / VE;  // at most 16 elements a thread
     Shape s;
-    s.ve = width % kVec == 0 ? kVec : 1;
-    const int small = s.ve == 1 ? 4 : 1;  // loads a thread of the variant for short rows
-    const int large = kEpt / s.ve;
-    if (width <= 16 * s.ve * small) {
-        s.nv = small, s.g = 16;
-    } else if (width <= 32 * s.ve * small) {
-        s.nv = small, s.g = 32;
-    } else if (width <= kWarpWidth) {
-        s.nv = large, s.g = 32;
-    } else {
-        s.nv = large, s.g = 0;
-    }
-    s.threads = s.g ? kRowThreads : ((width + s.ve * s.nv - 1) / (s.ve * s.nv) + 31) / 32 * 32;
+    s.aligned = width % VE == 0;
+    const int vecs = s.aligned ? width / VE : (width + VE - 1 + VE - 1) / VE;  // for any misalignment
+    s.g = vecs <= 16 ? 16 : vecs <= 32 * kMost ? 32 : 0;
+    const int lanes = s.g ? s.g : kRowThreads;
+    s.nv = 1;
+    while (s.nv < kMost && vecs > lanes * s.nv) s.nv *= 2;
+    if (vecs > 1024 * s.nv) s.nv *= 2;  // unaligned, and the widest by a few elements: one vector too many
+    s.threads = s.g ? kRowThreads : ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
     s.rows_per_cta = s.g ? kRowThreads / s.g : 1;
     return s;
 }
 
-// calls F<VE, NV, G>(...) for the shape
-#define GDN_LN_DISPATCH(T, s, F, ...)                                                  \
-    do {                                                                               \
-        constexpr int kV = 16 / int(sizeof(T));                                        \
-        if ((s).ve == kV) {                                                            \
-            if ((s).g == 16) F<T, kV, 1, 16>(__VA_ARGS__);                             \
-            else if ((s).g == 32 && (s).nv == 1) F<T, kV, 1, 32>(__VA_ARGS__);         \
-            else if ((s).g == 32) F<T, kV, ln::kEpt / kV, 32>(__VA_ARGS__);            \
-            else F<T, kV, ln::kEpt / kV, 0>(__VA_ARGS__);                              \
-        } else {                                                                       \
-            if ((s).g == 16) F<T, 1, 4, 16>(__VA_ARGS__);                              \
-            else if ((s).g == 32 && (s).nv == 4) F<T, 1, 4, 32>(__VA_ARGS__);          \
-            else if ((s).g == 32) F<T, 1, ln::kEpt, 32>(__VA_ARGS__);                  \
-            else F<T, 1, ln::kEpt, 0>(__VA_ARGS__);                                    \
-        }                                                                              \
-    } while (0)
+// calls F<T, NV, G, ALIGNED>(...) for the shape
+template <typename T, template <typename, int, int, bool> class F, bool ALIGNED, typename... A>
+inline cudaError_t dispatch_nv(const Shape &s, A &...a) {
+    constexpr int kMost = 4 * int(sizeof(T)) / 4;  // 16 / VE: 2 for bf16, 4 for f32
+    if (s.g == 16) return F<T, 1, 16, ALIGNED>::run(s, a...);
+    if (s.g == 32) {
+        if (s.nv == 1) return F<T, 1, 32, ALIGNED>::run(s, a...);
+        if (s.nv == 2) return F<T, 2, 32, ALIGNED>::run(s, a...);
+        return F<T, kMost, 32, ALIGNED>::run(s, a...);
+    }
+    if (s.nv == 1) return F<T, 1, 0, ALIGNED>::run(s, a...);
+    if (s.nv == 2) return F<T, 2, 0, ALIGNED>::run(s, a...);
+    if (ALIGNED || s.nv == kMost) return F<T, kMost, 0, ALIGNED>::run(s, a...);
+    return F<T, ALIGNED ? kMost : 2 * kMost, 0, ALIGNED>::run(s, a...);
+}
+template <typename T, template <typename, int, int, bool> class F, typename... A>
+inline cudaError_t dispatch(const Shape &s, A &...a) {
+    return s.aligned ? dispatch_nv<T, F, true>(s, a...) : dispatch_nv<T, F, false>(s, a...);
+}
+
+// CTAs of kernel `fn` that an SM holds at `threads` each, asked once a kernel
+// (K: a type of its own), thread count and device.
+template <typename K>
+inline int ctas_per_sm(const void *fn, int threads, size_t smem = 0) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][33];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) dev = -1;
+    int n = dev < 0 ? 0 : known[dev][threads / 32].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess || n < 1) n = 1;
+    if (dev >= 0) known[dev][threads / 32].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// A thread's place: its row group, and its vectors' columns.
+template <typename T, int NV, int G, bool ALIGNED>
+struct Place {
+    static constexpr int VE = 16 / int(sizeof(T));
+    using P = vec::Pack<T, VE>;
+    int tid;
+    long long row, base, step;  // first row; first row of the warp (CTA), which decides when it ends; rows apart
+    int col[NV];
+    int width;
+
+    __device__ __forceinline__ Place(int w) : width(w) {
+        constexpr int g = G ? G : 1;
+        const int groups = G ? int(blockDim.x) / g : 1, group = G ? int(threadIdx.x) / g : 0;
+        tid = G ? int(threadIdx.x) % g : int(threadIdx.x);
+        row = (long long)blockIdx.x * groups + group;
+        base = G ? row - (threadIdx.x & 31) / g : row;
+        step = (long long)gridDim.x * groups;
+        const int off = ALIGNED ? 0 : int(row * width % VE);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) col[i] = (tid + i * (G ? G : int(blockDim.x))) * VE - off;
+    }
+    __device__ __forceinline__ bool full(int i) const {
+        return ALIGNED ? col[i] < width : col[i] >= 0 && col[i] + VE <= width;
+    }
+    // whether element j of vector i is in the row
+    __device__ __forceinline__ bool has(int i, int j) const {
+        return ALIGNED ? col[i] < width : unsigned(col[i] + j) < unsigned(width);
+    }
+    // vector i of the row at p; zeros outside the row
+    __device__ __forceinline__ void load(P &v, int i, const T *p) const {
+        if (full(i)) {
+            v.load(p + col[i]);
+        } else if (!ALIGNED) {
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+                if (has(i, j)) v.e[j] = p[col[i] + j];
+        }
+    }
+    __device__ __forceinline__ void store(const P &v, int i, T *p) const {
+        if (full(i)) {
+            v.store(p + col[i]);
+        } else if (!ALIGNED) {
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+                if (has(i, j)) p[col[i] + j] = v.e[j];
+        }
+    }
+    // a per-column f32 array (null: `otherwise`), zeros outside the row
+    __device__ __forceinline__ void load_columns(float (&w)[NV][VE], const float *p, float otherwise) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (ALIGNED && p && full(i)) {
+#pragma unroll
+                for (int j = 0; j < VE; j += 4)
+                    *reinterpret_cast<float4 *>(&w[i][j]) = *reinterpret_cast<const float4 *>(p + col[i] + j);
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < VE; ++j) w[i][j] = !has(i, j) ? 0.f : p ? p[col[i] + j] : otherwise;
+        }
+    }
+};
 
 }  // namespace ln
 }  // namespace gdn

@@ -25,40 +25,70 @@ struct LnBwdArgs {
     int rows, width;
 };
 
-template <typename T, int VE, int NV, int G, int MT>
-__global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(const LnBwdArgs a) {
-    __shared__ float2 red[2][32];
-    const int per_row = G ? G : int(blockDim.x);
-    const int tid = G ? int(threadIdx.x) % (G ? G : 1) : int(threadIdx.x);
-    const long long step = (long long)gridDim.x * (G ? int(blockDim.x) / (G ? G : 1) : 1);
-    long long row = G ? (long long)blockIdx.x * (int(blockDim.x) / (G ? G : 1)) + int(threadIdx.x) / (G ? G : 1)
-                      : (long long)blockIdx.x;
-    const long long first = G ? row - (threadIdx.x & 31) / (G ? G : 1) : row;
-    const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
-    T *dx = static_cast<T *>(a.dx);
-    float w[NV][VE], dw[NV][VE], db[NV][VE];
-    bool has[NV];
-    int col[NV];
+// The thread's sums over rows: in registers, or (IN_SMEM) in shared memory, four
+// columns at a time at a thread's own place.
+template <int NV, int VE, bool IN_SMEM>
+struct Sums {
+    float v[NV][VE];
+    __device__ __forceinline__ explicit Sums(float4 *) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        col[i] = (tid + i * per_row) * VE;
-        has[i] = col[i] < a.width;
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            w[i][j] = has[i] && a.weight ? a.weight[col[i] + j] : 1.f;
-            dw[i][j] = db[i][j] = 0.f;
+            for (int j = 0; j < VE; ++j) v[i][j] = 0.f;
+    }
+    __device__ __forceinline__ void add(int i, const float (&a)[VE], const float (&b)[VE]) {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[i][j] = fmaf(a[j], b[j], v[i][j]);
+    }
+    __device__ __forceinline__ float get(int i, int j) const { return v[i][j]; }
+};
+template <int NV, int VE>
+struct Sums<NV, VE, true> {
+    float4 *p;
+    __device__ __forceinline__ explicit Sums(float4 *base) : p(base + threadIdx.x) {
+#pragma unroll
+        for (int k = 0; k < NV * VE / 4; ++k) p[k * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ void add(int i, const float (&a)[VE], const float (&b)[VE]) {
+#pragma unroll
+        for (int q = 0; q < VE; q += 4) {
+            float4 &r = p[(i * VE + q) / 4 * blockDim.x];
+            float4 t = r;
+            t.x = fmaf(a[q], b[q], t.x), t.y = fmaf(a[q + 1], b[q + 1], t.y);
+            t.z = fmaf(a[q + 2], b[q + 2], t.z), t.w = fmaf(a[q + 3], b[q + 3], t.w);
+            r = t;
         }
     }
+    __device__ __forceinline__ float get(int i, int j) const {
+        return reinterpret_cast<const float *>(p + (i * VE + j) / 4 * blockDim.x)[j % 4];
+    }
+};
+
+// MT, the most threads of a CTA: with 1024 a thread has 64 registers, too few
+// for its sums and its weights, which then are in shared memory and read again
+// for every row.
+template <typename T, int NV, int G, bool ALIGNED, int MT>
+__global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(const LnBwdArgs a) {
+    using L = ln::Place<T, NV, G, ALIGNED>;
+    constexpr int VE = L::VE;
+    constexpr bool kWide = MT == 1024;
+    extern __shared__ float4 wide_sums[];  // kWide: two sums for every column of a thread
+    __shared__ float2 red[2][32];
+    const L at(a.width);
+    const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
+    T *dx = static_cast<T *>(a.dx);
+    float w[NV][VE];
+    if (!kWide) at.load_columns(w, a.weight, 1.f);
+    Sums<NV, VE, kWide> dw(wide_sums), db(wide_sums + NV * VE / 4 * blockDim.x);
     const float inv_width = 1.f / float(a.width);
     Pack<T, VE> nx[NV], ny[NV];
     float nmean = 0.f, nrstd = 0.f;
     auto fetch = [&](long long r) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (has[i]) {
-                nx[i].load(x + r * a.width + col[i]);
-                ny[i].load(dy + r * a.width + col[i]);
-            }
+        for (int i = 0; i < NV; ++i) {
+            at.load(nx[i], i, x + r * a.width);
+            at.load(ny[i], i, dy + r * a.width);
+        }
         nmean = a.mean[r];
         nrstd = a.rstd[r];
     };
@@ -67,9 +97,10 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
         nx[i].zero();
         ny[i].zero();
     }
+    long long row = at.row;
     if (row < a.rows) fetch(row);
     int turn = 0;
-    for (long long base = first; base < a.rows; base += step, row += step, turn ^= 1) {
+    for (long long base = at.base; base < a.rows; base += at.step, row += at.step, turn ^= 1) {
         const bool live = row < a.rows;
         const float rstd = nrstd, mean = nmean;
         float xhat[NV][VE], g[NV][VE], s1 = 0.f, s2 = 0.f;
@@ -80,15 +111,18 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
                 xhat[i][j] = __fmul_rn(nx[i].f(j) - mean, rstd);
                 g[i][j] = ny[i].f(j);
             }
-        if (row + step < a.rows) fetch(row + step);
-        if (live) {
+        if (row + at.step < a.rows) fetch(row + at.step);
+        if (live) {  // outside the row g is zero
+            if (kWide) at.load_columns(w, a.weight, 1.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (!has[i]) continue;
+                float one[VE];
+#pragma unroll
+                for (int j = 0; j < VE; ++j) one[j] = 1.f;
+                dw.add(i, g[i], xhat[i]);
+                db.add(i, g[i], one);
 #pragma unroll
                 for (int j = 0; j < VE; ++j) {
-                    dw[i][j] = fmaf(g[i][j], xhat[i][j], dw[i][j]);
-                    db[i][j] += g[i][j];
                     g[i][j] = __fmul_rn(g[i][j], w[i][j]);
                     s1 += g[i][j];
                     s2 = fmaf(g[i][j], xhat[i][j], s2);
@@ -107,25 +141,24 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
         if (live) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (!has[i]) continue;
                 Pack<T, VE> o;
 #pragma unroll
                 for (int j = 0; j < VE; ++j) o.set(j, rstd * fmaf(-xhat[i][j], s2, g[i][j] - s1));
-                o.store(dx + row * a.width + col[i]);
+                at.store(o, i, dx + row * a.width);
             }
         }
     }
     if (!a.dw_part) return;
+    float *dwp = a.dw_part + (long long)blockIdx.x * a.width, *dbp = a.db_part + (long long)blockIdx.x * a.width;
     if (!G) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!has[i]) continue;
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                a.dw_part[(long long)blockIdx.x * a.width + col[i] + j] = dw[i][j];
-                a.db_part[(long long)blockIdx.x * a.width + col[i] + j] = db[i][j];
-            }
-        }
+            for (int j = 0; j < VE; ++j)
+                if (at.has(i, j)) {
+                    dwp[at.col[i] + j] = dw.get(i, j);
+                    dbp[at.col[i] + j] = db.get(i, j);
+                }
     } else {
         // the CTA's row groups, added in order; one of the two sums at a time
         constexpr int kCols = (G ? G : 1) * VE * NV;
@@ -138,11 +171,13 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < VE; ++j) part[group * kCols + col[i] + j] = pass ? db[i][j] : dw[i][j];
+                for (int j = 0; j < VE; ++j)
+                    if (at.has(i, j)) part[group * kCols + at.col[i] + j] = pass ? db.get(i, j) : dw.get(i, j);
             __syncthreads();
-            float *out = (pass ? a.db_part : a.dw_part) + (long long)blockIdx.x * a.width;
+            float *out = pass ? dbp : dwp;
             for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
                 float t = 0.f;
+#pragma unroll
                 for (int k = 0; k < kGroups; ++k) t += part[k * kCols + c];
                 out[c] = t;
             }
@@ -150,32 +185,45 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
     }
 }
 
-// CTAs of a launch, one partial row each. Short rows: enough CTAs to fill the
-// SMs with warps; long rows: two CTAs an SM, so that the partial rows stay few.
-// The bound is a constant of the width, so the workspace does not depend on
-// the device.
-int max_parts(int width) { return width <= ln::kWarpWidth ? 1216 : 304; }
+// Most CTAs of a launch, one partial row each: what the SMs hold of CTAs of
+// that size, as a constant of the width, so that the workspace does not depend
+// on the device.
+int max_parts(int threads) { return ln::kSms * (threads <= 128 ? 8 : threads <= 256 ? 4 : threads <= 512 ? 2 : 1); }
 
 template <typename T>
-int parts_of(int rows, int width) {
-    const ln::Shape sh = ln::shape_of<T>(width);
-    const long long ctas = ((long long)rows + sh.rows_per_cta - 1) / sh.rows_per_cta;
-    return int(ctas < max_parts(width) ? ctas : max_parts(width));
+size_t workspace_of(int rows, int width) {
+    const int most = max_parts(ln::shape_of<T>(width).threads);
+    return (2 * size_t(rows < most ? rows : most) * size_t(width) * sizeof(float) + 255) & ~size_t(255);
 }
 
-template <typename T, int VE, int NV, int G>
-void launch(const LnBwdArgs &a, const ln::Shape &sh, int parts, cudaStream_t s) {
-    if (sh.threads <= 512)
-        k_layernorm_bwd<T, VE, NV, G, 512><<<unsigned(parts), sh.threads, 0, s>>>(a);
-    else if (!G)
-        k_layernorm_bwd<T, VE, NV, G, G ? 512 : 1024><<<unsigned(parts), sh.threads, 0, s>>>(a);
-}
-
-template <typename T>
-void dispatch(const LnBwdArgs &a, int parts, cudaStream_t s) {
-    const ln::Shape sh = ln::shape_of<T>(a.width);
-    GDN_LN_DISPATCH(T, sh, launch, a, sh, parts, s);
-}
+template <typename T, int NV, int G, bool ALIGNED>
+struct Run {
+    template <int MT>
+    static cudaError_t go(const ln::Shape &sh, LnBwdArgs &a, bool sums, int &parts, cudaStream_t s) {
+        const auto fn = k_layernorm_bwd<T, NV, G, ALIGNED, MT>;
+        struct Key;
+        const size_t smem = MT == 1024 ? size_t(sh.threads) * NV * 16 / sizeof(T) * 2 * sizeof(float) : 0;
+        if (smem) {
+            const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+            if (e != cudaSuccess) return e;
+        }
+        const long long ctas = ((long long)a.rows + sh.rows_per_cta - 1) / sh.rows_per_cta;
+        long long most = (long long)ln::kSms * ln::ctas_per_sm<Key>(reinterpret_cast<const void *>(fn), sh.threads, smem);
+        if (most > max_parts(sh.threads)) most = max_parts(sh.threads);
+        // few rows: four at least a CTA, which writes two f32 rows of sums, while every SM has two CTAs
+        if (sums && ctas < 4 * most) most = ctas / 4 > 2 * ln::kSms ? ctas / 4 / 8 * 8 : 2 * ln::kSms;
+        parts = int(ctas < most ? ctas : most);
+        if (sums) a.db_part = a.dw_part + size_t(parts) * a.width;
+        fn<<<unsigned(parts), sh.threads, smem, s>>>(a);
+        return cudaGetLastError();
+    }
+    static cudaError_t run(const ln::Shape &sh, LnBwdArgs &a, bool sums, int &parts, cudaStream_t s) {
+        // more than 512 threads only with the most elements a thread
+        constexpr int kMost = !G && NV * 16 / int(sizeof(T)) >= 16 ? 1024 : 512;
+        return sh.threads <= 512 ? go<512>(sh, a, sums, parts, s) : go<kMost>(sh, a, sums, parts, s);
+    }
+};
 
 constexpr int kSumLanes = 32;  // rows of partial sums in work at a time
 
@@ -189,6 +237,7 @@ __global__ void __launch_bounds__(32 * kSumLanes) k_row_sums(const float *a, con
     const int c = blockIdx.x * 32 + threadIdx.x;
     float sum = 0.f;
     if (c < width)
+#pragma unroll 8
         for (int r = threadIdx.y; r < parts; r += kSumLanes) sum += in[(long long)r * width + c];
     t[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
@@ -208,29 +257,25 @@ cudaError_t launch_row_sums(const float *a, const float *b, int parts, int width
     return cudaGetLastError();
 }
 
-size_t layernorm_bwd_workspace(int rows, int width) {
-    const size_t parts = size_t(rows < max_parts(width) ? rows : max_parts(width));
-    return (2 * parts * size_t(width) * sizeof(float) + 255) & ~size_t(255);
+size_t layernorm_bwd_workspace(int rows, int width, int io_dtype) {
+    return io_dtype == GDN_DT_BF16 ? workspace_of<__nv_bfloat16>(rows, width) : workspace_of<float>(rows, width);
 }
 
 cudaError_t launch_layernorm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
                                  const float *weight, void *dx, float *dweight, float *dbias, void *workspace,
                                  int rows, int width, int io_dtype, cudaStream_t s) {
-    const bool bf = io_dtype == GDN_DT_BF16;
-    const int parts = bf ? parts_of<__nv_bfloat16>(rows, width) : parts_of<float>(rows, width);
-    float *dw = static_cast<float *>(workspace), *db = dw + size_t(parts) * width;
     const bool sums = dweight || dbias;
+    int parts = 0;
+    LnBwdArgs a{dy, x, mean, rstd, weight, dx, sums ? static_cast<float *>(workspace) : nullptr, nullptr, rows, width};
     if (rows > 0) {
-        const LnBwdArgs a{dy, x, mean, rstd, weight, dx, sums ? dw : nullptr, sums ? db : nullptr, rows, width};
         LaunchScope scope(GDN_K_LAYERNORM_BWD, s);
-        if (bf)
-            dispatch<__nv_bfloat16>(a, parts, s);
-        else
-            dispatch<float>(a, parts, s);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e =
+            io_dtype == GDN_DT_BF16
+                ? ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(width), a, sums, parts, s)
+                : ln::dispatch<float, Run>(ln::shape_of<float>(width), a, sums, parts, s);
         if (e != cudaSuccess) return e;
     }
-    return launch_row_sums(dw, db, parts, width, dweight, dbias, s);
+    return launch_row_sums(a.dw_part, a.db_part, parts, width, dweight, dbias, s);
 }
 
 }  // namespace gdn
