@@ -35,11 +35,12 @@ __global__ void __launch_bounds__(kBThreads, 3) k_gated_rmsnorm_bwd(const GateBw
     const T *dy = static_cast<const T *>(a.dy) + tid * VE, *o = static_cast<const T *>(a.o) + tid * VE,
             *z = static_cast<const T *>(a.z) + tid * VE;
     T *d_o = static_cast<T *>(a.d_o) + tid * VE, *d_z = static_cast<T *>(a.d_z) + tid * VE;
-    float w[VE], dw[VE];
+    constexpr int H = VE / 2;  // pairs of a thread
+    float2 w[H], dw[H];
 #pragma unroll
-    for (int j = 0; j < VE; ++j) {
-        w[j] = a.weight[tid * VE + j];
-        dw[j] = 0.f;
+    for (int k = 0; k < H; ++k) {
+        w[k] = reinterpret_cast<const float2 *>(a.weight + tid * VE)[k];
+        dw[k] = make_float2(0.f, 0.f);
     }
     const long long step = (long long)gridDim.x * kGroups;
     long long row = (long long)blockIdx.x * kGroups + group;
@@ -54,37 +55,40 @@ __global__ void __launch_bounds__(kBThreads, 3) k_gated_rmsnorm_bwd(const GateBw
         py.load(dy + r * kHeadDim);
     };
     if (row < a.rows) fetch(row);
+    using vec::both;
+    using vec::fma2;
+    using vec::mul2;
     for (long long base = first; base < a.rows; base += step, row += step) {
-        float n[VE], zz[VE], g[VE], ss = 0.f;
+        float2 n[H], zz[H], g[H], ss = both(0.f);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            n[j] = po.f(j);
-            zz[j] = pz.f(j);
-            g[j] = py.f(j);
-            ss = fmaf(n[j], n[j], ss);
+        for (int k = 0; k < H; ++k) {
+            n[k] = po.f2(k);
+            zz[k] = pz.f2(k);
+            g[k] = py.f2(k);
+            ss = fma2(n[k], n[k], ss);
         }
         if (row + step < a.rows) fetch(row + step);
         const bool live = row < a.rows;
-        const float r = 1.f / sqrtf(fmaf(vec::group_sum<G>(ss), 1.f / kHeadDim, a.eps));
-        float u[VE], un = 0.f;
+        const float r = 1.f / sqrtf(fmaf(vec::group_sum<G>(vec::sum2(ss)), 1.f / kHeadDim, a.eps));
+        float2 u[H], uns = both(0.f);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            const float sig = 1.f / (1.f + expf(-zz[j]));
-            const float silu = __fmul_rn(zz[j], sig);
-            n[j] = __fmul_rn(n[j], r);
-            const float gn = __fmul_rn(g[j], n[j]);
-            if (live) dw[j] = fmaf(gn, silu, dw[j]);
-            u[j] = __fmul_rn(__fmul_rn(g[j], w[j]), silu);
-            un = fmaf(u[j], n[j], un);
-            zz[j] = __fmul_rn(gn, w[j]) * fmaf(silu, 1.f - sig, sig);
+        for (int k = 0; k < H; ++k) {
+            const float2 sig = vec::sigmoid2(zz[k]), silu = mul2(zz[k], sig);
+            n[k] = mul2(n[k], both(r));
+            const float2 gn = mul2(g[k], n[k]);
+            if (live) dw[k] = fma2(gn, silu, dw[k]);
+            u[k] = mul2(mul2(g[k], w[k]), silu);
+            uns = fma2(u[k], n[k], uns);
+            // silu' = s + silu (1 - s)
+            zz[k] = mul2(mul2(gn, w[k]), fma2(silu, vec::add2(both(1.f), make_float2(-sig.x, -sig.y)), sig));
         }
-        un = vec::group_sum<G>(un) * (1.f / kHeadDim);
+        const float un = vec::group_sum<G>(vec::sum2(uns)) * (1.f / kHeadDim);
         if (live) {
             Pack<T, VE> q, t;
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                q.set(j, r * fmaf(-n[j], un, u[j]));
-                t.set(j, zz[j]);
+            for (int k = 0; k < H; ++k) {
+                q.set2(k, mul2(fma2(n[k], both(-un), u[k]), both(r)));
+                t.set2(k, zz[k]);
             }
             q.store(d_o + row * kHeadDim);
             t.store(d_z + row * kHeadDim);
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(kBThreads, 3) k_gated_rmsnorm_bwd(const GateBw
     if (!a.part) return;
     __shared__ float sums[kGroups][kHeadDim];
 #pragma unroll
-    for (int j = 0; j < VE; ++j) sums[group][tid * VE + j] = dw[j];
+    for (int k = 0; k < H; ++k) *reinterpret_cast<float2 *>(&sums[group][tid * VE + 2 * k]) = dw[k];
     __syncthreads();
     if (threadIdx.x < kHeadDim) {
         float t = 0.f;

@@ -6,9 +6,10 @@
 // (the mean first, then the squares about it: no cancellation whatever the
 // row's offset) and written once. Threads keep their columns' weight and bias
 // in registers over all their rows, and the next row's loads are issued
-// before the current row's reductions. Roundings are written out (fmaf,
-// __fmul_rn): the same row gives the same bits with and without the optional
-// outputs, which the compiler may turn into separate copies of the loop.
+// before the current row's reductions. Arithmetic is on pairs (two values an
+// instruction), and its roundings are written out: the same row gives the same
+// bits with and without the optional outputs, which the compiler may turn into
+// separate copies of the loop.
 #include "gdn_layernorm.cuh"
 
 namespace gdn {
@@ -33,7 +34,8 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm(const Ln
     const L at(a.width);
     const T *x = static_cast<const T *>(a.x);
     T *y = static_cast<T *>(a.y);
-    float w[NV][VE], b[NV][VE];
+    constexpr int H = VE / 2;  // pairs of a vector
+    float2 w[NV][H], b[NV][H];
     at.load_columns(w, a.weight, 1.f);
     at.load_columns(b, a.bias, 0.f);
     const float inv_width = 1.f / float(a.width);
@@ -46,24 +48,29 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm(const Ln
         for (int i = 0; i < NV; ++i) at.load(next[i], i, x + row * a.width);
     }
     for (long long base = at.base; base < a.rows; base += at.step, row += at.step) {
-        float v[NV][VE], sum = 0.f;
+        float2 v[NV][H], acc = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VE; ++j) sum += (v[i][j] = next[i].f(j));
+            for (int k = 0; k < H; ++k) acc = vec::add2(acc, v[i][k] = next[i].f2(k));
         if (row + at.step < a.rows) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) at.load(next[i], i, x + (row + at.step) * a.width);
         }
+        const float sum = vec::sum2(acc);
         const float mean = __fmul_rn(G ? vec::group_sum<G ? G : 1>(sum) : vec::block_sum(sum, red[0]), inv_width);
-        float sq = 0.f;
+        acc = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                v[i][j] -= mean;
-                if (at.has(i, j)) sq = fmaf(v[i][j], v[i][j], sq);
+            for (int k = 0; k < H; ++k) {
+                v[i][k] = vec::add2(v[i][k], vec::both(-mean));
+                float2 c = v[i][k];
+                if (!at.has(i, 2 * k)) c.x = 0.f;
+                if (!at.has(i, 2 * k + 1)) c.y = 0.f;
+                acc = vec::fma2(c, c, acc);
             }
+        const float sq = vec::sum2(acc);
         const float var = __fmul_rn(G ? vec::group_sum<G ? G : 1>(sq) : vec::block_sum(sq, red[1]), inv_width);
         const float rstd = 1.f / sqrtf(__fadd_rn(var, a.eps));
         if (row < a.rows) {
@@ -71,7 +78,8 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm(const Ln
             for (int i = 0; i < NV; ++i) {
                 Pack<T, VE> o;
 #pragma unroll
-                for (int j = 0; j < VE; ++j) o.set(j, fmaf(__fmul_rn(v[i][j], rstd), w[i][j], b[i][j]));
+                for (int k = 0; k < H; ++k)
+                    o.set2(k, vec::fma2(vec::mul2(v[i][k], vec::both(rstd)), w[i][k], b[i][k]));
                 at.store(o, i, y + row * a.width);
             }
             if (at.tid == 0) {

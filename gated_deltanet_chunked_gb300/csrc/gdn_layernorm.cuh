@@ -125,18 +125,26 @@ struct Place {
                 if (has(i, j)) p[col[i] + j] = v.e[j];
         }
     }
-    // a per-column f32 array (null: `otherwise`), zeros outside the row
-    __device__ __forceinline__ void load_columns(float (&w)[NV][VE], const float *p, float otherwise) const {
+    // pairs of a per-column f32 array (null: `otherwise`); what it gives
+    // outside the row is not used
+    __device__ __forceinline__ void load_columns(float2 (&w)[NV][VE / 2], const float *p, float otherwise) const {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (ALIGNED && p && full(i)) {
 #pragma unroll
-                for (int j = 0; j < VE; j += 4)
-                    *reinterpret_cast<float4 *>(&w[i][j]) = *reinterpret_cast<const float4 *>(p + col[i] + j);
-                continue;
+            for (int j = 0; j < VE; j += 4) {
+                if (ALIGNED) {
+                    float4 t = make_float4(otherwise, otherwise, otherwise, otherwise);
+                    if (p && full(i)) t = *reinterpret_cast<const float4 *>(p + col[i] + j);
+                    w[i][j / 2] = make_float2(t.x, t.y);
+                    w[i][j / 2 + 1] = make_float2(t.z, t.w);
+                } else {
+                    float t[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) t[m] = !has(i, j + m) ? 0.f : p ? p[col[i] + j + m] : otherwise;
+                    w[i][j / 2] = make_float2(t[0], t[1]);
+                    w[i][j / 2 + 1] = make_float2(t[2], t[3]);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < VE; ++j) w[i][j] = !has(i, j) ? 0.f : p ? p[col[i] + j] : otherwise;
         }
     }
 };

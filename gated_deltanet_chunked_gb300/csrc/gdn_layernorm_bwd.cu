@@ -29,18 +29,20 @@ struct LnBwdArgs {
 // columns at a time at a thread's own place.
 template <int NV, int VE, bool IN_SMEM>
 struct Sums {
-    float v[NV][VE];
+    float2 v[NV][VE / 2];
     __device__ __forceinline__ explicit Sums(float4 *) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VE; ++j) v[i][j] = 0.f;
+            for (int k = 0; k < VE / 2; ++k) v[i][k] = make_float2(0.f, 0.f);
     }
-    __device__ __forceinline__ void add(int i, const float (&a)[VE], const float (&b)[VE]) {
+    // each pair k of vector i becomes f(k, itself)
+    template <typename F>
+    __device__ __forceinline__ void add(int i, F f) {
 #pragma unroll
-        for (int j = 0; j < VE; ++j) v[i][j] = fmaf(a[j], b[j], v[i][j]);
+        for (int k = 0; k < VE / 2; ++k) v[i][k] = f(k, v[i][k]);
     }
-    __device__ __forceinline__ float get(int i, int j) const { return v[i][j]; }
+    __device__ __forceinline__ float get(int i, int j) const { return j & 1 ? v[i][j / 2].y : v[i][j / 2].x; }
 };
 template <int NV, int VE>
 struct Sums<NV, VE, true> {
@@ -49,14 +51,14 @@ struct Sums<NV, VE, true> {
 #pragma unroll
         for (int k = 0; k < NV * VE / 4; ++k) p[k * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    __device__ __forceinline__ void add(int i, const float (&a)[VE], const float (&b)[VE]) {
+    template <typename F>
+    __device__ __forceinline__ void add(int i, F f) {
 #pragma unroll
-        for (int q = 0; q < VE; q += 4) {
-            float4 &r = p[(i * VE + q) / 4 * blockDim.x];
-            float4 t = r;
-            t.x = fmaf(a[q], b[q], t.x), t.y = fmaf(a[q + 1], b[q + 1], t.y);
-            t.z = fmaf(a[q + 2], b[q + 2], t.z), t.w = fmaf(a[q + 3], b[q + 3], t.w);
-            r = t;
+        for (int q = 0; q < VE / 4; ++q) {
+            float4 &r = p[(i * VE / 4 + q) * blockDim.x];
+            const float4 t = r;
+            const float2 lo = f(2 * q, make_float2(t.x, t.y)), hi = f(2 * q + 1, make_float2(t.z, t.w));
+            r = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
     }
     __device__ __forceinline__ float get(int i, int j) const {
@@ -77,7 +79,8 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
     const L at(a.width);
     const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
     T *dx = static_cast<T *>(a.dx);
-    float w[NV][VE];
+    constexpr int H = VE / 2;  // pairs of a vector
+    float2 w[NV][H];
     if (!kWide) at.load_columns(w, a.weight, 1.f);
     Sums<NV, VE, kWide> dw(wide_sums), db(wide_sums + NV * VE / 4 * blockDim.x);
     const float inv_width = 1.f / float(a.width);
@@ -103,32 +106,30 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
     for (long long base = at.base; base < a.rows; base += at.step, row += at.step, turn ^= 1) {
         const bool live = row < a.rows;
         const float rstd = nrstd, mean = nmean;
-        float xhat[NV][VE], g[NV][VE], s1 = 0.f, s2 = 0.f;
+        float2 xhat[NV][H], g[NV][H], a1 = make_float2(0.f, 0.f), a2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                xhat[i][j] = __fmul_rn(nx[i].f(j) - mean, rstd);
-                g[i][j] = ny[i].f(j);
+            for (int k = 0; k < H; ++k) {
+                xhat[i][k] = vec::mul2(vec::add2(nx[i].f2(k), vec::both(-mean)), vec::both(rstd));
+                g[i][k] = ny[i].f2(k);
             }
         if (row + at.step < a.rows) fetch(row + at.step);
         if (live) {  // outside the row g is zero
             if (kWide) at.load_columns(w, a.weight, 1.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float one[VE];
+                dw.add(i, [&](int k, float2 s) { return vec::fma2(g[i][k], xhat[i][k], s); });
+                db.add(i, [&](int k, float2 s) { return vec::add2(g[i][k], s); });
 #pragma unroll
-                for (int j = 0; j < VE; ++j) one[j] = 1.f;
-                dw.add(i, g[i], xhat[i]);
-                db.add(i, g[i], one);
-#pragma unroll
-                for (int j = 0; j < VE; ++j) {
-                    g[i][j] = __fmul_rn(g[i][j], w[i][j]);
-                    s1 += g[i][j];
-                    s2 = fmaf(g[i][j], xhat[i][j], s2);
+                for (int k = 0; k < H; ++k) {
+                    g[i][k] = vec::mul2(g[i][k], w[i][k]);
+                    a1 = vec::add2(a1, g[i][k]);
+                    a2 = vec::fma2(g[i][k], xhat[i][k], a2);
                 }
             }
         }
+        float s1 = vec::sum2(a1), s2 = vec::sum2(a2);
         if (G) {
             s1 = vec::group_sum<G ? G : 1>(s1);
             s2 = vec::group_sum<G ? G : 1>(s2);
@@ -143,7 +144,9 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
             for (int i = 0; i < NV; ++i) {
                 Pack<T, VE> o;
 #pragma unroll
-                for (int j = 0; j < VE; ++j) o.set(j, rstd * fmaf(-xhat[i][j], s2, g[i][j] - s1));
+                for (int k = 0; k < H; ++k)
+                    o.set2(k, vec::mul2(vec::fma2(xhat[i][k], vec::both(-s2), vec::add2(g[i][k], vec::both(-s1))),
+                                        vec::both(rstd)));
                 at.store(o, i, dx + row * a.width);
             }
         }

@@ -72,24 +72,8 @@ struct Tile {
     static __device__ __forceinline__ int channel() { return (threadIdx.x >> 5) / kSegs * 64 + (threadIdx.x & 31) * 2; }
 };
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-
-// exp of two log-decays on the base-2 unit: with y = g log2 e rounded and r
-// what the rounding left, exp g = 2^y (1 + r ln 2), so that the only errors
-// are the unit's (2 steps) and one rounding. Below -200 (and at -inf, where r
-// would be NaN) the result is the same zero.
-__device__ __forceinline__ float2 decay2(float2 g) {
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g.x) : "f"(-200.f));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g.y) : "f"(-200.f));
-    const float2 l = make_float2(1.4426950408889634f, 1.4426950408889634f);
-    const float2 y = mul2(g, l);
-    const float2 r = mul2(fma2(g, l, make_float2(-y.x, -y.y)), make_float2(0.6931471805599453f, 0.6931471805599453f));
-    float2 e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
-    return fma2(e, r, e);
-}
+using vec::fma2;
+using vec::mul2;
 
 // (a, b) followed by (a2, b2)
 __device__ __forceinline__ void compose(float &a, float &b, float a2, float b2) {
@@ -344,7 +328,7 @@ struct HeadGates {
     __device__ __forceinline__ void store(float *to) const {
 #pragma unroll
         for (int k = 0; k < ROWS / 32; k += 2) {
-            const float2 d = decay2(make_float2(g[k], g[k + 1]));
+            const float2 d = vec::exp2_of(make_float2(g[k], g[k + 1]));
             to[k * 32 + int(threadIdx.x & 31)] = d.x;
             to[(k + 1) * 32 + int(threadIdx.x & 31)] = d.y;
         }
@@ -365,7 +349,7 @@ struct Decays<T, true> {
         for (int i = 0; i < kSeg; ++i) {
             Pack<T, 2> p;
             p.load(g_tile + i * Tile<false>::kCh);
-            d[i] = decay2(make_float2(p.f(0), p.f(1)));
+            d[i] = vec::exp2_of(make_float2(p.f(0), p.f(1)));
         }
     }
     __device__ __forceinline__ float2 fma(int i, float2 s, float2 x) const { return fma2(d[i], s, x); }

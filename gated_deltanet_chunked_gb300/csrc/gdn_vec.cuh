@@ -3,6 +3,8 @@
 // backward passes) and the recurrence's decode step.
 #pragma once
 
+#include <type_traits>
+
 #include "gdn_common.cuh"
 
 namespace gdn {
@@ -36,7 +38,55 @@ struct Pack {
     }
     __device__ __forceinline__ float f(int i) const { return to_f32<T>(e[i]); }
     __device__ __forceinline__ void set(int i, float v) { e[i] = from_f32<T>(v); }
+    // elements 2 k and 2 k + 1
+    __device__ __forceinline__ float2 f2(int k) const { return pair_f(reinterpret_cast<const Pair *>(e)[k]); }
+    __device__ __forceinline__ void set2(int k, float2 v) { reinterpret_cast<Pair *>(e)[k] = pair_t(v); }
+
+  private:
+    using Pair = typename std::conditional<sizeof(T) == 2, __nv_bfloat162, float2>::type;
+    static __device__ __forceinline__ float2 pair_f(float2 v) { return v; }
+    static __device__ __forceinline__ float2 pair_f(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+    static __device__ __forceinline__ Pair pair_t(float2 v) {
+        if constexpr (sizeof(T) == 2) return __floats2bfloat162_rn(v.x, v.y);
+        else return v;
+    }
 };
+
+// Packed f32 arithmetic, two values an instruction (each as the scalar one
+// rounds): these kernels are as much bound by instructions as by memory.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float sum2(float2 v) { return __fadd_rn(v.x, v.y); }
+
+// exp of two values on the base-2 unit: with y = v log2 e rounded and r what
+// the rounding left, exp v = 2^y (1 + r ln 2), so that the only errors are
+// the unit's (2 steps) and one rounding. v is at most 88; below -200 (and at
+// -inf, where r would be NaN) the result is the same zero.
+__device__ __forceinline__ float2 exp2_of(float2 v) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(v.x) : "f"(-200.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(v.y) : "f"(-200.f));
+    const float2 l = both(1.4426950408889634f);
+    const float2 y = mul2(v, l);
+    const float2 r = mul2(fma2(v, l, make_float2(-y.x, -y.y)), both(0.6931471805599453f));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
+    return fma2(e, r, e);
+}
+
+// 1 / (1 + exp(-z)) of two values: below -88 as at -88 (less than the
+// smallest normal number)
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+    float2 v = make_float2(-z.x, -z.y), s;
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(v.x) : "f"(88.f));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(v.y) : "f"(88.f));
+    v = add2(exp2_of(v), both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(v.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(v.y));
+    return s;
+}
 
 // sum over the G lanes (a power of two, lane-aligned) of each group of a warp
 template <int G>
