@@ -447,6 +447,7 @@ namespace {
 int check_layernorm(const gdn_problem *p) {
     if (!p || p->dv <= 0 || p->total_tokens < 0) return GDN_EINVAL;
     if (p->io_dtype != GDN_DT_F32 && p->io_dtype != GDN_DT_BF16) return GDN_EINVAL;
+    if (p->total_tokens > INT32_MAX - 65536) return GDN_EINVAL;  // rows past the end stay in int
     return p->dv > kLayerNormMaxWidth ? GDN_EUNSUPPORTED : GDN_OK;
 }
 

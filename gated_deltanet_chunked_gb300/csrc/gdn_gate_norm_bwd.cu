@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kBThreads, 3) k_gated_rmsnorm_bwd(const GateBw
         }
         if (row + step < a.rows) fetch(row + step);
         const bool live = row < a.rows;
-        const float r = 1.f / sqrtf(fmaf(vec::group_sum<G>(vec::sum2(ss)), 1.f / kHeadDim, a.eps));
+        const float r = rsqrtf(fmaf(vec::group_sum<G>(vec::sum2(ss)), 1.f / kHeadDim, a.eps));
         float2 u[H], uns = both(0.f);
 #pragma unroll
         for (int k = 0; k < H; ++k) {

@@ -30,33 +30,30 @@ template <typename T, int NV, int G, bool ALIGNED, int MT>
 __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm(const LnArgs a) {
     using L = ln::Place<T, NV, G, ALIGNED>;
     constexpr int VE = L::VE;
-    __shared__ float red[2][32];
+    __shared__ __align__(16) float red[2][32];
+    if (!G) {
+        if (threadIdx.x < 64) red[threadIdx.x / 32][threadIdx.x % 32] = 0.f;
+        __syncthreads();
+    }
     const L at(a.width);
-    const T *x = static_cast<const T *>(a.x);
+    extern __shared__ __align__(16) uint8_t smem[];
+    const T *const src[1] = {static_cast<const T *>(a.x)};
+    ln::Feed<T, 1, NV, G, ALIGNED> feed(at, src, a.rows, smem);
     T *y = static_cast<T *>(a.y);
     constexpr int H = VE / 2;  // pairs of a vector
     float2 w[NV][H], b[NV][H];
     at.load_columns(w, a.weight, 1.f);
     at.load_columns(b, a.bias, 0.f);
     const float inv_width = 1.f / float(a.width);
-    Pack<T, VE> next[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) next[i].zero();
-    long long row = at.row;
-    if (row < a.rows) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) at.load(next[i], i, x + row * a.width);
-    }
-    for (long long base = at.base; base < a.rows; base += at.step, row += at.step) {
+    int row = at.row;
+    for (int base = at.base; base < a.rows; base += at.step, row += at.step) {
+        Pack<T, VE> in[1][NV];
+        feed.get(in);
         float2 v[NV][H], acc = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int k = 0; k < H; ++k) acc = vec::add2(acc, v[i][k] = next[i].f2(k));
-        if (row + at.step < a.rows) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) at.load(next[i], i, x + (row + at.step) * a.width);
-        }
+            for (int k = 0; k < H; ++k) acc = vec::add2(acc, v[i][k] = in[0][i].f2(k));
         const float sum = vec::sum2(acc);
         const float mean = __fmul_rn(G ? vec::group_sum<G ? G : 1>(sum) : vec::block_sum(sum, red[0]), inv_width);
         acc = make_float2(0.f, 0.f);
@@ -72,7 +69,7 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm(const Ln
             }
         const float sq = vec::sum2(acc);
         const float var = __fmul_rn(G ? vec::group_sum<G ? G : 1>(sq) : vec::block_sum(sq, red[1]), inv_width);
-        const float rstd = 1.f / sqrtf(__fadd_rn(var, a.eps));
+        const float rstd = rsqrtf(__fadd_rn(var, a.eps));
         if (row < a.rows) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -80,7 +77,7 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm(const Ln
 #pragma unroll
                 for (int k = 0; k < H; ++k)
                     o.set2(k, vec::fma2(vec::mul2(v[i][k], vec::both(rstd)), w[i][k], b[i][k]));
-                at.store(o, i, y + row * a.width);
+                at.store(o, i, y + (long long)row * a.width);
             }
             if (at.tid == 0) {
                 if (a.mean) a.mean[row] = mean;
@@ -95,11 +92,15 @@ struct Run {
     template <int MT>
     static cudaError_t go(const ln::Shape &sh, const LnArgs &a, cudaStream_t s) {
         const auto fn = k_layernorm<T, NV, G, ALIGNED, MT>;
+        const void *f = reinterpret_cast<const void *>(fn);
         struct Key;
+        const size_t smem = ln::Feed<T, 1, NV, G, ALIGNED>::smem(sh.threads);
+        const cudaError_t e = ln::allow_smem(f, smem);
+        if (e != cudaSuccess) return e;
         const long long ctas = ((long long)a.rows + sh.rows_per_cta - 1) / sh.rows_per_cta;
         // all CTAs at once; a multiple of eight, which keeps a CTA's rows at one misalignment
-        const long long most = (long long)ln::kSms * ln::ctas_per_sm<Key>(reinterpret_cast<const void *>(fn), sh.threads);
-        fn<<<unsigned(ctas < most ? ctas : most), sh.threads, 0, s>>>(a);
+        const long long most = (long long)ln::kSms * ln::ctas_per_sm<Key>(f, sh.threads, smem);
+        fn<<<unsigned(ctas < most ? ctas : most), sh.threads, smem, s>>>(a);
         return cudaGetLastError();
     }
     static cudaError_t run(const ln::Shape &sh, const LnArgs &a, cudaStream_t s) {
@@ -117,8 +118,8 @@ cudaError_t launch_layernorm(const void *x, const float *weight, const float *bi
     const LnArgs a{x, weight, bias, eps, y, mean, rstd, rows, width};
     LaunchScope scope(GDN_K_LAYERNORM, s);
     if (io_dtype == GDN_DT_BF16)
-        return ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(width), a, s);
-    return ln::dispatch<float, Run>(ln::shape_of<float>(width), a, s);
+        return ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(rows, width), a, s);
+    return ln::dispatch<float, Run>(ln::shape_of<float>(rows, width), a, s);
 }
 
 }  // namespace gdn

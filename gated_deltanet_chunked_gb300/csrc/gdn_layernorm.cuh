@@ -12,7 +12,7 @@
 
 #include <atomic>
 
-#include "gdn_vec.cuh"
+#include "gdn_async.cuh"
 
 namespace gdn {
 namespace ln {
@@ -27,16 +27,19 @@ struct Shape {
     int rows_per_cta;  // rows in work at a time
 };
 
+// Long rows: 16 elements a thread, which is the least of reductions and
+// barriers for an element; but few rows (latency counts, not every SM has one)
+// over as many threads as help.
 template <typename T>
-inline Shape shape_of(int width) {
+inline Shape shape_of(int rows, int width) {
     constexpr int VE = 16 / int(sizeof(T)), kMost = 16 / VE;  // at most 16 elements a thread
     Shape s;
     s.aligned = width % VE == 0;
     const int vecs = s.aligned ? width / VE : (width + VE - 1 + VE - 1) / VE;  // for any misalignment
     s.g = vecs <= 16 ? 16 : vecs <= 32 * kMost ? 32 : 0;
-    const int lanes = s.g ? s.g : kRowThreads;
     s.nv = 1;
-    while (s.nv < kMost && vecs > lanes * s.nv) s.nv *= 2;
+    if (!s.g && rows > kSms) s.nv = kMost;
+    while (s.nv < kMost && vecs > (s.g ? s.g : kRowThreads) * s.nv) s.nv *= 2;
     if (vecs > 1024 * s.nv) s.nv *= 2;  // unaligned, and the widest by a few elements: one vector too many
     s.threads = s.g ? kRowThreads : ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
     s.rows_per_cta = s.g ? kRowThreads / s.g : 1;
@@ -64,9 +67,10 @@ inline cudaError_t dispatch(const Shape &s, A &...a) {
 }
 
 // CTAs of kernel `fn` that an SM holds at `threads` each, asked once a kernel
-// (K: a type of its own), thread count and device.
+// (K: a type of its own, whose shared memory is a function of the threads),
+// thread count and device.
 template <typename K>
-inline int ctas_per_sm(const void *fn, int threads, size_t smem = 0) {
+inline int ctas_per_sm(const void *fn, int threads, size_t smem) {
     constexpr int kDevices = 64;
     static std::atomic<int> known[kDevices][33];
     int dev = 0;
@@ -78,13 +82,20 @@ inline int ctas_per_sm(const void *fn, int threads, size_t smem = 0) {
     return n;
 }
 
+// Lets `fn` have so much dynamic shared memory; a kernel's static variables (up
+// to 16 KB here) count against the 48 KB that need no leave.
+inline cudaError_t allow_smem(const void *fn, size_t bytes) {
+    return bytes <= 24 << 10 ? cudaSuccess
+                             : cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+}
+
 // A thread's place: its row group, and its vectors' columns.
 template <typename T, int NV, int G, bool ALIGNED>
 struct Place {
     static constexpr int VE = 16 / int(sizeof(T));
     using P = vec::Pack<T, VE>;
     int tid;
-    long long row, base, step;  // first row; first row of the warp (CTA), which decides when it ends; rows apart
+    int row, base, step;  // first row; first row of the warp (CTA), which decides when it ends; rows apart
     int col[NV];
     int width;
 
@@ -92,10 +103,10 @@ struct Place {
         constexpr int g = G ? G : 1;
         const int groups = G ? int(blockDim.x) / g : 1, group = G ? int(threadIdx.x) / g : 0;
         tid = G ? int(threadIdx.x) % g : int(threadIdx.x);
-        row = (long long)blockIdx.x * groups + group;
+        row = int(blockIdx.x) * groups + group;
         base = G ? row - (threadIdx.x & 31) / g : row;
-        step = (long long)gridDim.x * groups;
-        const int off = ALIGNED ? 0 : int(row * width % VE);
+        step = int(gridDim.x) * groups;
+        const int off = ALIGNED ? 0 : int((long long)row * width % VE);
 #pragma unroll
         for (int i = 0; i < NV; ++i) col[i] = (tid + i * (G ? G : int(blockDim.x))) * VE - off;
     }
@@ -146,6 +157,78 @@ struct Place {
                 }
             }
         }
+    }
+};
+
+// The thread's vectors of its rows of NT tensors in turn, read ahead: through
+// its own place in shared memory, or one row ahead in registers: where vectors
+// at a row's ends go element by element (shorter than what cp.async copies),
+// and where shared memory is wanted for something else (IN_SMEM false).
+template <typename T, int NT, int NV, int G, bool ALIGNED, bool IN_SMEM = ALIGNED>
+struct Feed {
+    using L = Place<T, NV, G, ALIGNED>;
+    using A = vec::RowsAhead<NT, NV>;
+    using P = typename L::P;
+    static __host__ __device__ size_t smem(int threads) { return IN_SMEM ? A::smem(threads) : 0; }
+
+    const L &at;
+    const T *src[NT];  // of the next row to ask for, at the thread's first vector
+    long long pitch;   // elements between this thread's rows
+    int left;          // rows still to ask for
+    bool full[NV];
+    A a;
+    P next[IN_SMEM ? 1 : NT][IN_SMEM ? 1 : NV];
+
+    __device__ __forceinline__ Feed(const L &place, const T *const (&from)[NT], int rows, void *smem)
+        : at(place), pitch((long long)place.step * place.width), a(smem) {
+        left = at.row < rows ? (rows - 1 - at.row) / at.step + 1 : 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) full[i] = at.full(i);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) src[t] = from[t] + (long long)at.row * at.width + at.col[0];
+        if (IN_SMEM) {
+#pragma unroll
+            for (int s = 0; s < A::kAhead; ++s) ask();
+        } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) next[IN_SMEM ? 0 : t][IN_SMEM ? 0 : i].zero();
+            ask();
+        }
+    }
+    __device__ __forceinline__ void ask() {
+        if (left > 0) {
+            constexpr int VE = L::VE;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (!IN_SMEM) at.load(next[IN_SMEM ? 0 : t][IN_SMEM ? 0 : i], i, src[t] - at.col[0]);
+                    else if (full[i]) a.copy(t * NV + i, src[t] + (G ? G * VE : int(blockDim.x) * VE) * i);
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) src[t] += pitch;
+        --left;
+        if (IN_SMEM) a.commit();
+    }
+    // the next row's vectors: zeros outside the row, anything where there is no row
+    __device__ __forceinline__ void get(P (&v)[NT][NV]) {
+        if (IN_SMEM) {
+            ask();
+            a.wait();
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!IN_SMEM) v[t][i] = next[IN_SMEM ? 0 : t][IN_SMEM ? 0 : i];
+                else if (full[i]) v[t][i].r = a.take(t * NV + i);
+                else v[t][i].zero();
+            }
+        if (IN_SMEM) a.taken();
+        else ask();
     }
 };
 

@@ -74,47 +74,40 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
     using L = ln::Place<T, NV, G, ALIGNED>;
     constexpr int VE = L::VE;
     constexpr bool kWide = MT == 1024;
-    extern __shared__ float4 wide_sums[];  // kWide: two sums for every column of a thread
-    __shared__ float2 red[2][32];
+    extern __shared__ __align__(16) uint8_t smem[];  // rows ahead; then, kWide: two sums for every column of a thread
+    __shared__ __align__(16) float2 red[2][32];
+    if (!G) {
+        if (threadIdx.x < 64) red[threadIdx.x / 32][threadIdx.x % 32] = make_float2(0.f, 0.f);
+        __syncthreads();
+    }
     const L at(a.width);
-    const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
+    using F = ln::Feed<T, 2, NV, G, ALIGNED, ALIGNED && !kWide>;
+    const T *const src[2] = {static_cast<const T *>(a.x), static_cast<const T *>(a.dy)};
+    F feed(at, src, a.rows, smem);
+    float4 *wide_sums = reinterpret_cast<float4 *>(smem + F::smem(int(blockDim.x)));
     T *dx = static_cast<T *>(a.dx);
     constexpr int H = VE / 2;  // pairs of a vector
     float2 w[NV][H];
     if (!kWide) at.load_columns(w, a.weight, 1.f);
     Sums<NV, VE, kWide> dw(wide_sums), db(wide_sums + NV * VE / 4 * blockDim.x);
     const float inv_width = 1.f / float(a.width);
-    Pack<T, VE> nx[NV], ny[NV];
-    float nmean = 0.f, nrstd = 0.f;
-    auto fetch = [&](long long r) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            at.load(nx[i], i, x + r * a.width);
-            at.load(ny[i], i, dy + r * a.width);
-        }
-        nmean = a.mean[r];
-        nrstd = a.rstd[r];
-    };
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        nx[i].zero();
-        ny[i].zero();
-    }
-    long long row = at.row;
-    if (row < a.rows) fetch(row);
-    int turn = 0;
-    for (long long base = at.base; base < a.rows; base += at.step, row += at.step, turn ^= 1) {
+    int row = at.row;
+    // one row; its statistics are given, and those of the row after the next
+    // take their place (two rows ahead, without a move that would wait for them)
+    auto one_row = [&](float2 &stats, float2 *buf) {
         const bool live = row < a.rows;
-        const float rstd = nrstd, mean = nmean;
+        const float mean = stats.x, rstd = stats.y;
+        if (row + 2 * at.step < a.rows) stats = make_float2(a.mean[row + 2 * at.step], a.rstd[row + 2 * at.step]);
+        Pack<T, VE> in[2][NV];
+        feed.get(in);
         float2 xhat[NV][H], g[NV][H], a1 = make_float2(0.f, 0.f), a2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int k = 0; k < H; ++k) {
-                xhat[i][k] = vec::mul2(vec::add2(nx[i].f2(k), vec::both(-mean)), vec::both(rstd));
-                g[i][k] = ny[i].f2(k);
+                xhat[i][k] = vec::mul2(vec::add2(in[0][i].f2(k), vec::both(-mean)), vec::both(rstd));
+                g[i][k] = in[1][i].f2(k);
             }
-        if (row + at.step < a.rows) fetch(row + at.step);
         if (live) {  // outside the row g is zero
             if (kWide) at.load_columns(w, a.weight, 1.f);
 #pragma unroll
@@ -131,10 +124,10 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
         }
         float s1 = vec::sum2(a1), s2 = vec::sum2(a2);
         if (G) {
-            s1 = vec::group_sum<G ? G : 1>(s1);
-            s2 = vec::group_sum<G ? G : 1>(s2);
+            const float2 t = vec::group_sum2<G ? G : 2>(s1, s2);
+            s1 = t.x, s2 = t.y;
         } else {
-            const float2 t = vec::block_sum2(s1, s2, red[turn]);
+            const float2 t = vec::block_sum2(s1, s2, buf);
             s1 = t.x, s2 = t.y;
         }
         s1 = __fmul_rn(s1, inv_width);
@@ -147,21 +140,54 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
                 for (int k = 0; k < H; ++k)
                     o.set2(k, vec::mul2(vec::fma2(xhat[i][k], vec::both(-s2), vec::add2(g[i][k], vec::both(-s1))),
                                         vec::both(rstd)));
-                at.store(o, i, dx + row * a.width);
+                at.store(o, i, dx + (long long)row * a.width);
             }
         }
+        row += at.step;
+    };
+    float2 even = make_float2(0.f, 0.f), odd = even;
+    if (row < a.rows) even = make_float2(a.mean[row], a.rstd[row]);
+    if (row + at.step < a.rows) odd = make_float2(a.mean[row + at.step], a.rstd[row + at.step]);
+    for (int base = at.base; base < a.rows; base += 2 * at.step) {
+        one_row(even, red[0]);
+        if (base + at.step < a.rows) one_row(odd, red[1]);
     }
     if (!a.dw_part) return;
     float *dwp = a.dw_part + (long long)blockIdx.x * a.width, *dbp = a.db_part + (long long)blockIdx.x * a.width;
-    if (!G) {
+    if (!G && ALIGNED) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            if (!at.full(i)) continue;
 #pragma unroll
-            for (int j = 0; j < VE; ++j)
-                if (at.has(i, j)) {
-                    dwp[at.col[i] + j] = dw.get(i, j);
-                    dbp[at.col[i] + j] = db.get(i, j);
-                }
+            for (int j = 0; j < VE; j += 4) {
+                *reinterpret_cast<float4 *>(dwp + at.col[i] + j) =
+                    make_float4(dw.get(i, j), dw.get(i, j + 1), dw.get(i, j + 2), dw.get(i, j + 3));
+                *reinterpret_cast<float4 *>(dbp + at.col[i] + j) =
+                    make_float4(db.get(i, j), db.get(i, j + 1), db.get(i, j + 2), db.get(i, j + 3));
+            }
+        }
+    } else if (!G) {
+        // columns that no thread has 16 bytes of: through shared memory, so that the stores are whole lines
+        float *line = reinterpret_cast<float *>(smem);
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+            if (kWide) {  // which holds the sums: no room for a line
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < VE; ++j)
+                        if (at.has(i, j)) (pass ? dbp : dwp)[at.col[i] + j] = pass ? db.get(i, j) : dw.get(i, j);
+                continue;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+                    if (at.has(i, j)) line[at.col[i] + j] = pass ? db.get(i, j) : dw.get(i, j);
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.width; c += blockDim.x) (pass ? dbp : dwp)[c] = line[c];
+        }
     } else {
         // the CTA's row groups, added in order; one of the two sums at a time
         constexpr int kCols = (G ? G : 1) * VE * NV;
@@ -195,7 +221,7 @@ int max_parts(int threads) { return ln::kSms * (threads <= 128 ? 8 : threads <= 
 
 template <typename T>
 size_t workspace_of(int rows, int width) {
-    const int most = max_parts(ln::shape_of<T>(width).threads);
+    const int most = max_parts(ln::shape_of<T>(rows, width).threads);
     return (2 * size_t(rows < most ? rows : most) * size_t(width) * sizeof(float) + 255) & ~size_t(255);
 }
 
@@ -205,12 +231,12 @@ struct Run {
     static cudaError_t go(const ln::Shape &sh, LnBwdArgs &a, bool sums, int &parts, cudaStream_t s) {
         const auto fn = k_layernorm_bwd<T, NV, G, ALIGNED, MT>;
         struct Key;
-        const size_t smem = MT == 1024 ? size_t(sh.threads) * NV * 16 / sizeof(T) * 2 * sizeof(float) : 0;
-        if (smem) {
-            const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-            if (e != cudaSuccess) return e;
-        }
+        const size_t smem = ln::Feed<T, 2, NV, G, ALIGNED, ALIGNED && MT != 1024>::smem(sh.threads) +
+                            (MT == 1024     ? size_t(sh.threads) * NV * 16 / sizeof(T) * 2 * sizeof(float)
+                             : !ALIGNED && !G ? size_t(a.width) * sizeof(float)
+                                              : 0);
+        const cudaError_t e = ln::allow_smem(reinterpret_cast<const void *>(fn), smem);
+        if (e != cudaSuccess) return e;
         const long long ctas = ((long long)a.rows + sh.rows_per_cta - 1) / sh.rows_per_cta;
         long long most = (long long)ln::kSms * ln::ctas_per_sm<Key>(reinterpret_cast<const void *>(fn), sh.threads, smem);
         if (most > max_parts(sh.threads)) most = max_parts(sh.threads);
@@ -228,26 +254,28 @@ struct Run {
     }
 };
 
-constexpr int kSumLanes = 32;  // rows of partial sums in work at a time
+constexpr int kSumWarps = 16;
 
-// grid (ceil(width / 32), 2): 32 columns of one of the two arrays a CTA
-__global__ void __launch_bounds__(32 * kSumLanes) k_row_sums(const float *a, const float *b, int parts, int width,
+// grid (ceil(width / 32), 2): 32 columns of one of the two arrays a CTA, each
+// warp every kSumWarps-th row.
+__global__ void __launch_bounds__(32 * kSumWarps) k_row_sums(const float *a, const float *b, int parts, int width,
                                                              float *out_a, float *out_b) {
     const float *in = blockIdx.y ? b : a;
     float *out = blockIdx.y ? out_b : out_a;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    __shared__ float t[kSumWarps][32];
     if (!out) return;
-    __shared__ float t[kSumLanes][33];
-    const int c = blockIdx.x * 32 + threadIdx.x;
     float sum = 0.f;
     if (c < width)
-#pragma unroll 8
-        for (int r = threadIdx.y; r < parts; r += kSumLanes) sum += in[(long long)r * width + c];
-    t[threadIdx.y][threadIdx.x] = sum;
+#pragma unroll 10
+        for (int r = w; r < parts; r += kSumWarps) sum += in[(long long)r * width + c];
+    t[w][lane] = sum;
     __syncthreads();
-    // warp y adds the kSumLanes partial sums of column y
-    const float v = vec::group_sum<32>(t[threadIdx.x][threadIdx.y]);
-    const int co = blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && co < width) out[co] = v;
+    if (w == 0 && c < width) {
+#pragma unroll
+        for (int k = 1; k < kSumWarps; ++k) sum += t[k][lane];
+        out[c] = sum;
+    }
 }
 
 }  // namespace
@@ -256,7 +284,8 @@ cudaError_t launch_row_sums(const float *a, const float *b, int parts, int width
                             cudaStream_t s) {
     if (!out_a && !out_b) return cudaSuccess;
     LaunchScope scope(GDN_K_ROW_SUMS, s);
-    k_row_sums<<<dim3(unsigned((width + 31) / 32), 2), dim3(32, kSumLanes), 0, s>>>(a, b, parts, width, out_a, out_b);
+    k_row_sums<<<dim3(unsigned((width + 31) / 32), out_b ? 2 : 1), 32 * kSumWarps, 0, s>>>(a, b, parts, width, out_a,
+                                                                                           out_b);
     return cudaGetLastError();
 }
 
@@ -274,8 +303,8 @@ cudaError_t launch_layernorm_bwd(const void *dy, const void *x, const float *mea
         LaunchScope scope(GDN_K_LAYERNORM_BWD, s);
         const cudaError_t e =
             io_dtype == GDN_DT_BF16
-                ? ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(width), a, sums, parts, s)
-                : ln::dispatch<float, Run>(ln::shape_of<float>(width), a, sums, parts, s);
+                ? ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(rows, width), a, sums, parts, s)
+                : ln::dispatch<float, Run>(ln::shape_of<float>(rows, width), a, sums, parts, s);
         if (e != cudaSuccess) return e;
     }
     return launch_row_sums(a.dw_part, a.db_part, parts, width, dweight, dbias, s);

@@ -96,25 +96,46 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
+// two such sums: after the first step half of the lanes go on with either
+template <int G>
+__device__ __forceinline__ float2 group_sum2(float a, float b) {
+    const bool up = threadIdx.x & (G / 2);
+    const float send = up ? a : b;
+    float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, send, G / 2);
+#pragma unroll
+    for (int m = G / 4; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    const float o = __shfl_xor_sync(0xffffffffu, v, G / 2);
+    return up ? make_float2(o, v) : make_float2(v, o);
+}
+
 // sum over the CTA (blockDim.x a multiple of 32); every thread gets it. `buf`
-// holds 32 floats; calls in turn use two buffers alternately, so that one
-// barrier a call is enough.
+// holds 32 floats (pairs), 16-byte aligned and zero where no warp writes; calls
+// in turn use two buffers alternately, so that one barrier a call is enough. The warps' sums are read by every
+// thread, four at a time: fewer instructions than a second round of shuffles.
 __device__ __forceinline__ float block_sum(float v, float *buf) {
     v = group_sum<32>(v);
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     if (lane == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    return group_sum<32>(lane < warps ? buf[lane] : 0.f);
+    float4 s = *reinterpret_cast<const float4 *>(buf);
+    for (int w = 4; w < warps; w += 4) {
+        const float4 t = *reinterpret_cast<const float4 *>(buf + w);
+        s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
+    }
+    return (s.x + s.y) + (s.z + s.w);
 }
 
 __device__ __forceinline__ float2 block_sum2(float a, float b, float2 *buf) {
-    a = group_sum<32>(a);
-    b = group_sum<32>(b);
+    const float2 v = group_sum2<32>(a, b);
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+    if (lane == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    const float2 t = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
-    return make_float2(group_sum<32>(t.x), group_sum<32>(t.y));
+    float4 s = *reinterpret_cast<const float4 *>(buf);
+    for (int w = 2; w < warps; w += 2) {
+        const float4 t = *reinterpret_cast<const float4 *>(buf + w);
+        s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
+    }
+    return make_float2(s.x + s.z, s.y + s.w);
 }
 
 }  // namespace vec
