@@ -25,6 +25,11 @@ struct RowsAhead {
     __device__ __forceinline__ void copy(int v, const void *from) const {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(put + v * pitch), "l"(from) : "memory");
     }
+    // only the first `bytes` (1 to 16), zeros after them
+    __device__ __forceinline__ void copy_part(int v, const void *from, int bytes) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(put + v * pitch), "l"(from), "r"(bytes)
+                     : "memory");
+    }
     __device__ __forceinline__ void advance(uint32_t &at) const {
         at += NT * NV * pitch;
         if (at == base + kStages * NT * NV * pitch) at = base;

@@ -26,8 +26,10 @@ struct LnArgs {
     int rows, width;
 };
 
-template <typename T, int NV, int G, bool ALIGNED, int MT>
-__global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm(const LnArgs a) {
+constexpr int kMaxThreads = 576;  // 544 for the widest rows
+
+template <typename T, int NV, int G, bool ALIGNED>
+__global__ void __launch_bounds__(G ? ln::kRowThreads : kMaxThreads) k_layernorm(const LnArgs a) {
     using L = ln::Place<T, NV, G, ALIGNED>;
     constexpr int VE = L::VE;
     __shared__ __align__(16) float red[2][32];
@@ -38,12 +40,16 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm(const Ln
     const L at(a.width);
     extern __shared__ __align__(16) uint8_t smem[];
     const T *const src[1] = {static_cast<const T *>(a.x)};
-    ln::Feed<T, 1, NV, G, ALIGNED> feed(at, src, a.rows, smem);
+    ln::Feed<T, 1, NV, G, ALIGNED, true> feed(at, src, a.rows, smem);
     T *y = static_cast<T *>(a.y);
     constexpr int H = VE / 2;  // pairs of a vector
+    // 32 elements a thread leave no registers for weight and bias: read for every row
+    constexpr bool kReread = NV * VE > 16;
     float2 w[NV][H], b[NV][H];
-    at.load_columns(w, a.weight, 1.f);
-    at.load_columns(b, a.bias, 0.f);
+    if (!kReread) {
+        at.load_columns(w, a.weight, 1.f);
+        at.load_columns(b, a.bias, 0.f);
+    }
     const float inv_width = 1.f / float(a.width);
     int row = at.row;
     for (int base = at.base; base < a.rows; base += at.step, row += at.step) {
@@ -58,21 +64,29 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm(const Ln
         const float mean = __fmul_rn(G ? vec::group_sum<G ? G : 1>(sum) : vec::block_sum(sum, red[0]), inv_width);
         acc = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
 #pragma unroll
-            for (int k = 0; k < H; ++k) {
-                v[i][k] = vec::add2(v[i][k], vec::both(-mean));
-                float2 c = v[i][k];
-                if (!at.has(i, 2 * k)) c.x = 0.f;
-                if (!at.has(i, 2 * k + 1)) c.y = 0.f;
-                acc = vec::fma2(c, c, acc);
+            for (int k = 0; k < H; ++k) v[i][k] = vec::add2(v[i][k], vec::both(-mean));
+            if (!at.full(i)) {  // outside the row: not in the squares
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    if (!at.has(i, 2 * k)) v[i][k].x = 0.f;
+                    if (!at.has(i, 2 * k + 1)) v[i][k].y = 0.f;
+                }
             }
+#pragma unroll
+            for (int k = 0; k < H; ++k) acc = vec::fma2(v[i][k], v[i][k], acc);
+        }
         const float sq = vec::sum2(acc);
         const float var = __fmul_rn(G ? vec::group_sum<G ? G : 1>(sq) : vec::block_sum(sq, red[1]), inv_width);
         const float rstd = rsqrtf(__fadd_rn(var, a.eps));
         if (row < a.rows) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
+                if (kReread) {
+                    at.load_column(w[i], i, a.weight, 1.f);
+                    at.load_column(b[i], i, a.bias, 0.f);
+                }
                 Pack<T, VE> o;
 #pragma unroll
                 for (int k = 0; k < H; ++k)
@@ -89,12 +103,11 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm(const Ln
 
 template <typename T, int NV, int G, bool ALIGNED>
 struct Run {
-    template <int MT>
-    static cudaError_t go(const ln::Shape &sh, const LnArgs &a, cudaStream_t s) {
-        const auto fn = k_layernorm<T, NV, G, ALIGNED, MT>;
+    static cudaError_t run(const ln::Shape &sh, const LnArgs &a, cudaStream_t s) {
+        const auto fn = k_layernorm<T, NV, G, ALIGNED>;
         const void *f = reinterpret_cast<const void *>(fn);
         struct Key;
-        const size_t smem = ln::Feed<T, 1, NV, G, ALIGNED>::smem(sh.threads);
+        const size_t smem = ln::Feed<T, 1, NV, G, ALIGNED, true>::smem(sh.threads);
         const cudaError_t e = ln::allow_smem(f, smem);
         if (e != cudaSuccess) return e;
         const long long ctas = ((long long)a.rows + sh.rows_per_cta - 1) / sh.rows_per_cta;
@@ -102,11 +115,6 @@ struct Run {
         const long long most = (long long)ln::kSms * ln::ctas_per_sm<Key>(f, sh.threads, smem);
         fn<<<unsigned(ctas < most ? ctas : most), sh.threads, smem, s>>>(a);
         return cudaGetLastError();
-    }
-    static cudaError_t run(const ln::Shape &sh, const LnArgs &a, cudaStream_t s) {
-        // more than 512 threads only with the most elements a thread
-        constexpr int kMost = !G && NV * 16 / int(sizeof(T)) >= 16 ? 1024 : 512;
-        return sh.threads <= 512 ? go<512>(sh, a, s) : go<kMost>(sh, a, s);
     }
 };
 
@@ -118,8 +126,8 @@ cudaError_t launch_layernorm(const void *x, const float *weight, const float *bi
     const LnArgs a{x, weight, bias, eps, y, mean, rstd, rows, width};
     LaunchScope scope(GDN_K_LAYERNORM, s);
     if (io_dtype == GDN_DT_BF16)
-        return ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(rows, width), a, s);
-    return ln::dispatch<float, Run>(ln::shape_of<float>(rows, width), a, s);
+        return ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(rows, width, 32), a, s);
+    return ln::dispatch<float, Run>(ln::shape_of<float>(rows, width, 32), a, s);
 }
 
 }  // namespace gdn

@@ -3,9 +3,11 @@
 // A row is held in registers, so that it is read once; every load is 16 bytes,
 // VE elements, NV of them a thread. Rows whose width is no multiple of VE do
 // not start on 16 bytes: such a row's vectors begin up to VE - 1 elements
-// before it, at the last aligned address, and its first and last vector go
-// element by element. A CTA's rows are a multiple of eight apart, so all rows
-// of a thread have the same misalignment and it owns the same columns of all.
+// before it, at the last aligned address; of its first and last vector the
+// elements outside the row are read with the others (not past the tensor's
+// end), replaced by zeros and not written. A CTA's rows are a multiple of eight
+// apart, so all rows of a thread have the same misalignment and it owns the
+// same columns of all.
 // G lanes of a warp share a row where it is short, so that no lane is without
 // elements; longer rows take a whole CTA (G = 0).
 #pragma once
@@ -28,19 +30,22 @@ struct Shape {
 };
 
 // Long rows: 16 elements a thread, which is the least of reductions and
-// barriers for an element; but few rows (latency counts, not every SM has one)
-// over as many threads as help.
+// barriers for an element; few rows (latency counts) over as many threads as
+// help. Where that takes more than 512 threads, `most` = 32 elements a thread
+// keep two CTAs on an SM, whose reductions overlap (3000 x 16384 bf16 forward:
+// 56 us with 1024 threads, 51 with 512).
 template <typename T>
-inline Shape shape_of(int rows, int width) {
+inline Shape shape_of(int rows, int width, int most = 16) {
     constexpr int VE = 16 / int(sizeof(T)), kMost = 16 / VE;  // at most 16 elements a thread
     Shape s;
     s.aligned = width % VE == 0;
     const int vecs = s.aligned ? width / VE : (width + VE - 1 + VE - 1) / VE;  // for any misalignment
     s.g = vecs <= 16 ? 16 : vecs <= 32 * kMost ? 32 : 0;
     s.nv = 1;
-    if (!s.g && rows > kSms) s.nv = kMost;
+    if (!s.g && rows > 16 * kSms) s.nv = kMost;
     while (s.nv < kMost && vecs > (s.g ? s.g : kRowThreads) * s.nv) s.nv *= 2;
-    if (vecs > 1024 * s.nv) s.nv *= 2;  // unaligned, and the widest by a few elements: one vector too many
+    // (also the widest unaligned rows, by a few elements one vector too many for 1024 threads)
+    if (!s.g && vecs > (most > 16 ? 512 : 1024) * s.nv) s.nv *= 2;
     s.threads = s.g ? kRowThreads : ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
     s.rows_per_cta = s.g ? kRowThreads / s.g : 1;
     return s;
@@ -58,8 +63,8 @@ inline cudaError_t dispatch_nv(const Shape &s, A &...a) {
     }
     if (s.nv == 1) return F<T, 1, 0, ALIGNED>::run(s, a...);
     if (s.nv == 2) return F<T, 2, 0, ALIGNED>::run(s, a...);
-    if (ALIGNED || s.nv == kMost) return F<T, kMost, 0, ALIGNED>::run(s, a...);
-    return F<T, ALIGNED ? kMost : 2 * kMost, 0, ALIGNED>::run(s, a...);
+    if (s.nv == kMost) return F<T, kMost, 0, ALIGNED>::run(s, a...);
+    return F<T, 2 * kMost, 0, ALIGNED>::run(s, a...);
 }
 template <typename T, template <typename, int, int, bool> class F, typename... A>
 inline cudaError_t dispatch(const Shape &s, A &...a) {
@@ -138,33 +143,33 @@ struct Place {
     }
     // pairs of a per-column f32 array (null: `otherwise`); what it gives
     // outside the row is not used
-    __device__ __forceinline__ void load_columns(float2 (&w)[NV][VE / 2], const float *p, float otherwise) const {
+    __device__ __forceinline__ void load_column(float2 (&w)[VE / 2], int i, const float *p, float otherwise) const {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
+        for (int j = 0; j < VE; j += 4) {
+            if (ALIGNED) {
+                float4 t = make_float4(otherwise, otherwise, otherwise, otherwise);
+                if (p && full(i)) t = *reinterpret_cast<const float4 *>(p + col[i] + j);
+                w[j / 2] = make_float2(t.x, t.y);
+                w[j / 2 + 1] = make_float2(t.z, t.w);
+            } else {
+                float t[4];
 #pragma unroll
-            for (int j = 0; j < VE; j += 4) {
-                if (ALIGNED) {
-                    float4 t = make_float4(otherwise, otherwise, otherwise, otherwise);
-                    if (p && full(i)) t = *reinterpret_cast<const float4 *>(p + col[i] + j);
-                    w[i][j / 2] = make_float2(t.x, t.y);
-                    w[i][j / 2 + 1] = make_float2(t.z, t.w);
-                } else {
-                    float t[4];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) t[m] = !has(i, j + m) ? 0.f : p ? p[col[i] + j + m] : otherwise;
-                    w[i][j / 2] = make_float2(t[0], t[1]);
-                    w[i][j / 2 + 1] = make_float2(t[2], t[3]);
-                }
+                for (int m = 0; m < 4; ++m) t[m] = !has(i, j + m) ? 0.f : p ? p[col[i] + j + m] : otherwise;
+                w[j / 2] = make_float2(t[0], t[1]);
+                w[j / 2 + 1] = make_float2(t[2], t[3]);
             }
         }
+    }
+    __device__ __forceinline__ void load_columns(float2 (&w)[NV][VE / 2], const float *p, float otherwise) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) load_column(w[i], i, p, otherwise);
     }
 };
 
 // The thread's vectors of its rows of NT tensors in turn, read ahead: through
-// its own place in shared memory, or one row ahead in registers: where vectors
-// at a row's ends go element by element (shorter than what cp.async copies),
-// and where shared memory is wanted for something else (IN_SMEM false).
-template <typename T, int NT, int NV, int G, bool ALIGNED, bool IN_SMEM = ALIGNED>
+// its own place in shared memory, or (IN_SMEM false: a CTA of 1024 threads)
+// one row ahead in registers.
+template <typename T, int NT, int NV, int G, bool ALIGNED, bool IN_SMEM>
 struct Feed {
     using L = Place<T, NV, G, ALIGNED>;
     using A = vec::RowsAhead<NT, NV>;
@@ -174,16 +179,18 @@ struct Feed {
     const L &at;
     const T *src[NT];  // of the next row to ask for, at the thread's first vector
     long long pitch;   // elements between this thread's rows
+    long long rest;    // elements from src to the tensor's end (unaligned rows)
     int left;          // rows still to ask for
-    bool full[NV];
+    bool any[NV];      // whether the vector has elements of the row
     A a;
     P next[IN_SMEM ? 1 : NT][IN_SMEM ? 1 : NV];
 
     __device__ __forceinline__ Feed(const L &place, const T *const (&from)[NT], int rows, void *smem)
         : at(place), pitch((long long)place.step * place.width), a(smem) {
         left = at.row < rows ? (rows - 1 - at.row) / at.step + 1 : 0;
+        rest = (long long)(rows - at.row) * at.width - at.col[0];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) full[i] = at.full(i);
+        for (int i = 0; i < NV; ++i) any[i] = at.col[i] < at.width;
 #pragma unroll
         for (int t = 0; t < NT; ++t) src[t] = from[t] + (long long)at.row * at.width + at.col[0];
         if (IN_SMEM) {
@@ -204,10 +211,16 @@ struct Feed {
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    if (!IN_SMEM) at.load(next[IN_SMEM ? 0 : t][IN_SMEM ? 0 : i], i, src[t] - at.col[0]);
-                    else if (full[i]) a.copy(t * NV + i, src[t] + (G ? G * VE : int(blockDim.x) * VE) * i);
+                    const int off = (G ? G * VE : int(blockDim.x) * VE) * i;
+                    if (!IN_SMEM) {
+                        at.load(next[IN_SMEM ? 0 : t][IN_SMEM ? 0 : i], i, src[t] - at.col[0]);
+                    } else if (any[i]) {
+                        if (ALIGNED || rest - off >= VE) a.copy(t * NV + i, src[t] + off);
+                        else a.copy_part(t * NV + i, src[t] + off, int(rest - off) * int(sizeof(T)));
+                    }
                 }
         }
+        if (!ALIGNED) rest -= pitch;
 #pragma unroll
         for (int t = 0; t < NT; ++t) src[t] += pitch;
         --left;
@@ -224,8 +237,13 @@ struct Feed {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (!IN_SMEM) v[t][i] = next[IN_SMEM ? 0 : t][IN_SMEM ? 0 : i];
-                else if (full[i]) v[t][i].r = a.take(t * NV + i);
+                else if (any[i]) v[t][i].r = a.take(t * NV + i);
                 else v[t][i].zero();
+                if (IN_SMEM && !ALIGNED && any[i] && !at.full(i)) {
+#pragma unroll
+                    for (int j = 0; j < L::VE; ++j)
+                        if (!at.has(i, j)) v[t][i].set(j, 0.f);
+                }
             }
         if (IN_SMEM) a.taken();
         else ask();

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
         __syncthreads();
     }
     const L at(a.width);
-    using F = ln::Feed<T, 2, NV, G, ALIGNED, ALIGNED && !kWide>;
+    using F = ln::Feed<T, 2, NV, G, ALIGNED, !kWide>;
     const T *const src[2] = {static_cast<const T *>(a.x), static_cast<const T *>(a.dy)};
     F feed(at, src, a.rows, smem);
     float4 *wide_sums = reinterpret_cast<float4 *>(smem + F::smem(int(blockDim.x)));
@@ -93,11 +93,13 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
     const float inv_width = 1.f / float(a.width);
     int row = at.row;
     // one row; its statistics are given, and those of the row after the next
-    // take their place (two rows ahead, without a move that would wait for them)
+    // take their place (two rows ahead, without a move that would wait for
+    // them; kWide, short of registers: of the next row)
+    const int ahead = (kWide ? 1 : 2) * at.step;
     auto one_row = [&](float2 &stats, float2 *buf) {
         const bool live = row < a.rows;
         const float mean = stats.x, rstd = stats.y;
-        if (row + 2 * at.step < a.rows) stats = make_float2(a.mean[row + 2 * at.step], a.rstd[row + 2 * at.step]);
+        if (row + ahead < a.rows) stats = make_float2(a.mean[row + ahead], a.rstd[row + ahead]);
         Pack<T, VE> in[2][NV];
         feed.get(in);
         float2 xhat[NV][H], g[NV][H], a1 = make_float2(0.f, 0.f), a2 = make_float2(0.f, 0.f);
@@ -147,10 +149,11 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
     };
     float2 even = make_float2(0.f, 0.f), odd = even;
     if (row < a.rows) even = make_float2(a.mean[row], a.rstd[row]);
-    if (row + at.step < a.rows) odd = make_float2(a.mean[row + at.step], a.rstd[row + at.step]);
-    for (int base = at.base; base < a.rows; base += 2 * at.step) {
-        one_row(even, red[0]);
-        if (base + at.step < a.rows) one_row(odd, red[1]);
+    if (!kWide && row + at.step < a.rows) odd = make_float2(a.mean[row + at.step], a.rstd[row + at.step]);
+    int turn = 0;
+    for (int base = at.base; base < a.rows; base += ahead, turn ^= 1) {
+        one_row(even, red[kWide ? turn : 0]);
+        if (!kWide && base + at.step < a.rows) one_row(odd, red[1]);
     }
     if (!a.dw_part) return;
     float *dwp = a.dw_part + (long long)blockIdx.x * a.width, *dbp = a.db_part + (long long)blockIdx.x * a.width;
@@ -231,7 +234,7 @@ struct Run {
     static cudaError_t go(const ln::Shape &sh, LnBwdArgs &a, bool sums, int &parts, cudaStream_t s) {
         const auto fn = k_layernorm_bwd<T, NV, G, ALIGNED, MT>;
         struct Key;
-        const size_t smem = ln::Feed<T, 2, NV, G, ALIGNED, ALIGNED && MT != 1024>::smem(sh.threads) +
+        const size_t smem = ln::Feed<T, 2, NV, G, ALIGNED, MT != 1024>::smem(sh.threads) +
                             (MT == 1024     ? size_t(sh.threads) * NV * 16 / sizeof(T) * 2 * sizeof(float)
                              : !ALIGNED && !G ? size_t(a.width) * sizeof(float)
                                               : 0);
