@@ -10,8 +10,9 @@
 // parallelism along the time axis. A row's map s -> a s + x composes: a
 // segment of rows is s -> A s + B with A the product of its decays. A cluster
 // of CTAs takes half of a head's channels and walks the packed token axis in
-// rounds; in a round each CTA takes the next tile of 128 rows, each of its
-// warps a segment of kSeg rows, each lane two channels:
+// rounds; in a round each CTA takes the next tile of 128 rows (256 with gates
+// per head, which need no registers for decays), each of its warps a segment
+// of 16 (32) rows, each lane two channels:
 //  1. every warp composes its segment's rows (tile in shared memory by TMA,
 //     kept in registers from here on);
 //  2. the CTA composes its segments and stores the result into every CTA of
@@ -52,20 +53,20 @@ using vec::Pack;
 
 constexpr int kRecWarps = 8;
 constexpr int kRecThreads = 32 * kRecWarps;
-constexpr int kSeg = 16;  // rows of a warp in a round
-constexpr int kHalf = kSeg / 2;
+constexpr int kPart = 8;  // rows whose states the backward pass holds at a time
 constexpr int kMaxCluster = 16;  // above the portable eight
 constexpr float kReset = -1.f;  // in the place of a product of decays (never negative)
 
-// A CTA's tile: 64 channels x 8 segments of rows, or (WIDE) 128 x 4. A warp
-// has 64 channels, two a lane, of one segment.
-template <bool WIDE>
+// A CTA's tile: 64 channels x 8 segments of SEG rows, or (WIDE) 128 x 4. A
+// warp has 64 channels, two a lane, of one segment.
+template <bool WIDE, int SEG>
 struct Tile {
+    static constexpr int kSeg = SEG;
     static constexpr int kCh = WIDE ? 128 : 64;
     static constexpr int kSegs = WIDE ? 4 : 8;
     static constexpr int kRows = kSegs * kSeg;
     static constexpr int kParts = kHeadDim / kCh;  // clusters of a head
-    static_assert(kRows % kStateRows == 0, "");
+    static_assert(kRows % kStateRows == 0 && kStateRows % kSeg == 0 && kSeg % kPart == 0, "");
 
     static __device__ __forceinline__ int seg() { return (threadIdx.x >> 5) % kSegs; }
     // the lane's first channel in the tile
@@ -84,6 +85,15 @@ __device__ __forceinline__ void compose(float &a, float &b, float a2, float b2) 
 
 __device__ __forceinline__ float apply(float a, float b, float s) { return a < 0.f ? b : fmaf(a, s, b); }
 
+// Where sequences start and end in a tile, for all of its warps: bit i of
+// starts[k] (ends[k]) says that row i of segment k is a sequence's first
+// (last), `first` (`last`) at that row which sequence it is.
+template <typename S>
+struct Marks {
+    uint32_t starts[S::kSegs], ends[S::kSegs];
+    int first[S::kRows], last[S::kRows];
+};
+
 // The sequences' boundaries on the token axis.
 struct Bounds {
     const int32_t *cu;
@@ -91,25 +101,33 @@ struct Bounds {
 
     __device__ __forceinline__ int start(int i) const { return cu ? cu[i] : i * seqlen; }
 
-    // Boundaries of a tile of SEGS segments from row t0, by one warp: bit i
-    // (0 .. kSeg) of m[k] says that a sequence ends before, or starts at, row
-    // t0 + k kSeg + i. Packed: the offsets are searched 32 at a time from
-    // `next` on, where the last call left it (FORWARD: t0 rises from call to
-    // call and next starts at 0; else t0 falls and next starts at n + 1).
-    template <bool FORWARD, int SEGS>
-    __device__ __forceinline__ void masks(int t0, int &next, uint32_t *m) const {
-        const int lane = threadIdx.x & 31, end = min(t0 + SEGS * kSeg, total);
-        if (lane < SEGS) m[lane] = 0;
+    // Marks the tile from row t0, by one warp. Packed: the offsets are searched
+    // 32 at a time from `next` on, where the last call left it (FORWARD: t0
+    // rises from call to call and next starts at 0; else t0 falls and next
+    // starts at n + 1). Sequences without rows share an offset with their
+    // neighbours and are left out.
+    template <bool FORWARD, typename S>
+    __device__ __forceinline__ void mark(int t0, int &next, Marks<S> &m) const {
+        const int lane = threadIdx.x & 31, end = min(t0 + S::kRows, total);
+        if (lane < S::kSegs) m.starts[lane] = m.ends[lane] = 0;
         __syncwarp();
-        auto mark = [&](int r) {  // row r of the tile
-            if (r < SEGS * kSeg) atomicOr(&m[r / kSeg], 1u << (r % kSeg));
-            if (r && r % kSeg == 0) atomicOr(&m[r / kSeg - 1], 1u << kSeg);
-        };
         if (t0 >= total) return;
+        auto start_at = [&](int r, int seq) {
+            if (r >= S::kRows || t0 + r >= total) return;
+            atomicOr(&m.starts[r / S::kSeg], 1u << (r % S::kSeg));
+            m.first[r] = seq;
+        };
+        auto end_at = [&](int r, int seq) {
+            if (r < 0) return;
+            atomicOr(&m.ends[r / S::kSeg], 1u << (r % S::kSeg));
+            m.last[r] = seq;
+        };
         if (!cu) {
-            for (long long b = (long long)(t0 + seqlen - 1) / seqlen * seqlen + (long long)lane * seqlen; b <= end;
-                 b += 32ll * seqlen)
-                mark(int(b) - t0);
+            for (long long k = (t0 + seqlen - 1) / seqlen + lane; k * seqlen <= end; k += 32) {
+                const int r = int(k * seqlen) - t0;
+                start_at(r, int(k));
+                end_at(r - 1, int(k) - 1);
+            }
             return;
         }
         uint32_t moved;
@@ -126,47 +144,19 @@ struct Bounds {
         for (int k = next + lane; __ballot_sync(0xffffffffu, in) == 0xffffffffu; k += 32) {
             const int v = k <= n ? cu[k] : INT_MAX;
             in = v <= end;
-            if (in) mark(v - t0);
+            if (!in) continue;
+            if (k < n && cu[k + 1] != v) start_at(v - t0, k);    // the last sequence of those that start here
+            if (k > 0 && cu[k - 1] != v) end_at(v - t0 - 1, k - 1);  // the first of those that end here
         }
-    }
-
-    // the sequence that starts at row t (one with rows does)
-    __device__ __forceinline__ int starting(int t) const {
-        if (!cu) return t / seqlen;
-        int lo = 0, hi = n - 1;  // the last i with cu[i] <= t
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cu[mid] <= t) lo = mid;
-            else hi = mid - 1;
-        }
-        return lo;
-    }
-
-    // the sequence whose last row is t
-    __device__ __forceinline__ int ending(int t) const {
-        if (!cu) return t / seqlen;
-        int lo = 1, hi = n;  // the first i with cu[i] > t
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid] > t) hi = mid;
-            else lo = mid + 1;
-        }
-        return lo - 1;
     }
 };
 
-// A lane's channels of per-sequence states [num_seqs, hv, 128], read or
-// written at a boundary. Out of line: boundaries are rare, and the walks hold
-// one such place for every row.
-template <bool ENDING>
-__device__ __noinline__ float2 boundary_load(const float *from, Bounds bd, int t, int hv, int hc) {
-    if (!from) return make_float2(0.f, 0.f);
-    return *reinterpret_cast<const float2 *>(from + (long long)(ENDING ? bd.ending(t) : bd.starting(t)) * hv * kHeadDim +
-                                             hc);
+// A lane's two channels of sequence `seq` in per-sequence states [num_seqs, hv, 128] (null: zeros).
+__device__ __forceinline__ float2 state_of(const float *from, int seq, int width, int hc) {
+    return from ? *reinterpret_cast<const float2 *>(from + (long long)seq * width + hc) : make_float2(0.f, 0.f);
 }
-template <bool ENDING>
-__device__ __noinline__ void boundary_store(float *to, Bounds bd, int t, int hv, int hc, float2 v) {
-    *reinterpret_cast<float2 *>(to + (long long)(ENDING ? bd.ending(t) : bd.starting(t)) * hv * kHeadDim + hc) = v;
+__device__ __forceinline__ void set_state(float *to, int seq, int width, int hc, float2 v) {
+    *reinterpret_cast<float2 *>(to + (long long)seq * width + hc) = v;
 }
 
 __device__ __forceinline__ float2 &pair(float *p) { return *reinterpret_cast<float2 *>(p); }
@@ -184,11 +174,10 @@ __device__ __forceinline__ bool offsets_ok(const RecArgs &a) {
 }
 
 // Sequences without rows: `to` gets `from` (null: zeros).
-template <bool WIDE>
+template <typename S>
 __device__ __forceinline__ void copy_empty(const RecArgs &a, const Bounds &bd, const float *from, float *to, int hc,
                                            int rank, int ctas) {
     if (!to) return;
-    using S = Tile<WIDE>;
     for (int i = rank * S::kSegs + S::seg(); i < a.num_seqs; i += ctas * S::kSegs) {
         if (bd.start(i) != bd.start(i + 1)) continue;
         const long long o = (long long)i * a.hv * kHeadDim + hc;
@@ -198,20 +187,18 @@ __device__ __forceinline__ void copy_empty(const RecArgs &a, const Bounds &bd, c
 }
 
 // Shared memory of a round's exchange.
-template <bool WIDE>
+template <typename S>
 struct Exchange {
-    using S = Tile<WIDE>;
     float seg_a[S::kSegs][S::kCh], seg_b[S::kSegs][S::kCh];  // segments; seg_b then the state at each
     float2 cta[2][kMaxCluster][S::kCh];  // by round parity: every CTA's composed segments (a, b)
     uint64_t bar[2];
-    uint32_t masks[2][S::kSegs];  // boundaries, by round parity
-    float decays[2][S::kRows];    // of gates per head, by round parity
+    Marks<S> marks[2];          // by round parity
+    float decays[2][S::kRows];  // of gates per head, by round parity
 };
 
 // A channel's segments of a tile in walking order.
-template <bool WIDE, bool REVERSE>
+template <typename S, bool REVERSE>
 struct Segments {
-    using S = Tile<WIDE>;
     float a[S::kSegs], b[S::kSegs];
 
     static __device__ __forceinline__ int seg(int i) { return REVERSE ? S::kSegs - 1 - i : i; }
@@ -246,14 +233,13 @@ struct Segments {
 // thread a channel is the fewest instructions; the other warps have the
 // forward states of the backward pass, the next tiles' boundaries and gates
 // to see to meanwhile.
-template <bool WIDE, bool REVERSE, typename F>
-__device__ __forceinline__ void exchange(Exchange<WIDE> &ex, float &carry, int round, int rank, int ctas, bool &ok,
+template <bool REVERSE, typename S, typename F>
+__device__ __forceinline__ void exchange(Exchange<S> &ex, float &carry, int round, int rank, int ctas, bool &ok,
                                          unsigned long long limit, F at) {
     using namespace tc;
-    using S = Tile<WIDE>;
     const int ch = threadIdx.x, p = round & 1;
     if (threadIdx.x == 0) mbar_arrive_expect_tx(&ex.bar[p], uint32_t(ctas) * S::kCh * 8);
-    Segments<WIDE, REVERSE> sg(ex.seg_a, ex.seg_b, ch);
+    Segments<S, REVERSE> sg(ex.seg_a, ex.seg_b, ch);
     const float2 mine = sg.composed();
 #pragma unroll 4
     for (int r = 0; r < ctas; ++r)
@@ -274,14 +260,14 @@ __device__ __forceinline__ void exchange(Exchange<WIDE> &ex, float &carry, int r
 // Tile loads through a ring of stages: one thread issues, everyone waits.
 template <typename T, bool CHANNEL, bool BACKWARD>
 struct Ring {
-    using S = Tile<BACKWARD && !CHANNEL>;
+    using S = Tile<BACKWARD && !CHANNEL, (CHANNEL || BACKWARD || sizeof(T) == 4) ? 16 : 32>;
     static constexpr int kTile = S::kRows * S::kCh;                                 // elements of one tensor's tile
     static constexpr uint32_t kTiles = kTile * sizeof(T) * (1 + CHANNEL + BACKWARD);  // x, g per channel, dout
     static constexpr uint32_t kState = BACKWARD ? S::kCh * 4 : 0;                     // the state before the tile
     static constexpr uint32_t kBytes = kTiles + kState;
     // CTAs of an SM that registers allow, and stages that shared memory then allows
     static constexpr int kCtasPerSm = BACKWARD && sizeof(T) == 4 ? 1 : 2;
-    static constexpr int kStages = kTiles <= 16384 ? 3 : kTiles <= 32768 ? 2 : 1;
+    static constexpr int kStages = kTiles <= 32768 ? 2 : 1;
     static constexpr size_t kSmem = size_t(kStages) * kBytes + 128;
     uint8_t *base;
     uint64_t *full;
@@ -336,19 +322,18 @@ struct HeadGates {
 };
 
 // Decays of a segment's rows for the lane's two channels, and what the walks
-// do with them: packed operations on pairs of their own, scalar ones on the
-// head's one value.
-template <typename T, bool CHANNEL>
+// do with them: packed operations on pairs of their own; scalar ones on the
+// head's one value, which stays in shared memory.
+template <typename T, bool CHANNEL, typename S>
 struct Decays;
-template <typename T>
-struct Decays<T, true> {
-    using Product = float2;
-    float2 d[kSeg];
+template <typename T, typename S>
+struct Decays<T, true, S> {
+    float2 d[S::kSeg];
     __device__ __forceinline__ Decays(const T *g_tile, const float *) {
 #pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
+        for (int i = 0; i < S::kSeg; ++i) {
             Pack<T, 2> p;
-            p.load(g_tile + i * Tile<false>::kCh);
+            p.load(g_tile + i * S::kCh);
             d[i] = vec::exp2_of(make_float2(p.f(0), p.f(1)));
         }
     }
@@ -357,20 +342,14 @@ struct Decays<T, true> {
     __device__ __forceinline__ float2 product() const {
         float2 p = d[0];
 #pragma unroll
-        for (int i = 1; i < kSeg; ++i) p = mul2(p, d[i]);
+        for (int i = 1; i < S::kSeg; ++i) p = mul2(p, d[i]);
         return p;
     }
 };
-template <typename T>
-struct Decays<T, false> {
-    float d[kSeg];
-    __device__ __forceinline__ Decays(const T *, const float *decays) {
-#pragma unroll
-        for (int i = 0; i < kSeg; i += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(decays + i);
-            d[i] = v.x, d[i + 1] = v.y, d[i + 2] = v.z, d[i + 3] = v.w;
-        }
-    }
+template <typename T, typename S>
+struct Decays<T, false, S> {
+    const float *d;
+    __device__ __forceinline__ Decays(const T *, const float *decays) : d(decays) {}
     __device__ __forceinline__ float2 fma(int i, float2 s, float2 x) const {
         return make_float2(fmaf(d[i], s.x, x.x), fmaf(d[i], s.y, x.y));
     }
@@ -380,7 +359,7 @@ struct Decays<T, false> {
     __device__ __forceinline__ float2 product() const {
         float p = d[0];
 #pragma unroll
-        for (int i = 1; i < kSeg; ++i) p = __fmul_rn(p, d[i]);
+        for (int i = 1; i < S::kSeg; ++i) p = __fmul_rn(p, d[i]);
         return make_float2(p, p);
     }
 };
@@ -425,7 +404,8 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     using R = Ring<T, CHANNEL, false>;
     using S = typename R::S;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Exchange<false> ex;
+    constexpr int kSeg = S::kSeg;
+    __shared__ Exchange<S> ex;
     __shared__ uint64_t full[R::kStages];
     const int w = S::seg(), c = S::channel();
     const bool last_warp = threadIdx.x >= kRecThreads - 32, feeder = threadIdx.x == kRecThreads - 1;
@@ -455,14 +435,14 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     int next = 0;
     HeadGates<S::kRows> gates;
     if (last_warp) {
-        bd.masks<true, S::kSegs>(rank * S::kRows, next, ex.masks[0]);
+        bd.mark<true>(rank * S::kRows, next, ex.marks[0]);
         if (!CHANNEL) {
             gates.load(a, rank * S::kRows, h);
             gates.store(ex.decays[0]);
             gates.load(a, (ctas + rank) * S::kRows, h);
         }
     }
-    copy_empty<false>(a, bd, a.s0, a.final_state, hc, rank, ctas);
+    copy_empty<S>(a, bd, a.s0, a.final_state, hc, rank, ctas);
     __syncthreads();
     float carry = 0.f;  // of this thread's channel in the exchange, before the round
     const int width = a.hv * kHeadDim;  // of a row
@@ -470,28 +450,30 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     for (int round = 0; round < rounds; ++round) {
         const int t0 = (round * ctas + rank) * S::kRows, tw = t0 + w * kSeg;  // the tile's and the warp's first row
         const int rows = min(kSeg, a.total_tokens - tw);                     // may be negative
-        const uint32_t starts = ex.masks[round & 1][w];  // bit kSeg: before the next segment
+        const Marks<S> &marks = ex.marks[round & 1];
+        const uint32_t starts = marks.starts[w], ends = marks.ends[w];
+        const int *first = marks.first + w * kSeg, *last = marks.last + w * kSeg;
         ring.wait(round, ok, a.wait_ns);
         Pack<T, 2> x[kSeg];
         const int o = w * kSeg * S::kCh + c;
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) x[i].load(ring.x(round) + o + i * S::kCh);
-        const Decays<T, CHANNEL> d(ring.g(round) + o, ex.decays[round & 1] + w * kSeg);
-        const bool plain = starts == 0 && rows == kSeg;
+        const Decays<T, CHANNEL, S> d(ring.g(round) + o, ex.decays[round & 1] + w * kSeg);
+        const bool plain = !(starts | ends) && rows == kSeg;
         {
             float2 A = d.product(), B = make_float2(0.f, 0.f);
             walk<0, kSeg - 1>(plain, [&](int i, auto checked) {
-                if (checked && (starts >> i & 1) && i < rows) B = boundary_load<false>(a.s0, bd, tw + i, a.hv, hc);
+                if (checked && (starts >> i & 1)) B = state_of(a.s0, first[i], width, hc);
                 B = d.fma(i, B, f2(x[i]));
             });
-            if (starts & ((1u << max(rows, 0)) - 1)) A = make_float2(kReset, kReset);
+            if (starts) A = make_float2(kReset, kReset);
             pair(&ex.seg_a[w][c]) = A;
             pair(&ex.seg_b[w][c]) = B;
         }
         __syncthreads();
         if (round == 0) cluster_wait();  // every CTA's barriers are ready
         if (threadIdx.x < S::kCh)
-            exchange<false, false>(ex, carry, round, rank, ctas, ok, a.wait_ns, [&](int seg, float s) {
+            exchange<false>(ex, carry, round, rank, ctas, ok, a.wait_ns, [&](int seg, float s) {
                 const int t = t0 + seg * kSeg;
                 if (seg % (kStateRows / kSeg) == 0 && a.states && t < a.total_tokens)
                     a.states[(long long)(t / kStateRows) * width + h * kHeadDim + c0 + threadIdx.x] = s;
@@ -501,7 +483,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
             if (feeder && round + R::kStages < rounds)
                 ring.load(round + R::kStages, &mx, &mg, nullptr, a, c0, h, t0 + R::kStages * ctas * S::kRows);
             __syncwarp();
-            bd.masks<true, S::kSegs>(t0 + ctas * S::kRows, next, ex.masks[(round + 1) & 1]);
+            bd.mark<true>(t0 + ctas * S::kRows, next, ex.marks[(round + 1) & 1]);
             if (!CHANNEL) {
                 gates.store(ex.decays[(round + 1) & 1]);
                 gates.load(a, t0 + 2 * ctas * S::kRows, h);
@@ -513,12 +495,11 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
         walk<0, kSeg - 1>(plain, [&](int i, auto checked) {
             if (checked) {
                 if (i >= rows) return;
-                if (starts >> i & 1) s = boundary_load<false>(a.s0, bd, tw + i, a.hv, hc);
+                if (starts >> i & 1) s = state_of(a.s0, first[i], width, hc);
             }
             s = d.fma(i, s, f2(x[i]));
             store2(row_at(out, pitch, i), s);
-            if (checked && a.final_state && (starts >> (i + 1) & 1))
-                boundary_store<true>(a.final_state, bd, tw + i, a.hv, hc, s);
+            if (checked && a.final_state && (ends >> i & 1)) set_state(a.final_state, last[i], width, hc, s);
         });
     }
     if (!ok && (threadIdx.x & 31) == 0) record_status(a.status, GDN_ETIMEOUT);
@@ -534,9 +515,9 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     using namespace tc;
     using R = Ring<T, CHANNEL, true>;
     using S = typename R::S;
-    constexpr bool WIDE = !CHANNEL;
+    constexpr int kSeg = S::kSeg;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Exchange<WIDE> ex;
+    __shared__ Exchange<S> ex;
     __shared__ float fwd_a[S::kSegs][S::kCh], fwd_b[S::kSegs][S::kCh];
     __shared__ float head_sums[CHANNEL ? 1 : 2][2][CHANNEL ? 1 : S::kRows];  // by round parity, half of the head, row
     __shared__ uint64_t full[R::kStages];
@@ -569,14 +550,14 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     int next = a.num_seqs + 1;
     HeadGates<S::kRows> gates;
     if (last_warp) {
-        bd.masks<false, S::kSegs>(t_first, next, ex.masks[0]);
+        bd.mark<false>(t_first, next, ex.marks[0]);
         if (!CHANNEL) {
             gates.load(a, t_first, h);
             gates.store(ex.decays[0]);
             gates.load(a, t_first - t_step, h);
         }
     }
-    copy_empty<WIDE>(a, bd, a.dfinal, a.dinitial, hc, rank, ctas);
+    copy_empty<S>(a, bd, a.dfinal, a.dinitial, hc, rank, ctas);
     __syncthreads();
     float carry = 0.f;
     const int width = a.hv * kHeadDim;  // of a row
@@ -590,10 +571,11 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     for (int round = 0; round < rounds; ++round) {
         const int t0 = t_first - round * t_step, tw = t0 + w * kSeg;
         const int rows = min(kSeg, a.total_tokens - tw);
-        const uint32_t bounds = ex.masks[round & 1][w];
         // the segment's rows that start (s is reset) and end (e is reset) a sequence
-        const uint32_t starts = bounds & ((1u << max(rows, 0)) - 1), ends = bounds >> 1;
-        const bool plain = bounds == 0 && rows == kSeg;
+        const Marks<S> &marks = ex.marks[round & 1];
+        const uint32_t starts = marks.starts[w], ends = marks.ends[w];
+        const int *first = marks.first + w * kSeg, *last = marks.last + w * kSeg;
+        const bool plain = !(starts | ends) && rows == kSeg;
         ring.wait(round, ok, a.wait_ns);
         const float state = ring.state(round)[threadIdx.x % S::kCh];  // unused where the tile starts a sequence
         Pack<T, 2> x[kSeg], dy[kSeg];
@@ -603,17 +585,17 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
             x[i].load(ring.x(round) + o + i * S::kCh);
             dy[i].load(ring.dout(round) + o + i * S::kCh);
         }
-        const Decays<T, CHANNEL> d(ring.g(round) + o, ex.decays[round & 1] + w * kSeg);
+        const Decays<T, CHANNEL, S> d(ring.g(round) + o, ex.decays[round & 1] + w * kSeg);
         // the rows' maps: forward for s, in reverse for e
         {
             const float2 A = d.product();
             float2 B = make_float2(0.f, 0.f), E = make_float2(0.f, 0.f);
             walk<0, kSeg - 1>(plain, [&](int i, auto checked) {
-                if (checked && (starts >> i & 1)) B = boundary_load<false>(a.s0, bd, tw + i, a.hv, hc);
+                if (checked && (starts >> i & 1)) B = state_of(a.s0, first[i], width, hc);
                 B = d.fma(i, B, f2(x[i]));
             });
             walk<kSeg - 1, 0>(plain, [&](int i, auto checked) {
-                if (checked && (ends >> i & 1)) E = boundary_load<true>(a.dfinal, bd, tw + i, a.hv, hc);
+                if (checked && (ends >> i & 1)) E = state_of(a.dfinal, last[i], width, hc);
                 E = d.mul(i, __fadd2_rn(f2(dy[i]), E));
             });
             const float2 reset = make_float2(kReset, kReset);
@@ -629,55 +611,64 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         if (round == 0) cluster_wait();
         __syncwarp();
         if (threadIdx.x < S::kCh) {
-            exchange<WIDE, true>(ex, carry, round, rank, ctas, ok, a.wait_ns, [](int, float) {});
+            exchange<true>(ex, carry, round, rank, ctas, ok, a.wait_ns, [](int, float) {});
         } else if (threadIdx.x < 2 * S::kCh) {
             const int ch = threadIdx.x - S::kCh;
-            Segments<WIDE, false> sg(fwd_a, fwd_b, ch);
+            Segments<S, false> sg(fwd_a, fwd_b, ch);
             sg.finish(fwd_b, ch, state, [](int, float) {});
         }
         if (last_warp && round + 1 < rounds) {
             __syncwarp();
-            bd.masks<false, S::kSegs>(t0 - t_step, next, ex.masks[(round + 1) & 1]);
+            bd.mark<false>(t0 - t_step, next, ex.marks[(round + 1) & 1]);
             if (!CHANNEL) {
                 gates.store(ex.decays[(round + 1) & 1]);
                 gates.load(a, t0 - 2 * t_step, h);
             }
         }
         __syncthreads();
-        // The segment's states are kept for half of its rows at a time, the
-        // last half first: half the registers for one more walk over the
-        // first half.
-        float2 e = pair(&ex.seg_b[w][c]);
-        const float2 s0 = pair(&fwd_b[w][c]);
+        // The segment's states are kept for kPart rows at a time, the last part
+        // first: from the states at the parts' first rows, which one walk over
+        // the segment gives, each part is walked again.
+        constexpr int kParts = kSeg / kPart;
+        float2 e = pair(&ex.seg_b[w][c]), at_part[kParts];
+        {
+            float2 s = pair(&fwd_b[w][c]);
+            at_part[0] = s;
+            walk<0, kSeg - kPart - 1>(plain, [&](int i, auto checked) {
+                if (checked && (starts >> i & 1)) s = state_of(a.s0, first[i], width, hc);
+                s = d.fma(i, s, f2(x[i]));
+                if (i % kPart == kPart - 1) at_part[i / kPart + 1] = s;
+            });
+        }
         T *dx = static_cast<T *>(a.dx) + (long long)tw * width + hc;
         T *dgc = static_cast<T *>(a.dg) + (long long)tw * width + hc;  // per channel
-        auto half_walk = [&](auto half_) {
-            constexpr int half = decltype(half_)::value;
-            float2 s = s0, before[kHalf];
-            walk<0, (half + 1) * kHalf - 1>(plain, [&](int i, auto checked) {
-                if (checked && (starts >> i & 1)) s = boundary_load<false>(a.s0, bd, tw + i, a.hv, hc);
-                if (i >= half * kHalf) before[i % kHalf] = s;
+        auto part_walk = [&](auto part_) {
+            constexpr int part = decltype(part_)::value;
+            float2 s = at_part[part], before[kPart];
+            walk<part * kPart, part * kPart + kPart - 1>(plain, [&](int i, auto checked) {
+                if (checked && (starts >> i & 1)) s = state_of(a.s0, first[i], width, hc);
+                before[i % kPart] = s;
                 s = d.fma(i, s, f2(x[i]));
             });
-            float sums[kHalf];
-            walk<half * kHalf + kHalf - 1, half * kHalf>(plain, [&](int i, auto checked) {
-                if (checked && (ends >> i & 1)) e = boundary_load<true>(a.dfinal, bd, tw + i, a.hv, hc);
+            float sums[kPart];
+            walk<part * kPart + kPart - 1, part * kPart>(plain, [&](int i, auto checked) {
+                if (checked && (ends >> i & 1)) e = state_of(a.dfinal, last[i], width, hc);
                 const float2 ds = __fadd2_rn(f2(dy[i]), e);
                 e = d.mul(i, ds);
-                const float2 dg = mul2(e, before[i % kHalf]);
-                if (!CHANNEL) sums[i % kHalf] = dg.x + dg.y;
+                const float2 dg = mul2(e, before[i % kPart]);
+                if (!CHANNEL) sums[i % kPart] = dg.x + dg.y;
                 if (!checked || i < rows) {
                     store2(row_at(dx, pitch, i), ds);
                     if (CHANNEL) store2(row_at(dgc, pitch, i), dg);
                     if (checked && a.dinitial && (starts >> i & 1))
-                        boundary_store<false>(a.dinitial, bd, tw + i, a.hv, hc, e);
+                        set_state(a.dinitial, first[i], width, hc, e);
                 }
             });
             if (!CHANNEL) {
                 // eight rows' sums over the warp's channels: lanes halve the
                 // rows they add, lane 4 r ends with row r
 #pragma unroll
-                for (int m = 16, k = kHalf / 2; k; m >>= 1, k >>= 1) {
+                for (int m = 16, k = kPart / 2; k; m >>= 1, k >>= 1) {
                     const bool up = lane & m;
 #pragma unroll
                     for (int i = 0; i < k; ++i) {
@@ -688,11 +679,15 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
                 sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 2);
                 sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 1);
                 // written out after the next round's first barrier
-                if ((lane & 3) == 0) head_sums[round & 1][c / 64][w * kSeg + half * kHalf + (lane >> 2)] = sums[0];
+                if ((lane & 3) == 0) head_sums[round & 1][c / 64][w * kSeg + part * kPart + (lane >> 2)] = sums[0];
             }
         };
-        half_walk(std::integral_constant<int, 1>{});
-        half_walk(std::integral_constant<int, 0>{});
+        if constexpr (kParts == 4) {
+            part_walk(std::integral_constant<int, 3>{});
+            part_walk(std::integral_constant<int, 2>{});
+        }
+        part_walk(std::integral_constant<int, 1>{});
+        part_walk(std::integral_constant<int, 0>{});
     }
     if (!CHANNEL && rounds) {
         __syncthreads();
@@ -704,7 +699,7 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     cluster_wait();
 }
 
-static_assert(kHalf == 8, "the sums over a head's channels take eight rows at a time");
+static_assert(kPart == 8, "the sums over a head's channels take eight rows at a time");
 
 // Decode step: a warp takes one (sequence, head) row, four channels a lane.
 // HBM-bound (state read and written, x and out); every access of a warp is
