@@ -73,6 +73,7 @@ struct Tile {
     static __device__ __forceinline__ int channel() { return (threadIdx.x >> 5) / kSegs * 64 + (threadIdx.x & 31) * 2; }
 };
 
+using vec::both;
 using vec::fma2;
 using vec::mul2;
 
@@ -193,7 +194,10 @@ struct Exchange {
     float2 cta[2][kMaxCluster][S::kCh];  // by round parity: every CTA's composed segments (a, b)
     uint64_t bar[2];
     Marks<S> marks[2];          // by round parity
-    float decays[2][S::kRows];  // of gates per head, by round parity
+    // of gates per head, by round parity: every row's decay, twice (for packed
+    // arithmetic), and their product in parts of kPart rows
+    float2 decays[2][S::kRows];
+    float2 products[2][S::kRows / kPart];
 };
 
 // A channel's segments of a tile in walking order.
@@ -311,34 +315,42 @@ struct HeadGates {
             g[k] = t >= 0 && t < a.total_tokens ? static_cast<const float *>(a.g)[(long long)t * a.hv + h] : 0.f;
         }
     }
-    __device__ __forceinline__ void store(float *to) const {
+    __device__ __forceinline__ void store(float2 *to, float2 *products) const {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int k = 0; k < ROWS / 32; k += 2) {
-            const float2 d = vec::exp2_of(make_float2(g[k], g[k + 1]));
-            to[k * 32 + int(threadIdx.x & 31)] = d.x;
-            to[(k + 1) * 32 + int(threadIdx.x & 31)] = d.y;
+            float2 d = vec::exp2_of(make_float2(g[k], g[k + 1]));
+            to[k * 32 + lane] = vec::both(d.x);
+            to[(k + 1) * 32 + lane] = vec::both(d.y);
+#pragma unroll
+            for (int m = 1; m < kPart; m *= 2) {
+                d.x *= __shfl_xor_sync(0xffffffffu, d.x, m);
+                d.y *= __shfl_xor_sync(0xffffffffu, d.y, m);
+            }
+            if (lane % kPart == 0) {
+                products[(k * 32 + lane) / kPart] = vec::both(d.x);
+                products[((k + 1) * 32 + lane) / kPart] = vec::both(d.y);
+            }
         }
     }
 };
 
-// Decays of a segment's rows for the lane's two channels, and what the walks
-// do with them: packed operations on pairs of their own; scalar ones on the
-// head's one value, which stays in shared memory.
+// Decays of a segment's rows for the lane's two channels: pairs of their own,
+// in registers, or the head's one value, in shared memory.
 template <typename T, bool CHANNEL, typename S>
 struct Decays;
 template <typename T, typename S>
 struct Decays<T, true, S> {
     float2 d[S::kSeg];
-    __device__ __forceinline__ Decays(const T *g_tile, const float *) {
+    __device__ __forceinline__ Decays(const T *g_tile, const float2 *, const float2 *) {
 #pragma unroll
         for (int i = 0; i < S::kSeg; ++i) {
             Pack<T, 2> p;
             p.load(g_tile + i * S::kCh);
-            d[i] = vec::exp2_of(make_float2(p.f(0), p.f(1)));
+            d[i] = vec::exp2_of(p.f2(0));
         }
     }
-    __device__ __forceinline__ float2 fma(int i, float2 s, float2 x) const { return fma2(d[i], s, x); }
-    __device__ __forceinline__ float2 mul(int i, float2 s) const { return mul2(d[i], s); }
+    __device__ __forceinline__ float2 operator()(int i) const { return d[i]; }
     __device__ __forceinline__ float2 product() const {
         float2 p = d[0];
 #pragma unroll
@@ -348,19 +360,16 @@ struct Decays<T, true, S> {
 };
 template <typename T, typename S>
 struct Decays<T, false, S> {
-    const float *d;
-    __device__ __forceinline__ Decays(const T *, const float *decays) : d(decays) {}
-    __device__ __forceinline__ float2 fma(int i, float2 s, float2 x) const {
-        return make_float2(fmaf(d[i], s.x, x.x), fmaf(d[i], s.y, x.y));
-    }
-    __device__ __forceinline__ float2 mul(int i, float2 s) const {
-        return make_float2(__fmul_rn(d[i], s.x), __fmul_rn(d[i], s.y));
-    }
+    const float2 *d, *parts;
+    __device__ __forceinline__ Decays(const T *, const float2 *decays, const float2 *products)
+        : d(decays), parts(products) {}
+    __device__ __forceinline__ float2 operator()(int i) const { return d[i]; }
+    __device__ __forceinline__ float2 part(int k) const { return parts[k]; }
     __device__ __forceinline__ float2 product() const {
-        float p = d[0];
+        float2 p = parts[0];
 #pragma unroll
-        for (int i = 1; i < S::kSeg; ++i) p = __fmul_rn(p, d[i]);
-        return make_float2(p, p);
+        for (int k = 1; k < S::kSeg / kPart; ++k) p = mul2(p, parts[k]);
+        return p;
     }
 };
 
@@ -438,7 +447,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
         bd.mark<true>(rank * S::kRows, next, ex.marks[0]);
         if (!CHANNEL) {
             gates.load(a, rank * S::kRows, h);
-            gates.store(ex.decays[0]);
+            gates.store(ex.decays[0], ex.products[0]);
             gates.load(a, (ctas + rank) * S::kRows, h);
         }
     }
@@ -458,13 +467,14 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
         const int o = w * kSeg * S::kCh + c;
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) x[i].load(ring.x(round) + o + i * S::kCh);
-        const Decays<T, CHANNEL, S> d(ring.g(round) + o, ex.decays[round & 1] + w * kSeg);
+        const Decays<T, CHANNEL, S> d(ring.g(round) + o, ex.decays[round & 1] + w * kSeg,
+                                        ex.products[round & 1] + w * (kSeg / kPart));
         const bool plain = !(starts | ends) && rows == kSeg;
         {
             float2 A = d.product(), B = make_float2(0.f, 0.f);
             walk<0, kSeg - 1>(plain, [&](int i, auto checked) {
                 if (checked && (starts >> i & 1)) B = state_of(a.s0, first[i], width, hc);
-                B = d.fma(i, B, f2(x[i]));
+                B = fma2(d(i), B, f2(x[i]));
             });
             if (starts) A = make_float2(kReset, kReset);
             pair(&ex.seg_a[w][c]) = A;
@@ -485,7 +495,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
             __syncwarp();
             bd.mark<true>(t0 + ctas * S::kRows, next, ex.marks[(round + 1) & 1]);
             if (!CHANNEL) {
-                gates.store(ex.decays[(round + 1) & 1]);
+                gates.store(ex.decays[(round + 1) & 1], ex.products[(round + 1) & 1]);
                 gates.load(a, t0 + 2 * ctas * S::kRows, h);
             }
         }
@@ -497,7 +507,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
                 if (i >= rows) return;
                 if (starts >> i & 1) s = state_of(a.s0, first[i], width, hc);
             }
-            s = d.fma(i, s, f2(x[i]));
+            s = fma2(d(i), s, f2(x[i]));
             store2(row_at(out, pitch, i), s);
             if (checked && a.final_state && (ends >> i & 1)) set_state(a.final_state, last[i], width, hc, s);
         });
@@ -553,7 +563,7 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         bd.mark<false>(t_first, next, ex.marks[0]);
         if (!CHANNEL) {
             gates.load(a, t_first, h);
-            gates.store(ex.decays[0]);
+            gates.store(ex.decays[0], ex.products[0]);
             gates.load(a, t_first - t_step, h);
         }
     }
@@ -585,18 +595,21 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
             x[i].load(ring.x(round) + o + i * S::kCh);
             dy[i].load(ring.dout(round) + o + i * S::kCh);
         }
-        const Decays<T, CHANNEL, S> d(ring.g(round) + o, ex.decays[round & 1] + w * kSeg);
+        const Decays<T, CHANNEL, S> d(ring.g(round) + o, ex.decays[round & 1] + w * kSeg,
+                                        ex.products[round & 1] + w * (kSeg / kPart));
         // the rows' maps: forward for s, in reverse for e
+        float2 to_part[kSeg / kPart];  // from the segment's first row with s = 0 to every part's
         {
             const float2 A = d.product();
             float2 B = make_float2(0.f, 0.f), E = make_float2(0.f, 0.f);
             walk<0, kSeg - 1>(plain, [&](int i, auto checked) {
+                if (!CHANNEL && i % kPart == 0) to_part[i / kPart] = B;
                 if (checked && (starts >> i & 1)) B = state_of(a.s0, first[i], width, hc);
-                B = d.fma(i, B, f2(x[i]));
+                B = fma2(d(i), B, f2(x[i]));
             });
             walk<kSeg - 1, 0>(plain, [&](int i, auto checked) {
                 if (checked && (ends >> i & 1)) E = state_of(a.dfinal, last[i], width, hc);
-                E = d.mul(i, __fadd2_rn(f2(dy[i]), E));
+                E = mul2(d(i), vec::add2(f2(dy[i]), E));
             });
             const float2 reset = make_float2(kReset, kReset);
             pair(&fwd_a[w][c]) = starts ? reset : A;
@@ -621,24 +634,33 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
             __syncwarp();
             bd.mark<false>(t0 - t_step, next, ex.marks[(round + 1) & 1]);
             if (!CHANNEL) {
-                gates.store(ex.decays[(round + 1) & 1]);
+                gates.store(ex.decays[(round + 1) & 1], ex.products[(round + 1) & 1]);
                 gates.load(a, t0 - 2 * t_step, h);
             }
         }
         __syncthreads();
         // The segment's states are kept for kPart rows at a time, the last part
-        // first: from the states at the parts' first rows, which one walk over
-        // the segment gives, each part is walked again.
+        // first: from the states at the parts' first rows each part is walked
+        // again.
         constexpr int kParts = kSeg / kPart;
         float2 e = pair(&ex.seg_b[w][c]), at_part[kParts];
         {
             float2 s = pair(&fwd_b[w][c]);
             at_part[0] = s;
-            walk<0, kSeg - kPart - 1>(plain, [&](int i, auto checked) {
-                if (checked && (starts >> i & 1)) s = state_of(a.s0, first[i], width, hc);
-                s = d.fma(i, s, f2(x[i]));
-                if (i % kPart == kPart - 1) at_part[i / kPart + 1] = s;
-            });
+            if constexpr (CHANNEL) {
+                walk<0, kSeg - kPart - 1>(plain, [&](int i, auto checked) {
+                    if (checked && (starts >> i & 1)) s = state_of(a.s0, first[i], width, hc);
+                    s = fma2(d(i), s, f2(x[i]));
+                    if (i % kPart == kPart - 1) at_part[i / kPart + 1] = s;
+                });
+            } else {  // the parts' products are at hand: s is A s + what it would be from zero
+                float2 A = both(1.f);
+#pragma unroll
+                for (int k = 1; k < kParts; ++k) {
+                    A = mul2(A, d.part(k - 1));
+                    at_part[k] = starts & ((1u << (k * kPart)) - 1) ? to_part[k] : fma2(A, s, to_part[k]);
+                }
+            }
         }
         T *dx = static_cast<T *>(a.dx) + (long long)tw * width + hc;
         T *dgc = static_cast<T *>(a.dg) + (long long)tw * width + hc;  // per channel
@@ -648,13 +670,13 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
             walk<part * kPart, part * kPart + kPart - 1>(plain, [&](int i, auto checked) {
                 if (checked && (starts >> i & 1)) s = state_of(a.s0, first[i], width, hc);
                 before[i % kPart] = s;
-                s = d.fma(i, s, f2(x[i]));
+                s = fma2(d(i), s, f2(x[i]));
             });
             float sums[kPart];
             walk<part * kPart + kPart - 1, part * kPart>(plain, [&](int i, auto checked) {
                 if (checked && (ends >> i & 1)) e = state_of(a.dfinal, last[i], width, hc);
-                const float2 ds = __fadd2_rn(f2(dy[i]), e);
-                e = d.mul(i, ds);
+                const float2 ds = vec::add2(f2(dy[i]), e);
+                e = mul2(d(i), ds);
                 const float2 dg = mul2(e, before[i % kPart]);
                 if (!CHANNEL) sums[i % kPart] = dg.x + dg.y;
                 if (!checked || i < rows) {
