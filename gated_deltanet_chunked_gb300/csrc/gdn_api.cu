@@ -367,7 +367,6 @@ RecArgs linrec_args(const gdn_problem *p, const void *x, const void *g, const fl
     a.x = x; a.g = g; a.s0 = s0; a.cu = cu;
     a.total_tokens = p->total_tokens; a.num_seqs = p->num_seqs; a.hv = p->hv;
     a.dense_seqlen = cu ? 0 : p->seqlen;
-    a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     return a;
 }
 

@@ -112,7 +112,7 @@ struct Bounds {
         const int lane = threadIdx.x & 31, end = min(t0 + S::kRows, total);
         if (lane < S::kSegs) m.starts[lane] = m.ends[lane] = 0;
         __syncwarp();
-        if (t0 >= total) return;
+        if (t0 < 0 || t0 >= total) return;  // seqlen is not 0 where there are rows
         auto start_at = [&](int r, int seq) {
             if (r >= S::kRows || t0 + r >= total) return;
             atomicOr(&m.starts[r / S::kSeg], 1u << (r % S::kSeg));
@@ -124,7 +124,7 @@ struct Bounds {
             m.last[r] = seq;
         };
         if (!cu) {
-            for (long long k = (t0 + seqlen - 1) / seqlen + lane; k * seqlen <= end; k += 32) {
+            for (long long k = ((long long)t0 + seqlen - 1) / seqlen + lane; k * seqlen <= end; k += 32) {
                 const int r = int(k * seqlen) - t0;
                 start_at(r, int(k));
                 end_at(r - 1, int(k) - 1);
@@ -233,13 +233,14 @@ struct Segments {
 // in shared memory: moves `carry` (the value before the round) on to the next
 // round's; seg_b becomes the value that each segment starts from, which
 // at(segment, value) gets too. REVERSE: segments and CTAs from the last to the
-// first. ok turns false when a wait runs out (later ones are skipped). One
+// first. ok turns false when a wait runs out (2 s; later waits are skipped and no
+// more tiles are asked for: the rounds run out on what is there). One
 // thread a channel is the fewest instructions; the other warps have the
 // forward states of the backward pass, the next tiles' boundaries and gates
 // to see to meanwhile.
 template <bool REVERSE, typename S, typename F>
 __device__ __forceinline__ void exchange(Exchange<S> &ex, float &carry, int round, int rank, int ctas, bool &ok,
-                                         unsigned long long limit, F at) {
+                                         F at) {
     using namespace tc;
     const int ch = threadIdx.x, p = round & 1;
     if (threadIdx.x == 0) mbar_arrive_expect_tx(&ex.bar[p], uint32_t(ctas) * S::kCh * 8);
@@ -248,7 +249,7 @@ __device__ __forceinline__ void exchange(Exchange<S> &ex, float &carry, int roun
 #pragma unroll 4
     for (int r = 0; r < ctas; ++r)
         cluster_st_async(cluster_map(&ex.cta[p][rank][ch], r), mine.x, mine.y, cluster_map(&ex.bar[p], r));
-    if (ok && !mbar_wait_cluster(&ex.bar[p], uint32_t(round >> 1) & 1, limit)) ok = false;
+    if (ok && !mbar_wait_cluster(&ex.bar[p], uint32_t(round >> 1) & 1)) ok = false;
     float s = carry, in = carry;
 #pragma unroll 4
     for (int i = 0; i < ctas; ++i) {
@@ -297,8 +298,8 @@ struct Ring {
         if (CHANNEL) tc::tma_load_3d(const_cast<T *>(g(i)), mg, c0, h, t0, bar);
         if (BACKWARD) tc::tma_load_3d(const_cast<T *>(dout(i)), md, c0, h, t0, bar);
     }
-    __device__ __forceinline__ void wait(int i, bool &ok, unsigned long long limit) {
-        if (ok && !tc::mbar_wait(&full[i % kStages], uint32_t((i / kStages) & 1), limit)) ok = false;
+    __device__ __forceinline__ void wait(int i, bool &ok) {
+        if (ok && !tc::mbar_wait(&full[i % kStages], uint32_t((i / kStages) & 1))) ok = false;
     }
 };
 
@@ -436,14 +437,14 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     cluster_arrive();  // this CTA's barriers are ready
     bool ok = true;
     if (!offsets_ok(a)) {  // the same in every CTA: nothing is written
-        for (int i = 0; i < R::kStages && i < rounds; ++i) ring.wait(i, ok, a.wait_ns);
+        for (int i = 0; i < R::kStages && i < rounds; ++i) ring.wait(i, ok);
         cluster_wait();
         return;
     }
     const Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens};
     int next = 0;
     HeadGates<S::kRows> gates;
-    if (last_warp) {
+    if (last_warp && rounds) {
         bd.mark<true>(rank * S::kRows, next, ex.marks[0]);
         if (!CHANNEL) {
             gates.load(a, rank * S::kRows, h);
@@ -462,7 +463,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
         const Marks<S> &marks = ex.marks[round & 1];
         const uint32_t starts = marks.starts[w], ends = marks.ends[w];
         const int *first = marks.first + w * kSeg, *last = marks.last + w * kSeg;
-        ring.wait(round, ok, a.wait_ns);
+        ring.wait(round, ok);
         Pack<T, 2> x[kSeg];
         const int o = w * kSeg * S::kCh + c;
 #pragma unroll
@@ -483,14 +484,14 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
         __syncthreads();
         if (round == 0) cluster_wait();  // every CTA's barriers are ready
         if (threadIdx.x < S::kCh)
-            exchange<false>(ex, carry, round, rank, ctas, ok, a.wait_ns, [&](int seg, float s) {
+            exchange<false>(ex, carry, round, rank, ctas, ok, [&](int seg, float s) {
                 const int t = t0 + seg * kSeg;
                 if (seg % (kStateRows / kSeg) == 0 && a.states && t < a.total_tokens)
                     a.states[(long long)(t / kStateRows) * width + h * kHeadDim + c0 + threadIdx.x] = s;
             });
         if (last_warp && round + 1 < rounds) {
             // the tile is in registers: its stage takes a later one
-            if (feeder && round + R::kStages < rounds)
+            if (feeder && ok && round + R::kStages < rounds)
                 ring.load(round + R::kStages, &mx, &mg, nullptr, a, c0, h, t0 + R::kStages * ctas * S::kRows);
             __syncwarp();
             bd.mark<true>(t0 + ctas * S::kRows, next, ex.marks[(round + 1) & 1]);
@@ -552,14 +553,14 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     cluster_arrive();
     bool ok = true;
     if (!offsets_ok(a)) {
-        for (int i = 0; i < R::kStages && i < rounds; ++i) ring.wait(i, ok, a.wait_ns);
+        for (int i = 0; i < R::kStages && i < rounds; ++i) ring.wait(i, ok);
         cluster_wait();
         return;
     }
     const Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens};
     int next = a.num_seqs + 1;
     HeadGates<S::kRows> gates;
-    if (last_warp) {
+    if (last_warp && rounds) {  // without rows there is no first tile
         bd.mark<false>(t_first, next, ex.marks[0]);
         if (!CHANNEL) {
             gates.load(a, t_first, h);
@@ -586,7 +587,7 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         const uint32_t starts = marks.starts[w], ends = marks.ends[w];
         const int *first = marks.first + w * kSeg, *last = marks.last + w * kSeg;
         const bool plain = !(starts | ends) && rows == kSeg;
-        ring.wait(round, ok, a.wait_ns);
+        ring.wait(round, ok);
         const float state = ring.state(round)[threadIdx.x % S::kCh];  // unused where the tile starts a sequence
         Pack<T, 2> x[kSeg], dy[kSeg];
         const int o = w * kSeg * S::kCh + c;
@@ -618,13 +619,13 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
             pair(&ex.seg_b[w][c]) = E;
         }
         __syncthreads();
-        if (feeder && round + R::kStages < rounds)
+        if (feeder && ok && round + R::kStages < rounds)
             ring.load(round + R::kStages, &mx, &mg, &md, a, c0, h, t0 - R::kStages * t_step);
         if (!CHANNEL && round) write_head_sums((round - 1) & 1, t0 + t_step);
         if (round == 0) cluster_wait();
         __syncwarp();
         if (threadIdx.x < S::kCh) {
-            exchange<true>(ex, carry, round, rank, ctas, ok, a.wait_ns, [](int, float) {});
+            exchange<true>(ex, carry, round, rank, ctas, ok, [](int, float) {});
         } else if (threadIdx.x < 2 * S::kCh) {
             const int ch = threadIdx.x - S::kCh;
             Segments<S, false> sg(fwd_a, fwd_b, ch);

@@ -91,6 +91,17 @@ def test_dense_batch_is_the_packed_one(cuda, dtype, gate):
         assert torch.equal(v, dense[k].reshape(v.shape)), k
 
 
+@pytest.mark.parametrize("batch,seqlen", [(3, 0), (1, 1), (5, 7), (2, 128), (1, 3000), (40, 3)])
+def test_dense_batches(cuda, batch, seqlen):
+    lens = [seqlen] * batch
+    d = make(12, lens, 2, BF16, "channel", True)
+    c = to(d, cuda)
+    for k in ("x", "dout", "g"):
+        c[k] = c[k].reshape(batch, seqlen, 2, 128)
+    res = run(c, cu=None)
+    compare({k: v.reshape(sum(lens), 2, 128) if k in ("out", "dx", "dg") else v for k, v in res.items()}, d, lens, BF16)
+
+
 @DTYPES
 @GATES
 @pytest.mark.parametrize("mu", [-8.0, 4.0], ids=["slow_decay", "fast_decay"])
@@ -241,6 +252,39 @@ def test_same_bits_every_time_and_in_a_graph(cuda, gate):
     torch.cuda.synchronize()
     for k in fresh:
         assert torch.equal(captured[k], fresh[k]) and torch.equal(captured2[k], fresh[k]), k
+
+
+def test_two_calls_at_once(cuda):
+    """Two streams, no state in common: each gives what it gives alone."""
+    sets = [to(make(50 + i, lens, 4, BF16, gate, True), cuda)
+            for i, (lens, gate) in enumerate([([3000], "channel"), ([900, 0, 1200], "head")])]
+    alone = [run(d) for d in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for d, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append(run(d))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            for k in a:
+                assert torch.equal(a[k], b[k]), k
+    assert gdn.gdn_read_device_status() == gdn.GDN_OK
+
+
+def test_nan_gate_stays_in_its_channel(cuda):
+    lens = [200, 100]
+    d = make(53, lens, 2, BF16, "channel", True)
+    clean = run(to(d, cuda))
+    d["g"][50, 1, 7] = float("nan")
+    res = run(to(d, cuda))
+    keep = torch.ones(2, 128, dtype=torch.bool, device=cuda)
+    keep[1, 7] = False
+    for k in ("out", "dx", "dg"):
+        assert torch.equal(res[k][:, keep], clean[k][:, keep]), k
+        assert torch.equal(res[k][200:], clean[k][200:]), k
+    assert torch.isnan(res["out"][50:200, 1, 7]).all()
 
 
 def test_on_a_stream_given_by_the_caller(cuda):

@@ -100,6 +100,40 @@ def test_block_captured_into_a_graph(cuda):
         assert torch.equal(v, captured[k]), k
 
 
+FIRST_CALL_IN_A_GRAPH = """
+import sys
+sys.path[:0] = [{tests!r}, {root!r}]
+import torch
+from test_gpu_training_block import block, params
+from gated_deltanet_chunked_gb300 import gdn
+gdn.load()
+dev = torch.device("cuda:0")
+p = params(dev, [300, 0, 65], 3, torch.bfloat16)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    captured = block(p, gdn)
+g.replay()
+torch.cuda.synchronize()
+ref = block(p, gdn)
+torch.cuda.synchronize()
+assert all(torch.equal(v, captured[k]) for k, v in ref.items())
+print("same")
+"""
+
+
+def test_first_call_of_a_process_is_captured(cuda):
+    """Nothing has to be called before the capture (in a process of its own)."""
+    import os
+    import subprocess
+    import sys
+
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL_IN_A_GRAPH.format(tests=here, root=os.path.dirname(here))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
 def test_prefill_then_decode(cuda):
     """Two prompts of one packed prefill go on with decode steps on a slot
     cache; both parts together are the whole sequences."""
