@@ -276,6 +276,7 @@ struct Ring {
     static constexpr size_t kSmem = size_t(kStages) * kBytes + 128;
     uint8_t *base;
     uint64_t *full;
+    int asked = 0;  // tiles, by the issuing thread
 
     __device__ __forceinline__ const T *x(int i) const { return reinterpret_cast<const T *>(base + (i % kStages) * kBytes); }
     __device__ __forceinline__ const T *g(int i) const { return x(i) + kTile; }
@@ -289,6 +290,7 @@ struct Ring {
     __device__ __forceinline__ void load(int i, const CUtensorMap *mx, const CUtensorMap *mg, const CUtensorMap *md,
                                          const RecArgs &a, int c0, int h, int t0) {
         uint64_t *bar = &full[i % kStages];
+        asked = i + 1;
         const bool state = BACKWARD && t0 < a.total_tokens;
         tc::mbar_arrive_expect_tx(bar, state ? kBytes : kTiles);
         if (state)
@@ -300,6 +302,12 @@ struct Ring {
     }
     __device__ __forceinline__ void wait(int i, bool &ok) {
         if (ok && !tc::mbar_wait(&full[i % kStages], uint32_t((i / kStages) & 1))) ok = false;
+    }
+    // by the issuing thread, after a wait has run out: the last tiles asked for
+    // land (bounded too) before the CTA may exit
+    __device__ __forceinline__ void drain() {
+        for (int i = asked > kStages ? asked - kStages : 0; i < asked; ++i)
+            tc::mbar_wait(&full[i % kStages], uint32_t((i / kStages) & 1));
     }
 };
 
@@ -513,6 +521,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
             if (checked && a.final_state && (ends >> i & 1)) set_state(a.final_state, last[i], width, hc, s);
         });
     }
+    if (!ok && feeder) ring.drain();
     if (!ok && (threadIdx.x & 31) == 0) record_status(a.status, GDN_ETIMEOUT);
     if (!rounds) cluster_wait();
     cluster_arrive_relaxed();  // no CTA leaves while others may still store to it
@@ -716,6 +725,7 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         __syncthreads();
         write_head_sums((rounds - 1) & 1, rank * S::kRows);
     }
+    if (!ok && feeder) ring.drain();
     if (!ok && lane == 0) record_status(a.status, GDN_ETIMEOUT);
     if (!rounds) cluster_wait();
     cluster_arrive_relaxed();
