@@ -328,7 +328,7 @@ struct HeadGates {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int k = 0; k < ROWS / 32; k += 2) {
-            float2 d = vec::exp2_of(make_float2(g[k], g[k + 1]));
+            float2 d = vec::exp_exact2(make_float2(g[k], g[k + 1]));
             to[k * 32 + lane] = vec::both(d.x);
             to[(k + 1) * 32 + lane] = vec::both(d.y);
 #pragma unroll
@@ -345,7 +345,12 @@ struct HeadGates {
 };
 
 // Decays of a segment's rows for the lane's two channels: pairs of their own,
-// in registers, or the head's one value, in shared memory.
+// in registers, or the head's one value, in shared memory. A decay's error is
+// taken as often as the state remembers rows: gates per head (few) and f32
+// gates are exact to a rounding (state off by 2e-7 where it remembers 55 rows,
+// 7e-7 at 1000); for bf16 gates per channel that would cost 22% of the forward
+// pass's time (T = 65536 x 32 heads: 339 us against 278), and the base-2 unit's
+// two steps a decay are taken instead (6e-7 and 4e-6, against 2^-9 of out).
 template <typename T, bool CHANNEL, typename S>
 struct Decays;
 template <typename T, typename S>
@@ -356,7 +361,7 @@ struct Decays<T, true, S> {
         for (int i = 0; i < S::kSeg; ++i) {
             Pack<T, 2> p;
             p.load(g_tile + i * S::kCh);
-            d[i] = vec::exp2_of(p.f2(0));
+            d[i] = sizeof(T) == 4 ? vec::exp_exact2(p.f2(0)) : vec::exp2_of(p.f2(0));
         }
     }
     __device__ __forceinline__ float2 operator()(int i) const { return d[i]; }

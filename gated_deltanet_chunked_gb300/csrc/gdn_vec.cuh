@@ -76,6 +76,31 @@ __device__ __forceinline__ float2 exp2_of(float2 v) {
     return fma2(e, r, e);
 }
 
+// exp of two values to within a rounding of the last product: with n the
+// integer next to v log2 e, exp v = 2^n exp r for r = v - n ln 2 (ln 2 in two
+// parts, the first short enough that n times it is exact: the reduction of
+// Cody and Waite), |r| <= 0.35, where exp's Taylor polynomial of degree 7 is off
+// by 5e-9; 2^n is exact on the base-2 unit. NaN and underflow as exp2_of.
+__device__ __forceinline__ float2 exp_exact2(float2 v) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(v.x) : "f"(-200.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(v.y) : "f"(-200.f));
+    const float big = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+    const float2 n = add2(fma2(v, both(1.4426950408889634f), both(big)), both(-big));
+    const float ln2_hi = 0.693145751953125f, ln2_lo = 1.4286068203094173e-06f;  // 16 bits of ln 2, and the rest
+    const float2 r = fma2(n, both(-ln2_lo), fma2(n, both(-ln2_hi), v));
+    float2 p = fma2(r, both(1.f / 5040.f), both(1.f / 720.f));
+    p = fma2(p, r, both(1.f / 120.f));
+    p = fma2(p, r, both(1.f / 24.f));
+    p = fma2(p, r, both(1.f / 6.f));
+    p = fma2(p, r, both(0.5f));
+    p = fma2(p, r, both(1.f));
+    p = fma2(p, r, both(1.f));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(n.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(n.y));
+    return mul2(e, p);
+}
+
 // 1 / (1 + exp(-z)) of two values: below -88 as at -88 (less than the
 // smallest normal number)
 __device__ __forceinline__ float2 sigmoid2(float2 z) {
