@@ -147,12 +147,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _io_dtype(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
+def _io_type(dtype) -> int:
+    if dtype == torch.float32:
         return GDN_DT_F32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return GDN_DT_BF16
-    raise ValueError(f"unsupported io dtype {t.dtype}")
+    raise ValueError(f"unsupported io dtype {dtype}")
+
+
+def _io_dtype(t: torch.Tensor) -> int:
+    return _io_type(t.dtype)
 
 
 def _want(dtype, **tensors):
@@ -518,15 +522,15 @@ def _arg(name, t, dtype, shape, dev):
     shape, device and layout: ValueError before any call."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev} (the device of the first input)")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -548,24 +552,26 @@ def _current(dev) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
-def _linrec_layout(x, g, cu_seqlens):
+@functools.lru_cache(maxsize=1024)
+def _linrec_layout(shape, dtype, gate_dims, offsets):
     """(descriptor's reference, state shape, states shape, gate's type and
-    shape) of the recurrence on x [T, Hv, 128] or [B, T, Hv, 128]."""
-    packed = cu_seqlens is not None
-    if x.dim() != (3 if packed else 4):
+    shape) of the recurrence on x of ``shape``, [T, Hv, 128] with cu_seqlens of
+    shape ``offsets`` or [B, T, Hv, 128] with None."""
+    packed = offsets is not None
+    if len(shape) != (3 if packed else 4):
         raise ValueError("x must be [T, Hv, 128] with cu_seqlens, else [B, T, Hv, 128]")
-    if packed and cu_seqlens.dim() != 1:
+    if packed and len(offsets) != 1:
         raise ValueError("cu_seqlens must be a 1-D int32 tensor [N + 1]")
     if packed:
-        total, hv, dv = x.shape
-        batch, seqlen, num_seqs = 1, 0, cu_seqlens.shape[0] - 1
+        total, hv, dv = shape
+        batch, seqlen, num_seqs = 1, 0, offsets[0] - 1
     else:
-        batch, seqlen, hv, dv = x.shape
+        batch, seqlen, hv, dv = shape
         total, num_seqs = batch * seqlen, batch
-    channel = g.dim() == x.dim()
-    _, ref = _descriptor(batch, seqlen, num_seqs, total, hv, hv, dv, dv, _io_dtype(x),
+    channel = gate_dims == len(shape)
+    _, ref = _descriptor(batch, seqlen, num_seqs, total, hv, hv, dv, dv, _io_type(dtype),
                          GDN_FLAG_GATE_CHANNEL if channel else 0, 0)
-    gate = (x.dtype, x.shape) if channel else (torch.float32, x.shape[:-1])
+    gate = (dtype, shape) if channel else (torch.float32, shape[:-1])
     return ref, (num_seqs, hv, dv), ((total + 63) // 64, hv, dv), gate
 
 
@@ -585,7 +591,8 @@ def gdn_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, out=None, f
         with _launching(stream, dev):
             return gdn_linear_recurrence(x, g, initial_state, cu_seqlens, out, final_state, output_final_state,
                                          save_states, states)
-    ref, state_shape, states_shape, gate = _linrec_layout(x, g, cu_seqlens)
+    ref, state_shape, states_shape, gate = _linrec_layout(
+        x.shape, x.dtype, g.dim(), None if cu_seqlens is None else cu_seqlens.shape)
     f32 = torch.float32
     px = _arg("x", x, x.dtype, x.shape, dev)
     pg = _arg("g", g, *gate, dev)
@@ -596,7 +603,7 @@ def gdn_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, out=None, f
     pst = _arg("states", states, f32, states_shape, dev)
     handle = _current(dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty_like(x)
         po = out.data_ptr()
     if final_state is None and output_final_state:
         final_state = torch.empty(state_shape, dtype=f32, device=dev)
@@ -623,7 +630,8 @@ def gdn_linear_recurrence_bwd(dout, x, g, states, initial_state=None, cu_seqlens
                                              dinitial_state)
     if states is None:
         raise ValueError("the backward pass needs the forward pass's states (save_states=True)")
-    ref, state_shape, states_shape, gate = _linrec_layout(x, g, cu_seqlens)
+    ref, state_shape, states_shape, gate = _linrec_layout(
+        x.shape, x.dtype, g.dim(), None if cu_seqlens is None else cu_seqlens.shape)
     f32 = torch.float32
     px = _arg("x", x, x.dtype, x.shape, dev)
     pdo = _arg("dout", dout, x.dtype, x.shape, dev)
@@ -637,10 +645,10 @@ def gdn_linear_recurrence_bwd(dout, x, g, states, initial_state=None, cu_seqlens
     pd0 = _arg("dinitial_state", dinitial_state, f32, state_shape, dev)
     handle = _current(dev)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = torch.empty_like(x)
         pdx = dx.data_ptr()
     if dg is None:
-        dg = torch.empty(g.shape, dtype=g.dtype, device=dev)
+        dg = torch.empty_like(g)
         pdg = dg.data_ptr()
     if dinitial_state is None and initial_state is not None:
         dinitial_state = torch.empty(state_shape, dtype=f32, device=dev)
@@ -672,7 +680,7 @@ def gdn_linear_recurrence_step(x, g, state, state_indices=None, out=None, stream
     _, ref = _descriptor(N, 1, N, N, hv, hv, dv, dv, _io_dtype(x), GDN_FLAG_GATE_CHANNEL if channel else 0, slots)
     handle = _current(dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty_like(x)
         po = out.data_ptr()
     st = load().gdn_linear_recurrence_step(ref, px, pg, ps, pi, po, handle)
     if st != GDN_OK:
@@ -680,15 +688,15 @@ def gdn_linear_recurrence_step(x, g, state, state_indices=None, out=None, stream
     return out
 
 
-def _rows_descriptor(x):
-    """(descriptor's reference, leading shape, width) of a row-wise norm over the last dimension of x."""
-    if x.dim() < 1 or x.shape[-1] < 1:
+@functools.lru_cache(maxsize=1024)
+def _rows_descriptor(shape, dtype):
+    """(descriptor's reference, leading shape, width) of a row-wise norm over the last dimension."""
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("the last dimension must not be empty")
-    width = x.shape[-1]
-    rows = x.numel() // width
+    width, rows = shape[-1], shape[:-1].numel()
     if rows >= 1 << 31:
         raise ValueError("too many rows")
-    return _descriptor(1, 0, 1, rows, 1, 1, width, width, _io_dtype(x), 0, 0)[1], x.shape[:-1], width
+    return _descriptor(1, 0, 1, rows, 1, 1, width, width, _io_type(dtype), 0, 0)[1], shape[:-1], width
 
 
 def gdn_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, save_stats=False, mean=None, rstd=None,
@@ -701,7 +709,7 @@ def gdn_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, save_stats=Fals
     if _elsewhere(dev, stream):
         with _launching(stream, dev):
             return gdn_layernorm(x, weight, bias, eps, out, save_stats, mean, rstd)
-    ref, lead, width = _rows_descriptor(x)
+    ref, lead, width = _rows_descriptor(x.shape, x.dtype)
     f32 = torch.float32
     px = _arg("x", x, x.dtype, x.shape, dev)
     pw = _arg("weight", weight, f32, (width,), dev)
@@ -711,14 +719,14 @@ def gdn_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, save_stats=Fals
     pr = _arg("rstd", rstd, f32, lead, dev)
     handle = _current(dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty_like(x)
         po = out.data_ptr()
     if save_stats:
         if mean is None:
             mean = torch.empty(lead, dtype=f32, device=dev)
             pm = mean.data_ptr()
         if rstd is None:
-            rstd = torch.empty(lead, dtype=f32, device=dev)
+            rstd = torch.empty_like(mean)
             pr = rstd.data_ptr()
     st = load().gdn_layernorm(ref, px, pw, pb, eps, po, pm, pr, handle)
     if st != GDN_OK:
@@ -748,7 +756,7 @@ def gdn_layernorm_bwd(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbi
         with _launching(stream, dev):
             return gdn_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, need_dweight, need_dbias,
                                      workspace)
-    ref, lead, width = _rows_descriptor(x)
+    ref, lead, width = _rows_descriptor(x.shape, x.dtype)
     f32 = torch.float32
     px = _arg("x", x, x.dtype, x.shape, dev)
     pdy = _arg("dy", dy, x.dtype, x.shape, dev)
@@ -760,7 +768,7 @@ def gdn_layernorm_bwd(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbi
     pdb = _arg("dbias", dbias, f32, (width,), dev)
     handle = _current(dev)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = torch.empty_like(x)
         pdx = dx.data_ptr()
     if dweight is None and need_dweight:
         dweight = torch.empty(width, dtype=f32, device=dev)
@@ -802,10 +810,10 @@ def gdn_gated_rmsnorm_bwd(dy, o, z, weight, eps, do=None, dz=None, dweight=None,
     _, ref = _descriptor(1, 0, 1, T, 1, hv, dv, dv, _io_dtype(o), 0, 0)
     handle = _current(dev)
     if do is None:
-        do = torch.empty(shape, dtype=io, device=dev)
+        do = torch.empty_like(o)
         pdo = do.data_ptr()
     if dz is None:
-        dz = torch.empty(shape, dtype=io, device=dev)
+        dz = torch.empty_like(o)
         pdz = dz.data_ptr()
     if dweight is None and need_dweight:
         dweight = torch.empty(dv, dtype=f32, device=dev)
