@@ -22,6 +22,7 @@ struct LnBwdArgs {
     const float *mean, *rstd, *weight;
     void *dx;
     float *dw_part, *db_part;  // [gridDim.x, width] each, or null
+    bool sums;                 // whether either is wanted
     int rows, width;
 };
 
@@ -155,18 +156,21 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
         one_row(even, red[kWide ? turn : 0]);
         if (!kWide && base + at.step < a.rows) one_row(odd, red[1]);
     }
-    if (!a.dw_part) return;
-    float *dwp = a.dw_part + (long long)blockIdx.x * a.width, *dbp = a.db_part + (long long)blockIdx.x * a.width;
+    if (!a.sums) return;
+    float *dwp = a.dw_part ? a.dw_part + (long long)blockIdx.x * a.width : nullptr;
+    float *dbp = a.db_part ? a.db_part + (long long)blockIdx.x * a.width : nullptr;
     if (!G && ALIGNED) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!at.full(i)) continue;
 #pragma unroll
             for (int j = 0; j < VE; j += 4) {
-                *reinterpret_cast<float4 *>(dwp + at.col[i] + j) =
-                    make_float4(dw.get(i, j), dw.get(i, j + 1), dw.get(i, j + 2), dw.get(i, j + 3));
-                *reinterpret_cast<float4 *>(dbp + at.col[i] + j) =
-                    make_float4(db.get(i, j), db.get(i, j + 1), db.get(i, j + 2), db.get(i, j + 3));
+                if (dwp)
+                    *reinterpret_cast<float4 *>(dwp + at.col[i] + j) =
+                        make_float4(dw.get(i, j), dw.get(i, j + 1), dw.get(i, j + 2), dw.get(i, j + 3));
+                if (dbp)
+                    *reinterpret_cast<float4 *>(dbp + at.col[i] + j) =
+                        make_float4(db.get(i, j), db.get(i, j + 1), db.get(i, j + 2), db.get(i, j + 3));
             }
         }
     } else if (!G) {
@@ -174,12 +178,14 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
         float *line = reinterpret_cast<float *>(smem);
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
+            float *out = pass ? dbp : dwp;
+            if (!out) continue;
             if (kWide) {  // which holds the sums: no room for a line
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int j = 0; j < VE; ++j)
-                        if (at.has(i, j)) (pass ? dbp : dwp)[at.col[i] + j] = pass ? db.get(i, j) : dw.get(i, j);
+                        if (at.has(i, j)) out[at.col[i] + j] = pass ? db.get(i, j) : dw.get(i, j);
                 continue;
             }
             __syncthreads();
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
                 for (int j = 0; j < VE; ++j)
                     if (at.has(i, j)) line[at.col[i] + j] = pass ? db.get(i, j) : dw.get(i, j);
             __syncthreads();
-            for (int c = threadIdx.x; c < a.width; c += blockDim.x) (pass ? dbp : dwp)[c] = line[c];
+            for (int c = threadIdx.x; c < a.width; c += blockDim.x) out[c] = line[c];
         }
     } else {
         // the CTA's row groups, added in order; one of the two sums at a time
@@ -207,6 +213,7 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
                     if (at.has(i, j)) part[group * kCols + at.col[i] + j] = pass ? db.get(i, j) : dw.get(i, j);
             __syncthreads();
             float *out = pass ? dbp : dwp;
+            if (!out) continue;
             for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
                 float t = 0.f;
 #pragma unroll
@@ -231,7 +238,7 @@ size_t workspace_of(int rows, int width) {
 template <typename T, int NV, int G, bool ALIGNED>
 struct Run {
     template <int MT>
-    static cudaError_t go(const ln::Shape &sh, LnBwdArgs &a, bool sums, int &parts, cudaStream_t s) {
+    static cudaError_t go(const ln::Shape &sh, LnBwdArgs &a, int &parts, cudaStream_t s) {
         const auto fn = k_layernorm_bwd<T, NV, G, ALIGNED, MT>;
         struct Key;
         const size_t smem = ln::Feed<T, 2, NV, G, ALIGNED, MT != 1024>::smem(sh.threads) +
@@ -244,16 +251,16 @@ struct Run {
         long long most = (long long)ln::kSms * ln::ctas_per_sm<Key>(reinterpret_cast<const void *>(fn), sh.threads, smem);
         if (most > max_parts(sh.threads)) most = max_parts(sh.threads);
         // few rows: four at least a CTA, which writes two f32 rows of sums, while every SM has two CTAs
-        if (sums && ctas < 4 * most) most = ctas / 4 > 2 * ln::kSms ? ctas / 4 / 8 * 8 : 2 * ln::kSms;
+        if (a.sums && ctas < 4 * most) most = ctas / 4 > 2 * ln::kSms ? ctas / 4 / 8 * 8 : 2 * ln::kSms;
         parts = int(ctas < most ? ctas : most);
-        if (sums) a.db_part = a.dw_part + size_t(parts) * a.width;
+        if (a.dw_part && a.db_part) a.db_part = a.dw_part + size_t(parts) * a.width;
         fn<<<unsigned(parts), sh.threads, smem, s>>>(a);
         return cudaGetLastError();
     }
-    static cudaError_t run(const ln::Shape &sh, LnBwdArgs &a, bool sums, int &parts, cudaStream_t s) {
+    static cudaError_t run(const ln::Shape &sh, LnBwdArgs &a, int &parts, cudaStream_t s) {
         // more than 512 threads only with the most elements a thread
         constexpr int kMost = !G && NV * 16 / int(sizeof(T)) >= 16 ? 1024 : 512;
-        return sh.threads <= 512 ? go<512>(sh, a, sums, parts, s) : go<kMost>(sh, a, sums, parts, s);
+        return sh.threads <= 512 ? go<512>(sh, a, parts, s) : go<kMost>(sh, a, parts, s);
     }
 };
 
@@ -299,15 +306,16 @@ size_t layernorm_bwd_workspace(int rows, int width, int io_dtype) {
 cudaError_t launch_layernorm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
                                  const float *weight, void *dx, float *dweight, float *dbias, void *workspace,
                                  int rows, int width, int io_dtype, cudaStream_t s) {
-    const bool sums = dweight || dbias;
     int parts = 0;
-    LnBwdArgs a{dy, x, mean, rstd, weight, dx, sums ? static_cast<float *>(workspace) : nullptr, nullptr, rows, width};
+    float *ws = static_cast<float *>(workspace);
+    LnBwdArgs a{dy,   x,    mean, rstd, weight, dx, dweight ? ws : nullptr, dbias ? ws : nullptr, dweight || dbias,
+                rows, width};
     if (rows > 0) {
         LaunchScope scope(GDN_K_LAYERNORM_BWD, s);
         const cudaError_t e =
             io_dtype == GDN_DT_BF16
-                ? ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(rows, width), a, sums, parts, s)
-                : ln::dispatch<float, Run>(ln::shape_of<float>(rows, width), a, sums, parts, s);
+                ? ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(rows, width), a, parts, s)
+                : ln::dispatch<float, Run>(ln::shape_of<float>(rows, width), a, parts, s);
         if (e != cudaSuccess) return e;
     }
     return launch_row_sums(a.dw_part, a.db_part, parts, width, dweight, dbias, s);

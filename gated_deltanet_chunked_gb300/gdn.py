@@ -533,6 +533,13 @@ def _arg(name, t, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _first(name, t):
+    """Address of the tensor that the others are checked against."""
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 @functools.lru_cache(maxsize=1024)
 def _descriptor(*fields):
     """A problem descriptor and the reference that calls take (never written to)."""
@@ -594,7 +601,7 @@ def gdn_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, out=None, f
     ref, state_shape, states_shape, gate = _linrec_layout(
         x.shape, x.dtype, g.dim(), None if cu_seqlens is None else cu_seqlens.shape)
     f32 = torch.float32
-    px = _arg("x", x, x.dtype, x.shape, dev)
+    px = _first("x", x)
     pg = _arg("g", g, *gate, dev)
     ps0 = _arg("initial_state", initial_state, f32, state_shape, dev)
     pcu = _arg("cu_seqlens", cu_seqlens, torch.int32, (state_shape[0] + 1,), dev)
@@ -633,7 +640,7 @@ def gdn_linear_recurrence_bwd(dout, x, g, states, initial_state=None, cu_seqlens
     ref, state_shape, states_shape, gate = _linrec_layout(
         x.shape, x.dtype, g.dim(), None if cu_seqlens is None else cu_seqlens.shape)
     f32 = torch.float32
-    px = _arg("x", x, x.dtype, x.shape, dev)
+    px = _first("x", x)
     pdo = _arg("dout", dout, x.dtype, x.shape, dev)
     pg = _arg("g", g, *gate, dev)
     pst = _arg("states", states, f32, states_shape, dev)
@@ -672,7 +679,7 @@ def gdn_linear_recurrence_step(x, g, state, state_indices=None, out=None, stream
     N, hv, dv = x.shape
     slots = state.shape[0]
     channel = g.dim() == 3
-    px = _arg("x", x, x.dtype, x.shape, dev)
+    px = _first("x", x)
     pg = _arg("g", g, x.dtype if channel else torch.float32, x.shape if channel else (N, hv), dev)
     ps = _arg("state", state, torch.float32, (slots, hv, dv), dev)
     pi = _arg("state_indices", state_indices, torch.int32, (N,), dev)
@@ -711,7 +718,7 @@ def gdn_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, save_stats=Fals
             return gdn_layernorm(x, weight, bias, eps, out, save_stats, mean, rstd)
     ref, lead, width = _rows_descriptor(x.shape, x.dtype)
     f32 = torch.float32
-    px = _arg("x", x, x.dtype, x.shape, dev)
+    px = _first("x", x)
     pw = _arg("weight", weight, f32, (width,), dev)
     pb = _arg("bias", bias, f32, (width,), dev)
     po = _arg("out", out, x.dtype, x.shape, dev)
@@ -758,7 +765,7 @@ def gdn_layernorm_bwd(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbi
                                      workspace)
     ref, lead, width = _rows_descriptor(x.shape, x.dtype)
     f32 = torch.float32
-    px = _arg("x", x, x.dtype, x.shape, dev)
+    px = _first("x", x)
     pdy = _arg("dy", dy, x.dtype, x.shape, dev)
     pm = _arg("mean", mean, f32, lead, dev)
     pr = _arg("rstd", rstd, f32, lead, dev)
@@ -800,7 +807,7 @@ def gdn_gated_rmsnorm_bwd(dy, o, z, weight, eps, do=None, dz=None, dweight=None,
         raise ValueError("o must be [T, Hv, 128]")
     T, hv, dv = shape = o.shape
     f32, io = torch.float32, o.dtype
-    po = _arg("o", o, io, shape, dev)
+    po = _first("o", o)
     pdy = _arg("dy", dy, io, shape, dev)
     pz = _arg("z", z, io, shape, dev)
     pw = _arg("weight", weight, f32, (dv,), dev)

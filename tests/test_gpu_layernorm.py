@@ -119,6 +119,21 @@ def test_leading_dimensions_and_parts_of_the_answer(cuda):
     assert torch.equal(one, ref["y"][5])
 
 
+@DTYPES
+@pytest.mark.parametrize("width", [7, 128, 1001, 2048, 8192, 16383, 16384])
+def test_one_of_the_two_sums(cuda, width, dtype):
+    """Each sum alone has the bits that it has next to the other."""
+    d = make(12, 41, width, dtype)
+    ref = run(d, cuda)
+    c = {k: v.to(cuda) for k, v in d.items()}
+    for need_dw, need_db in ((True, False), (False, True)):
+        dx, dw, db = gdn.gdn_layernorm_bwd(c["dy"], c["x"], ref["mean"], ref["rstd"], c["w"], need_dweight=need_dw,
+                                           need_dbias=need_db)
+        assert torch.equal(dx, ref["dx"])
+        assert torch.equal(dw, ref["dweight"]) if need_dw else dw is None
+        assert torch.equal(db, ref["dbias"]) if need_db else db is None
+
+
 def test_no_rows(cuda):
     x = torch.empty(0, 300, device=cuda)
     y, mean, rstd = gdn.gdn_layernorm(x, save_stats=True)
