@@ -224,23 +224,28 @@ __device__ __forceinline__ void cluster_st_async(uint32_t addr, float a, float b
                  : "memory");
 }
 
-// Bounded wait for a phase that stores of the cluster's other CTAs complete.
+// Bounded wait for a phase that stores of the cluster's other CTAs into this
+// one's shared memory complete. Only shared memory is acquired: an acquire of
+// all memory at cluster scope also drops what the SM has cached of global
+// memory and waits meanwhile.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t limit_ns = 2000000000ull) {
     auto done = [&] {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
             : "r"(smem_u32(bar)), "r"(parity)
             : "memory");
         return ok != 0;
     };
-    if (done()) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!done())
-        if (globaltimer_ns() - t0 > limit_ns) return false;
+    if (!done()) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!done())
+            if (globaltimer_ns() - t0 > limit_ns) return false;
+    }
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
     return true;
 }
 
