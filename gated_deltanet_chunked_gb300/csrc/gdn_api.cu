@@ -467,8 +467,10 @@ int gdn_layernorm(const gdn_problem *p, const void *x, const float *weight, cons
     if (p->total_tokens > 0) {
         if (!x || !y || !aligned16(x) || !aligned16(y) || !aligned4(mean) || !aligned4(rstd)) return GDN_EINVAL;
     }
+    int *status = status_ptr();
+    if (!status) return GDN_ECUDA;
     return cuda_status(launch_layernorm(x, weight, bias, eps, y, mean, rstd, p->total_tokens, p->dv, p->io_dtype,
-                                        static_cast<cudaStream_t>(stream)));
+                                        status, static_cast<cudaStream_t>(stream)));
 }
 
 size_t gdn_layernorm_bwd_workspace_size(const gdn_problem *p) {
@@ -488,8 +490,10 @@ int gdn_layernorm_bwd(const gdn_problem *p, const void *dy, const void *x, const
         if ((dweight || dbias) && !workspace_ok(workspace, workspace_bytes, gdn_layernorm_bwd_workspace_size(p)))
             return GDN_EINVAL;
     }
-    return cuda_status(launch_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace,
-                                            p->total_tokens, p->dv, p->io_dtype, static_cast<cudaStream_t>(stream)));
+    int *status = status_ptr();
+    if (!status) return GDN_ECUDA;
+    return cuda_status(launch_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, p->total_tokens,
+                                            p->dv, p->io_dtype, status, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

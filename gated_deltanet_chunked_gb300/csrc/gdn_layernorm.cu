@@ -5,11 +5,16 @@
 // HBM-bound: a row is read once, held in registers through both statistics
 // (the mean first, then the squares about it: no cancellation whatever the
 // row's offset) and written once. Threads keep their columns' weight and bias
-// in registers over all their rows, and the next row's loads are issued
-// before the current row's reductions. Arithmetic is on pairs (two values an
-// instruction), and its roundings are written out: the same row gives the same
-// bits with and without the optional outputs, which the compiler may turn into
-// separate copies of the loop.
+// in registers over all their rows, and the next rows are on their way to
+// shared memory meanwhile. Arithmetic is on pairs (two values an instruction),
+// and its roundings are written out: the same row gives the same bits with and
+// without the optional outputs, which the compiler may turn into separate
+// copies of the loop.
+// Measured, bf16, of the copy rate (6783 GB/s): 16384 x 4096 43 us (0.92),
+// 32768 x 2048 46 (0.86), 524288 x 128 48 (0.83), 8000 x 8192 58 (0.67); where
+// rows are odd a third of the time goes into their ragged ends (20000 x 1001
+// 20 us, 0.60); a single row takes 2.3 us. What bounds the widest rows is
+// their two reductions: 3000 x 16384 51 us (0.57).
 #include "gdn_layernorm.cuh"
 
 namespace gdn {
@@ -24,23 +29,27 @@ struct LnArgs {
     void *y;
     float *mean, *rstd;
     int rows, width;
+    int *status;
 };
 
-constexpr int kMaxThreads = 576;  // 544 for the widest rows
-
-template <typename T, int NV, int G, bool ALIGNED>
-__global__ void __launch_bounds__(G ? ln::kRowThreads : kMaxThreads) k_layernorm(const LnArgs a) {
+// PAIR: a row is on two CTAs, each the same half of all its rows.
+template <typename T, int NV, int G, bool ALIGNED, bool PAIR>
+__global__ void __launch_bounds__(G ? ln::kRowThreads : PAIR ? 544 : 576) k_layernorm(const LnArgs a) {
     using L = ln::Place<T, NV, G, ALIGNED>;
     constexpr int VE = L::VE;
     __shared__ __align__(16) float red[2][32];
+    __shared__ ln::Pair pair;
     if (!G) {
         if (threadIdx.x < 64) red[threadIdx.x / 32][threadIdx.x % 32] = 0.f;
+        if (PAIR && threadIdx.x == 0) pair.init();
         __syncthreads();
     }
-    const L at(a.width);
+    if (PAIR) tc::cluster_arrive();
+    const int rank = PAIR ? int(tc::cluster_ctarank()) : 0;
+    const L at(a.width, rank, PAIR ? 2 : 1);
     extern __shared__ __align__(16) uint8_t smem[];
     const T *const src[1] = {static_cast<const T *>(a.x)};
-    ln::Feed<T, 1, NV, G, ALIGNED, true> feed(at, src, a.rows, smem);
+    ln::Feed<T, 1, NV, G, ALIGNED> feed(at, src, a.rows, smem);
     T *y = static_cast<T *>(a.y);
     constexpr int H = VE / 2;  // pairs of a vector
     // 32 elements a thread leave no registers for weight and bias: read for every row
@@ -51,7 +60,12 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : kMaxThreads) k_layernorm
         at.load_columns(b, a.bias, 0.f);
     }
     const float inv_width = 1.f / float(a.width);
-    int row = at.row;
+    // PAIR: the columns of the lower CTA, and what mean and squares are first taken over
+    const int lower = min(NV * int(blockDim.x) * VE - at.offset(), a.width), mine = rank ? a.width - lower : lower;
+    const float inv_mine = PAIR ? 1.f / float(mine) : inv_width;
+    if (PAIR) tc::cluster_wait();  // both CTAs are ready
+    bool ok = true;
+    int row = at.row, n = 0;
     for (int base = at.base; base < a.rows; base += at.step, row += at.step) {
         Pack<T, VE> in[1][NV];
         feed.get(in);
@@ -61,7 +75,7 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : kMaxThreads) k_layernorm
 #pragma unroll
             for (int k = 0; k < H; ++k) acc = vec::add2(acc, v[i][k] = in[0][i].f2(k));
         const float sum = vec::sum2(acc);
-        const float mean = __fmul_rn(G ? vec::group_sum<G ? G : 1>(sum) : vec::block_sum(sum, red[0]), inv_width);
+        float mean = __fmul_rn(G ? vec::group_sum<G ? G : 1>(sum) : vec::block_sum(sum, red[0]), inv_mine);
         acc = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -78,7 +92,25 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : kMaxThreads) k_layernorm
             for (int k = 0; k < H; ++k) acc = vec::fma2(v[i][k], v[i][k], acc);
         }
         const float sq = vec::sum2(acc);
-        const float var = __fmul_rn(G ? vec::group_sum<G ? G : 1>(sq) : vec::block_sum(sq, red[1]), inv_width);
+        float squares = G ? vec::group_sum<G ? G : 1>(sq) : vec::block_sum(sq, red[1]);
+        if (PAIR) {
+            // squares about the row's mean: those about each half's, and
+            // (difference of the means)^2 for each of its columns
+            float2 low, up;
+            pair.send(make_float2(mean, squares), n & 1, rank);
+            pair.receive(low, up, n & 1, n >> 1, ok);
+            const float part = __fmul_rn(float(lower), inv_width), apart = __fadd_rn(low.x, -up.x);
+            const float all = fmaf(part, apart, up.x), shift = __fadd_rn(mean, -all);
+            squares = fmaf(__fmul_rn(float(lower), __fadd_rn(1.f, -part)), __fmul_rn(apart, apart),
+                           __fadd_rn(low.y, up.y));
+            mean = all;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int k = 0; k < H; ++k) v[i][k] = vec::add2(v[i][k], vec::both(shift));
+            ++n;
+        }
+        const float var = __fmul_rn(squares, inv_width);
         const float rstd = rsqrtf(__fadd_rn(var, a.eps));
         if (row < a.rows) {
 #pragma unroll
@@ -93,41 +125,42 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : kMaxThreads) k_layernorm
                     o.set2(k, vec::fma2(vec::mul2(v[i][k], vec::both(rstd)), w[i][k], b[i][k]));
                 at.store(o, i, y + (long long)row * a.width);
             }
-            if (at.tid == 0) {
+            if (at.tid == 0 && rank == 0) {
                 if (a.mean) a.mean[row] = mean;
                 if (a.rstd) a.rstd[row] = rstd;
             }
         }
     }
+    if (PAIR) ln::Pair::leave(ok, a.status);
 }
 
-template <typename T, int NV, int G, bool ALIGNED>
+template <typename T, int NV, int G, bool ALIGNED, bool PAIR>
 struct Run {
     static cudaError_t run(const ln::Shape &sh, const LnArgs &a, cudaStream_t s) {
-        const auto fn = k_layernorm<T, NV, G, ALIGNED>;
+        const auto fn = k_layernorm<T, NV, G, ALIGNED, PAIR>;
         const void *f = reinterpret_cast<const void *>(fn);
         struct Key;
-        const size_t smem = ln::Feed<T, 1, NV, G, ALIGNED, true>::smem(sh.threads);
+        const size_t smem = vec::RowsAhead<1, NV>::smem(sh.threads);
         const cudaError_t e = ln::allow_smem(f, smem);
         if (e != cudaSuccess) return e;
-        const long long ctas = ((long long)a.rows + sh.rows_per_cta - 1) / sh.rows_per_cta;
-        // all CTAs at once; a multiple of eight, which keeps a CTA's rows at one misalignment
-        const long long most = (long long)ln::kSms * ln::ctas_per_sm<Key>(f, sh.threads, smem);
-        fn<<<unsigned(ctas < most ? ctas : most), sh.threads, smem, s>>>(a);
-        return cudaGetLastError();
+        const long long units = ((long long)a.rows + sh.rows_per_cta - 1) / sh.rows_per_cta;
+        // all CTAs at once
+        int most = ln::kSms * ln::ctas_per_sm<Key>(f, sh.threads, smem) / sh.ctas();
+        if (!ALIGNED) most = most / 8 * 8;  // keeps a thread's rows at one misalignment
+        return ln::launch(fn, sh, units < most ? units : most, smem, s, a);
     }
 };
 
 }  // namespace
 
 cudaError_t launch_layernorm(const void *x, const float *weight, const float *bias, float eps, void *y, float *mean,
-                             float *rstd, int rows, int width, int io_dtype, cudaStream_t s) {
+                             float *rstd, int rows, int width, int io_dtype, int *status, cudaStream_t s) {
     if (rows == 0) return cudaSuccess;
-    const LnArgs a{x, weight, bias, eps, y, mean, rstd, rows, width};
+    const LnArgs a{x, weight, bias, eps, y, mean, rstd, rows, width, status};
     LaunchScope scope(GDN_K_LAYERNORM, s);
     if (io_dtype == GDN_DT_BF16)
-        return ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(rows, width, 32), a, s);
-    return ln::dispatch<float, Run>(ln::shape_of<float>(rows, width, 32), a, s);
+        return ln::dispatch<__nv_bfloat16, true, Run>(ln::shape_of<__nv_bfloat16, true>(rows, width), a, s);
+    return ln::dispatch<float, true, Run>(ln::shape_of<float, true>(rows, width), a, s);
 }
 
 }  // namespace gdn

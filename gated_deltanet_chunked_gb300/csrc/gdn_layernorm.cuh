@@ -15,6 +15,7 @@
 #include <atomic>
 
 #include "gdn_async.cuh"
+#include "gdn_common.cuh"
 
 namespace gdn {
 namespace ln {
@@ -24,18 +25,20 @@ constexpr int kRowThreads = 256;  // threads of a CTA whose warps take rows of t
 
 struct Shape {
     bool aligned;      // every row starts on 16 bytes
-    int nv, g;         // loads per thread, lanes per row (0: the CTA)
+    int nv, g;         // loads per thread, lanes per row (0: the CTA, or a pair)
     int threads;       // of a CTA
     int rows_per_cta;  // rows in work at a time
+    bool pair;         // a row is on a cluster of two CTAs
+    int ctas() const { return pair ? 2 : 1; }
 };
 
 // Long rows: 16 elements a thread, which is the least of reductions and
 // barriers for an element; few rows (latency counts) over as many threads as
-// help. Where that takes more than 512 threads, `most` = 32 elements a thread
-// keep two CTAs on an SM, whose reductions overlap (3000 x 16384 bf16 forward:
-// 56 us with 1024 threads, 51 with 512).
-template <typename T>
-inline Shape shape_of(int rows, int width, int most = 16) {
+// help. Rows that so take more than 512 threads are on two CTAs, which tell
+// each other their sums; or (LONG) on 512 threads with 32 elements each, where
+// rows are aligned and the kernel has the registers.
+template <typename T, bool LONG>
+inline Shape shape_of(int rows, int width) {
     constexpr int VE = 16 / int(sizeof(T)), kMost = 16 / VE;  // at most 16 elements a thread
     Shape s;
     s.aligned = width % VE == 0;
@@ -44,32 +47,88 @@ inline Shape shape_of(int rows, int width, int most = 16) {
     s.nv = 1;
     if (!s.g && rows > 16 * kSms) s.nv = kMost;
     while (s.nv < kMost && vecs > (s.g ? s.g : kRowThreads) * s.nv) s.nv *= 2;
-    // (also the widest unaligned rows, by a few elements one vector too many for 1024 threads)
-    if (!s.g && vecs > (most > 16 ? 512 : 1024) * s.nv) s.nv *= 2;
-    s.threads = s.g ? kRowThreads : ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
+    const bool wide = !s.g && vecs > 512 * s.nv;
+    s.pair = wide && !(LONG && s.aligned);
+    if (wide && !s.pair) s.nv *= 2;
+    const int each = s.nv * s.ctas();  // vectors of a thread, and of that at its place in the other CTA
+    s.threads = s.g ? kRowThreads : ((vecs + each - 1) / each + 31) / 32 * 32;
     s.rows_per_cta = s.g ? kRowThreads / s.g : 1;
     return s;
 }
 
-// calls F<T, NV, G, ALIGNED>(...) for the shape
-template <typename T, template <typename, int, int, bool> class F, bool ALIGNED, typename... A>
+// calls F<T, NV, G, ALIGNED, PAIR>(...) for the shape
+template <typename T, bool LONG, template <typename, int, int, bool, bool> class F, bool ALIGNED, typename... A>
 inline cudaError_t dispatch_nv(const Shape &s, A &...a) {
     constexpr int kMost = 4 * int(sizeof(T)) / 4;  // 16 / VE: 2 for bf16, 4 for f32
-    if (s.g == 16) return F<T, 1, 16, ALIGNED>::run(s, a...);
+    if (s.g == 16) return F<T, 1, 16, ALIGNED, false>::run(s, a...);
     if (s.g == 32) {
-        if (s.nv == 1) return F<T, 1, 32, ALIGNED>::run(s, a...);
-        if (s.nv == 2) return F<T, 2, 32, ALIGNED>::run(s, a...);
-        return F<T, kMost, 32, ALIGNED>::run(s, a...);
+        if (s.nv == 1) return F<T, 1, 32, ALIGNED, false>::run(s, a...);
+        if (s.nv == 2) return F<T, 2, 32, ALIGNED, false>::run(s, a...);
+        return F<T, kMost, 32, ALIGNED, false>::run(s, a...);
     }
-    if (s.nv == 1) return F<T, 1, 0, ALIGNED>::run(s, a...);
-    if (s.nv == 2) return F<T, 2, 0, ALIGNED>::run(s, a...);
-    if (s.nv == kMost) return F<T, kMost, 0, ALIGNED>::run(s, a...);
-    return F<T, 2 * kMost, 0, ALIGNED>::run(s, a...);
+    if constexpr (LONG && ALIGNED) {
+        if (s.nv > kMost) return F<T, 2 * kMost, 0, ALIGNED, false>::run(s, a...);
+    } else {
+        if (s.pair) return F<T, kMost, 0, ALIGNED, true>::run(s, a...);
+    }
+    if (s.nv == 1) return F<T, 1, 0, ALIGNED, false>::run(s, a...);
+    if (s.nv == 2) return F<T, 2, 0, ALIGNED, false>::run(s, a...);
+    return F<T, kMost, 0, ALIGNED, false>::run(s, a...);
 }
-template <typename T, template <typename, int, int, bool> class F, typename... A>
+template <typename T, bool LONG, template <typename, int, int, bool, bool> class F, typename... A>
 inline cudaError_t dispatch(const Shape &s, A &...a) {
-    return s.aligned ? dispatch_nv<T, F, true>(s, a...) : dispatch_nv<T, F, false>(s, a...);
+    return s.aligned ? dispatch_nv<T, LONG, F, true>(s, a...) : dispatch_nv<T, LONG, F, false>(s, a...);
 }
+
+// Launches `units` CTAs, or pairs of CTAs.
+template <typename... P, typename... A>
+inline cudaError_t launch(void (*fn)(P...), const Shape &sh, long long units, size_t smem, cudaStream_t s,
+                          const A &...a) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at = {};
+    cfg.gridDim = dim3(unsigned(units * sh.ctas()));
+    cfg.blockDim = dim3(unsigned(sh.threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = unsigned(sh.ctas());
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = sh.pair ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, a...);
+}
+
+// Sums that the two CTAs of a pair tell each other, one row after the other, in
+// shared memory: two buffers in turn. A buffer's next sums come when both CTAs
+// have sent the other's, and so have read these.
+struct Pair {
+    float2 sums[2][2];  // by buffer, CTA
+    uint64_t bar[2];
+
+    __device__ __forceinline__ void init() {  // by one thread, before a cluster barrier
+        tc::mbar_init(&bar[0], 1);
+        tc::mbar_init(&bar[1], 1);
+        tc::fence_mbar_init();
+    }
+    // tells both CTAs v, the same in all threads of one
+    __device__ __forceinline__ void send(float2 v, int buf, int rank) {
+        using namespace tc;
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar[buf], 16);
+        if (threadIdx.x < 2)
+            cluster_st_async(cluster_map(&sums[buf][rank], threadIdx.x), v.x, v.y, cluster_map(&bar[buf], threadIdx.x));
+    }
+    // what both have sent, for the use-th time to buffer `buf`; ok turns false when the wait runs out
+    __device__ __forceinline__ void receive(float2 &lower, float2 &upper, int buf, int use, bool &ok) {
+        if (ok && !tc::mbar_wait_cluster(&bar[buf], uint32_t(use) & 1)) ok = false;
+        lower = sums[buf][0], upper = sums[buf][1];
+    }
+    // after the last row
+    static __device__ __forceinline__ void leave(bool ok, int *status) {
+        if (!ok && threadIdx.x == 0) record_status(status, GDN_ETIMEOUT);
+        tc::cluster_arrive_relaxed();  // neither CTA leaves while the other may still store to it
+        tc::cluster_wait();
+    }
+};
 
 // CTAs of kernel `fn` that an SM holds at `threads` each, asked once a kernel
 // (K: a type of its own, whose shared memory is a function of the threads),
@@ -104,17 +163,21 @@ struct Place {
     int col[NV];
     int width;
 
-    __device__ __forceinline__ Place(int w) : width(w) {
+    // a row on `ctas` CTAs, of which this is the rank-th
+    __device__ __forceinline__ Place(int w, int rank, int ctas) : width(w) {
         constexpr int g = G ? G : 1;
         const int groups = G ? int(blockDim.x) / g : 1, group = G ? int(threadIdx.x) / g : 0;
         tid = G ? int(threadIdx.x) % g : int(threadIdx.x);
-        row = int(blockIdx.x) * groups + group;
+        row = int(blockIdx.x) / ctas * groups + group;
         base = G ? row - (threadIdx.x & 31) / g : row;
-        step = int(gridDim.x) * groups;
-        const int off = ALIGNED ? 0 : int((long long)row * width % VE);
+        step = int(gridDim.x) / ctas * groups;
+        const int off = offset();
 #pragma unroll
-        for (int i = 0; i < NV; ++i) col[i] = (tid + i * (G ? G : int(blockDim.x))) * VE - off;
+        for (int i = 0; i < NV; ++i)
+            col[i] = (tid + (rank * NV + i) * (G ? G : int(blockDim.x))) * VE - off;
     }
+    // elements before the row in its first vector
+    __device__ __forceinline__ int offset() const { return ALIGNED ? 0 : int((long long)row * width % VE); }
     __device__ __forceinline__ bool full(int i) const {
         return ALIGNED ? col[i] < width : col[i] >= 0 && col[i] + VE <= width;
     }
@@ -122,16 +185,7 @@ struct Place {
     __device__ __forceinline__ bool has(int i, int j) const {
         return ALIGNED ? col[i] < width : unsigned(col[i] + j) < unsigned(width);
     }
-    // vector i of the row at p; zeros outside the row
-    __device__ __forceinline__ void load(P &v, int i, const T *p) const {
-        if (full(i)) {
-            v.load(p + col[i]);
-        } else if (!ALIGNED) {
-#pragma unroll
-            for (int j = 0; j < VE; ++j)
-                if (has(i, j)) v.e[j] = p[col[i] + j];
-        }
-    }
+    // of the row at p
     __device__ __forceinline__ void store(const P &v, int i, T *p) const {
         if (full(i)) {
             v.store(p + col[i]);
@@ -166,15 +220,13 @@ struct Place {
     }
 };
 
-// The thread's vectors of its rows of NT tensors in turn, read ahead: through
-// its own place in shared memory, or (IN_SMEM false: a CTA of 1024 threads)
-// one row ahead in registers.
-template <typename T, int NT, int NV, int G, bool ALIGNED, bool IN_SMEM>
+// The thread's vectors of its rows of NT tensors in turn, read ahead through
+// its own place in shared memory.
+template <typename T, int NT, int NV, int G, bool ALIGNED>
 struct Feed {
     using L = Place<T, NV, G, ALIGNED>;
     using A = vec::RowsAhead<NT, NV>;
     using P = typename L::P;
-    static __host__ __device__ size_t smem(int threads) { return IN_SMEM ? A::smem(threads) : 0; }
 
     const L &at;
     const T *src[NT];  // of the next row to ask for, at the thread's first vector
@@ -183,7 +235,6 @@ struct Feed {
     int left;          // rows still to ask for
     bool any[NV];      // whether the vector has elements of the row
     A a;
-    P next[IN_SMEM ? 1 : NT][IN_SMEM ? 1 : NV];
 
     __device__ __forceinline__ Feed(const L &place, const T *const (&from)[NT], int rows, void *smem)
         : at(place), pitch((long long)place.step * place.width), a(smem) {
@@ -193,16 +244,8 @@ struct Feed {
         for (int i = 0; i < NV; ++i) any[i] = at.col[i] < at.width;
 #pragma unroll
         for (int t = 0; t < NT; ++t) src[t] = from[t] + (long long)at.row * at.width + at.col[0];
-        if (IN_SMEM) {
 #pragma unroll
-            for (int s = 0; s < A::kAhead; ++s) ask();
-        } else {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < NV; ++i) next[IN_SMEM ? 0 : t][IN_SMEM ? 0 : i].zero();
-            ask();
-        }
+        for (int s = 0; s < A::kAhead; ++s) ask();
     }
     __device__ __forceinline__ void ask() {
         if (left > 0) {
@@ -212,41 +255,34 @@ struct Feed {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int off = (G ? G * VE : int(blockDim.x) * VE) * i;
-                    if (!IN_SMEM) {
-                        at.load(next[IN_SMEM ? 0 : t][IN_SMEM ? 0 : i], i, src[t] - at.col[0]);
-                    } else if (any[i]) {
-                        if (ALIGNED || rest - off >= VE) a.copy(t * NV + i, src[t] + off);
-                        else a.copy_part(t * NV + i, src[t] + off, int(rest - off) * int(sizeof(T)));
-                    }
+                    if (!any[i]) continue;
+                    if (ALIGNED || rest - off >= VE) a.copy(t * NV + i, src[t] + off);
+                    else a.copy_part(t * NV + i, src[t] + off, int(rest - off) * int(sizeof(T)));
                 }
         }
         if (!ALIGNED) rest -= pitch;
 #pragma unroll
         for (int t = 0; t < NT; ++t) src[t] += pitch;
         --left;
-        if (IN_SMEM) a.commit();
+        a.commit();
     }
     // the next row's vectors: zeros outside the row, anything where there is no row
     __device__ __forceinline__ void get(P (&v)[NT][NV]) {
-        if (IN_SMEM) {
-            ask();
-            a.wait();
-        }
+        ask();
+        a.wait();
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (!IN_SMEM) v[t][i] = next[IN_SMEM ? 0 : t][IN_SMEM ? 0 : i];
-                else if (any[i]) v[t][i].r = a.take(t * NV + i);
+                if (any[i]) v[t][i].r = a.take(t * NV + i);
                 else v[t][i].zero();
-                if (IN_SMEM && !ALIGNED && any[i] && !at.full(i)) {
+                if (!ALIGNED && any[i] && !at.full(i)) {
 #pragma unroll
                     for (int j = 0; j < L::VE; ++j)
                         if (!at.has(i, j)) v[t][i].set(j, 0.f);
                 }
             }
-        if (IN_SMEM) a.taken();
-        else ask();
+        a.taken();
     }
 };
 

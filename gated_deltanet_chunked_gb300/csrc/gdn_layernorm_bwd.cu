@@ -9,8 +9,15 @@
 // columns of every row that its CTA takes, so the two sums over rows stay in
 // its registers; each CTA writes one partial row of each at its end, and a
 // second launch adds those in a fixed order (no atomics: the same call gives
-// the same bits).
+// the same bits). Rows too wide for the registers of 512 threads, with weights
+// and sums, are on a cluster of two CTAs (3000 x 16384 bf16: 75 us; on 1024
+// threads of one CTA, with the sums in shared memory, 118).
+// Measured, bf16, of the copy rate (6783 GB/s): 16384 x 4096 66 us (0.90),
+// 32768 x 2048 66 (0.90), 524288 x 128 68 (0.87), 8000 x 8192 74 (0.78);
+// 4096 x 4096 24 (0.63), 17 of them without the sums: partial rows and their
+// second launch cost 5 to 7 us whatever the rows.
 #include "gdn_layernorm.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -24,83 +31,54 @@ struct LnBwdArgs {
     float *dw_part, *db_part;  // [gridDim.x, width] each, or null
     bool sums;                 // whether either is wanted
     int rows, width;
+    int *status;
 };
 
-// The thread's sums over rows: in registers, or (IN_SMEM) in shared memory, four
-// columns at a time at a thread's own place.
-template <int NV, int VE, bool IN_SMEM>
-struct Sums {
-    float2 v[NV][VE / 2];
-    __device__ __forceinline__ explicit Sums(float4 *) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int k = 0; k < VE / 2; ++k) v[i][k] = make_float2(0.f, 0.f);
-    }
-    // each pair k of vector i becomes f(k, itself)
-    template <typename F>
-    __device__ __forceinline__ void add(int i, F f) {
-#pragma unroll
-        for (int k = 0; k < VE / 2; ++k) v[i][k] = f(k, v[i][k]);
-    }
-    __device__ __forceinline__ float get(int i, int j) const { return j & 1 ? v[i][j / 2].y : v[i][j / 2].x; }
-};
-template <int NV, int VE>
-struct Sums<NV, VE, true> {
-    float4 *p;
-    __device__ __forceinline__ explicit Sums(float4 *base) : p(base + threadIdx.x) {
-#pragma unroll
-        for (int k = 0; k < NV * VE / 4; ++k) p[k * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    template <typename F>
-    __device__ __forceinline__ void add(int i, F f) {
-#pragma unroll
-        for (int q = 0; q < VE / 4; ++q) {
-            float4 &r = p[(i * VE / 4 + q) * blockDim.x];
-            const float4 t = r;
-            const float2 lo = f(2 * q, make_float2(t.x, t.y)), hi = f(2 * q + 1, make_float2(t.z, t.w));
-            r = make_float4(lo.x, lo.y, hi.x, hi.y);
-        }
-    }
-    __device__ __forceinline__ float get(int i, int j) const {
-        return reinterpret_cast<const float *>(p + (i * VE + j) / 4 * blockDim.x)[j % 4];
-    }
-};
-
-// MT, the most threads of a CTA: with 1024 a thread has 64 registers, too few
-// for its sums and its weights, which then are in shared memory and read again
-// for every row.
-template <typename T, int NV, int G, bool ALIGNED, int MT>
-__global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(const LnBwdArgs a) {
+// PAIR: a row is on two CTAs, each the same half of all its rows. MT: the most
+// threads of a CTA.
+template <typename T, int NV, int G, bool ALIGNED, bool PAIR, int MT>
+__global__ void __launch_bounds__(MT, G && NV == 1 && ALIGNED ? 3 : 1)
+k_layernorm_bwd(const LnBwdArgs a) {
     using L = ln::Place<T, NV, G, ALIGNED>;
     constexpr int VE = L::VE;
-    constexpr bool kWide = MT == 1024;
-    extern __shared__ __align__(16) uint8_t smem[];  // rows ahead; then, kWide: two sums for every column of a thread
+    extern __shared__ __align__(16) uint8_t smem[];  // rows ahead
     __shared__ __align__(16) float2 red[2][32];
+    __shared__ ln::Pair pair;
     if (!G) {
         if (threadIdx.x < 64) red[threadIdx.x / 32][threadIdx.x % 32] = make_float2(0.f, 0.f);
+        if (PAIR && threadIdx.x == 0) pair.init();
         __syncthreads();
     }
-    const L at(a.width);
-    using F = ln::Feed<T, 2, NV, G, ALIGNED, !kWide>;
+    if (PAIR) tc::cluster_arrive();
+    const int rank = PAIR ? int(tc::cluster_ctarank()) : 0;
+    const L at(a.width, rank, PAIR ? 2 : 1);
     const T *const src[2] = {static_cast<const T *>(a.x), static_cast<const T *>(a.dy)};
-    F feed(at, src, a.rows, smem);
-    float4 *wide_sums = reinterpret_cast<float4 *>(smem + F::smem(int(blockDim.x)));
+    ln::Feed<T, 2, NV, G, ALIGNED> feed(at, src, a.rows, smem);
     T *dx = static_cast<T *>(a.dx);
     constexpr int H = VE / 2;  // pairs of a vector
-    float2 w[NV][H];
-    if (!kWide) at.load_columns(w, a.weight, 1.f);
-    Sums<NV, VE, kWide> dw(wide_sums), db(wide_sums + NV * VE / 4 * blockDim.x);
+    float2 w[NV][H], dw[NV][H], db[NV][H];  // the columns' weights, their sums over rows
+    at.load_columns(w, a.weight, 1.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < H; ++k) dw[i][k] = db[i][k] = make_float2(0.f, 0.f);
+    if (PAIR) tc::cluster_wait();  // both CTAs are ready
+    bool ok = true;
     const float inv_width = 1.f / float(a.width);
     int row = at.row;
     // one row; its statistics are given, and those of the row after the next
     // take their place (two rows ahead, without a move that would wait for
-    // them; kWide, short of registers: of the next row)
-    const int ahead = (kWide ? 1 : 2) * at.step;
-    auto one_row = [&](float2 &stats, float2 *buf) {
+    // them). It is the use-th row with this `buf`.
+    auto one_row = [&](float2 &stats, int buf, int use) {
         const bool live = row < a.rows;
         const float mean = stats.x, rstd = stats.y;
-        if (row + ahead < a.rows) stats = make_float2(a.mean[row + ahead], a.rstd[row + ahead]);
+        // PAIR: not before the exchange, whose fence waits for loads under way
+        // (3000 x 16384 bf16: 74.8 us, 87.8 before it); of unaligned rows they
+        // are better late too (8000 x 4095: 66, 74), of aligned ones early (16384 x 4096: 66, 71)
+        auto next_stats = [&] {
+            if (row + 2 * at.step < a.rows) stats = make_float2(a.mean[row + 2 * at.step], a.rstd[row + 2 * at.step]);
+        };
+        if (!PAIR && ALIGNED) next_stats();
         Pack<T, VE> in[2][NV];
         feed.get(in);
         float2 xhat[NV][H], g[NV][H], a1 = make_float2(0.f, 0.f), a2 = make_float2(0.f, 0.f);
@@ -112,27 +90,27 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
                 g[i][k] = in[1][i].f2(k);
             }
         if (live) {  // outside the row g is zero
-            if (kWide) at.load_columns(w, a.weight, 1.f);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                dw.add(i, [&](int k, float2 s) { return vec::fma2(g[i][k], xhat[i][k], s); });
-                db.add(i, [&](int k, float2 s) { return vec::add2(g[i][k], s); });
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int k = 0; k < H; ++k) {
+                    dw[i][k] = vec::fma2(g[i][k], xhat[i][k], dw[i][k]);
+                    db[i][k] = vec::add2(g[i][k], db[i][k]);
                     g[i][k] = vec::mul2(g[i][k], w[i][k]);
                     a1 = vec::add2(a1, g[i][k]);
                     a2 = vec::fma2(g[i][k], xhat[i][k], a2);
                 }
-            }
         }
         float s1 = vec::sum2(a1), s2 = vec::sum2(a2);
-        if (G) {
-            const float2 t = vec::group_sum2<G ? G : 2>(s1, s2);
-            s1 = t.x, s2 = t.y;
-        } else {
-            const float2 t = vec::block_sum2(s1, s2, buf);
-            s1 = t.x, s2 = t.y;
+        const float2 t = G ? vec::group_sum2<G ? G : 2>(s1, s2) : vec::block_sum2(s1, s2, red[buf]);
+        s1 = t.x, s2 = t.y;
+        if (PAIR) {
+            pair.send(t, buf, rank);
+            float2 low, up;
+            pair.receive(low, up, buf, use, ok);
+            s1 = low.x + up.x, s2 = low.y + up.y;
         }
+        if (PAIR || !ALIGNED) next_stats();
         s1 = __fmul_rn(s1, inv_width);
         s2 = __fmul_rn(s2, inv_width);
         if (live) {
@@ -150,52 +128,43 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
     };
     float2 even = make_float2(0.f, 0.f), odd = even;
     if (row < a.rows) even = make_float2(a.mean[row], a.rstd[row]);
-    if (!kWide && row + at.step < a.rows) odd = make_float2(a.mean[row + at.step], a.rstd[row + at.step]);
-    int turn = 0;
-    for (int base = at.base; base < a.rows; base += ahead, turn ^= 1) {
-        one_row(even, red[kWide ? turn : 0]);
-        if (!kWide && base + at.step < a.rows) one_row(odd, red[1]);
+    if (row + at.step < a.rows) odd = make_float2(a.mean[row + at.step], a.rstd[row + at.step]);
+    int use = 0;
+    for (int base = at.base; base < a.rows; base += 2 * at.step, ++use) {
+        one_row(even, 0, use);
+        if (base + at.step < a.rows) one_row(odd, 1, use);
     }
+    if (PAIR) ln::Pair::leave(ok, a.status);
     if (!a.sums) return;
-    float *dwp = a.dw_part ? a.dw_part + (long long)blockIdx.x * a.width : nullptr;
-    float *dbp = a.db_part ? a.db_part + (long long)blockIdx.x * a.width : nullptr;
-    if (!G && ALIGNED) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!at.full(i)) continue;
-#pragma unroll
-            for (int j = 0; j < VE; j += 4) {
-                if (dwp)
-                    *reinterpret_cast<float4 *>(dwp + at.col[i] + j) =
-                        make_float4(dw.get(i, j), dw.get(i, j + 1), dw.get(i, j + 2), dw.get(i, j + 3));
-                if (dbp)
-                    *reinterpret_cast<float4 *>(dbp + at.col[i] + j) =
-                        make_float4(db.get(i, j), db.get(i, j + 1), db.get(i, j + 2), db.get(i, j + 3));
-            }
-        }
-    } else if (!G) {
-        // columns that no thread has 16 bytes of: through shared memory, so that the stores are whole lines
-        float *line = reinterpret_cast<float *>(smem);
+    const long long part_row = int(blockIdx.x) / (PAIR ? 2 : 1);
+    float *dwp = a.dw_part ? a.dw_part + part_row * a.width : nullptr;
+    float *dbp = a.db_part ? a.db_part + part_row * a.width : nullptr;
+    auto value = [&](int pass, int i, int j) {
+        const float2 v = pass ? db[i][j / 2] : dw[i][j / 2];
+        return j & 1 ? v.y : v.x;
+    };
+    if (!G) {
+        float *line = reinterpret_cast<float *>(smem);  // unaligned rows: the CTA's sums on their way to whole lines
+        const int lo = at.col[0] - int(threadIdx.x) * VE, hi = min(lo + NV * int(blockDim.x) * VE, a.width);
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
             float *out = pass ? dbp : dwp;
             if (!out) continue;
-            if (kWide) {  // which holds the sums: no room for a line
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < VE; ++j)
-                        if (at.has(i, j)) out[at.col[i] + j] = pass ? db.get(i, j) : dw.get(i, j);
-                continue;
-            }
-            __syncthreads();
+            if (!ALIGNED) __syncthreads();
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < VE; ++j)
-                    if (at.has(i, j)) line[at.col[i] + j] = pass ? db.get(i, j) : dw.get(i, j);
-            __syncthreads();
-            for (int c = threadIdx.x; c < a.width; c += blockDim.x) out[c] = line[c];
+                for (int j = 0; j < VE; j += ALIGNED ? 4 : 1) {
+                    if (ALIGNED && at.full(i))
+                        *reinterpret_cast<float4 *>(out + at.col[i] + j) =
+                            make_float4(value(pass, i, j), value(pass, i, j + 1), value(pass, i, j + 2), value(pass, i, j + 3));
+                    else if (!ALIGNED && at.has(i, j))
+                        line[at.col[i] + j - lo] = value(pass, i, j);
+                }
+            if (!ALIGNED) {
+                __syncthreads();
+                for (int c = max(lo, 0) + int(threadIdx.x); c < hi; c += int(blockDim.x)) out[c] = line[c - lo];
+            }
         }
     } else {
         // the CTA's row groups, added in order; one of the two sums at a time
@@ -210,7 +179,7 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int j = 0; j < VE; ++j)
-                    if (at.has(i, j)) part[group * kCols + at.col[i] + j] = pass ? db.get(i, j) : dw.get(i, j);
+                    if (at.has(i, j)) part[group * kCols + at.col[i] + j] = value(pass, i, j);
             __syncthreads();
             float *out = pass ? dbp : dwp;
             if (!out) continue;
@@ -224,43 +193,49 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : MT) k_layernorm_bwd(cons
     }
 }
 
-// Most CTAs of a launch, one partial row each: what the SMs hold of CTAs of
-// that size, as a constant of the width, so that the workspace does not depend
-// on the device.
-int max_parts(int threads) { return ln::kSms * (threads <= 128 ? 8 : threads <= 256 ? 4 : threads <= 512 ? 2 : 1); }
+// Most partial rows of a launch (a CTA's or a cluster's one each): what the SMs
+// hold of CTAs of that size, as a constant of the width, so that the workspace
+// does not depend on the device.
+int max_parts(const ln::Shape &sh) {
+    return ln::kSms * (sh.threads <= 128 ? 8 : sh.threads <= 256 ? 4 : 2) / sh.ctas();
+}
 
 template <typename T>
 size_t workspace_of(int rows, int width) {
-    const int most = max_parts(ln::shape_of<T>(rows, width).threads);
+    const int most = max_parts(ln::shape_of<T, false>(rows, width));
     return (2 * size_t(rows < most ? rows : most) * size_t(width) * sizeof(float) + 255) & ~size_t(255);
 }
 
-template <typename T, int NV, int G, bool ALIGNED>
+template <typename T, int NV, int G, bool ALIGNED, bool PAIR>
 struct Run {
     template <int MT>
     static cudaError_t go(const ln::Shape &sh, LnBwdArgs &a, int &parts, cudaStream_t s) {
-        const auto fn = k_layernorm_bwd<T, NV, G, ALIGNED, MT>;
+        const auto fn = k_layernorm_bwd<T, NV, G, ALIGNED, PAIR, MT>;
         struct Key;
-        const size_t smem = ln::Feed<T, 2, NV, G, ALIGNED, MT != 1024>::smem(sh.threads) +
-                            (MT == 1024     ? size_t(sh.threads) * NV * 16 / sizeof(T) * 2 * sizeof(float)
-                             : !ALIGNED && !G ? size_t(a.width) * sizeof(float)
-                                              : 0);
+        size_t smem = vec::RowsAhead<2, NV>::smem(sh.threads);
+        const size_t line = size_t(sh.threads) * NV * 16 / sizeof(T) * sizeof(float);
+        if (!ALIGNED && !G && smem < line) smem = line;
         const cudaError_t e = ln::allow_smem(reinterpret_cast<const void *>(fn), smem);
         if (e != cudaSuccess) return e;
-        const long long ctas = ((long long)a.rows + sh.rows_per_cta - 1) / sh.rows_per_cta;
-        long long most = (long long)ln::kSms * ln::ctas_per_sm<Key>(reinterpret_cast<const void *>(fn), sh.threads, smem);
-        if (most > max_parts(sh.threads)) most = max_parts(sh.threads);
-        // few rows: four at least a CTA, which writes two f32 rows of sums, while every SM has two CTAs
-        if (a.sums && ctas < 4 * most) most = ctas / 4 > 2 * ln::kSms ? ctas / 4 / 8 * 8 : 2 * ln::kSms;
-        parts = int(ctas < most ? ctas : most);
+        // CTAs, or pairs: a partial row each
+        const long long units = ((long long)a.rows + sh.rows_per_cta - 1) / sh.rows_per_cta;
+        const int ctas = ln::kSms * ln::ctas_per_sm<Key>(reinterpret_cast<const void *>(fn), sh.threads, smem);
+        int most = ctas / sh.ctas();
+        if (most > max_parts(sh)) most = max_parts(sh);
+        // few rows: four at least a unit, which writes two f32 rows of sums, while every SM has two CTAs (if it can)
+        const int least = 2 * ln::kSms / sh.ctas();
+        if (a.sums && most > least && units < 4 * most) most = units / 4 > least ? int(units / 4) : least;
+        if (!ALIGNED && most > 8) most = most / 8 * 8;  // keeps a thread's rows at one misalignment
+        parts = int(units < most ? units : most);
         if (a.dw_part && a.db_part) a.db_part = a.dw_part + size_t(parts) * a.width;
-        fn<<<unsigned(parts), sh.threads, smem, s>>>(a);
-        return cudaGetLastError();
+        return ln::launch(fn, sh, parts, smem, s, a);
     }
     static cudaError_t run(const ln::Shape &sh, LnBwdArgs &a, int &parts, cudaStream_t s) {
-        // more than 512 threads only with the most elements a thread
-        constexpr int kMost = !G && NV * 16 / int(sizeof(T)) >= 16 ? 1024 : 512;
-        return sh.threads <= 512 ? go<512>(sh, a, parts, s) : go<kMost>(sh, a, parts, s);
+        // a few elements of the widest unaligned rows take a warp more, and then registers that others need
+        // (3000 x 16383 bf16: 128 us, 16375: 91)
+        if constexpr (PAIR && !ALIGNED)
+            if (sh.threads > 512) return go<544>(sh, a, parts, s);
+        return go<G ? ln::kRowThreads : 512>(sh, a, parts, s);
     }
 };
 
@@ -305,17 +280,17 @@ size_t layernorm_bwd_workspace(int rows, int width, int io_dtype) {
 
 cudaError_t launch_layernorm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
                                  const float *weight, void *dx, float *dweight, float *dbias, void *workspace,
-                                 int rows, int width, int io_dtype, cudaStream_t s) {
+                                 int rows, int width, int io_dtype, int *status, cudaStream_t s) {
     int parts = 0;
     float *ws = static_cast<float *>(workspace);
     LnBwdArgs a{dy,   x,    mean, rstd, weight, dx, dweight ? ws : nullptr, dbias ? ws : nullptr, dweight || dbias,
-                rows, width};
+                rows, width, status};
     if (rows > 0) {
         LaunchScope scope(GDN_K_LAYERNORM_BWD, s);
         const cudaError_t e =
             io_dtype == GDN_DT_BF16
-                ? ln::dispatch<__nv_bfloat16, Run>(ln::shape_of<__nv_bfloat16>(rows, width), a, parts, s)
-                : ln::dispatch<float, Run>(ln::shape_of<float>(rows, width), a, parts, s);
+                ? ln::dispatch<__nv_bfloat16, false, Run>(ln::shape_of<__nv_bfloat16, false>(rows, width), a, parts, s)
+                : ln::dispatch<float, false, Run>(ln::shape_of<float, false>(rows, width), a, parts, s);
         if (e != cudaSuccess) return e;
     }
     return launch_row_sums(a.dw_part, a.db_part, parts, width, dweight, dbias, s);

@@ -163,6 +163,26 @@ def test_same_bits_every_time_and_in_a_graph(cuda):
             assert torch.equal(ref[k], captured2[k]), k
 
 
+@DTYPES
+@pytest.mark.parametrize("rows,width", [(701, 4097), (700, 5000), (613, 8193), (400, 12288), (701, 12345),
+                                        (333, 16383), (701, 16384)])
+def test_many_rows_over_several_ctas(cuda, rows, width, dtype):
+    """Wide rows are on a cluster of CTAs: the sums that these exchange for a
+    row are not another row's, and a row of NaN stays one row."""
+    d = make(rows, rows, width, dtype)
+    ref = run(d, cuda)
+    compare(ref, d, dtype)
+    again = run(d, cuda)
+    d["x"][300, width // 2] = float("nan")
+    res = run(d, cuda)
+    for k in ("y", "dx", "mean", "rstd", "dweight", "dbias"):
+        assert torch.equal(again[k], ref[k]), k
+        if k in ("dweight", "dbias"):
+            continue
+        keep = [r for r in range(rows) if r != 300]
+        assert torch.equal(res[k][keep], ref[k][keep]) and torch.isnan(res[k][300]).all(), k
+
+
 def test_offsets_past_32_bits(cuda):
     rows, width = (1 << 32) // 8192 + 3, 8192
     x = torch.randn(rows, width, device=cuda, dtype=BF16)
