@@ -183,6 +183,57 @@ def test_many_rows_over_several_ctas(cuda, rows, width, dtype):
         assert torch.equal(res[k][keep], ref[k][keep]) and torch.isnan(res[k][300]).all(), k
 
 
+@DTYPES
+@pytest.mark.parametrize("width", [9001, 12288, 16383])
+def test_in_place_over_several_ctas(cuda, width, dtype):
+    d = make(13, 90, width, dtype)
+    ref = run(d, cuda)
+    c = {k: v.to(cuda) for k, v in d.items()}
+    y = gdn.gdn_layernorm(c["x"], c["w"], c["b"], EPS, out=c["x"])
+    assert y is c["x"] and torch.equal(y, ref["y"])
+    for into in ("dy", "x"):
+        c = {k: v.to(cuda) for k, v in d.items()}
+        dx, dw, db = gdn.gdn_layernorm_bwd(c["dy"], c["x"], ref["mean"], ref["rstd"], c["w"], dx=c[into])
+        assert torch.equal(dx, ref["dx"]) and torch.equal(dw, ref["dweight"]) and torch.equal(db, ref["dbias"])
+
+
+@pytest.mark.parametrize("rows,width", [(300, 16384), (300, 16383), (3000, 1024)])
+def test_two_calls_at_once_and_in_graphs(cuda, rows, width):
+    """Calls on two streams, eager and replayed, do not see each other."""
+    sets = [{k: v.to(cuda) for k, v in make(14 + i, rows, width, BF16).items()} for i in range(2)]
+    refs = [run(c, cuda) for c in sets]
+    streams = [torch.cuda.Stream(cuda) for _ in sets]
+    torch.cuda.synchronize()
+    graphs, captured = [], []
+    for c in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            captured.append(run(c, cuda))
+        graphs.append(graph)
+    eager = [[], []]
+    for _ in range(5):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                eager[i].append(run(sets[i], cuda))
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for i, ref in enumerate(refs):
+        for k in ref:
+            assert torch.equal(captured[i][k], ref[k]) and all(torch.equal(e[k], ref[k]) for e in eager[i]), k
+
+
+def test_on_a_stream_given_by_the_caller(cuda):
+    d = {k: v.to(cuda) for k, v in make(15, 200, 1001, BF16).items()}
+    ref = run(d, cuda)
+    side = torch.cuda.Stream(cuda)
+    torch.cuda.synchronize()
+    y, mean, rstd = gdn.gdn_layernorm(d["x"], d["w"], d["b"], EPS, save_stats=True, stream=side)
+    dx, dw, db = gdn.gdn_layernorm_bwd(d["dy"], d["x"], mean, rstd, d["w"], stream=side)
+    side.synchronize()
+    for k, t in zip(("y", "mean", "rstd", "dx", "dweight", "dbias"), (y, mean, rstd, dx, dw, db)):
+        assert torch.equal(t, ref[k]), k
+
+
 def test_offsets_past_32_bits(cuda):
     rows, width = (1 << 32) // 8192 + 3, 8192
     x = torch.randn(rows, width, device=cuda, dtype=BF16)
