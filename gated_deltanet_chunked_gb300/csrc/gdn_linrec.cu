@@ -111,13 +111,22 @@ struct Bounds {
 
     __device__ __forceinline__ int start(int i) const { return cu ? cu[i] : i * seqlen; }
 
+    // Where the last mark() left off.
+    struct Cursor {
+        int next;    // the offsets before it are below that tile's first row, the others not
+        int offset;  // FORWARD: the first not below that tile's end; else: the last not above its first row
+    };
+    // FORWARD: t0 rises from call to call; else it falls
+    template <bool FORWARD>
+    __device__ __forceinline__ Cursor begin() const { return FORWARD ? Cursor{0, 0} : Cursor{n + 1, INT_MAX}; }
+
     // Marks the tile from row t0, by one warp. Packed: the offsets are searched
-    // 32 at a time from `next` on, where the last call left it (FORWARD: t0
-    // rises from call to call and next starts at 0; else t0 falls and next
-    // starts at n + 1). Sequences without rows share an offset with their
-    // neighbours and are left out.
+    // 32 at a time from the cursor on, unless its offset says that there is
+    // none in this tile (the reads depend on each other, and the CTA waits for
+    // them). Sequences without rows share an offset with their neighbours and
+    // are left out.
     template <bool FORWARD, typename S>
-    __device__ __forceinline__ void mark(int t0, int &next, Marks<S> &m) const {
+    __device__ __forceinline__ void mark(int t0, Cursor &cursor, Marks<S> &m) const {
         const int lane = threadIdx.x & 31, end = min(t0 + S::kRows, total);
         if (lane < S::kSegs) m.starts[lane] = m.ends[lane] = 0;
         __syncwarp();
@@ -140,6 +149,8 @@ struct Bounds {
             }
             return;
         }
+        if (FORWARD ? cursor.offset > end : cursor.offset < t0) return;
+        int &next = cursor.next;
         uint32_t moved;
         do {  // next becomes the first offset that is not below t0
             if (FORWARD) {
@@ -150,14 +161,20 @@ struct Bounds {
                 next -= __popc(moved);
             }
         } while (moved == 0xffffffffu);
-        bool in = true;
-        for (int k = next + lane; __ballot_sync(0xffffffffu, in) == 0xffffffffu; k += 32) {
+        if (FORWARD) cursor.offset = -1;
+        uint32_t in = 0xffffffffu;
+        for (int k = next + lane; in == 0xffffffffu; k += 32) {
             const int v = k <= n ? cu[k] : INT_MAX;
-            in = v <= end;
-            if (!in) continue;
+            in = __ballot_sync(0xffffffffu, v <= end);
+            if (FORWARD && cursor.offset < 0) {
+                const int below = __popc(__ballot_sync(0xffffffffu, v < end));  // offsets rise
+                if (below < 32) cursor.offset = __shfl_sync(0xffffffffu, v, below);
+            }
+            if (v > end) continue;
             if (k < n && cu[k + 1] != v) start_at(v - t0, k);    // the last sequence of those that start here
             if (k > 0 && cu[k - 1] != v) end_at(v - t0 - 1, k - 1);  // the first of those that end here
         }
+        if (!FORWARD) cursor.offset = next <= n && cu[next] == t0 ? t0 : cu[next - 1];  // the first offset is 0
     }
 };
 
@@ -320,35 +337,44 @@ struct Ring {
     }
 };
 
-// Gates per head of a tile's rows, by one warp a round ahead: load() issues the
-// reads for a tile, store() turns what the last load() brought into decays
-// (rows past the end pass the state on).
+// Gates per head of a tile's rows, a round ahead, by the last warps of the CTA,
+// 64 rows each: load() asks for a tile's, each lane's to its own place in shared
+// memory (in registers they would hold up the warp's next walk until they are
+// there, and with it the CTA), store() turns what the last load() brought into
+// decays (rows past the end pass the state on). One warp for 256 rows took
+// longer than the exchange beside it.
 template <int ROWS>
 struct HeadGates {
-    float g[ROWS / 32];
+    float g[ROWS ? ROWS : 1];
+    static __device__ __forceinline__ bool mine() { return int(threadIdx.x) >= kRecThreads - ROWS / 2; }
+    static __device__ __forceinline__ int row() {
+        return (int(threadIdx.x) - (kRecThreads - ROWS / 2)) / 32 * 64 + int(threadIdx.x & 31);
+    }
     __device__ __forceinline__ void load(const RecArgs &a, int t0, int h) {
 #pragma unroll
-        for (int k = 0; k < ROWS / 32; ++k) {
-            const int t = t0 + k * 32 + int(threadIdx.x & 31);
-            g[k] = t >= 0 && t < a.total_tokens ? static_cast<const float *>(a.g)[(long long)t * a.hv + h] : 0.f;
+        for (int k = 0; k < 64; k += 32) {
+            const int r = row() + k, t = t0 + r;
+            if (t >= 0 && t < a.total_tokens)
+                tc::async_copy_4(&g[r], static_cast<const float *>(a.g) + (long long)t * a.hv + h);
+            else
+                g[r] = 0.f;
         }
+        tc::async_copy_commit();
     }
     __device__ __forceinline__ void store(float2 *to, float2 *products) const {
-        const int lane = threadIdx.x & 31;
+        const int r = row();
+        tc::async_copy_wait_all();
+        float2 d = vec::exp_exact2(make_float2(g[r], g[r + 32]));
+        to[r] = vec::both(d.x);
+        to[r + 32] = vec::both(d.y);
 #pragma unroll
-        for (int k = 0; k < ROWS / 32; k += 2) {
-            float2 d = vec::exp_exact2(make_float2(g[k], g[k + 1]));
-            to[k * 32 + lane] = vec::both(d.x);
-            to[(k + 1) * 32 + lane] = vec::both(d.y);
-#pragma unroll
-            for (int m = 1; m < kPart; m *= 2) {
-                d.x *= __shfl_xor_sync(0xffffffffu, d.x, m);
-                d.y *= __shfl_xor_sync(0xffffffffu, d.y, m);
-            }
-            if (lane % kPart == 0) {
-                products[(k * 32 + lane) / kPart] = vec::both(d.x);
-                products[((k + 1) * 32 + lane) / kPart] = vec::both(d.y);
-            }
+        for (int m = 1; m < kPart; m *= 2) {
+            d.x *= __shfl_xor_sync(0xffffffffu, d.x, m);
+            d.y *= __shfl_xor_sync(0xffffffffu, d.y, m);
+        }
+        if (r % kPart == 0) {
+            products[r / kPart] = vec::both(d.x);
+            products[(r + 32) / kPart] = vec::both(d.y);
         }
     }
 };
@@ -439,6 +465,8 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kSeg = S::kSeg;
     __shared__ Exchange<S> ex;
+    using Gates = HeadGates<CHANNEL ? 0 : S::kRows>;
+    __shared__ Gates gates;
     __shared__ uint64_t full[R::kStages];
     const int w = S::seg(), c = S::channel();
     const bool last_warp = threadIdx.x >= kRecThreads - 32, feeder = threadIdx.x == kRecThreads - 1;
@@ -465,15 +493,12 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
         return;
     }
     const Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens};
-    int next = 0;
-    HeadGates<S::kRows> gates;
-    if (last_warp && rounds) {
-        bd.mark<true>(rank * S::kRows, next, ex.marks[0]);
-        if (!CHANNEL) {
-            gates.load(a, rank * S::kRows, h);
-            gates.store(ex.decays[0], ex.products[0]);
-            gates.load(a, (ctas + rank) * S::kRows, h);
-        }
+    Bounds::Cursor next = bd.begin<true>();
+    if (last_warp && rounds) bd.mark<true>(rank * S::kRows, next, ex.marks[0]);
+    if (!CHANNEL && Gates::mine()) {
+        gates.load(a, rank * S::kRows, h);
+        gates.store(ex.decays[0], ex.products[0]);
+        gates.load(a, (ctas + rank) * S::kRows, h);
     }
     copy_empty<S>(a, bd, a.s0, a.final_state, hc, rank, ctas);
     __syncthreads();
@@ -518,10 +543,10 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
                 ring.load(round + R::kStages, &mx, &mg, nullptr, a, c0, h, t0 + R::kStages * ctas * S::kRows);
             __syncwarp();
             bd.mark<true>(t0 + ctas * S::kRows, next, ex.marks[(round + 1) & 1]);
-            if (!CHANNEL) {
-                gates.store(ex.decays[(round + 1) & 1], ex.products[(round + 1) & 1]);
-                gates.load(a, t0 + 2 * ctas * S::kRows, h);
-            }
+        }
+        if (!CHANNEL && Gates::mine() && round + 1 < rounds) {
+            gates.store(ex.decays[(round + 1) & 1], ex.products[(round + 1) & 1]);
+            gates.load(a, t0 + 2 * ctas * S::kRows, h);
         }
         __syncthreads();
         float2 s = pair(&ex.seg_b[w][c]);
@@ -553,6 +578,8 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     constexpr int kSeg = S::kSeg;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Exchange<S> ex;
+    using Gates = HeadGates<CHANNEL ? 0 : S::kRows>;
+    __shared__ Gates gates;
     __shared__ float fwd_a[S::kSegs][S::kCh], fwd_b[S::kSegs][S::kCh];
     __shared__ float head_sums[CHANNEL ? 1 : 2][2][CHANNEL ? 1 : S::kRows];  // by round parity, half of the head, row
     __shared__ uint64_t full[R::kStages];
@@ -582,15 +609,12 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         return;
     }
     const Bounds bd{a.cu, a.num_seqs, a.dense_seqlen, a.total_tokens};
-    int next = a.num_seqs + 1;
-    HeadGates<S::kRows> gates;
-    if (last_warp && rounds) {  // without rows there is no first tile
-        bd.mark<false>(t_first, next, ex.marks[0]);
-        if (!CHANNEL) {
-            gates.load(a, t_first, h);
-            gates.store(ex.decays[0], ex.products[0]);
-            gates.load(a, t_first - t_step, h);
-        }
+    Bounds::Cursor next = bd.begin<false>();
+    if (last_warp && rounds) bd.mark<false>(t_first, next, ex.marks[0]);  // without rows there is no first tile
+    if (!CHANNEL && Gates::mine()) {
+        gates.load(a, t_first, h);
+        gates.store(ex.decays[0], ex.products[0]);
+        gates.load(a, t_first - t_step, h);
     }
     copy_empty<S>(a, bd, a.dfinal, a.dinitial, hc, rank, ctas);
     __syncthreads();
@@ -658,10 +682,11 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         if (last_warp && round + 1 < rounds) {
             __syncwarp();
             bd.mark<false>(t0 - t_step, next, ex.marks[(round + 1) & 1]);
-            if (!CHANNEL) {
-                gates.store(ex.decays[(round + 1) & 1], ex.products[(round + 1) & 1]);
-                gates.load(a, t0 - 2 * t_step, h);
-            }
+        }
+        if (!CHANNEL && Gates::mine() && round + 1 < rounds) {
+            __syncwarp();
+            gates.store(ex.decays[(round + 1) & 1], ex.products[(round + 1) & 1]);
+            gates.load(a, t0 - 2 * t_step, h);
         }
         __syncthreads();
         // The segment's states are kept for kPart rows at a time, the last part

@@ -224,6 +224,14 @@ __device__ __forceinline__ void cluster_st_async(uint32_t addr, float a, float b
                  : "memory");
 }
 
+// Copies of four bytes by the thread that asks, from global to shared memory,
+// which holds no register up; visible to that thread after its wait.
+__device__ __forceinline__ void async_copy_4(float *to, const float *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void async_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void async_copy_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
 // Bounded wait for a phase that stores of the cluster's other CTAs into this
 // one's shared memory complete. Only shared memory is acquired: an acquire of
 // all memory at cluster scope also drops what the SM has cached of global
