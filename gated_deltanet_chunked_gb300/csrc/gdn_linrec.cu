@@ -10,9 +10,8 @@
 // parallelism along the time axis. A row's map s -> a s + x composes: a
 // segment of rows is s -> A s + B with A the product of its decays. A cluster
 // of CTAs takes half of a head's channels and walks the packed token axis in
-// rounds; in a round each CTA takes the next tile of 128 rows (256 of bf16 rows
-// with gates per head, which need no registers for decays), each of its warps a
-// segment of 16 (32) rows, each lane two channels:
+// rounds; in a round each CTA takes the next tile of 128 rows, each of its warps
+// a segment of 16 rows, each lane two channels:
 //  1. every warp composes its segment's rows (tile in shared memory by TMA,
 //     kept in registers from here on);
 //  2. the CTA composes its segments and stores the result into every CTA of
@@ -66,11 +65,11 @@ constexpr int kPart = 8;  // rows whose states the backward pass holds at a time
 constexpr int kMaxCluster = 16;  // above the portable eight
 constexpr float kReset = -1.f;  // in the place of a product of decays (never negative)
 
-// A CTA's tile: 64 channels x 8 segments of SEG rows, or (WIDE) 128 x 4. A
+// A CTA's tile: 64 channels x 8 segments of 16 rows, or (WIDE) 128 x 4. A
 // warp has 64 channels, two a lane, of one segment.
-template <bool WIDE, int SEG>
+template <bool WIDE>
 struct Tile {
-    static constexpr int kSeg = SEG;
+    static constexpr int kSeg = 16;
     static constexpr int kCh = WIDE ? 128 : 64;
     static constexpr int kSegs = WIDE ? 4 : 8;
     static constexpr int kRows = kSegs * kSeg;
@@ -291,13 +290,16 @@ __device__ __forceinline__ void exchange(Exchange<S> &ex, float &carry, int roun
 // Tile loads through a ring of stages: one thread issues, everyone waits.
 template <typename T, bool CHANNEL, bool BACKWARD>
 struct Ring {
-    using S = Tile<BACKWARD && !CHANNEL, (CHANNEL || BACKWARD || sizeof(T) == 4) ? 16 : 32>;
+    using S = Tile<BACKWARD && !CHANNEL>;
     static constexpr int kTile = S::kRows * S::kCh;                                 // elements of one tensor's tile
     static constexpr uint32_t kTiles = kTile * sizeof(T) * (1 + CHANNEL + BACKWARD);  // x, g per channel, dout
     static constexpr uint32_t kState = BACKWARD ? S::kCh * 4 : 0;                     // the state before the tile
     static constexpr uint32_t kBytes = kTiles + kState;
-    // CTAs of an SM that registers allow, and stages that shared memory then allows
-    static constexpr int kCtasPerSm = BACKWARD && sizeof(T) == 4 ? 1 : 2;
+    // CTAs of an SM that registers allow, and stages that shared memory then
+    // allows. The smallest tiles (bf16, gates per head) leave room for three
+    // (8 heads x 700 rows 6.6 us, with two of twice the rows 8.4; 32 heads x
+    // 38429 136 against 135).
+    static constexpr int kCtasPerSm = BACKWARD && sizeof(T) == 4 ? 1 : kTiles <= 16384 ? 3 : 2;
     static constexpr int kStages = kTiles <= 32768 ? 2 : 1;
     static constexpr size_t kSmem = size_t(kStages) * kBytes + 128;
     uint8_t *base;
@@ -341,8 +343,8 @@ struct Ring {
 // 64 rows each: load() asks for a tile's, each lane's to its own place in shared
 // memory (in registers they would hold up the warp's next walk until they are
 // there, and with it the CTA), store() turns what the last load() brought into
-// decays (rows past the end pass the state on). One warp for 256 rows took
-// longer than the exchange beside it.
+// decays (rows past the end pass the state on). One warp for all took longer
+// than the exchange beside it.
 template <int ROWS>
 struct HeadGates {
     float g[ROWS ? ROWS : 1];
@@ -754,10 +756,6 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
                 if ((lane & 3) == 0) head_sums[round & 1][c / 64][w * kSeg + part * kPart + (lane >> 2)] = sums[0];
             }
         };
-        if constexpr (kParts == 4) {
-            part_walk(std::integral_constant<int, 3>{});
-            part_walk(std::integral_constant<int, 2>{});
-        }
         part_walk(std::integral_constant<int, 1>{});
         part_walk(std::integral_constant<int, 0>{});
     }
