@@ -384,7 +384,7 @@ int gdn_linear_recurrence(const gdn_problem *p, const void *x, const void *g, co
                           const int32_t *cu_seqlens, void *out, float *final_state, float *states, void *stream) {
     int st = check_linrec(p, cu_seqlens != nullptr);
     if (st) return st;
-    if (p->total_tokens > 0 && (!x || !out || x == out || !aligned16(x) || !aligned16(out) || !gate_ok(p, g)))
+    if (p->total_tokens > 0 && (!x || !out || x == out || g == out || !aligned16(x) || !aligned16(out) || !gate_ok(p, g)))
         return GDN_EINVAL;
     if (!aligned16(initial_state) || !aligned4(cu_seqlens) || !aligned16(final_state) || !aligned16(states))
         return GDN_EINVAL;
@@ -465,6 +465,7 @@ int gdn_layernorm(const gdn_problem *p, const void *x, const float *weight, cons
     if (st) return st;
     if (!(eps >= 0.f) || !aligned16(weight) || !aligned16(bias)) return GDN_EINVAL;
     if (p->total_tokens > 0) {
+        if (mean && mean == rstd) return GDN_EINVAL;
         if (!x || !y || !aligned16(x) || !aligned16(y) || !aligned4(mean) || !aligned4(rstd)) return GDN_EINVAL;
     }
     int *status = status_ptr();
@@ -483,6 +484,7 @@ int gdn_layernorm_bwd(const gdn_problem *p, const void *dy, const void *x, const
     const int st = check_layernorm(p);
     if (st) return st;
     if (!aligned16(weight) || !aligned16(dweight) || !aligned16(dbias)) return GDN_EINVAL;
+    if (dweight && dweight == dbias) return GDN_EINVAL;
     if (p->total_tokens > 0) {
         if (!dy || !x || !mean || !rstd || !dx) return GDN_EINVAL;
         if (!aligned16(dy) || !aligned16(x) || !aligned16(dx) || !aligned4(mean) || !aligned4(rstd))

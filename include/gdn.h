@@ -321,7 +321,7 @@ int gdn_gating(const gdn_problem *p, const float *a, const float *b, const float
  * layout, dense or packed, is gdn_chunk_fwd's. Only batch, seqlen, num_seqs,
  * total_tokens, hv, dv (128), io_dtype and flags of `p` are used.
  *   x, out        [total_tokens, hv, 128] io dtype, 16-byte aligned; out may
- *                 not be x
+ *                 be neither x nor g
  *   g             log-decays, g <= 0 (-inf forgets the state): [total_tokens,
  *                 hv] f32, 4-byte aligned, one per head (gdn_gating's g), or
  *                 with GDN_FLAG_GATE_CHANNEL [total_tokens, hv, 128] io dtype,
@@ -334,7 +334,8 @@ int gdn_gating(const gdn_problem *p, const float *a, const float *b, const float
  *                 start at 0, rise and end at total_tokens are recorded as
  *                 GDN_EDEVICE_INPUT and nothing is written.
  *   final_state   [num_seqs, hv, 128] f32, 16-byte aligned, or NULL; a
- *                 sequence without tokens gets its initial state (or zeros)
+ *                 sequence without tokens gets its initial state (or zeros).
+ *                 It may not be initial_state.
  *   states        NULL, or f32 storage of gdn_linear_recurrence_states_size(p)
  *                 bytes, 16-byte aligned, that the backward pass reads: s
  *                 before every 64th row of the packed token axis (what it

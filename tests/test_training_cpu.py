@@ -119,6 +119,14 @@ def test_layernorm_rejects_bad_arguments():
     assert back(dv=20000) == gdn.GDN_EUNSUPPORTED
 
 
+def test_outputs_in_one_place_are_refused():
+    lib, p = gdn.load(), ctypes.byref(problem(dv=100))
+    a, b = ptr(FAKE), ptr(2 * FAKE)
+    assert lib.gdn_layernorm(p, a, a, a, ctypes.c_float(1e-5), a, b, b, None) == gdn.GDN_EINVAL
+    assert lib.gdn_layernorm_bwd(p, a, a, a, a, a, a, b, b, a, ctypes.c_size_t(1 << 30), None) == gdn.GDN_EINVAL
+    assert fwd(problem(flags=CHANNEL), g=2 * FAKE, out=2 * FAKE) == gdn.GDN_EINVAL
+
+
 def test_layernorm_workspace_size_covers_every_partial_row():
     size = lambda r, d: int(gdn.load().gdn_layernorm_bwd_workspace_size(ctypes.byref(problem(total_tokens=r, dv=d))))
     assert size(1, 100) >= 2 * 100 * 4 and size(1, 100) % 256 == 0
