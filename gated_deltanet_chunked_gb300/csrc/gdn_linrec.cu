@@ -31,9 +31,9 @@
 // fill the memory pipe all the same (two CTAs an SM); gates per head carry
 // fewer bytes a round and do not.
 // Measured, bf16, 32 heads, of the copy rate (6783 GB/s) by a call's own bytes:
-// gates per channel, T = 65536: forward 262 us (0.91), backward 442 (0.90);
-// T = 4096: 25 (0.60), 37 (0.68); gates per head, 38429 packed rows: 142
-// (0.66), 266 (0.53). f32, 16 heads x 8000, per channel: 37 (0.79), 63 (0.77).
+// gates per channel, T = 65536: forward 260 us (0.91), backward 443 (0.90);
+// T = 4096: 25 (0.60), 37 (0.67); gates per head, 38429 packed rows: 136
+// (0.69), 260 (0.54). f32, 16 heads x 8000, per channel: 37 (0.79), 59 (0.82).
 //
 // Sequences are boundaries on the one axis. A segment that holds a sequence's
 // first row (for the backward pass: last row) does not depend on what comes
@@ -300,7 +300,7 @@ struct Ring {
     // (8 heads x 700 rows 6.6 us, with two of twice the rows 8.4; 32 heads x
     // 38429 136 against 135).
     static constexpr int kCtasPerSm = BACKWARD && sizeof(T) == 4 ? 1 : kTiles <= 16384 ? 3 : 2;
-    static constexpr int kStages = kTiles <= 32768 ? 2 : 1;
+    static constexpr int kStages = kCtasPerSm == 1 || kTiles <= 32768 ? 2 : 1;
     static constexpr size_t kSmem = size_t(kStages) * kBytes + 128;
     uint8_t *base;
     uint64_t *full;
