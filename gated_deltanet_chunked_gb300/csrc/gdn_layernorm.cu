@@ -32,7 +32,9 @@ struct LnArgs {
     int *status;
 };
 
-// PAIR: a row is on two CTAs, each the same half of all its rows.
+// PAIR: a row is on two CTAs, each the same half of all its rows. (Threads: 544
+// for the widest unaligned rows; 576 holds the others to 96 registers, with
+// which more CTAs fit: 20000 x 1001 20 us, with a bound of 512 23.)
 template <typename T, int NV, int G, bool ALIGNED, bool PAIR>
 __global__ void __launch_bounds__(G ? ln::kRowThreads : PAIR ? 544 : 576) k_layernorm(const LnArgs a) {
     using L = ln::Place<T, NV, G, ALIGNED>;
@@ -52,12 +54,22 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : PAIR ? 544 : 576) k_laye
     ln::Feed<T, 1, NV, G, ALIGNED> feed(at, src, a.rows, smem);
     T *y = static_cast<T *>(a.y);
     constexpr int H = VE / 2;  // pairs of a vector
-    // 32 elements a thread leave no registers for weight and bias: read for every row
-    constexpr bool kReread = NV * VE > 16;
+    // 32 elements a thread leave no registers for weight and bias: at the
+    // thread's own place in shared memory, or, where the rows ahead (f32) leave
+    // none of that either, read for every row
+    constexpr bool kShared = NV * VE > 16 && sizeof(T) == 2, kReread = NV * VE > 16 && !kShared;
+    float4 *const shared = reinterpret_cast<float4 *>(smem + vec::RowsAhead<1, NV>::smem(int(blockDim.x))) + threadIdx.x;
     float2 w[NV][H], b[NV][H];
     if (!kReread) {
         at.load_columns(w, a.weight, 1.f);
         at.load_columns(b, a.bias, 0.f);
+    }
+    if (kShared) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int k = 0; k < H; ++k)
+                shared[(i * H + k) * blockDim.x] = make_float4(w[i][k].x, w[i][k].y, b[i][k].x, b[i][k].y);
     }
     const float inv_width = 1.f / float(a.width);
     // PAIR: the columns of the lower CTA, and what mean and squares are first taken over
@@ -121,8 +133,13 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : PAIR ? 544 : 576) k_laye
                 }
                 Pack<T, VE> o;
 #pragma unroll
-                for (int k = 0; k < H; ++k)
+                for (int k = 0; k < H; ++k) {
+                    if (kShared) {
+                        const float4 t = shared[(i * H + k) * blockDim.x];
+                        w[i][k] = make_float2(t.x, t.y), b[i][k] = make_float2(t.z, t.w);
+                    }
                     o.set2(k, vec::fma2(vec::mul2(v[i][k], vec::both(rstd)), w[i][k], b[i][k]));
+                }
                 at.store(o, i, y + (long long)row * a.width);
             }
             if (at.tid == 0 && rank == 0) {
@@ -140,7 +157,9 @@ struct Run {
         const auto fn = k_layernorm<T, NV, G, ALIGNED, PAIR>;
         const void *f = reinterpret_cast<const void *>(fn);
         struct Key;
-        const size_t smem = vec::RowsAhead<1, NV>::smem(sh.threads);
+        constexpr int kElements = NV * 16 / int(sizeof(T));  // of a thread
+        size_t smem = vec::RowsAhead<1, NV>::smem(sh.threads);
+        if (kElements > 16 && sizeof(T) == 2) smem += size_t(sh.threads) * kElements * 2 * sizeof(float);
         const cudaError_t e = ln::allow_smem(f, smem);
         if (e != cudaSuccess) return e;
         const long long units = ((long long)a.rows + sh.rows_per_cta - 1) / sh.rows_per_cta;

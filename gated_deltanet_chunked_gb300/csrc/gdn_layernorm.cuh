@@ -35,8 +35,9 @@ struct Shape {
 // Long rows: 16 elements a thread, which is the least of reductions and
 // barriers for an element; few rows (latency counts) over as many threads as
 // help. Rows that so take more than 512 threads are on two CTAs, which tell
-// each other their sums; or (LONG) on 512 threads with 32 elements each, where
-// rows are aligned and the kernel has the registers.
+// each other their sums; or (LONG, the forward pass) on 512 threads with 32
+// elements each where they are aligned: 3000 x 16384 51 us, on two CTAs 57;
+// unaligned, 3000 x 16383, 126 and 77.
 template <typename T, bool LONG>
 inline Shape shape_of(int rows, int width) {
     constexpr int VE = 16 / int(sizeof(T)), kMost = 16 / VE;  // at most 16 elements a thread

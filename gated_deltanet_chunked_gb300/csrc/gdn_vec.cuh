@@ -1,4 +1,4 @@
-// Vectors of VE consecutive elements of one row (2 to 16 bytes) between
+// Vectors of VE consecutive elements of one row (4 to 16 bytes) between
 // memory and f32 registers, for the row-wise kernels (norms and their
 // backward passes) and the recurrence's decode step.
 #pragma once
@@ -18,8 +18,6 @@ template <>
 struct Raw<8> { using type = uint2; };
 template <>
 struct Raw<4> { using type = uint32_t; };
-template <>
-struct Raw<2> { using type = uint16_t; };
 
 // VE elements of T as they lie in memory
 template <typename T, int VE>
