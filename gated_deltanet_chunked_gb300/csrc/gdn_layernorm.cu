@@ -11,10 +11,10 @@
 // without the optional outputs, which the compiler may turn into separate
 // copies of the loop.
 // Measured, bf16, of the copy rate (6783 GB/s): 16384 x 4096 43 us (0.92),
-// 32768 x 2048 46 (0.86), 524288 x 128 48 (0.83), 8000 x 8192 58 (0.67); where
+// 32768 x 2048 46 (0.86), 524288 x 128 48 (0.83), 8000 x 8192 45 (0.85); where
 // rows are odd a third of the time goes into their ragged ends (20000 x 1001
 // 20 us, 0.60); a single row takes 2.3 us. What bounds the widest rows is
-// their two reductions: 3000 x 16384 51 us (0.57).
+// their two reductions, with one CTA on an SM: 3000 x 16384 44 us (0.66).
 #include "gdn_layernorm.cuh"
 
 namespace gdn {

@@ -36,8 +36,11 @@ struct Shape {
 // barriers for an element; few rows (latency counts) over as many threads as
 // help. Rows that so take more than 512 threads are on two CTAs, which tell
 // each other their sums; or (LONG, the forward pass) on 512 threads with 32
-// elements each where they are aligned: 3000 x 16384 51 us, on two CTAs 57;
-// unaligned, 3000 x 16383, 126 and 77.
+// elements each where they are aligned: 3000 x 16384 44 us, on two CTAs 57;
+// unaligned, 3000 x 16383, 126 and 77. Many bf16 rows of more than 400 such
+// threads are better on half of them too, so that an SM has two CTAs: 8000 x
+// 8192 45 us against 57, 7000 wide 45 and 59, but 6000 wide 30 and 28, and 400
+// rows of 8192 5.9 and 5.1.
 template <typename T, bool LONG>
 inline Shape shape_of(int rows, int width) {
     constexpr int VE = 16 / int(sizeof(T)), kMost = 16 / VE;  // at most 16 elements a thread
@@ -48,8 +51,9 @@ inline Shape shape_of(int rows, int width) {
     s.nv = 1;
     if (!s.g && rows > 16 * kSms) s.nv = kMost;
     while (s.nv < kMost && vecs > (s.g ? s.g : kRowThreads) * s.nv) s.nv *= 2;
-    const bool wide = !s.g && vecs > 512 * s.nv;
-    s.pair = wide && !(LONG && s.aligned);
+    const bool more = LONG && s.aligned;  // elements a thread
+    const bool wide = !s.g && vecs > (more && sizeof(T) == 2 && rows > 4 * kSms ? 400 : 512) * s.nv;
+    s.pair = wide && !more;
     if (wide && !s.pair) s.nv *= 2;
     const int each = s.nv * s.ctas();  // vectors of a thread, and of that at its place in the other CTA
     s.threads = s.g ? kRowThreads : ((vecs + each - 1) / each + 31) / 32 * 32;

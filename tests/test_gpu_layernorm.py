@@ -164,7 +164,8 @@ def test_same_bits_every_time_and_in_a_graph(cuda):
 
 
 @DTYPES
-@pytest.mark.parametrize("rows,width", [(701, 4097), (700, 5000), (613, 8193), (400, 12288), (701, 12345),
+@pytest.mark.parametrize("rows,width", [(701, 4097), (700, 5000), (650, 6408), (701, 8192), (613, 8193),
+                                        (400, 12288), (701, 12345),
                                         (333, 16383), (701, 16384)])
 def test_many_rows_over_several_ctas(cuda, rows, width, dtype):
     """Wide rows are on a cluster of CTAs: the sums that these exchange for a
