@@ -49,7 +49,14 @@ inline Shape shape_of(int rows, int width) {
     const int vecs = s.aligned ? width / VE : (width + VE - 1 + VE - 1) / VE;  // for any misalignment
     s.g = vecs <= 16 ? 16 : vecs <= 32 * kMost ? 32 : 0;
     s.nv = 1;
-    if (!s.g && rows > 16 * kSms) s.nv = kMost;
+    if (!s.g && rows > 16 * kSms) {
+        s.nv = kMost;
+        // LONG, bf16: not where three warps with one vector a lane do and two
+        // with two would have three tenths of their places empty (83333 x 600:
+        // 43 us for 49, 71428 x 700: 54 for 63; the backward pass and f32 lose
+        // as much, and so does 1040 wide with five warps for three)
+        if (LONG && sizeof(T) == 2 && vecs < 90) s.nv = 1;
+    }
     while (s.nv < kMost && vecs > (s.g ? s.g : kRowThreads) * s.nv) s.nv *= 2;
     const bool more = LONG && s.aligned;  // elements a thread
     const bool wide = !s.g && vecs > (more && sizeof(T) == 2 && rows > 4 * kSms ? 400 : 512) * s.nv;

@@ -45,7 +45,8 @@ def test_widths(cuda, width, dtype):
 
 
 @DTYPES
-@pytest.mark.parametrize("rows,width", [(2, 128), (31, 128), (3000, 128), (20011, 64), (2500, 1001), (1300, 2048)])
+@pytest.mark.parametrize("rows,width", [(2, 128), (31, 128), (3000, 128), (20011, 64), (2500, 1001), (2500, 600), (2501, 700),
+                                        (2500, 720), (1300, 2048)])
 def test_rows(cuda, rows, width, dtype):
     d = make(rows, rows, width, dtype)
     compare(run(d, cuda), d, dtype)
