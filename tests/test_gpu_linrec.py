@@ -102,6 +102,19 @@ def test_dense_batches(cuda, batch, seqlen):
     compare({k: v.reshape(sum(lens), 2, 128) if k in ("out", "dx", "dg") else v for k, v in res.items()}, d, lens, BF16)
 
 
+@GATES
+@pytest.mark.parametrize("hv", [1, 160])
+@pytest.mark.parametrize("lens", [[5120, 1, 127, 128, 3000, 0, 64, 64, 4000, 2], [128] * 30 + [0, 0] + [64] * 9,
+                                  [1] * 700 + [1500] + [1] * 70, [4096, 4096]], ids=["long", "tiles", "ones", "two"])
+def test_boundaries_that_rounds_skip_and_meet(cuda, lens, hv, gate):
+    """Sequences longer than a round, ending at tiles' ends, and more than 32 in a tile, with clusters of one CTA and
+    of many."""
+    if hv > 1:  # more clusters than fit at once with more than one CTA each
+        lens = [min(v, 300) for v in lens[:5] + lens[-5:]]
+    d = make(60, lens, hv, BF16, gate, True)
+    compare(run(to(d, cuda)), d, lens, BF16)
+
+
 @DTYPES
 @GATES
 @pytest.mark.parametrize("mu", [-8.0, 4.0], ids=["slow_decay", "fast_decay"])
