@@ -17,7 +17,7 @@ namespace {
 __device__ int g_status_word;  // device status word (first device-side error)
 
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
-std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};  // limit of the prefill kernels' bounded waits
+std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};  // limit of bounded waits
 
 constexpr int kMaxDevices = 64;
 int *g_status_ptr[kMaxDevices];
@@ -367,6 +367,7 @@ RecArgs linrec_args(const gdn_problem *p, const void *x, const void *g, const fl
     a.x = x; a.g = g; a.s0 = s0; a.cu = cu;
     a.total_tokens = p->total_tokens; a.num_seqs = p->num_seqs; a.hv = p->hv;
     a.dense_seqlen = cu ? 0 : p->seqlen;
+    a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     return a;
 }
 

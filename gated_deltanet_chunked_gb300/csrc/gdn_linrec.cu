@@ -223,6 +223,8 @@ struct Exchange {
     // arithmetic), and their product in parts of kPart rows
     float2 decays[2][S::kRows];
     float2 products[2][S::kRows / kPart];
+    tc::GiveUp<kMaxCluster> gave_up;
+    int stop;  // set where a wait of the exchange has run out
 };
 
 // A channel's segments of a tile in walking order.
@@ -258,14 +260,15 @@ struct Segments {
 // in shared memory: moves `carry` (the value before the round) on to the next
 // round's; seg_b becomes the value that each segment starts from, which
 // at(segment, value) gets too. REVERSE: segments and CTAs from the last to the
-// first. ok turns false when a wait runs out (2 s; later waits are skipped and no
-// more tiles are asked for: the rounds run out on what is there). One
+// first. When the wait runs out the round is finished on what is there and the
+// CTA leaves after it: all of its threads see `stop` alike, which is set between
+// the round's two barriers and read behind the second. One
 // thread a channel is the fewest instructions; the other warps have the
 // forward states of the backward pass, the next tiles' boundaries and gates
 // to see to meanwhile.
 template <bool REVERSE, typename S, typename F>
-__device__ __forceinline__ void exchange(Exchange<S> &ex, float &carry, int round, int rank, int ctas, bool &ok,
-                                         F at) {
+__device__ __forceinline__ void exchange(Exchange<S> &ex, float &carry, int round, int rank, int ctas,
+                                         unsigned long long wait_ns, bool &ok, F at) {
     using namespace tc;
     const int ch = threadIdx.x, p = round & 1;
     if (threadIdx.x == 0) mbar_arrive_expect_tx(&ex.bar[p], uint32_t(ctas) * S::kCh * 8);
@@ -274,7 +277,7 @@ __device__ __forceinline__ void exchange(Exchange<S> &ex, float &carry, int roun
 #pragma unroll 4
     for (int r = 0; r < ctas; ++r)
         cluster_st_async(cluster_map(&ex.cta[p][rank][ch], r), mine.x, mine.y, cluster_map(&ex.bar[p], r));
-    if (ok && !mbar_wait_cluster(&ex.bar[p], uint32_t(round >> 1) & 1)) ok = false;
+    if (!mbar_wait_cluster(&ex.bar[p], uint32_t(round >> 1) & 1, wait_ns)) ex.stop = 1, ok = false;
     float s = carry, in = carry;
 #pragma unroll 4
     for (int i = 0; i < ctas; ++i) {
@@ -285,6 +288,26 @@ __device__ __forceinline__ void exchange(Exchange<S> &ex, float &carry, int roun
     }
     carry = s;
     sg.finish(ex.seg_b, ch, in, at);
+}
+
+// The CTA's way out, all threads, after `round` of `rounds` rounds. Where a wait
+// has run out, tiles and gates on their way land first, and the cluster settles
+// its exchange.
+template <typename S, typename R>
+__device__ __forceinline__ void leave(Exchange<S> &ex, R &ring, bool ok, bool stop, int round, int rounds, int rank,
+                                      int ctas, bool feeder, int *status) {
+    using namespace tc;
+    if ((!ok || stop) && feeder) ring.drain();
+    if (__any_sync(0xffffffffu, !ok) && (threadIdx.x & 31) == 0) record_status(status, GDN_ETIMEOUT);
+    if (stop) {
+        async_copy_wait_all();
+        if (threadIdx.x == 0) ex.gave_up.tell(round, rank, ctas);
+        cluster_arrive();
+    } else {
+        cluster_arrive_relaxed();
+    }
+    cluster_wait();  // no CTA sends any more, and none leaves while another may
+    if (threadIdx.x < 32) ex.gave_up.settle(ex.bar, rounds, rank, ctas, S::kCh * 8);
 }
 
 // Tile loads through a ring of stages: one thread issues, everyone waits.
@@ -328,11 +351,11 @@ struct Ring {
         if (CHANNEL) tc::tma_load_3d(const_cast<T *>(g(i)), mg, c0, h, t0, bar);
         if (BACKWARD) tc::tma_load_3d(const_cast<T *>(dout(i)), md, c0, h, t0, bar);
     }
-    __device__ __forceinline__ void wait(int i, bool &ok) {
-        if (ok && !tc::mbar_wait(&full[i % kStages], uint32_t((i / kStages) & 1))) ok = false;
+    __device__ __forceinline__ void wait(int i, unsigned long long wait_ns, bool &ok) {
+        if (ok && !tc::mbar_wait_for(&full[i % kStages], uint32_t((i / kStages) & 1), wait_ns)) ok = false;
     }
-    // by the issuing thread, after a wait has run out: the last tiles asked for
-    // land (bounded too) before the CTA may exit
+    // by the issuing thread of a CTA that leaves early: the last tiles asked
+    // for land (2 s each at most) before it exits
     __device__ __forceinline__ void drain() {
         for (int i = asked > kStages ? asked - kStages : 0; i < asked; ++i)
             tc::mbar_wait(&full[i % kStages], uint32_t((i / kStages) & 1));
@@ -478,6 +501,8 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     const int tiles = (a.total_tokens + S::kRows - 1) / S::kRows;
     const int rounds = (tiles + ctas - 1) / ctas;
     R ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)), full};
+    ex.gave_up.init();
+    if (threadIdx.x == 0) ex.stop = 0;
     if (feeder) {
         for (int i = 0; i < R::kStages; ++i) mbar_init(&full[i], 1);
         mbar_init(&ex.bar[0], 1);
@@ -490,7 +515,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     cluster_arrive();  // this CTA's barriers are ready
     bool ok = true;
     if (!offsets_ok(a)) {  // the same in every CTA: nothing is written
-        for (int i = 0; i < R::kStages && i < rounds; ++i) ring.wait(i, ok);
+        if (feeder) ring.drain();
         cluster_wait();
         return;
     }
@@ -507,13 +532,15 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
     float carry = 0.f;  // of this thread's channel in the exchange, before the round
     const int width = a.hv * kHeadDim;  // of a row
     const unsigned pitch = unsigned(width) * sizeof(T);
-    for (int round = 0; round < rounds; ++round) {
+    bool stop = false;
+    int round = 0;
+    while (round < rounds && !stop) {
         const int t0 = (round * ctas + rank) * S::kRows, tw = t0 + w * kSeg;  // the tile's and the warp's first row
         const int rows = min(kSeg, a.total_tokens - tw);                     // may be negative
         const Marks<S> &marks = ex.marks[round & 1];
         const uint32_t starts = marks.starts[w], ends = marks.ends[w];
         const int *first = marks.first + w * kSeg, *last = marks.last + w * kSeg;
-        ring.wait(round, ok);
+        ring.wait(round, a.wait_ns, ok);
         Pack<T, 2> x[kSeg];
         const int o = w * kSeg * S::kCh + c;
 #pragma unroll
@@ -534,7 +561,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
         __syncthreads();
         if (round == 0) cluster_wait();  // every CTA's barriers are ready
         if (threadIdx.x < S::kCh)
-            exchange<false>(ex, carry, round, rank, ctas, ok, [&](int seg, float s) {
+            exchange<false>(ex, carry, round, rank, ctas, a.wait_ns, ok, [&](int seg, float s) {
                 const int t = t0 + seg * kSeg;
                 if (seg % (kStateRows / kSeg) == 0 && a.states && t < a.total_tokens)
                     a.states[(long long)(t / kStateRows) * width + h * kHeadDim + c0 + threadIdx.x] = s;
@@ -551,6 +578,7 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
             gates.load(a, t0 + 2 * ctas * S::kRows, h);
         }
         __syncthreads();
+        stop = ex.stop;
         float2 s = pair(&ex.seg_b[w][c]);
         T *out = static_cast<T *>(a.out) + (long long)tw * width + hc;
         walk<0, kSeg - 1>(plain, [&](int i, auto checked) {
@@ -562,12 +590,10 @@ k_linrec(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __grid_c
             store2(row_at(out, pitch, i), s);
             if (checked && a.final_state && (ends >> i & 1)) set_state(a.final_state, last[i], width, hc, s);
         });
+        ++round;
     }
-    if (!ok && feeder) ring.drain();
-    if (!ok && (threadIdx.x & 31) == 0) record_status(a.status, GDN_ETIMEOUT);
     if (!rounds) cluster_wait();
-    cluster_arrive_relaxed();  // no CTA leaves while others may still store to it
-    cluster_wait();
+    leave(ex, ring, ok, stop, round, rounds, rank, ctas, feeder, a.status);
 }
 
 template <typename T, bool CHANNEL>
@@ -594,6 +620,8 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     const int rounds = (tiles + ctas - 1) / ctas;
     const int t_first = ((rounds - 1) * ctas + rank) * S::kRows, t_step = ctas * S::kRows;
     R ring{reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 127) & ~uintptr_t(127)), full};
+    ex.gave_up.init();
+    if (threadIdx.x == 0) ex.stop = 0;
     if (feeder) {
         for (int i = 0; i < R::kStages; ++i) mbar_init(&full[i], 1);
         mbar_init(&ex.bar[0], 1);
@@ -606,7 +634,7 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
     cluster_arrive();
     bool ok = true;
     if (!offsets_ok(a)) {
-        for (int i = 0; i < R::kStages && i < rounds; ++i) ring.wait(i, ok);
+        if (feeder) ring.drain();
         cluster_wait();
         return;
     }
@@ -629,7 +657,9 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         if (r < S::kRows && t + r < a.total_tokens)
             static_cast<float *>(a.dg)[(long long)(t + r) * a.hv + h] = head_sums[parity][0][r] + head_sums[parity][1][r];
     };
-    for (int round = 0; round < rounds; ++round) {
+    bool stop = false;
+    int round = 0;
+    while (round < rounds && !stop) {
         const int t0 = t_first - round * t_step, tw = t0 + w * kSeg;
         const int rows = min(kSeg, a.total_tokens - tw);
         // the segment's rows that start (s is reset) and end (e is reset) a sequence
@@ -637,7 +667,7 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         const uint32_t starts = marks.starts[w], ends = marks.ends[w];
         const int *first = marks.first + w * kSeg, *last = marks.last + w * kSeg;
         const bool plain = !(starts | ends) && rows == kSeg;
-        ring.wait(round, ok);
+        ring.wait(round, a.wait_ns, ok);
         const float state = ring.state(round)[threadIdx.x % S::kCh];  // unused where the tile starts a sequence
         Pack<T, 2> x[kSeg], dy[kSeg];
         const int o = w * kSeg * S::kCh + c;
@@ -675,7 +705,7 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         if (round == 0) cluster_wait();
         __syncwarp();
         if (threadIdx.x < S::kCh) {
-            exchange<true>(ex, carry, round, rank, ctas, ok, [](int, float) {});
+            exchange<true>(ex, carry, round, rank, ctas, a.wait_ns, ok, [](int, float) {});
         } else if (threadIdx.x < 2 * S::kCh) {
             const int ch = threadIdx.x - S::kCh;
             Segments<S, false> sg(fwd_a, fwd_b, ch);
@@ -691,6 +721,7 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
             gates.load(a, t0 - 2 * t_step, h);
         }
         __syncthreads();
+        stop = ex.stop;
         // The segment's states are kept for kPart rows at a time, the last part
         // first: from the states at the parts' first rows each part is walked
         // again.
@@ -758,16 +789,14 @@ k_linrec_bwd(const RecArgs a, const __grid_constant__ CUtensorMap mx, const __gr
         };
         part_walk(std::integral_constant<int, 1>{});
         part_walk(std::integral_constant<int, 0>{});
+        ++round;
     }
     if (!CHANNEL && rounds) {
         __syncthreads();
-        write_head_sums((rounds - 1) & 1, rank * S::kRows);
+        if (!stop) write_head_sums((rounds - 1) & 1, rank * S::kRows);
     }
-    if (!ok && feeder) ring.drain();
-    if (!ok && lane == 0) record_status(a.status, GDN_ETIMEOUT);
     if (!rounds) cluster_wait();
-    cluster_arrive_relaxed();
-    cluster_wait();
+    leave(ex, ring, ok, stop, round, rounds, rank, ctas, feeder, a.status);
 }
 
 static_assert(kPart == 8, "the sums over a head's channels take eight rows at a time");

@@ -16,6 +16,7 @@ struct RecArgs {
     float *states;  // [ceil(total_tokens / kStateRows), hv, 128]; written forward (or null), read backward
     int total_tokens, num_seqs, dense_seqlen, hv;
     int *status;
+    unsigned long long wait_ns;  // limit of a wait
 };
 
 cudaError_t launch_linrec(const RecArgs &a, int io_dtype, bool channel, cudaStream_t s);

@@ -114,6 +114,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     return true;
 }
 
+// Limits below this are kept by polling: how long the hardware suspends a
+// thread that tries a phase is its own affair.
+constexpr uint64_t kShortLimitNs = 20000;
+
+__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_test_wait(bar, parity))
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    return true;
+}
+
+// mbar_wait that keeps limits of any length.
+__device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+    return limit_ns < kShortLimitNs || !mbar_try_wait(bar, parity) ? mbar_poll(bar, parity, limit_ns) : true;
+}
+
 // ---------------------------------------------------------------------------
 // TMA (tensor) and bulk (linear) copies global -> shared, completing on an
 // mbarrier with a transaction count
@@ -237,24 +253,20 @@ __device__ __forceinline__ void async_copy_wait_all() { asm volatile("cp.async.w
 // all memory at cluster scope also drops what the SM has cached of global
 // memory and waits meanwhile.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t limit_ns = 2000000000ull) {
-    auto done = [&] {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        return ok != 0;
-    };
-    if (!done()) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!done())
-            if (globaltimer_ns() - t0 > limit_ns) return false;
-    }
+    if (!mbar_wait_for(bar, parity, limit_ns)) return false;
     asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
     return true;
+}
+
+// `bytes` that will not come, counted on this CTA's barrier as if they had
+__device__ __forceinline__ void mbar_complete_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// An int to `addr` in another CTA's shared memory, for a reader behind a
+// cluster barrier at which this thread arrives with release.
+__device__ __forceinline__ void cluster_st(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Barrier over every thread of the cluster: each arrives, then waits. The
@@ -272,6 +284,44 @@ __device__ __forceinline__ void cluster_wait() {
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+
+// How the CTAs of a cluster leave an exchange in which a wait has run out.
+// Round by round each of them sends `bytes` to every CTA (itself too), counted
+// on that CTA's bar[round & 1], which it has armed when it sends itself. A CTA
+// sends a round only after its wait for the round before has ended; one whose
+// wait runs out sends and arms nothing more. So all have sent m rounds and
+// some one more, and only those two rounds' bytes can be under way.
+template <int CTAS>
+struct GiveUp {
+    int sent[CTAS];  // by rank: rounds sent + 1 by a CTA that gave up, else 0
+
+    // by the CTA's threads, before the cluster barrier that precedes the first round
+    __device__ __forceinline__ void init() {
+        if (threadIdx.x < CTAS) sent[threadIdx.x] = 0;
+    }
+    // by thread 0 of a CTA that has given up after `rounds` rounds; its warp then arrives with release
+    __device__ __forceinline__ void tell(int rounds, int rank, int ctas) {
+        for (int r = 0; r < ctas; ++r) cluster_st(cluster_map(&sent[rank], r), rounds + 1);
+    }
+    // By the CTA's first warp, behind a cluster barrier after which no CTA
+    // sends: if any gave up, waits (2 s each at most) until what was sent to
+    // this CTA has landed, so that it may exit. all: the rounds of a CTA that
+    // did not give up.
+    __device__ __forceinline__ void settle(uint64_t *bar, int all, int rank, int ctas, uint32_t bytes) const {
+        const int lane = threadIdx.x & 31, s = lane < ctas ? sent[lane] : 0;
+        if (!__any_sync(0xffffffffu, s)) return;
+        const int n = lane < ctas ? (s ? s - 1 : all) : INT_MAX;
+        const int m = __reduce_min_sync(0xffffffffu, n);
+        const int more = __popc(__ballot_sync(0xffffffffu, lane < ctas && n > m));
+        const bool armed = __shfl_sync(0xffffffffu, n, rank) > m;
+        if (lane) return;
+        if (m) mbar_wait_cluster(&bar[(m - 1) & 1], uint32_t((m - 1) >> 1) & 1);
+        if (!more) return;
+        if (armed) mbar_complete_tx(&bar[m & 1], uint32_t(ctas - more) * bytes);
+        else mbar_arrive_expect_tx(&bar[m & 1], uint32_t(more) * bytes);
+        mbar_wait_cluster(&bar[m & 1], uint32_t(m >> 1) & 1);
+    }
+};
 
 // ---------------------------------------------------------------------------
 // tcgen05: tensor memory

@@ -847,8 +847,8 @@ def gdn_get_device_status(stream=None) -> int:
 
 
 def gdn_set_wait_limit_ns(ns: int) -> None:
-    """Limit of the prefill kernels' bounded device-side waits for later
-    launches (0 restores the default 2 s); for tests of the timeout path."""
+    """Limit of the kernels' bounded device-side waits for later launches
+    (0 restores the default 2 s); for tests of the timeout path."""
     load().gdn_set_wait_limit_ns(int(ns))
 
 

@@ -340,7 +340,9 @@ int gdn_gating(const gdn_problem *p, const float *a, const float *b, const float
  *                 bytes, 16-byte aligned, that the backward pass reads: s
  *                 before every 64th row of the packed token axis (what it
  *                 holds for a row that starts a sequence is unspecified)
- * The state and all sums are f32; out is rounded once. */
+ * The state and all sums are f32; out is rounded once. (The CTAs that share an
+ * axis wait for their tiles and for each other, each wait at most 2 s:
+ * GDN_ETIMEOUT in the device status. So in the backward pass.) */
 int gdn_linear_recurrence(const gdn_problem *p, const void *x, const void *g, const float *initial_state,
                           const int32_t *cu_seqlens, void *out, float *final_state, float *states, void *stream);
 
@@ -490,14 +492,15 @@ int gdn_profile_collect(long long *launches, double *ms, long long *timed, int c
 const char *gdn_kernel_name(int kernel);
 
 /* Sets, process-wide, the limit of every bounded device-side wait in the
- * prefill kernels launched after the call (the tensor-core kernel's copy,
- * MMA and ready-flag waits), in nanoseconds of wall time; 0 restores the
- * default of 2 s. A wait that runs out records GDN_ETIMEOUT in the device
- * status word; the kernel then drains what it has in flight (copies and
- * MMAs, each drain bounded too), frees its tensor memory and returns, so the
- * context stays usable and the call's outputs are unspecified. Meant for
- * tests of that path: a limit of a few microseconds makes the waits on
- * not-yet-prepared chunks run out. Returns GDN_OK. */
+ * kernels launched after the call (the tensor-core prefill kernel's copy, MMA
+ * and ready-flag waits; the recurrence's waits on copies and on the other CTAs
+ * of a cluster), in nanoseconds of wall time; 0 restores the default of 2 s. A
+ * wait that runs out records GDN_ETIMEOUT in the device status word; the kernel
+ * then drains what it has in flight (copies, MMAs and stores between CTAs, each
+ * drain bounded too), frees its tensor memory and returns, so the context stays
+ * usable and the call's outputs are unspecified. Meant for tests of that path:
+ * a limit of a few microseconds makes the prefill's waits on not-yet-prepared
+ * chunks run out, one of some nanoseconds the others. Returns GDN_OK. */
 int gdn_set_wait_limit_ns(unsigned long long ns);
 
 #ifdef __cplusplus
