@@ -472,7 +472,8 @@ int gdn_layernorm(const gdn_problem *p, const void *x, const float *weight, cons
     int *status = status_ptr();
     if (!status) return GDN_ECUDA;
     return cuda_status(launch_layernorm(x, weight, bias, eps, y, mean, rstd, p->total_tokens, p->dv, p->io_dtype,
-                                        status, static_cast<cudaStream_t>(stream)));
+                                        status, g_wait_ns.load(std::memory_order_relaxed),
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 size_t gdn_layernorm_bwd_workspace_size(const gdn_problem *p) {
@@ -496,7 +497,8 @@ int gdn_layernorm_bwd(const gdn_problem *p, const void *dy, const void *x, const
     int *status = status_ptr();
     if (!status) return GDN_ECUDA;
     return cuda_status(launch_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, p->total_tokens,
-                                            p->dv, p->io_dtype, status, static_cast<cudaStream_t>(stream)));
+                                            p->dv, p->io_dtype, status, g_wait_ns.load(std::memory_order_relaxed),
+                                            static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

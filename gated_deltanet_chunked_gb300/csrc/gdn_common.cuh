@@ -104,12 +104,14 @@ cudaError_t launch_gating(const float *a, const float *b, const float *A_log, co
 cudaError_t launch_gated_rmsnorm(const void *o, const void *z, const float *weight, float eps, void *y,
                                  long long rows, int io_dtype, int *status, cudaStream_t s);
 cudaError_t launch_layernorm(const void *x, const float *weight, const float *bias, float eps, void *y, float *mean,
-                             float *rstd, int rows, int width, int io_dtype, int *status, cudaStream_t s);
+                             float *rstd, int rows, int width, int io_dtype, int *status, unsigned long long wait_ns,
+                             cudaStream_t s);
 constexpr int kLayerNormMaxWidth = 16384;  // widest row the layer norm's kernels hold in registers
 size_t layernorm_bwd_workspace(int rows, int width, int io_dtype);
 cudaError_t launch_layernorm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
                                  const float *weight, void *dx, float *dweight, float *dbias, void *workspace,
-                                 int rows, int width, int io_dtype, int *status, cudaStream_t s);
+                                 int rows, int width, int io_dtype, int *status, unsigned long long wait_ns,
+                                 cudaStream_t s);
 size_t gated_rmsnorm_bwd_workspace(long long rows, int io_dtype);
 cudaError_t launch_gated_rmsnorm_bwd(const void *dy, const void *o, const void *z, const float *weight, float eps,
                                      void *d_o, void *d_z, float *d_weight, void *workspace, long long rows,

@@ -30,6 +30,7 @@ struct LnArgs {
     float *mean, *rstd;
     int rows, width;
     int *status;
+    unsigned long long wait_ns;  // limit of a pair's wait
 };
 
 // PAIR: a row is on two CTAs, each the same half of all its rows. (Threads: 544
@@ -109,8 +110,8 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : PAIR ? 544 : 576) k_laye
             // squares about the row's mean: those about each half's, and
             // (difference of the means)^2 for each of its columns
             float2 low, up;
-            pair.send(make_float2(mean, squares), n & 1, rank);
-            pair.receive(low, up, n & 1, n >> 1, ok);
+            pair.send(make_float2(mean, squares), n & 1, rank, ok);
+            pair.receive(low, up, n & 1, n >> 1, a.wait_ns, ok);
             const float part = __fmul_rn(float(lower), inv_width), apart = __fadd_rn(low.x, -up.x);
             const float all = fmaf(part, apart, up.x), shift = __fadd_rn(mean, -all);
             squares = fmaf(__fmul_rn(float(lower), __fadd_rn(1.f, -part)), __fmul_rn(apart, apart),
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : PAIR ? 544 : 576) k_laye
             }
         }
     }
-    if (PAIR) ln::Pair::leave(ok, a.status);
+    if (PAIR) pair.leave(ok, at.rows_of(a.rows), rank, a.status);
 }
 
 template <typename T, int NV, int G, bool ALIGNED, bool PAIR>
@@ -173,9 +174,10 @@ struct Run {
 }  // namespace
 
 cudaError_t launch_layernorm(const void *x, const float *weight, const float *bias, float eps, void *y, float *mean,
-                             float *rstd, int rows, int width, int io_dtype, int *status, cudaStream_t s) {
+                             float *rstd, int rows, int width, int io_dtype, int *status, unsigned long long wait_ns,
+                             cudaStream_t s) {
     if (rows == 0) return cudaSuccess;
-    const LnArgs a{x, weight, bias, eps, y, mean, rstd, rows, width, status};
+    const LnArgs a{x, weight, bias, eps, y, mean, rstd, rows, width, status, wait_ns};
     LaunchScope scope(GDN_K_LAYERNORM, s);
     if (io_dtype == GDN_DT_BF16)
         return ln::dispatch<__nv_bfloat16, true, Run>(ln::shape_of<__nv_bfloat16, true>(rows, width), a, s);

@@ -112,33 +112,51 @@ inline cudaError_t launch(void (*fn)(P...), const Shape &sh, long long units, si
 
 // Sums that the two CTAs of a pair tell each other, one row after the other, in
 // shared memory: two buffers in turn. A buffer's next sums come when both CTAs
-// have sent the other's, and so have read these.
+// have sent the other's, and so have read these. ok is each thread's own: it
+// turns false when its wait runs out, and the rows go on on what is there,
+// without waits of that thread. Thread 0 sends, and none after its own.
 struct Pair {
     float2 sums[2][2];  // by buffer, CTA
     uint64_t bar[2];
+    tc::GiveUp<2> gave_up;
+    int sent;  // rows, by a CTA whose thread 0 gave up
 
     __device__ __forceinline__ void init() {  // by one thread, before a cluster barrier
         tc::mbar_init(&bar[0], 1);
         tc::mbar_init(&bar[1], 1);
         tc::fence_mbar_init();
+        gave_up.sent[0] = gave_up.sent[1] = 0;
     }
     // tells both CTAs v, the same in all threads of one
-    __device__ __forceinline__ void send(float2 v, int buf, int rank) {
+    __device__ __forceinline__ void send(float2 v, int buf, int rank, bool ok) {
         using namespace tc;
-        if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar[buf], 16);
-        if (threadIdx.x < 2)
-            cluster_st_async(cluster_map(&sums[buf][rank], threadIdx.x), v.x, v.y, cluster_map(&bar[buf], threadIdx.x));
+        if (threadIdx.x || !ok) return;
+        mbar_arrive_expect_tx(&bar[buf], 2 * sizeof(v));
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            cluster_st_async(cluster_map(&sums[buf][rank], r), v.x, v.y, cluster_map(&bar[buf], r));
     }
-    // what both have sent, for the use-th time to buffer `buf`; ok turns false when the wait runs out
-    __device__ __forceinline__ void receive(float2 &lower, float2 &upper, int buf, int use, bool &ok) {
-        if (ok && !tc::mbar_wait_cluster(&bar[buf], uint32_t(use) & 1)) ok = false;
+    // what both have sent, for the use-th time to buffer `buf`
+    __device__ __forceinline__ void receive(float2 &lower, float2 &upper, int buf, int use, unsigned long long wait_ns,
+                                            bool &ok) {
+        if (ok && !tc::mbar_wait_cluster(&bar[buf], uint32_t(use) & 1, wait_ns)) {
+            ok = false;
+            if (threadIdx.x == 0) sent = 2 * use + buf + 1;
+        }
         lower = sums[buf][0], upper = sums[buf][1];
     }
-    // after the last row
-    static __device__ __forceinline__ void leave(bool ok, int *status) {
-        if (!ok && threadIdx.x == 0) record_status(status, GDN_ETIMEOUT);
-        tc::cluster_arrive_relaxed();  // neither CTA leaves while the other may still store to it
-        tc::cluster_wait();
+    // after the last of `rows` rows
+    __device__ __forceinline__ void leave(bool ok, int rows, int rank, int *status) {
+        using namespace tc;
+        if (__any_sync(0xffffffffu, !ok) && (threadIdx.x & 31) == 0) record_status(status, GDN_ETIMEOUT);
+        if (__shfl_sync(0xffffffffu, int(threadIdx.x == 0 && !ok), 0)) {
+            if (threadIdx.x == 0) gave_up.tell(sent, rank, 2);
+            cluster_arrive();
+        } else {
+            cluster_arrive_relaxed();
+        }
+        cluster_wait();  // neither CTA sends any more, and none leaves while the other may
+        if (threadIdx.x < 32) gave_up.settle(bar, rows, rank, 2, sizeof(float2));
     }
 };
 
@@ -188,6 +206,8 @@ struct Place {
         for (int i = 0; i < NV; ++i)
             col[i] = (tid + (rank * NV + i) * (G ? G : int(blockDim.x))) * VE - off;
     }
+    // how many of `rows` rows are its CTA's (G = 0)
+    __device__ __forceinline__ int rows_of(int rows) const { return base < rows ? (rows - 1 - base) / step + 1 : 0; }
     // elements before the row in its first vector
     __device__ __forceinline__ int offset() const { return ALIGNED ? 0 : int((long long)row * width % VE); }
     __device__ __forceinline__ bool full(int i) const {

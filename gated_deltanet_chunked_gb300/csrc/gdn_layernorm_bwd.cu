@@ -32,6 +32,7 @@ struct LnBwdArgs {
     bool sums;                 // whether either is wanted
     int rows, width;
     int *status;
+    unsigned long long wait_ns;  // limit of a pair's wait
 };
 
 // PAIR: a row is on two CTAs, each the same half of all its rows. MT: the most
@@ -106,9 +107,9 @@ k_layernorm_bwd(const LnBwdArgs a) {
         const float2 t = G ? vec::group_sum2<G ? G : 2>(s1, s2) : vec::block_sum2(s1, s2, red[buf]);
         s1 = t.x, s2 = t.y;
         if (PAIR) {
-            pair.send(t, buf, rank);
+            pair.send(t, buf, rank, ok);
             float2 low, up;
-            pair.receive(low, up, buf, use, ok);
+            pair.receive(low, up, buf, use, a.wait_ns, ok);
             s1 = low.x + up.x, s2 = low.y + up.y;
         }
         if (PAIR || !ALIGNED) next_stats();
@@ -135,7 +136,7 @@ k_layernorm_bwd(const LnBwdArgs a) {
         one_row(even, 0, use);
         if (base + at.step < a.rows) one_row(odd, 1, use);
     }
-    if (PAIR) ln::Pair::leave(ok, a.status);
+    if (PAIR) pair.leave(ok, at.rows_of(a.rows), rank, a.status);
     if (!a.sums) return;
     const long long part_row = int(blockIdx.x) / (PAIR ? 2 : 1);
     float *dwp = a.dw_part ? a.dw_part + part_row * a.width : nullptr;
@@ -281,11 +282,12 @@ size_t layernorm_bwd_workspace(int rows, int width, int io_dtype) {
 
 cudaError_t launch_layernorm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
                                  const float *weight, void *dx, float *dweight, float *dbias, void *workspace,
-                                 int rows, int width, int io_dtype, int *status, cudaStream_t s) {
+                                 int rows, int width, int io_dtype, int *status, unsigned long long wait_ns,
+                                 cudaStream_t s) {
     int parts = 0;
     float *ws = static_cast<float *>(workspace);
     LnBwdArgs a{dy,   x,    mean, rstd, weight, dx, dweight ? ws : nullptr, dbias ? ws : nullptr, dweight || dbias,
-                rows, width, status};
+                rows, width, status, wait_ns};
     if (rows > 0) {
         LaunchScope scope(GDN_K_LAYERNORM_BWD, s);
         const cudaError_t e =

@@ -494,7 +494,7 @@ const char *gdn_kernel_name(int kernel);
 /* Sets, process-wide, the limit of every bounded device-side wait in the
  * kernels launched after the call (the tensor-core prefill kernel's copy, MMA
  * and ready-flag waits; the recurrence's waits on copies and on the other CTAs
- * of a cluster), in nanoseconds of wall time; 0 restores the default of 2 s. A
+ * of a cluster; the layer norm's on the other CTA of a pair), in nanoseconds of wall time; 0 restores the default of 2 s. A
  * wait that runs out records GDN_ETIMEOUT in the device status word; the kernel
  * then drains what it has in flight (copies, MMAs and stores between CTAs, each
  * drain bounded too), frees its tensor memory and returns, so the context stays

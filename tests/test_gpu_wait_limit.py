@@ -10,6 +10,7 @@ import contextlib
 import pytest
 import torch
 
+import test_gpu_layernorm as norm
 import test_gpu_linrec as linrec
 from gated_deltanet_chunked_gb300 import gdn
 
@@ -85,3 +86,16 @@ def test_recurrence_beside_an_undisturbed_one(cuda):
                 res = linrec.run(sets[1])
         assert gdn.gdn_get_device_status() in (gdn.GDN_OK, gdn.GDN_ETIMEOUT)
         assert all(torch.equal(res[k], ref[k]) for k in ref)
+
+
+@norm.DTYPES
+@pytest.mark.parametrize("rows,width", [(2000, 16383), (700, 9001), (500, 16384), (3, 12345)])
+def test_norm(cuda, rows, width, dtype):
+    """Rows on two CTAs (of aligned widths the backward pass alone)."""
+    d = {k: v.to(cuda) for k, v in norm.make(74, rows, width, dtype).items()}
+    ref = norm.run(d, cuda)
+    torch.cuda.synchronize()
+    assert gdn.gdn_get_device_status() == gdn.GDN_OK
+    seen = disturbed(lambda: norm.run(d, cuda), ref)
+    if rows >= 500:  # a pair waits many times
+        assert gdn.GDN_ETIMEOUT in seen
