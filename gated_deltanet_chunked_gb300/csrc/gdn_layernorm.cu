@@ -2,16 +2,20 @@
 //
 //   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(mean (x - mean)^2 + eps)
 //
-// HBM-bound: a row is read once, held in registers through both statistics
-// (the mean first, then the squares about it: no cancellation whatever the
-// row's offset) and written once. Threads keep their columns' weight and bias
+// HBM-bound: a row is read once, held in registers through both statistics and
+// written once. The mean comes first, then the squares about it. Where the mean
+// is more than 4 deviations, what rounding left in it counts (6e-5 in a row that
+// is 1000 all over, which 1 / sqrt(eps) makes 0.02): there the values about it
+// are summed too, and correct it. So whatever the row's offset, errors are small
+// beside its deviations. (Summed in every row that takes 48 us at 16384 x 4096,
+// where 44 are taken.) Threads keep their columns' weight and bias
 // in registers over all their rows, and the next rows are on their way to
 // shared memory meanwhile. Arithmetic is on pairs (two values an instruction),
 // and its roundings are written out: the same row gives the same bits with and
 // without the optional outputs, which the compiler may turn into separate
 // copies of the loop.
-// Measured, bf16, of the copy rate (6783 GB/s): 16384 x 4096 43 us (0.92),
-// 32768 x 2048 46 (0.86), 524288 x 128 48 (0.83), 8000 x 8192 45 (0.85); where
+// Measured, bf16, of the copy rate (6783 GB/s): 16384 x 4096 44 us (0.90),
+// 32768 x 2048 45 (0.88), 524288 x 128 46 (0.86), 8000 x 8192 46 (0.84); where
 // rows are odd a third of the time goes into their ragged ends (20000 x 1001
 // 20 us, 0.60); a single row takes 2.3 us. What bounds the widest rows is
 // their two reductions, with one CTA on an SM: 3000 x 16384 44 us (0.66).
@@ -40,10 +44,10 @@ template <typename T, int NV, int G, bool ALIGNED, bool PAIR>
 __global__ void __launch_bounds__(G ? ln::kRowThreads : PAIR ? 544 : 576) k_layernorm(const LnArgs a) {
     using L = ln::Place<T, NV, G, ALIGNED>;
     constexpr int VE = L::VE;
-    __shared__ __align__(16) float red[2][32];
-    __shared__ ln::Pair pair;
+    __shared__ __align__(16) float red[3][32];
+    __shared__ ln::Pair<float4> pair;
     if (!G) {
-        if (threadIdx.x < 64) red[threadIdx.x / 32][threadIdx.x % 32] = 0.f;
+        if (threadIdx.x < 32) red[0][threadIdx.x] = red[1][threadIdx.x] = red[2][threadIdx.x] = 0.f;
         if (PAIR && threadIdx.x == 0) pair.init();
         __syncthreads();
     }
@@ -94,7 +98,7 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : PAIR ? 544 : 576) k_laye
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
             for (int k = 0; k < H; ++k) v[i][k] = vec::add2(v[i][k], vec::both(-mean));
-            if (!at.full(i)) {  // outside the row: not in the squares
+            if (!at.full(i)) {  // outside the row: in neither sum
 #pragma unroll
                 for (int k = 0; k < H; ++k) {
                     if (!at.has(i, 2 * k)) v[i][k].x = 0.f;
@@ -106,25 +110,39 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : PAIR ? 544 : 576) k_laye
         }
         const float sq = vec::sum2(acc);
         float squares = G ? vec::group_sum<G ? G : 1>(sq) : vec::block_sum(sq, red[1]);
-        if (PAIR) {
-            // squares about the row's mean: those about each half's, and
-            // (difference of the means)^2 for each of its columns
-            float2 low, up;
-            pair.send(make_float2(mean, squares), n & 1, rank, ok);
-            pair.receive(low, up, n & 1, n >> 1, a.wait_ns, ok);
-            const float part = __fmul_rn(float(lower), inv_width), apart = __fadd_rn(low.x, -up.x);
-            const float all = fmaf(part, apart, up.x), shift = __fadd_rn(mean, -all);
-            squares = fmaf(__fmul_rn(float(lower), __fadd_rn(1.f, -part)), __fmul_rn(apart, apart),
-                           __fadd_rn(low.y, up.y));
-            mean = all;
+        float off = 0.f;  // the mean is `mean` + off, the squares about it sum v^2 - (sum v) off
+        const bool far = __fmul_rn(mean, mean) > __fmul_rn(16.f * inv_mine, squares);  // the same in all of the row's threads
+        if (G ? __any_sync(0xffffffffu, far) : far) {
+            acc = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int k = 0; k < H; ++k) v[i][k] = vec::add2(v[i][k], vec::both(shift));
+                for (int k = 0; k < H; ++k) acc = vec::add2(acc, v[i][k]);
+            const float left = G ? vec::group_sum<G ? G : 1>(vec::sum2(acc)) : vec::block_sum(vec::sum2(acc), red[2]);
+            if (far) {
+                off = __fmul_rn(left, inv_mine);
+                // rounding may leave less than 0 where all values are one
+                squares = fmaxf(fmaf(-left, off, squares), 0.f);
+            }
+        }
+        float shift = -off;  // v + shift: the values about the mean
+        if (PAIR) {
+            // squares about the row's mean: those about each half's, and
+            // (difference of the means)^2 for each of its columns
+            float4 low, up;
+            pair.send(make_float4(mean, off, squares, 0.f), n & 1, rank, ok);
+            pair.receive(low, up, n & 1, n >> 1, a.wait_ns, ok);
+            const float part = __fmul_rn(float(lower), inv_width), rest = __fadd_rn(1.f, -part);
+            const float apart = __fadd_rn(__fadd_rn(low.x, -up.x), __fadd_rn(low.y, -up.y));
+            shift = fmaf(rank ? -part : rest, apart, shift);
+            squares = fmaf(__fmul_rn(float(lower), rest), __fmul_rn(apart, apart), __fadd_rn(low.z, up.z));
+            mean = __fadd_rn(up.x, fmaf(part, apart, up.y));
             ++n;
+        } else {
+            mean = __fadd_rn(mean, off);
         }
         const float var = __fmul_rn(squares, inv_width);
-        const float rstd = rsqrtf(__fadd_rn(var, a.eps));
+        const float rstd = rsqrtf(__fadd_rn(var, a.eps)), shifted = __fmul_rn(shift, rstd);
         if (row < a.rows) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -139,7 +157,7 @@ __global__ void __launch_bounds__(G ? ln::kRowThreads : PAIR ? 544 : 576) k_laye
                         const float4 t = shared[(i * H + k) * blockDim.x];
                         w[i][k] = make_float2(t.x, t.y), b[i][k] = make_float2(t.z, t.w);
                     }
-                    o.set2(k, vec::fma2(vec::mul2(v[i][k], vec::both(rstd)), w[i][k], b[i][k]));
+                    o.set2(k, vec::fma2(vec::fma2(v[i][k], vec::both(rstd), vec::both(shifted)), w[i][k], b[i][k]));
                 }
                 at.store(o, i, y + (long long)row * a.width);
             }

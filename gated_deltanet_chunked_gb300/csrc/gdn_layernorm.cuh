@@ -115,8 +115,10 @@ inline cudaError_t launch(void (*fn)(P...), const Shape &sh, long long units, si
 // have sent the other's, and so have read these. ok is each thread's own: it
 // turns false when its wait runs out, and the rows go on on what is there,
 // without waits of that thread. Thread 0 sends, and none after its own.
+// V: float2 or float4.
+template <typename V>
 struct Pair {
-    float2 sums[2][2];  // by buffer, CTA
+    V sums[2][2];  // by buffer, CTA
     uint64_t bar[2];
     tc::GiveUp<2> gave_up;
     int sent;  // rows, by a CTA whose thread 0 gave up
@@ -128,17 +130,16 @@ struct Pair {
         gave_up.sent[0] = gave_up.sent[1] = 0;
     }
     // tells both CTAs v, the same in all threads of one
-    __device__ __forceinline__ void send(float2 v, int buf, int rank, bool ok) {
+    __device__ __forceinline__ void send(V v, int buf, int rank, bool ok) {
         using namespace tc;
         if (threadIdx.x || !ok) return;
-        mbar_arrive_expect_tx(&bar[buf], 2 * sizeof(v));
+        mbar_arrive_expect_tx(&bar[buf], 2 * sizeof(V));
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-            cluster_st_async(cluster_map(&sums[buf][rank], r), v.x, v.y, cluster_map(&bar[buf], r));
+            cluster_st_async(cluster_map(&sums[buf][rank], r), v, cluster_map(&bar[buf], r));
     }
     // what both have sent, for the use-th time to buffer `buf`
-    __device__ __forceinline__ void receive(float2 &lower, float2 &upper, int buf, int use, unsigned long long wait_ns,
-                                            bool &ok) {
+    __device__ __forceinline__ void receive(V &lower, V &upper, int buf, int use, unsigned long long wait_ns, bool &ok) {
         if (ok && !tc::mbar_wait_cluster(&bar[buf], uint32_t(use) & 1, wait_ns)) {
             ok = false;
             if (threadIdx.x == 0) sent = 2 * use + buf + 1;
@@ -156,7 +157,7 @@ struct Pair {
             cluster_arrive_relaxed();
         }
         cluster_wait();  // neither CTA sends any more, and none leaves while the other may
-        if (threadIdx.x < 32) gave_up.settle(bar, rows, rank, 2, sizeof(float2));
+        if (threadIdx.x < 32) gave_up.settle(bar, rows, rank, 2, sizeof(V));
     }
 };
 

@@ -45,7 +45,7 @@ k_layernorm_bwd(const LnBwdArgs a) {
     constexpr int VE = L::VE;
     extern __shared__ __align__(16) uint8_t smem[];  // rows ahead
     __shared__ __align__(16) float2 red[2][32];
-    __shared__ ln::Pair pair;
+    __shared__ ln::Pair<float2> pair;
     if (!G) {
         if (threadIdx.x < 64) red[threadIdx.x / 32][threadIdx.x % 32] = make_float2(0.f, 0.f);
         if (PAIR && threadIdx.x == 0) pair.init();

@@ -240,6 +240,17 @@ __device__ __forceinline__ void cluster_st_async(uint32_t addr, float a, float b
                  : "memory");
 }
 
+// the same of four f32 (16-byte aligned, 16 bytes)
+__device__ __forceinline__ void cluster_st_async(uint32_t addr, float4 v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                     addr),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_st_async(uint32_t addr, float2 v, uint32_t bar) {
+    cluster_st_async(addr, v.x, v.y, bar);
+}
+
 // Copies of four bytes by the thread that asks, from global to shared memory,
 // which holds no register up; visible to that thread after its wait.
 __device__ __forceinline__ void async_copy_4(float *to, const float *from) {

@@ -391,7 +391,8 @@ int gdn_linear_recurrence_step(const gdn_problem *p, const void *x, const void *
  *   weight, bias [dv] f32, 16-byte aligned, or NULL (1 and 0)
  *   mean, rstd   [total_tokens] f32, 4-byte aligned, or NULL to skip: kept
  *                for the backward pass
- * The statistics are f32: the mean first, then the squares about it. (Rows too
+ * The statistics are f32: the mean first, then the squares about it; a mean
+ * above four deviations is corrected by that of the values about it. (Rows too
  * wide for one CTA are on two that wait for each other's sums, each wait at
  * most 2 s: GDN_ETIMEOUT in the device status. So in the backward pass.) */
 int gdn_layernorm(const gdn_problem *p, const void *x, const float *weight, const float *bias, float eps, void *y,
