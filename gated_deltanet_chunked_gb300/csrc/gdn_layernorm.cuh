@@ -295,6 +295,11 @@ struct Feed {
 #pragma unroll
         for (int s = 0; s < A::kAhead; ++s) ask();
     }
+    // whether element j of vector i is in the row
+    __device__ __forceinline__ bool in_row(int i, int j) const {
+        constexpr int kOf = 4 / int(sizeof(T));
+        return kMasks ? keep[kMasks ? i : 0][j / kOf] >> (j % kOf * 16) & 1 : at.has(i, j);
+    }
     __device__ __forceinline__ void ask() {
         if (left > 0) {
             constexpr int VE = L::VE;

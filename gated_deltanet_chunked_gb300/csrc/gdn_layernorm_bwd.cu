@@ -91,7 +91,17 @@ k_layernorm_bwd(const LnBwdArgs a) {
                 xhat[i][k] = vec::mul2(vec::add2(in[0][i].f2(k), vec::both(-mean)), vec::both(rstd));
                 g[i][k] = in[1][i].f2(k);
             }
-        if (live) {  // outside the row g is zero
+        // outside the row x and g are zero: so is what they add, unless mean rstd is infinite
+        if (!(fabsf(__fmul_rn(mean, rstd)) < INFINITY)) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    if (!feed.in_row(i, 2 * k)) xhat[i][k].x = 0.f;
+                    if (!feed.in_row(i, 2 * k + 1)) xhat[i][k].y = 0.f;
+                }
+        }
+        if (live) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll

@@ -81,3 +81,18 @@ def test_constant_rows_without_eps(cuda, width):
     e0 = R.SUM * R.f64(x[:, 0])
     ev = 1.01 * ((R.SUM + 6 * R.u) * e0 ** 2 + 2 * e0 * (R.SUM + 4 * R.u) * e0)
     assert (R.f64(rstd) >= 0.99 / np.sqrt(ev)).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("width", [1, 8, 9, 100, 600, 1001, 9001, 12000])
+def test_backward_of_a_mean_whose_normalised_value_overflows(cuda, width, dtype):
+    """mean * rstd is infinite, every normalised value finite: what a thread holds outside the row reaches no sum."""
+    gen = torch.Generator().manual_seed(width)
+    level = torch.tensor(1.5e36, dtype=dtype)
+    x = level.repeat(5, width)
+    dy, w = torch.randn(5, width, generator=gen).to(dtype), torch.randn(width, generator=gen) + 1
+    mean, rstd = level.float().repeat(5), torch.full((5,), 316.0)
+    res = gdn.gdn_layernorm_bwd(dy.to(cuda), x.to(cuda), mean.to(cuda), rstd.to(cuda), w.to(cuda))
+    ref = R.layernorm_bwd(R.f64(dy), R.f64(x), R.f64(mean), R.f64(rstd), R.f64(w), dtype)
+    for name, t in zip(("dx", "dweight", "dbias"), res):
+        R.assert_within(t, *ref[name], name)
