@@ -5,6 +5,7 @@
 // compute path per io dtype (f32: SIMT kernels; bf16: tensor-core kernels)
 // and no host-side fallback of any kind.
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "gdn_common.cuh"
@@ -343,6 +344,34 @@ int gdn_gating(const gdn_problem *p, const float *a, const float *b, const float
 namespace gdn {
 namespace {
 
+struct Span {
+    const void *p;
+    size_t bytes;
+};
+
+bool overlap(const Span &a, const Span &b) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+    return p && q && a.bytes && b.bytes && p < q + b.bytes && q < p + a.bytes;
+}
+
+// Whether an output overlaps an input or another output. The first `in_place`
+// outputs may be any of the first `as` inputs, in exactly its place.
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins, int in_place = 0, int as = 0) {
+    int o = 0;
+    for (auto a = outs.begin(); a != outs.end(); ++a, ++o) {
+        for (auto b = a + 1; b != outs.end(); ++b)
+            if (overlap(*a, *b)) return true;
+        int i = 0;
+        for (const Span &b : ins) {
+            const bool may = o < in_place && i++ < as && a->p == b.p;
+            if (!may && overlap(*a, b)) return true;
+        }
+    }
+    return false;
+}
+
+size_t io_bytes(const gdn_problem *p, size_t elements) { return elements * (p->io_dtype == GDN_DT_BF16 ? 2 : 4); }
+
 // Descriptor checks of the gated linear recurrence's forward and backward pass.
 int check_linrec(const gdn_problem *p, bool packed) {
     if (!p || p->hv <= 0 || p->dv <= 0 || p->num_seqs < 1 || p->total_tokens < 0) return GDN_EINVAL;
@@ -361,6 +390,18 @@ int check_linrec(const gdn_problem *p, bool packed) {
 bool gate_ok(const gdn_problem *p, const void *g) {
     return g && (p->flags & GDN_FLAG_GATE_CHANNEL ? aligned16(g) : aligned4(g));
 }
+
+// the recurrence's tensors: rows [total_tokens, hv, 128], gates, states [seqs, hv, 128], offsets
+Span rows_of(const gdn_problem *p, const void *x) {
+    return {x, io_bytes(p, size_t(p->total_tokens) * p->hv * kHeadDim)};
+}
+Span gates_of(const gdn_problem *p, const void *g) {
+    return p->flags & GDN_FLAG_GATE_CHANNEL ? rows_of(p, g) : Span{g, size_t(p->total_tokens) * p->hv * sizeof(float)};
+}
+Span states_of(const gdn_problem *p, const void *s, size_t seqs) {
+    return {s, seqs * p->hv * kHeadDim * sizeof(float)};
+}
+Span offsets_of(const gdn_problem *p, const void *cu) { return {cu, (size_t(p->num_seqs) + 1) * sizeof(int32_t)}; }
 
 RecArgs linrec_args(const gdn_problem *p, const void *x, const void *g, const float *s0, const int32_t *cu) {
     RecArgs a{};
@@ -385,11 +426,14 @@ int gdn_linear_recurrence(const gdn_problem *p, const void *x, const void *g, co
                           const int32_t *cu_seqlens, void *out, float *final_state, float *states, void *stream) {
     int st = check_linrec(p, cu_seqlens != nullptr);
     if (st) return st;
-    if (p->total_tokens > 0 && (!x || !out || x == out || g == out || !aligned16(x) || !aligned16(out) || !gate_ok(p, g)))
+    if (p->total_tokens > 0 && (!x || !out || !aligned16(x) || !aligned16(out) || !gate_ok(p, g)))
         return GDN_EINVAL;
     if (!aligned16(initial_state) || !aligned4(cu_seqlens) || !aligned16(final_state) || !aligned16(states))
         return GDN_EINVAL;
-    if (final_state && final_state == initial_state) return GDN_EINVAL;
+    const size_t seqs = size_t(p->num_seqs);
+    if (clash({rows_of(p, out), states_of(p, final_state, seqs), {states, gdn_linear_recurrence_states_size(p)}},
+              {rows_of(p, x), gates_of(p, g), states_of(p, initial_state, seqs), offsets_of(p, cu_seqlens)}))
+        return GDN_EINVAL;
     RecArgs a = linrec_args(p, x, g, initial_state, cu_seqlens);
     a.out = out; a.final_state = final_state; a.states = states;
     if (!(a.status = status_ptr())) return GDN_ECUDA;
@@ -405,13 +449,14 @@ int gdn_linear_recurrence_bwd(const gdn_problem *p, const void *dout, const void
     if (p->total_tokens > 0) {
         if (!dout || !x || !states || !dx || !gate_ok(p, g) || !gate_ok(p, dg)) return GDN_EINVAL;
         if (!aligned16(dout) || !aligned16(x) || !aligned16(states) || !aligned16(dx)) return GDN_EINVAL;
-        for (const void *in : {dout, x, g})
-            if (dx == in || dg == in) return GDN_EINVAL;
-        if (dx == dg) return GDN_EINVAL;
     }
     if (!aligned16(initial_state) || !aligned16(dfinal_state) || !aligned4(cu_seqlens) || !aligned16(dinitial_state))
         return GDN_EINVAL;
-    if (dinitial_state && (dinitial_state == initial_state || dinitial_state == dfinal_state)) return GDN_EINVAL;
+    const size_t seqs = size_t(p->num_seqs);
+    if (clash({rows_of(p, dx), gates_of(p, dg), states_of(p, dinitial_state, seqs)},
+              {rows_of(p, dout), rows_of(p, x), gates_of(p, g), {states, gdn_linear_recurrence_states_size(p)},
+               states_of(p, initial_state, seqs), states_of(p, dfinal_state, seqs), offsets_of(p, cu_seqlens)}))
+        return GDN_EINVAL;
     RecArgs a = linrec_args(p, x, g, initial_state, cu_seqlens);
     a.dout = dout; a.dfinal = dfinal_state; a.dx = dx; a.dg = dg; a.dinitial = dinitial_state;
     a.states = const_cast<float *>(states);  // read only
@@ -430,7 +475,9 @@ int gdn_linear_recurrence_step(const gdn_problem *p, const void *x, const void *
     if (p->num_seqs > 0) {
         if (!x || !state || !out || !gate_ok(p, g)) return GDN_EINVAL;
         if (!aligned16(x) || !aligned16(state) || !aligned16(out) || !aligned4(state_indices)) return GDN_EINVAL;
-        if (out == g || out == state) return GDN_EINVAL;
+        if (clash({rows_of(p, out), states_of(p, state, size_t(p->num_state_slots))},
+                  {rows_of(p, x), gates_of(p, g), {state_indices, size_t(p->num_seqs) * sizeof(int32_t)}}, 1, 1))
+            return GDN_EINVAL;
     }
     int *status = status_ptr();
     if (!status) return GDN_ECUDA;
@@ -451,6 +498,11 @@ int check_layernorm(const gdn_problem *p) {
     return p->dv > kLayerNormMaxWidth ? GDN_EUNSUPPORTED : GDN_OK;
 }
 
+// the norm's tensors: rows [total_tokens, dv], one value a row, one a column
+Span norm_rows(const gdn_problem *p, const void *x) { return {x, io_bytes(p, size_t(p->total_tokens) * p->dv)}; }
+Span row_stats(const gdn_problem *p, const void *s) { return {s, size_t(p->total_tokens) * sizeof(float)}; }
+Span columns(const gdn_problem *p, const void *w) { return {w, size_t(p->dv) * sizeof(float)}; }
+
 bool workspace_ok(const void *ws, size_t have, size_t need) {
     return ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) && have >= need;
 }
@@ -466,8 +518,10 @@ int gdn_layernorm(const gdn_problem *p, const void *x, const float *weight, cons
     if (st) return st;
     if (!(eps >= 0.f) || !aligned16(weight) || !aligned16(bias)) return GDN_EINVAL;
     if (p->total_tokens > 0) {
-        if (mean && mean == rstd) return GDN_EINVAL;
         if (!x || !y || !aligned16(x) || !aligned16(y) || !aligned4(mean) || !aligned4(rstd)) return GDN_EINVAL;
+        if (clash({norm_rows(p, y), row_stats(p, mean), row_stats(p, rstd)},
+                  {norm_rows(p, x), columns(p, weight), columns(p, bias)}, 1, 1))
+            return GDN_EINVAL;
     }
     int *status = status_ptr();
     if (!status) return GDN_ECUDA;
@@ -486,12 +540,17 @@ int gdn_layernorm_bwd(const gdn_problem *p, const void *dy, const void *x, const
     const int st = check_layernorm(p);
     if (st) return st;
     if (!aligned16(weight) || !aligned16(dweight) || !aligned16(dbias)) return GDN_EINVAL;
-    if (dweight && dweight == dbias) return GDN_EINVAL;
+    const size_t need = dweight || dbias ? gdn_layernorm_bwd_workspace_size(p) : 0;
+    // (the sums are written when all inputs have been read)
+    if (clash({norm_rows(p, dx), {workspace, need}},
+              {norm_rows(p, dy), norm_rows(p, x), row_stats(p, mean), row_stats(p, rstd), columns(p, weight)}, 1, 2) ||
+        clash({norm_rows(p, dx), {workspace, need}, columns(p, dweight), columns(p, dbias)}, {}))
+        return GDN_EINVAL;
     if (p->total_tokens > 0) {
         if (!dy || !x || !mean || !rstd || !dx) return GDN_EINVAL;
         if (!aligned16(dy) || !aligned16(x) || !aligned16(dx) || !aligned4(mean) || !aligned4(rstd))
             return GDN_EINVAL;
-        if ((dweight || dbias) && !workspace_ok(workspace, workspace_bytes, gdn_layernorm_bwd_workspace_size(p)))
+        if ((dweight || dbias) && !workspace_ok(workspace, workspace_bytes, need))
             return GDN_EINVAL;
     }
     int *status = status_ptr();
@@ -531,11 +590,16 @@ int gdn_gated_rmsnorm_bwd(const gdn_problem *p, const void *dy, const void *o, c
     if (!(eps >= 0.f) || !aligned16(d_weight)) return GDN_EINVAL;
     const long long rows = (long long)p->total_tokens * p->hv;
     if (rows > 0) {
-        if (!dy || !o || !z || !weight || !d_o || !d_z || d_o == d_z) return GDN_EINVAL;
+        if (!dy || !o || !z || !weight || !d_o || !d_z) return GDN_EINVAL;
         if (!aligned16(dy) || !aligned16(o) || !aligned16(z) || !aligned16(weight) || !aligned16(d_o) ||
             !aligned16(d_z))
             return GDN_EINVAL;
-        if (d_weight && !workspace_ok(workspace, workspace_bytes, gdn_gated_rmsnorm_bwd_workspace_size(p)))
+        const size_t need = d_weight ? gdn_gated_rmsnorm_bwd_workspace_size(p) : 0;
+        if (d_weight && !workspace_ok(workspace, workspace_bytes, need)) return GDN_EINVAL;
+        const size_t columns = kHeadDim * sizeof(float);
+        if (clash({rows_of(p, d_o), rows_of(p, d_z), {workspace, need}},
+                  {rows_of(p, dy), rows_of(p, o), rows_of(p, z), {weight, columns}}, 2, 3) ||
+            clash({rows_of(p, d_o), rows_of(p, d_z), {workspace, need}, {d_weight, columns}}, {}))
             return GDN_EINVAL;
     }
     return cuda_status(launch_gated_rmsnorm_bwd(dy, o, z, weight, eps, d_o, d_z, d_weight, workspace, rows,

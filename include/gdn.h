@@ -312,7 +312,12 @@ int gdn_causal_conv1d_silu_step(const gdn_problem *p, const void *x, const float
 int gdn_gating(const gdn_problem *p, const float *a, const float *b, const float *A_log, const float *dt_bias,
                float *g, float *beta, void *stream);
 
-/* ---- training and long sequences: recurrence, norm, output gate ---- */
+/* ---- training and long sequences: recurrence, norm, output gate ----
+ *
+ * An output (workspace and states among them) that overlaps an input or another
+ * output is refused with GDN_EINVAL, but for the places where one may be the
+ * other, which then have the same first byte. (dweight, dbias and d_weight are
+ * written when all inputs have been read: only other outputs count for them.) */
 
 /* Gated linear recurrence, a mixer whose state is one value per channel: for
  * every sequence, in token order, and every head h and channel j,
@@ -320,8 +325,7 @@ int gdn_gating(const gdn_problem *p, const float *a, const float *b, const float
  * s before the first token being the sequence's initial state. The sequence
  * layout, dense or packed, is gdn_chunk_fwd's. Only batch, seqlen, num_seqs,
  * total_tokens, hv, dv (128), io_dtype and flags of `p` are used.
- *   x, out        [total_tokens, hv, 128] io dtype, 16-byte aligned; out may
- *                 be neither x nor g
+ *   x, out        [total_tokens, hv, 128] io dtype, 16-byte aligned
  *   g             log-decays, g <= 0 (-inf forgets the state): [total_tokens,
  *                 hv] f32, 4-byte aligned, one per head (gdn_gating's g), or
  *                 with GDN_FLAG_GATE_CHANNEL [total_tokens, hv, 128] io dtype,
@@ -334,8 +338,7 @@ int gdn_gating(const gdn_problem *p, const float *a, const float *b, const float
  *                 start at 0, rise and end at total_tokens are recorded as
  *                 GDN_EDEVICE_INPUT and nothing is written.
  *   final_state   [num_seqs, hv, 128] f32, 16-byte aligned, or NULL; a
- *                 sequence without tokens gets its initial state (or zeros).
- *                 It may not be initial_state.
+ *                 sequence without tokens gets its initial state (or zeros)
  *   states        NULL, or f32 storage of gdn_linear_recurrence_states_size(p)
  *                 bytes, 16-byte aligned, that the backward pass reads: s
  *                 before every 64th row of the packed token axis (what it
@@ -364,7 +367,7 @@ size_t gdn_linear_recurrence_states_size(const gdn_problem *p);
  *   dinitial_state [num_seqs, hv, 128] f32, 16-byte aligned, or NULL; a
  *                  sequence without tokens gets its dfinal_state (or zeros)
  * The state is recomputed in f32 from `states` and x, not taken from the
- * rounded out. No output may be an input. */
+ * rounded out. */
 int gdn_linear_recurrence_bwd(const gdn_problem *p, const void *dout, const void *x, const void *g,
                               const float *states, const float *initial_state, const float *dfinal_state,
                               const int32_t *cu_seqlens, void *dx, void *dg, float *dinitial_state, void *stream);
