@@ -36,11 +36,11 @@ struct Shape {
 // barriers for an element; few rows (latency counts) over as many threads as
 // help. Rows that so take more than 512 threads are on two CTAs, which tell
 // each other their sums; or (LONG, the forward pass) on 512 threads with 32
-// elements each where they are aligned: 3000 x 16384 44 us, on two CTAs 57;
+// elements each where they are aligned: 3000 x 16384 43 us, on two CTAs 57;
 // unaligned, 3000 x 16383, 126 and 77. Many bf16 rows of more than 400 such
 // threads are better on half of them too, so that an SM has two CTAs: 8000 x
-// 8192 45 us against 57, 7000 wide 45 and 59, but 6000 wide 30 and 28, and 400
-// rows of 8192 5.9 and 5.1.
+// 8192 46 us against 57, 7000 wide 46 and 59, but 6000 wide 30 and 29, and 400
+// rows of 8192 5.9 and 5.2.
 template <typename T, bool LONG>
 inline Shape shape_of(int rows, int width) {
     constexpr int VE = 16 / int(sizeof(T)), kMost = 16 / VE;  // at most 16 elements a thread
@@ -53,7 +53,7 @@ inline Shape shape_of(int rows, int width) {
         s.nv = kMost;
         // LONG, bf16: not where three warps with one vector a lane do and two
         // with two would have three tenths of their places empty (83333 x 600:
-        // 43 us for 49, 71428 x 700: 54 for 63; the backward pass and f32 lose
+        // 45 us for 49, 71428 x 700: 56 for 63; the backward pass and f32 lose
         // as much, and so does 1040 wide with five warps for three)
         if (LONG && sizeof(T) == 2 && vecs < 90) s.nv = 1;
     }

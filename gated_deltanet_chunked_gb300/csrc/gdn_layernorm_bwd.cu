@@ -10,10 +10,10 @@
 // its registers; each CTA writes one partial row of each at its end, and a
 // second launch adds those in a fixed order (no atomics: the same call gives
 // the same bits). Rows too wide for the registers of 512 threads, with weights
-// and sums, are on a cluster of two CTAs (3000 x 16384 bf16: 75 us; on 1024
+// and sums, are on a cluster of two CTAs (3000 x 16384 bf16: 71 us; on 1024
 // threads of one CTA, with the sums in shared memory, 118).
 // Measured, bf16, of the copy rate (6783 GB/s): 16384 x 4096 66 us (0.90),
-// 32768 x 2048 66 (0.90), 524288 x 128 68 (0.87), 8000 x 8192 74 (0.78);
+// 32768 x 2048 66 (0.90), 524288 x 128 68 (0.87), 8000 x 8192 74 (0.79);
 // 4096 x 4096 24 (0.63), 17 of them without the sums: partial rows and their
 // second launch cost 5 to 7 us whatever the rows.
 #include "gdn_layernorm.cuh"
@@ -81,7 +81,7 @@ k_layernorm_bwd(const LnBwdArgs a) {
         const bool live = row < a.rows;
         const float mean = stats.x, rstd = stats.y;
         // PAIR: not before the exchange, whose fence waits for loads under way
-        // (3000 x 16384 bf16: 74.8 us, 87.8 before it); of unaligned rows they
+        // (3000 x 16384 bf16: 75 us, 88 before it); of unaligned rows they
         // are better late too (8000 x 4095: 66, 74), of aligned ones early (16384 x 4096: 66, 71)
         auto next_stats = [&] {
             if (row + 2 * at.step < a.rows) stats = make_float2(a.mean[row + 2 * at.step], a.rstd[row + 2 * at.step]);
@@ -251,7 +251,7 @@ struct Run {
     }
     static cudaError_t run(const ln::Shape &sh, LnBwdArgs &a, int &parts, cudaStream_t s) {
         // a few elements of the widest unaligned rows take a warp more, and then registers that others need
-        // (3000 x 16383 bf16: 128 us, 16375: 91)
+        // (3000 x 16383 bf16: 134 us, 16375: 94; spills)
         if constexpr (PAIR && !ALIGNED)
             if (sh.threads > 512) return go<544>(sh, a, parts, s);
         return go<G ? ln::kRowThreads : 512>(sh, a, parts, s);

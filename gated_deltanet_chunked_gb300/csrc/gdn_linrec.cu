@@ -33,7 +33,9 @@
 // Measured, bf16, 32 heads, of the copy rate (6783 GB/s) by a call's own bytes:
 // gates per channel, T = 65536: forward 260 us (0.91), backward 443 (0.90);
 // T = 4096: 25 (0.60), 37 (0.67); gates per head, 38429 packed rows: 136
-// (0.69), 260 (0.54). f32, 16 heads x 8000, per channel: 37 (0.79), 59 (0.82).
+// (0.69), 264 (0.53). f32, 16 heads x 8000, per channel: 37 (0.79), 58 (0.83).
+// Few heads on a long axis leave SMs idle (launch_clusters): 4 heads x 65536
+// per channel 82 (0.36), 117 (0.42), per head 67 (0.30), 169 (0.18).
 //
 // Sequences are boundaries on the one axis. A segment that holds a sequence's
 // first row (for the backward pass: last row) does not depend on what comes
@@ -407,11 +409,14 @@ struct HeadGates {
 // Decays of a segment's rows for the lane's two channels: pairs of their own,
 // in registers, or the head's one value, in shared memory. A decay's error is
 // taken as often as the state remembers rows: gates per head (few) and f32
-// gates are exact to a rounding (state off by 2e-7 where it remembers 55 rows,
-// 7e-7 at 1000); for bf16 gates per channel that would cost a quarter of the
-// forward pass's time (T = 65536 x 32 heads: 327 us against 262), and the
-// base-2 unit's two steps a decay are taken instead (6e-7 and 4e-6, against
-// 2^-9 of out).
+// gates are exact to a rounding (with u = 2^-24, 1.1 u at most; the state is off
+// by 2e-7 where it remembers 55 rows, 7e-7 at 1000). For bf16 gates per channel
+// that would cost a quarter of the forward pass's time (T = 65536 x 32 heads:
+// 327 us against 260), and the base-2 unit is taken instead. Over all bf16 gates
+// from -4 on it is off by 1.9 u at most, 0.5 to 0.85 u in the mean square and
+// -0.1 to -0.5 u in the mean, much as expf, which the decode step takes, is (1.9,
+// 0.5 to 0.7, -0.1 to 0.4); the state by 6e-7 and 4e-6. Below, where the state is
+// forgotten, log2 e's own rounding adds up to |g| / 4.5 u.
 template <typename T, bool CHANNEL, typename S>
 struct Decays;
 template <typename T, typename S>
@@ -879,7 +884,10 @@ cudaError_t active_clusters(F *fn, int ctas, int &clusters) {
 // The more CTAs a cluster has, the more of the axis is in work: as many as
 // there are tiles, as kMaxCluster, and as lets all clusters run at once (a
 // second wave would start on the whole axis when the first is done: at
-// T = 65536 with 64 units, 262 us with clusters of 4 against 289 with 8).
+// T = 65536 with 64 units, 262 us with clusters of 4 against 289 with 8). So a
+// unit has at most kMaxCluster CTAs: with few heads most SMs are without work,
+// and the time goes with the rounds (1 head x 65536 rows 61 us forward, 32 CTAs
+// of 128 rows; its bytes would take 7).
 template <typename R, typename... P, typename... A>
 cudaError_t launch_clusters(void (*fn)(P...), const RecArgs &a, cudaStream_t s, const A &...maps) {
     using S = typename R::S;
