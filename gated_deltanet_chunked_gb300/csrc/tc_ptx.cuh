@@ -6,7 +6,10 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 namespace gdn {
 namespace tc {
@@ -118,16 +121,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
 // thread that tries a phase is its own affair.
 constexpr uint64_t kShortLimitNs = 20000;
 
-__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+// mbar_wait that keeps limits of any length.
+__device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+    if (limit_ns >= kShortLimitNs && mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_test_wait(bar, parity))
         if (globaltimer_ns() - t0 > limit_ns) return false;
     return true;
-}
-
-// mbar_wait that keeps limits of any length.
-__device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
-    return limit_ns < kShortLimitNs || !mbar_try_wait(bar, parity) ? mbar_poll(bar, parity, limit_ns) : true;
 }
 
 // ---------------------------------------------------------------------------
@@ -264,7 +264,31 @@ __device__ __forceinline__ void async_copy_wait_all() { asm volatile("cp.async.w
 // all memory at cluster scope also drops what the SM has cached of global
 // memory and waits meanwhile.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t limit_ns = 2000000000ull) {
-    if (!mbar_wait_for(bar, parity, limit_ns)) return false;
+    auto done = [&](auto suspend) {
+        uint32_t ok;
+        if constexpr (suspend)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity)
+                : "memory");
+        else
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity)
+                : "memory");
+        return ok != 0;
+    };
+    if (limit_ns < kShortLimitNs || !done(std::true_type{})) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!done(std::false_type{}))
+            if (globaltimer_ns() - t0 > limit_ns) return false;
+    }
     asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
     return true;
 }
