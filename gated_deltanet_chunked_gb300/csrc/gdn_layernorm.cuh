@@ -282,12 +282,13 @@ struct Feed {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             any[i] = at.col[i] < at.width;
-            if (!kMasks) continue;
+            if constexpr (kMasks) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                constexpr int kOf = 4 / int(sizeof(T));  // elements of a word
-                keep[kMasks ? i : 0][k] = (at.has(i, k * kOf) ? sizeof(T) == 4 ? ~0u : 0xffffu : 0u) |
-                                           (kOf == 2 && at.has(i, k * kOf + kOf - 1) ? 0xffff0000u : 0u);
+                for (int k = 0; k < 4; ++k) {
+                    constexpr int kOf = 4 / int(sizeof(T));  // elements of a word
+                    keep[i][k] = (at.has(i, k * kOf) ? sizeof(T) == 4 ? ~0u : 0xffffu : 0u) |
+                                 (kOf == 2 && at.has(i, k * kOf + kOf - 1) ? 0xffff0000u : 0u);
+                }
             }
         }
 #pragma unroll
