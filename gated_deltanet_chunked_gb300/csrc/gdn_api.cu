@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "gdn_common.cuh"
+#include "gdn_linattn.cuh"
 #include "gdn_linrec.cuh"
 #include "tma_host.cuh"
 
@@ -105,7 +106,7 @@ using namespace gdn;
 
 extern "C" {
 
-int gdn_version(void) { return 103; }
+int gdn_version(void) { return 104; }
 
 const char *gdn_status_string(int status) {
     switch (status) {
@@ -604,6 +605,329 @@ int gdn_gated_rmsnorm_bwd(const gdn_problem *p, const void *dy, const void *o, c
     }
     return cuda_status(launch_gated_rmsnorm_bwd(dy, o, z, weight, eps, d_o, d_z, d_weight, workspace, rows,
                                                 p->io_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace gdn {
+namespace {
+
+constexpr int kBwdRoles = 3;  // dq, dv, dk
+
+int check_linattn(const gdn_problem *p, bool packed) {
+    int st = check_common(p);
+    if (st) return st;
+    if (p->num_seqs < 1) return GDN_EINVAL;
+    if (!packed) {
+        if (p->batch < 1 || p->seqlen < 0 || p->num_seqs != p->batch) return GDN_EINVAL;
+        if (int64_t(p->batch) * p->seqlen != p->total_tokens) return GDN_EINVAL;
+    }
+    if (p->total_tokens > INT32_MAX - 65536 || p->hv > (1 << 20) || p->num_seqs == INT32_MAX) return GDN_EINVAL;
+    // segments times heads times roles are counted in int (a segment has 32 rows at least)
+    if ((int64_t(p->total_tokens) / 32 + p->num_seqs) * p->hv * kBwdRoles > INT32_MAX) return GDN_EINVAL;
+    return GDN_OK;
+}
+
+struct LaLayout {
+    int seg_len, max_segs;
+    size_t first_off, segs_off, states_off, states_bytes, parts_off, part_bytes, total;
+};
+
+LaLayout la_layout(const gdn_problem *p, int roles) {
+    LaLayout l;
+    l.seg_len = la::segment_rows(p->total_tokens, p->num_seqs, p->hv, roles, p->io_dtype);
+    l.max_segs = p->total_tokens / l.seg_len + p->num_seqs;
+    l.first_off = 256;
+    l.segs_off = l.first_off + align256(sizeof(int) * (size_t(p->num_seqs) + 1));
+    l.states_off = l.segs_off + align256(sizeof(la::Seg) * size_t(l.max_segs));
+    l.states_bytes = l.seg_len < p->total_tokens ? size_t(l.max_segs) * p->hv * la::kState * sizeof(float) : 0;
+    l.parts_off = l.states_off + l.states_bytes * roles;
+    l.part_bytes = roles > 1 && p->hq != p->hv ? size_t(p->total_tokens) * p->hv * kHeadDim * sizeof(float) : 0;
+    l.total = l.parts_off + 2 * l.part_bytes;
+    return l;
+}
+
+la::Args la_args(const gdn_problem *p, const LaLayout &l, const float *decay, const int32_t *cu, void *ws) {
+    la::Args a{};
+    char *w = static_cast<char *>(ws);
+    a.decay = decay; a.cu = cu;
+    a.hv = p->hv; a.num_seqs = p->num_seqs; a.total_tokens = p->total_tokens;
+    a.dense_seqlen = cu ? 0 : p->seqlen;
+    a.seg_len = l.seg_len; a.max_segs = l.max_segs;
+    a.n_segs = reinterpret_cast<int *>(w);
+    a.seq_first = reinterpret_cast<int *>(w + l.first_off);
+    a.segs = reinterpret_cast<la::Seg *>(w + l.segs_off);
+    a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    return a;
+}
+
+// linear attention's tensors: rows of query and key heads, states of value heads
+Span qk_rows_of(const gdn_problem *p, const void *x) {
+    return {x, io_bytes(p, size_t(p->total_tokens) * p->hq * kHeadDim)};
+}
+Span head_states_of(const gdn_problem *p, const void *s) {
+    return {s, size_t(p->num_seqs) * p->hv * la::kState * sizeof(float)};
+}
+Span decays_of(const gdn_problem *p, const void *d) { return {d, size_t(p->hv) * sizeof(float)}; }
+
+cudaError_t launch_linattn(const gdn_problem *p, const la::Args &a, cudaStream_t s) {
+    return p->io_dtype == GDN_DT_BF16 ? la::launch_tc(a, s) : la::launch_simt(a, s);
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" {
+
+size_t gdn_linear_attention_workspace_size(const gdn_problem *p) {
+    return check_linattn(p, /*packed=*/true) == GDN_OK ? la_layout(p, 1).total : 0;  // whatever the layout
+}
+
+int gdn_linear_attention(const gdn_problem *p, const void *q, const void *k, const void *v, const float *decay,
+                         float scale, const float *initial_state, const int32_t *cu_seqlens, void *out,
+                         float *final_state, void *workspace, size_t workspace_bytes, void *stream) {
+    int st = check_linattn(p, cu_seqlens != nullptr);
+    if (st) return st;
+    if (!decay || !aligned4(decay)) return GDN_EINVAL;
+    if (p->total_tokens > 0) {
+        if (!q || !k || !v || !out) return GDN_EINVAL;
+        if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return GDN_EINVAL;
+    }
+    if (!aligned16(initial_state) || !aligned4(cu_seqlens) || !aligned16(final_state)) return GDN_EINVAL;
+    const LaLayout l = la_layout(p, 1);
+    if (!workspace_ok(workspace, workspace_bytes, l.total)) return GDN_EINVAL;
+    if (clash({rows_of(p, out), head_states_of(p, final_state), {workspace, l.total}},
+              {qk_rows_of(p, q), qk_rows_of(p, k), rows_of(p, v), decays_of(p, decay), head_states_of(p, initial_state),
+               offsets_of(p, cu_seqlens)}))
+        return GDN_EINVAL;
+    la::Args a = la_args(p, l, decay, cu_seqlens, workspace);
+    const int g = p->hv / p->hq;
+    a.roles = 1;
+    la::Role &r = a.role[0];
+    r.a = q; r.b = k; r.c = v; r.out = out;
+    r.init = initial_state; r.fin = final_state;
+    r.states = reinterpret_cast<float *>(static_cast<char *>(workspace) + l.states_off);
+    r.scale_in = 1.f; r.scale_out = scale;
+    r.ga = r.gb = g; r.gc = 1;
+    if (!(a.status = status_ptr())) return GDN_ECUDA;
+    return cuda_status(launch_linattn(p, a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_linear_attention_bwd_workspace_size(const gdn_problem *p) {
+    return check_linattn(p, /*packed=*/true) == GDN_OK ? la_layout(p, kBwdRoles).total : 0;
+}
+
+int gdn_linear_attention_bwd(const gdn_problem *p, const void *dout, const void *q, const void *k, const void *v,
+                             const float *decay, float scale, const float *initial_state, const float *dfinal_state,
+                             const int32_t *cu_seqlens, void *dq, void *dk, void *dv, float *dinitial_state,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+    int st = check_linattn(p, cu_seqlens != nullptr);
+    if (st) return st;
+    if (!decay || !aligned4(decay)) return GDN_EINVAL;
+    if (p->total_tokens > 0) {
+        if (!dout || !q || !k || !v || !dq || !dk || !dv) return GDN_EINVAL;
+        if (!aligned16(dout) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dq) || !aligned16(dk) ||
+            !aligned16(dv))
+            return GDN_EINVAL;
+    }
+    if (!aligned16(initial_state) || !aligned16(dfinal_state) || !aligned4(cu_seqlens) || !aligned16(dinitial_state))
+        return GDN_EINVAL;
+    const LaLayout l = la_layout(p, kBwdRoles);
+    if (!workspace_ok(workspace, workspace_bytes, l.total)) return GDN_EINVAL;
+    if (clash({qk_rows_of(p, dq), qk_rows_of(p, dk), rows_of(p, dv), head_states_of(p, dinitial_state),
+               {workspace, l.total}},
+              {rows_of(p, dout), qk_rows_of(p, q), qk_rows_of(p, k), rows_of(p, v), decays_of(p, decay),
+               head_states_of(p, initial_state), head_states_of(p, dfinal_state), offsets_of(p, cu_seqlens)}))
+        return GDN_EINVAL;
+    la::Args a = la_args(p, l, decay, cu_seqlens, workspace);
+    const int g = p->hv / p->hq;
+    char *ws = static_cast<char *>(workspace);
+    float *parts[2] = {nullptr, nullptr};
+    if (g > 1)
+        for (int i = 0; i < 2; ++i) parts[i] = reinterpret_cast<float *>(ws + l.parts_off + i * l.part_bytes);
+    a.roles = kBwdRoles;
+    for (int i = 0; i < kBwdRoles; ++i)
+        a.role[i].states = reinterpret_cast<float *>(ws + l.states_off + i * l.states_bytes);
+    la::Role &rq = a.role[0], &rv = a.role[1], &rk = a.role[2];
+    rq.a = dout; rq.b = v; rq.c = k; rq.out = g > 1 ? parts[0] : dq;
+    rq.init = initial_state; rq.swapped = 1;
+    rq.scale_in = 1.f; rq.scale_out = scale;
+    rq.ga = rq.gb = 1; rq.gc = g;
+    rq.partial = g > 1;
+    rv.a = k; rv.b = q; rv.c = dout; rv.out = dv;
+    rv.init = dfinal_state; rv.fin = dinitial_state;
+    rv.scale_in = scale; rv.scale_out = 1.f;
+    rv.ga = rv.gb = g; rv.gc = 1;
+    rv.against = 1;
+    rk.a = v; rk.b = dout; rk.c = q; rk.out = g > 1 ? parts[1] : dk;
+    rk.init = dfinal_state; rk.swapped = 1;
+    rk.scale_in = scale; rk.scale_out = 1.f;
+    rk.ga = rk.gb = 1; rk.gc = g;
+    rk.against = 1; rk.partial = g > 1;
+    if (!(a.status = status_ptr())) return GDN_ECUDA;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_linattn(p, a, s);
+    if (e == cudaSuccess && g > 1) {
+        e = la::launch_group_sum(parts[0], dq, p->total_tokens, p->hq, g, p->io_dtype, s);
+        if (e == cudaSuccess) e = la::launch_group_sum(parts[1], dk, p->total_tokens, p->hq, g, p->io_dtype, s);
+    }
+    return cuda_status(e);
+}
+
+int gdn_linear_attention_step(const gdn_problem *p, const void *q, const void *k, const void *v, const float *decay,
+                              float scale, void *state, const int32_t *state_indices, void *out, void *stream) {
+    int st = check_common(p, GDN_FLAG_STATE_BF16);
+    if (st) return st;
+    if (p->total_tokens != p->num_seqs || p->num_state_slots < 0) return GDN_EINVAL;
+    if (!state_indices && p->num_state_slots < p->num_seqs) return GDN_EINVAL;
+    if (int64_t(p->num_seqs) * p->hv > INT32_MAX) return GDN_EINVAL;
+    if (!decay || !aligned4(decay)) return GDN_EINVAL;
+    if (p->num_seqs > 0) {
+        if (!q || !k || !v || !state || !out) return GDN_EINVAL;
+        if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(out) ||
+            !aligned4(state_indices))
+            return GDN_EINVAL;
+        const size_t states = size_t(p->num_state_slots) * p->hv * la::kState * (p->flags & GDN_FLAG_STATE_BF16 ? 2 : 4);
+        if (clash({rows_of(p, out), {state, states}},
+                  {qk_rows_of(p, q), qk_rows_of(p, k), rows_of(p, v), decays_of(p, decay),
+                   {state_indices, size_t(p->num_seqs) * sizeof(int32_t)}}))
+            return GDN_EINVAL;
+    }
+    int *status = status_ptr();
+    if (!status) return GDN_ECUDA;
+    return cuda_status(launch_linattn_step(*p, q, k, v, decay, scale, state, state_indices, out, status,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace gdn {
+namespace {
+
+// heads * 128 elements of each of `tokens` rows that lie `stride` elements apart
+struct Slices {
+    const void *p;
+    int64_t stride, heads, tokens;
+    int size;  // of an element
+    size_t width() const { return size_t(heads) * kHeadDim * size; }
+    size_t pitch() const { return size_t(stride) * size; }
+    Span span() const { return {p, tokens > 0 ? size_t(tokens - 1) * pitch() + width() : 0}; }
+    bool ok() const {
+        return aligned16(p) && stride >= heads * kHeadDim && pitch() % 16 == 0 &&
+               (tokens == 0 || (p && stride <= INT64_MAX / 8 / tokens));
+    }
+};
+
+// Whether two slices overlap: those of the same pitch (of one projection's
+// rows) only where their rows' parts do.
+bool overlap(const Slices &a, const Slices &b) {
+    if (!overlap(a.span(), b.span())) return false;
+    if (a.stride != b.stride || a.tokens < 2) return true;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+    const size_t pitch = a.pitch(), ahead = q >= p ? (q - p) % pitch : (pitch - (p - q) % pitch) % pitch;
+    return ahead < a.width() || ahead + b.width() > pitch;
+}
+
+bool same(const Slices &a, const Slices &b) { return a.p == b.p && a.stride == b.stride && a.heads == b.heads; }
+
+int check_qk_rope(const gdn_qk_rope *r) {
+    if (!r || r->tokens < 0 || r->hq < 1 || r->hk < 1) return GDN_EINVAL;
+    if (r->io_dtype != GDN_DT_F32 && r->io_dtype != GDN_DT_BF16) return GDN_EINVAL;
+    if (r->rotary < 0 || r->rotary > kHeadDim || r->rotary % 2 || r->axes < 1 || r->axes > 8) return GDN_EINVAL;
+    if (r->hq > (1 << 16) || r->hk > (1 << 16) || !(r->eps >= 0.f)) return GDN_EINVAL;
+    return GDN_OK;
+}
+
+// the inputs that both passes read besides q and k
+bool rope_inputs_ok(const gdn_qk_rope *r) {
+    if (!aligned4(r->q_weight) || !aligned4(r->k_weight) || !aligned4(r->inv_freq) || !aligned4(r->positions) ||
+        !aligned4(r->pair_axis))
+        return false;
+    return r->tokens == 0 || r->rotary == 0 || (r->inv_freq && r->positions);
+}
+
+// Whether one of the outputs (slices and whole spans) overlaps an input or
+// another output; outs[i] may be ins[i] or, with gradients, ins[i + 2].
+bool rope_clash(const gdn_qk_rope *r, std::initializer_list<Slices> outs, std::initializer_list<Slices> ins,
+                std::initializer_list<Span> sums) {
+    const Span small[] = {{r->q_weight, kHeadDim * sizeof(float)}, {r->k_weight, kHeadDim * sizeof(float)},
+                          {r->inv_freq, size_t(r->rotary) / 2 * sizeof(float)},
+                          {r->positions, size_t(r->axes) * r->tokens * sizeof(int32_t)},
+                          {r->pair_axis, size_t(r->rotary) / 2 * sizeof(int32_t)}};
+    int o = 0;
+    for (auto a = outs.begin(); a != outs.end(); ++a, ++o) {
+        for (auto b = a + 1; b != outs.end(); ++b)
+            if (overlap(*a, *b)) return true;
+        int i = 0;
+        for (const Slices &b : ins) {
+            if (!(i++ % 2 == o && same(*a, b)) && overlap(*a, b)) return true;
+        }
+        for (const Span &b : small)
+            if (overlap(a->span(), b)) return true;
+    }
+    for (auto a = sums.begin(); a != sums.end(); ++a) {
+        for (auto b = a + 1; b != sums.end(); ++b)
+            if (overlap(*a, *b)) return true;
+        for (const Slices &b : outs)
+            if (overlap(*a, b.span())) return true;
+        for (const Slices &b : ins)
+            if (overlap(*a, b.span())) return true;
+        for (const Span &b : small)
+            if (overlap(*a, b)) return true;
+    }
+    return false;
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" {
+
+int gdn_qk_norm_rope(const gdn_qk_rope *r, void *out_q, int64_t out_q_stride, void *out_k, int64_t out_k_stride,
+                     void *stream) {
+    const int st = check_qk_rope(r);
+    if (st) return st;
+    const int size = r->io_dtype == GDN_DT_BF16 ? 2 : 4;
+    const Slices q{r->q, r->q_stride, r->hq, r->tokens, size}, k{r->k, r->k_stride, r->hk, r->tokens, size};
+    const Slices oq{out_q, out_q_stride, r->hq, r->tokens, size}, ok{out_k, out_k_stride, r->hk, r->tokens, size};
+    if (!q.ok() || !k.ok() || !oq.ok() || !ok.ok() || !rope_inputs_ok(r)) return GDN_EINVAL;
+    if (rope_clash(r, {oq, ok}, {q, k}, {})) return GDN_EINVAL;
+    int *status = status_ptr();
+    if (!status) return GDN_ECUDA;
+    void *const y[2] = {out_q, out_k};
+    const long long ys[2] = {out_q_stride, out_k_stride};
+    return cuda_status(launch_qk_rope(*r, nullptr, nullptr, y, ys, nullptr, nullptr, status,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_rope *r) {
+    return check_qk_rope(r) == GDN_OK ? qk_rope_bwd_workspace(r->tokens, r->hq + r->hk, r->io_dtype) : 0;
+}
+
+int gdn_qk_norm_rope_bwd(const gdn_qk_rope *r, const void *dout_q, int64_t dout_q_stride, const void *dout_k,
+                         int64_t dout_k_stride, void *dq, int64_t dq_stride, void *dk, int64_t dk_stride,
+                         float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes, void *stream) {
+    const int st = check_qk_rope(r);
+    if (st) return st;
+    const int size = r->io_dtype == GDN_DT_BF16 ? 2 : 4;
+    const Slices q{r->q, r->q_stride, r->hq, r->tokens, size}, k{r->k, r->k_stride, r->hk, r->tokens, size};
+    const Slices gq{dout_q, dout_q_stride, r->hq, r->tokens, size}, gk{dout_k, dout_k_stride, r->hk, r->tokens, size};
+    const Slices oq{dq, dq_stride, r->hq, r->tokens, size}, ok{dk, dk_stride, r->hk, r->tokens, size};
+    if (!q.ok() || !k.ok() || !gq.ok() || !gk.ok() || !oq.ok() || !ok.ok() || !rope_inputs_ok(r)) return GDN_EINVAL;
+    if (!aligned4(dq_weight) || !aligned4(dk_weight)) return GDN_EINVAL;
+    const size_t need = dq_weight || dk_weight ? gdn_qk_norm_rope_bwd_workspace_size(r) : 0;
+    if (need && !workspace_ok(workspace, workspace_bytes, need)) return GDN_EINVAL;
+    if (rope_clash(r, {oq, ok}, {q, k, gq, gk},
+                   {{workspace, need}, {dq_weight, kHeadDim * sizeof(float)}, {dk_weight, kHeadDim * sizeof(float)}}))
+        return GDN_EINVAL;
+    int *status = status_ptr();
+    if (!status) return GDN_ECUDA;
+    const void *const dy[2] = {dout_q, dout_k};
+    const long long ds[2] = {dout_q_stride, dout_k_stride};
+    void *const y[2] = {dq, dk};
+    const long long ys[2] = {dq_stride, dk_stride};
+    float *const dw[2] = {dq_weight, dk_weight};
+    return cuda_status(launch_qk_rope(*r, dy, ds, y, ys, dw, workspace, status, static_cast<cudaStream_t>(stream)));
 }
 
 int gdn_read_device_status(void *stream, int clear) {

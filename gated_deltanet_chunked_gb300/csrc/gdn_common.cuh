@@ -116,6 +116,11 @@ size_t gated_rmsnorm_bwd_workspace(long long rows, int io_dtype);
 cudaError_t launch_gated_rmsnorm_bwd(const void *dy, const void *o, const void *z, const float *weight, float eps,
                                      void *d_o, void *d_z, float *d_weight, void *workspace, long long rows,
                                      int io_dtype, cudaStream_t s);
+size_t qk_rope_bwd_workspace(long long tokens, int heads, int io_dtype);
+// dy null: the forward pass into y; else the backward pass into y (dx) and dweight
+cudaError_t launch_qk_rope(const gdn_qk_rope &r, const void *const dy[2], const long long dy_stride[2],
+                           void *const y[2], const long long y_stride[2], float *const dweight[2], void *workspace,
+                           int *status, cudaStream_t s);
 cudaError_t launch_prefill_simt(const PrefillArgs &a, void *ws_data, cudaStream_t s);
 size_t prefill_simt_workspace(int max_chunks, int hv);
 cudaError_t launch_prefill_tc(const PrefillArgs &a, void *ws_data, cudaStream_t s);

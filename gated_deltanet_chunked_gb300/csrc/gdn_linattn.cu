@@ -1,0 +1,193 @@
+// Linear attention with a decay for each head: segments of the sequences, the
+// chain of their sums, sums over a group's heads, and how long segments are.
+#include "gdn_linattn.cuh"
+
+namespace gdn {
+namespace la {
+namespace {
+
+constexpr int kTableThreads = 1024;
+
+__device__ __forceinline__ int seq_begin(const Args &a, int n) { return a.cu ? a.cu[n] : n * a.dense_seqlen; }
+// an empty sequence has one empty segment: its state passes through
+__device__ __forceinline__ int seq_segs(int len, int seg_len) { return len > 0 ? (len - 1) / seg_len + 1 : 1; }
+
+// One CTA: checks the offsets (start at 0, do not decrease, end at the token
+// count), counts each sequence's segments, and lists them.
+__global__ void __launch_bounds__(kTableThreads) k_la_table(const __grid_constant__ Args a) {
+    __shared__ int wsum[32];
+    __shared__ int bad;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, N = a.num_seqs;
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    const int per = (N + kTableThreads - 1) / kTableThreads;
+    const int n0 = min(N, tid * per), n1 = min(N, n0 + per);
+    int local = 0, last = n0 < n1 ? seq_begin(a, n0) : 0;
+    if (n0 == 0 && n0 < n1 && last != 0) bad = 1;
+    for (int n = n0; n < n1; ++n) {
+        const int e = seq_begin(a, n + 1);
+        if (e < last || last < 0 || e > a.total_tokens) bad = 1;
+        else local += seq_segs(e - last, a.seg_len);
+        last = e;
+    }
+    if (n0 < n1 && n1 == N && last != a.total_tokens) bad = 1;
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) wsum[wid] = incl;
+    __syncthreads();
+    if (bad) {  // the same for all behind the barrier
+        if (tid == 0) {
+            record_status(a.status, GDN_EDEVICE_INPUT);
+            *a.n_segs = 0;
+        }
+        return;
+    }
+    if (wid == 0) {
+        int x = wsum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += t;
+        }
+        wsum[lane] = x;
+    }
+    __syncthreads();
+    int first = (wid > 0 ? wsum[wid - 1] : 0) + incl - local;
+    const int total = wsum[31];
+    if (tid == 0) {
+        *a.n_segs = total;
+        a.seq_first[N] = total;
+    }
+    for (int n = n0; n < n1; ++n) {
+        a.seq_first[n] = first;
+        first += seq_segs(seq_begin(a, n + 1) - seq_begin(a, n), a.seg_len);
+    }
+    __syncthreads();
+    for (int i = tid; i < total; i += kTableThreads) {
+        int lo = 0, hi = N - 1;  // the last sequence whose first segment is at most i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.seq_first[mid] <= i) lo = mid;
+            else hi = mid - 1;
+        }
+        const int b = seq_begin(a, lo), len = seq_begin(a, lo + 1) - b, k = i - a.seq_first[lo];
+        const int rest = len - k * a.seg_len;
+        a.segs[i] = Seg{lo, b + k * a.seg_len, min(a.seg_len, rest),
+                        (k == 0 ? kFirst : 0) | (rest <= a.seg_len ? kLast : 0)};
+    }
+}
+
+// Chains the segments' sums: behind it, states[seg] is the state that enters
+// the segment (of those that another one comes before). Four elements a
+// thread; a sequence's segments one after the other.
+constexpr int kChainThreads = 256, kChainCtas = kState / 4 / kChainThreads;
+
+__global__ void __launch_bounds__(kChainThreads) k_la_chain(const __grid_constant__ Args a) {
+    if (*a.n_segs == 0) return;
+    const int part = blockIdx.x % kChainCtas, rest = blockIdx.x / kChainCtas, h = rest % a.hv;
+    const Role &r = a.role[rest / a.hv];
+    const float decay = a.decay[h];
+    const int e = (part * kChainThreads + threadIdx.x) * 4;
+    const size_t per_head = size_t(a.hv) * kState;
+    for (int n = blockIdx.y; n < a.num_seqs; n += gridDim.y) {
+        const int s0 = a.seq_first[n], s1 = a.seq_first[n + 1];
+        if (s1 - s0 < 2) continue;
+        const int step = r.against ? -1 : 1, from = r.against ? s1 - 1 : s0, count = s1 - s0;
+        float *states = r.states + size_t(h) * kState + e;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r.init) {
+            const float *init = r.init + size_t(n) * per_head + size_t(h) * kState;
+            if (r.swapped) {
+                const int b = e / kHeadDim, c = e % kHeadDim;
+                s = make_float4(init[c * kHeadDim + b], init[(c + 1) * kHeadDim + b], init[(c + 2) * kHeadDim + b],
+                                init[(c + 3) * kHeadDim + b]);
+            } else {
+                s = *reinterpret_cast<const float4 *>(init + e);
+            }
+        }
+        float4 sum = *reinterpret_cast<const float4 *>(states + size_t(from) * per_head);
+        for (int k = 1; k < count; ++k) {
+            const int at = from + k * step;
+            float4 next = sum;
+            if (k + 1 < count) next = *reinterpret_cast<const float4 *>(states + size_t(at) * per_head);
+            const Seg seg = a.segs[at - step];
+            const float keep = power(decay, seg.len - 1 + entry_offset(r, seg, true));
+            s.x = fmaf(keep, s.x, sum.x), s.y = fmaf(keep, s.y, sum.y);
+            s.z = fmaf(keep, s.z, sum.z), s.w = fmaf(keep, s.w, sum.w);
+            *reinterpret_cast<float4 *>(states + size_t(at) * per_head) = s;
+            sum = next;
+        }
+    }
+}
+
+// y[t, hq] = sum over the group's heads of x[t, hv], in their order, rounded once
+template <typename T>
+__global__ void __launch_bounds__(256) k_la_group_sum(const float *__restrict__ x, T *__restrict__ y, long long items,
+                                                      int group) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // four channels of a (token, query head)
+    if (i >= items) return;
+    const float *from = x + (i / 32 * group) * kHeadDim + (i % 32) * 4;
+    float4 s = *reinterpret_cast<const float4 *>(from);
+    for (int g = 1; g < group; ++g) {
+        const float4 v = *reinterpret_cast<const float4 *>(from + g * kHeadDim);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    vec::Pack<T, 4> out;
+    out.set2(0, make_float2(s.x, s.y));
+    out.set2(1, make_float2(s.z, s.w));
+    out.store(y + i * 4);
+}
+
+}  // namespace
+
+cudaError_t launch_table(const Args &a, cudaStream_t s) {
+    LaunchScope scope(GDN_K_LINATTN_TABLE, s);
+    k_la_table<<<1, kTableThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_chain(const Args &a, cudaStream_t s) {
+    LaunchScope scope(GDN_K_LINATTN_CHAIN, s);
+    k_la_chain<<<dim3(unsigned(kChainCtas) * unsigned(a.hv) * unsigned(a.roles), unsigned(a.num_seqs < 1024 ? a.num_seqs : 1024)),
+                 kChainThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_group_sum(const float *x, void *y, long long rows, int heads, int group, int io_dtype,
+                             cudaStream_t s) {
+    const long long items = rows * heads * 32;
+    if (items == 0) return cudaSuccess;
+    LaunchScope scope(GDN_K_LINATTN_GROUP_SUM, s);
+    const unsigned ctas = unsigned((items + 255) / 256);
+    if (io_dtype == GDN_DT_BF16)
+        k_la_group_sum<<<ctas, 256, 0, s>>>(x, static_cast<__nv_bfloat16 *>(y), items, group);
+    else
+        k_la_group_sum<<<ctas, 256, 0, s>>>(x, static_cast<float *>(y), items, group);
+    return cudaGetLastError();
+}
+
+int segment_rows(long long total_tokens, long long num_seqs, int hv, int roles, int io_dtype) {
+    constexpr int kSms = 152;
+    const int unit = io_dtype == GDN_DT_BF16 ? 128 : 32;
+    const long long slots = io_dtype == GDN_DT_BF16 ? kSms : 2 * kSms;
+    const double walk = io_dtype == GDN_DT_BF16 ? 1.8 : 4.0, sum = io_dtype == GDN_DT_BF16 ? 0.9 : 2.0, start = 5.0;
+    const long long units = (total_tokens + unit - 1) / unit;
+    long long best = 1;
+    double least = 0;
+    for (long long u = 1;; u = u < 16 ? u + 1 : u + u / 8) {
+        if (u > units && u > 1) u = units;
+        const long long items = ((units + u - 1) / u + num_seqs - 1) * hv * roles;
+        const double waves = double((items + slots - 1) / slots);
+        const double t = waves * (start + double(u) * (u < units ? walk + sum : walk));
+        if (u == 1 || t < least) least = t, best = u;
+        if (u >= units || u * unit >= 65536) break;
+    }
+    return int(best * unit);
+}
+
+}  // namespace la
+}  // namespace gdn

@@ -41,7 +41,8 @@ const char *const kNames[GDN_K_COUNT] = {
     "chunk_table", "prep_simt", "state_simt", "output_simt", "recurrent_step",
     "chunk_fused_tc", "recurrent_step_gated", "gated_rmsnorm", "conv1d_silu", "gating", "conv1d_step",
     "linear_recurrence", "linear_recurrence_bwd", "linear_recurrence_step", "layernorm", "layernorm_bwd",
-    "gated_rmsnorm_bwd", "row_sums",
+    "gated_rmsnorm_bwd", "row_sums", "linear_attention_table", "linear_attention_sum", "linear_attention_chain",
+    "linear_attention_walk", "linear_attention_group_sum", "linear_attention_step", "qk_norm_rope", "qk_norm_rope_bwd",
 };
 
 }  // namespace

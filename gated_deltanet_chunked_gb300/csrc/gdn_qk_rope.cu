@@ -1,0 +1,343 @@
+// Norm of every query and key head and the rotation by position in one pass
+// (gdn_qk_norm_rope), and its backward pass. For a head's row x of 128 channels
+//   n = x / sqrt(mean x^2 + eps) * weight,
+//   (y_a, y_b) = (n_a cos t - n_b sin t, n_a sin t + n_b cos t)
+// for each of the rotated pairs (a, b), t = position * frequency of the pair.
+// Backward, with dn the gradient turned back, xhat = x r, u = dn weight:
+//   dx = r (u - xhat mean(u xhat)),  dweight = sum over rows of dn xhat.
+//
+// Bound by memory: each row is read and written once, 16 bytes a lane. A CTA
+// takes the rows of a few tokens at a time and has their angles' sines and
+// cosines in shared memory, once for all heads of a token.
+//
+// Angles. A position has up to 31 bits and t is wanted to 2^-24 of a turn:
+// frequency / 2 pi is held in three f32 (from 64 bits), the position in two
+// whole f32, and the parts' products, exact by FMA, lose their whole turns
+// before they are added.
+#include "gdn_common.cuh"
+#include "gdn_vec.cuh"
+
+namespace gdn {
+namespace {
+
+using vec::both;
+using vec::fma2;
+using vec::mul2;
+
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = kHeadDim / 2;
+constexpr int kMaxTokens = 32;  // of a CTA's step
+
+struct RopeArgs {
+    const void *x[2];         // q, k: [tokens, heads, 128], tokens `stride` elements apart
+    const void *dy[2];        // backward
+    void *y[2];               // forward: y; backward: dx
+    long long xs[2], ds[2], ys[2];
+    const float *weight[2];   // [128] or null for ones
+    const float *inv_freq;    // [pairs]
+    const int *positions;     // [axes, tokens]
+    const int *pair_axis;     // [pairs] or null
+    float *partial[2];        // backward: [CTAs, 128] sums of dweight, or null
+    float eps;
+    int tokens, heads[2], pairs, axes;
+    int step;                 // tokens of a CTA's step
+    int *status;
+};
+
+// How a row's pairs lie: next to each other, or half a rotation apart, whole
+// 16-byte lanes from lane to lane or not.
+enum Pairs { kNeighbours, kLanes, kAnywhere };
+
+__device__ __forceinline__ float less_turns(float x) { return x - rintf(x); }
+
+// cos and sin of position * frequency
+__device__ __forceinline__ float2 angle(int pos, const float3 &f) {
+    const float p1 = float(pos & ~0xfff), p0 = float(pos & 0xfff);
+    const float a = p1 * f.x, b = p0 * f.x, c = p1 * f.y;
+    float lo = fmaf(p1, f.x, -a);
+    lo = less_turns(lo) + less_turns(c);
+    lo += fmaf(p0, f.x, -b) + fmaf(p1, f.y, -c) + (p0 * f.y + p1 * f.z);
+    float t = less_turns(less_turns(a) + less_turns(b));
+    t = less_turns(t + less_turns(lo));
+    float s, co;
+    sincospif(2.f * t, &s, &co);
+    return make_float2(co, s);
+}
+
+template <typename T>
+struct Layout {
+    static constexpr int kVe = 16 / sizeof(T), kLanesOfRow = kHeadDim / kVe, kRows = kThreads / kLanesOfRow;
+};
+
+struct RopeShared {
+    float2 turn[2][kMaxTokens * kMaxPairs];
+    float weight[2][kHeadDim];
+    int pos_bad;
+};
+
+// The partner's channels of a lane's VE channels in a row of f32 values, for
+// pairs that do not lie in whole lanes: through shared memory.
+template <int VE>
+__device__ __forceinline__ void partners(float *row, int ch, int pairs, const float2 *v, float2 *o) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < VE / 2; ++i) *reinterpret_cast<float2 *>(row + ch + 2 * i) = v[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+        const int c = ch + i;
+        const float w = c < 2 * pairs ? row[c < pairs ? c + pairs : c - pairs] : 0.f;
+        (i & 1 ? o[i / 2].y : o[i / 2].x) = w;
+    }
+}
+
+// Turns a lane's VE channels v (partners' o) by `turn` (kBack: back); channels
+// behind the rotated ones stay.
+template <int VE, int P, bool kBack>
+__device__ __forceinline__ void rotate(const float2 *turn, int ch, int pairs, float2 *v, const float2 *o) {
+    if (ch >= 2 * pairs) return;
+    if constexpr (P == kNeighbours) {
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+            if (ch / 2 + i >= pairs) break;
+            float2 t = turn[ch / 2 + i];
+            if (kBack) t.y = -t.y;
+            v[i] = make_float2(v[i].x * t.x - v[i].y * t.y, v[i].x * t.y + v[i].y * t.x);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            const int c = ch + i;
+            if (P == kAnywhere && c >= 2 * pairs) break;
+            const bool first = c < pairs;
+            const float2 t = turn[first ? c : c - pairs];
+            const float sn = first != kBack ? -t.y : t.y;
+            float &a = i & 1 ? v[i / 2].y : v[i / 2].x;
+            const float b = i & 1 ? o[i / 2].y : o[i / 2].x;
+            a = fmaf(a, t.x, b * sn);
+        }
+    }
+}
+
+template <typename T, int P, bool kBwd>
+__global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid_constant__ RopeArgs a) {
+    using L = Layout<T>;
+    constexpr int VE = L::kVe;
+    using Row = vec::Pack<T, VE>;
+    __shared__ __align__(16) RopeShared s;
+    __shared__ __align__(16) float swap[P == kAnywhere ? L::kRows : 1][kHeadDim];
+    const int tid = threadIdx.x, lane = tid % L::kLanesOfRow, group = tid / L::kLanesOfRow, ch = lane * VE;
+    const int heads = a.heads[0] + a.heads[1];
+    if (tid < kHeadDim) {
+        s.weight[0][tid] = a.weight[0] ? a.weight[0][tid] : 1.f;
+        s.weight[1][tid] = a.weight[1] ? a.weight[1][tid] : 1.f;
+    }
+    // this thread's pair of the angles (kMaxPairs divides the CTA's threads)
+    const int pair = tid % kMaxPairs;
+    int axis = 0;
+    float3 f = make_float3(0.f, 0.f, 0.f);
+    if (pair < a.pairs) {
+        if (a.pair_axis) axis = a.pair_axis[pair];
+        const double turns = double(a.inv_freq[pair]) * 0.15915494309189533577;
+        f.x = float(turns);
+        f.y = float(turns - double(f.x));
+        f.z = float(turns - double(f.x) - double(f.y));
+    }
+    if (__syncthreads_or(axis < 0 || axis >= a.axes)) {
+        if (tid == 0) record_status(a.status, GDN_EDEVICE_INPUT);
+        if (kBwd && tid < kHeadDim)
+            for (int w = 0; w < 2; ++w)
+                if (a.partial[w]) a.partial[w][size_t(blockIdx.x) * kHeadDim + tid] = 0.f;
+        return;
+    }
+    const int *pos = a.positions + size_t(axis) * a.tokens;
+    float2 dw[2][VE / 2] = {};
+    int which = 0;
+    for (long long t0 = (long long)blockIdx.x * a.step; t0 < a.tokens; t0 += (long long)gridDim.x * a.step, which ^= 1) {
+        const int step = int(min((long long)a.step, a.tokens - t0)), rows = step * heads;
+        float2 *turn = s.turn[which];  // two in turn, so that one barrier a step is enough
+        // two rows a lane group at a time; the first loads are under way while the angles are taken
+        for (int r0 = 0; r0 < rows; r0 += 2 * L::kRows) {
+            Row x[2], d[2];
+            bool has[2], is_k[2];
+            int token[2];
+            long long at[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int row = r0 + k * L::kRows + group;
+                has[k] = row < rows;
+                token[k] = has[k] ? row / heads : 0;
+                const int h = has[k] ? row % heads : 0;
+                is_k[k] = h >= a.heads[0];
+                const int w = is_k[k];
+                const long long t = t0 + token[k];
+                const int hw = is_k[k] ? h - a.heads[0] : h;
+                at[k] = t * a.ys[w] + hw * kHeadDim + ch;
+                x[k].zero();
+                if (kBwd) d[k].zero();
+                if (has[k]) {
+                    x[k].load(static_cast<const T *>(a.x[w]) + t * a.xs[w] + hw * kHeadDim + ch);
+                    if (kBwd) d[k].load(static_cast<const T *>(a.dy[w]) + t * a.ds[w] + hw * kHeadDim + ch);
+                }
+            }
+            if (r0 == 0) {
+                if (pair < a.pairs)
+                    for (int k = tid / kMaxPairs; k < step; k += kThreads / kMaxPairs)
+                        turn[k * kMaxPairs + pair] = angle(pos[t0 + k], f);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int w = is_k[k];
+                const float *weight = &s.weight[w][ch];
+                const float2 *tt = turn + token[k] * kMaxPairs;
+                float2 v[VE / 2], o[VE / 2];
+                float2 ss = both(0.f);
+#pragma unroll
+                for (int i = 0; i < VE / 2; ++i) {
+                    v[i] = x[k].f2(i);
+                    ss = fma2(v[i], v[i], ss);
+                }
+                if constexpr (!kBwd) {
+                    const float r = rsqrtf(vec::group_sum<L::kLanesOfRow>(vec::sum2(ss)) * (1.f / kHeadDim) + a.eps);
+                    if constexpr (P == kLanes) {
+                        // the partner lane's channels come as they lie in memory, and take their weights here
+                        const int off = a.pairs / VE, to = lane < off ? lane + off : lane < 2 * off ? lane - off : lane;
+                        const float *wp = &s.weight[w][to * VE];
+                        Row p;
+                        constexpr int kWords = sizeof(Row) / 4;
+                        const uint32_t *from = reinterpret_cast<const uint32_t *>(&x[k]);
+                        uint32_t *into = reinterpret_cast<uint32_t *>(&p);
+#pragma unroll
+                        for (int i = 0; i < kWords; ++i) into[i] = __shfl_sync(0xffffffffu, from[i], to, L::kLanesOfRow);
+#pragma unroll
+                        for (int i = 0; i < VE / 2; ++i)
+                            o[i] = mul2(mul2(p.f2(i), both(r)), *reinterpret_cast<const float2 *>(wp + 2 * i));
+                    }
+#pragma unroll
+                    for (int i = 0; i < VE / 2; ++i)
+                        v[i] = mul2(mul2(v[i], both(r)), *reinterpret_cast<const float2 *>(weight + 2 * i));
+                    if constexpr (P == kAnywhere) partners<VE>(swap[group], ch, a.pairs, v, o);
+                    rotate<VE, P, false>(tt, ch, a.pairs, v, o);
+#pragma unroll
+                    for (int i = 0; i < VE / 2; ++i) x[k].set2(i, v[i]);
+                } else {
+                    float2 n[VE / 2];
+#pragma unroll
+                    for (int i = 0; i < VE / 2; ++i) n[i] = d[k].f2(i);
+                    if constexpr (P == kLanes) {
+                        const int off = a.pairs / VE, to = lane < off ? lane + off : lane < 2 * off ? lane - off : lane;
+                        Row p;
+                        constexpr int kWords = sizeof(Row) / 4;
+                        const uint32_t *from = reinterpret_cast<const uint32_t *>(&d[k]);
+                        uint32_t *into = reinterpret_cast<uint32_t *>(&p);
+#pragma unroll
+                        for (int i = 0; i < kWords; ++i) into[i] = __shfl_sync(0xffffffffu, from[i], to, L::kLanesOfRow);
+#pragma unroll
+                        for (int i = 0; i < VE / 2; ++i) o[i] = p.f2(i);
+                    }
+                    if constexpr (P == kAnywhere) partners<VE>(swap[group], ch, a.pairs, n, o);
+                    rotate<VE, P, true>(tt, ch, a.pairs, n, o);
+                    float2 u[VE / 2], ux = both(0.f);
+#pragma unroll
+                    for (int i = 0; i < VE / 2; ++i) {
+                        u[i] = mul2(n[i], *reinterpret_cast<const float2 *>(weight + 2 * i));
+                        ux = fma2(u[i], v[i], ux);
+                    }
+                    const float2 sums = vec::group_sum2<L::kLanesOfRow>(vec::sum2(ss), vec::sum2(ux));
+                    const float r = rsqrtf(sums.x * (1.f / kHeadDim) + a.eps);
+                    const float m = sums.y * r * (1.f / kHeadDim);  // mean(u xhat)
+#pragma unroll
+                    for (int i = 0; i < VE / 2; ++i) {
+                        const float2 xhat = mul2(v[i], both(r));
+                        x[k].set2(i, mul2(both(r), fma2(xhat, both(-m), u[i])));
+                        if (has[k]) {
+                            if (w) dw[1][i] = fma2(n[i], xhat, dw[1][i]);
+                            else dw[0][i] = fma2(n[i], xhat, dw[0][i]);
+                        }
+                    }
+                }
+                if (has[k]) x[k].store(static_cast<T *>(a.y[w]) + at[k]);
+            }
+        }
+    }
+    if constexpr (kBwd) {
+        float(*sums)[2][kHeadDim] = reinterpret_cast<float(*)[2][kHeadDim]>(s.turn);  // [lane groups]
+        static_assert(sizeof s.turn >= L::kRows * 2 * kHeadDim * sizeof(float), "sums over the lane groups");
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < VE / 2; ++i) *reinterpret_cast<float2 *>(&sums[group][w][ch + 2 * i]) = dw[w][i];
+        __syncthreads();
+        const int w = tid / kHeadDim, c = tid % kHeadDim;
+        if (a.partial[w]) {
+            float v = 0.f;
+            for (int g = 0; g < L::kRows; ++g) v += sums[g][w][c];
+            a.partial[w][size_t(blockIdx.x) * kHeadDim + c] = v;
+        }
+    }
+}
+
+int ctas_of(long long tokens, int step, bool bwd) {
+    const long long steps = (tokens + step - 1) / step, most = 152 * (bwd ? 3 : 4);
+    return int(steps < most ? steps : most);
+}
+
+// tokens of a CTA's step: two rows for each of its lane groups
+int step_of(int heads, int io_dtype) {
+    const int rows = io_dtype == GDN_DT_BF16 ? 2 * Layout<__nv_bfloat16>::kRows : 2 * Layout<float>::kRows;
+    const int n = rows / heads;
+    return n < 1 ? 1 : n > kMaxTokens ? kMaxTokens : n;
+}
+
+template <typename T, bool kBwd>
+void go(const RopeArgs &a, int interleaved, int ctas, cudaStream_t s) {
+    if (interleaved) k_qk_rope<T, kNeighbours, kBwd><<<ctas, kThreads, 0, s>>>(a);
+    else if (a.pairs % Layout<T>::kVe == 0) k_qk_rope<T, kLanes, kBwd><<<ctas, kThreads, 0, s>>>(a);
+    else k_qk_rope<T, kAnywhere, kBwd><<<ctas, kThreads, 0, s>>>(a);
+}
+
+}  // namespace
+
+size_t qk_rope_bwd_workspace(long long tokens, int heads, int io_dtype) {
+    return size_t(ctas_of(tokens, step_of(heads, io_dtype), true)) * 2 * kHeadDim * sizeof(float);
+}
+
+cudaError_t launch_qk_rope(const gdn_qk_rope &r, const void *const dy[2], const long long dy_stride[2], void *const y[2],
+                           const long long y_stride[2], float *const dweight[2], void *workspace, int *status,
+                           cudaStream_t s) {
+    const int heads = r.hq + r.hk;
+    RopeArgs a{};
+    a.x[0] = r.q, a.x[1] = r.k;
+    a.xs[0] = r.q_stride, a.xs[1] = r.k_stride;
+    const bool bwd = dy != nullptr;
+    float *parts = static_cast<float *>(workspace);
+    a.heads[0] = r.hq, a.heads[1] = r.hk;
+    a.step = step_of(heads, r.io_dtype);
+    const int ctas = ctas_of(r.tokens, a.step, bwd);
+    for (int w = 0; w < 2; ++w) {
+        if (bwd) a.dy[w] = dy[w], a.ds[w] = dy_stride[w];
+        a.y[w] = y[w], a.ys[w] = y_stride[w];
+        if (bwd && dweight[w]) a.partial[w] = parts + size_t(w) * ctas * kHeadDim;
+    }
+    a.weight[0] = r.q_weight, a.weight[1] = r.k_weight;
+    a.inv_freq = r.inv_freq, a.positions = r.positions, a.pair_axis = r.pair_axis;
+    a.eps = r.eps;
+    a.tokens = r.tokens, a.pairs = r.rotary / 2, a.axes = r.axes;
+    a.status = status;
+    if (ctas > 0) {
+        LaunchScope scope(bwd ? GDN_K_QK_NORM_ROPE_BWD : GDN_K_QK_NORM_ROPE, s);
+        if (r.io_dtype == GDN_DT_BF16)
+            bwd ? go<__nv_bfloat16, true>(a, r.interleaved, ctas, s) : go<__nv_bfloat16, false>(a, r.interleaved, ctas, s);
+        else
+            bwd ? go<float, true>(a, r.interleaved, ctas, s) : go<float, false>(a, r.interleaved, ctas, s);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (bwd && (dweight[0] || dweight[1]))
+        return launch_row_sums(a.partial[0], a.partial[1], ctas, kHeadDim, dweight[0], dweight[1], s);
+    return cudaSuccess;
+}
+
+}  // namespace gdn

@@ -9,7 +9,9 @@ The entry points keep the C names:
   gdn_recurrent_step_gated, gdn_gated_rmsnorm, gdn_causal_conv1d_silu,
   gdn_causal_conv1d_silu_step, gdn_gating, gdn_linear_recurrence,
   gdn_linear_recurrence_bwd, gdn_linear_recurrence_step, gdn_layernorm,
-  gdn_layernorm_bwd, gdn_gated_rmsnorm_bwd,
+  gdn_layernorm_bwd, gdn_gated_rmsnorm_bwd, gdn_linear_attention,
+  gdn_linear_attention_bwd, gdn_linear_attention_step, gdn_qk_norm_rope,
+  gdn_qk_norm_rope_bwd,
   gdn_read_device_status, gdn_get_device_status, gdn_status_string, gdn_version.
 """
 from __future__ import annotations
@@ -35,8 +37,11 @@ SYMBOLS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "gdn_recurrent_step"
            "gdn_gating", "gdn_causal_conv1d_silu_step", "gdn_chunk_fwd_gated", "gdn_get_device_status",
            "gdn_set_wait_limit_ns", "gdn_linear_recurrence", "gdn_linear_recurrence_states_size",
            "gdn_linear_recurrence_bwd", "gdn_linear_recurrence_step", "gdn_layernorm", "gdn_layernorm_bwd",
-           "gdn_layernorm_bwd_workspace_size", "gdn_gated_rmsnorm_bwd", "gdn_gated_rmsnorm_bwd_workspace_size")
-GDN_K_COUNT = 18
+           "gdn_layernorm_bwd_workspace_size", "gdn_gated_rmsnorm_bwd", "gdn_gated_rmsnorm_bwd_workspace_size",
+           "gdn_linear_attention", "gdn_linear_attention_workspace_size", "gdn_linear_attention_bwd",
+           "gdn_linear_attention_bwd_workspace_size", "gdn_linear_attention_step", "gdn_qk_norm_rope",
+           "gdn_qk_norm_rope_bwd", "gdn_qk_norm_rope_bwd_workspace_size")
+GDN_K_COUNT = 26
 
 
 class GdnProblem(ctypes.Structure):
@@ -44,6 +49,15 @@ class GdnProblem(ctypes.Structure):
                 ("total_tokens", ctypes.c_int32), ("hq", ctypes.c_int32), ("hv", ctypes.c_int32),
                 ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
                 ("flags", ctypes.c_uint32), ("num_state_slots", ctypes.c_int32)]
+
+
+class GdnQkRope(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("tokens", ctypes.c_int32), ("hq", ctypes.c_int32), ("hk", ctypes.c_int32),
+                ("rotary", ctypes.c_int32), ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32)]
 
 
 class GdnError(RuntimeError):
@@ -105,7 +119,7 @@ def load(path: Optional[str] = None):
             lib.gdn_chunk_fwd_noalloc.argtypes = [P, _vp, _vp, _vp, _fp, _fp, ctypes.c_float, _fp, _ip, _vp, _fp,
                                                   _vp]
             lib.gdn_chunk_fwd_noalloc.restype = ctypes.c_int
-            cf, sz = ctypes.c_float, ctypes.c_size_t
+            cf, sz, i64, R = ctypes.c_float, ctypes.c_size_t, ctypes.c_int64, ctypes.POINTER(GdnQkRope)
             for name, res, args in (
                     ("gdn_linear_recurrence", ctypes.c_int, [P, _vp, _vp, _fp, _ip, _vp, _fp, _fp, _vp]),
                     ("gdn_linear_recurrence_states_size", sz, [P]),
@@ -118,7 +132,18 @@ def load(path: Optional[str] = None):
                     ("gdn_layernorm_bwd_workspace_size", sz, [P]),
                     ("gdn_gated_rmsnorm_bwd", ctypes.c_int,
                      [P, _vp, _vp, _vp, _fp, cf, _vp, _vp, _fp, _vp, sz, _vp]),
-                    ("gdn_gated_rmsnorm_bwd_workspace_size", sz, [P])):
+                    ("gdn_gated_rmsnorm_bwd_workspace_size", sz, [P]),
+                    ("gdn_linear_attention", ctypes.c_int,
+                     [P, _vp, _vp, _vp, _fp, cf, _fp, _ip, _vp, _fp, _vp, sz, _vp]),
+                    ("gdn_linear_attention_workspace_size", sz, [P]),
+                    ("gdn_linear_attention_bwd", ctypes.c_int,
+                     [P, _vp, _vp, _vp, _vp, _fp, cf, _fp, _fp, _ip, _vp, _vp, _vp, _fp, _vp, sz, _vp]),
+                    ("gdn_linear_attention_bwd_workspace_size", sz, [P]),
+                    ("gdn_linear_attention_step", ctypes.c_int, [P, _vp, _vp, _vp, _fp, cf, _vp, _ip, _vp, _vp]),
+                    ("gdn_qk_norm_rope", ctypes.c_int, [R, _vp, i64, _vp, i64, _vp]),
+                    ("gdn_qk_norm_rope_bwd", ctypes.c_int,
+                     [R, _vp, i64, _vp, i64, _vp, i64, _vp, i64, _fp, _fp, _vp, sz, _vp]),
+                    ("gdn_qk_norm_rope_bwd_workspace_size", sz, [R])):
                 fn = getattr(lib, name)
                 fn.restype, fn.argtypes = res, args
             lib.gdn_kernel_name.argtypes = [ctypes.c_int]
@@ -832,6 +857,259 @@ def gdn_gated_rmsnorm_bwd(dy, o, z, weight, eps, do=None, dz=None, dweight=None,
     if st != GDN_OK:
         raise GdnError(st, "gdn_gated_rmsnorm_bwd")
     return do, dz, dweight
+
+
+@functools.lru_cache(maxsize=1024)
+def _linattn_layout(q_shape, v_shape, dtype, offsets):
+    """(descriptor's reference, state shape) of linear attention on q of
+    ``q_shape``, [T, Hq, 128] with cu_seqlens of shape ``offsets`` or
+    [B, T, Hq, 128] with None."""
+    packed = offsets is not None
+    if len(q_shape) != (3 if packed else 4) or len(v_shape) != len(q_shape):
+        raise ValueError("q must be [T, Hq, 128] and v [T, Hv, 128] with cu_seqlens, else [B, T, Hq, 128] and "
+                         "[B, T, Hv, 128]")
+    if packed and len(offsets) != 1:
+        raise ValueError("cu_seqlens must be a 1-D int32 tensor [N + 1]")
+    if q_shape[:-2] != v_shape[:-2]:
+        raise ValueError(f"v must have q's leading shape {tuple(q_shape[:-2])}, got {tuple(v_shape[:-2])}")
+    hq, dk = q_shape[-2:]
+    hv, dv = v_shape[-2:]
+    if packed:
+        batch, seqlen, num_seqs, total = 1, 0, offsets[0] - 1, q_shape[0]
+    else:
+        batch, seqlen = q_shape[:2]
+        num_seqs, total = batch, batch * seqlen
+    _, ref = _descriptor(batch, seqlen, num_seqs, total, hq, hv, dk, dv, _io_type(dtype), 0, 0)
+    return ref, (num_seqs, hv, dk, dv)
+
+
+def gdn_linear_attention(q, k, v, decay, scale, initial_state=None, cu_seqlens=None, out=None, final_state=None,
+                         output_final_state=True, workspace=None, stream=None):
+    """Linear attention with a decay for each head: S_t = exp(decay_h) S_{t-1} +
+    k_t^T v_t, o_t = scale q_t S_t. q, k [T, Hq, 128] and v [T, Hv, 128] packed by
+    ``cu_seqlens`` (int32 [N + 1]), or with a batch dimension in front and
+    without it; ``decay`` [Hv] f32, the log of what a token keeps (<= 0).
+    ``initial_state`` and the returned final state are [N, Hv, 128, 128] f32.
+
+    Returns (out, final_state). ``workspace`` (uint8) is allocated when not
+    supplied."""
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_linear_attention(q, k, v, decay, scale, initial_state, cu_seqlens, out, final_state,
+                                        output_final_state, workspace)
+    ref, state_shape = _linattn_layout(q.shape, v.shape, q.dtype, None if cu_seqlens is None else cu_seqlens.shape)
+    f32, io = torch.float32, q.dtype
+    pq = _first("q", q)
+    pk = _arg("k", k, io, q.shape, dev)
+    pv = _arg("v", v, io, v.shape, dev)
+    pd = _arg("decay", decay, f32, (state_shape[1],), dev)
+    ps0 = _arg("initial_state", initial_state, f32, state_shape, dev)
+    pcu = _arg("cu_seqlens", cu_seqlens, torch.int32, (state_shape[0] + 1,), dev)
+    po = _arg("out", out, io, v.shape, dev)
+    pf = _arg("final_state", final_state, f32, state_shape, dev)
+    handle = _current(dev)
+    if out is None:
+        out = torch.empty_like(v)
+        po = out.data_ptr()
+    if final_state is None and output_final_state:
+        final_state = torch.empty(state_shape, dtype=f32, device=dev)
+        pf = final_state.data_ptr()
+    lib = load()
+    pws, nbytes, workspace = _workspace(workspace, lib.gdn_linear_attention_workspace_size(ref), dev)
+    st = lib.gdn_linear_attention(ref, pq, pk, pv, pd, scale, ps0, pcu, po, pf, pws, nbytes, handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_linear_attention")
+    return out, final_state
+
+
+def gdn_linear_attention_bwd(dout, q, k, v, decay, scale, initial_state=None, cu_seqlens=None, dfinal_state=None,
+                             dq=None, dk=None, dv=None, dinitial_state=None, workspace=None, stream=None):
+    """Backward pass of gdn_linear_attention from the gradients of out and of the
+    final state (None: zeros). Returns (dq, dk, dv, dinitial_state);
+    dinitial_state is None unless an ``initial_state`` or a dinitial_state to
+    write is given. The decays get no gradient."""
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_linear_attention_bwd(dout, q, k, v, decay, scale, initial_state, cu_seqlens, dfinal_state, dq,
+                                            dk, dv, dinitial_state, workspace)
+    ref, state_shape = _linattn_layout(q.shape, v.shape, q.dtype, None if cu_seqlens is None else cu_seqlens.shape)
+    f32, io = torch.float32, q.dtype
+    pq = _first("q", q)
+    pdo = _arg("dout", dout, io, v.shape, dev)
+    pk = _arg("k", k, io, q.shape, dev)
+    pv = _arg("v", v, io, v.shape, dev)
+    pd = _arg("decay", decay, f32, (state_shape[1],), dev)
+    ps0 = _arg("initial_state", initial_state, f32, state_shape, dev)
+    pcu = _arg("cu_seqlens", cu_seqlens, torch.int32, (state_shape[0] + 1,), dev)
+    pdf = _arg("dfinal_state", dfinal_state, f32, state_shape, dev)
+    pdq = _arg("dq", dq, io, q.shape, dev)
+    pdk = _arg("dk", dk, io, q.shape, dev)
+    pdv = _arg("dv", dv, io, v.shape, dev)
+    pd0 = _arg("dinitial_state", dinitial_state, f32, state_shape, dev)
+    handle = _current(dev)
+    if dq is None:
+        dq = torch.empty_like(q)
+        pdq = dq.data_ptr()
+    if dk is None:
+        dk = torch.empty_like(k)
+        pdk = dk.data_ptr()
+    if dv is None:
+        dv = torch.empty_like(v)
+        pdv = dv.data_ptr()
+    if dinitial_state is None and initial_state is not None:
+        dinitial_state = torch.empty(state_shape, dtype=f32, device=dev)
+        pd0 = dinitial_state.data_ptr()
+    lib = load()
+    pws, nbytes, workspace = _workspace(workspace, lib.gdn_linear_attention_bwd_workspace_size(ref), dev)
+    st = lib.gdn_linear_attention_bwd(ref, pdo, pq, pk, pv, pd, scale, ps0, pdf, pcu, pdq, pdk, pdv, pd0, pws, nbytes,
+                                      handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_linear_attention_bwd")
+    return dq, dk, dv, dinitial_state
+
+
+def gdn_linear_attention_step(q, k, v, decay, scale, state, state_indices=None, out=None, stream=None):
+    """One decode token per sequence: q, k [N, Hq, 128], v [N, Hv, 128], decay
+    [Hv] f32; ``state`` [slots, Hv, 128, 128] (f32, or bf16 for a bf16 cache) is
+    updated in place at ``state_indices`` (int32 [N]; None: slot n; negative:
+    skipped, its out rows are not written)."""
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_linear_attention_step(q, k, v, decay, scale, state, state_indices, out)
+    _decode_checks(q, v, state, state_indices, out)
+    N, hq, dk = q.shape
+    hv, dv = v.shape[1:]
+    io, slots = q.dtype, state.shape[0]
+    pq = _first("q", q)
+    pk = _arg("k", k, io, q.shape, dev)
+    pv = _arg("v", v, io, v.shape, dev)
+    pd = _arg("decay", decay, torch.float32, (hv,), dev)
+    ps = _arg("state", state, state.dtype, state.shape, dev)
+    pi = _arg("state_indices", state_indices, torch.int32, (N,), dev)
+    po = _arg("out", out, io, v.shape, dev)
+    _, ref = _descriptor(N, 1, N, N, hq, hv, dk, dv, _io_dtype(q), _decode_flags(state, False), slots)
+    handle = _current(dev)
+    if out is None:
+        out = torch.empty_like(v)
+        po = out.data_ptr()
+    st = load().gdn_linear_attention_step(ref, pq, pk, pv, pd, scale, ps, pi, po, handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_linear_attention_step")
+    return out
+
+
+def _head_rows(name, t, dtype, shape, dev):
+    """(address, elements from token to token) of ``t`` [T, H, 128], whose heads
+    lie together and whose tokens may lie apart."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev} (the device of the first input)")
+    T, H, D = shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"a token's heads of {name} must lie together")
+    return t.data_ptr(), (t.stride(0) if T > 1 else H * D)
+
+
+def _rope_problem(q, k, q_weight, k_weight, inv_freq, positions, pair_axis, interleaved, eps):
+    """(descriptor, its reference) of gdn_qk_norm_rope's inputs after their checks."""
+    dev, io = q.device, q.dtype
+    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != 128:
+        raise ValueError("q must be [T, Hq, 128] and k [T, Hk, 128]")
+    T, hq, d = q.shape
+    pq, sq = _head_rows("q", q, io, q.shape, dev)
+    pk, sk = _head_rows("k", k, io, (T, k.shape[1], d), dev)
+    f32, i32 = torch.float32, torch.int32
+    if inv_freq.dim() != 1 or inv_freq.shape[0] > d // 2:
+        raise ValueError(f"inv_freq must be 1-D with at most {d // 2} elements, got {tuple(inv_freq.shape)}")
+    half = inv_freq.shape[0]
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if axes > 1 and pair_axis is None:
+        raise ValueError("positions of several axes need pair_axis, each pair's axis")
+    r = GdnQkRope(pq, pk, sq, sk, _arg("q_weight", q_weight, f32, (d,), dev), _arg("k_weight", k_weight, f32, (d,), dev),
+                  _arg("inv_freq", inv_freq, f32, (half,), dev),
+                  _arg("positions", positions, i32, (T,) if positions.dim() == 1 else (axes, T), dev),
+                  _arg("pair_axis", pair_axis, i32, (half,), dev), eps, T, hq, k.shape[1], 2 * half, axes,
+                  int(bool(interleaved)), _io_type(io))
+    return r, ctypes.byref(r)
+
+
+def gdn_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, pair_axis=None, interleaved=False, eps=1e-6,
+                     out_q=None, out_k=None, stream=None):
+    """The RMS norm of every head of q [T, Hq, 128] and k [T, Hk, 128] with
+    ``q_weight`` and ``k_weight`` ([128] f32 or None), and its rotation by
+    ``positions`` (int32 [T]) times ``inv_freq`` ([R / 2] f32, R <= 128 channels
+    rotated) in one pass. A head's pairs are channels (i, i + R / 2), or
+    (2 i, 2 i + 1) with ``interleaved``. With positions [A, T] of several axes
+    ``pair_axis`` (int32 [R / 2]) names the axis that turns each pair.
+
+    q and k may be slices of a projection's rows (their tokens apart, a token's
+    heads together), and so may ``out_q`` and ``out_k``; out_q may be q and out_k
+    may be k. Returns (out_q, out_k)."""
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, pair_axis, interleaved, eps, out_q,
+                                    out_k)
+    r, ref = _rope_problem(q, k, q_weight, k_weight, inv_freq, positions, pair_axis, interleaved, eps)
+    handle = _current(dev)
+    if out_q is None:
+        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if out_k is None:
+        out_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    poq, soq = _head_rows("out_q", out_q, q.dtype, q.shape, dev)
+    pok, sok = _head_rows("out_k", out_k, q.dtype, k.shape, dev)
+    st = load().gdn_qk_norm_rope(ref, poq, soq, pok, sok, handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_qk_norm_rope")
+    return out_q, out_k
+
+
+def gdn_qk_norm_rope_bwd(dout_q, dout_k, q, k, q_weight, k_weight, inv_freq, positions, pair_axis=None,
+                         interleaved=False, eps=1e-6, dq=None, dk=None, dq_weight=None, dk_weight=None,
+                         need_dweight=True, workspace=None, stream=None):
+    """Backward pass of gdn_qk_norm_rope from the gradients of its outputs.
+    Returns (dq, dk, dq_weight, dk_weight), the weights' gradients [128] f32 sums
+    over all tokens and heads (None where not needed). The gradients may be
+    slices of rows as q and k are; dq may be q or dout_q, dk may be k or dout_k.
+    ``workspace`` (uint8, of gdn_qk_norm_rope_bwd_workspace_size bytes) is
+    allocated when not supplied."""
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with _launching(stream, dev):
+            return gdn_qk_norm_rope_bwd(dout_q, dout_k, q, k, q_weight, k_weight, inv_freq, positions, pair_axis,
+                                        interleaved, eps, dq, dk, dq_weight, dk_weight, need_dweight, workspace)
+    r, ref = _rope_problem(q, k, q_weight, k_weight, inv_freq, positions, pair_axis, interleaved, eps)
+    f32, io = torch.float32, q.dtype
+    pgq, sgq = _head_rows("dout_q", dout_q, io, q.shape, dev)
+    pgk, sgk = _head_rows("dout_k", dout_k, io, k.shape, dev)
+    pqw = _arg("dq_weight", dq_weight, f32, (128,), dev)
+    pkw = _arg("dk_weight", dk_weight, f32, (128,), dev)
+    handle = _current(dev)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=io, device=dev)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=io, device=dev)
+    pdq, sdq = _head_rows("dq", dq, io, q.shape, dev)
+    pdk, sdk = _head_rows("dk", dk, io, k.shape, dev)
+    if dq_weight is None and need_dweight:
+        dq_weight = torch.empty(128, dtype=f32, device=dev)
+        pqw = dq_weight.data_ptr()
+    if dk_weight is None and need_dweight:
+        dk_weight = torch.empty(128, dtype=f32, device=dev)
+        pkw = dk_weight.data_ptr()
+    lib, pws, nbytes = load(), None, 0
+    if pqw or pkw or workspace is not None:
+        pws, nbytes, workspace = _workspace(workspace, lib.gdn_qk_norm_rope_bwd_workspace_size(ref), dev)
+    st = lib.gdn_qk_norm_rope_bwd(ref, pgq, sgq, pgk, sgk, pdq, sdq, pdk, sdk, pqw, pkw, pws, nbytes, handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_qk_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
 
 
 def gdn_read_device_status(stream=None, clear: bool = True) -> int:

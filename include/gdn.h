@@ -445,6 +445,123 @@ int gdn_gated_rmsnorm_bwd(const gdn_problem *p, const void *dy, const void *o, c
                           void *stream);
 size_t gdn_gated_rmsnorm_bwd_workspace_size(const gdn_problem *p);
 
+/* ---- linear attention with a decay for each head ---- */
+
+/* Over each sequence, per value head h with lambda = exp(decay[h]) and its
+ * query and key head floor(h / (hv / hq)):
+ *   S_t = lambda S_{t-1} + k_t^T v_t,  o_t = scale q_t S_t   (S is dk x dv)
+ * (the recurrence of [Lab3] "Linear Attention 与 Gated DeltaNet" with a
+ * constant gate), chunk by chunk as gdn_chunk_fwd. Layouts, packed and dense,
+ * are gdn_chunk_fwd's.
+ *   q, k          [total_tokens, hq, 128] io dtype (used as they are)
+ *   v, out        [total_tokens, hv, 128] io dtype
+ *   decay         [hv] f32, 4-byte aligned: the log of the factor a token's
+ *                 state is kept by, <= 0 (0 keeps all, -inf nothing)
+ *   initial_state [num_seqs, hv, 128, 128] f32, or NULL for zeros
+ *   cu_seqlens    int32 [num_seqs+1], or NULL (dense), checked on the device
+ *   final_state   [num_seqs, hv, 128, 128] f32, or NULL to skip. A sequence
+ *                 of length 0 copies its initial state (or zeros).
+ *   workspace     gdn_linear_attention_workspace_size(p) bytes, 256-byte
+ *                 aligned; contents need no initialisation. Calls that share a
+ *                 workspace must be ordered on one stream (captured graphs that
+ *                 share one, too).
+ * States and sums are f32, decays powers taken from their exponent. bf16: the
+ * decayed scores inside a chunk of 128 tokens and the state in the product
+ * with q are rounded to bf16, as out is; final_state is not rounded on its way
+ * (what is added to a state is exact to 2^-24). Infinities and NaN stay in
+ * their sequence and value heads (with bf16 they reach tokens up to 127 places
+ * before their own). (The bf16 kernels wait for copies and products, at most 2 s
+ * a wait: GDN_ETIMEOUT in the device status.) */
+int gdn_linear_attention(const gdn_problem *p, const void *q, const void *k, const void *v, const float *decay,
+                         float scale, const float *initial_state, const int32_t *cu_seqlens, void *out,
+                         float *final_state, void *workspace, size_t workspace_bytes, void *stream);
+size_t gdn_linear_attention_workspace_size(const gdn_problem *p);
+
+/* Backward pass of gdn_linear_attention: with dS_t = scale q_t^T dout_t +
+ * lambda dS_{t+1} (behind a sequence's last token dfinal_state, undecayed),
+ *   dq_t = scale dout_t S_t^T,  dk_t = v_t dS_t^T,  dv_t = k_t dS_t,
+ *   dinitial_state = lambda dS of the first token,
+ * dq and dk summed over the value heads of each query and key head in their
+ * order. The decays are constants of the model and get no gradient.
+ *   dout, dv       [total_tokens, hv, 128] io dtype
+ *   dq, dk         [total_tokens, hq, 128] io dtype
+ *   initial_state  what the forward pass was given (or NULL)
+ *   dfinal_state   [num_seqs, hv, 128, 128] f32, or NULL for zeros
+ *   dinitial_state [num_seqs, hv, 128, 128] f32, or NULL to skip; a sequence
+ *                  without tokens gets its dfinal_state (or zeros)
+ *   workspace      gdn_linear_attention_bwd_workspace_size(p) bytes
+ * The states are recomputed from the inputs; precision as in the forward pass.
+ * The same call gives the same bits. */
+int gdn_linear_attention_bwd(const gdn_problem *p, const void *dout, const void *q, const void *k, const void *v,
+                             const float *decay, float scale, const float *initial_state, const float *dfinal_state,
+                             const int32_t *cu_seqlens, void *dq, void *dk, void *dv, float *dinitial_state,
+                             void *workspace, size_t workspace_bytes, void *stream);
+size_t gdn_linear_attention_bwd_workspace_size(const gdn_problem *p);
+
+/* Decode step of linear attention, one token per sequence: for n < num_seqs
+ * with slot i = state_indices[n] (n when NULL),
+ *   state[i] = lambda state[i] + k_n^T v_n,  out_n = scale q_n state[i].
+ *   q, k [num_seqs, hq, 128], v, out [num_seqs, hv, 128] io dtype; decay as above
+ *   state [num_state_slots, hv, 128, 128] f32 (bf16 with GDN_FLAG_STATE_BF16:
+ *        out is taken from the f32 state, which is then rounded), in place
+ *   state_indices int32 [num_seqs] or NULL. A negative index skips the sequence
+ *        (its out rows stay as they were); one >= num_state_slots is skipped and
+ *        recorded as GDN_EDEVICE_INPUT. Two sequences must not name the same slot. */
+int gdn_linear_attention_step(const gdn_problem *p, const void *q, const void *k, const void *v, const float *decay,
+                              float scale, void *state, const int32_t *state_indices, void *out, void *stream);
+
+/* ---- norm and rotation of queries and keys ---- */
+
+/* What both passes of gdn_qk_norm_rope are given. */
+typedef struct gdn_qk_rope {
+    const void *q, *k;           /* [tokens, hq, 128], [tokens, hk, 128] io dtype, 16-byte aligned; a token's
+                                    heads lie together, tokens q_stride and k_stride elements apart (a multiple
+                                    of 16 bytes, at least the heads' elements): slices of a projection's rows
+                                    need no copy */
+    int64_t q_stride, k_stride;
+    const float *q_weight, *k_weight; /* [128] f32, 4-byte aligned, or NULL (1) */
+    const float *inv_freq;       /* [rotary / 2] f32: radians per position of each pair */
+    const int32_t *positions;    /* [axes, tokens] */
+    const int32_t *pair_axis;    /* [rotary / 2], the axis whose position turns a pair, or NULL (axis 0) */
+    float eps;
+    int32_t tokens, hq, hk;
+    int32_t rotary;              /* channels rotated, the first ones of a head: even, 0 .. 128 */
+    int32_t axes;                /* 1 .. 8 */
+    int32_t interleaved;         /* pairs: 0: channels (i, i + rotary / 2); 1: (2 i, 2 i + 1) */
+    int32_t io_dtype;            /* gdn_dtype of q, k and the outputs */
+} gdn_qk_rope;
+
+/* The norm of every query and key head and its rotation by position: with
+ * n = x / sqrt(mean_j x_j^2 + eps) * weight and t = position * inv_freq,
+ *   (y_a, y_b) = (n_a cos t - n_b sin t, n_a sin t + n_b cos t)
+ * for every pair (a, b); channels behind `rotary` are n. With several axes
+ * (time, height, width of a patch) each pair is turned by the position of its
+ * own axis.
+ *   out_q, out_k  like q and k, with strides of their own; out_q may be q and
+ *                 out_k may be k, in exactly their places
+ * The angle's error is below 2^-22 radian for every int32 position, all else
+ * is f32 and rounded once. An axis outside 0 .. axes - 1 is recorded as
+ * GDN_EDEVICE_INPUT and nothing is written. */
+int gdn_qk_norm_rope(const gdn_qk_rope *r, void *out_q, int64_t out_q_stride, void *out_k, int64_t out_k_stride,
+                     void *stream);
+
+/* Backward pass of gdn_qk_norm_rope: with dn the outputs' gradient turned back,
+ * xhat = x / sqrt(mean x^2 + eps) and u = dn * weight,
+ *   dx = (u - xhat mean_j(u xhat)) / sqrt(mean x^2 + eps),
+ *   dweight[j] = sum over tokens and heads of dn xhat.
+ *   dout_q, dout_k, dq, dk  like q and k, with strides of their own; dq may be
+ *                 q or dout_q, dk may be k or dout_k
+ *   dq_weight, dk_weight [128] f32, or NULL to skip; written (not added to),
+ *                 with no tokens zeros
+ *   workspace     gdn_qk_norm_rope_bwd_workspace_size(r) bytes, 256-byte
+ *                 aligned; may be NULL when both are. Calls that share it must
+ *                 be ordered on one stream.
+ * The sums over rows are taken in a fixed order. */
+int gdn_qk_norm_rope_bwd(const gdn_qk_rope *r, const void *dout_q, int64_t dout_q_stride, const void *dout_k,
+                         int64_t dout_k_stride, void *dq, int64_t dq_stride, void *dk, int64_t dk_stride,
+                         float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes, void *stream);
+size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_rope *r);
+
 /* Synchronises `stream`, returns the device status word (GDN_OK or the first
  * device-side error recorded since the last clear) and clears it when
  * `clear` is non-zero. Returns GDN_ECUDA if the CUDA calls themselves fail. */
@@ -485,7 +602,15 @@ typedef enum gdn_kernel {
     GDN_K_LAYERNORM_BWD = 15,     /* layer norm, backward: dx and partial sums over rows */
     GDN_K_GATED_RMSNORM_BWD = 16, /* output gate, backward: d_o, d_z and partial sums over rows */
     GDN_K_ROW_SUMS = 17,          /* partial sums over rows -> weight and bias gradients */
-    GDN_K_COUNT = 18
+    GDN_K_LINATTN_TABLE = 18,     /* linear attention: segments of the sequences */
+    GDN_K_LINATTN_SUM = 19,       /* linear attention: sums of the segments */
+    GDN_K_LINATTN_CHAIN = 20,     /* linear attention: states that enter the segments */
+    GDN_K_LINATTN_WALK = 21,      /* linear attention: outputs (gradients) and final states */
+    GDN_K_LINATTN_GROUP_SUM = 22, /* linear attention, backward: dq and dk over the heads of a group */
+    GDN_K_LINATTN_STEP = 23,      /* linear attention, decode step */
+    GDN_K_QK_NORM_ROPE = 24,      /* norm and rotation of queries and keys */
+    GDN_K_QK_NORM_ROPE_BWD = 25,  /* its backward pass */
+    GDN_K_COUNT = 26
 } gdn_kernel;
 
 /* Turns per-kernel CUDA-event timing on (non-zero) or off for every later
