@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kTableThreads) k_la_table(const __grid_constan
 // Chains the segments' sums: behind it, states[seg] is the state that enters
 // the segment (of those that another one comes before). Four elements a
 // thread; a sequence's segments one after the other.
-constexpr int kChainThreads = 256, kChainCtas = kState / 4 / kChainThreads;
+constexpr int kChainThreads = 256, kChainCtas = kState / 4 / kChainThreads, kChainBatch = 8;
 
 __global__ void __launch_bounds__(kChainThreads) k_la_chain(const __grid_constant__ Args a) {
     if (*a.n_segs == 0) return;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kChainThreads) k_la_chain(const __grid_constan
         if (s1 - s0 < 2) continue;
         const int step = r.against ? -1 : 1, from = r.against ? s1 - 1 : s0, count = s1 - s0;
         float *states = r.states + size_t(h) * kState + e;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f), left = s;
         if (r.init) {
             const float *init = r.init + size_t(n) * per_head + size_t(h) * kState;
             if (r.swapped) {
@@ -109,17 +109,28 @@ __global__ void __launch_bounds__(kChainThreads) k_la_chain(const __grid_constan
                 s = *reinterpret_cast<const float4 *>(init + e);
             }
         }
-        float4 sum = *reinterpret_cast<const float4 *>(states + size_t(from) * per_head);
-        for (int k = 1; k < count; ++k) {
-            const int at = from + k * step;
-            float4 next = sum;
-            if (k + 1 < count) next = *reinterpret_cast<const float4 *>(states + size_t(at) * per_head);
-            const Seg seg = a.segs[at - step];
-            const float keep = power(decay, seg.len - 1 + entry_offset(r, seg, true));
-            s.x = fmaf(keep, s.x, sum.x), s.y = fmaf(keep, s.y, sum.y);
-            s.z = fmaf(keep, s.z, sum.z), s.w = fmaf(keep, s.w, sum.w);
-            *reinterpret_cast<float4 *>(states + size_t(at) * per_head) = s;
-            sum = next;
+        // the sums come in batches, whose loads are under way together
+        for (int k = 1; k < count; k += kChainBatch) {
+            float4 sum[kChainBatch];
+            float keep[kChainBatch];
+#pragma unroll
+            for (int i = 0; i < kChainBatch; ++i) {
+                if (k + i >= count) break;
+                const int at = from + (k + i - 1) * step;  // the segment left
+                sum[i] = k + i == 1 || i > 0 ? *reinterpret_cast<const float4 *>(states + size_t(at) * per_head) : left;
+                const Seg seg = a.segs[at];
+                keep[i] = power(decay, seg.len - 1 + entry_offset(r, seg, true));
+            }
+            // (the batch's last place is read before the state goes there: it is the next one's first sum)
+            if (k + kChainBatch < count)
+                left = *reinterpret_cast<const float4 *>(states + size_t(from + (k + kChainBatch - 1) * step) * per_head);
+#pragma unroll
+            for (int i = 0; i < kChainBatch; ++i) {
+                if (k + i >= count) break;
+                s.x = fmaf(keep[i], s.x, sum[i].x), s.y = fmaf(keep[i], s.y, sum[i].y);
+                s.z = fmaf(keep[i], s.z, sum[i].z), s.w = fmaf(keep[i], s.w, sum[i].w);
+                *reinterpret_cast<float4 *>(states + size_t(from + (k + i) * step) * per_head) = s;
+            }
         }
     }
 }
@@ -174,7 +185,7 @@ int segment_rows(long long total_tokens, long long num_seqs, int hv, int roles, 
     constexpr int kSms = 152;
     const int unit = io_dtype == GDN_DT_BF16 ? 128 : 32;
     const long long slots = io_dtype == GDN_DT_BF16 ? kSms : 2 * kSms;
-    const double walk = io_dtype == GDN_DT_BF16 ? 1.8 : 4.0, sum = io_dtype == GDN_DT_BF16 ? 0.9 : 2.0, start = 5.0;
+    const double walk = io_dtype == GDN_DT_BF16 ? 2.8 : 4.0, sum = io_dtype == GDN_DT_BF16 ? 1.3 : 2.0, start = io_dtype == GDN_DT_BF16 ? 14.0 : 5.0;
     const long long units = (total_tokens + unit - 1) / unit;
     long long best = 1;
     double least = 0;

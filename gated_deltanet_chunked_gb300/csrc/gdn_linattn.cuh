@@ -40,6 +40,7 @@ struct Role {
     int against;        // against time
     int swapped;        // init and fin are [c, b]
     int partial;        // out is f32 [tokens, hv, 128], to be summed over the group's heads
+    int sectors;        // out starts at a multiple of 32 bytes
 };
 
 struct Args {

@@ -5,12 +5,16 @@
 //   out_i = scale_out (lambda^(i+1) a_i S + sum_{j<=i} lambda^(i-j) (a_i b_j) c_j)
 //   S'    = lambda^len S + sum_j lambda^(len-1-j) b_j^T c_j
 // and against time with the mirrored exponents. Four products of 128^3 a chunk:
-//   P = A B^T, intra = (P o decays) C, inter = A S, sum = C^T (decayed B).
+//   P = A B^T, intra = (P o decays) C, inter = A S, sum = (decayed B)^T C.
 // A, B and C are exact in bf16. Roundings to bf16 are those of the decayed
 // scores and of the state as an operand of `inter`: each is of the size of the
 // output's own rounding. The state itself stays f32 in registers, and what is
-// added to it is exact to 2^-26: decayed B goes in as three bf16 parts (two
-// leave 3e-6 in a final state that is f32, one 2e-3).
+// added to it is exact to 2^-24: with the decay in three bf16 parts
+// w = w1 + w2 + w3, decayed B goes in as four (fl rounds to bf16),
+//   h = fl(w1 b),  w1 b - h,  m = fl(w2 b),  fl(w3 b + (w2 b - m)),
+// where the differences are exact, so that each takes one bf16x2 FMA for two
+// elements. (Two parts would leave 3e-6 in a final state that is f32, one 2e-3;
+// three of f32 arithmetic take 12 instructions a pair instead of 5.)
 #include <string.h>
 
 #include "gdn_linattn.cuh"
@@ -24,6 +28,7 @@ namespace {
 constexpr int kC = 128;                  // tokens of a chunk
 constexpr uint32_t kTile = kC * 128 * 2;  // bytes of a bf16 tile: two halves of 64 columns, 128-byte swizzled rows
 constexpr uint32_t kHalf = kTile / 2;
+constexpr uint32_t kTmem = 0;  // where an allocation of all 512 columns starts
 constexpr uint64_t kDrainNs = 100000000ull;
 
 struct Maps {
@@ -35,36 +40,37 @@ struct Item {
     Seg seg;
     int index, h, role;
 };
-__device__ __forceinline__ bool item_of(const Args &p, Item &it) {
+__device__ __forceinline__ bool item_of(const Args &p, uint32_t smem, Item &it) {
     const int i = blockIdx.x;
     it.role = i % p.roles;
     it.h = (i / p.roles) % p.hv;
     it.index = i / (p.roles * p.hv);
+    it.seg = p.segs[it.index];  // (beside the count, not behind it)
     if (it.index >= *p.n_segs) return false;
-    it.seg = p.segs[it.index];
+    if (smem & 1023u) {  // (dynamic shared memory alone starts at a multiple: the tiles' swizzle counts on it)
+        record_status(p.status, GDN_ECUDA);
+        return false;
+    }
     return true;
 }
 
-// Bounded waits of one thread: one that runs out marks the CTA, and every other
-// wait of it ends then.
+// Bounded waits: one that runs out marks the CTA, and every other wait of it
+// ends then. They poll (a suspended thread goes on some 500 cycles later: the
+// walk takes 7% longer). The limit is one of cycles, of which there is more
+// than one a nanosecond: little code, since the roles' loops have to stay in the
+// instruction cache together.
 struct Waiter {
     volatile int *dead;
-    int *status;
-    unsigned long long limit;
+    long long limit;
+    // of one thread
     __device__ __forceinline__ bool one(uint64_t *bar, uint32_t parity) const {
-        if (limit >= tc::kShortLimitNs && tc::mbar_try_wait(bar, parity)) return true;
-        const uint64_t t0 = tc::globaltimer_ns();
-        for (;;) {
-#pragma unroll 1
-            for (int i = 0; i < 16; ++i)
-                if (tc::mbar_test_wait(bar, parity)) return true;
-            if (*dead) return false;
-            if (tc::globaltimer_ns() - t0 > limit) {
+        const long long t0 = clock64();
+        while (!tc::mbar_test_wait(bar, parity))
+            if (*dead || clock64() - t0 > limit) {
                 *dead = 1;
-                record_status(status, GDN_ETIMEOUT);
                 return false;
             }
-        }
+        return true;
     }
     // of a whole warp, which goes on as one
     __device__ __forceinline__ bool warp(uint64_t *bar, uint32_t parity) const {
@@ -80,63 +86,112 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// w times two bf16, as three bf16 parts (each the nearest to what is left)
-__device__ __forceinline__ void split3(uint32_t x, float w, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    float2 v = __fmul2_rn(unpack2(x), make_float2(w, w));
-    hi = pack2(v.x, v.y);
-    float2 u = unpack2(hi);
-    v = __fadd2_rn(v, make_float2(-u.x, -u.y));
-    mid = pack2(v.x, v.y);
-    u = unpack2(mid);
-    v = __fadd2_rn(v, make_float2(-u.x, -u.y));
-    lo = pack2(v.x, v.y);
-}
-
-// Address inside one half of a tile of row `row`'s 16-byte group `g`
+// Address inside one column half of a tile of row `row`'s 16-byte group `g`
 __device__ __forceinline__ uint8_t *at(uint8_t *half, int row, int g) { return half + tc::sw128_offset(row, g); }
 
-// this thread's row (64 columns) of decayed B in three parts; w 0: zeros
-// whatever the row holds
-__device__ __forceinline__ void split_row(uint8_t *b_half, int row, float w, uint4 *hi, uint4 *mid, uint4 *lo) {
+// The decays of a pair of rows of B in three bf16 parts.
+struct PairDecay {
+    uint32_t w[3];
+};
+__device__ __forceinline__ PairDecay pair_decay(float2 w) {
+    PairDecay d;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-        uint4 x = *reinterpret_cast<const uint4 *>(at(b_half, row, g));
-        if (w == 0.f) x = make_uint4(0, 0, 0, 0);
-        split3(x.x, w, hi[g].x, mid[g].x, lo[g].x);
-        split3(x.y, w, hi[g].y, mid[g].y, lo[g].y);
-        split3(x.z, w, hi[g].z, mid[g].z, lo[g].z);
-        split3(x.w, w, hi[g].w, mid[g].w, lo[g].w);
+    for (int i = 0; i < 3; ++i) {
+        d.w[i] = pack2(w.x, w.y);
+        const float2 u = unpack2(d.w[i]);
+        w.x -= u.x, w.y -= u.y;
     }
-}
-__device__ __forceinline__ void store_row(uint8_t *half, int row, const uint4 *x) {
-#pragma unroll
-    for (int g = 0; g < 8; ++g) *reinterpret_cast<uint4 *>(at(half, row, g)) = x[g];
+    return d;
 }
 
+__device__ __forceinline__ __nv_bfloat162 bf2(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); }
+__device__ __forceinline__ uint32_t raw2(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t *>(&v); }
+
+// B's rows row0 .. row0 + 15 of a tile, transposed, decayed and in four parts,
+// into tensor-memory columns to + step q .. + 7 for part q. w[i][j]: part i of
+// the decays of rows row0 + 2 j and the next. Rows behind `len` count as zeros
+// whatever they hold. The warp's lanes are B's columns 32 (warp % 4) ...
+__device__ __forceinline__ void split_rows(const uint8_t *tile, int row0, const uint32_t *w0, const uint32_t *w1,
+                                           const uint32_t *w2, int len, uint32_t to, uint32_t step) {
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+    const uint32_t from = tc::smem_u32(tile) + (quarter >> 1) * kHalf;
+    // this lane's row of the blocks: of (columns 0-7, 8-15) x (rows 0-7, 8-15)
+    const int block = lane >> 3, trow = row0 + (block >> 1) * 8 + (lane & 7);
+    uint32_t x[8], y[8], d[3][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)  // 16 columns of B
+        tc::ldmatrix_x4_trans(from + tc::sw128_offset(trow, (quarter & 1) * 4 + 2 * c + (block & 1)), x + 4 * c);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int j = 4 * k + (lane & 3);
+        d[0][k] = w0[j], d[1][k] = w1[j], d[2][k] = w2[j];
+    }
+    if (row0 + 16 > len) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int row = row0 + 8 * (k >> 1 & 1) + 2 * (lane & 3);
+            if (row >= len) x[k] = 0;
+            else if (row + 1 >= len) x[k] &= 0xffffu;
+        }
+    }
+    const uint32_t lanes = tc::tmem_addr(to, quarter * 32, 0);
+    auto store = [&](int part) {
+        tc::tmem_st_16x8(lanes + part * step, y);
+        tc::tmem_st_16x8(lanes + (16 << 16) + part * step, y + 4);
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = raw2(__hmul2_rn(bf2(d[i][k >> 1 & 1]), bf2(x[k])));
+        store(2 * i);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            __nv_bfloat162 v = __hfma2(bf2(d[i][k >> 1 & 1]), bf2(x[k]), __hneg2(bf2(y[k])));
+            if (i) v = __hfma2(bf2(d[2][k >> 1 & 1]), bf2(x[k]), v);
+            y[k] = raw2(v);
+        }
+        store(2 * i + 1);
+    }
+}
+
+// zeros in the rows of a tile behind the sequence, by 256 threads
+__device__ __forceinline__ void zero_behind(uint8_t *tile, int len, int t) {
+    const int row = t & 127;
+    if (row >= len) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g) *reinterpret_cast<uint4 *>(at(tile + (t >> 7) * kHalf, row, g)) = make_uint4(0, 0, 0, 0);
+    }
+    tc::fence_proxy_async_smem();
+}
+
+// a tile, counted on `full`
 __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, int head, int row, uint64_t *full) {
-    tc::mbar_arrive_expect_tx(full, kTile);
     tc::tma_load_3d(dst, map, 0, head, row, full);
     tc::tma_load_3d(dst + kHalf, map, 64, head, row, full);
 }
 
-// operand descriptors of k-step `k` (16 of the product's inner dimension) of a tile
-__device__ __forceinline__ uint64_t k_major(uint32_t tile, int k) {
-    return tc::sdesc_sw128(tile + (k >> 2) * kHalf + (k & 3) * 32, 0, 1024);
+// brings a tile into L2
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap *map, int head, int row) {
+    tc::tma_prefetch_3d(map, 0, head, row);
+    tc::tma_prefetch_3d(map, 64, head, row);
 }
-__device__ __forceinline__ uint64_t mn_major(uint32_t tile, int k) {
-    return tc::sdesc_sw128(tile + k * 2048, kHalf, 1024);
-}
+
+// operand descriptors: of a whole tile, and what k-step `k` (16 of the product's inner dimension) adds to it
+__device__ __forceinline__ uint64_t k_major(const void *tile) { return tc::sdesc_sw128(tc::smem_u32(tile), 0, 1024); }
+__device__ __forceinline__ uint64_t mn_major(const void *tile) { return tc::sdesc_sw128(tc::smem_u32(tile), kHalf, 1024); }
+__host__ __device__ constexpr uint32_t k_step(int k) { return ((k >> 2) * kHalf + (k & 3) * 32) >> 4; }
+__host__ __device__ constexpr uint32_t mn_step(int k) { return k * 2048 >> 4; }
 constexpr uint32_t kIdKK = tc::idesc_bf16_f32(128, 128, false, false);
-constexpr uint32_t kIdMM = tc::idesc_bf16_f32(128, 128, true, true);
 constexpr uint32_t kIdKM = tc::idesc_bf16_f32(128, 128, false, true);
 
-__device__ __forceinline__ uint32_t smem_base(const uint8_t *p) { return tc::smem_u32(p); }
-
-// sum[tmem] (+)= C^T part
-__device__ __forceinline__ void mma_sum(uint32_t d, const uint8_t *c, const uint8_t *part, bool fresh) {
-    const uint32_t ca = smem_base(c), pa = smem_base(part);
+// sum (+)= the four parts' products with C's rows row0 .. row0 + 16 K - 1
+template <int K>
+__device__ __forceinline__ void mma_parts(uint32_t sum, uint32_t part, uint32_t step, uint64_t c, int row0, bool fresh) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) tc::mma_bf16(d, mn_major(ca, k), mn_major(pa, k), kIdMM, !(fresh && k == 0));
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            tc::mma_bf16_ts(sum, part + q * step + 8 * k, c + mn_step(row0 / 16 + k), kIdKM, !(fresh && q == 0 && k == 0));
 }
 
 // ---------------------------------------------------------------------------
@@ -145,11 +200,13 @@ __device__ __forceinline__ void mma_sum(uint32_t d, const uint8_t *c, const uint
 // all chunks. 8 warps split B, one copies, one issues the products.
 // ---------------------------------------------------------------------------
 constexpr int kSumThreads = 320;
+constexpr uint32_t kSumParts = 128;  // tensor-memory columns of the parts: 3 sets of 4 x 32
 
 struct SumShared {
-    uint8_t b[2][kTile], c[2][kTile], part[3][kTile];
+    uint8_t b[3][kTile], c[3][kTile];
+    uint32_t w[8][3][32];  // decays of a warp's rows
     float tab[kC + 4];
-    uint64_t b_full[2], b_free[2], c_full[2], c_free[2], part_full[3], part_free[3], done;
+    uint64_t b_full[3], b_free[3], c_full[3], c_clean[3], c_free[3], part_full[3], part_free[3], done;
     uint32_t tmem;
     int dead;
 };
@@ -157,174 +214,230 @@ struct SumShared {
 __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_constant__ Args p,
                                                               const __grid_constant__ Maps m) {
     extern __shared__ __align__(1024) uint8_t raw[];
-    SumShared &s = *reinterpret_cast<SumShared *>(raw + (-tc::smem_u32(raw) & 1023u));
+    SumShared &s = *reinterpret_cast<SumShared *>(raw);
     Item it;
-    if (!item_of(p, it)) return;
+    if (!item_of(p, tc::smem_u32(raw), it)) return;
     const Role &r = p.role[it.role];
     const Seg seg = it.seg;
     if (seg.flags & (r.against ? kFirst : kLast)) return;  // no segment follows
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const float decay = p.decay[it.h];
-    for (int n = tid; n <= kC; n += kSumThreads) s.tab[n] = power(decay, n);
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+    const int chunks = (seg.len + kC - 1) / kC;
+    auto load = [&](int n) {
+        const int u = n % 3;
+        tc::mbar_arrive_expect_tx(&s.b_full[u], kTile);
+        tc::mbar_arrive_expect_tx(&s.c_full[u], kTile);
+        load_tile(s.b[u], &m.b[it.role], it.h / r.gb, seg.start + n * kC, &s.b_full[u]);
+        load_tile(s.c[u], &m.c[it.role], it.h / r.gc, seg.start + n * kC, &s.c_full[u]);
+    };
+    if (warp == 8 && lane == 0) {
+        for (int i = 0; i < 3; ++i) {
             tc::mbar_init(&s.b_full[i], 1);
             tc::mbar_init(&s.b_free[i], 8);
             tc::mbar_init(&s.c_full[i], 1);
+            tc::mbar_init(&s.c_clean[i], 8);
             tc::mbar_init(&s.c_free[i], 1);
-        }
-        for (int i = 0; i < 3; ++i) {
-            tc::mbar_init(&s.part_full[i], 8);
+            tc::mbar_init(&s.part_full[i], 4);
             tc::mbar_init(&s.part_free[i], 1);
         }
         tc::mbar_init(&s.done, 1);
         s.dead = 0;
         tc::fence_mbar_init();
+        for (int n = 0; n < min(3, chunks); ++n) load(n);
     }
+    const float decay = p.decay[it.h];
+    if (tid <= kC) s.tab[tid] = power(decay, tid);
     if (warp == 9) {
-        tc::tmem_alloc(&s.tmem, 128);
+        tc::tmem_alloc(&s.tmem, 512);
         tc::tmem_relinquish();
     }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = s.tmem;
-    const Waiter wait{&s.dead, p.status, p.wait_ns};
-    const int chunks = (seg.len + kC - 1) / kC;
+    const Waiter wait{&s.dead, (long long)p.wait_ns};
+    // the sets of parts in turn: half `hf` of chunk n is batch 2 n + hf
+    auto part_of = [&](int batch) { return kTmem + kSumParts + (batch % 3) * 128; };
 
     if (warp == 8) {
         if (lane == 0) {
-            int n = 0;
+            int n = 3;
             for (; n < chunks; ++n) {
-                const int u = n & 1;
-                const uint32_t ph = ((n >> 1) - 1) & 1;
-                if (n >= 2 && (!wait.one(&s.b_free[u], ph) || !wait.one(&s.c_free[u], ph))) break;
-                load_tile(s.b[u], &m.b[it.role], it.h / r.gb, seg.start + n * kC, &s.b_full[u]);
-                load_tile(s.c[u], &m.c[it.role], it.h / r.gc, seg.start + n * kC, &s.c_full[u]);
+                const uint32_t ph = (n / 3 - 1) & 1;
+                if (!wait.one(&s.b_free[n % 3], ph) || !wait.one(&s.c_free[n % 3], ph)) break;
+                load(n);
             }
             if (s.dead)  // what is on its way has to land before the CTA ends
-                for (int k = max(0, n - 2); k < n; ++k) {
-                    tc::mbar_wait(&s.b_full[k & 1], (k >> 1) & 1, kDrainNs);
-                    tc::mbar_wait(&s.c_full[k & 1], (k >> 1) & 1, kDrainNs);
+                for (int k = max(0, min(n, chunks) - 3); k < min(n, chunks); ++k) {
+                    tc::mbar_wait(&s.b_full[k % 3], (k / 3) & 1, kDrainNs);
+                    tc::mbar_wait(&s.c_full[k % 3], (k / 3) & 1, kDrainNs);
                 }
         }
     } else if (warp == 9) {
-        if (lane == 0) {
-            bool ok = true;
-            for (int n = 0; n < chunks && ok; ++n) {
-                const int u = n & 1;
-                if (!(ok = wait.one(&s.c_full[u], (n >> 1) & 1))) break;
-                for (int q = 0; q < 3; ++q) {
-                    if (!(ok = wait.one(&s.part_full[q], n & 1))) break;
-                    tc::tc_fence_after();
-                    mma_sum(tmem, s.c[u], s.part[q], n == 0 && q == 0);
-                    tc::mma_commit(&s.part_free[q]);
+        const bool leader = tc::elect_one();
+        const uint64_t tiles = mn_major(s.c[0]);
+        bool ok = true;
+        for (int n = 0; n < chunks && ok; ++n) {
+            const int u = n % 3;
+            ok = wait.warp(&s.c_full[u], (n / 3) & 1) && wait.warp(&s.c_clean[u], (n / 3) & 1);
+            const uint64_t c = tiles + u * (kTile >> 4);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int batch = 2 * n + hf;
+                if (!(ok = ok && wait.warp(&s.part_full[batch % 3], (batch / 3) & 1))) break;
+                tc::tc_fence_after();
+                if (leader) {
+                    mma_parts<4>(kTmem, part_of(batch), 32, c, 64 * hf, batch == 0);
+                    tc::mma_commit(&s.part_free[batch % 3]);
+                    if (hf) tc::mma_commit(&s.c_free[u]);
                 }
-                if (ok) tc::mma_commit(&s.c_free[u]);
             }
+        }
+        if (leader) {
             tc::mma_commit(&s.done);  // all products have ended
             tc::mbar_wait(&s.done, 0, kDrainNs);
         }
     } else {
-        const int half = warp >> 2, row = tid & 127;
+        const int hf = warp >> 2;
         bool ok = true;
         for (int n = 0; n < chunks && ok; ++n) {
-            const int u = n & 1, from = n * kC, len = min(kC, seg.len - from);
-            const uint32_t ph = (n >> 1) & 1;
-            float w = 0.f;
-            if (row < len)
-                w = r.scale_in * (r.against ? power(decay, from) * s.tab[row]
-                                            : power(decay, seg.len - from - len) * s.tab[len - 1 - row]);
-            if (!(ok = wait.warp(&s.b_full[u], ph))) break;
-            uint4 part[3][8];
-            split_row(s.b[u] + half * kHalf, row, w, part[0], part[1], part[2]);
-            tc::warp_arrive(&s.b_free[u]);
-            if (len < kC) {  // rows of the next sequence, or behind the tensor's end
+            const int u = n % 3, from = n * kC, len = min(kC, seg.len - from), batch = 2 * n + hf;
+            const uint32_t ph = (n / 3) & 1;
+            if (len < kC) {
                 if (!(ok = wait.warp(&s.c_full[u], ph))) break;
-                if (row >= len) {
-                    const uint4 zero[8] = {};
-                    store_row(s.c[u] + half * kHalf, row, zero);
-                }
+                zero_behind(s.c[u], len, tid);
             }
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                if (ok && n > 0) ok = wait.warp(&s.part_free[q], (n - 1) & 1);
-                if (ok) {
-                    store_row(s.part[q] + half * kHalf, row, part[q]);
-                    tc::fence_proxy_async_smem();
-                    tc::warp_arrive(&s.part_full[q]);
-                }
-            }
+            tc::warp_arrive(&s.c_clean[u]);
+            const float over = r.scale_in * power(decay, r.against ? from : seg.len - from - len);
+            const int row = 64 * hf + 2 * lane;
+            const PairDecay d = pair_decay(r.against ? make_float2(over * s.tab[row], over * s.tab[row + 1])
+                                                     : make_float2(over * s.tab[max(len - 1 - row, 0)],
+                                                                   over * s.tab[max(len - 2 - row, 0)]));
+            uint32_t(*w)[32] = s.w[warp];
+            __syncwarp();
+            w[0][lane] = d.w[0], w[1][lane] = d.w[1], w[2][lane] = d.w[2];
+            __syncwarp();
+            if (!(ok = wait.warp(&s.b_full[u], ph))) break;
+            if (batch >= 3 && !(ok = wait.warp(&s.part_free[batch % 3], (batch / 3 - 1) & 1))) break;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int t = 0; t < 4; ++t)
+                split_rows(s.b[u], 64 * hf + 16 * t, w[0] + 8 * t, w[1] + 8 * t, w[2] + 8 * t, len, part_of(batch) + 8 * t, 32);
+            tc::warp_arrive(&s.b_free[u]);
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::warp_arrive(&s.part_full[batch % 3]);
         }
     }
     __syncwarp();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    if (warp < 8 && !s.dead) {  // lane: c, columns: b
-        const int c = tid & 127, b0 = (warp >> 2) * 64;
-        float *to = r.states + (size_t(it.index) * p.hv + it.h) * kState + c;
+    if (warp < 8 && !s.dead) {  // lane: b, columns: c
+        const int b = tid & 127, c0 = (warp >> 2) * 64;
+        float *to = r.states + (size_t(it.index) * p.hv + it.h) * kState + b * kHeadDim + c0;
 #pragma unroll
         for (int x = 0; x < 64; x += 16) {
             float v[16];
-            tc::tmem_ld16(tc::tmem_addr(tmem, (warp & 3) * 32, b0 + x), v);
+            tc::tmem_ld16(tc::tmem_addr(kTmem, (warp & 3) * 32, c0 + x), v);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) to[(b0 + x + i) * kHeadDim] = v[i];
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4 *>(to + x + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
         tc::tc_fence_before();
     }
     __syncthreads();
-    if (warp == 9) tc::tmem_dealloc(tmem, 128);
+    if (tid == 0 && s.dead) record_status(p.status, GDN_ETIMEOUT);
+    if (warp == 9) tc::tmem_dealloc(kTmem, 512);
 }
 
 // ---------------------------------------------------------------------------
-// The walk of one segment. Warps 0-3 take the scores' decays, warps 4-11 hold
-// the state (row c, 64 columns b a thread), split B and finish the output,
-// warp 12 copies, warp 13 issues the products (14 and 15 fill a group of four
-// warps, to which registers are dealt).
+// The walk of one segment. Warps 0-3 take the scores' decays, warps 4-11 split
+// B (each group of four every other 16 rows), warps 12-19 hold the state (row
+// b, 64 columns c a thread) and finish the output, warps 20 and 22 copy in and
+// out, warp 21 issues the products (23 fills their group of four, whose registers
+// the others get). The products' order, P, sum, inter, intra of each chunk, leaves
+// each of the other warps the time of five products or more.
+// inter and intra have one accumulator: both are taken over the row's
+// e = max(lambda^(i+1), 2^-64), which the finished row is multiplied with.
+// Where a decay is below 2^-64 the state's part is 2^-64 of the undecayed one
+// instead.
+// What bounds a chunk is shared memory as much as the products: 56 products of
+// 128 x 128 x 16 take 67 cycles each, an operand in shared memory is 4 KiB of
+// its 128 bytes a cycle, and both operands there would fill it. So the parts of
+// B and the scores are operands in tensor memory.
 // ---------------------------------------------------------------------------
-constexpr int kWalkThreads = 512;
-constexpr uint32_t kColP = 0, kColIntra = 128, kColInter = 256, kColSum = 384;
+constexpr int kWalkThreads = 768;
+constexpr uint32_t kColP = 0, kColOut = 128, kColSum = 256, kColPart = 384;  // parts: 4 sets of 4 x 8 columns
+constexpr float kLeast = 5.421010862427522e-20f;                             // 2^-64
 
 struct WalkShared {
-    uint8_t a[2][kTile], b[kTile], c[kTile], part[2][kTile], state[kTile];
-    float tab[kC + 4];   // lambda^n
-    float down[kC + 4];  // lambda^(128 - n)
-    uint64_t a_full[2], a_free[2], b_full, b_free, c_full, c_free, part_full, third_full, first_free, p_full, scores_full,
-        sum_full, sum_free, state_full, state_free, out_full, out_free, staged[2], drain;
+    uint8_t a[2][kTile], b[2][kTile], c[2][kTile], state[kTile];
+    float between[2 * kC];  // [128 + d]: lambda^|d|, d from -128 to 127
+    uint32_t w[2][3][kC / 2];  // decays of B's rows, of a whole chunk and of the sequence's last one
+    uint64_t ab_full[2], c_full[2], a_free[2], b_free[2], c_clean[2], c_free[2], part_full[4], part_free[4], p_full,
+        scores_full, sum_full, sum_free, state_full, state_free, out_full, out_free, staged, drain;
     uint32_t tmem;
     int dead;
 };
 
+// 32 bytes to global memory: one sector a thread
+__device__ __forceinline__ void store_sector(void *to, const uint32_t *w, bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_constant__ Args p,
                                                                 const __grid_constant__ Maps m) {
     extern __shared__ __align__(1024) uint8_t raw[];
-    WalkShared &s = *reinterpret_cast<WalkShared *>(raw + (-tc::smem_u32(raw) & 1023u));
+    WalkShared &s = *reinterpret_cast<WalkShared *>(raw);
     Item it;
-    if (!item_of(p, it)) return;
+    if (!item_of(p, tc::smem_u32(raw), it)) return;
     const Role &r = p.role[it.role];
     const Seg seg = it.seg;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const float decay = p.decay[it.h];
-    for (int n = tid; n <= kC; n += kWalkThreads) {
-        const float f = power(decay, n);
-        s.tab[n] = f;
-        s.down[kC - n] = f;
-    }
-    if (tid == 0) {
+    const int chunks = (seg.len + kC - 1) / kC;
+    const bool leaves = r.fin && (seg.flags & (r.against ? kFirst : kLast));  // the state behind the last chunk is wanted
+    // the walk's n-th chunk
+    auto chunk_from = [&](int n) { return (r.against ? chunks - 1 - n : n) * kC; };
+    auto chunk_len = [&](int n) { return min(kC, seg.len - chunk_from(n)); };
+    auto sums = [&](int n) { return n + 1 < chunks || leaves; };
+    // tiles of the n-th chunk; A and B are counted on one barrier
+    auto row_of = [&](int n) { return seg.start + chunk_from(n); };
+    auto load_b = [&](int n) {
+        tc::mbar_arrive_expect_tx(&s.ab_full[n & 1], 2 * kTile);
+        load_tile(s.b[n & 1], &m.b[it.role], it.h / r.gb, row_of(n), &s.ab_full[n & 1]);
+    };
+    auto load_a = [&](int n) { load_tile(s.a[n & 1], &m.a[it.role], it.h / r.ga, row_of(n), &s.ab_full[n & 1]); };
+    auto load_c = [&](int n) {
+        tc::mbar_arrive_expect_tx(&s.c_full[n & 1], kTile);
+        load_tile(s.c[n & 1], &m.c[it.role], it.h / r.gc, row_of(n), &s.c_full[n & 1]);
+    };
+    // the chunk after those under way comes from HBM meanwhile
+    auto prefetch = [&](int n) {
+        if (n >= chunks) return;
+        prefetch_tile(&m.b[it.role], it.h / r.gb, row_of(n));
+        prefetch_tile(&m.a[it.role], it.h / r.ga, row_of(n));
+        prefetch_tile(&m.c[it.role], it.h / r.gc, row_of(n));
+    };
+    if (warp == 20 && lane == 0) {
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&s.a_full[i], 1);
-            tc::mbar_init(&s.a_free[i], 2);
-            tc::mbar_init(&s.staged[i], 4);
+            tc::mbar_init(&s.ab_full[i], 1);
+            tc::mbar_init(&s.c_full[i], 1);
+            tc::mbar_init(&s.a_free[i], 1);
+            tc::mbar_init(&s.b_free[i], 9);
+            tc::mbar_init(&s.c_clean[i], 8);
+            tc::mbar_init(&s.c_free[i], 1);
         }
-        tc::mbar_init(&s.b_full, 1);
-        tc::mbar_init(&s.b_free, 9);
-        tc::mbar_init(&s.c_full, 1);
-        tc::mbar_init(&s.c_free, 1);
-        tc::mbar_init(&s.part_full, 8);
-        tc::mbar_init(&s.third_full, 8);
-        tc::mbar_init(&s.first_free, 1);
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(&s.part_full[i], 4);
+            tc::mbar_init(&s.part_free[i], 1);
+        }
         tc::mbar_init(&s.p_full, 1);
         tc::mbar_init(&s.scores_full, 4);
         tc::mbar_init(&s.sum_full, 1);
@@ -333,308 +446,342 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
         tc::mbar_init(&s.state_free, 1);
         tc::mbar_init(&s.out_full, 1);
         tc::mbar_init(&s.out_free, 8);
+        tc::mbar_init(&s.staged, 8);
         tc::mbar_init(&s.drain, 1);
         s.dead = 0;
         tc::fence_mbar_init();
+        for (int n = 0; n < min(2, chunks); ++n) load_b(n), load_a(n), load_c(n);
+        prefetch(2);
     }
-    if (warp == 13) {
+    const float decay = p.decay[it.h];
+    if (tid <= kC) {
+        const float f = power(decay, tid);
+        s.between[kC - tid] = f;
+        if (tid < kC) s.between[kC + tid] = f;
+    }
+    if (tid >= 256 && tid < 256 + kC) {  // B's decays, of a whole chunk and of the one that ends the segment
+        const int which = (tid - 256) / (kC / 2), pair = tid % (kC / 2), row = 2 * pair;
+        const int len = which ? seg.len - (chunks - 1) * kC : kC;
+        float2 f = make_float2(0.f, 0.f);
+        if (row < len) f.x = r.scale_in * power(decay, r.against ? row : len - 1 - row);
+        if (row + 1 < len) f.y = r.scale_in * power(decay, r.against ? row + 1 : len - 2 - row);
+        const PairDecay d = pair_decay(f);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) s.w[which][i][pair] = d.w[i];
+    }
+    if (warp == 21) {
         tc::tmem_alloc(&s.tmem, 512);
         tc::tmem_relinquish();
     }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = s.tmem;
-    const Waiter wait{&s.dead, p.status, p.wait_ns};
-    const int chunks = (seg.len + kC - 1) / kC;
-    const bool leaves = r.fin && (seg.flags & (r.against ? kFirst : kLast));  // the state behind the last chunk is wanted
-    // the walk's n-th chunk
-    auto chunk_from = [&](int n) { return (r.against ? chunks - 1 - n : n) * kC; };
-    auto chunk_len = [&](int n) { return min(kC, seg.len - chunk_from(n)); };
-    auto sums = [&](int n) { return n + 1 < chunks || leaves; };
+    const Waiter wait{&s.dead, (long long)p.wait_ns};
+    auto power_of = [&](int n) { return s.between[kC - n]; };  // lambda^n, n from 0 to 128
 
-    if (warp >= 12) {
+    // 768 threads are launched with 80 registers each: 128 x (56 + 40) + 256 x (64 + 128) is the same
+    if (warp >= 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 12 && lane == 0) {
-            int n = 0;
-            for (; n < chunks; ++n) {
-                const int u = n & 1, row = seg.start + chunk_from(n);
-                if (n >= 2 && !wait.one(&s.a_free[u], ((n >> 1) - 1) & 1)) break;
-                load_tile(s.a[u], &m.a[it.role], it.h / r.ga, row, &s.a_full[u]);
-                if (n >= 1 && !wait.one(&s.b_free, (n - 1) & 1)) { ++n; break; }
-                load_tile(s.b, &m.b[it.role], it.h / r.gb, row, &s.b_full);
-                if (n >= 1 && !wait.one(&s.c_free, (n - 1) & 1)) { ++n; break; }
-                load_tile(s.c, &m.c[it.role], it.h / r.gc, row, &s.c_full);
+        if (warp == 20 && lane == 0) {
+            int na = min(2, chunks), nc = na;  // tiles asked for
+            for (int n = 2; n < chunks; ++n) {
+                const int u = n & 1;
+                const uint32_t ph = ((n >> 1) - 1) & 1;
+                if (!wait.one(&s.b_free[u], ph) || !wait.one(&s.a_free[u], ph)) break;
+                load_b(n), load_a(n), ++na;
+                prefetch(n + 1);
+                if (!wait.one(&s.c_free[u], ph)) break;
+                load_c(n), ++nc;
             }
-            if (s.dead && n > 0) {  // what is on its way has to land before the CTA ends
-                for (int k = max(0, n - 2); k < n; ++k) tc::mbar_wait(&s.a_full[k & 1], (k >> 1) & 1, kDrainNs);
-                tc::mbar_wait(&s.b_full, (n - 1) & 1, kDrainNs);
-                tc::mbar_wait(&s.c_full, (n - 1) & 1, kDrainNs);
+            if (s.dead) {  // what is on its way has to land before the CTA ends
+                for (int k = max(0, na - 2); k < na; ++k) tc::mbar_wait(&s.ab_full[k & 1], (k >> 1) & 1, kDrainNs);
+                for (int k = max(0, nc - 2); k < nc; ++k) tc::mbar_wait(&s.c_full[k & 1], (k >> 1) & 1, kDrainNs);
             }
-        } else if (warp == 13 && lane == 0) {
-            const uint32_t b = smem_base(s.b), c = smem_base(s.c), st = smem_base(s.state);
+        } else if (warp == 22 && lane == 0) {  // finished chunks out, and their C's place back
             for (int n = 0; n < chunks; ++n) {
-                const uint32_t ph = n & 1, before = (n - 1) & 1, a = smem_base(s.a[n & 1]);
-                if (!wait.one(&s.a_full[n & 1], (n >> 1) & 1) || !wait.one(&s.b_full, ph)) break;
-                tc::tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) tc::mma_bf16(tmem + kColP, k_major(a, k), k_major(b, k), kIdKK, k > 0);
-                tc::mma_commit(&s.p_full);
-                tc::mma_commit(&s.b_free);
-                if (!wait.one(&s.c_full, ph)) break;
-                if (sums(n)) {
-                    if (!wait.one(&s.part_full, ph) || (n > 0 && !wait.one(&s.sum_free, before))) break;
-                    tc::tc_fence_after();
-                    mma_sum(tmem + kColSum, s.c, s.part[0], true);
-                    tc::mma_commit(&s.first_free);
-                    mma_sum(tmem + kColSum, s.c, s.part[1], false);
-                    if (!wait.one(&s.third_full, ph)) break;
-                    tc::tc_fence_after();
-                    mma_sum(tmem + kColSum, s.c, s.part[0], false);
-                    tc::mma_commit(&s.sum_full);
+                if (!wait.one(&s.staged, n & 1)) break;
+                if (chunk_len(n) == kC && !r.partial) {
+                    for (int half = 0; half < 2; ++half)
+                        tc::tma_store_3d(&m.o[it.role], half * 64, it.h, seg.start + chunk_from(n), s.c[n & 1] + half * kHalf);
+                    tc::bulk_commit_group();
+                    tc::bulk_wait_group_read<0>();
                 }
-                // (a chunk's rows behind its sequence are zeroed in C before the state is handed over)
-                if (!wait.one(&s.scores_full, ph) || (chunk_len(n) < kC && !wait.one(&s.state_full, ph)) ||
-                    (n > 0 && !wait.one(&s.out_free, before)))
-                    break;
-                tc::tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    tc::mma_bf16_ts(tmem + kColIntra, tmem + kColP + k * 8, mn_major(c, k), kIdKM, k > 0);
-                tc::mma_commit(&s.c_free);
-                if (!wait.one(&s.state_full, ph)) break;
-                tc::tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) tc::mma_bf16(tmem + kColInter, k_major(a, k), k_major(st, k), kIdKK, k > 0);
-                tc::mma_commit(&s.state_free);
-                tc::mma_commit(&s.out_full);
+                tc::mbar_arrive(&s.c_free[n & 1]);
             }
-            tc::mma_commit(&s.drain);
-            tc::mbar_wait(&s.drain, 0, kDrainNs);
-        }
-    } else if (warp < 4) {
-        // decayed scores: row i of the chunk, bf16 over the scores' own columns. Left of the diagonal block of
-        // 32 the decay is one factor of the row times one of the column (both at most 1), in it one of i - j.
-        const int i = tid, i0 = warp * 32;
-        const uint32_t mine = tc::tmem_addr(tmem + kColP, i0, 0);
-        for (int n = 0; n < chunks; ++n) {
-            if (!wait.warp(&s.p_full, n & 1)) break;
-            tc::tc_fence_after();
-            const int len = chunk_len(n);
-            const float row = r.scale_in * (r.against ? s.tab[i0 + 32 - i] : s.tab[i - i0]);
+            tc::bulk_wait_group_all();
+        } else if (warp == 21 && chunks > 0) {
+            const bool leader = tc::elect_one();
+            const uint64_t a0 = k_major(s.a[0]), b0 = k_major(s.b[0]), c0 = mn_major(s.c[0]), st = mn_major(s.state);
+            auto tile = [](int n) { return uint64_t(n & 1) * (kTile >> 4); };
+            auto scores = [&](int n) {
+                if (!wait.warp(&s.ab_full[n & 1], (n >> 1) & 1)) return false;
+                tc::tc_fence_after();
+                const uint64_t a = a0 + tile(n), b = b0 + tile(n);
+                if (leader) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t w[16];
-                const int j0 = 32 * x;
-                if (r.against ? x < warp || j0 >= len : x > warp) {
+                    for (int k = 0; k < 8; ++k) tc::mma_bf16(kTmem + kColP, a + k_step(k), b + k_step(k), kIdKK, k > 0);
+                    tc::mma_commit(&s.p_full);
+                    tc::mma_commit(&s.b_free[n & 1]);
+                }
+                return true;
+            };
+            bool ok = true;
+            for (int n = 0; ok && n < chunks; ++n) {
+                const uint32_t ph = n & 1, before = (n - 1) & 1;
+                const uint64_t c = c0 + tile(n), a = a0 + tile(n);
+                const bool more = sums(n);
+                if (!(ok = scores(n) && wait.warp(&s.c_full[n & 1], (n >> 1) & 1) &&
+                           (chunk_len(n) == kC || wait.warp(&s.c_clean[n & 1], (n >> 1) & 1))))
+                    break;
+                if (more) {
+                    if (n > 0 && !(ok = wait.warp(&s.sum_free, before))) break;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) w[k] = 0;
-                } else {
-                    float v[32];
-                    tc::tmem_ld32(mine + j0, v);
-                    tc::tmem_ld_wait();
-                    if (x == warp) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int d = r.against ? k - lane : lane - k;
-                            v[k] = d >= 0 && (!r.against || j0 + k < len) ? v[k] * (r.scale_in * s.tab[max(d, 0)]) : 0.f;
-                        }
-                    } else {
-                        const float *col = r.against ? s.tab + (j0 - i0 - 32) : s.down + (kC - i0 + j0);
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(col + k);
-                            v[k] *= row * f.x, v[k + 1] *= row * f.y, v[k + 2] *= row * f.z, v[k + 3] *= row * f.w;
-                        }
-                        if (r.against && j0 + 32 > len) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (j0 + k >= len) v[k] = 0.f;
+                    for (int t = 0; t < 8; ++t) {
+                        if (!(ok = ok && wait.warp(&s.part_full[t & 3], t >> 2))) break;
+                        tc::tc_fence_after();
+                        if (leader) {
+                            mma_parts<1>(kTmem + kColSum, kTmem + kColPart + (t & 3) * 32, 8, c, 16 * t, t == 0);
+                            tc::mma_commit(&s.part_free[t & 3]);
+                            if (t == 7) tc::mma_commit(&s.sum_full);
                         }
                     }
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) w[k] = pack2(v[2 * k], v[2 * k + 1]);
+                    if (!ok) break;
                 }
-                tc::tmem_st16(mine + 16 * x, w);
+                if (!(ok = wait.warp(&s.state_full, ph) && (n == 0 || wait.warp(&s.out_free, before)))) break;
+                tc::tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) tc::mma_bf16(kTmem + kColOut, a + k_step(k), st + mn_step(k), kIdKM, k > 0);
+                    tc::mma_commit(&s.state_free);
+                    tc::mma_commit(&s.a_free[n & 1]);
+                }
+                if (!(ok = wait.warp(&s.scores_full, ph))) break;
+                tc::tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(kTmem + kColOut, kTmem + kColP + k * 8, c + mn_step(k), kIdKM, 1);
+                    tc::mma_commit(&s.out_full);
+                }
+            }
+            if (leader) {
+                tc::mma_commit(&s.drain);
+                tc::mbar_wait(&s.drain, 0, kDrainNs);
+            }
+        }
+    } else if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // decayed scores: row i of the chunk, bf16 over the scores' own columns. Beside the diagonal block of
+        // 32 the decay is one factor of the row times one of the column (at most 1), in it one of i - j.
+        const int i = tid, i0 = warp * 32;
+        const uint32_t mine = tc::tmem_addr(kTmem + kColP, i0, 0);
+        const float row_in = r.against ? power_of(i0 + 32 - i) : power_of(i - i0);
+        const float *diagonal = s.between + kC - i, *beside = s.between + kC - i0 - (r.against ? 32 : 0);
+#pragma unroll 1
+        for (int n = 0; n < chunks; ++n) {
+            const int len = chunk_len(n), off = entry_offset(r, seg, n == 0);
+            const float over = r.scale_in / fmaxf(power_of(r.against ? max(len - 1 - i, 0) + off : i + off), kLeast);
+            const float2 over2 = make_float2(over, over), row2 = make_float2(row_in * over, row_in * over);
+            if (!wait.warp(&s.p_full, n & 1)) break;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int j0 = 0; j0 < kC; j0 += 16) {
+                uint32_t w[8];
+                const int x = j0 >> 5;
+                if (r.against ? x < warp || j0 >= len : x > warp) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) w[k] = 0;
+                } else {
+                    float v[16];
+                    tc::tmem_ld16(mine + j0, v);
+                    tc::tmem_ld_wait();
+                    if (x == warp) {
+                        const float *f = diagonal + j0;
+                        const int at = r.against ? j0 - i : i - j0, step = r.against ? 1 : -1;
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            const float2 y = __fmul2_rn(make_float2(v[k], v[k + 1]), __fmul2_rn(over2, make_float2(f[k], f[k + 1])));
+                            v[k] = at + step * k >= 0 ? y.x : 0.f;
+                            v[k + 1] = at + step * (k + 1) >= 0 ? y.y : 0.f;
+                        }
+                    } else {
+                        const float *f = beside + j0;
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4) {
+                            const float4 g = *reinterpret_cast<const float4 *>(f + k);
+                            const float2 v0 = __fmul2_rn(make_float2(v[k], v[k + 1]), __fmul2_rn(row2, make_float2(g.x, g.y)));
+                            const float2 v1 = __fmul2_rn(make_float2(v[k + 2], v[k + 3]), __fmul2_rn(row2, make_float2(g.z, g.w)));
+                            v[k] = v0.x, v[k + 1] = v0.y, v[k + 2] = v1.x, v[k + 3] = v1.y;
+                        }
+                    }
+                    if (j0 + 16 > len) {  // columns behind the sequence
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (j0 + k >= len) v[k] = 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) w[k] = pack2(v[2 * k], v[2 * k + 1]);
+                }
+                tc::tmem_st8(mine + j0 / 2, w);
             }
             tc::tmem_st_wait();
             tc::tc_fence_before();
             tc::warp_arrive(&s.scores_full);
         }
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // B, decayed, in parts, every other 16 rows; C's rows behind the sequence
+        const int group = (warp - 4) >> 2;
+        bool ok = true;
+#pragma unroll 1
+        for (int n = 0; n < chunks && ok; ++n) {
+            const int len = chunk_len(n);
+            if (len < kC) {
+                if (!(ok = wait.warp(&s.c_full[n & 1], (n >> 1) & 1))) break;
+                zero_behind(s.c[n & 1], len, tid - 128);
+            }
+            tc::warp_arrive(&s.c_clean[n & 1]);
+            if (!sums(n)) break;  // the last chunk
+            if (!(ok = wait.warp(&s.ab_full[n & 1], (n >> 1) & 1))) break;
+            const uint32_t(*w)[kC / 2] = s.w[len < kC];
+#pragma unroll 1
+            for (int t = group; t < 8; t += 2) {
+                const int set = t & 3;
+                if (8 * n + t >= 4 && !(ok = wait.warp(&s.part_free[set], (t >> 2) ^ 1))) break;
+                tc::tc_fence_after();
+                split_rows(s.b[n & 1], 16 * t, w[0] + 8 * t, w[1] + 8 * t, w[2] + 8 * t, len, kTmem + kColPart + set * 32, 8);
+                if (t >= 6) tc::warp_arrive(&s.b_free[n & 1]);
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                tc::warp_arrive(&s.part_full[set]);
+            }
+        }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        const int half = (warp - 4) >> 2, row = tid & 127, lane0 = (warp & 3) * 32, b0 = half * 64;
-        const uint32_t sum = tc::tmem_addr(tmem + kColSum, lane0, b0), intra = tc::tmem_addr(tmem + kColIntra, lane0, b0),
-                       inter = tc::tmem_addr(tmem + kColInter, lane0, b0);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        const int half = (warp - 12) >> 2, row = tid & 127, lane0 = (warp & 3) * 32, c0 = half * 64;
+        const uint32_t sum = tc::tmem_addr(kTmem + kColSum, lane0, c0), acc = tc::tmem_addr(kTmem + kColOut, lane0, c0);
         const size_t per_head = size_t(p.hv) * kState;
-        float st[64];
+        float2 st[32];  // row b of the state, columns c0 ..
         // the state that enters: the sequence's own, or the chained sum of the segments before
-        const bool enters = seg.flags & (r.against ? kLast : kFirst);
-        if (!enters) {
-            const float *from = r.states + size_t(it.index) * per_head + size_t(it.h) * kState + row;
+        const bool own = seg.flags & (r.against ? kLast : kFirst);
+        const float *enters = own ? r.init : r.states;
+        if (enters) {
+            enters += size_t(own ? seg.seq : it.index) * per_head + size_t(it.h) * kState;
+            if (own && r.swapped) {
 #pragma unroll
-            for (int k = 0; k < 64; ++k) st[k] = from[(b0 + k) * kHeadDim];
-        } else if (r.init) {
-            const float *from = r.init + size_t(seg.seq) * per_head + size_t(it.h) * kState;
+                for (int k = 0; k < 32; ++k)
+                    st[k] = make_float2(enters[(c0 + 2 * k) * kHeadDim + row], enters[(c0 + 2 * k + 1) * kHeadDim + row]);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 64; ++k) st[k] = r.swapped ? from[row * kHeadDim + b0 + k] : from[(b0 + k) * kHeadDim + row];
+                for (int k = 0; k < 32; k += 2) {
+                    const float4 v = *reinterpret_cast<const float4 *>(enters + row * kHeadDim + c0 + 2 * k);
+                    st[k] = make_float2(v.x, v.y), st[k + 1] = make_float2(v.z, v.w);
+                }
+            }
         } else {
 #pragma unroll
-            for (int k = 0; k < 64; ++k) st[k] = 0.f;
+            for (int k = 0; k < 32; ++k) st[k] = make_float2(0.f, 0.f);
         }
-        // S = lambda^len S + the chunk's sum
-        auto advance = [&](int n) {
-            const float keep = s.tab[chunk_len(n) - 1 + entry_offset(r, seg, n == 0)];
-#pragma unroll
-            for (int x = 0; x < 64; x += 16) {
-                float v[16];
-                tc::tmem_ld16(sum + x, v);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) st[x + k] = fmaf(keep, st[x + k], v[k]);
-            }
-            tc::tc_fence_before();
-        };
-        uint32_t stores = 0;
-        // the output of chunk n, through the place of its A tile when it is whole
-        auto finish = [&](int n) {
-            const int len = chunk_len(n), from = seg.start + chunk_from(n);
-            const int off = entry_offset(r, seg, n == 0);
-            const float f = row < len ? r.scale_out * s.tab[r.against ? len - 1 - row + off : row + off] : 0.f;
-            const bool staged = len == kC && !r.partial;
-            uint8_t *half_tile = s.a[n & 1] + half * kHalf;
-            const size_t at_out = (size_t(from + row) * p.hv + it.h) * kHeadDim + b0;
-#pragma unroll
-            for (int x = 0; x < 64; x += 16) {
-                float u[16], v[16];
-                tc::tmem_ld16(intra + x, u);
-                tc::tmem_ld16(inter + x, v);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) u[k] = fmaf(f, v[k], r.scale_out * u[k]);
-                if (r.partial) {
-                    if (row < len) {
-                        float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(r.out) + at_out + x);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) to[k] = make_float4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float *w = u + 8 * g;
-                        const uint4 y = make_uint4(pack2(w[0], w[1]), pack2(w[2], w[3]), pack2(w[4], w[5]), pack2(w[6], w[7]));
-                        if (staged) *reinterpret_cast<uint4 *>(at(half_tile, row, x / 8 + g)) = y;
-                        else if (row < len)
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(r.out) + at_out + x + 8 * g) = y;
-                    }
-                }
-            }
-            tc::tc_fence_before();
-            tc::warp_arrive(&s.out_free);
-            if (staged) {
-                tc::fence_proxy_async_smem();
-                tc::warp_arrive(&s.staged[half]);
-                if (row == 0 && wait.one(&s.staged[half], stores++ & 1)) {
-                    tc::tma_store_3d(&m.o[it.role], b0, it.h, from, half_tile);
-                    tc::bulk_commit_group();
-                }
-                __syncwarp();
-            }
-        };
-        uint8_t *b_half = s.b + half * kHalf;
-        int n = 0;
-        for (; n < chunks; ++n) {
-            const uint32_t ph = n & 1, before = (n - 1) & 1;
-            const int len = chunk_len(n);
-            const bool more = sums(n);
-            if (n > 0) {
-                if (!wait.warp(&s.sum_full, before)) break;
+        bool ok = true;
+#pragma unroll 1
+        for (int n = 0; n <= chunks; ++n) {
+            const uint32_t before = (n - 1) & 1;
+            if (n > 0 && sums(n - 1)) {  // S = lambda^len S + the chunk's sum
+                if (!(ok = wait.warp(&s.sum_full, before))) break;
                 tc::tc_fence_after();
-                advance(n - 1);
+                const float keep = power_of(chunk_len(n - 1) - 1 + entry_offset(r, seg, n == 1));
+#pragma unroll
+                for (int x = 0; x < 64; x += 16) {
+                    float v[16];
+                    tc::tmem_ld16(sum + x, v);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        st[x / 2 + k] = __ffma2_rn(make_float2(keep, keep), st[x / 2 + k], make_float2(v[2 * k], v[2 * k + 1]));
+                }
+                tc::tc_fence_before();
                 tc::warp_arrive(&s.sum_free);
             }
-            if (len < kC) {
-                if (!wait.warp(&s.c_full, ph)) break;
-                if (row >= len) {
-                    const uint4 zero[8] = {};
-                    store_row(s.c + half * kHalf, row, zero);
-                }
-            }
-            uint4 lo[8];
-            if (more) {
-                if (!wait.warp(&s.b_full, ph)) break;
-                const float w = row < len ? r.scale_in * s.tab[r.against ? row : len - 1 - row] : 0.f;
+            if (n < chunks) {
+                if (n > 0 && !(ok = wait.warp(&s.state_free, before))) break;
 #pragma unroll
                 for (int g = 0; g < 8; ++g) {
-                    uint4 x = *reinterpret_cast<const uint4 *>(at(b_half, row, g)), hi, mid;
-                    if (w == 0.f) x = make_uint4(0, 0, 0, 0);
-                    split3(x.x, w, hi.x, mid.x, lo[g].x);
-                    split3(x.y, w, hi.y, mid.y, lo[g].y);
-                    split3(x.z, w, hi.z, mid.z, lo[g].z);
-                    split3(x.w, w, hi.w, mid.w, lo[g].w);
-                    *reinterpret_cast<uint4 *>(at(s.part[0] + half * kHalf, row, g)) = hi;
-                    *reinterpret_cast<uint4 *>(at(s.part[1] + half * kHalf, row, g)) = mid;
+                    const float2 *x = st + 4 * g;
+                    *reinterpret_cast<uint4 *>(at(s.state + half * kHalf, row, g)) =
+                        make_uint4(pack2(x[0].x, x[0].y), pack2(x[1].x, x[1].y), pack2(x[2].x, x[2].y), pack2(x[3].x, x[3].y));
                 }
                 tc::fence_proxy_async_smem();
-                tc::warp_arrive(&s.part_full);
+                tc::warp_arrive(&s.state_full);
             }
-            tc::warp_arrive(&s.b_free);
-            if (n > 0 && !wait.warp(&s.state_free, before)) break;
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const float *x = st + 8 * g;
-                *reinterpret_cast<uint4 *>(at(s.state + half * kHalf, row, g)) =
-                    make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-            }
-            tc::fence_proxy_async_smem();
-            tc::warp_arrive(&s.state_full);
-            if (n > 0) {
-                if (!wait.warp(&s.out_full, before)) break;
+            if (n > 0) {  // the output of the chunk before
+                const int c = n - 1, len = chunk_len(c), from = seg.start + chunk_from(c);
+                const int off = entry_offset(r, seg, c == 0);
+                const float f = r.scale_out * fmaxf(power_of(r.against ? max(len - 1 - row, 0) + off : row + off), kLeast);
+                const float2 f2 = make_float2(f, f);
+                const size_t at_out = (size_t(from + row) * p.hv + it.h) * kHeadDim + c0;
+                if (!(ok = wait.warp(&s.out_full, before))) break;
                 tc::tc_fence_after();
-                finish(n - 1);
-            }
-            if (more) {
-                if (!wait.warp(&s.first_free, ph)) break;
-                store_row(s.part[0] + half * kHalf, row, lo);
-                tc::fence_proxy_async_smem();
-                tc::warp_arrive(&s.third_full);
-            }
-            if (n > 0 && row == 0) {  // the output's copy has read the tile that the next A goes to
-                tc::bulk_wait_group_read<0>();
-                tc::mbar_arrive(&s.a_free[(n - 1) & 1]);
-            }
-            __syncwarp();
-        }
-        if (n == chunks) {
-            bool ok = true;
-            if (leaves && chunks > 0) {
-                ok = wait.warp(&s.sum_full, (chunks - 1) & 1);
-                if (ok) {
-                    tc::tc_fence_after();
-                    advance(chunks - 1);
-                }
-            }
-            if (chunks > 0 && ok && wait.warp(&s.out_full, (chunks - 1) & 1)) {
-                tc::tc_fence_after();
-                finish(chunks - 1);
-            }
-            if (leaves && ok) {
-                const float f = r.against && seg.len > 0 ? s.tab[1] : 1.f;  // to the gradient of the state before the first token
-                float *to = r.fin + size_t(seg.seq) * per_head + size_t(it.h) * kState;
+                // a whole chunk's rows go through the place of its C, and out by one copy
+                const bool staged = len == kC && !r.partial;
+                uint8_t *stage = s.c[c & 1] + half * kHalf;
+#pragma unroll 1
+                for (int x = 0; x < 64; x += 16) {
+                    float v[16];
+                    tc::tmem_ld16(acc + x, v);
+                    tc::tmem_ld_wait();
+                    if (x == 48) {
+                        tc::tc_fence_before();
+                        tc::warp_arrive(&s.out_free);
+                    }
+                    uint32_t w[16];
 #pragma unroll
-                for (int k = 0; k < 64; ++k) {
-                    const float x = f == 1.f ? st[k] : f * st[k];
-                    if (r.swapped) to[row * kHeadDim + b0 + k] = x;
-                    else to[(b0 + k) * kHeadDim + row] = x;
+                    for (int k = 0; k < 8; ++k) {
+                        const float2 y = __fmul2_rn(f2, make_float2(v[2 * k], v[2 * k + 1]));
+                        if (r.partial) w[2 * k] = __float_as_uint(y.x), w[2 * k + 1] = __float_as_uint(y.y);
+                        else w[k] = pack2(y.x, y.y);
+                    }
+                    if (staged) {
+                        *reinterpret_cast<uint4 *>(at(stage, row, x / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(at(stage, row, x / 8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else if (row < len) {
+                        if (r.partial) {
+                            float *to = static_cast<float *>(r.out) + at_out + x;
+                            store_sector(to, w, r.sectors);
+                            store_sector(to + 8, w + 8, r.sectors);
+                        } else {
+                            store_sector(static_cast<__nv_bfloat16 *>(r.out) + at_out + x, w, r.sectors);
+                        }
+                    }
                 }
+                if (staged) tc::fence_proxy_async_smem();
+                tc::warp_arrive(&s.staged);
             }
         }
-        if (row == 0) tc::bulk_wait_group_all();
+        if (leaves && ok) {
+            const float f = r.against && seg.len > 0 ? power_of(1) : 1.f;  // to the gradient of the state before the first token
+            float *to = r.fin + size_t(seg.seq) * per_head + size_t(it.h) * kState;
+            if (f != 1.f) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) st[k] = __fmul2_rn(make_float2(f, f), st[k]);
+            }
+            if (r.swapped) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    to[(c0 + 2 * k) * kHeadDim + row] = st[k].x;
+                    to[(c0 + 2 * k + 1) * kHeadDim + row] = st[k].y;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; k += 2)
+                    *reinterpret_cast<float4 *>(to + row * kHeadDim + c0 + 2 * k) =
+                        make_float4(st[k].x, st[k].y, st[k + 1].x, st[k + 1].y);
+            }
+        }
     }
     __syncwarp();
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 13) tc::tmem_dealloc(tmem, 512);
+    if (tid == 0 && s.dead) record_status(p.status, GDN_ETIMEOUT);
+    if (warp == 21) tc::tmem_dealloc(kTmem, 512);
 }
 
 bool tile_map(CUtensorMap *map, const void *base, int heads, int tokens) {
@@ -643,7 +790,9 @@ bool tile_map(CUtensorMap *map, const void *base, int heads, int tokens) {
 
 }  // namespace
 
-cudaError_t launch_tc(const Args &a, cudaStream_t s) {
+cudaError_t launch_tc(const Args &args, cudaStream_t s) {
+    Args a = args;
+    for (int i = 0; i < a.roles; ++i) a.role[i].sectors = (reinterpret_cast<uintptr_t>(a.role[i].out) & 31) == 0;
     Maps m;
     memset(&m, 0, sizeof m);
     if (a.total_tokens > 0)
@@ -654,7 +803,7 @@ cudaError_t launch_tc(const Args &a, cudaStream_t s) {
                 (!r.partial && !tile_map(&m.o[i], r.out, a.hv, a.total_tokens)))
                 return cudaErrorInvalidValue;
         }
-    constexpr int kSumBytes = sizeof(SumShared) + 1024, kWalkBytes = sizeof(WalkShared) + 1024;
+    constexpr int kSumBytes = sizeof(SumShared), kWalkBytes = sizeof(WalkShared);
     static_assert(kSumBytes <= 232448 && kWalkBytes <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(k_la_sum_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kSumBytes);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_la_walk_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kWalkBytes);
