@@ -55,26 +55,31 @@ __device__ __forceinline__ bool item_of(const Args &p, uint32_t smem, Item &it) 
 }
 
 // Bounded waits: one that runs out marks the CTA, and every other wait of it
-// ends then. They poll (a suspended thread goes on some 500 cycles later: the
-// walk takes 7% longer). The limit is one of cycles, of which there is more
-// than one a nanosecond: little code, since the roles' loops have to stay in the
-// instruction cache together.
+// ends then. The limit is one of cycles, of which there is more than one a
+// nanosecond: little code, since the roles' loops have to stay in the
+// instruction cache together (with 77 KB of code the walk took a fifth longer).
+// The warp that issues the products polls; the many that wait for it suspend,
+// which leaves the issue slots to those at work (5% of the walk).
 struct Waiter {
     volatile int *dead;
     long long limit;
-    // of one thread
+    template <bool kPoll>
     __device__ __forceinline__ bool one(uint64_t *bar, uint32_t parity) const {
         const long long t0 = clock64();
-        while (!tc::mbar_test_wait(bar, parity))
+        while (!(kPoll || limit < (long long)tc::kShortLimitNs ? tc::mbar_test_wait(bar, parity) : tc::mbar_try_wait(bar, parity)))
             if (*dead || clock64() - t0 > limit) {
                 *dead = 1;
                 return false;
             }
         return true;
     }
+    __device__ __forceinline__ bool one(uint64_t *bar, uint32_t parity) const { return one<false>(bar, parity); }
     // of a whole warp, which goes on as one
     __device__ __forceinline__ bool warp(uint64_t *bar, uint32_t parity) const {
-        return __all_sync(0xffffffffu, one(bar, parity));
+        return __all_sync(0xffffffffu, one<false>(bar, parity));
+    }
+    __device__ __forceinline__ bool poll(uint64_t *bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, one<true>(bar, parity));
     }
 };
 
@@ -277,12 +282,12 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
         bool ok = true;
         for (int n = 0; n < chunks && ok; ++n) {
             const int u = n % 3;
-            ok = wait.warp(&s.c_full[u], (n / 3) & 1) && wait.warp(&s.c_clean[u], (n / 3) & 1);
+            ok = wait.poll(&s.c_full[u], (n / 3) & 1) && wait.poll(&s.c_clean[u], (n / 3) & 1);
             const uint64_t c = tiles + u * (kTile >> 4);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int batch = 2 * n + hf;
-                if (!(ok = ok && wait.warp(&s.part_full[batch % 3], (batch / 3) & 1))) break;
+                if (!(ok = ok && wait.poll(&s.part_full[batch % 3], (batch / 3) & 1))) break;
                 tc::tc_fence_after();
                 if (leader) {
                     mma_parts<4>(kTmem, part_of(batch), 32, c, 64 * hf, batch == 0);
@@ -374,7 +379,7 @@ struct WalkShared {
     uint8_t a[2][kTile], b[2][kTile], c[2][kTile], state[kTile];
     float between[2 * kC];  // [128 + d]: lambda^|d|, d from -128 to 127
     uint32_t w[2][3][kC / 2];  // decays of B's rows, of a whole chunk and of the sequence's last one
-    uint64_t ab_full[2], c_full[2], a_free[2], b_free[2], c_clean[2], c_free[2], part_full[4], part_free[4], p_full,
+    uint64_t ab_full[2], c_full[2], a_free[2], b_free[2], c_clean, c_free[2], part_full[4], part_free[4], p_full,
         scores_full, sum_full, sum_free, state_full, state_free, out_full, out_free, staged, drain;
     uint32_t tmem;
     int dead;
@@ -431,7 +436,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
             tc::mbar_init(&s.c_full[i], 1);
             tc::mbar_init(&s.a_free[i], 1);
             tc::mbar_init(&s.b_free[i], 9);
-            tc::mbar_init(&s.c_clean[i], 8);
             tc::mbar_init(&s.c_free[i], 1);
         }
         for (int i = 0; i < 4; ++i) {
@@ -447,6 +451,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
         tc::mbar_init(&s.out_full, 1);
         tc::mbar_init(&s.out_free, 8);
         tc::mbar_init(&s.staged, 8);
+        tc::mbar_init(&s.c_clean, 8);
         tc::mbar_init(&s.drain, 1);
         s.dead = 0;
         tc::fence_mbar_init();
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
             const uint64_t a0 = k_major(s.a[0]), b0 = k_major(s.b[0]), c0 = mn_major(s.c[0]), st = mn_major(s.state);
             auto tile = [](int n) { return uint64_t(n & 1) * (kTile >> 4); };
             auto scores = [&](int n) {
-                if (!wait.warp(&s.ab_full[n & 1], (n >> 1) & 1)) return false;
+                if (!wait.poll(&s.ab_full[n & 1], (n >> 1) & 1)) return false;
                 tc::tc_fence_after();
                 const uint64_t a = a0 + tile(n), b = b0 + tile(n);
                 if (leader) {
@@ -530,14 +535,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
                 const uint32_t ph = n & 1, before = (n - 1) & 1;
                 const uint64_t c = c0 + tile(n), a = a0 + tile(n);
                 const bool more = sums(n);
-                if (!(ok = scores(n) && wait.warp(&s.c_full[n & 1], (n >> 1) & 1) &&
-                           (chunk_len(n) == kC || wait.warp(&s.c_clean[n & 1], (n >> 1) & 1))))
+                if (!(ok = scores(n) && wait.poll(&s.c_full[n & 1], (n >> 1) & 1) &&
+                           (chunk_len(n) == kC || wait.poll(&s.c_clean, 0))))
                     break;
                 if (more) {
-                    if (n > 0 && !(ok = wait.warp(&s.sum_free, before))) break;
+                    if (n > 0 && !(ok = wait.poll(&s.sum_free, before))) break;
 #pragma unroll
                     for (int t = 0; t < 8; ++t) {
-                        if (!(ok = ok && wait.warp(&s.part_full[t & 3], t >> 2))) break;
+                        if (!(ok = ok && wait.poll(&s.part_full[t & 3], t >> 2))) break;
                         tc::tc_fence_after();
                         if (leader) {
                             mma_parts<1>(kTmem + kColSum, kTmem + kColPart + (t & 3) * 32, 8, c, 16 * t, t == 0);
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
                     }
                     if (!ok) break;
                 }
-                if (!(ok = wait.warp(&s.state_full, ph) && (n == 0 || wait.warp(&s.out_free, before)))) break;
+                if (!(ok = wait.poll(&s.state_full, ph) && (n == 0 || wait.poll(&s.out_free, before)))) break;
                 tc::tc_fence_after();
                 if (leader) {
 #pragma unroll
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
                     tc::mma_commit(&s.state_free);
                     tc::mma_commit(&s.a_free[n & 1]);
                 }
-                if (!(ok = wait.warp(&s.scores_full, ph))) break;
+                if (!(ok = wait.poll(&s.scores_full, ph))) break;
                 tc::tc_fence_after();
                 if (leader) {
 #pragma unroll
@@ -638,8 +643,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
             if (len < kC) {
                 if (!(ok = wait.warp(&s.c_full[n & 1], (n >> 1) & 1))) break;
                 zero_behind(s.c[n & 1], len, tid - 128);
+                tc::warp_arrive(&s.c_clean);  // (one chunk of a segment at most is not whole)
             }
-            tc::warp_arrive(&s.c_clean[n & 1]);
             if (!sums(n)) break;  // the last chunk
             if (!(ok = wait.warp(&s.ab_full[n & 1], (n >> 1) & 1))) break;
             const uint32_t(*w)[kC / 2] = s.w[len < kC];

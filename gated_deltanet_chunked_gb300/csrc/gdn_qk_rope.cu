@@ -75,6 +75,16 @@ struct RopeShared {
     int pos_bad;
 };
 
+// VE consecutive f32 of shared memory, 16 bytes a load
+template <int VE>
+__device__ __forceinline__ void load_f32(const float *from, float2 *v) {
+#pragma unroll
+    for (int i = 0; i < VE / 4; ++i) {
+        const float4 x = reinterpret_cast<const float4 *>(from)[i];
+        v[2 * i] = make_float2(x.x, x.y), v[2 * i + 1] = make_float2(x.z, x.w);
+    }
+}
+
 // The partner's channels of a lane's VE channels in a row of f32 values, for
 // pairs that do not lie in whole lanes: through shared memory.
 template <int VE>
@@ -104,11 +114,21 @@ __device__ __forceinline__ void rotate(const float2 *turn, int ch, int pairs, fl
             if (kBack) t.y = -t.y;
             v[i] = make_float2(v[i].x * t.x - v[i].y * t.y, v[i].x * t.y + v[i].y * t.x);
         }
+    } else if constexpr (P == kLanes) {
+        const bool first = ch < pairs;
+        float2 t[VE];  // cos, sin
+        load_f32<2 * VE>(reinterpret_cast<const float *>(turn + (first ? ch : ch - pairs)), t);
+        const float2 sign = both(first != kBack ? -1.f : 1.f);
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+            const float2 co = make_float2(t[2 * i].x, t[2 * i + 1].x), si = make_float2(t[2 * i].y, t[2 * i + 1].y);
+            v[i] = fma2(v[i], co, mul2(mul2(o[i], sign), si));
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
             const int c = ch + i;
-            if (P == kAnywhere && c >= 2 * pairs) break;
+            if (c >= 2 * pairs) break;
             const bool first = c < pairs;
             const float2 t = turn[first ? c : c - pairs];
             const float sn = first != kBack ? -t.y : t.y;
@@ -122,7 +142,7 @@ __device__ __forceinline__ void rotate(const float2 *turn, int ch, int pairs, fl
 template <typename T, int P, bool kBwd>
 __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid_constant__ RopeArgs a) {
     using L = Layout<T>;
-    constexpr int VE = L::kVe;
+    constexpr int VE = L::kVe, R = kBwd ? 2 : 4;
     using Row = vec::Pack<T, VE>;
     __shared__ __align__(16) RopeShared s;
     __shared__ __align__(16) float swap[P == kAnywhere ? L::kRows : 1][kHeadDim];
@@ -156,14 +176,14 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
     for (long long t0 = (long long)blockIdx.x * a.step; t0 < a.tokens; t0 += (long long)gridDim.x * a.step, which ^= 1) {
         const int step = int(min((long long)a.step, a.tokens - t0)), rows = step * heads;
         float2 *turn = s.turn[which];  // two in turn, so that one barrier a step is enough
-        // two rows a lane group at a time; the first loads are under way while the angles are taken
-        for (int r0 = 0; r0 < rows; r0 += 2 * L::kRows) {
-            Row x[2], d[2];
-            bool has[2], is_k[2];
-            int token[2];
-            long long at[2];
+        // R rows a lane group at a time; the first loads are under way while the angles are taken
+        for (int r0 = 0; r0 < rows; r0 += R * L::kRows) {
+            Row x[R], d[kBwd ? R : 1];
+            bool has[R], is_k[R];
+            int token[R];
+            long long at[R];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < R; ++k) {
                 const int row = r0 + k * L::kRows + group;
                 has[k] = row < rows;
                 token[k] = has[k] ? row / heads : 0;
@@ -187,9 +207,10 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
                 __syncthreads();
             }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < R; ++k) {
                 const int w = is_k[k];
-                const float *weight = &s.weight[w][ch];
+                float2 wt[VE / 2];
+                load_f32<VE>(&s.weight[w][ch], wt);
                 const float2 *tt = turn + token[k] * kMaxPairs;
                 float2 v[VE / 2], o[VE / 2];
                 float2 ss = both(0.f);
@@ -203,7 +224,8 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
                     if constexpr (P == kLanes) {
                         // the partner lane's channels come as they lie in memory, and take their weights here
                         const int off = a.pairs / VE, to = lane < off ? lane + off : lane < 2 * off ? lane - off : lane;
-                        const float *wp = &s.weight[w][to * VE];
+                        float2 wo[VE / 2];
+                        load_f32<VE>(&s.weight[w][to * VE], wo);
                         Row p;
                         constexpr int kWords = sizeof(Row) / 4;
                         const uint32_t *from = reinterpret_cast<const uint32_t *>(&x[k]);
@@ -212,11 +234,11 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
                         for (int i = 0; i < kWords; ++i) into[i] = __shfl_sync(0xffffffffu, from[i], to, L::kLanesOfRow);
 #pragma unroll
                         for (int i = 0; i < VE / 2; ++i)
-                            o[i] = mul2(mul2(p.f2(i), both(r)), *reinterpret_cast<const float2 *>(wp + 2 * i));
+                            o[i] = mul2(mul2(p.f2(i), both(r)), wo[i]);
                     }
 #pragma unroll
                     for (int i = 0; i < VE / 2; ++i)
-                        v[i] = mul2(mul2(v[i], both(r)), *reinterpret_cast<const float2 *>(weight + 2 * i));
+                        v[i] = mul2(mul2(v[i], both(r)), wt[i]);
                     if constexpr (P == kAnywhere) partners<VE>(swap[group], ch, a.pairs, v, o);
                     rotate<VE, P, false>(tt, ch, a.pairs, v, o);
 #pragma unroll
@@ -241,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
                     float2 u[VE / 2], ux = both(0.f);
 #pragma unroll
                     for (int i = 0; i < VE / 2; ++i) {
-                        u[i] = mul2(n[i], *reinterpret_cast<const float2 *>(weight + 2 * i));
+                        u[i] = mul2(n[i], wt[i]);
                         ux = fma2(u[i], v[i], ux);
                     }
                     const float2 sums = vec::group_sum2<L::kLanesOfRow>(vec::sum2(ss), vec::sum2(ux));
@@ -279,16 +301,19 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
     }
 }
 
+constexpr int kSms = 152;
+
 int ctas_of(long long tokens, int step, bool bwd) {
-    const long long steps = (tokens + step - 1) / step, most = 152 * (bwd ? 3 : 4);
+    const long long steps = (tokens + step - 1) / step, most = kSms * (bwd ? 3 : 4);
     return int(steps < most ? steps : most);
 }
 
-// tokens of a CTA's step: two rows for each of its lane groups
-int step_of(int heads, int io_dtype) {
-    const int rows = io_dtype == GDN_DT_BF16 ? 2 * Layout<__nv_bfloat16>::kRows : 2 * Layout<float>::kRows;
-    const int n = rows / heads;
-    return n < 1 ? 1 : n > kMaxTokens ? kMaxTokens : n;
+// Tokens of a CTA's step: eight rows for each of its lane groups (angles and a
+// barrier come once a step), fewer where that would leave SMs without work.
+int step_of(long long tokens, int heads, int io_dtype) {
+    const int rows = 8 * (io_dtype == GDN_DT_BF16 ? Layout<__nv_bfloat16>::kRows : Layout<float>::kRows);
+    const long long most = tokens / (kSms * 4), n = rows / heads < most ? rows / heads : most;
+    return int(n < 1 ? 1 : n > kMaxTokens ? kMaxTokens : n);
 }
 
 template <typename T, bool kBwd>
@@ -301,7 +326,7 @@ void go(const RopeArgs &a, int interleaved, int ctas, cudaStream_t s) {
 }  // namespace
 
 size_t qk_rope_bwd_workspace(long long tokens, int heads, int io_dtype) {
-    return size_t(ctas_of(tokens, step_of(heads, io_dtype), true)) * 2 * kHeadDim * sizeof(float);
+    return size_t(ctas_of(tokens, step_of(tokens, heads, io_dtype), true)) * 2 * kHeadDim * sizeof(float);
 }
 
 cudaError_t launch_qk_rope(const gdn_qk_rope &r, const void *const dy[2], const long long dy_stride[2], void *const y[2],
@@ -314,7 +339,7 @@ cudaError_t launch_qk_rope(const gdn_qk_rope &r, const void *const dy[2], const 
     const bool bwd = dy != nullptr;
     float *parts = static_cast<float *>(workspace);
     a.heads[0] = r.hq, a.heads[1] = r.hk;
-    a.step = step_of(heads, r.io_dtype);
+    a.step = step_of(r.tokens, heads, r.io_dtype);
     const int ctas = ctas_of(r.tokens, a.step, bwd);
     for (int w = 0; w < 2; ++w) {
         if (bwd) a.dy[w] = dy[w], a.ds[w] = dy_stride[w];
