@@ -11,9 +11,8 @@
 // cosines in shared memory, once for all heads of a token.
 //
 // Angles. A position has up to 31 bits and t is wanted to 2^-24 of a turn:
-// frequency / 2 pi is held in three f32 (from 64 bits), the position in two
-// whole f32, and the parts' products, exact by FMA, lose their whole turns
-// before they are added.
+// frequency / 2 pi is held in three f32, the position in two whole f32, and the
+// parts' products, exact by FMA, lose their whole turns before they are added.
 #include "gdn_common.cuh"
 #include "gdn_vec.cuh"
 
@@ -26,7 +25,7 @@ using vec::mul2;
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = kHeadDim / 2;
-constexpr int kMaxTokens = 32;  // of a CTA's step
+constexpr int kMaxTokens = 16;  // of a CTA's step
 
 struct RopeArgs {
     const void *x[2];         // q, k: [tokens, heads, 128], tokens `stride` elements apart
@@ -69,18 +68,36 @@ struct Layout {
     static constexpr int kVe = 16 / sizeof(T), kLanesOfRow = kHeadDim / kVe, kRows = kThreads / kLanesOfRow;
 };
 
+// frequency / 2 pi in three parts: 1 / 2 pi in three, their products with the
+// frequency exact by FMA, the middle ones added exactly
+__device__ __forceinline__ float3 turns_of(float f) {
+    const float h = 0.15915493667125702f, l = 6.4206382432985265e-09f, l2 = 7.342738699078887e-17f;
+    const float a = f * h, e = fmaf(f, h, -a), g = f * l, b = e + g, v = b - e;
+    return make_float3(a, b, (e - (b - v)) + (g - v) + fmaf(f, l, -g) + f * l2);
+}
+
 struct RopeShared {
-    float2 turn[2][kMaxTokens * kMaxPairs];
+    float turn[2][3][kMaxTokens * kMaxPairs];  // cos, sin, -sin
     float weight[2][kHeadDim];
-    int pos_bad;
 };
 
-// VE consecutive f32 of shared memory, 16 bytes a load
+// Where element i of a row of values lies that lanes read 4 VE bytes each of
+// (with `lanes`, else in order): a lane's first 16 bytes beside the other lanes'
+// first ones, so that a load meets every bank once.
 template <int VE>
-__device__ __forceinline__ void load_f32(const float *from, float2 *v) {
+__device__ __forceinline__ int place(int i, bool lanes) {
+    return lanes && VE == 8 ? (i & 4) * (kMaxPairs / 8) + (i >> 3) * 4 + (i & 3) : i;
+}
+template <int VE>
+__device__ __forceinline__ int weight_place(int i) {
+    return VE == 8 ? (i & 4) * (kHeadDim / 8) + (i >> 3) * 4 + (i & 3) : i;
+}
+// a lane's VE of them (those of lane `lane`, `rest` elements from the first 16 bytes to the next)
+template <int VE>
+__device__ __forceinline__ void load_lane(const float *row, int lane, int rest, float2 *v) {
 #pragma unroll
     for (int i = 0; i < VE / 4; ++i) {
-        const float4 x = reinterpret_cast<const float4 *>(from)[i];
+        const float4 x = *reinterpret_cast<const float4 *>(row + i * rest + lane * 4);
         v[2 * i] = make_float2(x.x, x.y), v[2 * i + 1] = make_float2(x.z, x.w);
     }
 }
@@ -101,40 +118,39 @@ __device__ __forceinline__ void partners(float *row, int ch, int pairs, const fl
     }
 }
 
-// Turns a lane's VE channels v (partners' o) by `turn` (kBack: back); channels
-// behind the rotated ones stay.
+// Turns a lane's VE channels v (partners' o) by the token's cos, sin and -sin
+// (kBack: back); channels behind the rotated ones stay.
 template <int VE, int P, bool kBack>
-__device__ __forceinline__ void rotate(const float2 *turn, int ch, int pairs, float2 *v, const float2 *o) {
+__device__ __forceinline__ void rotate(const float *co, const float *si, const float *minus, int lane, int pairs, float2 *v,
+                                       const float2 *o) {
+    const int ch = lane * VE;
     if (ch >= 2 * pairs) return;
     if constexpr (P == kNeighbours) {
 #pragma unroll
         for (int i = 0; i < VE / 2; ++i) {
-            if (ch / 2 + i >= pairs) break;
-            float2 t = turn[ch / 2 + i];
-            if (kBack) t.y = -t.y;
-            v[i] = make_float2(v[i].x * t.x - v[i].y * t.y, v[i].x * t.y + v[i].y * t.x);
+            const int p = ch / 2 + i;
+            if (p >= pairs) break;
+            const float c = co[p], s = kBack ? minus[p] : si[p];
+            v[i] = make_float2(v[i].x * c - v[i].y * s, v[i].x * s + v[i].y * c);
         }
     } else if constexpr (P == kLanes) {
         const bool first = ch < pairs;
-        float2 t[VE];  // cos, sin
-        load_f32<2 * VE>(reinterpret_cast<const float *>(turn + (first ? ch : ch - pairs)), t);
-        const float2 sign = both(first != kBack ? -1.f : 1.f);
+        const int at = first ? lane : lane - pairs / VE;
+        float2 c[VE / 2], s[VE / 2];
+        load_lane<VE>(co, at, kMaxPairs / 2, c);
+        load_lane<VE>(first != kBack ? minus : si, at, kMaxPairs / 2, s);
 #pragma unroll
-        for (int i = 0; i < VE / 2; ++i) {
-            const float2 co = make_float2(t[2 * i].x, t[2 * i + 1].x), si = make_float2(t[2 * i].y, t[2 * i + 1].y);
-            v[i] = fma2(v[i], co, mul2(mul2(o[i], sign), si));
-        }
+        for (int i = 0; i < VE / 2; ++i) v[i] = fma2(v[i], c[i], mul2(o[i], s[i]));
     } else {
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
             const int c = ch + i;
             if (c >= 2 * pairs) break;
             const bool first = c < pairs;
-            const float2 t = turn[first ? c : c - pairs];
-            const float sn = first != kBack ? -t.y : t.y;
+            const int p = first ? c : c - pairs;
             float &a = i & 1 ? v[i / 2].y : v[i / 2].x;
             const float b = i & 1 ? o[i / 2].y : o[i / 2].x;
-            a = fmaf(a, t.x, b * sn);
+            a = fmaf(a, co[p], b * (first != kBack ? minus[p] : si[p]));
         }
     }
 }
@@ -142,15 +158,16 @@ __device__ __forceinline__ void rotate(const float2 *turn, int ch, int pairs, fl
 template <typename T, int P, bool kBwd>
 __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid_constant__ RopeArgs a) {
     using L = Layout<T>;
-    constexpr int VE = L::kVe, R = kBwd ? 2 : 4;
+    // rows a lane group has under way: 16 bytes a lane of each
+    constexpr int VE = L::kVe, R = kBwd ? 2 : 4, kWords = 4;
     using Row = vec::Pack<T, VE>;
     __shared__ __align__(16) RopeShared s;
     __shared__ __align__(16) float swap[P == kAnywhere ? L::kRows : 1][kHeadDim];
     const int tid = threadIdx.x, lane = tid % L::kLanesOfRow, group = tid / L::kLanesOfRow, ch = lane * VE;
     const int heads = a.heads[0] + a.heads[1];
-    if (tid < kHeadDim) {
-        s.weight[0][tid] = a.weight[0] ? a.weight[0][tid] : 1.f;
-        s.weight[1][tid] = a.weight[1] ? a.weight[1][tid] : 1.f;
+    for (int i = tid; i < 2 * kHeadDim; i += kThreads) {
+        const int w = i / kHeadDim, c = i % kHeadDim;
+        s.weight[w][weight_place<VE>(c)] = a.weight[w] ? a.weight[w][c] : 1.f;
     }
     // this thread's pair of the angles (kMaxPairs divides the CTA's threads)
     const int pair = tid % kMaxPairs;
@@ -158,10 +175,7 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
     float3 f = make_float3(0.f, 0.f, 0.f);
     if (pair < a.pairs) {
         if (a.pair_axis) axis = a.pair_axis[pair];
-        const double turns = double(a.inv_freq[pair]) * 0.15915494309189533577;
-        f.x = float(turns);
-        f.y = float(turns - double(f.x));
-        f.z = float(turns - double(f.x) - double(f.y));
+        f = turns_of(a.inv_freq[pair]);
     }
     if (__syncthreads_or(axis < 0 || axis >= a.axes)) {
         if (tid == 0) record_status(a.status, GDN_EDEVICE_INPUT);
@@ -171,76 +185,80 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
         return;
     }
     const int *pos = a.positions + size_t(axis) * a.tokens;
+    const int pair_at = place<VE>(pair, P == kLanes);
+    // from one of a lane group's rows to its next: tokens and heads
+    const int next_t = L::kRows / heads, next_h = L::kRows % heads;
+    // partner's lane, for pairs in whole lanes
+    const int off = a.pairs / VE, other = lane < off ? lane + off : lane < 2 * off ? lane - off : lane;
     float2 dw[2][VE / 2] = {};
     int which = 0;
     for (long long t0 = (long long)blockIdx.x * a.step; t0 < a.tokens; t0 += (long long)gridDim.x * a.step, which ^= 1) {
-        const int step = int(min((long long)a.step, a.tokens - t0)), rows = step * heads;
-        float2 *turn = s.turn[which];  // two in turn, so that one barrier a step is enough
-        // R rows a lane group at a time; the first loads are under way while the angles are taken
-        for (int r0 = 0; r0 < rows; r0 += R * L::kRows) {
+        const int step = int(min((long long)a.step, a.tokens - t0));
+        float(*turn)[kMaxTokens * kMaxPairs] = s.turn[which];  // two in turn, so that one barrier a step is enough
+        int t = group / heads, h = group % heads;
+        bool angles = false;
+        // R rows at a time; the first loads are under way while the angles are taken
+        for (int r0 = 0; r0 < step * heads; r0 += R * L::kRows) {
             Row x[R], d[kBwd ? R : 1];
-            bool has[R], is_k[R];
-            int token[R];
+            int token[R], w[R];
             long long at[R];
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                const int row = r0 + k * L::kRows + group;
-                has[k] = row < rows;
-                token[k] = has[k] ? row / heads : 0;
-                const int h = has[k] ? row % heads : 0;
-                is_k[k] = h >= a.heads[0];
-                const int w = is_k[k];
-                const long long t = t0 + token[k];
-                const int hw = is_k[k] ? h - a.heads[0] : h;
-                at[k] = t * a.ys[w] + hw * kHeadDim + ch;
+                token[k] = t;
+                w[k] = h >= a.heads[0];
+                const int head = (w[k] ? h - a.heads[0] : h) * kHeadDim + ch;
+                at[k] = (t0 + t) * a.ys[w[k]] + head;
                 x[k].zero();
                 if (kBwd) d[k].zero();
-                if (has[k]) {
-                    x[k].load(static_cast<const T *>(a.x[w]) + t * a.xs[w] + hw * kHeadDim + ch);
-                    if (kBwd) d[k].load(static_cast<const T *>(a.dy[w]) + t * a.ds[w] + hw * kHeadDim + ch);
+                if (t < step) {
+                    x[k].load(static_cast<const T *>(a.x[w[k]]) + (t0 + t) * a.xs[w[k]] + head);
+                    if (kBwd) d[k].load(static_cast<const T *>(a.dy[w[k]]) + (t0 + t) * a.ds[w[k]] + head);
                 }
+                t += next_t, h += next_h;
+                if (h >= heads) h -= heads, ++t;
             }
-            if (r0 == 0) {
+            if (!angles) {
                 if (pair < a.pairs)
-                    for (int k = tid / kMaxPairs; k < step; k += kThreads / kMaxPairs)
-                        turn[k * kMaxPairs + pair] = angle(pos[t0 + k], f);
+                    for (int k = tid / kMaxPairs; k < step; k += kThreads / kMaxPairs) {
+                        const float2 v = angle(pos[t0 + k], f);
+                        turn[0][k * kMaxPairs + pair_at] = v.x;
+                        turn[1][k * kMaxPairs + pair_at] = v.y;
+                        turn[2][k * kMaxPairs + pair_at] = -v.y;
+                    }
                 __syncthreads();
+                angles = true;
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                const int w = is_k[k];
-                float2 wt[VE / 2];
-                load_f32<VE>(&s.weight[w][ch], wt);
-                const float2 *tt = turn + token[k] * kMaxPairs;
-                float2 v[VE / 2], o[VE / 2];
-                float2 ss = both(0.f);
+                const bool has = token[k] < step;
+                const float *weight = s.weight[w[k]];
+                const int tt = has ? token[k] * kMaxPairs : 0;
+                const float *co = turn[0] + tt, *si = turn[1] + tt, *minus = turn[2] + tt;
+                float2 v[VE / 2], o[VE / 2], wt[VE / 2], ss = both(0.f);
+                load_lane<VE>(weight, lane, kHeadDim / 2, wt);
 #pragma unroll
                 for (int i = 0; i < VE / 2; ++i) {
                     v[i] = x[k].f2(i);
                     ss = fma2(v[i], v[i], ss);
                 }
                 if constexpr (!kBwd) {
-                    const float r = rsqrtf(vec::group_sum<L::kLanesOfRow>(vec::sum2(ss)) * (1.f / kHeadDim) + a.eps);
+                    const float2 r = both(rsqrtf(vec::group_sum<L::kLanesOfRow>(vec::sum2(ss)) * (1.f / kHeadDim) + a.eps));
                     if constexpr (P == kLanes) {
                         // the partner lane's channels come as they lie in memory, and take their weights here
-                        const int off = a.pairs / VE, to = lane < off ? lane + off : lane < 2 * off ? lane - off : lane;
-                        float2 wo[VE / 2];
-                        load_f32<VE>(&s.weight[w][to * VE], wo);
                         Row p;
-                        constexpr int kWords = sizeof(Row) / 4;
+                        float2 wo[VE / 2];
+                        load_lane<VE>(weight, other, kHeadDim / 2, wo);
                         const uint32_t *from = reinterpret_cast<const uint32_t *>(&x[k]);
                         uint32_t *into = reinterpret_cast<uint32_t *>(&p);
 #pragma unroll
-                        for (int i = 0; i < kWords; ++i) into[i] = __shfl_sync(0xffffffffu, from[i], to, L::kLanesOfRow);
+                        for (int i = 0; i < kWords; ++i) into[i] = __shfl_sync(0xffffffffu, from[i], other, L::kLanesOfRow);
 #pragma unroll
-                        for (int i = 0; i < VE / 2; ++i)
-                            o[i] = mul2(mul2(p.f2(i), both(r)), wo[i]);
+                        for (int i = 0; i < VE / 2; ++i) o[i] = mul2(mul2(p.f2(i), r), wo[i]);
                     }
 #pragma unroll
-                    for (int i = 0; i < VE / 2; ++i)
-                        v[i] = mul2(mul2(v[i], both(r)), wt[i]);
+                    for (int i = 0; i < VE / 2; ++i) v[i] = mul2(mul2(v[i], r), wt[i]);
                     if constexpr (P == kAnywhere) partners<VE>(swap[group], ch, a.pairs, v, o);
-                    rotate<VE, P, false>(tt, ch, a.pairs, v, o);
+                    rotate<VE, P, false>(co, si, minus, lane, a.pairs, v, o);
 #pragma unroll
                     for (int i = 0; i < VE / 2; ++i) x[k].set2(i, v[i]);
                 } else {
@@ -248,18 +266,16 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
 #pragma unroll
                     for (int i = 0; i < VE / 2; ++i) n[i] = d[k].f2(i);
                     if constexpr (P == kLanes) {
-                        const int off = a.pairs / VE, to = lane < off ? lane + off : lane < 2 * off ? lane - off : lane;
                         Row p;
-                        constexpr int kWords = sizeof(Row) / 4;
                         const uint32_t *from = reinterpret_cast<const uint32_t *>(&d[k]);
                         uint32_t *into = reinterpret_cast<uint32_t *>(&p);
 #pragma unroll
-                        for (int i = 0; i < kWords; ++i) into[i] = __shfl_sync(0xffffffffu, from[i], to, L::kLanesOfRow);
+                        for (int i = 0; i < kWords; ++i) into[i] = __shfl_sync(0xffffffffu, from[i], other, L::kLanesOfRow);
 #pragma unroll
                         for (int i = 0; i < VE / 2; ++i) o[i] = p.f2(i);
                     }
                     if constexpr (P == kAnywhere) partners<VE>(swap[group], ch, a.pairs, n, o);
-                    rotate<VE, P, true>(tt, ch, a.pairs, n, o);
+                    rotate<VE, P, true>(co, si, minus, lane, a.pairs, n, o);
                     float2 u[VE / 2], ux = both(0.f);
 #pragma unroll
                     for (int i = 0; i < VE / 2; ++i) {
@@ -273,13 +289,13 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
                     for (int i = 0; i < VE / 2; ++i) {
                         const float2 xhat = mul2(v[i], both(r));
                         x[k].set2(i, mul2(both(r), fma2(xhat, both(-m), u[i])));
-                        if (has[k]) {
-                            if (w) dw[1][i] = fma2(n[i], xhat, dw[1][i]);
+                        if (has) {
+                            if (w[k]) dw[1][i] = fma2(n[i], xhat, dw[1][i]);
                             else dw[0][i] = fma2(n[i], xhat, dw[0][i]);
                         }
                     }
                 }
-                if (has[k]) x[k].store(static_cast<T *>(a.y[w]) + at[k]);
+                if (has) x[k].store(static_cast<T *>(a.y[w[k]]) + at[k]);
             }
         }
     }
