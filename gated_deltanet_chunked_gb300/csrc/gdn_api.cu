@@ -767,10 +767,8 @@ int gdn_linear_attention_bwd(const gdn_problem *p, const void *dout, const void 
     if (!(a.status = status_ptr())) return GDN_ECUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_linattn(p, a, s);
-    if (e == cudaSuccess && g > 1) {
-        e = la::launch_group_sum(parts[0], dq, p->total_tokens, p->hq, g, p->io_dtype, s);
-        if (e == cudaSuccess) e = la::launch_group_sum(parts[1], dk, p->total_tokens, p->hq, g, p->io_dtype, s);
-    }
+    if (e == cudaSuccess && g > 1)
+        e = la::launch_group_sums(parts[0], dq, parts[1], dk, p->total_tokens, p->hq, g, p->io_dtype, s);
     return cuda_status(e);
 }
 
@@ -839,21 +837,21 @@ int check_qk_rope(const gdn_qk_rope *r) {
 }
 
 // the inputs that both passes read besides q and k
-bool rope_inputs_ok(const gdn_qk_rope *r) {
-    if (!aligned4(r->q_weight) || !aligned4(r->k_weight) || !aligned4(r->inv_freq) || !aligned4(r->positions) ||
-        !aligned4(r->pair_axis))
+bool rope_inputs_ok(const gdn_qk_rope *r, const QkRopeTensors &t) {
+    if (!aligned4(t.weight[0]) || !aligned4(t.weight[1]) || !aligned4(t.inv_freq) || !aligned4(t.positions) ||
+        !aligned4(t.pair_axis))
         return false;
-    return r->tokens == 0 || r->rotary == 0 || (r->inv_freq && r->positions);
+    return r->tokens == 0 || r->rotary == 0 || (t.inv_freq && t.positions);
 }
 
 // Whether one of the outputs (slices and whole spans) overlaps an input or
 // another output; outs[i] may be ins[i] or, with gradients, ins[i + 2].
-bool rope_clash(const gdn_qk_rope *r, std::initializer_list<Slices> outs, std::initializer_list<Slices> ins,
-                std::initializer_list<Span> sums) {
-    const Span small[] = {{r->q_weight, kHeadDim * sizeof(float)}, {r->k_weight, kHeadDim * sizeof(float)},
-                          {r->inv_freq, size_t(r->rotary) / 2 * sizeof(float)},
-                          {r->positions, size_t(r->axes) * r->tokens * sizeof(int32_t)},
-                          {r->pair_axis, size_t(r->rotary) / 2 * sizeof(int32_t)}};
+bool rope_clash(const gdn_qk_rope *r, const QkRopeTensors &t, std::initializer_list<Slices> outs,
+                std::initializer_list<Slices> ins, std::initializer_list<Span> sums) {
+    const Span small[] = {{t.weight[0], kHeadDim * sizeof(float)}, {t.weight[1], kHeadDim * sizeof(float)},
+                          {t.inv_freq, size_t(r->rotary) / 2 * sizeof(float)},
+                          {t.positions, size_t(r->axes) * r->tokens * sizeof(int32_t)},
+                          {t.pair_axis, size_t(r->rotary) / 2 * sizeof(int32_t)}};
     int o = 0;
     for (auto a = outs.begin(); a != outs.end(); ++a, ++o) {
         for (auto b = a + 1; b != outs.end(); ++b)
@@ -883,51 +881,52 @@ bool rope_clash(const gdn_qk_rope *r, std::initializer_list<Slices> outs, std::i
 
 extern "C" {
 
-int gdn_qk_norm_rope(const gdn_qk_rope *r, void *out_q, int64_t out_q_stride, void *out_k, int64_t out_k_stride,
+int gdn_qk_norm_rope(const gdn_qk_rope *r, const void *q, const void *k, const float *q_weight, const float *k_weight,
+                     const float *inv_freq, const int32_t *positions, const int32_t *pair_axis, void *out_q, void *out_k,
                      void *stream) {
     const int st = check_qk_rope(r);
     if (st) return st;
     const int size = r->io_dtype == GDN_DT_BF16 ? 2 : 4;
-    const Slices q{r->q, r->q_stride, r->hq, r->tokens, size}, k{r->k, r->k_stride, r->hk, r->tokens, size};
-    const Slices oq{out_q, out_q_stride, r->hq, r->tokens, size}, ok{out_k, out_k_stride, r->hk, r->tokens, size};
-    if (!q.ok() || !k.ok() || !oq.ok() || !ok.ok() || !rope_inputs_ok(r)) return GDN_EINVAL;
-    if (rope_clash(r, {oq, ok}, {q, k}, {})) return GDN_EINVAL;
+    QkRopeTensors t{};
+    t.x[0] = q, t.x[1] = k, t.y[0] = out_q, t.y[1] = out_k, t.weight[0] = q_weight, t.weight[1] = k_weight;
+    t.inv_freq = inv_freq, t.positions = positions, t.pair_axis = pair_axis;
+    const Slices sq{q, r->q_stride, r->hq, r->tokens, size}, sk{k, r->k_stride, r->hk, r->tokens, size};
+    const Slices oq{out_q, r->out_q_stride, r->hq, r->tokens, size}, ok{out_k, r->out_k_stride, r->hk, r->tokens, size};
+    if (!sq.ok() || !sk.ok() || !oq.ok() || !ok.ok() || !rope_inputs_ok(r, t)) return GDN_EINVAL;
+    if (rope_clash(r, t, {oq, ok}, {sq, sk}, {})) return GDN_EINVAL;
     int *status = status_ptr();
     if (!status) return GDN_ECUDA;
-    void *const y[2] = {out_q, out_k};
-    const long long ys[2] = {out_q_stride, out_k_stride};
-    return cuda_status(launch_qk_rope(*r, nullptr, nullptr, y, ys, nullptr, nullptr, status,
-                                      static_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_qk_rope(*r, t, nullptr, status, static_cast<cudaStream_t>(stream)));
 }
 
 size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_rope *r) {
     return check_qk_rope(r) == GDN_OK ? qk_rope_bwd_workspace(r->tokens, r->hq + r->hk, r->io_dtype) : 0;
 }
 
-int gdn_qk_norm_rope_bwd(const gdn_qk_rope *r, const void *dout_q, int64_t dout_q_stride, const void *dout_k,
-                         int64_t dout_k_stride, void *dq, int64_t dq_stride, void *dk, int64_t dk_stride,
-                         float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes, void *stream) {
+int gdn_qk_norm_rope_bwd(const gdn_qk_rope *r, const void *dout_q, const void *dout_k, const void *q, const void *k,
+                         const float *q_weight, const float *k_weight, const float *inv_freq, const int32_t *positions,
+                         const int32_t *pair_axis, void *dq, void *dk, float *dq_weight, float *dk_weight,
+                         void *workspace, size_t workspace_bytes, void *stream) {
     const int st = check_qk_rope(r);
     if (st) return st;
     const int size = r->io_dtype == GDN_DT_BF16 ? 2 : 4;
-    const Slices q{r->q, r->q_stride, r->hq, r->tokens, size}, k{r->k, r->k_stride, r->hk, r->tokens, size};
-    const Slices gq{dout_q, dout_q_stride, r->hq, r->tokens, size}, gk{dout_k, dout_k_stride, r->hk, r->tokens, size};
-    const Slices oq{dq, dq_stride, r->hq, r->tokens, size}, ok{dk, dk_stride, r->hk, r->tokens, size};
-    if (!q.ok() || !k.ok() || !gq.ok() || !gk.ok() || !oq.ok() || !ok.ok() || !rope_inputs_ok(r)) return GDN_EINVAL;
+    QkRopeTensors t{};
+    t.x[0] = q, t.x[1] = k, t.dy[0] = dout_q, t.dy[1] = dout_k, t.y[0] = dq, t.y[1] = dk;
+    t.weight[0] = q_weight, t.weight[1] = k_weight, t.dweight[0] = dq_weight, t.dweight[1] = dk_weight;
+    t.inv_freq = inv_freq, t.positions = positions, t.pair_axis = pair_axis;
+    const Slices sq{q, r->q_stride, r->hq, r->tokens, size}, sk{k, r->k_stride, r->hk, r->tokens, size};
+    const Slices gq{dout_q, r->dout_q_stride, r->hq, r->tokens, size}, gk{dout_k, r->dout_k_stride, r->hk, r->tokens, size};
+    const Slices oq{dq, r->out_q_stride, r->hq, r->tokens, size}, ok{dk, r->out_k_stride, r->hk, r->tokens, size};
+    if (!sq.ok() || !sk.ok() || !gq.ok() || !gk.ok() || !oq.ok() || !ok.ok() || !rope_inputs_ok(r, t)) return GDN_EINVAL;
     if (!aligned4(dq_weight) || !aligned4(dk_weight)) return GDN_EINVAL;
     const size_t need = dq_weight || dk_weight ? gdn_qk_norm_rope_bwd_workspace_size(r) : 0;
     if (need && !workspace_ok(workspace, workspace_bytes, need)) return GDN_EINVAL;
-    if (rope_clash(r, {oq, ok}, {q, k, gq, gk},
+    if (rope_clash(r, t, {oq, ok}, {sq, sk, gq, gk},
                    {{workspace, need}, {dq_weight, kHeadDim * sizeof(float)}, {dk_weight, kHeadDim * sizeof(float)}}))
         return GDN_EINVAL;
     int *status = status_ptr();
     if (!status) return GDN_ECUDA;
-    const void *const dy[2] = {dout_q, dout_k};
-    const long long ds[2] = {dout_q_stride, dout_k_stride};
-    void *const y[2] = {dq, dk};
-    const long long ys[2] = {dq_stride, dk_stride};
-    float *const dw[2] = {dq_weight, dk_weight};
-    return cuda_status(launch_qk_rope(*r, dy, ds, y, ys, dw, workspace, status, static_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_qk_rope(*r, t, workspace, status, static_cast<cudaStream_t>(stream)));
 }
 
 int gdn_read_device_status(void *stream, int clear) {

@@ -117,10 +117,15 @@ cudaError_t launch_gated_rmsnorm_bwd(const void *dy, const void *o, const void *
                                      void *d_o, void *d_z, float *d_weight, void *workspace, long long rows,
                                      int io_dtype, cudaStream_t s);
 size_t qk_rope_bwd_workspace(long long tokens, int heads, int io_dtype);
-// dy null: the forward pass into y; else the backward pass into y (dx) and dweight
-cudaError_t launch_qk_rope(const gdn_qk_rope &r, const void *const dy[2], const long long dy_stride[2],
-                           void *const y[2], const long long y_stride[2], float *const dweight[2], void *workspace,
-                           int *status, cudaStream_t s);
+// What both passes take besides the descriptor; index 0: q, 1: k.
+struct QkRopeTensors {
+    const void *x[2], *dy[2];  // dy null: the forward pass into y, else the backward pass into y (dx) and dweight
+    void *y[2];
+    const float *weight[2], *inv_freq;
+    const int *positions, *pair_axis;
+    float *dweight[2];
+};
+cudaError_t launch_qk_rope(const gdn_qk_rope &r, const QkRopeTensors &t, void *workspace, int *status, cudaStream_t s);
 cudaError_t launch_prefill_simt(const PrefillArgs &a, void *ws_data, cudaStream_t s);
 size_t prefill_simt_workspace(int max_chunks, int hv);
 cudaError_t launch_prefill_tc(const PrefillArgs &a, void *ws_data, cudaStream_t s);

@@ -17,6 +17,7 @@ __device__ __forceinline__ int seq_segs(int len, int seg_len) { return len > 0 ?
 __global__ void __launch_bounds__(kTableThreads) k_la_table(const __grid_constant__ Args a) {
     __shared__ int wsum[32];
     __shared__ int bad;
+    next_may_start();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, N = a.num_seqs;
     if (tid == 0) bad = 0;
     __syncthreads();
@@ -87,6 +88,8 @@ __global__ void __launch_bounds__(kTableThreads) k_la_table(const __grid_constan
 constexpr int kChainThreads = 256, kChainCtas = kState / 4 / kChainThreads, kChainBatch = 8;
 
 __global__ void __launch_bounds__(kChainThreads) k_la_chain(const __grid_constant__ Args a) {
+    next_may_start();
+    wait_for_previous();
     if (*a.n_segs == 0) return;
     const int part = blockIdx.x % kChainCtas, rest = blockIdx.x / kChainCtas, h = rest % a.hv;
     const Role &r = a.role[rest / a.hv];
@@ -135,10 +138,14 @@ __global__ void __launch_bounds__(kChainThreads) k_la_chain(const __grid_constan
     }
 }
 
-// y[t, hq] = sum over the group's heads of x[t, hv], in their order, rounded once
+// y[t, hq] = sum over the group's heads of x[t, hv], in their order, rounded once; of two tensors
 template <typename T>
-__global__ void __launch_bounds__(256) k_la_group_sum(const float *__restrict__ x, T *__restrict__ y, long long items,
-                                                      int group) {
+__global__ void __launch_bounds__(256) k_la_group_sums(const float *__restrict__ x0, T *__restrict__ y0,
+                                                       const float *__restrict__ x1, T *__restrict__ y1, long long items,
+                                                       int group) {
+    wait_for_previous();
+    const float *x = blockIdx.y ? x1 : x0;
+    T *y = blockIdx.y ? y1 : y0;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // four channels of a (token, query head)
     if (i >= items) return;
     const float *from = x + (i / 32 * group) * kHeadDim + (i % 32) * 4;
@@ -163,22 +170,22 @@ cudaError_t launch_table(const Args &a, cudaStream_t s) {
 
 cudaError_t launch_chain(const Args &a, cudaStream_t s) {
     LaunchScope scope(GDN_K_LINATTN_CHAIN, s);
-    k_la_chain<<<dim3(unsigned(kChainCtas) * unsigned(a.hv) * unsigned(a.roles), unsigned(a.num_seqs < 1024 ? a.num_seqs : 1024)),
-                 kChainThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(k_la_chain, dim3(unsigned(kChainCtas) * unsigned(a.hv) * unsigned(a.roles),
+                                          unsigned(a.num_seqs < 1024 ? a.num_seqs : 1024)),
+                         kChainThreads, 0, s, a);
 }
 
-cudaError_t launch_group_sum(const float *x, void *y, long long rows, int heads, int group, int io_dtype,
-                             cudaStream_t s) {
+cudaError_t launch_group_sums(const float *x0, void *y0, const float *x1, void *y1, long long rows, int heads, int group,
+                              int io_dtype, cudaStream_t s) {
     const long long items = rows * heads * 32;
     if (items == 0) return cudaSuccess;
     LaunchScope scope(GDN_K_LINATTN_GROUP_SUM, s);
-    const unsigned ctas = unsigned((items + 255) / 256);
+    const dim3 ctas(unsigned((items + 255) / 256), 2);
     if (io_dtype == GDN_DT_BF16)
-        k_la_group_sum<<<ctas, 256, 0, s>>>(x, static_cast<__nv_bfloat16 *>(y), items, group);
-    else
-        k_la_group_sum<<<ctas, 256, 0, s>>>(x, static_cast<float *>(y), items, group);
-    return cudaGetLastError();
+        return launch_behind(k_la_group_sums<__nv_bfloat16>, ctas, 256, 0, s, x0, static_cast<__nv_bfloat16 *>(y0), x1,
+                             static_cast<__nv_bfloat16 *>(y1), items, group);
+    return launch_behind(k_la_group_sums<float>, ctas, 256, 0, s, x0, static_cast<float *>(y0), x1,
+                         static_cast<float *>(y1), items, group);
 }
 
 int segment_rows(long long total_tokens, long long num_seqs, int hv, int roles, int io_dtype) {

@@ -77,12 +77,28 @@ __device__ __forceinline__ int entry_offset(const Role &r, const Seg &s, bool fi
     return r.against && first_chunk && (s.flags & kLast) ? 0 : 1;
 }
 
+// The kernels of a call follow one another closely: each lets the next one
+// start when all of its CTAs have, and that one reads nothing its predecessors
+// wrote before they have ended (each waits for the one before it, so for all).
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, A &&...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid, c.blockDim = dim3(block), c.dynamicSmemBytes = smem, c.stream = s, c.attrs = &attr, c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 cudaError_t launch_tc(const Args &a, cudaStream_t s);
 cudaError_t launch_simt(const Args &a, cudaStream_t s);
 cudaError_t launch_table(const Args &a, cudaStream_t s);
 cudaError_t launch_chain(const Args &a, cudaStream_t s);
-cudaError_t launch_group_sum(const float *x, void *y, long long rows, int heads, int group, int io_dtype,
-                             cudaStream_t s);
+cudaError_t launch_group_sums(const float *x0, void *y0, const float *x1, void *y1, long long rows, int heads, int group,
+                              int io_dtype, cudaStream_t s);
 // rows a segment may have: longest of the whole walk's estimated times
 int segment_rows(long long total_tokens, long long num_seqs, int hv, int roles, int io_dtype);
 

@@ -33,6 +33,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_la_simt(const __grid_constant__
     extern __shared__ __align__(16) uint8_t raw[];
     SimtShared &s = *reinterpret_cast<SimtShared *>(raw);
     const int role = blockIdx.x % p.roles, h = blockIdx.x / p.roles % p.hv, index = blockIdx.x / (p.roles * p.hv);
+    next_may_start();
+    wait_for_previous();
     if (index >= *p.n_segs) return;
     const Role &r = p.role[role];
     const Seg seg = p.segs[index];
@@ -44,10 +46,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_la_simt(const __grid_constant__
     const size_t per_head = size_t(p.hv) * kState;
     float *mine = r.states + size_t(index) * per_head + size_t(h) * kState;
     const float *init = kWalk && enters ? r.init ? r.init + size_t(seg.seq) * per_head + size_t(h) * kState : nullptr : mine;
-    for (int e = tid; e < kState; e += kThreads) {
-        float v = 0.f;
-        if (kWalk && init) v = enters && r.swapped ? init[e % kHeadDim * kHeadDim + e / kHeadDim] : init[e];
-        s.state[e] = v;
+    if (kWalk && init && enters && r.swapped) {
+#pragma unroll 16
+        for (int k = 0; k < kState / kThreads; ++k) {
+            const int e = k * kThreads + tid;
+            s.state[e] = init[e % kHeadDim * kHeadDim + e / kHeadDim];
+        }
+    } else {
+#pragma unroll 8
+        for (int k = 0; k < kState / 4 / kThreads; ++k) {
+            const int e = k * kThreads + tid;
+            reinterpret_cast<float4 *>(s.state)[e] =
+                kWalk && init ? reinterpret_cast<const float4 *>(init)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     }
 
     const int blocks = (seg.len + kB - 1) / kB;
@@ -197,10 +208,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_la_simt(const __grid_constant__
     }
     __syncthreads();
     if (!kWalk) {
-        for (int e = tid; e < kState; e += kThreads) mine[e] = s.state[e];
+#pragma unroll 8
+        for (int k = 0; k < kState / 4 / kThreads; ++k) {
+            const int e = k * kThreads + tid;
+            reinterpret_cast<float4 *>(mine)[e] = reinterpret_cast<const float4 *>(s.state)[e];
+        }
     } else if (leaves && r.fin) {
         const float f = r.against && seg.len > 0 ? s.tab[1] : 1.f;  // to the gradient of the state before the first token
         float *to = r.fin + size_t(seg.seq) * per_head + size_t(h) * kState;
+#pragma unroll 4
         for (int e = tid; e < kState; e += kThreads) {
             const float x = s.state[r.swapped ? e % kHeadDim * kHeadDim + e / kHeadDim : e];
             to[e] = f == 1.f ? x : f * x;
@@ -219,13 +235,12 @@ cudaError_t launch_simt(const Args &a, cudaStream_t s) {
     if (a.seg_len < a.total_tokens) {
         {
             LaunchScope scope(GDN_K_LINATTN_SUM, s);
-            k_la_simt<false><<<items, kThreads, kBytes, s>>>(a);
+            e = launch_behind(k_la_simt<false>, dim3(items), kThreads, kBytes, s, a);
         }
-        if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_chain(a, s)) != cudaSuccess) return e;
+        if (e != cudaSuccess || (e = launch_chain(a, s)) != cudaSuccess) return e;
     }
     LaunchScope scope(GDN_K_LINATTN_WALK, s);
-    k_la_simt<true><<<items, kThreads, kBytes, s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(k_la_simt<true>, dim3(items), kThreads, kBytes, s, a);
 }
 
 }  // namespace la

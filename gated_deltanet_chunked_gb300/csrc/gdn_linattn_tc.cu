@@ -35,16 +35,15 @@ struct Maps {
     CUtensorMap a[3], b[3], c[3], o[3];
 };
 
-// Segment, head and role of CTA `item`.
+// Segment, head and role of a CTA.
 struct Item {
     Seg seg;
     int index, h, role;
+    __device__ __forceinline__ explicit Item(const Args &p)
+        : index(blockIdx.x / (p.roles * p.hv)), h(blockIdx.x / p.roles % p.hv), role(blockIdx.x % p.roles) {}
 };
-__device__ __forceinline__ bool item_of(const Args &p, uint32_t smem, Item &it) {
-    const int i = blockIdx.x;
-    it.role = i % p.roles;
-    it.h = (i / p.roles) % p.hv;
-    it.index = i / (p.roles * p.hv);
+__device__ __forceinline__ bool segment_of(const Args &p, uint32_t smem, Item &it) {
+    wait_for_previous();
     it.seg = p.segs[it.index];  // (beside the count, not behind it)
     if (it.index >= *p.n_segs) return false;
     if (smem & 1023u) {  // (dynamic shared memory alone starts at a multiple: the tiles' swizzle counts on it)
@@ -220,20 +219,12 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
                                                               const __grid_constant__ Maps m) {
     extern __shared__ __align__(1024) uint8_t raw[];
     SumShared &s = *reinterpret_cast<SumShared *>(raw);
-    Item it;
-    if (!item_of(p, tc::smem_u32(raw), it)) return;
+    Item it(p);
     const Role &r = p.role[it.role];
-    const Seg seg = it.seg;
-    if (seg.flags & (r.against ? kFirst : kLast)) return;  // no segment follows
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int chunks = (seg.len + kC - 1) / kC;
-    auto load = [&](int n) {
-        const int u = n % 3;
-        tc::mbar_arrive_expect_tx(&s.b_full[u], kTile);
-        tc::mbar_arrive_expect_tx(&s.c_full[u], kTile);
-        load_tile(s.b[u], &m.b[it.role], it.h / r.gb, seg.start + n * kC, &s.b_full[u]);
-        load_tile(s.c[u], &m.c[it.role], it.h / r.gc, seg.start + n * kC, &s.c_full[u]);
-    };
+    next_may_start();
+    const float decay = p.decay[it.h];
+    if (tid <= kC) s.tab[tid] = power(decay, tid);
     if (warp == 8 && lane == 0) {
         for (int i = 0; i < 3; ++i) {
             tc::mbar_init(&s.b_full[i], 1);
@@ -247,10 +238,20 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
         tc::mbar_init(&s.done, 1);
         s.dead = 0;
         tc::fence_mbar_init();
-        for (int n = 0; n < min(3, chunks); ++n) load(n);
     }
-    const float decay = p.decay[it.h];
-    if (tid <= kC) s.tab[tid] = power(decay, tid);
+    if (!segment_of(p, tc::smem_u32(raw), it)) return;
+    const Seg seg = it.seg;
+    if (seg.flags & (r.against ? kFirst : kLast)) return;  // no segment follows
+    const int chunks = (seg.len + kC - 1) / kC;
+    auto load = [&](int n) {
+        const int u = n % 3;
+        tc::mbar_arrive_expect_tx(&s.b_full[u], kTile);
+        tc::mbar_arrive_expect_tx(&s.c_full[u], kTile);
+        load_tile(s.b[u], &m.b[it.role], it.h / r.gb, seg.start + n * kC, &s.b_full[u]);
+        load_tile(s.c[u], &m.c[it.role], it.h / r.gc, seg.start + n * kC, &s.c_full[u]);
+    };
+    if (warp == 8 && lane == 0)
+        for (int n = 0; n < min(3, chunks); ++n) load(n);
     if (warp == 9) {
         tc::tmem_alloc(&s.tmem, 512);
         tc::tmem_relinquish();
@@ -401,35 +402,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
                                                                 const __grid_constant__ Maps m) {
     extern __shared__ __align__(1024) uint8_t raw[];
     WalkShared &s = *reinterpret_cast<WalkShared *>(raw);
-    Item it;
-    if (!item_of(p, tc::smem_u32(raw), it)) return;
+    Item it(p);
     const Role &r = p.role[it.role];
-    const Seg seg = it.seg;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int chunks = (seg.len + kC - 1) / kC;
-    const bool leaves = r.fin && (seg.flags & (r.against ? kFirst : kLast));  // the state behind the last chunk is wanted
-    // the walk's n-th chunk
-    auto chunk_from = [&](int n) { return (r.against ? chunks - 1 - n : n) * kC; };
-    auto chunk_len = [&](int n) { return min(kC, seg.len - chunk_from(n)); };
-    auto sums = [&](int n) { return n + 1 < chunks || leaves; };
-    // tiles of the n-th chunk; A and B are counted on one barrier
-    auto row_of = [&](int n) { return seg.start + chunk_from(n); };
-    auto load_b = [&](int n) {
-        tc::mbar_arrive_expect_tx(&s.ab_full[n & 1], 2 * kTile);
-        load_tile(s.b[n & 1], &m.b[it.role], it.h / r.gb, row_of(n), &s.ab_full[n & 1]);
-    };
-    auto load_a = [&](int n) { load_tile(s.a[n & 1], &m.a[it.role], it.h / r.ga, row_of(n), &s.ab_full[n & 1]); };
-    auto load_c = [&](int n) {
-        tc::mbar_arrive_expect_tx(&s.c_full[n & 1], kTile);
-        load_tile(s.c[n & 1], &m.c[it.role], it.h / r.gc, row_of(n), &s.c_full[n & 1]);
-    };
-    // the chunk after those under way comes from HBM meanwhile
-    auto prefetch = [&](int n) {
-        if (n >= chunks) return;
-        prefetch_tile(&m.b[it.role], it.h / r.gb, row_of(n));
-        prefetch_tile(&m.a[it.role], it.h / r.ga, row_of(n));
-        prefetch_tile(&m.c[it.role], it.h / r.gc, row_of(n));
-    };
+    next_may_start();
+    const float decay = p.decay[it.h];
+    if (tid <= kC) {
+        const float f = power(decay, tid);
+        s.between[kC - tid] = f;
+        if (tid < kC) s.between[kC + tid] = f;
+    }
     if (warp == 20 && lane == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&s.ab_full[i], 1);
@@ -455,14 +437,36 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
         tc::mbar_init(&s.drain, 1);
         s.dead = 0;
         tc::fence_mbar_init();
+    }
+    if (!segment_of(p, tc::smem_u32(raw), it)) return;
+    const Seg seg = it.seg;
+    const int chunks = (seg.len + kC - 1) / kC;
+    const bool leaves = r.fin && (seg.flags & (r.against ? kFirst : kLast));  // the state behind the last chunk is wanted
+    // the walk's n-th chunk
+    auto chunk_from = [&](int n) { return (r.against ? chunks - 1 - n : n) * kC; };
+    auto chunk_len = [&](int n) { return min(kC, seg.len - chunk_from(n)); };
+    auto sums = [&](int n) { return n + 1 < chunks || leaves; };
+    // tiles of the n-th chunk; A and B are counted on one barrier
+    auto row_of = [&](int n) { return seg.start + chunk_from(n); };
+    auto load_b = [&](int n) {
+        tc::mbar_arrive_expect_tx(&s.ab_full[n & 1], 2 * kTile);
+        load_tile(s.b[n & 1], &m.b[it.role], it.h / r.gb, row_of(n), &s.ab_full[n & 1]);
+    };
+    auto load_a = [&](int n) { load_tile(s.a[n & 1], &m.a[it.role], it.h / r.ga, row_of(n), &s.ab_full[n & 1]); };
+    auto load_c = [&](int n) {
+        tc::mbar_arrive_expect_tx(&s.c_full[n & 1], kTile);
+        load_tile(s.c[n & 1], &m.c[it.role], it.h / r.gc, row_of(n), &s.c_full[n & 1]);
+    };
+    // the chunk after those under way comes from HBM meanwhile
+    auto prefetch = [&](int n) {
+        if (n >= chunks) return;
+        prefetch_tile(&m.b[it.role], it.h / r.gb, row_of(n));
+        prefetch_tile(&m.a[it.role], it.h / r.ga, row_of(n));
+        prefetch_tile(&m.c[it.role], it.h / r.gc, row_of(n));
+    };
+    if (warp == 20 && lane == 0) {
         for (int n = 0; n < min(2, chunks); ++n) load_b(n), load_a(n), load_c(n);
         prefetch(2);
-    }
-    const float decay = p.decay[it.h];
-    if (tid <= kC) {
-        const float f = power(decay, tid);
-        s.between[kC - tid] = f;
-        if (tid < kC) s.between[kC + tid] = f;
     }
     if (tid >= 256 && tid < 256 + kC) {  // B's decays, of a whole chunk and of the one that ends the segment
         const int which = (tid - 256) / (kC / 2), pair = tid % (kC / 2), row = 2 * pair;
@@ -818,13 +822,12 @@ cudaError_t launch_tc(const Args &args, cudaStream_t s) {
     if (a.seg_len < a.total_tokens) {
         {
             LaunchScope scope(GDN_K_LINATTN_SUM, s);
-            k_la_sum_tc<<<items, kSumThreads, kSumBytes, s>>>(a, m);
+            e = launch_behind(k_la_sum_tc, dim3(items), kSumThreads, kSumBytes, s, a, m);
         }
-        if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_chain(a, s)) != cudaSuccess) return e;
+        if (e != cudaSuccess || (e = launch_chain(a, s)) != cudaSuccess) return e;
     }
     LaunchScope scope(GDN_K_LINATTN_WALK, s);
-    k_la_walk_tc<<<items, kWalkThreads, kWalkBytes, s>>>(a, m);
-    return cudaGetLastError();
+    return launch_behind(k_la_walk_tc, dim3(items), kWalkThreads, kWalkBytes, s, a, m);
 }
 
 }  // namespace la

@@ -345,25 +345,22 @@ size_t qk_rope_bwd_workspace(long long tokens, int heads, int io_dtype) {
     return size_t(ctas_of(tokens, step_of(tokens, heads, io_dtype), true)) * 2 * kHeadDim * sizeof(float);
 }
 
-cudaError_t launch_qk_rope(const gdn_qk_rope &r, const void *const dy[2], const long long dy_stride[2], void *const y[2],
-                           const long long y_stride[2], float *const dweight[2], void *workspace, int *status,
-                           cudaStream_t s) {
+cudaError_t launch_qk_rope(const gdn_qk_rope &r, const QkRopeTensors &t, void *workspace, int *status, cudaStream_t s) {
     const int heads = r.hq + r.hk;
+    const bool bwd = t.dy[0] != nullptr || t.dy[1] != nullptr || t.dweight[0] || t.dweight[1];
     RopeArgs a{};
-    a.x[0] = r.q, a.x[1] = r.k;
     a.xs[0] = r.q_stride, a.xs[1] = r.k_stride;
-    const bool bwd = dy != nullptr;
-    float *parts = static_cast<float *>(workspace);
+    a.ds[0] = r.dout_q_stride, a.ds[1] = r.dout_k_stride;
+    a.ys[0] = r.out_q_stride, a.ys[1] = r.out_k_stride;
     a.heads[0] = r.hq, a.heads[1] = r.hk;
     a.step = step_of(r.tokens, heads, r.io_dtype);
     const int ctas = ctas_of(r.tokens, a.step, bwd);
+    float *const parts = static_cast<float *>(workspace), *const *dweight = t.dweight;
     for (int w = 0; w < 2; ++w) {
-        if (bwd) a.dy[w] = dy[w], a.ds[w] = dy_stride[w];
-        a.y[w] = y[w], a.ys[w] = y_stride[w];
-        if (bwd && dweight[w]) a.partial[w] = parts + size_t(w) * ctas * kHeadDim;
+        a.x[w] = t.x[w], a.dy[w] = t.dy[w], a.y[w] = t.y[w], a.weight[w] = t.weight[w];
+        if (dweight[w]) a.partial[w] = parts + size_t(w) * ctas * kHeadDim;
     }
-    a.weight[0] = r.q_weight, a.weight[1] = r.k_weight;
-    a.inv_freq = r.inv_freq, a.positions = r.positions, a.pair_axis = r.pair_axis;
+    a.inv_freq = t.inv_freq, a.positions = t.positions, a.pair_axis = t.pair_axis;
     a.eps = r.eps;
     a.tokens = r.tokens, a.pairs = r.rotary / 2, a.axes = r.axes;
     a.status = status;

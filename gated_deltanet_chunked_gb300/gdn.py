@@ -52,12 +52,11 @@ class GdnProblem(ctypes.Structure):
 
 
 class GdnQkRope(ctypes.Structure):
-    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
-                ("k_stride", ctypes.c_int64), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
-                ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
-                ("eps", ctypes.c_float), ("tokens", ctypes.c_int32), ("hq", ctypes.c_int32), ("hk", ctypes.c_int32),
-                ("rotary", ctypes.c_int32), ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
-                ("io_dtype", ctypes.c_int32)]
+    _fields_ = [("tokens", ctypes.c_int32), ("hq", ctypes.c_int32), ("hk", ctypes.c_int32), ("rotary", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("out_q_stride", ctypes.c_int64), ("out_k_stride", ctypes.c_int64), ("dout_q_stride", ctypes.c_int64),
+                ("dout_k_stride", ctypes.c_int64)]
 
 
 class GdnError(RuntimeError):
@@ -119,7 +118,7 @@ def load(path: Optional[str] = None):
             lib.gdn_chunk_fwd_noalloc.argtypes = [P, _vp, _vp, _vp, _fp, _fp, ctypes.c_float, _fp, _ip, _vp, _fp,
                                                   _vp]
             lib.gdn_chunk_fwd_noalloc.restype = ctypes.c_int
-            cf, sz, i64, R = ctypes.c_float, ctypes.c_size_t, ctypes.c_int64, ctypes.POINTER(GdnQkRope)
+            cf, sz, R = ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(GdnQkRope)
             for name, res, args in (
                     ("gdn_linear_recurrence", ctypes.c_int, [P, _vp, _vp, _fp, _ip, _vp, _fp, _fp, _vp]),
                     ("gdn_linear_recurrence_states_size", sz, [P]),
@@ -140,9 +139,9 @@ def load(path: Optional[str] = None):
                      [P, _vp, _vp, _vp, _vp, _fp, cf, _fp, _fp, _ip, _vp, _vp, _vp, _fp, _vp, sz, _vp]),
                     ("gdn_linear_attention_bwd_workspace_size", sz, [P]),
                     ("gdn_linear_attention_step", ctypes.c_int, [P, _vp, _vp, _vp, _fp, cf, _vp, _ip, _vp, _vp]),
-                    ("gdn_qk_norm_rope", ctypes.c_int, [R, _vp, i64, _vp, i64, _vp]),
+                    ("gdn_qk_norm_rope", ctypes.c_int, [R, _vp, _vp, _fp, _fp, _fp, _ip, _ip, _vp, _vp, _vp]),
                     ("gdn_qk_norm_rope_bwd", ctypes.c_int,
-                     [R, _vp, i64, _vp, i64, _vp, i64, _vp, i64, _fp, _fp, _vp, sz, _vp]),
+                     [R, _vp, _vp, _vp, _vp, _fp, _fp, _fp, _ip, _ip, _vp, _vp, _fp, _fp, _vp, sz, _vp]),
                     ("gdn_qk_norm_rope_bwd_workspace_size", sz, [R])):
                 fn = getattr(lib, name)
                 fn.restype, fn.argtypes = res, args
@@ -861,7 +860,8 @@ def gdn_gated_rmsnorm_bwd(dy, o, z, weight, eps, do=None, dz=None, dweight=None,
 
 @functools.lru_cache(maxsize=1024)
 def _linattn_layout(q_shape, v_shape, dtype, offsets):
-    """(descriptor's reference, state shape) of linear attention on q of
+    """(descriptor's reference, state shape, workspace bytes of the forward and
+    of the backward pass) of linear attention on q of
     ``q_shape``, [T, Hq, 128] with cu_seqlens of shape ``offsets`` or
     [B, T, Hq, 128] with None."""
     packed = offsets is not None
@@ -880,7 +880,9 @@ def _linattn_layout(q_shape, v_shape, dtype, offsets):
         batch, seqlen = q_shape[:2]
         num_seqs, total = batch, batch * seqlen
     _, ref = _descriptor(batch, seqlen, num_seqs, total, hq, hv, dk, dv, _io_type(dtype), 0, 0)
-    return ref, (num_seqs, hv, dk, dv)
+    lib = load()
+    return (ref, (num_seqs, hv, dk, dv), int(lib.gdn_linear_attention_workspace_size(ref)),
+            int(lib.gdn_linear_attention_bwd_workspace_size(ref)))
 
 
 def gdn_linear_attention(q, k, v, decay, scale, initial_state=None, cu_seqlens=None, out=None, final_state=None,
@@ -898,7 +900,8 @@ def gdn_linear_attention(q, k, v, decay, scale, initial_state=None, cu_seqlens=N
         with _launching(stream, dev):
             return gdn_linear_attention(q, k, v, decay, scale, initial_state, cu_seqlens, out, final_state,
                                         output_final_state, workspace)
-    ref, state_shape = _linattn_layout(q.shape, v.shape, q.dtype, None if cu_seqlens is None else cu_seqlens.shape)
+    ref, state_shape, need, need_bwd = _linattn_layout(q.shape, v.shape, q.dtype,
+                                                       None if cu_seqlens is None else cu_seqlens.shape)
     f32, io = torch.float32, q.dtype
     pq = _first("q", q)
     pk = _arg("k", k, io, q.shape, dev)
@@ -916,7 +919,7 @@ def gdn_linear_attention(q, k, v, decay, scale, initial_state=None, cu_seqlens=N
         final_state = torch.empty(state_shape, dtype=f32, device=dev)
         pf = final_state.data_ptr()
     lib = load()
-    pws, nbytes, workspace = _workspace(workspace, lib.gdn_linear_attention_workspace_size(ref), dev)
+    pws, nbytes, workspace = _workspace(workspace, need, dev)
     st = lib.gdn_linear_attention(ref, pq, pk, pv, pd, scale, ps0, pcu, po, pf, pws, nbytes, handle)
     if st != GDN_OK:
         raise GdnError(st, "gdn_linear_attention")
@@ -934,7 +937,8 @@ def gdn_linear_attention_bwd(dout, q, k, v, decay, scale, initial_state=None, cu
         with _launching(stream, dev):
             return gdn_linear_attention_bwd(dout, q, k, v, decay, scale, initial_state, cu_seqlens, dfinal_state, dq,
                                             dk, dv, dinitial_state, workspace)
-    ref, state_shape = _linattn_layout(q.shape, v.shape, q.dtype, None if cu_seqlens is None else cu_seqlens.shape)
+    ref, state_shape, need, need_bwd = _linattn_layout(q.shape, v.shape, q.dtype,
+                                                       None if cu_seqlens is None else cu_seqlens.shape)
     f32, io = torch.float32, q.dtype
     pq = _first("q", q)
     pdo = _arg("dout", dout, io, v.shape, dev)
@@ -962,7 +966,7 @@ def gdn_linear_attention_bwd(dout, q, k, v, decay, scale, initial_state=None, cu
         dinitial_state = torch.empty(state_shape, dtype=f32, device=dev)
         pd0 = dinitial_state.data_ptr()
     lib = load()
-    pws, nbytes, workspace = _workspace(workspace, lib.gdn_linear_attention_bwd_workspace_size(ref), dev)
+    pws, nbytes, workspace = _workspace(workspace, need_bwd, dev)
     st = lib.gdn_linear_attention_bwd(ref, pdo, pq, pk, pv, pd, scale, ps0, pdf, pcu, pdq, pdk, pdv, pd0, pws, nbytes,
                                       handle)
     if st != GDN_OK:
@@ -1001,42 +1005,42 @@ def gdn_linear_attention_step(q, k, v, decay, scale, state, state_indices=None, 
     return out
 
 
-def _head_rows(name, t, dtype, shape, dev):
-    """(address, elements from token to token) of ``t`` [T, H, 128], whose heads
-    lie together and whose tokens may lie apart."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev} (the device of the first input)")
+def _token_stride(name, shape, stride):
+    """Elements from token to token of [T, H, 128] whose heads lie together."""
     T, H, D = shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+    if stride[2] != 1 or (H > 1 and stride[1] != D):
         raise ValueError(f"a token's heads of {name} must lie together")
-    return t.data_ptr(), (t.stride(0) if T > 1 else H * D)
+    return stride[0] if T > 1 else H * D
 
 
-def _rope_problem(q, k, q_weight, k_weight, inv_freq, positions, pair_axis, interleaved, eps):
-    """(descriptor, its reference) of gdn_qk_norm_rope's inputs after their checks."""
-    dev, io = q.device, q.dtype
-    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != 128:
+@functools.lru_cache(maxsize=1024)
+def _rope_layout(q_shape, k_shape, freq_shape, pos_shape, has_axis, interleaved, eps, dtype, strides):
+    """(descriptor's reference, positions' shape, workspace bytes of the backward pass) of gdn_qk_norm_rope; strides:
+    those of q, k, the two outputs and (None in the forward pass) their gradients, None for a contiguous tensor."""
+    if len(q_shape) != 3 or len(k_shape) != 3 or q_shape[2] != 128:
         raise ValueError("q must be [T, Hq, 128] and k [T, Hk, 128]")
-    T, hq, d = q.shape
-    pq, sq = _head_rows("q", q, io, q.shape, dev)
-    pk, sk = _head_rows("k", k, io, (T, k.shape[1], d), dev)
-    f32, i32 = torch.float32, torch.int32
-    if inv_freq.dim() != 1 or inv_freq.shape[0] > d // 2:
-        raise ValueError(f"inv_freq must be 1-D with at most {d // 2} elements, got {tuple(inv_freq.shape)}")
-    half = inv_freq.shape[0]
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if axes > 1 and pair_axis is None:
+    T, hq, d = q_shape
+    if k_shape != (T, k_shape[1], d):
+        raise ValueError(f"k must have shape {(T, k_shape[1], d)}, got {tuple(k_shape)}")
+    if len(freq_shape) != 1 or freq_shape[0] > d // 2:
+        raise ValueError(f"inv_freq must be 1-D with at most {d // 2} elements, got {tuple(freq_shape)}")
+    axes = 1 if len(pos_shape) == 1 else pos_shape[0]
+    if axes > 1 and not has_axis:
         raise ValueError("positions of several axes need pair_axis, each pair's axis")
-    r = GdnQkRope(pq, pk, sq, sk, _arg("q_weight", q_weight, f32, (d,), dev), _arg("k_weight", k_weight, f32, (d,), dev),
-                  _arg("inv_freq", inv_freq, f32, (half,), dev),
-                  _arg("positions", positions, i32, (T,) if positions.dim() == 1 else (axes, T), dev),
-                  _arg("pair_axis", pair_axis, i32, (half,), dev), eps, T, hq, k.shape[1], 2 * half, axes,
-                  int(bool(interleaved)), _io_type(io))
-    return r, ctypes.byref(r)
+    names = ("q", "k", "the output of q", "the output of k", "the gradient of q's output", "the gradient of k's output")
+    tokens = [s if s is None else _token_stride(n, k_shape if i % 2 else q_shape, s)
+              for i, (n, s) in enumerate(zip(names, strides))]
+    tokens = [(k_shape[1] if i % 2 else hq) * d if s is None else s for i, s in enumerate(tokens)]
+    r = GdnQkRope(T, hq, k_shape[1], 2 * freq_shape[0], axes, int(interleaved), _io_type(dtype), eps, *tokens)
+    ref = ctypes.byref(r)
+    return ref, (T,) if len(pos_shape) == 1 else (axes, T), int(load().gdn_qk_norm_rope_bwd_workspace_size(ref))
+
+
+def _rows_arg(name, t, dtype, shape, dev):
+    """Address of ``t`` after the checks of its type, shape and device (its strides are _rope_layout's)."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev:
+        return t.data_ptr()
+    return _arg(name, t, dtype, shape, dev)
 
 
 def gdn_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, pair_axis=None, interleaved=False, eps=1e-6,
@@ -1056,15 +1060,24 @@ def gdn_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, pair_axis=No
         with _launching(stream, dev):
             return gdn_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, pair_axis, interleaved, eps, out_q,
                                     out_k)
-    r, ref = _rope_problem(q, k, q_weight, k_weight, inv_freq, positions, pair_axis, interleaved, eps)
+    io, f32, i32 = q.dtype, torch.float32, torch.int32
+    ref, pos_shape, _ = _rope_layout(
+        q.shape, k.shape, inv_freq.shape, positions.shape, pair_axis is not None, bool(interleaved), eps, io,
+        (q.stride(), k.stride(), None if out_q is None else out_q.stride(), None if out_k is None else out_k.stride(),
+         None, None))
+    pk = _rows_arg("k", k, io, k.shape, dev)
+    pqw = _arg("q_weight", q_weight, f32, (128,), dev)
+    pkw = _arg("k_weight", k_weight, f32, (128,), dev)
+    pf = _arg("inv_freq", inv_freq, f32, inv_freq.shape, dev)
+    pp = _arg("positions", positions, i32, pos_shape, dev)
+    pa = _arg("pair_axis", pair_axis, i32, inv_freq.shape, dev)
     handle = _current(dev)
     if out_q is None:
-        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out_q = torch.empty(q.shape, dtype=io, device=dev)
     if out_k is None:
-        out_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    poq, soq = _head_rows("out_q", out_q, q.dtype, q.shape, dev)
-    pok, sok = _head_rows("out_k", out_k, q.dtype, k.shape, dev)
-    st = load().gdn_qk_norm_rope(ref, poq, soq, pok, sok, handle)
+        out_k = torch.empty(k.shape, dtype=io, device=dev)
+    st = load().gdn_qk_norm_rope(ref, q.data_ptr(), pk, pqw, pkw, pf, pp, pa, _rows_arg("out_q", out_q, io, q.shape, dev),
+                                 _rows_arg("out_k", out_k, io, k.shape, dev), handle)
     if st != GDN_OK:
         raise GdnError(st, "gdn_qk_norm_rope")
     return out_q, out_k
@@ -1084,29 +1097,40 @@ def gdn_qk_norm_rope_bwd(dout_q, dout_k, q, k, q_weight, k_weight, inv_freq, pos
         with _launching(stream, dev):
             return gdn_qk_norm_rope_bwd(dout_q, dout_k, q, k, q_weight, k_weight, inv_freq, positions, pair_axis,
                                         interleaved, eps, dq, dk, dq_weight, dk_weight, need_dweight, workspace)
-    r, ref = _rope_problem(q, k, q_weight, k_weight, inv_freq, positions, pair_axis, interleaved, eps)
-    f32, io = torch.float32, q.dtype
-    pgq, sgq = _head_rows("dout_q", dout_q, io, q.shape, dev)
-    pgk, sgk = _head_rows("dout_k", dout_k, io, k.shape, dev)
-    pqw = _arg("dq_weight", dq_weight, f32, (128,), dev)
-    pkw = _arg("dk_weight", dk_weight, f32, (128,), dev)
+    io, f32, i32 = q.dtype, torch.float32, torch.int32
+    ref, pos_shape, need = _rope_layout(
+        q.shape, k.shape, inv_freq.shape, positions.shape, pair_axis is not None, bool(interleaved), eps, io,
+        (q.stride(), k.stride(), None if dq is None else dq.stride(), None if dk is None else dk.stride(),
+         dout_q.stride(), dout_k.stride()))
+    pk = _rows_arg("k", k, io, k.shape, dev)
+    pgq = _rows_arg("dout_q", dout_q, io, q.shape, dev)
+    pgk = _rows_arg("dout_k", dout_k, io, k.shape, dev)
+    pqw = _arg("q_weight", q_weight, f32, (128,), dev)
+    pkw = _arg("k_weight", k_weight, f32, (128,), dev)
+    pf = _arg("inv_freq", inv_freq, f32, inv_freq.shape, dev)
+    pp = _arg("positions", positions, i32, pos_shape, dev)
+    pa = _arg("pair_axis", pair_axis, i32, inv_freq.shape, dev)
+    pdqw = _arg("dq_weight", dq_weight, f32, (128,), dev)
+    pdkw = _arg("dk_weight", dk_weight, f32, (128,), dev)
     handle = _current(dev)
     if dq is None:
         dq = torch.empty(q.shape, dtype=io, device=dev)
     if dk is None:
         dk = torch.empty(k.shape, dtype=io, device=dev)
-    pdq, sdq = _head_rows("dq", dq, io, q.shape, dev)
-    pdk, sdk = _head_rows("dk", dk, io, k.shape, dev)
-    if dq_weight is None and need_dweight:
-        dq_weight = torch.empty(128, dtype=f32, device=dev)
-        pqw = dq_weight.data_ptr()
-    if dk_weight is None and need_dweight:
-        dk_weight = torch.empty(128, dtype=f32, device=dev)
-        pkw = dk_weight.data_ptr()
-    lib, pws, nbytes = load(), None, 0
-    if pqw or pkw or workspace is not None:
-        pws, nbytes, workspace = _workspace(workspace, lib.gdn_qk_norm_rope_bwd_workspace_size(ref), dev)
-    st = lib.gdn_qk_norm_rope_bwd(ref, pgq, sgq, pgk, sgk, pdq, sdq, pdk, sdk, pqw, pkw, pws, nbytes, handle)
+    if need_dweight and (dq_weight is None or dk_weight is None):
+        both = torch.empty((2, 128), dtype=f32, device=dev)
+        if dq_weight is None:
+            dq_weight = both[0]
+            pdqw = dq_weight.data_ptr()
+        if dk_weight is None:
+            dk_weight = both[1]
+            pdkw = dk_weight.data_ptr()
+    pws, nbytes = None, 0
+    if pdqw or pdkw or workspace is not None:
+        pws, nbytes, workspace = _workspace(workspace, need, dev)
+    st = load().gdn_qk_norm_rope_bwd(ref, pgq, pgk, q.data_ptr(), pk, pqw, pkw, pf, pp, pa,
+                                     _rows_arg("dq", dq, io, q.shape, dev), _rows_arg("dk", dk, io, k.shape, dev), pdqw,
+                                     pdkw, pws, nbytes, handle)
     if st != GDN_OK:
         raise GdnError(st, "gdn_qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight

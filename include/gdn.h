@@ -512,23 +512,20 @@ int gdn_linear_attention_step(const gdn_problem *p, const void *q, const void *k
 
 /* ---- norm and rotation of queries and keys ---- */
 
-/* What both passes of gdn_qk_norm_rope are given. */
+/* Descriptor of gdn_qk_norm_rope and its backward pass. Strides are elements
+ * from a token to the next, a multiple of 16 bytes and at least the heads'
+ * elements: a token's heads lie together, so that slices of a projection's
+ * rows need no copy. */
 typedef struct gdn_qk_rope {
-    const void *q, *k;           /* [tokens, hq, 128], [tokens, hk, 128] io dtype, 16-byte aligned; a token's
-                                    heads lie together, tokens q_stride and k_stride elements apart (a multiple
-                                    of 16 bytes, at least the heads' elements): slices of a projection's rows
-                                    need no copy */
-    int64_t q_stride, k_stride;
-    const float *q_weight, *k_weight; /* [128] f32, 4-byte aligned, or NULL (1) */
-    const float *inv_freq;       /* [rotary / 2] f32: radians per position of each pair */
-    const int32_t *positions;    /* [axes, tokens] */
-    const int32_t *pair_axis;    /* [rotary / 2], the axis whose position turns a pair, or NULL (axis 0) */
-    float eps;
     int32_t tokens, hq, hk;
     int32_t rotary;              /* channels rotated, the first ones of a head: even, 0 .. 128 */
     int32_t axes;                /* 1 .. 8 */
     int32_t interleaved;         /* pairs: 0: channels (i, i + rotary / 2); 1: (2 i, 2 i + 1) */
-    int32_t io_dtype;            /* gdn_dtype of q, k and the outputs */
+    int32_t io_dtype;            /* gdn_dtype of q, k, the outputs and their gradients */
+    float eps;
+    int64_t q_stride, k_stride;
+    int64_t out_q_stride, out_k_stride;   /* of out_q and out_k; backward: of dq and dk */
+    int64_t dout_q_stride, dout_k_stride; /* backward only */
 } gdn_qk_rope;
 
 /* The norm of every query and key head and its rotation by position: with
@@ -537,29 +534,36 @@ typedef struct gdn_qk_rope {
  * for every pair (a, b); channels behind `rotary` are n. With several axes
  * (time, height, width of a patch) each pair is turned by the position of its
  * own axis.
- *   out_q, out_k  like q and k, with strides of their own; out_q may be q and
- *                 out_k may be k, in exactly their places
+ *   q, out_q      [tokens, hq, 128] io dtype, 16-byte aligned; k and out_k with
+ *                 hk heads; out_q may be q and out_k may be k, in exactly their
+ *                 places
+ *   q_weight, k_weight [128] f32, 4-byte aligned, or NULL (1)
+ *   inv_freq      [rotary / 2] f32: radians per position of each pair
+ *   positions     int32 [axes, tokens]
+ *   pair_axis     int32 [rotary / 2], the axis that turns a pair, or NULL (axis 0)
  * The angle's error is below 2^-22 radian for every int32 position, all else
  * is f32 and rounded once. An axis outside 0 .. axes - 1 is recorded as
  * GDN_EDEVICE_INPUT and nothing is written. */
-int gdn_qk_norm_rope(const gdn_qk_rope *r, void *out_q, int64_t out_q_stride, void *out_k, int64_t out_k_stride,
+int gdn_qk_norm_rope(const gdn_qk_rope *r, const void *q, const void *k, const float *q_weight, const float *k_weight,
+                     const float *inv_freq, const int32_t *positions, const int32_t *pair_axis, void *out_q, void *out_k,
                      void *stream);
 
 /* Backward pass of gdn_qk_norm_rope: with dn the outputs' gradient turned back,
  * xhat = x / sqrt(mean x^2 + eps) and u = dn * weight,
  *   dx = (u - xhat mean_j(u xhat)) / sqrt(mean x^2 + eps),
  *   dweight[j] = sum over tokens and heads of dn xhat.
- *   dout_q, dout_k, dq, dk  like q and k, with strides of their own; dq may be
- *                 q or dout_q, dk may be k or dout_k
+ *   dout_q, dout_k, dq, dk  like q and k; dq may be q or dout_q, dk may be k
+ *                 or dout_k
  *   dq_weight, dk_weight [128] f32, or NULL to skip; written (not added to),
  *                 with no tokens zeros
  *   workspace     gdn_qk_norm_rope_bwd_workspace_size(r) bytes, 256-byte
  *                 aligned; may be NULL when both are. Calls that share it must
  *                 be ordered on one stream.
  * The sums over rows are taken in a fixed order. */
-int gdn_qk_norm_rope_bwd(const gdn_qk_rope *r, const void *dout_q, int64_t dout_q_stride, const void *dout_k,
-                         int64_t dout_k_stride, void *dq, int64_t dq_stride, void *dk, int64_t dk_stride,
-                         float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes, void *stream);
+int gdn_qk_norm_rope_bwd(const gdn_qk_rope *r, const void *dout_q, const void *dout_k, const void *q, const void *k,
+                         const float *q_weight, const float *k_weight, const float *inv_freq, const int32_t *positions,
+                         const int32_t *pair_axis, void *dq, void *dk, float *dq_weight, float *dk_weight,
+                         void *workspace, size_t workspace_bytes, void *stream);
 size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_rope *r);
 
 /* Synchronises `stream`, returns the device status word (GDN_OK or the first

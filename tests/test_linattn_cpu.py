@@ -104,16 +104,17 @@ def test_step_refusals():
     assert step(flags=2) == gdn.GDN_EUNSUPPORTED
 
 
-def rope_call(back=False, oq=8 * FAKE, oqs=256, ok=9 * FAKE, oks=128, gq=10 * FAKE, gk=11 * FAKE, dqw=None, dkw=None,
-              ws=None, nbytes=0, **kw):
-    r = gdn.GdnQkRope(**{**dict(q=FAKE, k=2 * FAKE, q_stride=256, k_stride=128, q_weight=3 * FAKE, k_weight=4 * FAKE,
-                                inv_freq=5 * FAKE, positions=6 * FAKE, pair_axis=7 * FAKE, eps=1e-6, tokens=64, hq=2,
-                                hk=1, rotary=128, axes=1, interleaved=0, io_dtype=gdn.GDN_DT_BF16), **kw})
-    lib = gdn.load()
+def rope_call(back=False, q=FAKE, k=2 * FAKE, q_weight=3 * FAKE, k_weight=4 * FAKE, inv_freq=5 * FAKE, positions=6 * FAKE,
+              pair_axis=7 * FAKE, oq=8 * FAKE, ok=9 * FAKE, gq=10 * FAKE, gk=11 * FAKE, dqw=None, dkw=None, ws=None, nbytes=0,
+              **kw):
+    r = gdn.GdnQkRope(**{**dict(q_stride=256, k_stride=128, out_q_stride=256, out_k_stride=128, dout_q_stride=256,
+                                dout_k_stride=128, eps=1e-6, tokens=64, hq=2, hk=1, rotary=128, axes=1, interleaved=0,
+                                io_dtype=gdn.GDN_DT_BF16), **kw})
+    lib, inputs = gdn.load(), [ptr(x) for x in (q, k, q_weight, k_weight, inv_freq, positions, pair_axis)]
     if not back:
-        return lib.gdn_qk_norm_rope(ctypes.byref(r), ptr(oq), oqs, ptr(ok), oks, None)
-    return lib.gdn_qk_norm_rope_bwd(ctypes.byref(r), ptr(gq), 256, ptr(gk), 128, ptr(oq), oqs, ptr(ok), oks, ptr(dqw),
-                                    ptr(dkw), ptr(ws), ctypes.c_size_t(nbytes), None)
+        return lib.gdn_qk_norm_rope(ctypes.byref(r), *inputs, ptr(oq), ptr(ok), None)
+    return lib.gdn_qk_norm_rope_bwd(ctypes.byref(r), ptr(gq), ptr(gk), *inputs, ptr(oq), ptr(ok), ptr(dqw), ptr(dkw),
+                                    ptr(ws), ctypes.c_size_t(nbytes), None)
 
 
 @pytest.mark.parametrize("back", [False, True])
@@ -121,10 +122,10 @@ def test_rope_refusals(back):
     bad = [dict(tokens=-1), dict(hq=0), dict(hk=0), dict(rotary=3), dict(rotary=-2), dict(rotary=130), dict(axes=0),
            dict(axes=9), dict(io_dtype=7), dict(eps=-1.0), dict(eps=float("nan")), dict(q=None), dict(k=None),
            dict(q=FAKE + 8), dict(oq=None), dict(ok=9 * FAKE + 2), dict(q_stride=255), dict(q_stride=128),
-           dict(oqs=128), dict(oqs=257), dict(q_stride=-256), dict(q_stride=1 << 62), dict(q_weight=3 * FAKE + 2),
+           dict(out_q_stride=128), dict(out_q_stride=257), dict(q_stride=-256), dict(q_stride=1 << 62), dict(q_weight=3 * FAKE + 2),
            dict(inv_freq=None), dict(positions=None), dict(positions=6 * FAKE + 1), dict(pair_axis=7 * FAKE + 2),
            dict(oq=9 * FAKE), dict(oq=FAKE + 16), dict(oq=2 * FAKE), dict(ok=FAKE), dict(ok=6 * FAKE), dict(oq=5 * FAKE),
-           dict(oq=FAKE, oqs=512)]  # q's place, but rows further apart
+           dict(oq=FAKE, out_q_stride=512)]  # q's place, but rows further apart
     for kw in bad:
         assert rope_call(back, **kw) == gdn.GDN_EINVAL, kw
     if back:
@@ -136,10 +137,12 @@ def test_rope_refusals(back):
         for kw in (dict(), dict(oq=FAKE), dict(ok=2 * FAKE), dict(rotary=0, inv_freq=None, positions=None),
                    dict(q_weight=None, k_weight=None, pair_axis=None), dict(tokens=0, q=None, k=None, oq=None, ok=None),
                    # q and k in one projection's rows of 384 channels, outputs over them
-                   dict(q_stride=384, k=FAKE + 512, k_stride=384, oq=FAKE, oqs=384, ok=FAKE + 512, oks=384)):
+                   dict(q_stride=384, k=FAKE + 512, k_stride=384, oq=FAKE, out_q_stride=384, ok=FAKE + 512,
+                        out_k_stride=384)):
             assert rope_call(back, **kw) == gdn.GDN_ECUDA, kw
     # k's output over q's part of the rows
-    assert rope_call(back, q_stride=384, k=FAKE + 512, k_stride=384, ok=FAKE + 256, oks=384) == gdn.GDN_EINVAL
+    assert rope_call(back, q_stride=384, k=FAKE + 512, k_stride=384, ok=FAKE + 256,
+                     out_k_stride=384) == gdn.GDN_EINVAL
 
 
 def test_binding_refusals():
