@@ -188,21 +188,30 @@ cudaError_t launch_group_sums(const float *x0, void *y0, const float *x1, void *
                          static_cast<float *>(y1), items, group);
 }
 
+// Microseconds of a chunk (bf16: 128 rows, f32: blocks of 32) in the walk and in
+// the sum and of a CTA's start and end, as measured at 4096 and 65536 tokens.
 int segment_rows(long long total_tokens, long long num_seqs, int hv, int roles, int io_dtype) {
-    constexpr int kSms = 152;
-    const int unit = io_dtype == GDN_DT_BF16 ? 128 : 32;
-    const long long slots = io_dtype == GDN_DT_BF16 ? kSms : 2 * kSms;
-    const double walk = io_dtype == GDN_DT_BF16 ? 2.8 : 4.0, sum = io_dtype == GDN_DT_BF16 ? 1.3 : 2.0, start = io_dtype == GDN_DT_BF16 ? 14.0 : 5.0;
+    const bool tc = io_dtype == GDN_DT_BF16;
+    const int unit = tc ? 128 : 32;
+    const double slots = tc ? 152 : 2 * 152, walk = tc ? 2.8 : 3.6, sum = tc ? 1.3 : 2.0, start = tc ? 14.0 : 5.0;
     const long long units = (total_tokens + unit - 1) / unit;
+    const double heads = double(hv) * roles;
+    auto waves = [&](double items) { return ceil(items / slots); };
     long long best = 1;
     double least = 0;
     for (long long u = 1;; u = u < 16 ? u + 1 : u + u / 8) {
         if (u > units && u > 1) u = units;
-        const long long items = ((units + u - 1) / u + num_seqs - 1) * hv * roles;
-        const double waves = double((items + slots - 1) / slots);
-        const double t = waves * (start + double(u) * (u < units ? walk + sum : walk));
+        const double t = waves(double((units + u - 1) / u + num_seqs - 1) * heads) * (start + double(u) * (u < units ? walk + sum : walk));
         if (u == 1 || t < least) least = t, best = u;
         if (u >= units || u * unit >= 65536) break;
+    }
+    // Several sequences (their lengths are on the device): segments of twice the mean length leave most of them whole,
+    // and those need no sums. Lengths that differ cost a quarter where CTAs take several, half where they take one.
+    if (num_seqs > 1) {
+        const double mean = double(units) / double(num_seqs), items = double(num_seqs) * heads;
+        const double whole = items > slots ? 1.25 * items / slots * (start + mean * walk) : start + 1.5 * mean * walk;
+        const long long u = (2 * units + num_seqs - 1) / num_seqs;
+        if (whole < least && u > 0 && u * unit < 65536) best = u;
     }
     return int(best * unit);
 }

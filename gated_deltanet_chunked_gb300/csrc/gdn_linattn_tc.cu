@@ -201,14 +201,14 @@ __device__ __forceinline__ void mma_parts(uint32_t sum, uint32_t part, uint32_t 
 // ---------------------------------------------------------------------------
 // Sum of one segment: states[seg] = sum_j lambda^(distance to the segment's
 // end that the walk leaves by) b_j^T c_j, accumulated in tensor memory over
-// all chunks. 8 warps split B, one copies, one issues the products.
+// all chunks. 16 warps split B (32 rows each group of four), one copies, one issues the products.
 // ---------------------------------------------------------------------------
-constexpr int kSumThreads = 320;
+constexpr int kSumThreads = 576, kSumSplit = 16;  // warps that split B
 constexpr uint32_t kSumParts = 128;  // tensor-memory columns of the parts: 3 sets of 4 x 32
 
 struct SumShared {
     uint8_t b[3][kTile], c[3][kTile];
-    uint32_t w[8][3][32];  // decays of a warp's rows
+    uint32_t w[kSumSplit][3][16];  // decays of a warp's rows
     float tab[kC + 4];
     uint64_t b_full[3], b_free[3], c_full[3], c_clean[3], c_free[3], part_full[3], part_free[3], done;
     uint32_t tmem;
@@ -225,14 +225,14 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
     next_may_start();
     const float decay = p.decay[it.h];
     if (tid <= kC) s.tab[tid] = power(decay, tid);
-    if (warp == 8 && lane == 0) {
+    if (warp == kSumSplit && lane == 0) {
         for (int i = 0; i < 3; ++i) {
             tc::mbar_init(&s.b_full[i], 1);
-            tc::mbar_init(&s.b_free[i], 8);
+            tc::mbar_init(&s.b_free[i], kSumSplit);
             tc::mbar_init(&s.c_full[i], 1);
-            tc::mbar_init(&s.c_clean[i], 8);
+            tc::mbar_init(&s.c_clean[i], kSumSplit);
             tc::mbar_init(&s.c_free[i], 1);
-            tc::mbar_init(&s.part_full[i], 4);
+            tc::mbar_init(&s.part_full[i], kSumSplit / 2);
             tc::mbar_init(&s.part_free[i], 1);
         }
         tc::mbar_init(&s.done, 1);
@@ -250,9 +250,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
         load_tile(s.b[u], &m.b[it.role], it.h / r.gb, seg.start + n * kC, &s.b_full[u]);
         load_tile(s.c[u], &m.c[it.role], it.h / r.gc, seg.start + n * kC, &s.c_full[u]);
     };
-    if (warp == 8 && lane == 0)
+    if (warp == kSumSplit && lane == 0)
         for (int n = 0; n < min(3, chunks); ++n) load(n);
-    if (warp == 9) {
+    if (warp == kSumSplit + 1) {
         tc::tmem_alloc(&s.tmem, 512);
         tc::tmem_relinquish();
     }
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
     // the sets of parts in turn: half `hf` of chunk n is batch 2 n + hf
     auto part_of = [&](int batch) { return kTmem + kSumParts + (batch % 3) * 128; };
 
-    if (warp == 8) {
+    if (warp == kSumSplit) {
         if (lane == 0) {
             int n = 3;
             for (; n < chunks; ++n) {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
                     tc::mbar_wait(&s.c_full[k % 3], (k / 3) & 1, kDrainNs);
                 }
         }
-    } else if (warp == 9) {
+    } else if (warp == kSumSplit + 1) {
         const bool leader = tc::elect_one();
         const uint64_t tiles = mn_major(s.c[0]);
         bool ok = true;
@@ -302,31 +302,34 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
             tc::mbar_wait(&s.done, 0, kDrainNs);
         }
     } else {
-        const int hf = warp >> 2;
+        const int hf = warp >> 3, row0 = (warp >> 2) * 32;
         bool ok = true;
         for (int n = 0; n < chunks && ok; ++n) {
             const int u = n % 3, from = n * kC, len = min(kC, seg.len - from), batch = 2 * n + hf;
             const uint32_t ph = (n / 3) & 1;
             if (len < kC) {
                 if (!(ok = wait.warp(&s.c_full[u], ph))) break;
-                zero_behind(s.c[u], len, tid);
+                if (warp < 8) zero_behind(s.c[u], len, tid);
             }
             tc::warp_arrive(&s.c_clean[u]);
             const float over = r.scale_in * power(decay, r.against ? from : seg.len - from - len);
-            const int row = 64 * hf + 2 * lane;
-            const PairDecay d = pair_decay(r.against ? make_float2(over * s.tab[row], over * s.tab[row + 1])
-                                                     : make_float2(over * s.tab[max(len - 1 - row, 0)],
-                                                                   over * s.tab[max(len - 2 - row, 0)]));
-            uint32_t(*w)[32] = s.w[warp];
+            const int row = row0 + 2 * lane;
+            uint32_t(*w)[16] = s.w[warp];
             __syncwarp();
-            w[0][lane] = d.w[0], w[1][lane] = d.w[1], w[2][lane] = d.w[2];
+            if (lane < 16) {
+                const PairDecay d = pair_decay(r.against ? make_float2(over * s.tab[row], over * s.tab[row + 1])
+                                                         : make_float2(over * s.tab[max(len - 1 - row, 0)],
+                                                                       over * s.tab[max(len - 2 - row, 0)]));
+                w[0][lane] = d.w[0], w[1][lane] = d.w[1], w[2][lane] = d.w[2];
+            }
             __syncwarp();
             if (!(ok = wait.warp(&s.b_full[u], ph))) break;
             if (batch >= 3 && !(ok = wait.warp(&s.part_free[batch % 3], (batch / 3 - 1) & 1))) break;
             tc::tc_fence_after();
 #pragma unroll 1
-            for (int t = 0; t < 4; ++t)
-                split_rows(s.b[u], 64 * hf + 16 * t, w[0] + 8 * t, w[1] + 8 * t, w[2] + 8 * t, len, part_of(batch) + 8 * t, 32);
+            for (int t = 0; t < 2; ++t)
+                split_rows(s.b[u], row0 + 16 * t, w[0] + 8 * t, w[1] + 8 * t, w[2] + 8 * t, len,
+                           part_of(batch) + (row0 & 32) / 2 + 8 * t, 32);
             tc::warp_arrive(&s.b_free[u]);
             tc::tmem_st_wait();
             tc::tc_fence_before();
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
     }
     __syncthreads();
     if (tid == 0 && s.dead) record_status(p.status, GDN_ETIMEOUT);
-    if (warp == 9) tc::tmem_dealloc(kTmem, 512);
+    if (warp == kSumSplit + 1) tc::tmem_dealloc(kTmem, 512);
 }
 
 // ---------------------------------------------------------------------------

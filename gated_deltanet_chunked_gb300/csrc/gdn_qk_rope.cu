@@ -102,6 +102,14 @@ __device__ __forceinline__ void load_lane(const float *row, int lane, int rest, 
     }
 }
 
+// the values of lane `other` of the row
+template <int Lanes, int N>
+__device__ __forceinline__ void from_lane(const float2 (&v)[N], int other, float2 (&o)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        o[i] = make_float2(__shfl_sync(0xffffffffu, v[i].x, other, Lanes), __shfl_sync(0xffffffffu, v[i].y, other, Lanes));
+}
+
 // The partner's channels of a lane's VE channels in a row of f32 values, for
 // pairs that do not lie in whole lanes: through shared memory.
 template <int VE>
@@ -159,7 +167,7 @@ template <typename T, int P, bool kBwd>
 __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid_constant__ RopeArgs a) {
     using L = Layout<T>;
     // rows a lane group has under way: 16 bytes a lane of each
-    constexpr int VE = L::kVe, R = kBwd ? 2 : 4, kWords = 4;
+    constexpr int VE = L::kVe, R = kBwd ? 2 : 4;
     using Row = vec::Pack<T, VE>;
     __shared__ __align__(16) RopeShared s;
     __shared__ __align__(16) float swap[P == kAnywhere ? L::kRows : 1][kHeadDim];
@@ -197,22 +205,31 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
         float(*turn)[kMaxTokens * kMaxPairs] = s.turn[which];  // two in turn, so that one barrier a step is enough
         int t = group / heads, h = group % heads;
         bool angles = false;
+        const T *x0[2], *d0[2];
+        T *y0[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // k's first head counts on from q's
+            const int from = ch - (k ? a.heads[0] * kHeadDim : 0);
+            x0[k] = static_cast<const T *>(a.x[k]) + t0 * a.xs[k] + from;
+            if (kBwd) d0[k] = static_cast<const T *>(a.dy[k]) + t0 * a.ds[k] + from;
+            y0[k] = static_cast<T *>(a.y[k]) + t0 * a.ys[k] + from;
+        }
         // R rows at a time; the first loads are under way while the angles are taken
         for (int r0 = 0; r0 < step * heads; r0 += R * L::kRows) {
             Row x[R], d[kBwd ? R : 1];
-            int token[R], w[R];
-            long long at[R];
+            int token[R];
+            bool w[R];
+            T *to[R];
 #pragma unroll
             for (int k = 0; k < R; ++k) {
                 token[k] = t;
                 w[k] = h >= a.heads[0];
-                const int head = (w[k] ? h - a.heads[0] : h) * kHeadDim + ch;
-                at[k] = (t0 + t) * a.ys[w[k]] + head;
+                to[k] = (w[k] ? y0[1] : y0[0]) + t * (w[k] ? a.ys[1] : a.ys[0]) + h * kHeadDim;
                 x[k].zero();
                 if (kBwd) d[k].zero();
                 if (t < step) {
-                    x[k].load(static_cast<const T *>(a.x[w[k]]) + (t0 + t) * a.xs[w[k]] + head);
-                    if (kBwd) d[k].load(static_cast<const T *>(a.dy[w[k]]) + (t0 + t) * a.ds[w[k]] + head);
+                    x[k].load((w[k] ? x0[1] : x0[0]) + t * (w[k] ? a.xs[1] : a.xs[0]) + h * kHeadDim);
+                    if (kBwd) d[k].load((w[k] ? d0[1] : d0[0]) + t * (w[k] ? a.ds[1] : a.ds[0]) + h * kHeadDim);
                 }
                 t += next_t, h += next_h;
                 if (h >= heads) h -= heads, ++t;
@@ -243,20 +260,9 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
                 }
                 if constexpr (!kBwd) {
                     const float2 r = both(rsqrtf(vec::group_sum<L::kLanesOfRow>(vec::sum2(ss)) * (1.f / kHeadDim) + a.eps));
-                    if constexpr (P == kLanes) {
-                        // the partner lane's channels come as they lie in memory, and take their weights here
-                        Row p;
-                        float2 wo[VE / 2];
-                        load_lane<VE>(weight, other, kHeadDim / 2, wo);
-                        const uint32_t *from = reinterpret_cast<const uint32_t *>(&x[k]);
-                        uint32_t *into = reinterpret_cast<uint32_t *>(&p);
-#pragma unroll
-                        for (int i = 0; i < kWords; ++i) into[i] = __shfl_sync(0xffffffffu, from[i], other, L::kLanesOfRow);
-#pragma unroll
-                        for (int i = 0; i < VE / 2; ++i) o[i] = mul2(mul2(p.f2(i), r), wo[i]);
-                    }
 #pragma unroll
                     for (int i = 0; i < VE / 2; ++i) v[i] = mul2(mul2(v[i], r), wt[i]);
+                    if constexpr (P == kLanes) from_lane<L::kLanesOfRow>(v, other, o);
                     if constexpr (P == kAnywhere) partners<VE>(swap[group], ch, a.pairs, v, o);
                     rotate<VE, P, false>(co, si, minus, lane, a.pairs, v, o);
 #pragma unroll
@@ -265,15 +271,7 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
                     float2 n[VE / 2];
 #pragma unroll
                     for (int i = 0; i < VE / 2; ++i) n[i] = d[k].f2(i);
-                    if constexpr (P == kLanes) {
-                        Row p;
-                        const uint32_t *from = reinterpret_cast<const uint32_t *>(&d[k]);
-                        uint32_t *into = reinterpret_cast<uint32_t *>(&p);
-#pragma unroll
-                        for (int i = 0; i < kWords; ++i) into[i] = __shfl_sync(0xffffffffu, from[i], other, L::kLanesOfRow);
-#pragma unroll
-                        for (int i = 0; i < VE / 2; ++i) o[i] = p.f2(i);
-                    }
+                    if constexpr (P == kLanes) from_lane<L::kLanesOfRow>(n, other, o);
                     if constexpr (P == kAnywhere) partners<VE>(swap[group], ch, a.pairs, n, o);
                     rotate<VE, P, true>(co, si, minus, lane, a.pairs, n, o);
                     float2 u[VE / 2], ux = both(0.f);
@@ -295,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) k_qk_rope(const __grid
                         }
                     }
                 }
-                if (has) x[k].store(static_cast<T *>(a.y[w[k]]) + at[k]);
+                if (has) x[k].store(to[k]);
             }
         }
     }
@@ -324,12 +322,20 @@ int ctas_of(long long tokens, int step, bool bwd) {
     return int(steps < most ? steps : most);
 }
 
-// Tokens of a CTA's step: eight rows for each of its lane groups (angles and a
-// barrier come once a step), fewer where that would leave SMs without work.
+// Tokens of a CTA's step (angles and a barrier come once a step): those whose
+// rows fill the lane groups best, four at a time, but not so many that SMs are
+// without work.
 int step_of(long long tokens, int heads, int io_dtype) {
-    const int rows = 8 * (io_dtype == GDN_DT_BF16 ? Layout<__nv_bfloat16>::kRows : Layout<float>::kRows);
-    const long long most = tokens / (kSms * 4), n = rows / heads < most ? rows / heads : most;
-    return int(n < 1 ? 1 : n > kMaxTokens ? kMaxTokens : n);
+    const int at_once = 4 * (io_dtype == GDN_DT_BF16 ? Layout<__nv_bfloat16>::kRows : Layout<float>::kRows);
+    const long long most = tokens / (kSms * 4) < kMaxTokens ? tokens / (kSms * 4) : kMaxTokens;
+    int best = 1;
+    double full = 0;
+    for (int n = 1; n <= most; ++n) {
+        const long long rows = (long long)n * heads;
+        const double f = double(rows) / double((rows + at_once - 1) / at_once * at_once);
+        if (f > full + 0.02) full = f, best = n;
+    }
+    return best;
 }
 
 template <typename T, bool kBwd>
