@@ -468,7 +468,9 @@ size_t gdn_gated_rmsnorm_bwd_workspace_size(const gdn_problem *p);
  * States and sums are f32, decays powers taken from their exponent. bf16: the
  * decayed scores inside a chunk of 128 tokens and the state in the product
  * with q are rounded to bf16, as out is; final_state is not rounded on its way
- * (what is added to a state is exact to 2^-24). Infinities and NaN stay in
+ * (what is added to a state is exact to 2^-24); where a decay from a chunk's
+ * start to a token is below 2^-64, it counts as 2^-64 in the product of q with
+ * the state, and scores q k above 2^63 overflow there. Infinities and NaN stay in
  * their sequence and value heads (with bf16 they reach tokens up to 127 places
  * before their own). (The bf16 kernels wait for copies and products, at most 2 s
  * a wait: GDN_ETIMEOUT in the device status.) */
@@ -633,7 +635,9 @@ const char *gdn_kernel_name(int kernel);
 /* Sets, process-wide, the limit of every bounded device-side wait in the
  * kernels launched after the call (the tensor-core prefill kernel's copy, MMA
  * and ready-flag waits; the recurrence's waits on copies and on the other CTAs
- * of a cluster; the layer norm's on the other CTA of a pair), in nanoseconds of wall time; 0 restores the default of 2 s. A
+ * of a cluster; the layer norm's on the other CTA of a pair; linear attention's
+ * on copies and products, counted in cycles of which there is more than one a
+ * nanosecond), in nanoseconds of wall time; 0 restores the default of 2 s. A
  * wait that runs out records GDN_ETIMEOUT in the device status word; the kernel
  * then drains what it has in flight (copies, MMAs and stores between CTAs, each
  * drain bounded too), frees its tensor memory and returns, so the context stays
