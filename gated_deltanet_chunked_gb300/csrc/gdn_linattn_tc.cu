@@ -512,13 +512,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
         } else if (warp == 22 && lane == 0) {  // finished chunks out, and their C's place back
             for (int n = 0; n < chunks; ++n) {
                 if (!wait.one(&s.staged, n & 1)) break;
-                if (chunk_len(n) == kC && !r.partial) {
-                    for (int half = 0; half < 2; ++half)
-                        tc::tma_store_3d(&m.o[it.role], half * 64, it.h, seg.start + chunk_from(n), s.c[n & 1] + half * kHalf);
+                if (chunk_len(n) == kC) {
+                    const int boxes = r.partial ? 4 : 2;  // of 128 bytes a row
+                    for (int q = 0; q < boxes; ++q)
+                        tc::tma_store_3d(&m.o[it.role], q * 64, it.h, row_of(n), (q < 2 ? s.c : s.a)[n & 1] + (q & 1) * kHalf);
                     tc::bulk_commit_group();
                     tc::bulk_wait_group_read<0>();
                 }
                 tc::mbar_arrive(&s.c_free[n & 1]);
+                if (r.partial) tc::mbar_arrive(&s.a_free[n & 1]);
             }
             tc::bulk_wait_group_all();
         } else if (warp == 21 && chunks > 0) {
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
 #pragma unroll
                     for (int k = 0; k < 8; ++k) tc::mma_bf16(kTmem + kColOut, a + k_step(k), st + mn_step(k), kIdKM, k > 0);
                     tc::mma_commit(&s.state_free);
-                    tc::mma_commit(&s.a_free[n & 1]);
+                    if (!r.partial) tc::mma_commit(&s.a_free[n & 1]);
                 }
                 if (!(ok = wait.poll(&s.scores_full, ph))) break;
                 tc::tc_fence_after();
@@ -732,9 +734,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
                 const size_t at_out = (size_t(from + row) * p.hv + it.h) * kHeadDim + c0;
                 if (!(ok = wait.warp(&s.out_full, before))) break;
                 tc::tc_fence_after();
-                // a whole chunk's rows go through the place of its C, and out by one copy
-                const bool staged = len == kC && !r.partial;
-                uint8_t *stage = s.c[c & 1] + half * kHalf;
+                // a whole chunk's rows go through the place of its C (f32 ones' second half through that of its A), and
+                // out by copies
+                const bool staged = len == kC;
+                uint8_t *stage = r.partial ? (half ? s.a : s.c)[c & 1] : s.c[c & 1] + half * kHalf;
 #pragma unroll 1
                 for (int x = 0; x < 64; x += 16) {
                     float v[16];
@@ -752,8 +755,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
                         else w[k] = pack2(y.x, y.y);
                     }
                     if (staged) {
-                        *reinterpret_cast<uint4 *>(at(stage, row, x / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4 *>(at(stage, row, x / 8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+                        uint8_t *box = r.partial ? stage + (x >> 5) * kHalf : stage;
+                        const int g = r.partial ? (x & 31) / 4 : x / 8;
+                        *reinterpret_cast<uint4 *>(at(box, row, g)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(at(box, row, g + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+                        if (r.partial) {
+                            *reinterpret_cast<uint4 *>(at(box, row, g + 2)) = make_uint4(w[8], w[9], w[10], w[11]);
+                            *reinterpret_cast<uint4 *>(at(box, row, g + 3)) = make_uint4(w[12], w[13], w[14], w[15]);
+                        }
                     } else if (row < len) {
                         if (r.partial) {
                             float *to = static_cast<float *>(r.out) + at_out + x;
@@ -796,8 +805,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
     if (warp == 21) tc::tmem_dealloc(kTmem, 512);
 }
 
-bool tile_map(CUtensorMap *map, const void *base, int heads, int tokens) {
-    return make_tmap_bf16_3d(map, base, 128, uint64_t(heads), uint64_t(tokens), 256, uint64_t(heads) * 256, 64, 1, kC);
+// Boxes of 128 rows and 64 bf16 of a head (of f32 rows, `wide` 2, 32 elements as pairs of bf16: copies only)
+bool tile_map(CUtensorMap *map, const void *base, int heads, int tokens, int wide = 1) {
+    const uint64_t row = 256 * uint64_t(wide);
+    return make_tmap_bf16_3d(map, base, 128 * wide, uint64_t(heads), uint64_t(tokens), row, uint64_t(heads) * row, 64, 1, kC);
 }
 
 }  // namespace
@@ -812,7 +823,7 @@ cudaError_t launch_tc(const Args &args, cudaStream_t s) {
             const Role &r = a.role[i];
             if (!tile_map(&m.a[i], r.a, a.hv / r.ga, a.total_tokens) || !tile_map(&m.b[i], r.b, a.hv / r.gb, a.total_tokens) ||
                 !tile_map(&m.c[i], r.c, a.hv / r.gc, a.total_tokens) ||
-                (!r.partial && !tile_map(&m.o[i], r.out, a.hv, a.total_tokens)))
+                !tile_map(&m.o[i], r.out, a.hv, a.total_tokens, r.partial ? 2 : 1))
                 return cudaErrorInvalidValue;
         }
     constexpr int kSumBytes = sizeof(SumShared), kWalkBytes = sizeof(WalkShared);
