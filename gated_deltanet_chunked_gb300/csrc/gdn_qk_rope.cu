@@ -6,9 +6,14 @@
 // Backward, with dn the gradient turned back, xhat = x r, u = dn weight:
 //   dx = r (u - xhat mean(u xhat)),  dweight = sum over rows of dn xhat.
 //
-// Bound by memory: each row is read and written once, 16 bytes a lane. A CTA
-// takes the rows of a few tokens at a time and has their angles' sines and
-// cosines in shared memory, once for all heads of a token.
+// Each row is read and written once, 16 bytes a lane. A CTA takes the rows of a
+// few tokens at a time and has their angles' sines and cosines in shared memory,
+// once for all heads of a token. Bound by issue slots: 65536 tokens of 32 + 4
+// heads, bf16, take 257 us (1.21 GB: 4.7 TB/s, 0.69 of the measured copy rate),
+// 4096 tokens of 16 + 16 heads 19 us and 31 backward (0.52 and 0.48). What made
+// it faster: values in an order without bank conflicts and no division a row (35
+// -> 24 us), a partner's channels by shuffles after the norm, not before (24 ->
+// 23), steps whose rows fill the lane groups (36 heads: 336 -> 272 us).
 //
 // Angles. A position has up to 31 bits and t is wanted to 2^-24 of a turn:
 // frequency / 2 pi is held in three f32, the position in two whole f32, and the
