@@ -56,7 +56,7 @@ __device__ __forceinline__ bool segment_of(const Args &p, uint32_t smem, Item &i
 // Bounded waits: one that runs out marks the CTA, and every other wait of it
 // ends then. The limit is one of cycles, of which there is more than one a
 // nanosecond: little code, since the roles' loops have to stay in the
-// instruction cache together (with 77 KB of code the walk took a fifth longer).
+// instruction cache together (521 us of walk with 77 KB of code, 436 with 58).
 // The warp that issues the products polls; the many that wait for it suspend,
 // which leaves the issue slots to those at work (5% of the walk).
 struct Waiter {
@@ -376,11 +376,11 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
 // What bounds a chunk is shared memory as much as the products: 56 products of
 // 128 x 128 x 16 take 67 cycles each, an operand in shared memory is 4 KiB of
 // its 128 bytes a cycle, and both operands there would fill it. So the parts of
-// B and the scores are operands in tensor memory (with B's parts in shared
-// memory a chunk took 4.7 us). Descriptors are in uniform registers: products
+// B and the scores are operands in tensor memory (for B's parts alone that gave
+// nothing, 535 and 534 us of walk, while other steps bound it). Descriptors are in uniform registers: products
 // under `lane == 0` instead of an elected lane cost 8%.
-// Measured: 375 us at 65536 tokens x 32 heads (1.6 GB of its own at 4.3 TB/s),
-// 37 us at 4096: 3.4 us a chunk and SM, 1.94 of it products. The rest is the
+// Measured: 375 to 385 us at 65536 tokens x 32 heads (1.6 GB of its own at
+// 4.2 TB/s), 37 us at 4096: 3.5 us a chunk and SM, 1.94 of it products. The rest is the
 // latency of about ten hand-offs a chunk (250 to 600 cycles each) around P ->
 // scores -> intra -> output. Tried and left: a second issuing warp for the sums,
 // and warps of their own for the output (375 -> 390 to 424 us: as many again

@@ -10,7 +10,7 @@
 // few tokens at a time and has their angles' sines and cosines in shared memory,
 // once for all heads of a token. Bound by issue slots: 65536 tokens of 32 + 4
 // heads, bf16, take 257 us (1.21 GB: 4.7 TB/s, 0.69 of the measured copy rate),
-// 4096 tokens of 16 + 16 heads 19 us and 31 backward (0.52 and 0.48). What made
+// 4096 tokens of 16 + 16 heads 21 us and 35 backward with the sums (0.46 and 0.43). What made
 // it faster: values in an order without bank conflicts and no division a row (35
 // -> 24 us), a partner's channels by shuffles after the norm, not before (24 ->
 // 23), steps whose rows fill the lane groups (36 heads: 336 -> 272 us).
