@@ -768,7 +768,8 @@ int gdn_linear_attention_bwd(const gdn_problem *p, const void *dout, const void 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_linattn(p, a, s);
     if (e == cudaSuccess && g > 1)
-        e = la::launch_group_sums(parts[0], dq, parts[1], dk, p->total_tokens, p->hq, g, p->io_dtype, s);
+        e = la::launch_group_sums(parts[0], dq, parts[1], dk, p->total_tokens, p->hq, g, a.n_segs, p->io_dtype,
+                                  s);
     return cuda_status(e);
 }
 

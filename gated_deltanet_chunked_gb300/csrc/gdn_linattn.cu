@@ -141,13 +141,14 @@ __global__ void __launch_bounds__(kChainThreads) k_la_chain(const __grid_constan
     }
 }
 
-// y[t, hq] = sum over the group's heads of x[t, hv], in their order, rounded once; of two tensors. Bound by memory: 25 us
-// for 4096 tokens x 32 heads on 16 (168 MB, 6.7 TB/s).
+// y[t, hq] = sum over the group's heads of x[t, hv], in their order, rounded once; of two tensors; nothing after a failed
+// check, whose x nobody wrote. Bound by memory: 25 us for 4096 tokens x 32 heads on 16 (168 MB, 6.7 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256) k_la_group_sums(const float *__restrict__ x0, T *__restrict__ y0,
                                                        const float *__restrict__ x1, T *__restrict__ y1, long long items,
-                                                       int group) {
+                                                       int group, const int *n_segs) {
     wait_for_previous();
+    if (*n_segs == 0) return;
     const float *x = blockIdx.y ? x1 : x0;
     T *y = blockIdx.y ? y1 : y0;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // four channels of a (token, query head)
@@ -180,16 +181,16 @@ cudaError_t launch_chain(const Args &a, cudaStream_t s) {
 }
 
 cudaError_t launch_group_sums(const float *x0, void *y0, const float *x1, void *y1, long long rows, int heads, int group,
-                              int io_dtype, cudaStream_t s) {
+                              const int *n_segs, int io_dtype, cudaStream_t s) {
     const long long items = rows * heads * 32;
     if (items == 0) return cudaSuccess;
     LaunchScope scope(GDN_K_LINATTN_GROUP_SUM, s);
     const dim3 ctas(unsigned((items + 255) / 256), 2);
     if (io_dtype == GDN_DT_BF16)
         return launch_behind(k_la_group_sums<__nv_bfloat16>, ctas, 256, 0, s, x0, static_cast<__nv_bfloat16 *>(y0), x1,
-                             static_cast<__nv_bfloat16 *>(y1), items, group);
+                             static_cast<__nv_bfloat16 *>(y1), items, group, n_segs);
     return launch_behind(k_la_group_sums<float>, ctas, 256, 0, s, x0, static_cast<float *>(y0), x1,
-                         static_cast<float *>(y1), items, group);
+                         static_cast<float *>(y1), items, group, n_segs);
 }
 
 // Microseconds of a chunk (bf16: 128 rows, f32: blocks of 32) in the walk and in

@@ -98,7 +98,7 @@ cudaError_t launch_simt(const Args &a, cudaStream_t s);
 cudaError_t launch_table(const Args &a, cudaStream_t s);
 cudaError_t launch_chain(const Args &a, cudaStream_t s);
 cudaError_t launch_group_sums(const float *x0, void *y0, const float *x1, void *y1, long long rows, int heads, int group,
-                              int io_dtype, cudaStream_t s);
+                              const int *n_segs, int io_dtype, cudaStream_t s);
 // rows a segment may have: those with the least estimated time
 int segment_rows(long long total_tokens, long long num_seqs, int hv, int roles, int io_dtype);
 

@@ -165,8 +165,24 @@ def test_bad_offsets_write_nothing(cuda, dtype, bad):
     gdn.gdn_linear_attention_bwd(d["dout"], d["q"], d["k"], d["v"], d["decay"], SCALE, cu_seqlens=d["cu"], dq=grads[0],
                                  dk=grads[1], dv=grads[2])
     assert gdn.gdn_get_device_status() == gdn.GDN_EDEVICE_INPUT
-    if d["q"].shape[1] == d["v"].shape[1]:
-        assert all((x == 3).all() for x in grads)
+    assert all((x == 3).all() for x in grads)
+
+
+@DTYPES
+@pytest.mark.parametrize("hq,hv", [(2, 2), (1, 2), (2, 6)])
+@pytest.mark.parametrize("bad", [[0, 150, 100], [0, 100, 199]])
+def test_bad_offsets_leave_gradients(cuda, dtype, hq, hv, bad):
+    """With and without sums over a group's heads, whatever the workspace holds."""
+    d = to(make(23, [100, 100], hq, hv, dtype, True), cuda)
+    d["cu"] = torch.tensor(bad, dtype=torch.int32, device=cuda)
+    grads = [torch.full_like(d[k], 3.0) for k in ("q", "k", "v", "s0")]
+    workspace = torch.zeros(1 << 24, dtype=torch.uint8, device=cuda)
+    gdn.gdn_linear_attention_bwd(d["dout"], d["q"], d["k"], d["v"], d["decay"], SCALE, initial_state=d["s0"],
+                                 cu_seqlens=d["cu"], dfinal_state=d["dfinal"], dq=grads[0], dk=grads[1], dv=grads[2],
+                                 dinitial_state=grads[3], workspace=workspace)
+    assert gdn.gdn_get_device_status() == gdn.GDN_EDEVICE_INPUT
+    for name, x in zip(("dq", "dk", "dv", "dinitial_state"), grads):
+        assert (x == 3).all(), name
 
 
 @DTYPES
