@@ -561,7 +561,9 @@ int gdn_qk_norm_rope(const gdn_qk_rope *r, const void *q, const void *k, const f
  *   workspace     gdn_qk_norm_rope_bwd_workspace_size(r) bytes, 256-byte
  *                 aligned; may be NULL when both are. Calls that share it must
  *                 be ordered on one stream.
- * The sums over rows are taken in a fixed order. */
+ * The sums over rows are taken in a fixed order. After an axis outside 0 ..
+ * axes - 1 (GDN_EDEVICE_INPUT) dq and dk are not written, and the weights'
+ * gradients are zeros. */
 int gdn_qk_norm_rope_bwd(const gdn_qk_rope *r, const void *dout_q, const void *dout_k, const void *q, const void *k,
                          const float *q_weight, const float *k_weight, const float *inv_freq, const int32_t *positions,
                          const int32_t *pair_axis, void *dq, void *dk, float *dq_weight, float *dk_weight,

@@ -138,6 +138,31 @@ def test_bad_axis_writes_nothing(cuda):
         assert all((x == 2).all() for x in out)
 
 
+def test_bad_axis_backward(cuda):
+    """dq and dk stay as they were, and the weights' gradients are zeros whatever the workspace holds."""
+    c = to(make(9, 70, 2, 2, BF16, 128, axes=3), cuda, 2)
+    axis = c["axis"].clone()
+    axis[40] = 3
+    out = [torch.full_like(c[k], 2.0) for k in ("dq", "dk")]
+    ws = torch.full((1 << 20,), 63, dtype=torch.uint8, device=cuda)
+    g = gdn.gdn_qk_norm_rope_bwd(c["dq"], c["dk"], *args(c), pair_axis=axis, dq=out[0], dk=out[1], workspace=ws)
+    assert gdn.gdn_get_device_status() == gdn.GDN_EDEVICE_INPUT
+    assert all((x == 2).all() for x in out) and (g[2] == 0).all() and (g[3] == 0).all()
+
+
+def test_one_weight_gradient(cuda):
+    """Either weight's gradient without the other is the one of both."""
+    c = to(make(11, 300, 3, 2, BF16, 128), cuda, 2)
+    both = gdn.gdn_qk_norm_rope_bwd(c["dq"], c["dk"], *args(c), eps=EPS)
+    for i, name in ((2, "dq_weight"), (3, "dk_weight")):
+        w = torch.full((128,), 5.0, device=cuda)
+        g = gdn.gdn_qk_norm_rope_bwd(c["dq"], c["dk"], *args(c), eps=EPS, need_dweight=False, **{name: w})
+        assert torch.equal(w, both[i]) and torch.equal(g[0], both[0]) and torch.equal(g[1], both[1])
+        assert g[5 - i] is None
+    g = gdn.gdn_qk_norm_rope_bwd(c["dq"], c["dk"], *args(c), eps=EPS, need_dweight=False)
+    assert torch.equal(g[0], both[0]) and torch.equal(g[1], both[1]) and g[2] is None and g[3] is None
+
+
 def test_infinities_stay_in_their_row(cuda):
     c = to(make(10, 40, 3, 2, BF16, 128), cuda, 3)
     ref = run(c, False)
