@@ -253,8 +253,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
         load_tile(s.b[u], &m.b[it.role], it.h / r.gb, seg.start + n * kC, &s.b_full[u]);
         load_tile(s.c[u], &m.c[it.role], it.h / r.gc, seg.start + n * kC, &s.c_full[u]);
     };
+    int asked = 0;  // chunks whose tiles the copying thread has asked for
     if (warp == kSumSplit && lane == 0)
-        for (int n = 0; n < min(3, chunks); ++n) load(n);
+        for (; asked < min(3, chunks); ++asked) load(asked);
     if (warp == kSumSplit + 1) {
         tc::tmem_alloc(&s.tmem, 512);
         tc::tmem_relinquish();
@@ -268,17 +269,11 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
 
     if (warp == kSumSplit) {
         if (lane == 0) {
-            int n = 3;
-            for (; n < chunks; ++n) {
-                const uint32_t ph = (n / 3 - 1) & 1;
-                if (!wait.one(&s.b_free[n % 3], ph) || !wait.one(&s.c_free[n % 3], ph)) break;
-                load(n);
+            for (; asked < chunks; ++asked) {
+                const uint32_t ph = (asked / 3 - 1) & 1;
+                if (!wait.one(&s.b_free[asked % 3], ph) || !wait.one(&s.c_free[asked % 3], ph)) break;
+                load(asked);
             }
-            if (s.dead)  // what is on its way has to land before the CTA ends
-                for (int k = max(0, min(n, chunks) - 3); k < min(n, chunks); ++k) {
-                    tc::mbar_wait(&s.b_full[k % 3], (k / 3) & 1, kDrainNs);
-                    tc::mbar_wait(&s.c_full[k % 3], (k / 3) & 1, kDrainNs);
-                }
         }
     } else if (warp == kSumSplit + 1) {
         const bool leader = tc::elect_one();
@@ -359,6 +354,12 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
     }
     __syncthreads();
     if (tid == 0 && s.dead) record_status(p.status, GDN_ETIMEOUT);
+    if (warp == kSumSplit && lane == 0 && s.dead)
+        // tiles on their way have to land before the CTA ends, whichever warp gave up (behind the barrier: none will)
+        for (int k = max(0, asked - 3); k < asked; ++k) {
+            tc::mbar_wait(&s.b_full[k % 3], (k / 3) & 1, kDrainNs);
+            tc::mbar_wait(&s.c_full[k % 3], (k / 3) & 1, kDrainNs);
+        }
     if (warp == kSumSplit + 1) tc::tmem_dealloc(kTmem, 512);
 }
 
@@ -478,8 +479,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
         prefetch_tile(&m.a[it.role], it.h / r.ga, row_of(n));
         prefetch_tile(&m.c[it.role], it.h / r.gc, row_of(n));
     };
+    int na = min(2, chunks), nc = na;  // chunks whose A and B, and whose C the copying thread has asked for
     if (warp == 20 && lane == 0) {
-        for (int n = 0; n < min(2, chunks); ++n) load_b(n), load_a(n), load_c(n);
+        for (int n = 0; n < na; ++n) load_b(n), load_a(n), load_c(n);
         prefetch(2);
     }
     if (tid >= 256 && tid < 256 + kC) {  // B's decays, of a whole chunk and of the one that ends the segment
@@ -506,7 +508,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
     if (warp >= 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 20 && lane == 0) {
-            int na = min(2, chunks), nc = na;  // tiles asked for
             for (int n = 2; n < chunks; ++n) {
                 const int u = n & 1;
                 const uint32_t ph = ((n >> 1) - 1) & 1;
@@ -515,10 +516,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
                 prefetch(n + 1);
                 if (!wait.one(&s.c_free[u], ph)) break;
                 load_c(n), ++nc;
-            }
-            if (s.dead) {  // what is on its way has to land before the CTA ends
-                for (int k = max(0, na - 2); k < na; ++k) tc::mbar_wait(&s.ab_full[k & 1], (k >> 1) & 1, kDrainNs);
-                for (int k = max(0, nc - 2); k < nc; ++k) tc::mbar_wait(&s.c_full[k & 1], (k >> 1) & 1, kDrainNs);
             }
         } else if (warp == 22 && lane == 0) {  // finished chunks out, and their C's place back
             for (int n = 0; n < chunks; ++n) {
@@ -813,6 +810,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
     tc::tc_fence_before();
     __syncthreads();
     if (tid == 0 && s.dead) record_status(p.status, GDN_ETIMEOUT);
+    if (warp == 20 && lane == 0 && s.dead) {
+        // tiles on their way have to land before the CTA ends, whichever warp gave up (behind the barrier: none will)
+        for (int k = max(0, na - 2); k < na; ++k) tc::mbar_wait(&s.ab_full[k & 1], (k >> 1) & 1, kDrainNs);
+        for (int k = max(0, nc - 2); k < nc; ++k) tc::mbar_wait(&s.c_full[k & 1], (k >> 1) & 1, kDrainNs);
+    }
     if (warp == 21) tc::tmem_dealloc(kTmem, 512);
 }
 
