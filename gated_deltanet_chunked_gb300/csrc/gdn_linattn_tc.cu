@@ -396,7 +396,7 @@ struct WalkShared {
     float between[2 * kC];  // [128 + d]: lambda^|d|, d from -128 to 127
     uint32_t w[2][3][kC / 2];  // decays of B's rows, of a whole chunk and of the sequence's last one
     uint64_t ab_full[2], c_full[2], a_free[2], b_free[2], c_clean, c_free[2], part_full[4], part_free[4], p_full,
-        scores_full, sum_full, sum_free, state_full, state_free, out_full, out_free, staged, drain;
+        scores_full, sum_full, sum_free, state_full, state_free, out_full, out_free, staged[2], drain;
     uint32_t tmem;
     int dead;
 };
@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
             tc::mbar_init(&s.a_free[i], 1);
             tc::mbar_init(&s.b_free[i], 9);
             tc::mbar_init(&s.c_free[i], 1);
+            tc::mbar_init(&s.staged[i], 8);
         }
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(&s.part_full[i], 4);
@@ -447,7 +448,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
         tc::mbar_init(&s.state_free, 1);
         tc::mbar_init(&s.out_full, 1);
         tc::mbar_init(&s.out_free, 8);
-        tc::mbar_init(&s.staged, 8);
         tc::mbar_init(&s.c_clean, 8);
         tc::mbar_init(&s.drain, 1);
         s.dead = 0;
@@ -518,8 +518,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
                 load_c(n), ++nc;
             }
         } else if (warp == 22 && lane == 0) {  // finished chunks out, and their C's place back
+            // (of the two barriers the one of chunk n is not arrived at again before C's place is: chunk n + 2 needs it)
             for (int n = 0; n < chunks; ++n) {
-                if (!wait.one(&s.staged, n & 1)) break;
+                if (!wait.one(&s.staged[n & 1], (n >> 1) & 1)) break;
                 if (chunk_len(n) == kC) {
                     const int boxes = r.partial ? 4 : 2;  // of 128 bytes a row
                     for (int q = 0; q < boxes; ++q)
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
                     }
                 }
                 if (staged) tc::fence_proxy_async_smem();
-                tc::warp_arrive(&s.staged);
+                tc::warp_arrive(&s.staged[c & 1]);
             }
         }
         if (leaves && ok) {
