@@ -11,6 +11,8 @@
 // Bound by the FMA units and by the loads from shared memory that feed them:
 // about 3.6 us a block and CTA with two CTAs on an SM, 29 us for 200 tokens x 2
 // heads with all four kernels (with the state by 4-byte loads 45).
+#include <type_traits>
+
 #include "gdn_linattn.cuh"
 
 namespace gdn {
@@ -146,8 +148,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_la_simt(const __grid_constant__
                 x0[k] = vec::mul2(vec::both(f), x0[k]);
                 x1[k] = vec::mul2(vec::both(f), x1[k]);
             }
-#pragma unroll 2
-            for (int j = 0; j < kB; j += 4) {
+            // Rows of c that a row's sum has, and no other: a score of 0 times an infinity or NaN is no number. Beside the
+            // warp's own four, which see a part of one another, they are the same for all four.
+            auto add = [&](int j, auto own) {
                 float4 y[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) y[q] = *reinterpret_cast<const float4 *>(&s.c[j + q][4 * lane]);
@@ -157,11 +160,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_la_simt(const __grid_constant__
                     const float f[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
+                        if (own && (r.against ? q < k : q > k)) continue;
                         x0[k] = vec::fma2(vec::both(f[q]), lo2(y[q]), x0[k]);
                         x1[k] = vec::fma2(vec::both(f[q]), hi2(y[q]), x1[k]);
                     }
                 }
-            }
+            };
+            const int own4 = 4 * warp;
+            if (r.against) add(own4, std::true_type{});
+#pragma unroll 2
+            for (int j = r.against ? own4 + 4 : 0; j < (r.against ? kB : own4); j += 4) add(j, std::false_type{});
+            if (!r.against) add(own4, std::true_type{});
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int i = 4 * warp + k;

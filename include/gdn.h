@@ -471,9 +471,11 @@ size_t gdn_gated_rmsnorm_bwd_workspace_size(const gdn_problem *p);
  * (what is added to a state is exact to 2^-24); where a decay from a chunk's
  * start to a token is below 2^-64, it counts as 2^-64 in the product of q with
  * the state, and scores q k above 2^63 overflow there. Infinities and NaN stay in
- * their sequence and value heads (with bf16 they reach tokens up to 127 places
- * before their own). (The bf16 kernels wait for copies and products, at most 2 s
- * a wait: GDN_ETIMEOUT in the device status.) */
+ * their sequence and value heads, and in f32 reach only tokens whose sums they
+ * are in. With bf16 those of v also reach out up to 127 tokens before their own,
+ * and in the backward pass those of k dq as far, those of dout dv and those of q
+ * dk up to 127 tokens behind. (The bf16 kernels wait for copies and products, at
+ * most 2 s a wait: GDN_ETIMEOUT in the device status.) */
 int gdn_linear_attention(const gdn_problem *p, const void *q, const void *k, const void *v, const float *decay,
                          float scale, const float *initial_state, const int32_t *cu_seqlens, void *out,
                          float *final_state, void *workspace, size_t workspace_bytes, void *stream);
