@@ -545,8 +545,8 @@ typedef struct gdn_qk_rope {
  *   inv_freq      [rotary / 2] f32: radians per position of each pair
  *   positions     int32 [axes, tokens]
  *   pair_axis     int32 [rotary / 2], the axis that turns a pair, or NULL (axis 0)
- * The angle's error is below 2^-22 radian for every int32 position, all else
- * is f32 and rounded once. An axis outside 0 .. axes - 1 is recorded as
+ * The angle's error is below 2^-22 radian for every int32 position and
+ * frequencies up to 64, all else is f32 and rounded once. An axis outside 0 .. axes - 1 is recorded as
  * GDN_EDEVICE_INPUT and nothing is written. */
 int gdn_qk_norm_rope(const gdn_qk_rope *r, const void *q, const void *k, const float *q_weight, const float *k_weight,
                      const float *inv_freq, const int32_t *positions, const int32_t *pair_axis, void *out_q, void *out_k,
