@@ -200,20 +200,26 @@ __device__ __forceinline__ void mma_parts(uint32_t sum, uint32_t part, uint32_t 
 
 // ---------------------------------------------------------------------------
 // Sum of one segment: states[seg] = sum_j lambda^(distance to the segment's
-// end that the walk leaves by) b_j^T c_j, accumulated in tensor memory over
-// all chunks. 16 warps split B (32 rows each group of four), one copies, one issues the products.
+// end that the walk leaves by) b_j^T c_j. 16 warps split B (32 rows each group
+// of four) and add up the chunks' sums (32 columns each group), one copies, one
+// issues the products.
+// The tensor cores cut what they add to an accumulator instead of rounding it:
+// 32 additions a chunk in one accumulator over 57 chunks left a sum 2e-5 too
+// small, one chunk leaves 4e-7. So each chunk has an accumulator of its own, of
+// two in turn, and the chunks' sums are added in f32 registers.
 // ---------------------------------------------------------------------------
-// Bound by latency between HBM and the products (1.1 us of a chunk): 1.55 us a
-// chunk and SM, 168 us for 62464 tokens x 32 heads (763 MB, 4.5 TB/s); 8
-// splitting warps take 3% longer.
+// Bound by latency between HBM and the products (1.1 us of a chunk): 178 us at
+// 65536 tokens x 32 heads (256 segments of 57 chunks on 152 SMs, 1.56 us a chunk;
+// 717 MB at 4.0 TB/s). With one accumulator for all chunks it took 168 us, with
+// one for two chunks 174 us and errors of 9e-7.
 constexpr int kSumThreads = 576, kSumSplit = 16;  // warps that split B
-constexpr uint32_t kSumParts = 128;  // tensor-memory columns of the parts: 3 sets of 4 x 32
+constexpr uint32_t kSumParts = 256;  // tensor-memory columns of the parts: 4 sets of 4 x 16, behind two accumulators
 
 struct SumShared {
     uint8_t b[3][kTile], c[3][kTile];
     uint32_t w[kSumSplit][3][16];  // decays of a warp's rows
     float tab[kC + 4];
-    uint64_t b_full[3], b_free[3], c_full[3], c_clean[3], c_free[3], part_full[3], part_free[3], done;
+    uint64_t b_full[3], b_free[3], c_full[3], c_clean[3], c_free[3], part_full[4], part_free[4], sum_full[2], sum_free[2], done;
     uint32_t tmem;
     int dead;
 };
@@ -235,8 +241,14 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
             tc::mbar_init(&s.c_full[i], 1);
             tc::mbar_init(&s.c_clean[i], kSumSplit);
             tc::mbar_init(&s.c_free[i], 1);
-            tc::mbar_init(&s.part_full[i], kSumSplit / 2);
+        }
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(&s.part_full[i], 4);
             tc::mbar_init(&s.part_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&s.sum_full[i], 1);
+            tc::mbar_init(&s.sum_free[i], kSumSplit);
         }
         tc::mbar_init(&s.done, 1);
         s.dead = 0;
@@ -264,8 +276,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
     __syncthreads();
     tc::tc_fence_after();
     const Waiter wait{&s.dead, (long long)p.wait_ns};
-    // the sets of parts in turn: half `hf` of chunk n is batch 2 n + hf
-    auto part_of = [&](int batch) { return kTmem + kSumParts + (batch % 3) * 128; };
+    // a set of parts for each quarter of a chunk's rows
+    auto part_of = [&](int quarter) { return kTmem + kSumParts + quarter * 64; };
+    auto sum_of = [&](int n) { return kTmem + (n & 1) * 128; };
 
     if (warp == kSumSplit) {
         if (lane == 0) {
@@ -281,17 +294,20 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
         bool ok = true;
         for (int n = 0; n < chunks && ok; ++n) {
             const int u = n % 3;
-            ok = wait.poll(&s.c_full[u], (n / 3) & 1) && wait.poll(&s.c_clean[u], (n / 3) & 1);
+            ok = wait.poll(&s.c_full[u], (n / 3) & 1) && wait.poll(&s.c_clean[u], (n / 3) & 1) &&
+                 (n < 2 || wait.poll(&s.sum_free[n & 1], ((n >> 1) - 1) & 1));
             const uint64_t c = tiles + u * (kTile >> 4);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int batch = 2 * n + hf;
-                if (!(ok = ok && wait.poll(&s.part_full[batch % 3], (batch / 3) & 1))) break;
+            for (int g = 0; g < 4; ++g) {
+                if (!(ok = ok && wait.poll(&s.part_full[g], n & 1))) break;
                 tc::tc_fence_after();
                 if (leader) {
-                    mma_parts<4>(kTmem, part_of(batch), 32, c, 64 * hf, batch == 0);
-                    tc::mma_commit(&s.part_free[batch % 3]);
-                    if (hf) tc::mma_commit(&s.c_free[u]);
+                    mma_parts<2>(sum_of(n), part_of(g), 16, c, 32 * g, g == 0);
+                    tc::mma_commit(&s.part_free[g]);
+                    if (g == 3) {
+                        tc::mma_commit(&s.c_free[u]);
+                        tc::mma_commit(&s.sum_full[n & 1]);
+                    }
                 }
             }
         }
@@ -300,10 +316,23 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
             tc::mbar_wait(&s.done, 0, kDrainNs);
         }
     } else {
-        const int hf = warp >> 3, row0 = (warp >> 2) * 32;
+        const int group = warp >> 2, row0 = group * 32;
+        float sum[32] = {};  // lane: b, columns 32 group ..: c
+        auto add_sum = [&](int n) {
+            if (!wait.warp(&s.sum_full[n & 1], (n >> 1) & 1)) return false;
+            tc::tc_fence_after();
+            float v[32];
+            tc::tmem_ld32(tc::tmem_addr(sum_of(n), (warp & 3) * 32, 32 * group), v);
+            tc::tmem_ld_wait();
+            tc::tc_fence_before();
+            tc::warp_arrive(&s.sum_free[n & 1]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[i] += v[i];
+            return true;
+        };
         bool ok = true;
         for (int n = 0; n < chunks && ok; ++n) {
-            const int u = n % 3, from = n * kC, len = min(kC, seg.len - from), batch = 2 * n + hf;
+            const int u = n % 3, from = n * kC, len = min(kC, seg.len - from);
             const uint32_t ph = (n / 3) & 1;
             if (len < kC) {
                 if (!(ok = wait.warp(&s.c_full[u], ph))) break;
@@ -321,37 +350,27 @@ __global__ void __launch_bounds__(kSumThreads, 1) k_la_sum_tc(const __grid_const
                 w[0][lane] = d.w[0], w[1][lane] = d.w[1], w[2][lane] = d.w[2];
             }
             __syncwarp();
+            if (n > 1 && !(ok = add_sum(n - 2))) break;  // (while the last chunk's products run)
             if (!(ok = wait.warp(&s.b_full[u], ph))) break;
-            if (batch >= 3 && !(ok = wait.warp(&s.part_free[batch % 3], (batch / 3 - 1) & 1))) break;
+            if (n > 0 && !(ok = wait.warp(&s.part_free[group], (n - 1) & 1))) break;
             tc::tc_fence_after();
 #pragma unroll 1
             for (int t = 0; t < 2; ++t)
-                split_rows(s.b[u], row0 + 16 * t, w[0] + 8 * t, w[1] + 8 * t, w[2] + 8 * t, len,
-                           part_of(batch) + (row0 & 32) / 2 + 8 * t, 32);
+                split_rows(s.b[u], row0 + 16 * t, w[0] + 8 * t, w[1] + 8 * t, w[2] + 8 * t, len, part_of(group) + 8 * t, 16);
             tc::warp_arrive(&s.b_free[u]);
             tc::tmem_st_wait();
             tc::tc_fence_before();
-            tc::warp_arrive(&s.part_full[batch % 3]);
+            tc::warp_arrive(&s.part_full[group]);
+        }
+        if (ok && (chunks < 2 || add_sum(chunks - 2)) && add_sum(chunks - 1)) {
+            float *to = r.states + (size_t(it.index) * p.hv + it.h) * kState + ((warp & 3) * 32 + lane) * kHeadDim + 32 * group;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(to + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
         }
     }
     __syncwarp();
     tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
-    if (warp < 8 && !s.dead) {  // lane: b, columns: c
-        const int b = tid & 127, c0 = (warp >> 2) * 64;
-        float *to = r.states + (size_t(it.index) * p.hv + it.h) * kState + b * kHeadDim + c0;
-#pragma unroll
-        for (int x = 0; x < 64; x += 16) {
-            float v[16];
-            tc::tmem_ld16(tc::tmem_addr(kTmem, (warp & 3) * 32, c0 + x), v);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4 *>(to + x + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        }
-        tc::tc_fence_before();
-    }
     __syncthreads();
     if (tid == 0 && s.dead) record_status(p.status, GDN_ETIMEOUT);
     if (warp == kSumSplit && lane == 0 && s.dead)

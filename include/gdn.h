@@ -468,9 +468,10 @@ size_t gdn_gated_rmsnorm_bwd_workspace_size(const gdn_problem *p);
  * States and sums are f32, decays powers taken from their exponent. bf16: the
  * decayed scores inside a chunk of 128 tokens and the state in the product
  * with q are rounded to bf16, as out is; final_state is not rounded on its way
- * (what is added to a state is exact to 2^-24); where a decay from a chunk's
- * start to a token is below 2^-64, it counts as 2^-64 in the product of q with
- * the state, and scores q k above 2^63 overflow there. Infinities and NaN stay in
+ * (a token's part of it is exact to 2^-24, and the tensor cores cut the sums over
+ * a chunk's tokens: 5e-7 of the state's norm as measured, however many chunks).
+ * Where a decay from a chunk's start to a token is below 2^-64, it counts as 2^-64
+ * in the product of q with the state, and scores q k above 2^63 overflow there. Infinities and NaN stay in
  * their sequence and value heads, and in f32 reach only tokens whose sums they
  * are in. With bf16 those of v also reach out up to 127 tokens before their own,
  * and in the backward pass those of k dq as far, those of dout dv and those of q

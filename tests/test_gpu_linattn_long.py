@@ -1,5 +1,5 @@
-"""Linear attention where its pipelines go round many times, walks of long sequences left whole: every token of a few
-heads, normwise, against the definition in 64 bits."""
+"""Linear attention where its pipelines go round many times, walks of long sequences left whole and segments of many chunks
+summed and chained: every token of a few heads, normwise, against the definition in 64 bits."""
 import pytest
 import torch
 
@@ -47,3 +47,30 @@ def test_whole_sequences(cuda, dtype, hq, hv):
     res = la.run(d)
     assert gdn.gdn_get_device_status() == gdn.GDN_OK
     L.compare(res, d, lens, dtype, [0, hq - 1])
+
+
+SLOW = [-1e-5, 0.0]  # heads that keep nearly everything, so that one segment's sum goes on into all later ones
+
+
+def test_summed_segments(cuda):
+    """Segments of 57 chunks, forward."""
+    d = inputs(51, [65536], 16, 32, BF16, True, cuda)
+    d["decay"][-2:] = torch.tensor(SLOW, device=cuda)
+    assert 50 * 128 <= segment_rows(d, False) <= 65536 // 8
+    out, final = gdn.gdn_linear_attention(d["q"], d["k"], d["v"], d["decay"], d["scale"], initial_state=d["s0"],
+                                          cu_seqlens=d["cu"])
+    assert gdn.gdn_get_device_status() == gdn.GDN_OK
+    L.compare({"out": out, "final": final}, d, [65536], BF16, [0, 15])
+
+
+@DTYPES
+@pytest.mark.parametrize("hq,hv", [(8, 8), (4, 8)], ids=["heads", "groups"])
+def test_summed_segments_backward(cuda, dtype, hq, hv):
+    """Segments of 8 chunks forward and 26 backward, the last one ragged."""
+    d = inputs(52, [20001], hq, hv, dtype, True, cuda)
+    d["decay"][-2:] = torch.tensor(SLOW, device=cuda)
+    if dtype == BF16:
+        assert segment_rows(d, False) >= 8 * 128 and 20 * 128 <= segment_rows(d, True) <= 20001 // 5
+    res = la.run(d)
+    assert gdn.gdn_get_device_status() == gdn.GDN_OK
+    L.compare(res, d, [20001], dtype, [0, hq - 1])
