@@ -193,12 +193,19 @@ cudaError_t launch_group_sums(const float *x0, void *y0, const float *x1, void *
                          static_cast<float *>(y1), items, group, n_segs);
 }
 
-// Microseconds of a chunk (bf16: 128 rows, f32: blocks of 32) in the walk and in
-// the sum and of a CTA's start and end, as measured at 4096 and 65536 tokens.
+// Rows of a segment: those with the least estimated time. Microseconds of a
+// chunk (bf16: 128 rows, f32: blocks of 32) in the walk and in the sum, of a
+// CTA's start and end, and of the two kernels that several segments need. bf16:
+// as measured at 4096 and 65536 tokens x 32 heads; f32: on 76 to 608 CTAs of 1 to
+// 32 blocks; both with a CTA an SM.
+// Against the best of 2 to 17 lengths the choice took up to 9% longer for 47 of 50
+// calls: one sequence of 200 to 16384 tokens and sets of 2 to 64, 2 to 40 heads,
+// forward and backward. The others, bf16, are a sequence of 4000 tokens with one
+// of 60 (11%), ten of 0 to 1000 backward (16%), 8000 with two of 100 backward (23%).
 int segment_rows(long long total_tokens, long long num_seqs, int hv, int roles, int io_dtype) {
     const bool tc = io_dtype == GDN_DT_BF16;
     const int unit = tc ? 128 : 32;
-    const double slots = tc ? 152 : 2 * 152, walk = tc ? 2.8 : 3.6, sum = tc ? 1.3 : 2.0, start = tc ? 14.0 : 5.0;
+    const double slots = 152, walk = tc ? 2.8 : 10.5, sum = tc ? 1.3 : 4.4, start = tc ? 14.0 : 4.0, kernels = 8.0;
     const long long units = (total_tokens + unit - 1) / unit;
     const double heads = double(hv) * roles;
     auto waves = [&](double items) { return ceil(items / slots); };
@@ -206,15 +213,20 @@ int segment_rows(long long total_tokens, long long num_seqs, int hv, int roles, 
     double least = 0;
     for (long long u = 1;; u = u < 16 ? u + 1 : u + u / 8) {
         if (u > units && u > 1) u = units;
-        const double t = waves(double((units + u - 1) / u + num_seqs - 1) * heads) * (start + double(u) * (u < units ? walk + sum : walk));
+        const bool cut = u < units;
+        const double t = waves(double((units + u - 1) / u + num_seqs - 1) * heads) * (start + double(u) * (cut ? walk + sum : walk)) +
+                         (cut ? kernels : 0);
         if (u == 1 || t < least) least = t, best = u;
         if (u >= units || u * unit >= 65536) break;
     }
     // Several sequences (their lengths are on the device): segments of twice the mean length leave most of them whole,
-    // and those need no sums. Lengths that differ cost a quarter where CTAs take several, half where they take one.
+    // and those need no sums. Lengths that differ cost a quarter where CTAs take several, half where they take one; equal
+    // ones whole rounds (bf16 8 prompts x 32 heads 278 us whole and 347 to 438 cut, 64 short ones 258 and 281 to 567; f32
+    // 4 x 1500 tokens x 40 heads 982 whole and 792 cut).
     if (num_seqs > 1) {
         const double mean = double(units) / double(num_seqs), items = double(num_seqs) * heads;
-        const double whole = items > slots ? 1.25 * items / slots * (start + mean * walk) : start + 1.5 * mean * walk;
+        const double rounds = fmax(waves(items), 1.25 * items / slots);
+        const double whole = (items > slots ? rounds * (start + mean * walk) : start + 1.5 * mean * walk) + kernels;
         const long long u = (2 * units + num_seqs - 1) / num_seqs;
         if (whole < least && u > 0 && u * unit < 65536) best = u;
     }

@@ -8,9 +8,13 @@
 // All arithmetic is f32 (f32 inputs want more than the tensor cores' 11 bits),
 // the decays are powers taken from the exponent, not products over tokens,
 // whose errors would add up over the state's memory.
-// Bound by the FMA units and by the loads from shared memory that feed them:
-// about 3.6 us a block and CTA with two CTAs on an SM, 29 us for 200 tokens x 2
-// heads with all four kernels (with the state by 4-byte loads 45).
+// Bound by the FMA units and by the loads from shared memory that feed them. A CTA
+// has an SM to itself: 4 us for its start and end, 10.5 us a block in the walk and
+// 4.4 in the sum (1.2 M and 0.5 M multiply-adds, 5 and 2 us on the units alone).
+// With the scores over a's rows two fit: 21 us a block and 10 each, no gain, and
+// alone on its SM, where there are few segments, such a CTA takes 12.3 and 6.0,
+// for its 128 registers. 29 us for 200 tokens x 2 heads with all four kernels
+// (with the state by 4-byte loads 45).
 #include <type_traits>
 
 #include "gdn_linattn.cuh"
@@ -34,7 +38,7 @@ __device__ __forceinline__ float2 hi2(const float4 &v) { return make_float2(v.z,
 
 // kWalk: the segment's output and the state that leaves it; else its sum alone
 template <bool kWalk>
-__global__ void __launch_bounds__(kThreads, 2) k_la_simt(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(kThreads, 1) k_la_simt(const __grid_constant__ Args p) {
     extern __shared__ __align__(16) uint8_t raw[];
     SimtShared &s = *reinterpret_cast<SimtShared *>(raw);
     const int role = blockIdx.x % p.roles, h = blockIdx.x / p.roles % p.hv, index = blockIdx.x / (p.roles * p.hv);
