@@ -38,7 +38,7 @@ struct Role {
     float scale_in, scale_out;  // of a's products with b and of b in the state; of the output
     int ga, gb, gc;     // value heads to a head of a, b, c (out has one for each value head)
     int against;        // against time
-    int swapped;        // init and fin are [c, b]
+    int swapped;        // init is [c, b] (no role with a fin)
     int partial;        // out is f32 [tokens, hv, 128], to be summed over the group's heads
     int sectors;        // out starts at a multiple of 32 bytes
 };

@@ -233,10 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_simt(const __grid_constant__
         const float f = r.against && seg.len > 0 ? s.tab[1] : 1.f;  // to the gradient of the state before the first token
         float *to = r.fin + size_t(seg.seq) * per_head + size_t(h) * kState;
 #pragma unroll 4
-        for (int e = tid; e < kState; e += kThreads) {
-            const float x = s.state[r.swapped ? e % kHeadDim * kHeadDim + e / kHeadDim : e];
-            to[e] = f == 1.f ? x : f * x;
-        }
+        for (int e = tid; e < kState; e += kThreads) to[e] = f == 1.f ? s.state[e] : f * s.state[e];
     }
 }
 

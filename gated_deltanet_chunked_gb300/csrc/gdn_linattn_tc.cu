@@ -812,18 +812,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_la_walk_tc(const __grid_con
 #pragma unroll
                 for (int k = 0; k < 32; ++k) st[k] = __fmul2_rn(make_float2(f, f), st[k]);
             }
-            if (r.swapped) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    to[(c0 + 2 * k) * kHeadDim + row] = st[k].x;
-                    to[(c0 + 2 * k + 1) * kHeadDim + row] = st[k].y;
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 32; k += 2)
-                    *reinterpret_cast<float4 *>(to + row * kHeadDim + c0 + 2 * k) =
-                        make_float4(st[k].x, st[k].y, st[k + 1].x, st[k + 1].y);
-            }
+            for (int k = 0; k < 32; k += 2)
+                *reinterpret_cast<float4 *>(to + row * kHeadDim + c0 + 2 * k) =
+                    make_float4(st[k].x, st[k].y, st[k + 1].x, st[k + 1].y);
         }
     }
     __syncwarp();
