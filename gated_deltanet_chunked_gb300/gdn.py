@@ -1024,6 +1024,8 @@ def _rope_layout(q_shape, k_shape, freq_shape, pos_shape, has_axis, interleaved,
         raise ValueError(f"k must have shape {(T, k_shape[1], d)}, got {tuple(k_shape)}")
     if len(freq_shape) != 1 or freq_shape[0] > d // 2:
         raise ValueError(f"inv_freq must be 1-D with at most {d // 2} elements, got {tuple(freq_shape)}")
+    if len(pos_shape) not in (1, 2):
+        raise ValueError(f"positions must be [T] or [A, T], got {tuple(pos_shape)}")
     axes = 1 if len(pos_shape) == 1 else pos_shape[0]
     if axes > 1 and not has_axis:
         raise ValueError("positions of several axes need pair_axis, each pair's axis")
