@@ -74,3 +74,21 @@ def test_summed_segments_backward(cuda, dtype, hq, hv):
     res = la.run(d)
     assert gdn.gdn_get_device_status() == gdn.GDN_OK
     L.compare(res, d, [20001], dtype, [0, hq - 1])
+
+
+@DTYPES
+@pytest.mark.parametrize("hq,hv", [(1, 1), (1, 3)])
+@pytest.mark.parametrize("init", [False, True], ids=["zero", "init"])
+def test_few_chunks_normwise(cuda, dtype, hq, hv, init):
+    lens = [1100, 129, 300, 256]
+    d = inputs(53, lens, hq, hv, dtype, init, cuda)
+    L.compare(la.run(d), d, lens, dtype, range(hq))
+
+
+@DTYPES
+@pytest.mark.parametrize("decay", [[0.0, -1e-4], [-0.7, -5.0], [-30.0, -0.34657]])
+def test_decays_normwise(cuda, dtype, decay):
+    lens = [700, 130, 1024]
+    d = inputs(54, lens, 2, 2, dtype, True, cuda)
+    d["decay"] = torch.tensor(decay, device=cuda)
+    L.compare(la.run(d), d, lens, dtype, [0, 1])
