@@ -8,12 +8,18 @@
 //
 // Each row is read and written once, 16 bytes a lane. A CTA takes the rows of a
 // few tokens at a time and has their angles' sines and cosines in shared memory,
-// once for all heads of a token. Bound by issue slots: 65536 tokens of 32 + 4
-// heads, bf16, take 257 us (1.21 GB: 4.7 TB/s, 0.69 of the measured copy rate),
-// 4096 tokens of 16 + 16 heads 21 us and 35 backward with the sums (0.46 and 0.43). What made
-// it faster: values in an order without bank conflicts and no division a row (35
-// -> 24 us), a partner's channels by shuffles after the norm, not before (24 ->
-// 23), steps whose rows fill the lane groups (36 heads: 336 -> 272 us).
+// once for all heads of a token. Bound by latency, no unit is full: 0.56 to 0.59
+// of the issue slots, DRAM at 31 to 47%, a third of the warps. To the 16 bytes of
+// a bf16 row that a lane reads come six loads of 16 bytes from shared memory
+// (weight, cos and +-sin), anew for each head of a token, and a step's rows are
+// asked for when the step before has been stored, so that with one batch a step
+// only the two other CTAs have loads under way during the arithmetic. 65536 tokens
+// of 32 + 4 heads, bf16, take 256 us (1.21 GB: 4.7 TB/s, 0.69 of the measured copy
+// rate), 4096 tokens of 16 + 16 heads 21 us and 35 backward with the sums (0.46
+// and 0.43). What made it faster: values in an order without bank conflicts and
+// no division a row (35 -> 24 us), a partner's channels by shuffles after the
+// norm, not before (24 -> 23), steps whose rows fill the lane groups (36 heads:
+// 336 -> 272 us).
 //
 // Angles. A position has up to 31 bits and t is wanted to 2^-24 of a turn:
 // frequency / 2 pi is held in three f32, the position in two whole f32, and the

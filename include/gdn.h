@@ -471,12 +471,12 @@ size_t gdn_gated_rmsnorm_bwd_workspace_size(const gdn_problem *p);
  * (a token's part of it is exact to 2^-24, and the tensor cores cut the sums over
  * a chunk's tokens: 5e-7 of the state's norm as measured, however many chunks).
  * Where a decay from a chunk's start to a token is below 2^-64, it counts as 2^-64
- * in the product of q with the state, and scores q k above 2^63 overflow there. Infinities and NaN stay in
- * their sequence and value heads, and in f32 reach only tokens whose sums they
- * are in. With bf16 those of v also reach out up to 127 tokens before their own,
- * and in the backward pass those of k dq as far, those of dout dv and those of q
- * dk up to 127 tokens behind. (The bf16 kernels wait for copies and products, at
- * most 2 s a wait: GDN_ETIMEOUT in the device status.) */
+ * in the product of q with the state, and scores q k above 2^63 overflow there.
+ * Infinities and NaN stay in their sequence and value heads, and in f32 reach only
+ * tokens whose sums they are in. With bf16 those of v also reach out up to 127
+ * tokens before their own, and in the backward pass those of k dq as far, those of
+ * dout dv and those of q dk up to 127 tokens behind. (The bf16 kernels wait for
+ * copies and products, at most 2 s a wait: GDN_ETIMEOUT in the device status.) */
 int gdn_linear_attention(const gdn_problem *p, const void *q, const void *k, const void *v, const float *decay,
                          float scale, const float *initial_state, const int32_t *cu_seqlens, void *out,
                          float *final_state, void *workspace, size_t workspace_bytes, void *stream);
@@ -547,8 +547,9 @@ typedef struct gdn_qk_rope {
  *   positions     int32 [axes, tokens]
  *   pair_axis     int32 [rotary / 2], the axis that turns a pair, or NULL (axis 0)
  * The angle's error is below 2^-22 radian for every int32 position and
- * frequencies up to 64, all else is f32 and rounded once. An axis outside 0 .. axes - 1 is recorded as
- * GDN_EDEVICE_INPUT and nothing is written. */
+ * frequencies up to 64, all else is f32 and rounded once (a row whose mean square
+ * overflows f32 counts as one of infinite norm: zeros). An axis outside
+ * 0 .. axes - 1 is recorded as GDN_EDEVICE_INPUT and nothing is written. */
 int gdn_qk_norm_rope(const gdn_qk_rope *r, const void *q, const void *k, const float *q_weight, const float *k_weight,
                      const float *inv_freq, const int32_t *positions, const int32_t *pair_axis, void *out_q, void *out_k,
                      void *stream);
